@@ -1,4 +1,5 @@
-"""ctypes loader for libccv.so, the CUDA library behind include/ccv.h.
+"""ctypes loader for libccv.so, the CUDA library behind include/ccv.h and
+include/ccv_layer.h.
 
 There is no fallback: if the library has not been built, loading raises.
 """
@@ -11,10 +12,12 @@ import re
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libccv.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "ccv.h")
+LAYER_HEADER = os.path.join(os.path.dirname(HERE), "include", "ccv_layer.h")
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
 I32 = ctypes.c_int
+F32 = ctypes.c_float
 
 
 class PagedStream(ctypes.Structure):
@@ -50,6 +53,38 @@ SIGNATURES = {
                                  P, P, P, P, I64, I32, I32, P, I32, I32, I32, I32, P, P], I32),
 }
 
+
+class HeadsView(ctypes.Structure):
+    """struct ccv_heads_view of include/ccv_layer.h."""
+    _fields_ = [("data", P), ("stride_row", I64), ("stride_tok", I64), ("stride_head", I64),
+                ("stride_dim", I64)]
+
+
+class GdrArgs(ctypes.Structure):
+    """struct ccv_gdr_args of include/ccv_layer.h."""
+    _fields_ = [("q", HeadsView), ("k", HeadsView), ("v", HeadsView), ("out", HeadsView),
+                ("g", P), ("beta", P), ("gate_stride_row", I64), ("gate_stride_tok", I64),
+                ("gate_stride_head", I64), ("a_log", P), ("dt_bias", P), ("state", P),
+                ("s_stride_line", I64), ("s_stride_head", I64), ("s_stride_v", I64),
+                ("s_stride_k", I64), ("num_lines", I32), ("num_k_heads", I32),
+                ("num_v_heads", I32), ("dim_k", I32), ("dim_v", I32), ("scale", F32),
+                ("qk_l2norm", I32), ("pad_slot_id", I32)]
+
+
+# Argument lists of include/ccv_layer.h, in the order of its declarations.
+LAYER_SIGNATURES = {
+    "gdr_fwd": ([ctypes.POINTER(GdrArgs), P, I32, P, P, I32, P, I64, P, P], I32),
+    "gdr_fwd_workspace": ([I32, I32, I32, I32, I32, I32], I64),
+    "gdr_update": ([ctypes.POINTER(GdrArgs), P, P, P, I64, I64, I32, I32, I32, P, P], I32),
+    "gated_rms_norm": ([ctypes.POINTER(HeadsView), ctypes.POINTER(HeadsView), P,
+                        ctypes.POINTER(HeadsView), I32, I32, I32, F32, I32, I32, P], I32),
+    "residual_rms_norm": ([P, I64, I64, P, I64, I64, I32, P, P, P, I64, I64, P, I64, I64,
+                           P, I64, I64, I32, I32, F32, F32, F32, P], I32),
+    "spec_verify": ([P, I32, I64, I64, P, I64, I64, P, I64, I64, P, P, P, I64, I64, P, I64,
+                     P, P, I32, I32, I32, P, I64, P, P], I32),
+    "spec_verify_workspace": ([I32, I32, I32], I64),
+}
+
 _LIB = None
 
 
@@ -68,7 +103,7 @@ def load():
                 f"libccv.so is not built ({LIB_PATH} missing); build it with "
                 "`python -c 'import __graft_entry__ as g; g.build()'`")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in SIGNATURES.items():
+        for name, (args, res) in (*SIGNATURES.items(), *LAYER_SIGNATURES.items()):
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
@@ -80,8 +115,8 @@ def status_string(status: int) -> str:
     return load().ccv_status_string(int(status)).decode()
 
 
-def declared_functions():
-    """Names of the functions declared in include/ccv.h."""
-    text = open(HEADER).read()
+def declared_functions(header: str = HEADER):
+    """Names of the functions declared in include/ccv.h (or the given header)."""
+    text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return re.findall(r"^\s*(?:const\s+)?\w+\s*\*?\s*(\w+)\s*\(", text, flags=re.M)

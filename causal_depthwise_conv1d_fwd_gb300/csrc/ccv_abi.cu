@@ -1,5 +1,6 @@
 // Status strings and version of the ccv C ABI.
 #include "ccv_common.cuh"
+#include "ccv_layer.h"
 
 extern "C" const char *ccv_status_string(int status) {
     switch (status) {
@@ -13,7 +14,10 @@ extern "C" const char *ccv_status_string(int status) {
         case CCV_ERR_RANGE:
             return "a stream's D-range [off_s, off_s+ws) leaves the cache or overlaps another stream's";
         case CCV_ERR_CAPACITY: return "an output buffer has fewer entries than the call needs";
-        case CCV_ERR_ARGUMENT: return "has_initial_state needs conv_states";
+        case CCV_ERR_ARGUMENT: return "an argument combination the entry point rejects (has_initial_state without states, ...)";
+        case CCV_ERR_DIM: return "a head dimension or row length the operator does not support";
+        case CCV_ERR_HEADS: return "value heads must be a multiple of key heads";
+        case CCV_ERR_WORKSPACE: return "the workspace is missing, too small or misaligned";
         default: break;
     }
     if (status > 0) return cudaGetErrorString(static_cast<cudaError_t>(status));

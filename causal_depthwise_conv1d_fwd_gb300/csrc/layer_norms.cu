@@ -1,0 +1,340 @@
+// The norms around a block: gated_rms_norm (of its heads, with the gate) and residual_rms_norm (its output's norm, gate
+// and scale, the residual addition, and the norm that opens the next block).
+//
+// Both read each element once, keep the row in registers in fp32, reduce it, and write once: 6 bytes an element for the
+// first, 8 to 14 for the second, so HBM bounds them at any size that fills the card and one launch's latency below.
+// A row belongs to LPR lanes: within a warp the reductions are shuffles; longer rows reduce over the block's warps.
+#include "ccv_common.cuh"
+#include "ccv_layer.h"
+
+namespace ccv {
+namespace {
+
+constexpr int kMaxRow = 32768;
+constexpr int kNormThreads = 128;  // threads of a block when a row needs no more
+
+// Sum over the LPR lanes of a row; the block is one row when LPR > 32.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x, float *warp_sums) {
+#pragma unroll
+    for (int m = 1; m < (LPR < 32 ? LPR : 32); m <<= 1) x += __shfl_xor_sync(kFullMask, x, m);
+    if constexpr (LPR > 32) {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        if (lane == 0) warp_sums[warp] = x;
+        __syncthreads();
+        x = lane < LPR / 32 ? warp_sums[lane] : 0.0f;
+#pragma unroll
+        for (int m = 1; m < LPR / 32; m <<= 1) x += __shfl_xor_sync(kFullMask, x, m);
+        x = __shfl_sync(kFullMask, x, 0);
+        __syncthreads();
+    }
+    return x;
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_row(const uint16_t *p, int64_t stride, int d, int dim, float (&f)[VEC]) {
+    Raw<VEC> r;
+    r.zero();
+    if (d < dim) r = load_plain<VEC>(p + (VEC == 8 ? d : d * stride));
+    r.to_float(f);
+}
+template <int VEC>
+__device__ __forceinline__ void load_row(const float *p, int64_t stride, int d, int dim, float (&f)[VEC]) {
+    if constexpr (VEC == 8) {
+        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 a = d < dim ? *reinterpret_cast<const float4 *>(p + d) : z;
+        const float4 b = d < dim ? *reinterpret_cast<const float4 *>(p + d + 4) : z;
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+        f[0] = d < dim ? p[d * stride] : 0.0f;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_row(uint16_t *p, int64_t stride, int d, int dim, const float (&f)[VEC]) {
+    Raw<VEC> r;
+    r.from_float(f);
+    if (d < dim) store_plain<VEC>(p + (VEC == 8 ? d : d * stride), r);
+}
+template <int VEC>
+__device__ __forceinline__ void store_row(float *p, int64_t stride, int d, int dim, const float (&f)[VEC]) {
+    if (d >= dim) return;
+    if constexpr (VEC == 8) {
+        *reinterpret_cast<float4 *>(p + d) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4 *>(p + d + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        p[d * stride] = f[0];
+    }
+}
+
+__device__ __forceinline__ float gate_act(float z, int activation) {
+    if (activation == 0) return z;
+    const float s = rcp_approx(1.0f + __expf(-z));
+    return activation == 1 ? z * s : s;
+}
+
+struct GatedArgs {
+    ccv_heads_view x, gate, out;
+    const uint16_t *weight;
+    int64_t rows;
+    int heads, dim;
+    float eps;
+    int activation, before;
+};
+
+template <int LPR, int VEC, int NV>
+__global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) gated_rms_norm_kernel(const __grid_constant__ GatedArgs a) {
+    __shared__ float warp_sums[32];
+    wait_prior_grid();
+    release_next_grid();
+    constexpr int kThreads = LPR > kNormThreads ? LPR : kNormThreads;
+    const int lane = threadIdx.x % LPR;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
+    const bool live = row < a.rows;
+    const int64_t tok = live ? row / a.heads : 0, head = live ? row % a.heads : 0;
+    const int dim = live ? a.dim : 0;
+    const uint16_t *xp = static_cast<const uint16_t *>(a.x.data) + tok * a.x.stride_tok + head * a.x.stride_head;
+    const uint16_t *gp = static_cast<const uint16_t *>(a.gate.data) + tok * a.gate.stride_tok + head * a.gate.stride_head;
+    uint16_t *op = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + tok * a.out.stride_tok + head * a.out.stride_head;
+    float x[NV][VEC], z[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int d = (j * LPR + lane) * VEC;
+        load_row<VEC>(xp, a.x.stride_dim, d, dim, x[j]);
+        load_row<VEC>(gp, a.gate.stride_dim, d, dim, z[j]);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            z[j][i] = gate_act(z[j][i], a.activation);
+            if (!a.before) {  // past the row's end x is 0 and the gate finite
+                x[j][i] *= z[j][i];
+                z[j][i] = 1.0f;
+            }
+            sum = fmaf(x[j][i], x[j][i], sum);
+        }
+    const float scale = rsqrtf(row_sum<LPR>(sum, warp_sums) / a.dim + a.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int d = (j * LPR + lane) * VEC;
+        float w[VEC];
+        load_row<VEC>(a.weight, 1, d, dim, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[i] = x[j][i] * scale * w[i] * z[j][i];
+        store_row<VEC>(op, a.out.stride_dim, d, dim, w);
+    }
+}
+
+struct ResidualArgs {
+    const uint16_t *x;
+    const void *residual;
+    const uint16_t *weight, *post_weight, *gate;
+    uint16_t *out;
+    void *residual_out;
+    int64_t xt, xd, rt, rd, gt, gd, ot, od, rot, rod;
+    int tokens, dim;
+    float scale, eps, offset;
+};
+
+template <int LPR, int VEC, int NV, typename Res>
+__global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) residual_rms_norm_kernel(const __grid_constant__ ResidualArgs a) {
+    __shared__ float warp_sums[32];
+    wait_prior_grid();
+    release_next_grid();
+    constexpr int kThreads = LPR > kNormThreads ? LPR : kNormThreads;
+    const int lane = threadIdx.x % LPR;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
+    const int dim = row < a.tokens ? a.dim : 0;
+    if (row >= a.tokens) row = 0;
+    const uint16_t *xp = a.x + row * a.xt;
+    const Res *rp = static_cast<const Res *>(a.residual) + row * a.rt;
+    float x[NV][VEC], h[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int d = (j * LPR + lane) * VEC;
+        load_row<VEC>(xp, a.xd, d, dim, x[j]);
+        load_row<VEC>(rp, a.rd, d, dim, h[j]);
+    }
+    float post = a.scale;
+    if (a.post_weight != nullptr) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) sum = fmaf(x[j][i], x[j][i], sum);
+        post *= rsqrtf(row_sum<LPR>(sum, warp_sums) / a.dim + a.eps);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int d = (j * LPR + lane) * VEC;
+        float f[VEC];
+        if (a.post_weight != nullptr) {
+            load_row<VEC>(a.post_weight, 1, d, dim, f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[j][i] *= f[i] + a.offset;
+        }
+        if (a.gate != nullptr) {
+            load_row<VEC>(a.gate + row * a.gt, a.gd, d, dim, f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[j][i] *= f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            h[j][i] = fmaf(post, x[j][i], h[j][i]);
+            sum = fmaf(h[j][i], h[j][i], sum);
+        }
+    }
+    const float scale = rsqrtf(row_sum<LPR>(sum, warp_sums) / a.dim + a.eps);
+    Res *hp = static_cast<Res *>(a.residual_out) + row * a.rot;
+    uint16_t *op = a.out + row * a.ot;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int d = (j * LPR + lane) * VEC;
+        store_row<VEC>(hp, a.rod, d, dim, h[j]);
+        float w[VEC];
+        load_row<VEC>(a.weight, 1, d, dim, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[i] = h[j][i] * scale * (w[i] + a.offset);
+        store_row<VEC>(op, a.od, d, dim, w);
+    }
+}
+
+// Calls f.template operator()<LPR, VEC, NV>() with the least lanes a row of `dim` elements needs.  With vectors of 8 a
+// lane holds 1 vector up to 256 elements (a warp's 32 lanes), 2 vectors a lane up to 512, then whole blocks with 2 or 4.
+template <typename F>
+int for_row(int dim, bool vec, F f) {
+    if (vec) {
+        if (dim <= 64) return f.template operator()<8, 8, 1>();
+        if (dim <= 128) return f.template operator()<16, 8, 1>();
+        if (dim <= 256) return f.template operator()<32, 8, 1>();
+        if (dim <= 512) return f.template operator()<32, 8, 2>();
+        if (dim <= 2048) return f.template operator()<128, 8, 2>();
+        if (dim <= 4096) return f.template operator()<256, 8, 2>();
+        if (dim <= 8192) return f.template operator()<512, 8, 2>();
+        if (dim <= 16384) return f.template operator()<1024, 8, 2>();
+        return f.template operator()<1024, 8, 4>();
+    }
+    if (dim <= 256) return f.template operator()<32, 1, 8>();
+    if (dim <= 2048) return f.template operator()<256, 1, 8>();
+    return f.template operator()<1024, 1, 32>();
+}
+
+unsigned row_blocks(int64_t rows, int lanes) {
+    const int per = lanes > kNormThreads ? 1 : kNormThreads / lanes;
+    return static_cast<unsigned>((rows + per - 1) / per);
+}
+
+struct GatedLaunch {
+    GatedArgs a;
+    cudaStream_t stream;
+    template <int LPR, int VEC, int NV>
+    int operator()() const {
+        return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV>, dim3(row_blocks(a.rows, LPR)),
+                          dim3(LPR > kNormThreads ? LPR : kNormThreads), 0, stream, a);
+    }
+};
+
+template <typename Res>
+struct ResidualLaunch {
+    ResidualArgs a;
+    cudaStream_t stream;
+    template <int LPR, int VEC, int NV>
+    int operator()() const {
+        return launch_pdl(residual_rms_norm_kernel<LPR, VEC, NV, Res>, dim3(row_blocks(a.tokens, LPR)),
+                          dim3(LPR > kNormThreads ? LPR : kNormThreads), 0, stream, a);
+    }
+};
+
+Extent extent2(const void *p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int size) {
+    const uintptr_t base = reinterpret_cast<uintptr_t>(p);
+    const int64_t last = (n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2;
+    return Extent{base, base + static_cast<uintptr_t>(last) * size + size - 1};
+}
+
+bool vec_view(const void *p, int64_t s0, int64_t s1, int64_t sd) {
+    return aligned16(p) && sd == 1 && s0 % 8 == 0 && s1 % 8 == 0;
+}
+
+}  // namespace
+}  // namespace ccv
+
+extern "C" int gated_rms_norm(const ccv_heads_view *x, const ccv_heads_view *gate, const void *weight,
+                              const ccv_heads_view *out, int tokens, int heads, int dim, float eps, int activation,
+                              int norm_before_gate, ccv_stream_t stream) {
+    using namespace ccv;
+    if (x == nullptr || gate == nullptr || out == nullptr) return CCV_ERR_NULL_POINTER;
+    if (tokens < 0 || heads < 0 || dim < 0) return CCV_ERR_SIZE;
+    if (activation < 0 || activation > 2) return CCV_ERR_ARGUMENT;
+    if (dim > kMaxRow) return CCV_ERR_DIM;
+    for (const ccv_heads_view *v : {x, gate, out})
+        if (v->stride_tok < 0 || v->stride_head < 0 || v->stride_dim < 0) return CCV_ERR_STRIDE;
+    if (tokens == 0 || heads == 0 || dim == 0) return CCV_OK;
+    if (x->data == nullptr || gate->data == nullptr || weight == nullptr || out->data == nullptr) return CCV_ERR_NULL_POINTER;
+    auto extent = [&](const ccv_heads_view *v) {
+        return extent2(v->data, tokens, v->stride_tok, heads, v->stride_head, dim, v->stride_dim, 2);
+    };
+    for (const ccv_heads_view *v : {x, gate}) {
+        const bool same = v->data == out->data && v->stride_tok == out->stride_tok && v->stride_head == out->stride_head &&
+                          v->stride_dim == out->stride_dim;
+        if (!same && overlaps(extent(v), extent(out))) return CCV_ERR_ALIAS;
+    }
+    if (overlaps(extent2(weight, 1, 0, 1, 0, dim, 1, 2), extent(out))) return CCV_ERR_ALIAS;
+    const int64_t rows = static_cast<int64_t>(tokens) * heads;
+    if (rows > 0x7fffffff) return CCV_ERR_SIZE;
+    bool vec = dim % 8 == 0 && aligned16(weight);
+    for (const ccv_heads_view *v : {x, gate, out}) vec = vec && vec_view(v->data, v->stride_tok, v->stride_head, v->stride_dim);
+    const GatedArgs a{*x, *gate, *out, static_cast<const uint16_t *>(weight), rows, heads, dim, eps, activation, norm_before_gate};
+    return for_row(dim, vec, GatedLaunch{a, stream});
+}
+
+extern "C" int residual_rms_norm(const void *x, int64_t x_stride_tok, int64_t x_stride_dim, const void *residual,
+                                 int64_t r_stride_tok, int64_t r_stride_dim, int residual_fp32, const void *weight,
+                                 const void *post_weight, const void *gate, int64_t g_stride_tok, int64_t g_stride_dim,
+                                 void *out, int64_t out_stride_tok, int64_t out_stride_dim, void *residual_out,
+                                 int64_t ro_stride_tok, int64_t ro_stride_dim, int tokens, int dim, float scale, float eps,
+                                 float weight_offset, ccv_stream_t stream) {
+    using namespace ccv;
+    if (tokens < 0 || dim < 0) return CCV_ERR_SIZE;
+    if (dim > kMaxRow) return CCV_ERR_DIM;
+    for (int64_t s : {x_stride_tok, x_stride_dim, r_stride_tok, r_stride_dim, g_stride_tok, g_stride_dim, out_stride_tok,
+                      out_stride_dim, ro_stride_tok, ro_stride_dim})
+        if (s < 0) return CCV_ERR_STRIDE;
+    if (tokens == 0 || dim == 0) return CCV_OK;
+    if (x == nullptr || residual == nullptr || weight == nullptr || out == nullptr || residual_out == nullptr)
+        return CCV_ERR_NULL_POINTER;
+    const int rsize = residual_fp32 ? 4 : 2;
+    const Extent ex = extent2(x, tokens, x_stride_tok, dim, x_stride_dim, 1, 0, 2);
+    const Extent er = extent2(residual, tokens, r_stride_tok, dim, r_stride_dim, 1, 0, rsize);
+    const Extent eo = extent2(out, tokens, out_stride_tok, dim, out_stride_dim, 1, 0, 2);
+    const Extent ero = extent2(residual_out, tokens, ro_stride_tok, dim, ro_stride_dim, 1, 0, rsize);
+    const Extent ew = extent2(weight, 1, 0, dim, 1, 1, 0, 2);
+    const bool out_is_x = out == x && out_stride_tok == x_stride_tok && out_stride_dim == x_stride_dim;
+    const bool in_place = residual_out == residual && ro_stride_tok == r_stride_tok && ro_stride_dim == r_stride_dim;
+    if ((!out_is_x && overlaps(eo, ex)) || (!in_place && overlaps(ero, er)) || overlaps(eo, er) || overlaps(ero, ex) ||
+        overlaps(eo, ero) || overlaps(ew, eo) || overlaps(ew, ero))
+        return CCV_ERR_ALIAS;
+    if (post_weight != nullptr) {
+        const Extent ep = extent2(post_weight, 1, 0, dim, 1, 1, 0, 2);
+        if (overlaps(ep, eo) || overlaps(ep, ero)) return CCV_ERR_ALIAS;
+    }
+    if (gate != nullptr) {
+        const Extent eg = extent2(gate, tokens, g_stride_tok, dim, g_stride_dim, 1, 0, 2);
+        if (overlaps(eg, eo) || overlaps(eg, ero)) return CCV_ERR_ALIAS;
+    }
+    auto vec_res = [&](const void *p, int64_t st, int64_t sd) {
+        return aligned16(p) && sd == 1 && st % (residual_fp32 ? 4 : 8) == 0;
+    };
+    const bool vec = dim % 8 == 0 && aligned16(weight) && (post_weight == nullptr || aligned16(post_weight)) &&
+                     vec_view(x, x_stride_tok, 0, x_stride_dim) && vec_view(out, out_stride_tok, 0, out_stride_dim) &&
+                     vec_res(residual, r_stride_tok, r_stride_dim) && vec_res(residual_out, ro_stride_tok, ro_stride_dim) &&
+                     (gate == nullptr || vec_view(gate, g_stride_tok, 0, g_stride_dim));
+    const ResidualArgs a{static_cast<const uint16_t *>(x), residual, static_cast<const uint16_t *>(weight),
+                         static_cast<const uint16_t *>(post_weight), static_cast<const uint16_t *>(gate),
+                         static_cast<uint16_t *>(out), residual_out, x_stride_tok, x_stride_dim, r_stride_tok, r_stride_dim,
+                         g_stride_tok, g_stride_dim, out_stride_tok, out_stride_dim, ro_stride_tok, ro_stride_dim,
+                         tokens, dim, scale, eps, weight_offset};
+    return residual_fp32 ? for_row(dim, vec, ResidualLaunch<float>{a, stream})
+                         : for_row(dim, vec, ResidualLaunch<uint16_t>{a, stream});
+}
