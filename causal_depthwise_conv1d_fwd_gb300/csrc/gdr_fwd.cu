@@ -1,8 +1,803 @@
-// Gated delta rule over varlen sequences (prefill).
+// Gated delta rule over varlen sequences (prefill), chunked form on the tensor cores.
+//
+// A chunk holds C = 64 tokens.  With k and q as normalised, G the running sum of g inside the chunk, and d_j the delta of
+// token j, unrolling the recurrence gives
+//     (I + A) d = R,   A_ij = b_i (k_i . k_j) e^{G_i - G_j}  (j < i),   R_j = b_j (v_j - e^{G_j} S k_j)
+//     o_i = e^{G_i} S q_i + sum_{j <= i} P_ij d_j,   P_ij = (q_i . k_j) e^{G_i - G_j}
+//     S  <- e^{G_C} S + sum_j e^{G_C - G_j} d_j k_j^T
+// Only the products with S are sequential, so there are two kernels:
+//   gdr_prep_kernel   for every chunk and key head at once: the two products, the decays, T = (I + A)^-1, P, and what each
+//                     token multiplies by; written to the workspace in the layout the tensor cores read.
+//   gdr_chunk_kernel  for every sequence and value head: the chunks in order with S^T kept on chip.
+//
+// Precision.  The state is fp32, so every product that reaches it is formed to 24 bits: k and q enter as their own bf16
+// values (exact; their norms are factors of a token, applied to sums), and each inexact operand (S, R, T, d) as three bf16
+// parts, of whose products the ones above 2^-24 are kept: 3 with an exact operand, 6 without.  Products that reach the
+// output alone keep 16 bits (the output has 8).  bf16 parts span the range of fp32, so nothing needs scaling and nothing
+// overflows or vanishes that would not in fp32, however far e^G falls inside a chunk.
+#include <cstdlib>
+#include <cstring>
+
+#include "ccv_tcgen05.cuh"
 #include "gdr_common.cuh"
 
+namespace ccv {
+namespace {
+
+constexpr int C = 64;            // tokens of a chunk
+constexpr int kTile = C * 128;   // bytes of 64 rows of 64 bf16 values
+constexpr int kScalars = 5;      // vectors of C floats a (chunk, value head) carries
+enum { kBeta, kKey, kState, kQuery, kMisc };  // their order; kMisc[0] is e^{G_C}
+enum { kT = 0, kP = 3 * kTile, kVec = 5 * kTile };              // T in 3 parts, P in 2, the vectors
+constexpr int kHeadBytes = kVec + kScalars * C * 4;
+
+struct FwdArgs {
+    ccv_gdr_args a;
+    const int32_t *query_start_loc, *cache_indices;
+    const uint8_t *has_initial_state;
+    int batch, total_tokens, slots;
+    uint8_t *heads;  // (slots, num_v_heads) blocks of kHeadBytes
+    int *err_count;
+};
+
+// Chunk j of sequence i is in slot first_slot(i) + j.  floor(s / 64) + i leaves every sequence room for its
+// ceil(n / 64) chunks, needs no sum over the lengths, and total / 64 + batch slots in all.
+__device__ __forceinline__ int first_slot(int start, int i) { return (start >> 6) + i; }
+
+__device__ __forceinline__ bool sequence_ok(int s, int e, int total) { return s >= 0 && e >= s && e <= total; }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Copies `rows` (of which the first n are real) of a head's bf16 vectors into swizzled tiles of 64 values a row, `panels`
+// tiles `panel_bytes` apart, zeros past n and past dim; by threads `id` of `count`.  VEC: 16-byte asynchronous copies.
+template <int PANELS, bool VEC>
+__device__ __forceinline__ void stage_rows(uint8_t *tile, int panel_bytes, const ccv_heads_view &view, int64_t tok, int head, int n,
+                                           int dim, int id, int count) {
+    const uint16_t *src = static_cast<const uint16_t *>(view.data) + tok * view.stride_tok + head * view.stride_head;
+    for (int i = id; i < C * 8 * PANELS; i += count) {
+        const int row = i / (8 * PANELS), piece = i % (8 * PANELS);
+        uint8_t *dst = tile + (piece >> 3) * panel_bytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+        if constexpr (VEC) {
+            const bool real = row < n && piece * 8 < dim;
+            cp_async16_or_zero(smem_u32(dst), real ? src + row * view.stride_tok + piece * 8 : src, real);
+        } else {
+            Raw<8> r;
+            r.zero();
+            if (row < n) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (piece * 8 + k < dim) r.set_elem(k, src[row * view.stride_tok + (piece * 8 + k) * view.stride_dim]);
+            }
+            *reinterpret_cast<uint4 *>(dst) = r.v;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ prep ----
+
+constexpr int kPrepThreads = 128;
+constexpr int kLd = 68;  // floats of a row of A in shared memory: 16-byte rows, spread over the banks
+
+struct PrepSmem {
+    float a[2][C * kLd];           // A, then T, of two value heads
+    float ghi[2][C], glo[2][C];    // G log2(e) as a float pair
+    float beta[2][C];
+    float rk[C], rq[C];            // factors of the rows of K and Q
+    double carry[2];
+    uint64_t bar;
+    uint32_t tmem;
+    int seq, abort;
+};
+
+// T = (I + A)^-1 for the unit lower triangular 64 x 64 matrix in `a` (strictly lower part A, zeros above), by 64 threads:
+// forward substitution of the two diagonal 32 x 32 blocks, a column a thread, then T21 = -T22 (A21 T11).  Substitution, not
+// a power series: its error stays at the rounding of T however alike the keys are.  The upper right block holds scratch.
+__device__ __forceinline__ void invert(float *a, int tid, int barrier) {
+    const int half = tid >> 5, j = tid & 31;
+    auto sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory"); };
+    float t[32];
+    {
+        float *d = a + half * (32 * kLd + 32);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < i; m += 4) {
+                const float4 r = *reinterpret_cast<const float4 *>(d + i * kLd + m);
+                acc[0] = fmaf(r.x, t[m], acc[0]);
+                acc[1] = fmaf(r.y, t[m + 1], acc[1]);
+                acc[2] = fmaf(r.z, t[m + 2], acc[2]);
+                acc[3] = fmaf(r.w, t[m + 3], acc[3]);
+            }
+            t[i] = (i == j ? 1.0f : 0.0f) - ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) d[i * kLd + j] = t[i];
+    }
+    sync();
+    // Two products of 32 x 32 blocks, 16 rows of column j a thread: X = A21 T11, then -T22 X.
+#pragma unroll 1
+    for (int step = 0; step < 2; ++step) {
+        const float *left = a + (32 + 16 * half) * kLd + 32 * step;
+        const float *right = a + 32 * step + j;
+        float *out = a + (16 * half + 32 * step) * kLd + 32 * (1 - step) + j;
+        const float sign = step ? -1.0f : 1.0f;
+#pragma unroll
+        for (int m = 0; m < 32; ++m) t[m] = right[m * kLd];
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < 32; m += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(left + i * kLd + m);
+                acc[0] = fmaf(v.x, t[m], acc[0]);
+                acc[1] = fmaf(v.y, t[m + 1], acc[1]);
+                acc[2] = fmaf(v.z, t[m + 2], acc[2]);
+                acc[3] = fmaf(v.w, t[m + 3], acc[3]);
+            }
+            out[i * kLd] = sign * ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+        }
+        sync();
+    }
+}
+
+// PANELS: dim_k rounded up to 64 PANELS.  V: rows of q and k allow 16-byte vectors.
+template <int PANELS, bool V>
+__global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_constant__ FwdArgs p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *ab = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    PrepSmem &sm = *reinterpret_cast<PrepSmem *>(ab + PANELS * 2 * kTile);
+    const ccv_gdr_args &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hk = blockIdx.x % a.num_k_heads, slot = blockIdx.x / a.num_k_heads;
+    wait_prior_grid();
+
+    // The sequence of this slot: the last i with first_slot(i) <= slot, found by a warp 32 candidates at a time.
+    if (warp == 0) {
+        int lo = 0, hi = p.batch;  // the answer is in [lo, hi)
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int i = lo + lane * step;
+            const bool below = i < hi && first_slot(p.query_start_loc[i], i) <= slot;
+            const int last = 31 - __clz(__ballot_sync(kFullMask, below) | 1);
+            lo += last * step;
+            hi = min(hi, lo + step);
+        }
+        if (lane == 0) sm.seq = lo;
+    }
+    if (tid == 0) {
+        sm.abort = 0;
+        mbar_init(&sm.bar, 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    const int seq = sm.seq;
+    const int s = p.query_start_loc[seq], e = p.query_start_loc[seq + 1];
+    if (!sequence_ok(s, e, p.total_tokens)) return;  // counted by the chunk kernel
+    const int chunk = slot - first_slot(s, seq);
+    if (chunk < 0 || chunk * C >= e - s) return;
+    if (p.cache_indices != nullptr && p.cache_indices[seq] == a.pad_slot_id) return;
+    const int t0 = s + chunk * C, n = min(C, e - t0);
+
+    // Panels of 128 rows: the chunk's keys, then its queries.
+    stage_rows<PANELS, V>(ab, 2 * kTile, a.k, t0, hk, n, a.dim_k, tid, kPrepThreads);
+    stage_rows<PANELS, V>(ab + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, tid, kPrepThreads);
+    if (warp == 0) tmem_alloc<64>(&sm.tmem);
+    cp_async_commit();
+    cp_async_wait<0>();
+    fence_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    if (tid == 0) {  // [K; Q] K^T, 128 x 64
+#pragma unroll
+        for (int ks = 0; ks < PANELS * 4; ++ks) {
+            const uint64_t d = smem_desc(smem_u32(ab) + (ks / 4) * 2 * kTile + (ks % 4) * 32, 0, 1024);
+            mma_ss(tmem, d, d, mma_desc(128, C, false), ks > 0);
+        }
+        mma_commit(&sm.bar);
+    }
+    // Meanwhile the rows' norms, a row a thread.
+    const int i = tid & (C - 1), side = tid >> 6;
+    {
+        float ss = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8 * PANELS; ++c) {
+            Raw<8> r;
+            r.v = *reinterpret_cast<const uint4 *>(ab + (c >> 3) * 2 * kTile + tid * 128 + (((c & 7) ^ (tid & 7)) << 4));
+            float f[8];
+            r.to_float(f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
+        }
+        const float r = a.qk_l2norm ? rsqrtf(ss + kGdrNormEps) : 1.0f;
+        if (side) sm.rq[i] = r * a.scale;
+        else sm.rk[i] = r;
+    }
+
+    // The value heads of this key head, two at a time, 64 threads each.
+    const int rep = a.num_v_heads / a.num_k_heads;
+    bool done = false;
+    for (int r0 = 0; r0 < rep; r0 += 2) {
+        const int nh = min(2, rep - r0);
+        auto block = [&](int w) { return p.heads + (static_cast<int64_t>(slot) * a.num_v_heads + hk * rep + r0 + w) * kHeadBytes; };
+        {   // gates, and G by a scan in 64 bits: a difference of two sums has to be exact to its own rounding
+            const int h = hk * rep + r0 + (side < nh ? side : 0);
+            float g = 0.0f, beta = 0.0f;
+            if (i < n) gdr_gates(a, (t0 + i) * a.gate_stride_tok + h * a.gate_stride_head, h, g, beta);
+            if (g < -200.0f) g = -200.0f;  // e^-200 is 0 in fp32; keeps -inf - -inf out of the differences
+            double sum = static_cast<double>(g) * 1.4426950408889634074;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const double o = __shfl_up_sync(kFullMask, sum, m);
+                if (lane >= m) sum += o;
+            }
+            if ((warp & 1) == 0 && lane == 31) sm.carry[side] = sum;
+            __syncthreads();
+            if (warp & 1) sum += sm.carry[side];
+            const float ghi = static_cast<float>(sum), glo = static_cast<float>(sum - ghi);
+            sm.ghi[side][i] = ghi;
+            sm.glo[side][i] = glo;
+            sm.beta[side][i] = beta;
+            __syncthreads();
+            if (side < nh) {
+                float *vec = reinterpret_cast<float *>(block(side) + kVec);
+                const float decay = ex2(ghi + glo), rk = sm.rk[i];
+                vec[kBeta * C + i] = beta;
+                vec[kKey * C + i] = beta * rk * decay;
+                vec[kState * C + i] = ex2((sm.ghi[side][C - 1] - ghi) + (sm.glo[side][C - 1] - glo)) * rk;
+                vec[kQuery * C + i] = sm.rq[i] * decay;
+                if (i == 0) vec[kMisc * C] = ex2(sm.ghi[side][C - 1] + sm.glo[side][C - 1]);
+            }
+        }
+        if (!done) {
+            if (!mbar_wait_warp(&sm.bar, 0, &sm.abort) && lane == 0) count_error(p.err_count);
+            tc_fence_after();
+            done = true;
+        }
+        // Rows of A (threads of K rows, to shared memory) and of P (threads of Q rows, to the workspace).
+        const uint32_t addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        for (int w = 0; w < nh; ++w) {
+            const float ghi = sm.ghi[w][i], glo = sm.glo[w][i];
+            const float own = side ? sm.rq[i] : sm.beta[w][i] * sm.rk[i];
+            uint8_t *out_p = block(w) + kP + i * 128;
+#pragma unroll
+            for (int j0 = 0; j0 < C; j0 += 32) {
+                float f[32];
+                tmem_load32(addr + j0, f);
+                tmem_wait_load();
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 gh = *reinterpret_cast<const float4 *>(&sm.ghi[w][j0 + j]);
+                    const float4 gl = *reinterpret_cast<const float4 *>(&sm.glo[w][j0 + j]);
+                    const float4 rh = *reinterpret_cast<const float4 *>(&sm.rk[j0 + j]);
+                    const float gj[4] = {gh.x, gh.y, gh.z, gh.w}, lj[4] = {gl.x, gl.y, gl.z, gl.w};
+                    const float rj[4] = {rh.x, rh.y, rh.z, rh.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const bool in = j0 + j + u < i + side;
+                        f[j + u] = in ? f[j + u] * (own * rj[u]) * ex2((ghi - gj[u]) + (glo - lj[u])) : 0.0f;
+                    }
+                }
+                if (side) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint4 hi, mid;
+                        split_bf16x2(f[8 * c], f[8 * c + 1], hi.x, mid.x);
+                        split_bf16x2(f[8 * c + 2], f[8 * c + 3], hi.y, mid.y);
+                        split_bf16x2(f[8 * c + 4], f[8 * c + 5], hi.z, mid.z);
+                        split_bf16x2(f[8 * c + 6], f[8 * c + 7], hi.w, mid.w);
+                        const int at = ((j0 / 8 + c) ^ (i & 7)) << 4;
+                        *reinterpret_cast<uint4 *>(out_p + at) = hi;
+                        *reinterpret_cast<uint4 *>(out_p + kTile + at) = mid;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4 *>(&sm.a[w][i * kLd + j0 + j]) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                }
+            }
+        }
+        __syncthreads();
+        if (side < nh) {
+            invert(sm.a[side], i, 1 + side);
+            uint8_t *out = block(side) + kT;
+            const int c = i & 7;
+#pragma unroll 2
+            for (int it = 0; it < 8; ++it) {
+                const int row = it * 8 + (i >> 3);
+                uint4 hi = make_uint4(0u, 0u, 0u, 0u), mid = hi, lo = hi;
+                if (row >= 32 || c < 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&sm.a[side][row * kLd + c * 8]);
+                    const float4 y = *reinterpret_cast<const float4 *>(&sm.a[side][row * kLd + c * 8 + 4]);
+                    split_bf16x3(x.x, x.y, hi.x, mid.x, lo.x);
+                    split_bf16x3(x.z, x.w, hi.y, mid.y, lo.y);
+                    split_bf16x3(y.x, y.y, hi.z, mid.z, lo.z);
+                    split_bf16x3(y.z, y.w, hi.w, mid.w, lo.w);
+                }
+                const int at = row * 128 + ((c ^ (row & 7)) << 4);
+                *reinterpret_cast<uint4 *>(out + at) = hi;
+                *reinterpret_cast<uint4 *>(out + kTile + at) = mid;
+                *reinterpret_cast<uint4 *>(out + 2 * kTile + at) = lo;
+            }
+        }
+        __syncthreads();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_free<64>(tmem);
+}
+
+// ----------------------------------------------------------------- chunks ----
+
+constexpr int kCompute = 256;                 // two warpgroups, each half of the columns of every row
+constexpr int kLoaders = 96;                  // three warps that copy; the fourth of their group issues the MMAs
+constexpr int kChunkThreads = kCompute + 128;
+constexpr int kStages = 2;
+constexpr int kIssueWarp = 8;
+// Registers a thread: 384 threads launch with 168 each, 64512 in all; the compute warpgroups take 208 and the other 88.
+constexpr int kComputeRegs = 208, kOtherRegs = 88;
+static_assert(kCompute * kComputeRegs + 128 * kOtherRegs <= kChunkThreads * 168, "register split");
+
+// Columns of tensor memory.  Operands in parts keep each warpgroup's share together, so that a thread overwrites only
+// columns that it alone has read.
+enum : uint32_t {
+    kColS = 0,       // 192: S^T in 3 parts (a warpgroup: 32 columns each); then what the chunk adds to S^T
+    kColP = 192,     // 64: S^T k^T
+    kColO = 256,     // 64: S^T q^T, then d P^T
+    kColR = 320,     // 96: R in 3 parts (a warpgroup: 16 columns each), then the decayed d in 3 parts
+    kColN = 416,     // 64: d, then d in 2 parts
+};
+
+template <int PANELS>
+struct Stage {
+    static constexpr int kq = PANELS * 2 * kTile;  // per panel: 64 rows of K, 64 of Q
+    static constexpr int v = kq;                   // 64 rows of 128 values, not swizzled
+    static constexpr int head = v + 2 * kTile;
+    static constexpr int bytes = (head + kHeadBytes + 1023) / 1024 * 1024;
+};
+
+struct ChunkSmem {
+    uint64_t full[kStages];
+    uint64_t mma_p, mma_o, mma_n, mma_delta, mma_out;   // completed by the tensor cores
+    uint64_t have_s, have_read, have_r, have_n;         // arrived on by the compute threads
+    uint64_t out_full, out_free;                        // the output tile: written by them, stored by a loader warp
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+};
+
+// V: the state allows 16-byte vectors.  VIO: rows of q, k, v and out do.
+template <int PANELS, bool V, bool VIO>
+__global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __grid_constant__ FwdArgs p, int slices) {
+    using St = Stage<PANELS>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *out_tile = base + kStages * St::bytes;  // 64 rows of 128 bf16 values
+    ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(out_tile + 2 * kTile);
+    const ccv_gdr_args &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slice = blockIdx.x % slices;
+    const int bh = blockIdx.x / slices;
+    const int h = bh % a.num_v_heads, seq = bh / a.num_v_heads;
+    const int hk = h / (a.num_v_heads / a.num_k_heads);
+    wait_prior_grid();
+
+    const int s = p.query_start_loc[seq], e = p.query_start_loc[seq + 1];
+    const int line = p.cache_indices != nullptr ? p.cache_indices[seq] : seq;
+    const bool counts = tid == 0 && slice == 0 && h == 0;
+    if (!sequence_ok(s, e, p.total_tokens)) {
+        if (counts) count_error(p.err_count);
+        return;
+    }
+    if (e == s || line == a.pad_slot_id) return;
+    if (a.state != nullptr && (line < 0 || line >= a.num_lines)) {
+        if (counts) count_error(p.err_count);
+        return;
+    }
+    const int chunks = (e - s + C - 1) / C;
+    const int slot0 = first_slot(s, seq);
+
+    if (tid == 0) {
+        sm.abort = 0;
+        for (uint64_t &b : sm.full) mbar_init(&b, kLoaders + 1);
+        for (uint64_t *b : {&sm.mma_p, &sm.mma_o, &sm.mma_n, &sm.mma_delta, &sm.mma_out, &sm.drain}) mbar_init(b, 1);
+        for (uint64_t *b : {&sm.have_s, &sm.have_read, &sm.have_r, &sm.have_n, &sm.out_full}) mbar_init(b, kCompute);
+        mbar_init(&sm.out_free, 32);
+        mbar_init_fence();
+    }
+    if (warp == kIssueWarp) tmem_alloc<512>(&sm.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+
+    if (warp >= kIssueWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kIssueWarp) {
+            if (lane == 0) {
+                int c = 0;
+                for (; c < chunks; ++c) {
+                    const uint32_t par = c & 1;
+                    const uint32_t kq = smem_u32(base + (c % kStages) * St::bytes);
+                    const uint32_t head = kq + St::head;
+                    if (!mbar_wait(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort)) break;
+                    if (!mbar_wait(&sm.have_s, par, &sm.abort)) break;
+                    tc_fence_after();
+                    auto s_col = [](int ks, int part) {
+                        return PANELS == 2 ? (ks / 4) * 96 + (ks % 4) * 8 + part * 32 : (ks / 2) * 48 + (ks % 2) * 8 + part * 16;
+                    };
+                    // S^T k^T, three parts of S; the keys are exact
+#pragma unroll
+                    for (int part = 0; part < 3; ++part)
+#pragma unroll
+                        for (int ks = 0; ks < PANELS * 4; ++ks)
+                            mma_ts(tmem + kColP, tmem + kColS + s_col(ks, part),
+                                   smem_desc(kq + (ks / 4) * 2 * kTile + (ks % 4) * 32, 0, 1024), mma_desc(128, C, false), part + ks > 0);
+                    mma_commit(&sm.mma_p);
+                    // S^T q^T, once the previous chunk's output has left these columns
+                    if (!mbar_wait(&sm.have_read, par, &sm.abort)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int ks = 0; ks < PANELS * 4; ++ks)
+                            mma_ts(tmem + kColO, tmem + kColS + s_col(ks, part),
+                                   smem_desc(kq + (ks / 4) * 2 * kTile + kTile + (ks % 4) * 32, 0, 1024), mma_desc(128, C, false),
+                                   part + ks > 0);
+                    mma_commit(&sm.mma_o);
+                    if (!mbar_wait(&sm.have_r, par, &sm.abort)) break;
+                    tc_fence_after();
+                    // d^T = R^T T^T: the six products of parts above 2^-24, largest first
+#pragma unroll
+                    for (int sum = 0; sum < 3; ++sum)
+#pragma unroll
+                        for (int part = 0; part <= sum; ++part)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_ts(tmem + kColN, tmem + kColR + (ks / 2) * 48 + (ks % 2) * 8 + part * 16,
+                                       smem_desc(head + kT + (sum - part) * kTile + ks * 32, 0, 1024), mma_desc(128, C, false),
+                                       sum + part + ks > 0);
+                    mma_commit(&sm.mma_n);
+                    if (!mbar_wait(&sm.have_n, par, &sm.abort)) break;
+                    tc_fence_after();
+                    // what the chunk adds to S^T: tokens are the inner axis, so the keys are read MN-major; 64 keys a time,
+                    // each into the columns of the warpgroup that holds them
+#pragma unroll
+                    for (int w = 0; w < 2; ++w)
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_ts(tmem + kColS + w * 48 * PANELS, tmem + kColR + (ks / 2) * 48 + (ks % 2) * 8 + part * 16,
+                                       smem_desc(kq + (PANELS == 2 ? w * 2 * kTile : w * 64) + ks * 2048, 0, 1024),
+                                       mma_desc(128, 32 * PANELS, true), part + ks > 0);
+                    mma_commit(&sm.mma_delta);
+                    // d P^T: the three products of parts above 2^-16
+#pragma unroll
+                    for (int term = 0; term < 3; ++term)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts(tmem + kColO, tmem + kColN + (ks / 2) * 32 + (ks % 2) * 8 + (term == 1 ? 16 : 0),
+                                   smem_desc(head + kP + (term == 2 ? kTile : 0) + ks * 32, 0, 1024), mma_desc(128, C, false),
+                                   term + ks > 0);
+                    mma_commit(&sm.mma_out);
+                }
+                if (c < chunks) {  // gave up: let the MMAs end before their memories go
+                    count_error(p.err_count);
+                    int quiet = 0;
+                    mma_commit(&sm.drain);
+                    mbar_wait(&sm.drain, 0, &quiet);
+                }
+            }
+            __syncwarp();
+        } else {
+            const int id = tid - (kIssueWarp + 1) * 32;
+            uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + slice * 128 * a.out.stride_dim;
+            const int width = min(128, a.dim_v - slice * 128);
+            ccv_heads_view vv = a.v;
+            vv.data = static_cast<const uint16_t *>(a.v.data) + slice * 128 * a.v.stride_dim;
+            int loaded = 0;
+            bool ok = true;
+            for (int c = 0; c < chunks + 2; ++c) {
+                // the output of chunk c - 2, once the compute threads have written it (while chunk c - 1 runs)
+                if (c >= 2) {
+                    ok = ok && mbar_wait_warp(&sm.out_full, c & 1, &sm.abort);
+                    if (ok && warp == kIssueWarp + 1) {
+                        const int t0 = s + (c - 2) * C, n = min(C, e - t0);
+                        if constexpr (VIO) {
+                            for (int r = lane; r < n; r += 32) bulk_store(out + (t0 + r) * a.out.stride_tok, out_tile + r * 256, width * 2);
+                            bulk_commit();
+                            bulk_wait<true>();
+                        } else {
+                            for (int i = lane; i < n * 128; i += 32)
+                                if ((i & 127) < width)
+                                    out[(t0 + (i >> 7)) * a.out.stride_tok + (i & 127) * a.out.stride_dim] =
+                                        reinterpret_cast<const uint16_t *>(out_tile)[i];
+                        }
+                        mbar_arrive(&sm.out_free);
+                    }
+                }
+                if (!ok) break;
+                if (c >= chunks) continue;
+                // That output also says that chunk c - 2 is done with its stage.
+                uint8_t *st = base + (c % kStages) * St::bytes;
+                uint64_t *bar = &sm.full[c % kStages];
+                const int t0 = s + c * C, n = min(C, e - t0);
+                if (id == 0) {
+                    mbar_expect_tx(bar, kHeadBytes);
+                    bulk_load(st + St::head, p.heads + (static_cast<int64_t>(slot0 + c) * a.num_v_heads + h) * kHeadBytes, kHeadBytes, bar);
+                }
+                stage_rows<PANELS, VIO>(st, 2 * kTile, a.k, t0, hk, n, a.dim_k, id, kLoaders);
+                stage_rows<PANELS, VIO>(st + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, id, kLoaders);
+                // V: rows of 128 values, token after token
+                const uint16_t *src = static_cast<const uint16_t *>(vv.data) + t0 * vv.stride_tok + h * vv.stride_head;
+                for (int i = id; i < C * 16; i += kLoaders) {
+                    const int row = i >> 4, piece = i & 15;
+                    uint8_t *dst = st + St::v + row * 256 + piece * 16;
+                    if constexpr (VIO) {
+                        const bool real = row < n && piece * 8 < width;
+                        cp_async16_or_zero(smem_u32(dst), real ? src + row * vv.stride_tok + piece * 8 : src, real);
+                    } else {
+                        Raw<8> r;
+                        r.zero();
+                        if (row < n) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (piece * 8 + k < width) r.set_elem(k, src[row * vv.stride_tok + (piece * 8 + k) * vv.stride_dim]);
+                        }
+                        *reinterpret_cast<uint4 *>(dst) = r.v;
+                    }
+                }
+                if constexpr (VIO) {
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                }
+                fence_async_shared();
+                mbar_arrive(bar);
+                loaded = c + 1;
+            }
+            if (!ok) {  // gave up: let the copies land before the shared memory goes
+                int quiet = 0;
+                for (int i = 0; i < loaded; ++i)
+                    if (i + kStages >= loaded) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1, &quiet);
+            }
+            bulk_wait<false>();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+        constexpr int KH = 32 * PANELS;  // keys of the state a thread holds
+        const int wg = warp >> 2, d = (warp & 3) * 32 + lane, row = slice * 128 + d;
+        const bool live = row < a.dim_v;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const bool init = a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
+        float *sp = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + row * a.s_stride_v : nullptr;
+
+        float st[KH];  // this thread's part of row d of S
+#pragma unroll
+        for (int k = 0; k < KH; k += 4) {
+            const int kk = wg * KH + k;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (init && live) {
+                if constexpr (V) {
+                    if (kk < a.dim_k) x = *reinterpret_cast<const float4 *>(sp + kk);
+                } else {
+                    if (kk < a.dim_k) x.x = sp[kk * a.s_stride_k];
+                    if (kk + 1 < a.dim_k) x.y = sp[(kk + 1) * a.s_stride_k];
+                    if (kk + 2 < a.dim_k) x.z = sp[(kk + 2) * a.s_stride_k];
+                    if (kk + 3 < a.dim_k) x.w = sp[(kk + 3) * a.s_stride_k];
+                }
+            }
+            st[k] = x.x; st[k + 1] = x.y; st[k + 2] = x.z; st[k + 3] = x.w;
+        }
+        auto stage = [&](int c) { return base + (c % kStages) * St::bytes; };
+        auto scalars = [&](int c) { return reinterpret_cast<const float *>(stage(c) + St::head + kVec); };
+        // d P^T of chunk c onto oi, into the output tile
+        float oi[32];
+        auto finish = [&](int c) {
+            float x[32];
+            tmem_load32(lanes + kColO + wg * 32, x);
+            tmem_wait_load();
+            tc_fence_before();
+            mbar_arrive(&sm.have_read);
+            // the tile is free once the output before last has been read from it
+            if (c > 0 && !mbar_wait_warp(&sm.out_free, (c - 1) & 1, &sm.abort)) return false;
+            uint16_t *o = reinterpret_cast<uint16_t *>(out_tile) + wg * 32 * 128 + d;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i * 128] = round_bf16(oi[i] + x[i]);
+            fence_async_shared();
+            mbar_arrive(&sm.out_full);
+            return true;
+        };
+
+        bool ok = true;
+        float gamma = 1.0f;
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t par = c & 1;
+            // S^T <- e^{G_C} S^T + what the last chunk adds, and its parts
+            if (c > 0) {
+                if (!(ok = mbar_wait_warp(&sm.mma_delta, par ^ 1, &sm.abort))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k0 = 0; k0 < KH; k0 += 32) {
+                    float x[32];
+                    tmem_load32(lanes + kColS + wg * 48 * PANELS + k0, x);
+                    tmem_wait_load();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) st[k0 + k] = fmaf(gamma, st[k0 + k], x[k]);
+                }
+            }
+#pragma unroll
+            for (int k0 = 0; k0 < KH; k0 += 32) {
+                uint32_t hi[16], mid[16], lo[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) split_bf16x3(st[k0 + 2 * k], st[k0 + 2 * k + 1], hi[k], mid[k], lo[k]);
+                const uint32_t at = lanes + kColS + wg * 48 * PANELS + k0 / 2;
+                tmem_store16(at, hi);
+                tmem_store16(at + KH / 2, mid);
+                tmem_store16(at + KH, lo);
+            }
+            tmem_wait_store();
+            tc_fence_before();
+            mbar_arrive(&sm.have_s);
+
+            if (c > 0) {  // the output of the chunk before
+                if (!(ok = mbar_wait_warp(&sm.mma_out, par ^ 1, &sm.abort))) break;
+                tc_fence_after();
+                if (!(ok = finish(c - 1))) break;
+            } else {
+                mbar_arrive(&sm.have_read);
+            }
+            if (!(ok = mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
+            const float *f = scalars(c) + wg * 32;
+            const uint16_t *v = reinterpret_cast<const uint16_t *>(stage(c) + St::v) + wg * 32 * 128 + d;
+            float vb[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) vb[i] = bf16_bits(v[i * 128]) * f[kBeta * C + i];
+
+            // R = b v - b e^G S k
+            if (!(ok = mbar_wait_warp(&sm.mma_p, par, &sm.abort))) break;
+            tc_fence_after();
+            {
+                float x[32];
+                tmem_load32(lanes + kColP + wg * 32, x);
+                tmem_wait_load();
+                uint32_t hi[16], mid[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    split_bf16x3(fmaf(-f[kKey * C + 2 * i], x[2 * i], vb[2 * i]),
+                                 fmaf(-f[kKey * C + 2 * i + 1], x[2 * i + 1], vb[2 * i + 1]), hi[i], mid[i], lo[i]);
+                tmem_store16(lanes + kColR + wg * 48, hi);
+                tmem_store16(lanes + kColR + wg * 48 + 16, mid);
+                tmem_store16(lanes + kColR + wg * 48 + 32, lo);
+            }
+            tmem_wait_store();
+            tc_fence_before();
+            mbar_arrive(&sm.have_r);
+            if (!(ok = mbar_wait_warp(&sm.mma_o, par, &sm.abort))) break;
+            tc_fence_after();
+            tmem_load32(lanes + kColO + wg * 32, oi);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) oi[i] *= f[kQuery * C + i];
+
+            // d, decayed for the state (3 parts) and for the output (2)
+            if (!(ok = mbar_wait_warp(&sm.mma_n, par, &sm.abort))) break;
+            tc_fence_after();
+            {
+                float x[32];
+                tmem_load32(lanes + kColN + wg * 32, x);
+                tmem_wait_load();
+                uint32_t hi[16], mid[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    split_bf16x3(f[kState * C + 2 * i] * x[2 * i], f[kState * C + 2 * i + 1] * x[2 * i + 1], hi[i], mid[i], lo[i]);
+                tmem_store16(lanes + kColR + wg * 48, hi);
+                tmem_store16(lanes + kColR + wg * 48 + 16, mid);
+                tmem_store16(lanes + kColR + wg * 48 + 32, lo);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) split_bf16x2(x[2 * i], x[2 * i + 1], hi[i], mid[i]);
+                tmem_store16(lanes + kColN + wg * 32, hi);
+                tmem_store16(lanes + kColN + wg * 32 + 16, mid);
+            }
+            tmem_wait_store();
+            tc_fence_before();
+            mbar_arrive(&sm.have_n);
+            gamma = scalars(c)[kMisc * C];
+        }
+        // the last chunk's output and the final state
+        if (ok) ok = mbar_wait_warp(&sm.mma_out, (chunks - 1) & 1, &sm.abort);
+        if (ok) {
+            tc_fence_after();
+            finish(chunks - 1);
+#pragma unroll
+            for (int k0 = 0; k0 < KH; k0 += 32) {
+                float x[32];
+                tmem_load32(lanes + kColS + wg * 48 * PANELS + k0, x);
+                tmem_wait_load();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) st[k0 + k] = fmaf(gamma, st[k0 + k], x[k]);
+            }
+            if (sp != nullptr && live) {
+#pragma unroll
+                for (int k = 0; k < KH; k += 4) {
+                    const int kk = wg * KH + k;
+                    if constexpr (V) {
+                        if (kk < a.dim_k) *reinterpret_cast<float4 *>(sp + kk) = make_float4(st[k], st[k + 1], st[k + 2], st[k + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (kk + i < a.dim_k) sp[(kk + i) * a.s_stride_k] = st[k + i];
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == kIssueWarp) tmem_free<512>(tmem);
+}
+
+// ------------------------------------------------------------------- host ----
+
+template <int PANELS>
+constexpr size_t prep_smem() { return 1024 + PANELS * 2 * kTile + sizeof(PrepSmem); }
+template <int PANELS>
+constexpr size_t chunk_smem() { return 1024 + kStages * Stage<PANELS>::bytes + 2 * kTile + sizeof(ChunkSmem); }
+
+template <int PANELS, bool VS, bool VIO>
+int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
+    int dev = 0;
+    current_device_sms(&dev);
+    cudaError_t err;
+    if (resident_blocks<gdr_prep_kernel<PANELS, VIO>>(kPrepThreads, prep_smem<PANELS>(), dev, &err) == 0 ||
+        resident_blocks<gdr_chunk_kernel<PANELS, VS, VIO>>(kChunkThreads, chunk_smem<PANELS>(), dev, &err) == 0)
+        return static_cast<int>(err);
+    const int64_t prep = static_cast<int64_t>(p.slots) * p.a.num_k_heads;
+    const int slices = (p.a.dim_v + 127) / 128;
+    const int64_t blocks = static_cast<int64_t>(p.batch) * p.a.num_v_heads * slices;
+    if (prep > 0x7fffffff || blocks > 0x7fffffff) return CCV_ERR_SIZE;
+    const int status = launch_pdl(gdr_prep_kernel<PANELS, VIO>, dim3(static_cast<unsigned>(prep)), dim3(kPrepThreads),
+                                  prep_smem<PANELS>(), stream, p);
+    if (status != CCV_OK) return status;
+    return launch_pdl(gdr_chunk_kernel<PANELS, VS, VIO>, dim3(static_cast<unsigned>(blocks)), dim3(kChunkThreads),
+                      chunk_smem<PANELS>(), stream, p, slices);
+}
+
+template <int PANELS>
+int launch_chunked(const FwdArgs &p, bool vs, bool vio, cudaStream_t stream) {
+    if (vio) return vs ? launch_chunked<PANELS, true, true>(p, stream) : launch_chunked<PANELS, false, true>(p, stream);
+    return vs ? launch_chunked<PANELS, true, false>(p, stream) : launch_chunked<PANELS, false, false>(p, stream);
+}
+
+bool chunked_dims(int dim_k) { return dim_k <= 128; }
+
+// CCV_GDR_PATH=recurrent or =chunked, read at each call, forces one form (for testing and tuning).
+bool use_chunked(const ccv_gdr_args &a, int batch, int total) {
+    if (!chunked_dims(a.dim_k)) return false;
+    const char *path = std::getenv("CCV_GDR_PATH");
+    if (path != nullptr && std::strcmp(path, "recurrent") == 0) return false;
+    if (path != nullptr && std::strcmp(path, "chunked") == 0) return true;
+    return true;
+}
+
+int64_t slot_count(int total_tokens, int batch) { return static_cast<int64_t>(total_tokens / C) + batch; }
+
+}  // namespace
+}  // namespace ccv
+
 extern "C" int64_t gdr_fwd_workspace(int total_tokens, int batch, int num_k_heads, int num_v_heads, int dim_k, int dim_v) {
-    return 0;
+    using namespace ccv;
+    if (total_tokens <= 0 || batch <= 0 || num_k_heads <= 0 || num_v_heads <= 0 || dim_k <= 0 || dim_v <= 0) return 0;
+    return chunked_dims(dim_k) ? slot_count(total_tokens, batch) * num_v_heads * kHeadBytes : 0;
 }
 
 extern "C" int gdr_fwd(const ccv_gdr_args *args, const int32_t *query_start_loc, int batch, const int32_t *cache_indices,
@@ -15,7 +810,24 @@ extern "C" int gdr_fwd(const ccv_gdr_args *args, const int32_t *query_start_loc,
     if (has_initial_state != nullptr && args->state == nullptr) return CCV_ERR_ARGUMENT;
     if (batch == 0 || total_tokens == 0 || args->num_v_heads == 0 || args->dim_v == 0 || args->dim_k == 0) return CCV_OK;
     if (query_start_loc == nullptr) return CCV_ERR_NULL_POINTER;
-    const GdrRows rows{query_start_loc, cache_indices, has_initial_state, nullptr, nullptr, 0, 0, 0, batch, 0,
-                       total_tokens, err_count};
-    return gdr_launch_recurrent(*args, rows, stream);
+    const ccv_gdr_args &a = *args;
+    const int64_t need = gdr_fwd_workspace(total_tokens, batch, a.num_k_heads, a.num_v_heads, a.dim_k, a.dim_v);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 127u) != 0))
+        return CCV_ERR_WORKSPACE;
+    if (!use_chunked(a, batch, total_tokens)) {
+        const GdrRows rows{query_start_loc, cache_indices, has_initial_state, nullptr, nullptr, 0, 0, 0, batch, 0,
+                           total_tokens, err_count};
+        return gdr_launch_recurrent(a, rows, stream);
+    }
+    const int64_t slots = slot_count(total_tokens, batch);
+    if (slots > 0x7fffffff) return CCV_ERR_SIZE;
+    const FwdArgs p{a, query_start_loc, cache_indices, has_initial_state, batch, total_tokens, static_cast<int>(slots),
+                    static_cast<uint8_t *>(workspace), err_count};
+    auto vec = [](const ccv_heads_view &v) {
+        return aligned16(v.data) && v.stride_dim == 1 && v.stride_tok % 8 == 0 && v.stride_head % 8 == 0;
+    };
+    const bool vio = a.dim_k % 8 == 0 && a.dim_v % 8 == 0 && vec(a.q) && vec(a.k) && vec(a.v) && vec(a.out);
+    const bool vs = a.state == nullptr || (a.dim_k % 4 == 0 && aligned16(a.state) && a.s_stride_k == 1 && a.s_stride_line % 4 == 0 &&
+                                           a.s_stride_head % 4 == 0 && a.s_stride_v % 4 == 0);
+    return a.dim_k <= 64 ? launch_chunked<1>(p, vs, vio, stream) : launch_chunked<2>(p, vs, vio, stream);
 }

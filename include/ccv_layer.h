@@ -50,8 +50,6 @@ typedef struct ccv_heads_view {
  *               dt_bias of num_v_heads: g = -exp(a_log) softplus(x + dt_bias),
  *               b = 1 / (1 + exp(-y)).
  * state         pool (num_lines, num_v_heads, dim_v, dim_k) fp32.
- * The keys are expected to satisfy b |k|^2 <= 2 (always so with qk_l2norm and
- * b <= 2): beyond that the recurrence itself grows without bound.
  * dim_k <= 256 and dim_v <= 1024 (CCV_ERR_DIM).
  */
 typedef struct ccv_gdr_args {
@@ -74,7 +72,9 @@ typedef struct ccv_gdr_args {
  * ccv_fwd: sequence i owns tokens [qsl[i], qsl[i+1]) and state line
  * cache_indices[i] (line i when NULL); a line equal to pad_slot_id skips the
  * sequence; without an initial state the state starts at zero, and the final
- * state is written to the line either way.  args->state may be NULL (zero
+ * state is written to the line either way.  Offsets must not decrease: a
+ * sequence whose own offsets do, or leave [0, total_tokens], is skipped and
+ * counted in err_count, and the others' results are then undefined.  args->state may be NULL (zero
  * start, no write-back; then has_initial_state must be NULL:
  * CCV_ERR_ARGUMENT).  A sequence of no tokens writes nothing.
  * workspace     gdr_fwd_workspace(...) bytes, 128-byte aligned, not shared
