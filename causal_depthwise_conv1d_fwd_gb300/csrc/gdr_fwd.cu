@@ -201,9 +201,9 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
 #pragma unroll
         for (int ks = 0; ks < PANELS * 4; ++ks) {
             const uint64_t d = smem_desc(smem_u32(ab) + (ks / 4) * 2 * kTile + (ks % 4) * 32, 0, 1024);
-            mma_ss(tmem, d, d, mma_desc(128, C, false), ks > 0);
+            mma_ss(tmem, d, d, mma_desc(128, C, false), ks > 0, 1);
         }
-        mma_commit(&sm.bar);
+        mma_commit(&sm.bar, 1);
     }
     // Meanwhile the rows' norms, a row a thread.
     const int i = tid & (C - 1), side = tid >> 6;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
                 float *vec = reinterpret_cast<float *>(block(side) + kVec);
                 const float decay = ex2(ghi + glo), rk = sm.rk[i];
                 vec[kBeta * C + i] = beta;
-                vec[kKey * C + i] = beta * rk * decay;
+                vec[kKey * C + i] = -beta * rk * decay;
                 vec[kState * C + i] = ex2((sm.ghi[side][C - 1] - ghi) + (sm.glo[side][C - 1] - glo)) * rk;
                 vec[kQuery * C + i] = sm.rq[i] * decay;
                 if (i == 0) vec[kMisc * C] = ex2(sm.ghi[side][C - 1] + sm.glo[side][C - 1]);
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
 #pragma unroll
             for (int j0 = 0; j0 < C; j0 += 32) {
                 float f[32];
-                tmem_load32(addr + j0, f);
+                tmem_load(addr + j0, f);
                 tmem_wait_load();
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
@@ -291,10 +291,10 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint4 hi, mid;
-                        split_bf16x2(f[8 * c], f[8 * c + 1], hi.x, mid.x);
-                        split_bf16x2(f[8 * c + 2], f[8 * c + 3], hi.y, mid.y);
-                        split_bf16x2(f[8 * c + 4], f[8 * c + 5], hi.z, mid.z);
-                        split_bf16x2(f[8 * c + 6], f[8 * c + 7], hi.w, mid.w);
+                        split_bf16x2(pack2(f[8 * c], f[8 * c + 1]), hi.x, mid.x);
+                        split_bf16x2(pack2(f[8 * c + 2], f[8 * c + 3]), hi.y, mid.y);
+                        split_bf16x2(pack2(f[8 * c + 4], f[8 * c + 5]), hi.z, mid.z);
+                        split_bf16x2(pack2(f[8 * c + 6], f[8 * c + 7]), hi.w, mid.w);
                         const int at = ((j0 / 8 + c) ^ (i & 7)) << 4;
                         *reinterpret_cast<uint4 *>(out_p + at) = hi;
                         *reinterpret_cast<uint4 *>(out_p + kTile + at) = mid;
@@ -318,10 +318,10 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
                 if (row >= 32 || c < 4) {
                     const float4 x = *reinterpret_cast<const float4 *>(&sm.a[side][row * kLd + c * 8]);
                     const float4 y = *reinterpret_cast<const float4 *>(&sm.a[side][row * kLd + c * 8 + 4]);
-                    split_bf16x3(x.x, x.y, hi.x, mid.x, lo.x);
-                    split_bf16x3(x.z, x.w, hi.y, mid.y, lo.y);
-                    split_bf16x3(y.x, y.y, hi.z, mid.z, lo.z);
-                    split_bf16x3(y.z, y.w, hi.w, mid.w, lo.w);
+                    split_bf16x3(pack2(x.x, x.y), hi.x, mid.x, lo.x);
+                    split_bf16x3(pack2(x.z, x.w), hi.y, mid.y, lo.y);
+                    split_bf16x3(pack2(y.x, y.y), hi.z, mid.z, lo.z);
+                    split_bf16x3(pack2(y.z, y.w), hi.w, mid.w, lo.w);
                 }
                 const int at = row * 128 + ((c ^ (row & 7)) << 4);
                 *reinterpret_cast<uint4 *>(out + at) = hi;
@@ -357,19 +357,24 @@ enum : uint32_t {
     kColN = 416,     // 64: d, then d in 2 parts
 };
 
+// V and the output cross shared memory as rows of 64 tokens (144 bytes apart, which spreads them over the banks): the
+// compute threads own a row each.  The loader warps turn them from and to rows of values.
+constexpr int kRowBytes = 144;
+constexpr int kRawBytes = 272;  // a token's 128 values on the way in
+
 template <int PANELS>
 struct Stage {
     static constexpr int kq = PANELS * 2 * kTile;  // per panel: 64 rows of K, 64 of Q
-    static constexpr int v = kq;                   // 64 rows of 128 values, not swizzled
-    static constexpr int head = v + 2 * kTile;
+    static constexpr int v = kq;
+    static constexpr int head = v + 128 * kRowBytes;
     static constexpr int bytes = (head + kHeadBytes + 1023) / 1024 * 1024;
 };
 
 struct ChunkSmem {
-    uint64_t full[kStages];
-    uint64_t mma_p, mma_o, mma_n, mma_delta, mma_out;   // completed by the tensor cores
-    uint64_t have_s, have_read, have_r, have_n;         // arrived on by the compute threads
-    uint64_t out_full, out_free;                        // the output tile: written by them, stored by a loader warp
+    uint64_t full[kStages], empty[kStages];               // a stage is loaded; its chunk's MMAs, the last to use it, are done
+    uint64_t mma_p, mma_o, mma_n, mma_delta, mma_out;     // completed by the tensor cores
+    uint64_t have_s, have_read, have_r, have_vs, have_d;  // arrived on by the compute threads
+    uint64_t out_full, out_free;                          // the output tile: written by them, stored by the loaders
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -381,10 +386,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     using St = Stage<PANELS>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *out_tile = base + kStages * St::bytes;  // 64 rows of 128 bf16 values
-    ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(out_tile + 2 * kTile);
+    uint8_t *out_tile = base + kStages * St::bytes;
+    uint8_t *raw_v = out_tile + 128 * kRowBytes;
+    ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(raw_v + C * kRawBytes);
     const ccv_gdr_args &a = p.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFullMask, tid >> 5, 0);
     const int slice = blockIdx.x % slices;
     const int bh = blockIdx.x / slices;
     const int h = bh % a.num_v_heads, seq = bh / a.num_v_heads;
@@ -409,168 +416,177 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     if (tid == 0) {
         sm.abort = 0;
         for (uint64_t &b : sm.full) mbar_init(&b, kLoaders + 1);
+        for (uint64_t &b : sm.empty) mbar_init(&b, 1);
         for (uint64_t *b : {&sm.mma_p, &sm.mma_o, &sm.mma_n, &sm.mma_delta, &sm.mma_out, &sm.drain}) mbar_init(b, 1);
-        for (uint64_t *b : {&sm.have_s, &sm.have_read, &sm.have_r, &sm.have_n, &sm.out_full}) mbar_init(b, kCompute);
-        mbar_init(&sm.out_free, 32);
+        for (uint64_t *b : {&sm.have_s, &sm.have_read, &sm.have_r, &sm.have_vs, &sm.have_d, &sm.out_full}) mbar_init(b, kCompute);
+        mbar_init(&sm.out_free, kLoaders);
         mbar_init_fence();
     }
     if (warp == kIssueWarp) tmem_alloc<512>(&sm.tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem;
+    const uint32_t tmem = __shfl_sync(kFullMask, sm.tmem, 0);
 
     if (warp >= kIssueWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kIssueWarp) {
-            if (lane == 0) {
-                int c = 0;
-                for (; c < chunks; ++c) {
-                    const uint32_t par = c & 1;
-                    const uint32_t kq = smem_u32(base + (c % kStages) * St::bytes);
-                    const uint32_t head = kq + St::head;
-                    if (!mbar_wait(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort)) break;
-                    if (!mbar_wait(&sm.have_s, par, &sm.abort)) break;
-                    tc_fence_after();
-                    auto s_col = [](int ks, int part) {
-                        return PANELS == 2 ? (ks / 4) * 96 + (ks % 4) * 8 + part * 32 : (ks / 2) * 48 + (ks % 2) * 8 + part * 16;
-                    };
-                    // S^T k^T, three parts of S; the keys are exact
+            const uint32_t el = elect_lane();
+            const uint32_t smem0 = __shfl_sync(kFullMask, smem_u32(base), 0);
+            auto s_col = [](int ks, int part) {
+                return PANELS == 2 ? (ks / 4) * 96 + (ks % 4) * 8 + part * 32 : (ks / 2) * 48 + (ks % 2) * 8 + part * 16;
+            };
+            int c = 0;
+            for (; c < chunks; ++c) {
+                const uint32_t par = c & 1;
+                const uint32_t kq = smem0 + (c % kStages) * St::bytes;
+                const uint32_t head = kq + St::head;
+                if (!mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort)) break;
+                if (!mbar_wait_warp(&sm.have_s, par, &sm.abort)) break;
+                tc_fence_after();
+                // S^T k^T, three parts of S; the keys are exact
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < PANELS * 4; ++ks)
+                        mma_ts(tmem + kColP, tmem + kColS + s_col(ks, part),
+                               smem_desc(kq + (ks / 4) * 2 * kTile + (ks % 4) * 32, 0, 1024), mma_desc(128, C, false), part + ks > 0, el);
+                mma_commit(&sm.mma_p, el);
+                // S^T q^T, once the previous chunk's output has left these columns
+                if (!mbar_wait_warp(&sm.have_read, par, &sm.abort)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < PANELS * 4; ++ks)
+                        mma_ts(tmem + kColO, tmem + kColS + s_col(ks, part),
+                               smem_desc(kq + (ks / 4) * 2 * kTile + kTile + (ks % 4) * 32, 0, 1024), mma_desc(128, C, false),
+                               part + ks > 0, el);
+                mma_commit(&sm.mma_o, el);
+                if (!mbar_wait_warp(&sm.have_r, par, &sm.abort)) break;
+                tc_fence_after();
+                // d^T = R^T T^T: the six products of parts above 2^-24, largest first
+#pragma unroll
+                for (int sum = 0; sum < 3; ++sum)
+#pragma unroll
+                    for (int part = 0; part <= sum; ++part)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts(tmem + kColN, tmem + kColR + (ks / 2) * 48 + (ks % 2) * 8 + part * 16,
+                                   smem_desc(head + kT + (sum - part) * kTile + ks * 32, 0, 1024), mma_desc(128, C, false),
+                                   sum + part + ks > 0, el);
+                mma_commit(&sm.mma_n, el);
+                if (!mbar_wait_warp(&sm.have_vs, par, &sm.abort)) break;
+                if (!mbar_wait_warp(&sm.mma_o, par, &sm.abort)) break;  // S is about to be overwritten
+                tc_fence_after();
+                // what the chunk adds to S^T: tokens are the inner axis, so the keys are read MN-major; half of the keys a
+                // time, each half into the columns of the warpgroup that holds them
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
 #pragma unroll
                     for (int part = 0; part < 3; ++part)
 #pragma unroll
-                        for (int ks = 0; ks < PANELS * 4; ++ks)
-                            mma_ts(tmem + kColP, tmem + kColS + s_col(ks, part),
-                                   smem_desc(kq + (ks / 4) * 2 * kTile + (ks % 4) * 32, 0, 1024), mma_desc(128, C, false), part + ks > 0);
-                    mma_commit(&sm.mma_p);
-                    // S^T q^T, once the previous chunk's output has left these columns
-                    if (!mbar_wait(&sm.have_read, par, &sm.abort)) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int ks = 0; ks < PANELS * 4; ++ks)
-                            mma_ts(tmem + kColO, tmem + kColS + s_col(ks, part),
-                                   smem_desc(kq + (ks / 4) * 2 * kTile + kTile + (ks % 4) * 32, 0, 1024), mma_desc(128, C, false),
-                                   part + ks > 0);
-                    mma_commit(&sm.mma_o);
-                    if (!mbar_wait(&sm.have_r, par, &sm.abort)) break;
-                    tc_fence_after();
-                    // d^T = R^T T^T: the six products of parts above 2^-24, largest first
-#pragma unroll
-                    for (int sum = 0; sum < 3; ++sum)
-#pragma unroll
-                        for (int part = 0; part <= sum; ++part)
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_ts(tmem + kColN, tmem + kColR + (ks / 2) * 48 + (ks % 2) * 8 + part * 16,
-                                       smem_desc(head + kT + (sum - part) * kTile + ks * 32, 0, 1024), mma_desc(128, C, false),
-                                       sum + part + ks > 0);
-                    mma_commit(&sm.mma_n);
-                    if (!mbar_wait(&sm.have_n, par, &sm.abort)) break;
-                    tc_fence_after();
-                    // what the chunk adds to S^T: tokens are the inner axis, so the keys are read MN-major; 64 keys a time,
-                    // each into the columns of the warpgroup that holds them
-#pragma unroll
-                    for (int w = 0; w < 2; ++w)
-#pragma unroll
-                        for (int part = 0; part < 3; ++part)
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_ts(tmem + kColS + w * 48 * PANELS, tmem + kColR + (ks / 2) * 48 + (ks % 2) * 8 + part * 16,
-                                       smem_desc(kq + (PANELS == 2 ? w * 2 * kTile : w * 64) + ks * 2048, 0, 1024),
-                                       mma_desc(128, 32 * PANELS, true), part + ks > 0);
-                    mma_commit(&sm.mma_delta);
-                    // d P^T: the three products of parts above 2^-16
-#pragma unroll
-                    for (int term = 0; term < 3; ++term)
-#pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(tmem + kColO, tmem + kColN + (ks / 2) * 32 + (ks % 2) * 8 + (term == 1 ? 16 : 0),
-                                   smem_desc(head + kP + (term == 2 ? kTile : 0) + ks * 32, 0, 1024), mma_desc(128, C, false),
-                                   term + ks > 0);
-                    mma_commit(&sm.mma_out);
-                }
-                if (c < chunks) {  // gave up: let the MMAs end before their memories go
-                    count_error(p.err_count);
-                    int quiet = 0;
-                    mma_commit(&sm.drain);
-                    mbar_wait(&sm.drain, 0, &quiet);
-                }
+                            mma_ts(tmem + kColS + w * 48 * PANELS, tmem + kColR + (ks / 2) * 48 + (ks % 2) * 8 + part * 16,
+                                   smem_desc(kq + (PANELS == 2 ? w * 2 * kTile : w * 64) + ks * 2048, 0, 1024),
+                                   mma_desc(128, 32 * PANELS, true), part + ks > 0, el);
+                mma_commit(&sm.mma_delta, el);
+                if (!mbar_wait_warp(&sm.have_d, par, &sm.abort)) break;
+                tc_fence_after();
+                // d P^T: the three products of parts above 2^-16
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ts(tmem + kColO, tmem + kColN + (ks / 2) * 32 + (ks % 2) * 8 + (term == 1 ? 16 : 0),
+                               smem_desc(head + kP + (term == 2 ? kTile : 0) + ks * 32, 0, 1024), mma_desc(128, C, false),
+                               term + ks > 0, el);
+                mma_commit(&sm.mma_out, el);
+                mma_commit(&sm.empty[c % kStages], el);
             }
-            __syncwarp();
+            if (c < chunks) {  // gave up: let the MMAs end before their memories go
+                if (el) count_error(p.err_count);
+                int quiet = 0;
+                mma_commit(&sm.drain, el);
+                mbar_wait_warp(&sm.drain, 0, &quiet);
+            }
         } else {
-            const int id = tid - (kIssueWarp + 1) * 32;
-            uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + slice * 128 * a.out.stride_dim;
+            const int id = tid - (kIssueWarp + 1) * 32, lw = warp - (kIssueWarp + 1);
+            auto sync_loaders = [] { asm volatile("bar.sync 1, %0;" ::"n"(kLoaders) : "memory"); };
             const int width = min(128, a.dim_v - slice * 128);
-            ccv_heads_view vv = a.v;
-            vv.data = static_cast<const uint16_t *>(a.v.data) + slice * 128 * a.v.stride_dim;
+            const uint16_t *vsrc = static_cast<const uint16_t *>(a.v.data) + h * a.v.stride_head + slice * 128 * a.v.stride_dim;
+            uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + slice * 128 * a.out.stride_dim;
             int loaded = 0;
             bool ok = true;
             for (int c = 0; c < chunks + 2; ++c) {
-                // the output of chunk c - 2, once the compute threads have written it (while chunk c - 1 runs)
-                if (c >= 2) {
-                    ok = ok && mbar_wait_warp(&sm.out_full, c & 1, &sm.abort);
-                    if (ok && warp == kIssueWarp + 1) {
-                        const int t0 = s + (c - 2) * C, n = min(C, e - t0);
-                        if constexpr (VIO) {
-                            for (int r = lane; r < n; r += 32) bulk_store(out + (t0 + r) * a.out.stride_tok, out_tile + r * 256, width * 2);
-                            bulk_commit();
-                            bulk_wait<true>();
-                        } else {
-                            for (int i = lane; i < n * 128; i += 32)
-                                if ((i & 127) < width)
-                                    out[(t0 + (i >> 7)) * a.out.stride_tok + (i & 127) * a.out.stride_dim] =
-                                        reinterpret_cast<const uint16_t *>(out_tile)[i];
-                        }
-                        mbar_arrive(&sm.out_free);
+                if (c < chunks) {
+                    if (c >= kStages && !(ok = mbar_wait_warp(&sm.empty[c % kStages], (c / kStages - 1) & 1, &sm.abort))) break;
+                    uint8_t *st = base + (c % kStages) * St::bytes;
+                    uint64_t *bar = &sm.full[c % kStages];
+                    const int t0 = s + c * C, n = min(C, e - t0);
+                    if (id == 0) {
+                        mbar_expect_tx(bar, kHeadBytes);
+                        bulk_load(st + St::head, p.heads + (static_cast<int64_t>(slot0 + c) * a.num_v_heads + h) * kHeadBytes, kHeadBytes, bar);
                     }
-                }
-                if (!ok) break;
-                if (c >= chunks) continue;
-                // That output also says that chunk c - 2 is done with its stage.
-                uint8_t *st = base + (c % kStages) * St::bytes;
-                uint64_t *bar = &sm.full[c % kStages];
-                const int t0 = s + c * C, n = min(C, e - t0);
-                if (id == 0) {
-                    mbar_expect_tx(bar, kHeadBytes);
-                    bulk_load(st + St::head, p.heads + (static_cast<int64_t>(slot0 + c) * a.num_v_heads + h) * kHeadBytes, kHeadBytes, bar);
-                }
-                stage_rows<PANELS, VIO>(st, 2 * kTile, a.k, t0, hk, n, a.dim_k, id, kLoaders);
-                stage_rows<PANELS, VIO>(st + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, id, kLoaders);
-                // V: rows of 128 values, token after token
-                const uint16_t *src = static_cast<const uint16_t *>(vv.data) + t0 * vv.stride_tok + h * vv.stride_head;
-                for (int i = id; i < C * 16; i += kLoaders) {
-                    const int row = i >> 4, piece = i & 15;
-                    uint8_t *dst = st + St::v + row * 256 + piece * 16;
+                    const uint16_t *src = vsrc + t0 * a.v.stride_tok;
                     if constexpr (VIO) {
-                        const bool real = row < n && piece * 8 < width;
-                        cp_async16_or_zero(smem_u32(dst), real ? src + row * vv.stride_tok + piece * 8 : src, real);
-                    } else {
-                        Raw<8> r;
-                        r.zero();
-                        if (row < n) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (piece * 8 + k < width) r.set_elem(k, src[row * vv.stride_tok + (piece * 8 + k) * vv.stride_dim]);
+                        for (int i = id; i < C * 16; i += kLoaders) {
+                            const int row = i >> 4, piece = i & 15;
+                            const bool real = row < n && piece * 8 < width;
+                            cp_async16_or_zero(smem_u32(raw_v + row * kRawBytes + piece * 16), real ? src + row * a.v.stride_tok + piece * 8 : src, real);
                         }
-                        *reinterpret_cast<uint4 *>(dst) = r.v;
+                    } else {
+                        for (int i = id; i < C * 128; i += kLoaders) {
+                            const int row = i >> 7, dv = i & 127;
+                            reinterpret_cast<uint16_t *>(st + St::v + dv * kRowBytes)[row] =
+                                row < n && dv < width ? src[row * a.v.stride_tok + dv * a.v.stride_dim] : uint16_t(0);
+                        }
                     }
+                    stage_rows<PANELS, VIO>(st, 2 * kTile, a.k, t0, hk, n, a.dim_k, id, kLoaders);
+                    stage_rows<PANELS, VIO>(st + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, id, kLoaders);
+                    if constexpr (VIO) {
+                        cp_async_commit();
+                        cp_async_wait<0>();
+                        sync_loaders();
+                        for (int g = lw; g < 32; g += kLoaders / 32) {  // values 8 (g / 2), tokens 32 (g % 2)
+                            uint32_t r[4];
+                            load_transposed(smem_u32(raw_v) + ((g & 1) * 32 + lane) * kRawBytes + (g >> 1) * 16, r);
+                            uint8_t *dst = st + St::v + ((g >> 1) * 8 + (lane >> 2)) * kRowBytes + (g & 1) * 64 + (lane & 3) * 4;
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) *reinterpret_cast<uint32_t *>(dst + m * 16) = r[m];
+                        }
+                        sync_loaders();
+                    }
+                    fence_async_shared();
+                    mbar_arrive(bar);
+                    loaded = c + 1;
                 }
-                if constexpr (VIO) {
-                    cp_async_commit();
-                    cp_async_wait<0>();
+                if (c >= 2) {  // the output of chunk c - 2, written while chunk c - 1 runs
+                    if (!(ok = mbar_wait_warp(&sm.out_full, c & 1, &sm.abort))) break;
+                    const int t0 = s + (c - 2) * C, n = min(C, e - t0);
+                    if constexpr (VIO) {
+                        for (int g = lw; g < 32; g += kLoaders / 32) {  // tokens 8 (g / 4), values 32 (g % 4)
+                            uint32_t r[4];
+                            load_transposed(smem_u32(out_tile) + ((g & 3) * 32 + lane) * kRowBytes + (g >> 2) * 16, r);
+                            transpose_quad(r);
+                            const int row = (g >> 2) * 8 + (lane >> 2), dv = (g & 3) * 32 + (lane & 3) * 8;
+                            if (row < n && dv < width)
+                                *reinterpret_cast<uint4 *>(out + (t0 + row) * a.out.stride_tok + dv) = make_uint4(r[0], r[1], r[2], r[3]);
+                        }
+                    } else {
+                        for (int i = id; i < n * 128; i += kLoaders)
+                            if ((i & 127) < width)
+                                out[(t0 + (i >> 7)) * a.out.stride_tok + (i & 127) * a.out.stride_dim] =
+                                    reinterpret_cast<const uint16_t *>(out_tile + (i & 127) * kRowBytes)[i >> 7];
+                    }
+                    mbar_arrive(&sm.out_free);
                 }
-                fence_async_shared();
-                mbar_arrive(bar);
-                loaded = c + 1;
             }
             if (!ok) {  // gave up: let the copies land before the shared memory goes
                 int quiet = 0;
                 for (int i = 0; i < loaded; ++i)
                     if (i + kStages >= loaded) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1, &quiet);
             }
-            bulk_wait<false>();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
@@ -578,10 +594,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         const int wg = warp >> 2, d = (warp & 3) * 32 + lane, row = slice * 128 + d;
         const bool live = row < a.dim_v;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t col_s = lanes + kColS + wg * 48 * PANELS, col_r = lanes + kColR + wg * 48, col_n = lanes + kColN + wg * 32;
         const bool init = a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
         float *sp = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + row * a.s_stride_v : nullptr;
 
-        float st[KH];  // this thread's part of row d of S
+        f32x2 st[KH / 2];  // this thread's part of row d of S
 #pragma unroll
         for (int k = 0; k < KH; k += 4) {
             const int kk = wg * KH + k;
@@ -596,24 +613,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                     if (kk + 3 < a.dim_k) x.w = sp[(kk + 3) * a.s_stride_k];
                 }
             }
-            st[k] = x.x; st[k + 1] = x.y; st[k + 2] = x.z; st[k + 3] = x.w;
+            st[k / 2] = pack2(x.x, x.y);
+            st[k / 2 + 1] = pack2(x.z, x.w);
         }
         auto stage = [&](int c) { return base + (c % kStages) * St::bytes; };
-        auto scalars = [&](int c) { return reinterpret_cast<const float *>(stage(c) + St::head + kVec); };
+        // S^T <- gamma S^T + what the chunk added, 16 keys a time
+        auto add_delta = [&](float gamma, int k0) {
+            float x[16];
+            tmem_load(col_s + k0, x);
+            tmem_wait_load();
+            const f32x2 g2 = pack2(gamma, gamma);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) st[k0 / 2 + k] = fma2(g2, st[k0 / 2 + k], pack2(x[2 * k], x[2 * k + 1]));
+        };
         // d P^T of chunk c onto oi, into the output tile
-        float oi[32];
+        f32x2 oi[16];
         auto finish = [&](int c) {
             float x[32];
-            tmem_load32(lanes + kColO + wg * 32, x);
+            tmem_load(lanes + kColO + wg * 32, x);
             tmem_wait_load();
             tc_fence_before();
             mbar_arrive(&sm.have_read);
-            // the tile is free once the output before last has been read from it
             if (c > 0 && !mbar_wait_warp(&sm.out_free, (c - 1) & 1, &sm.abort)) return false;
-            uint16_t *o = reinterpret_cast<uint16_t *>(out_tile) + wg * 32 * 128 + d;
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i * 128] = round_bf16(oi[i] + x[i]);
-            fence_async_shared();
+            for (int i = 0; i < 16; ++i) w[i] = f32x2_to_bf16x2(add2(oi[i], pack2(x[2 * i], x[2 * i + 1])));
+            uint4 *o = reinterpret_cast<uint4 *>(out_tile + d * kRowBytes + wg * 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
             mbar_arrive(&sm.out_full);
             return true;
         };
@@ -622,28 +649,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         float gamma = 1.0f;
         for (int c = 0; c < chunks; ++c) {
             const uint32_t par = c & 1;
-            // S^T <- e^{G_C} S^T + what the last chunk adds, and its parts
+            // b v of this thread's 32 tokens, while the tensor cores add up the last chunk
+            if (!(ok = mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
+            const float *f = reinterpret_cast<const float *>(stage(c) + St::head + kVec) + wg * 32;
+            auto vec2 = [&](int which, int i) { return *reinterpret_cast<const ulonglong2 *>(f + which * C + i); };
+            f32x2 vb[16];
+            {
+                const uint4 *v = reinterpret_cast<const uint4 *>(stage(c) + St::v + d * kRowBytes + wg * 64);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 x = v[i];
+                    const ulonglong2 b0 = vec2(kBeta, 8 * i), b1 = vec2(kBeta, 8 * i + 4);
+                    vb[4 * i] = mul2(pack2(bf16_lo(x.x), bf16_hi(x.x)), b0.x);
+                    vb[4 * i + 1] = mul2(pack2(bf16_lo(x.y), bf16_hi(x.y)), b0.y);
+                    vb[4 * i + 2] = mul2(pack2(bf16_lo(x.z), bf16_hi(x.z)), b1.x);
+                    vb[4 * i + 3] = mul2(pack2(bf16_lo(x.w), bf16_hi(x.w)), b1.y);
+                }
+            }
             if (c > 0) {
                 if (!(ok = mbar_wait_warp(&sm.mma_delta, par ^ 1, &sm.abort))) break;
                 tc_fence_after();
+            }
+            // All of S is read before any of it is overwritten by its parts (they are wider).
+            if (c > 0) {
 #pragma unroll
-                for (int k0 = 0; k0 < KH; k0 += 32) {
-                    float x[32];
-                    tmem_load32(lanes + kColS + wg * 48 * PANELS + k0, x);
-                    tmem_wait_load();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) st[k0 + k] = fmaf(gamma, st[k0 + k], x[k]);
-                }
+                for (int k0 = 0; k0 < KH; k0 += 16) add_delta(gamma, k0);
             }
 #pragma unroll
-            for (int k0 = 0; k0 < KH; k0 += 32) {
-                uint32_t hi[16], mid[16], lo[16];
+            for (int k0 = 0; k0 < KH; k0 += 16) {
+                uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) split_bf16x3(st[k0 + 2 * k], st[k0 + 2 * k + 1], hi[k], mid[k], lo[k]);
-                const uint32_t at = lanes + kColS + wg * 48 * PANELS + k0 / 2;
-                tmem_store16(at, hi);
-                tmem_store16(at + KH / 2, mid);
-                tmem_store16(at + KH, lo);
+                for (int k = 0; k < 8; ++k) split_bf16x3(st[k0 / 2 + k], hi[k], mid[k], lo[k]);
+                tmem_store(col_s + k0 / 2, hi);
+                tmem_store(col_s + KH / 2 + k0 / 2, mid);
+                tmem_store(col_s + KH + k0 / 2, lo);
             }
             tmem_wait_store();
             tc_fence_before();
@@ -656,62 +695,80 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             } else {
                 mbar_arrive(&sm.have_read);
             }
-            if (!(ok = mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
-            const float *f = scalars(c) + wg * 32;
-            const uint16_t *v = reinterpret_cast<const uint16_t *>(stage(c) + St::v) + wg * 32 * 128 + d;
-            float vb[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) vb[i] = bf16_bits(v[i * 128]) * f[kBeta * C + i];
 
             // R = b v - b e^G S k
             if (!(ok = mbar_wait_warp(&sm.mma_p, par, &sm.abort))) break;
             tc_fence_after();
-            {
-                float x[32];
-                tmem_load32(lanes + kColP + wg * 32, x);
-                tmem_wait_load();
-                uint32_t hi[16], mid[16], lo[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    split_bf16x3(fmaf(-f[kKey * C + 2 * i], x[2 * i], vb[2 * i]),
-                                 fmaf(-f[kKey * C + 2 * i + 1], x[2 * i + 1], vb[2 * i + 1]), hi[i], mid[i], lo[i]);
-                tmem_store16(lanes + kColR + wg * 48, hi);
-                tmem_store16(lanes + kColR + wg * 48 + 16, mid);
-                tmem_store16(lanes + kColR + wg * 48 + 32, lo);
+            for (int i0 = 0; i0 < 32; i0 += 16) {
+                float x[16];
+                tmem_load(lanes + kColP + wg * 32 + i0, x);
+                tmem_wait_load();
+                uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const ulonglong2 key = vec2(kKey, i0 + 2 * i);
+                    split_bf16x3(fma2(key.x, pack2(x[2 * i], x[2 * i + 1]), vb[i0 / 2 + i]), hi[i], mid[i], lo[i]);
+                    split_bf16x3(fma2(key.y, pack2(x[2 * i + 2], x[2 * i + 3]), vb[i0 / 2 + i + 1]), hi[i + 1], mid[i + 1], lo[i + 1]);
+                }
+                tmem_store(col_r + i0 / 2, hi);
+                tmem_store(col_r + 16 + i0 / 2, mid);
+                tmem_store(col_r + 32 + i0 / 2, lo);
             }
             tmem_wait_store();
             tc_fence_before();
             mbar_arrive(&sm.have_r);
-            if (!(ok = mbar_wait_warp(&sm.mma_o, par, &sm.abort))) break;
-            tc_fence_after();
-            tmem_load32(lanes + kColO + wg * 32, oi);
-            tmem_wait_load();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) oi[i] *= f[kQuery * C + i];
 
             // d, decayed for the state (3 parts) and for the output (2)
             if (!(ok = mbar_wait_warp(&sm.mma_n, par, &sm.abort))) break;
             tc_fence_after();
-            {
-                float x[32];
-                tmem_load32(lanes + kColN + wg * 32, x);
+            f32x2 x[16];
+#pragma unroll
+            for (int i0 = 0; i0 < 32; i0 += 16) {
+                float y[16];
+                tmem_load(col_n + i0, y);
                 tmem_wait_load();
-                uint32_t hi[16], mid[16], lo[16];
+                uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    split_bf16x3(f[kState * C + 2 * i] * x[2 * i], f[kState * C + 2 * i + 1] * x[2 * i + 1], hi[i], mid[i], lo[i]);
-                tmem_store16(lanes + kColR + wg * 48, hi);
-                tmem_store16(lanes + kColR + wg * 48 + 16, mid);
-                tmem_store16(lanes + kColR + wg * 48 + 32, lo);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) split_bf16x2(x[2 * i], x[2 * i + 1], hi[i], mid[i]);
-                tmem_store16(lanes + kColN + wg * 32, hi);
-                tmem_store16(lanes + kColN + wg * 32 + 16, mid);
+                for (int i = 0; i < 8; i += 2) {
+                    const ulonglong2 left = vec2(kState, i0 + 2 * i);
+                    x[i0 / 2 + i] = pack2(y[2 * i], y[2 * i + 1]);
+                    x[i0 / 2 + i + 1] = pack2(y[2 * i + 2], y[2 * i + 3]);
+                    split_bf16x3(mul2(left.x, x[i0 / 2 + i]), hi[i], mid[i], lo[i]);
+                    split_bf16x3(mul2(left.y, x[i0 / 2 + i + 1]), hi[i + 1], mid[i + 1], lo[i + 1]);
+                }
+                tmem_store(col_r + i0 / 2, hi);
+                tmem_store(col_r + 16 + i0 / 2, mid);
+                tmem_store(col_r + 32 + i0 / 2, lo);
             }
             tmem_wait_store();
             tc_fence_before();
-            mbar_arrive(&sm.have_n);
-            gamma = scalars(c)[kMisc * C];
+            mbar_arrive(&sm.have_vs);
+#pragma unroll
+            for (int i0 = 0; i0 < 16; i0 += 8) {
+                uint32_t hi[8], mid[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split_bf16x2(x[i0 + i], hi[i], mid[i]);
+                tmem_store(col_n + i0, hi);
+                tmem_store(col_n + 16 + i0, mid);
+            }
+            if (!(ok = mbar_wait_warp(&sm.mma_o, par, &sm.abort))) break;
+            tc_fence_after();
+            {
+                float y[32];
+                tmem_load(lanes + kColO + wg * 32, y);
+                tmem_wait_load();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const ulonglong2 q = vec2(kQuery, 2 * i);
+                    oi[i] = mul2(q.x, pack2(y[2 * i], y[2 * i + 1]));
+                    oi[i + 1] = mul2(q.y, pack2(y[2 * i + 2], y[2 * i + 3]));
+                }
+            }
+            gamma = f[kMisc * C - wg * 32];
+            tmem_wait_store();
+            tc_fence_before();
+            mbar_arrive(&sm.have_d);
         }
         // the last chunk's output and the final state
         if (ok) ok = mbar_wait_warp(&sm.mma_out, (chunks - 1) & 1, &sm.abort);
@@ -719,23 +776,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             tc_fence_after();
             finish(chunks - 1);
 #pragma unroll
-            for (int k0 = 0; k0 < KH; k0 += 32) {
-                float x[32];
-                tmem_load32(lanes + kColS + wg * 48 * PANELS + k0, x);
-                tmem_wait_load();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) st[k0 + k] = fmaf(gamma, st[k0 + k], x[k]);
-            }
+            for (int k0 = 0; k0 < KH; k0 += 16) add_delta(gamma, k0);
             if (sp != nullptr && live) {
 #pragma unroll
                 for (int k = 0; k < KH; k += 4) {
                     const int kk = wg * KH + k;
+                    float4 x;
+                    unpack2(st[k / 2], x.x, x.y);
+                    unpack2(st[k / 2 + 1], x.z, x.w);
                     if constexpr (V) {
-                        if (kk < a.dim_k) *reinterpret_cast<float4 *>(sp + kk) = make_float4(st[k], st[k + 1], st[k + 2], st[k + 3]);
+                        if (kk < a.dim_k) *reinterpret_cast<float4 *>(sp + kk) = x;
                     } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (kk + i < a.dim_k) sp[(kk + i) * a.s_stride_k] = st[k + i];
+                        if (kk < a.dim_k) sp[kk * a.s_stride_k] = x.x;
+                        if (kk + 1 < a.dim_k) sp[(kk + 1) * a.s_stride_k] = x.y;
+                        if (kk + 2 < a.dim_k) sp[(kk + 2) * a.s_stride_k] = x.z;
+                        if (kk + 3 < a.dim_k) sp[(kk + 3) * a.s_stride_k] = x.w;
                     }
                 }
             }
@@ -751,7 +806,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 template <int PANELS>
 constexpr size_t prep_smem() { return 1024 + PANELS * 2 * kTile + sizeof(PrepSmem); }
 template <int PANELS>
-constexpr size_t chunk_smem() { return 1024 + kStages * Stage<PANELS>::bytes + 2 * kTile + sizeof(ChunkSmem); }
+constexpr size_t chunk_smem() { return 1024 + kStages * Stage<PANELS>::bytes + 128 * kRowBytes + C * kRawBytes + sizeof(ChunkSmem); }
 
 template <int PANELS, bool VS, bool VIO>
 int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
