@@ -52,27 +52,40 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Copies `rows` (of which the first n are real) of a head's bf16 vectors into swizzled tiles of 64 values a row, `panels`
-// tiles `panel_bytes` apart, zeros past n and past dim; by threads `id` of `count`.  VEC: 16-byte asynchronous copies.
-template <int PANELS, bool VEC>
+// Copies 64 rows (of which the first n are real) of a head's bf16 vectors into swizzled tiles of 64 values a row, `PANELS`
+// tiles `panel_bytes` apart, zeros past n and past dim; by COUNT threads `id`.  VEC: 16-byte asynchronous copies.
+template <int PANELS, bool VEC, int COUNT>
 __device__ __forceinline__ void stage_rows(uint8_t *tile, int panel_bytes, const ccv_heads_view &view, int64_t tok, int head, int n,
-                                           int dim, int id, int count) {
-    const uint16_t *src = static_cast<const uint16_t *>(view.data) + tok * view.stride_tok + head * view.stride_head;
-    for (int i = id; i < C * 8 * PANELS; i += count) {
-        const int row = i / (8 * PANELS), piece = i % (8 * PANELS);
-        uint8_t *dst = tile + (piece >> 3) * panel_bytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
-        if constexpr (VEC) {
-            const bool real = row < n && piece * 8 < dim;
-            cp_async16_or_zero(smem_u32(dst), real ? src + row * view.stride_tok + piece * 8 : src, real);
-        } else {
+                                           int dim, int id) {
+    constexpr int kPieces = 8 * PANELS, kStep = COUNT / kPieces;
+    static_assert(C % kStep == 0, "");
+    const int piece = id % kPieces, row0 = id / kPieces;
+    const uint16_t *src = static_cast<const uint16_t *>(view.data) + (tok + row0) * view.stride_tok + head * view.stride_head;
+    const int64_t step = kStep * view.stride_tok;
+    uint8_t *dst = tile + (piece >> 3) * panel_bytes + row0 * 128;
+    const bool wide = piece * 8 < dim;
+    if constexpr (VEC) {
+        src += piece * 8;
+        const uint32_t to = smem_u32(dst);
+#pragma unroll
+        for (int i = 0; i < C / kStep; ++i) {
+            const int row = row0 + i * kStep;
+            const bool real = wide && row < n;
+            cp_async16_or_zero(to + i * kStep * 128 + (((piece ^ row) & 7) << 4), real ? src : static_cast<const uint16_t *>(view.data), real);
+            src += step;
+        }
+    } else {
+        for (int i = 0; i < C / kStep; ++i) {
+            const int row = row0 + i * kStep;
             Raw<8> r;
             r.zero();
             if (row < n) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (piece * 8 + k < dim) r.set_elem(k, src[row * view.stride_tok + (piece * 8 + k) * view.stride_dim]);
+                    if (piece * 8 + k < dim) r.set_elem(k, src[(piece * 8 + k) * view.stride_dim]);
             }
-            *reinterpret_cast<uint4 *>(dst) = r.v;
+            *reinterpret_cast<uint4 *>(dst + i * kStep * 128 + (((piece ^ row) & 7) << 4)) = r.v;
+            src += step;
         }
     }
 }
@@ -83,77 +96,111 @@ constexpr int kPrepThreads = 128;
 constexpr int kLd = 68;  // floats of a row of A in shared memory: 16-byte rows, spread over the banks
 
 struct PrepSmem {
-    float a[2][C * kLd];           // A, then T, of two value heads
     float ghi[2][C], glo[2][C];    // G log2(e) as a float pair
     float beta[2][C];
     float rk[C], rq[C];            // factors of the rows of K and Q
-    double carry[2];
+    int64_t carry[2];
     uint64_t bar;
     uint32_t tmem;
-    int seq, abort;
+    int seq, start, end, abort;
 };
+constexpr int kMatrixBytes = 2 * C * kLd * 4;  // A, then T, of two value heads; over the rows of K and Q once they are used
 
-// T = (I + A)^-1 for the unit lower triangular 64 x 64 matrix in `a` (strictly lower part A, zeros above), by 64 threads:
-// forward substitution of the two diagonal 32 x 32 blocks, a column a thread, then T21 = -T22 (A21 T11).  Substitution, not
-// a power series: its error stays at the rounding of T however alike the keys are.  The upper right block holds scratch.
-__device__ __forceinline__ void invert(float *a, int tid, int barrier) {
-    const int half = tid >> 5, j = tid & 31;
-    auto sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory"); };
-    float t[32];
-    {
-        float *d = a + half * (32 * kLd + 32);
+// Adds row . t for two columns, values paired along the inner index: 2 packed FMAs a pair of A's values for each.
+template <int N>
+__device__ __forceinline__ void dot2(const float *row, const f32x2 (&t)[2][16], f32x2 (&acc)[2][2]) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) t[i] = 0.0f;
+    for (int m = 0; m < N; m += 4) {
+        const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(row + m);
+#pragma unroll
+        for (int col = 0; col < 2; ++col) {
+            acc[col][0] = fma2(r.x, t[col][m / 2], acc[col][0]);
+            acc[col][1] = fma2(r.y, t[col][m / 2 + 1], acc[col][1]);
+        }
+    }
+}
+__device__ __forceinline__ float sum_pairs(const f32x2 (&acc)[2]) {
+    float a, b;
+    unpack2(add2(acc[0], acc[1]), a, b);
+    return a + b;
+}
+
+// T = (I + A)^-1 for the unit lower triangular 64 x 64 matrices of two heads (strictly lower part A, zeros above), by the
+// block's 128 threads: forward substitution of the diagonal 32 x 32 blocks, then T21 = -T22 (A21 T11).  Substitution, not a
+// power series: its error stays at the rounding of T however alike the keys are.  A thread has two columns, since a
+// broadcast load of 16 bytes costs the shared-memory pipe as much as 16 bytes for every lane; one column a thread made that
+// pipe the bound (19000 cycles a block against FMAs for 2500).  The upper right blocks hold scratch.
+__device__ __forceinline__ void invert(float *matrices, int tid) {
+    f32x2 t[2][16];  // two columns, pairs of rows
+    if (tid < 64) {
+        const int which = tid >> 4, j = (tid & 15) * 2;
+        float *d = matrices + (which >> 1) * (C * kLd) + (which & 1) * (32 * kLd + 32);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[0][i] = t[1][i] = 0ull;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            f32x2 acc[2][2] = {{0ull, 0ull}, {0ull, 0ull}};
 #pragma unroll
             for (int m = 0; m < i; m += 4) {
-                const float4 r = *reinterpret_cast<const float4 *>(d + i * kLd + m);
-                acc[0] = fmaf(r.x, t[m], acc[0]);
-                acc[1] = fmaf(r.y, t[m + 1], acc[1]);
-                acc[2] = fmaf(r.z, t[m + 2], acc[2]);
-                acc[3] = fmaf(r.w, t[m + 3], acc[3]);
+                const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(d + i * kLd + m);
+#pragma unroll
+                for (int col = 0; col < 2; ++col) {
+                    acc[col][0] = fma2(r.x, t[col][m / 2], acc[col][0]);
+                    if (m + 2 < i) acc[col][1] = fma2(r.y, t[col][m / 2 + 1], acc[col][1]);
+                }
             }
-            t[i] = (i == j ? 1.0f : 0.0f) - ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+            float lo, hi;
+#pragma unroll
+            for (int col = 0; col < 2; ++col) {
+                const float x = (i == j + col ? 1.0f : 0.0f) - sum_pairs(acc[col]);
+                unpack2(t[col][i / 2], lo, hi);
+                t[col][i / 2] = (i & 1) ? pack2(lo, x) : pack2(x, hi);
+            }
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) d[i * kLd + j] = t[i];
+        for (int i = 0; i < 16; ++i) {
+            float a0, a1, b0, b1;
+            unpack2(t[0][i], a0, a1);
+            unpack2(t[1][i], b0, b1);
+            *reinterpret_cast<float2 *>(d + (2 * i) * kLd + j) = make_float2(a0, b0);
+            *reinterpret_cast<float2 *>(d + (2 * i + 1) * kLd + j) = make_float2(a1, b1);
+        }
     }
-    sync();
-    // Two products of 32 x 32 blocks, 16 rows of column j a thread: X = A21 T11, then -T22 X.
+    __syncthreads();
+    // Two products of 32 x 32 blocks, 8 rows of two columns a thread: X = A21 T11, then -T22 X.
+    const int group = (tid >> 4) & 3, j = (tid & 15) * 2;
+    float *a = matrices + (tid >> 6) * (C * kLd);
 #pragma unroll 1
     for (int step = 0; step < 2; ++step) {
-        const float *left = a + (32 + 16 * half) * kLd + 32 * step;
+        const float *left = a + (32 + 8 * group) * kLd + 32 * step;
         const float *right = a + 32 * step + j;
-        float *out = a + (16 * half + 32 * step) * kLd + 32 * (1 - step) + j;
+        float *out = a + (8 * group + 32 * step) * kLd + 32 * (1 - step) + j;
         const float sign = step ? -1.0f : 1.0f;
 #pragma unroll
-        for (int m = 0; m < 32; ++m) t[m] = right[m * kLd];
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int m = 0; m < 32; m += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(left + i * kLd + m);
-                acc[0] = fmaf(v.x, t[m], acc[0]);
-                acc[1] = fmaf(v.y, t[m + 1], acc[1]);
-                acc[2] = fmaf(v.z, t[m + 2], acc[2]);
-                acc[3] = fmaf(v.w, t[m + 3], acc[3]);
-            }
-            out[i * kLd] = sign * ((acc[0] + acc[1]) + (acc[2] + acc[3]));
+        for (int m = 0; m < 16; ++m) {
+            const float2 x = *reinterpret_cast<const float2 *>(right + 2 * m * kLd), y = *reinterpret_cast<const float2 *>(right + (2 * m + 1) * kLd);
+            t[0][m] = pack2(x.x, y.x);
+            t[1][m] = pack2(x.y, y.y);
         }
-        sync();
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+            f32x2 acc[2][2] = {{0ull, 0ull}, {0ull, 0ull}};
+            dot2<32>(left + i * kLd, t, acc);
+            *reinterpret_cast<float2 *>(out + i * kLd) = make_float2(sign * sum_pairs(acc[0]), sign * sum_pairs(acc[1]));
+        }
+        __syncthreads();
     }
 }
 
 // PANELS: dim_k rounded up to 64 PANELS.  V: rows of q and k allow 16-byte vectors.
 template <int PANELS, bool V>
-__global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_constant__ FwdArgs p) {
+__global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_constant__ FwdArgs p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ab = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    PrepSmem &sm = *reinterpret_cast<PrepSmem *>(ab + PANELS * 2 * kTile);
+    float *matrices = reinterpret_cast<float *>(ab);
+    PrepSmem &sm = *reinterpret_cast<PrepSmem *>(ab + kMatrixBytes);
+    static_assert(kMatrixBytes >= PANELS * 2 * kTile && kMatrixBytes % 16 == 0, "");
     const ccv_gdr_args &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hk = blockIdx.x % a.num_k_heads, slot = blockIdx.x / a.num_k_heads;
@@ -161,25 +208,31 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
 
     // The sequence of this slot: the last i with first_slot(i) <= slot, found by a warp 32 candidates at a time.
     if (warp == 0) {
-        int lo = 0, hi = p.batch;  // the answer is in [lo, hi)
-        while (hi - lo > 1) {
+        int lo = 0, hi = p.batch, s = 0, e = 0;  // the answer is in [lo, hi)
+        do {
             const int step = (hi - lo + 31) / 32;
-            const int i = lo + lane * step;
-            const bool below = i < hi && first_slot(p.query_start_loc[i], i) <= slot;
+            const int i = min(lo + lane * step, p.batch), next = max(i, min(i + step, hi));
+            const int at = p.query_start_loc[i], to = p.query_start_loc[next];
+            const bool below = i < hi && first_slot(at, i) <= slot;
             const int last = 31 - __clz(__ballot_sync(kFullMask, below) | 1);
             lo += last * step;
             hi = min(hi, lo + step);
+            s = __shfl_sync(kFullMask, at, last);
+            e = __shfl_sync(kFullMask, to, last);
+        } while (hi - lo > 1);
+        if (lane == 0) {
+            sm.seq = lo;
+            sm.start = s;
+            sm.end = e;
         }
-        if (lane == 0) sm.seq = lo;
     }
-    if (tid == 0) {
+    if (tid == 32) {
         sm.abort = 0;
         mbar_init(&sm.bar, 1);
         mbar_init_fence();
     }
     __syncthreads();
-    const int seq = sm.seq;
-    const int s = p.query_start_loc[seq], e = p.query_start_loc[seq + 1];
+    const int seq = sm.seq, s = sm.start, e = sm.end;
     if (!sequence_ok(s, e, p.total_tokens)) return;  // counted by the chunk kernel
     const int chunk = slot - first_slot(s, seq);
     if (chunk < 0 || chunk * C >= e - s) return;
@@ -187,10 +240,37 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
     const int t0 = s + chunk * C, n = min(C, e - t0);
 
     // Panels of 128 rows: the chunk's keys, then its queries.
-    stage_rows<PANELS, V>(ab, 2 * kTile, a.k, t0, hk, n, a.dim_k, tid, kPrepThreads);
-    stage_rows<PANELS, V>(ab + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, tid, kPrepThreads);
-    if (warp == 0) tmem_alloc<64>(&sm.tmem);
+    stage_rows<PANELS, V, kPrepThreads>(ab, 2 * kTile, a.k, t0, hk, n, a.dim_k, tid);
+    stage_rows<PANELS, V, kPrepThreads>(ab + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, tid);
     cp_async_commit();
+    if (warp == 0) tmem_alloc<64>(&sm.tmem);
+
+    // The value heads of this key head go two at a time, 64 threads each.
+    const int i = tid & (C - 1), side = tid >> 6;
+    const int rep = a.num_v_heads / a.num_k_heads;
+    auto block = [&](int w) { return p.heads + (static_cast<int64_t>(slot) * a.num_v_heads + hk * rep + w) * kHeadBytes; };
+    // Gates, and G by a scan in 64-bit fixed point: a difference of two sums has to be exact to its own rounding.
+    auto scan_gates = [&](int r0) {
+        const int h = hk * rep + min(r0 + side, rep - 1);
+        float g = 0.0f, beta = 0.0f;
+        if (i < n) gdr_gates(a, (t0 + i) * a.gate_stride_tok + h * a.gate_stride_head, h, g, beta);
+        if (g < -200.0f) g = -200.0f;  // e^-200 is 0 in fp32; keeps -inf - -inf out of the differences
+        constexpr float kOne = 1099511627776.0f;  // 2^40
+        int64_t sum = __float2ll_rn(g * 1.4426950408889634f * kOne);
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t o = __shfl_up_sync(kFullMask, sum, m);
+            if (lane >= m) sum += o;
+        }
+        if ((warp & 1) == 0 && lane == 31) sm.carry[side] = sum;
+        __syncthreads();
+        if (warp & 1) sum += sm.carry[side];
+        const float hi = __ll2float_rn(sum);
+        sm.ghi[side][i] = hi / kOne;
+        sm.glo[side][i] = __ll2float_rn(sum - __float2ll_rn(hi)) / kOne;
+        sm.beta[side][i] = g != g ? g : beta;
+    };
+    scan_gates(0);
     cp_async_wait<0>();
     fence_async_shared();
     tc_fence_before();
@@ -206,7 +286,6 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
         mma_commit(&sm.bar, 1);
     }
     // Meanwhile the rows' norms, a row a thread.
-    const int i = tid & (C - 1), side = tid >> 6;
     {
         float ss = 0.0f;
 #pragma unroll
@@ -222,55 +301,46 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
         if (side) sm.rq[i] = r * a.scale;
         else sm.rk[i] = r;
     }
+    if (!mbar_wait_warp(&sm.bar, 0, &sm.abort) && lane == 0) count_error(p.err_count);
+    tc_fence_after();
+    __syncthreads();  // the rows of K and Q are no longer needed: A takes their place
 
-    // The value heads of this key head, two at a time, 64 threads each.
-    const int rep = a.num_v_heads / a.num_k_heads;
-    bool done = false;
+    const uint32_t addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     for (int r0 = 0; r0 < rep; r0 += 2) {
         const int nh = min(2, rep - r0);
-        auto block = [&](int w) { return p.heads + (static_cast<int64_t>(slot) * a.num_v_heads + hk * rep + r0 + w) * kHeadBytes; };
-        {   // gates, and G by a scan in 64 bits: a difference of two sums has to be exact to its own rounding
-            const int h = hk * rep + r0 + (side < nh ? side : 0);
-            float g = 0.0f, beta = 0.0f;
-            if (i < n) gdr_gates(a, (t0 + i) * a.gate_stride_tok + h * a.gate_stride_head, h, g, beta);
-            if (g < -200.0f) g = -200.0f;  // e^-200 is 0 in fp32; keeps -inf - -inf out of the differences
-            double sum = static_cast<double>(g) * 1.4426950408889634074;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double o = __shfl_up_sync(kFullMask, sum, m);
-                if (lane >= m) sum += o;
-            }
-            if ((warp & 1) == 0 && lane == 31) sm.carry[side] = sum;
+        if (r0 > 0) {
+            scan_gates(r0);
             __syncthreads();
-            if (warp & 1) sum += sm.carry[side];
-            const float ghi = static_cast<float>(sum), glo = static_cast<float>(sum - ghi);
-            sm.ghi[side][i] = ghi;
-            sm.glo[side][i] = glo;
-            sm.beta[side][i] = beta;
-            __syncthreads();
-            if (side < nh) {
-                float *vec = reinterpret_cast<float *>(block(side) + kVec);
-                const float decay = ex2(ghi + glo), rk = sm.rk[i];
-                vec[kBeta * C + i] = beta;
-                vec[kKey * C + i] = -beta * rk * decay;
-                vec[kState * C + i] = ex2((sm.ghi[side][C - 1] - ghi) + (sm.glo[side][C - 1] - glo)) * rk;
-                vec[kQuery * C + i] = sm.rq[i] * decay;
-                if (i == 0) vec[kMisc * C] = ex2(sm.ghi[side][C - 1] + sm.glo[side][C - 1]);
-            }
         }
-        if (!done) {
-            if (!mbar_wait_warp(&sm.bar, 0, &sm.abort) && lane == 0) count_error(p.err_count);
-            tc_fence_after();
-            done = true;
+        if (side < nh) {
+            float *vec = reinterpret_cast<float *>(block(r0 + side) + kVec);
+            const float ghi = sm.ghi[side][i], glo = sm.glo[side][i], beta = sm.beta[side][i];
+            const float decay = ex2(ghi + glo), rk = sm.rk[i];
+            vec[kBeta * C + i] = beta;
+            vec[kKey * C + i] = -beta * rk * decay;
+            vec[kState * C + i] = ex2((sm.ghi[side][C - 1] - ghi) + (sm.glo[side][C - 1] - glo)) * rk;
+            vec[kQuery * C + i] = sm.rq[i] * decay;
+            if (i == 0) vec[kMisc * C] = ex2(sm.ghi[side][C - 1] + sm.glo[side][C - 1]);
         }
         // Rows of A (threads of K rows, to shared memory) and of P (threads of Q rows, to the workspace).
-        const uint32_t addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         for (int w = 0; w < nh; ++w) {
             const float ghi = sm.ghi[w][i], glo = sm.glo[w][i];
             const float own = side ? sm.rq[i] : sm.beta[w][i] * sm.rk[i];
-            uint8_t *out_p = block(w) + kP + i * 128;
+            uint8_t *out_p = block(r0 + w) + kP + i * 128;
+            float *out_a = matrices + w * (C * kLd) + i * kLd;
 #pragma unroll
             for (int j0 = 0; j0 < C; j0 += 32) {
+                if (j0 >= (warp & 1) * 32 + 32) {  // above the diagonal for this warp's rows
+                    if (side) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int at = ((j0 / 8 + c) ^ (i & 7)) << 4;
+                            *reinterpret_cast<uint4 *>(out_p + at) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(out_p + kTile + at) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    continue;  // of A nothing there is read
+                }
                 float f[32];
                 tmem_load(addr + j0, f);
                 tmem_wait_load();
@@ -302,26 +372,26 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<float4 *>(&sm.a[w][i * kLd + j0 + j]) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                        *reinterpret_cast<float4 *>(out_a + j0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
                 }
             }
         }
         __syncthreads();
+        invert(matrices, tid);
         if (side < nh) {
-            invert(sm.a[side], i, 1 + side);
-            uint8_t *out = block(side) + kT;
+            uint8_t *out = block(r0 + side) + kT;
             const int c = i & 7;
-#pragma unroll 2
+#pragma unroll 4
             for (int it = 0; it < 8; ++it) {
                 const int row = it * 8 + (i >> 3);
                 uint4 hi = make_uint4(0u, 0u, 0u, 0u), mid = hi, lo = hi;
                 if (row >= 32 || c < 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&sm.a[side][row * kLd + c * 8]);
-                    const float4 y = *reinterpret_cast<const float4 *>(&sm.a[side][row * kLd + c * 8 + 4]);
-                    split_bf16x3(pack2(x.x, x.y), hi.x, mid.x, lo.x);
-                    split_bf16x3(pack2(x.z, x.w), hi.y, mid.y, lo.y);
-                    split_bf16x3(pack2(y.x, y.y), hi.z, mid.z, lo.z);
-                    split_bf16x3(pack2(y.z, y.w), hi.w, mid.w, lo.w);
+                    const float *x = matrices + side * (C * kLd) + row * kLd + c * 8;
+                    const ulonglong2 x0 = *reinterpret_cast<const ulonglong2 *>(x), x1 = *reinterpret_cast<const ulonglong2 *>(x + 4);
+                    split_bf16x3(x0.x, hi.x, mid.x, lo.x);
+                    split_bf16x3(x0.y, hi.y, mid.y, lo.y);
+                    split_bf16x3(x1.x, hi.z, mid.z, lo.z);
+                    split_bf16x3(x1.y, hi.w, mid.w, lo.w);
                 }
                 const int at = row * 128 + ((c ^ (row & 7)) << 4);
                 *reinterpret_cast<uint4 *>(out + at) = hi;
@@ -339,10 +409,10 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const __grid_con
 // ----------------------------------------------------------------- chunks ----
 
 constexpr int kCompute = 256;                 // two warpgroups, each half of the columns of every row
-constexpr int kLoaders = 96;                  // three warps that copy; the fourth of their group issues the MMAs
+constexpr int kLoaders = 64;                  // two warps that load, beside one that stores and one that issues the MMAs
 constexpr int kChunkThreads = kCompute + 128;
 constexpr int kStages = 2;
-constexpr int kIssueWarp = 8;
+constexpr int kIssueWarp = 8, kStoreWarp = 9, kLoadWarp = 10;
 // Registers a thread: 384 threads launch with 168 each, 64512 in all; the compute warpgroups take 208 and the other 88.
 constexpr int kComputeRegs = 208, kOtherRegs = 88;
 static_assert(kCompute * kComputeRegs + 128 * kOtherRegs <= kChunkThreads * 168, "register split");
@@ -374,7 +444,7 @@ struct ChunkSmem {
     uint64_t full[kStages], empty[kStages];               // a stage is loaded; its chunk's MMAs, the last to use it, are done
     uint64_t mma_p, mma_o, mma_n, mma_delta, mma_out;     // completed by the tensor cores
     uint64_t have_s, have_read, have_r, have_vs, have_d;  // arrived on by the compute threads
-    uint64_t out_full, out_free;                          // the output tile: written by them, stored by the loaders
+    uint64_t out_full, out_free;                          // the output tile: written by them, stored by one warp
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -419,7 +489,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         for (uint64_t &b : sm.empty) mbar_init(&b, 1);
         for (uint64_t *b : {&sm.mma_p, &sm.mma_o, &sm.mma_n, &sm.mma_delta, &sm.mma_out, &sm.drain}) mbar_init(b, 1);
         for (uint64_t *b : {&sm.have_s, &sm.have_read, &sm.have_r, &sm.have_vs, &sm.have_d, &sm.out_full}) mbar_init(b, kCompute);
-        mbar_init(&sm.out_free, kLoaders);
+        mbar_init(&sm.out_free, 32);
         mbar_init_fence();
     }
     if (warp == kIssueWarp) tmem_alloc<512>(&sm.tmem);
@@ -510,82 +580,93 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 mma_commit(&sm.drain, el);
                 mbar_wait_warp(&sm.drain, 0, &quiet);
             }
+        } else if (warp == kStoreWarp) {
+            const int width = min(128, a.dim_v - slice * 128);
+            uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + slice * 128 * a.out.stride_dim;
+            for (int c = 0; c < chunks; ++c) {
+                if (!mbar_wait_warp(&sm.out_full, c & 1, &sm.abort)) break;
+                const int t0 = s + c * C, n = min(C, e - t0);
+                if constexpr (VIO) {
+                    // tokens 8 g .. + 7, values 32 m .. + 31
+#pragma unroll 2
+                    for (int g = 0; g < 8; ++g) {
+                        uint32_t r[4][4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) load_transposed(smem_u32(out_tile) + (m * 32 + lane) * kRowBytes + g * 16, r[m]);
+                        const int row = g * 8 + (lane >> 2);
+                        uint16_t *dst = out + (t0 + row) * a.out.stride_tok + (lane & 3) * 8;
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            transpose_quad(r[m]);
+                            if (row < n && m * 32 + (lane & 3) * 8 < width)
+                                *reinterpret_cast<uint4 *>(dst + m * 32) = make_uint4(r[m][0], r[m][1], r[m][2], r[m][3]);
+                        }
+                    }
+                } else {
+                    for (int i = lane; i < n * 128; i += 32)
+                        if ((i & 127) < width)
+                            out[(t0 + (i >> 7)) * a.out.stride_tok + (i & 127) * a.out.stride_dim] =
+                                reinterpret_cast<const uint16_t *>(out_tile + (i & 127) * kRowBytes)[i >> 7];
+                }
+                mbar_arrive(&sm.out_free);
+            }
         } else {
-            const int id = tid - (kIssueWarp + 1) * 32, lw = warp - (kIssueWarp + 1);
+            const int id = tid - kLoadWarp * 32, lw = warp - kLoadWarp;
             auto sync_loaders = [] { asm volatile("bar.sync 1, %0;" ::"n"(kLoaders) : "memory"); };
             const int width = min(128, a.dim_v - slice * 128);
             const uint16_t *vsrc = static_cast<const uint16_t *>(a.v.data) + h * a.v.stride_head + slice * 128 * a.v.stride_dim;
-            uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + slice * 128 * a.out.stride_dim;
-            int loaded = 0;
-            bool ok = true;
-            for (int c = 0; c < chunks + 2; ++c) {
-                if (c < chunks) {
-                    if (c >= kStages && !(ok = mbar_wait_warp(&sm.empty[c % kStages], (c / kStages - 1) & 1, &sm.abort))) break;
-                    uint8_t *st = base + (c % kStages) * St::bytes;
-                    uint64_t *bar = &sm.full[c % kStages];
-                    const int t0 = s + c * C, n = min(C, e - t0);
-                    if (id == 0) {
-                        mbar_expect_tx(bar, kHeadBytes);
-                        bulk_load(st + St::head, p.heads + (static_cast<int64_t>(slot0 + c) * a.num_v_heads + h) * kHeadBytes, kHeadBytes, bar);
-                    }
-                    const uint16_t *src = vsrc + t0 * a.v.stride_tok;
-                    if constexpr (VIO) {
-                        for (int i = id; i < C * 16; i += kLoaders) {
-                            const int row = i >> 4, piece = i & 15;
-                            const bool real = row < n && piece * 8 < width;
-                            cp_async16_or_zero(smem_u32(raw_v + row * kRawBytes + piece * 16), real ? src + row * a.v.stride_tok + piece * 8 : src, real);
-                        }
-                    } else {
-                        for (int i = id; i < C * 128; i += kLoaders) {
-                            const int row = i >> 7, dv = i & 127;
-                            reinterpret_cast<uint16_t *>(st + St::v + dv * kRowBytes)[row] =
-                                row < n && dv < width ? src[row * a.v.stride_tok + dv * a.v.stride_dim] : uint16_t(0);
-                        }
-                    }
-                    stage_rows<PANELS, VIO>(st, 2 * kTile, a.k, t0, hk, n, a.dim_k, id, kLoaders);
-                    stage_rows<PANELS, VIO>(st + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, id, kLoaders);
-                    if constexpr (VIO) {
-                        cp_async_commit();
-                        cp_async_wait<0>();
-                        sync_loaders();
-                        for (int g = lw; g < 32; g += kLoaders / 32) {  // values 8 (g / 2), tokens 32 (g % 2)
-                            uint32_t r[4];
-                            load_transposed(smem_u32(raw_v) + ((g & 1) * 32 + lane) * kRawBytes + (g >> 1) * 16, r);
-                            uint8_t *dst = st + St::v + ((g >> 1) * 8 + (lane >> 2)) * kRowBytes + (g & 1) * 64 + (lane & 3) * 4;
+            int c = 0;
+            for (; c < chunks; ++c) {
+                if (c >= kStages && !mbar_wait_warp(&sm.empty[c % kStages], (c / kStages - 1) & 1, &sm.abort)) break;
+                uint8_t *st = base + (c % kStages) * St::bytes;
+                uint64_t *bar = &sm.full[c % kStages];
+                const int t0 = s + c * C, n = min(C, e - t0);
+                if (id == 0) {
+                    mbar_expect_tx(bar, kHeadBytes);
+                    bulk_load(st + St::head, p.heads + (static_cast<int64_t>(slot0 + c) * a.num_v_heads + h) * kHeadBytes, kHeadBytes, bar);
+                }
+                if constexpr (VIO) {
+                    const int piece = id & 15;
+                    const uint16_t *src = vsrc + (t0 + (id >> 4)) * a.v.stride_tok + piece * 8;
+                    const uint32_t to = smem_u32(raw_v + (id >> 4) * kRawBytes + piece * 16);
 #pragma unroll
-                            for (int m = 0; m < 4; ++m) *reinterpret_cast<uint32_t *>(dst + m * 16) = r[m];
-                        }
-                        sync_loaders();
+                    for (int i = 0; i < C / 4; ++i) {
+                        const bool real = (id >> 4) + 4 * i < n && piece * 8 < width;
+                        cp_async16_or_zero(to + i * 4 * kRawBytes, real ? src : vsrc, real);
+                        src += 4 * a.v.stride_tok;
                     }
-                    fence_async_shared();
-                    mbar_arrive(bar);
-                    loaded = c + 1;
-                }
-                if (c >= 2) {  // the output of chunk c - 2, written while chunk c - 1 runs
-                    if (!(ok = mbar_wait_warp(&sm.out_full, c & 1, &sm.abort))) break;
-                    const int t0 = s + (c - 2) * C, n = min(C, e - t0);
-                    if constexpr (VIO) {
-                        for (int g = lw; g < 32; g += kLoaders / 32) {  // tokens 8 (g / 4), values 32 (g % 4)
-                            uint32_t r[4];
-                            load_transposed(smem_u32(out_tile) + ((g & 3) * 32 + lane) * kRowBytes + (g >> 2) * 16, r);
-                            transpose_quad(r);
-                            const int row = (g >> 2) * 8 + (lane >> 2), dv = (g & 3) * 32 + (lane & 3) * 8;
-                            if (row < n && dv < width)
-                                *reinterpret_cast<uint4 *>(out + (t0 + row) * a.out.stride_tok + dv) = make_uint4(r[0], r[1], r[2], r[3]);
-                        }
-                    } else {
-                        for (int i = id; i < n * 128; i += kLoaders)
-                            if ((i & 127) < width)
-                                out[(t0 + (i >> 7)) * a.out.stride_tok + (i & 127) * a.out.stride_dim] =
-                                    reinterpret_cast<const uint16_t *>(out_tile + (i & 127) * kRowBytes)[i >> 7];
+                } else {
+                    const uint16_t *src = vsrc + t0 * a.v.stride_tok;
+                    for (int i = id; i < C * 128; i += kLoaders) {
+                        const int row = i >> 7, dv = i & 127;
+                        reinterpret_cast<uint16_t *>(st + St::v + dv * kRowBytes)[row] =
+                            row < n && dv < width ? src[row * a.v.stride_tok + dv * a.v.stride_dim] : uint16_t(0);
                     }
-                    mbar_arrive(&sm.out_free);
                 }
+                cp_async_commit();
+                stage_rows<PANELS, VIO, kLoaders>(st, 2 * kTile, a.k, t0, hk, n, a.dim_k, id);
+                stage_rows<PANELS, VIO, kLoaders>(st + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, id);
+                cp_async_commit();
+                if constexpr (VIO) {
+                    cp_async_wait<1>();
+                    sync_loaders();
+#pragma unroll 4
+                    for (int g = lw; g < 32; g += kLoaders / 32) {  // values 8 (g / 2), tokens 32 (g % 2)
+                        uint32_t r[4];
+                        load_transposed(smem_u32(raw_v) + ((g & 1) * 32 + lane) * kRawBytes + (g >> 1) * 16, r);
+                        uint8_t *dst = st + St::v + ((g >> 1) * 8 + (lane >> 2)) * kRowBytes + (g & 1) * 64 + (lane & 3) * 4;
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) *reinterpret_cast<uint32_t *>(dst + m * 16) = r[m];
+                    }
+                    cp_async_wait<0>();
+                    sync_loaders();  // raw_v is read: the next chunk may overwrite it
+                }
+                fence_async_shared();
+                mbar_arrive(bar);
             }
-            if (!ok) {  // gave up: let the copies land before the shared memory goes
+            if (c < chunks) {  // gave up: let the copies land before the shared memory goes
                 int quiet = 0;
-                for (int i = 0; i < loaded; ++i)
-                    if (i + kStages >= loaded) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1, &quiet);
+                for (int i = max(0, c - kStages); i < c; ++i) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1, &quiet);
             }
         }
     } else {
@@ -804,7 +885,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 // ------------------------------------------------------------------- host ----
 
 template <int PANELS>
-constexpr size_t prep_smem() { return 1024 + PANELS * 2 * kTile + sizeof(PrepSmem); }
+constexpr size_t prep_smem() { return 1024 + kMatrixBytes + sizeof(PrepSmem); }
 template <int PANELS>
 constexpr size_t chunk_smem() { return 1024 + kStages * Stage<PANELS>::bytes + 128 * kRowBytes + C * kRawBytes + sizeof(ChunkSmem); }
 
