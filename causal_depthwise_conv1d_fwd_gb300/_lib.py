@@ -73,11 +73,10 @@ class GdrArgs(ctypes.Structure):
 
 # Argument lists of include/ccv_layer.h, in the order of its declarations.
 LAYER_SIGNATURES = {
-    "gdr_fwd": ([ctypes.POINTER(GdrArgs), P, I32, P, P, I32, P, I64, P, P], I32),
+    "gdr_fwd": ([P, P, I32, P, P, I32, P, I64, P, P], I32),
     "gdr_fwd_workspace": ([I32, I32, I32, I32, I32, I32], I64),
-    "gdr_update": ([ctypes.POINTER(GdrArgs), P, P, P, I64, I64, I32, I32, I32, P, P], I32),
-    "gated_rms_norm": ([ctypes.POINTER(HeadsView), ctypes.POINTER(HeadsView), P,
-                        ctypes.POINTER(HeadsView), I32, I32, I32, F32, I32, I32, P], I32),
+    "gdr_update": ([P, P, P, P, I64, I64, I32, I32, I32, P, P], I32),
+    "gated_rms_norm": ([P, P, P, P, I32, I32, I32, F32, I32, I32, P], I32),
     "residual_rms_norm": ([P, I64, I64, P, I64, I64, I32, P, P, P, I64, I64, P, I64, I64,
                            P, I64, I64, I32, I32, F32, F32, F32, P], I32),
     "spec_verify": ([P, I32, I64, I64, P, I64, I64, P, I64, I64, P, P, P, I64, I64, P, I64,

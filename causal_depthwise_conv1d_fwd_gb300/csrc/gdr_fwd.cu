@@ -106,39 +106,64 @@ struct PrepSmem {
 };
 constexpr int kMatrixBytes = 2 * C * kLd * 4;  // A, then T, of two value heads; over the rows of K and Q once they are used
 
-// Adds row . t for two columns, values paired along the inner index: 2 packed FMAs a pair of A's values for each.
-template <int N>
-__device__ __forceinline__ void dot2(const float *row, const f32x2 (&t)[2][16], f32x2 (&acc)[2][2]) {
+// C = sign A B for a 16 x 8 NT block of fp32 matrices in shared memory (leading dimension kLd), inner length 8 KS, by a warp
+// on the tensor cores.  Each value goes in as two tf32 parts (11 bits each; the second by the unit's own truncation) and
+// three of their products are added, so the result is good to 2^-21.
+template <int KS, int NT>
+__device__ __forceinline__ void multiply_block(const float *a, const float *b, float *c, float sign, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float acc[NT][4];
 #pragma unroll
-    for (int m = 0; m < N; m += 4) {
-        const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(row + m);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int col = 0; col < 2; ++col) {
-            acc[col][0] = fma2(r.x, t[col][m / 2], acc[col][0]);
-            acc[col][1] = fma2(r.y, t[col][m / 2 + 1], acc[col][1]);
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+    auto parts = [](float x, uint32_t &hi, uint32_t &lo) {
+        hi = __float_as_uint(x) & 0xffffe000u;
+        lo = __float_as_uint(x - __uint_as_float(hi));
+    };
+    auto mma = [](float (&d)[4], const uint32_t (&x)[4], const uint32_t (&y)[2]) {
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y[0]), "r"(y[1]));
+    };
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        uint32_t ah[4], al[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) parts(a[(g + 8 * (i & 1)) * kLd + 8 * k + t + 4 * (i >> 1)], ah[i], al[i]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) parts(b[(8 * k + t + 4 * i) * kLd + 8 * n + g], bh[i], bl[i]);
+            mma(acc[n], al, bh);
+            mma(acc[n], ah, bl);
+            mma(acc[n], ah, bh);
         }
     }
-}
-__device__ __forceinline__ float sum_pairs(const f32x2 (&acc)[2]) {
-    float a, b;
-    unpack2(add2(acc[0], acc[1]), a, b);
-    return a + b;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2 *>(c + (g + 8 * i) * kLd + 8 * n + 2 * t) = make_float2(sign * acc[n][2 * i], sign * acc[n][2 * i + 1]);
 }
 
 // T = (I + A)^-1 for the unit lower triangular 64 x 64 matrices of two heads (strictly lower part A, zeros above), by the
-// block's 128 threads: forward substitution of the diagonal 32 x 32 blocks, then T21 = -T22 (A21 T11).  Substitution, not a
-// power series: its error stays at the rounding of T however alike the keys are.  A thread has two columns, since a
-// broadcast load of 16 bytes costs the shared-memory pipe as much as 16 bytes for every lane; one column a thread made that
-// pipe the bound (19000 cycles a block against FMAs for 2500).  The upper right blocks hold scratch.
+// block's 128 threads: forward substitution of the diagonal 16 x 16 blocks, then twice T21 = -T22 (A21 T11), which doubles
+// the blocks.  Substitution and not a power series: its error stays at the rounding of T however alike the keys are.
+// Substitution reads a value of A for every column, and a broadcast load fills the shared-memory pipe like any other: done
+// for all 64 columns it took 17400 cycles a block (4 blocks an SM) against INVERT_CLK this way, the products on the tensor
+// cores.  The upper right 32 x 32 blocks hold scratch at the end.
 __device__ __forceinline__ void invert(float *matrices, int tid) {
-    f32x2 t[2][16];  // two columns, pairs of rows
-    if (tid < 64) {
-        const int which = tid >> 4, j = (tid & 15) * 2;
-        float *d = matrices + (which >> 1) * (C * kLd) + (which & 1) * (32 * kLd + 32);
+    const int warp = tid >> 5, lane = tid & 31;
+    if (tid < 64) {  // 8 blocks, two columns a thread, pairs of rows
+        const int which = tid >> 3, j = (tid & 7) * 2;
+        float *d = matrices + (which >> 2) * (C * kLd) + (which & 3) * (16 * kLd + 16);
+        f32x2 t[2][8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t[0][i] = t[1][i] = 0ull;
+        for (int i = 0; i < 8; ++i) t[0][i] = t[1][i] = 0ull;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
             f32x2 acc[2][2] = {{0ull, 0ull}, {0ull, 0ull}};
 #pragma unroll
             for (int m = 0; m < i; m += 4) {
@@ -149,17 +174,18 @@ __device__ __forceinline__ void invert(float *matrices, int tid) {
                     if (m + 2 < i) acc[col][1] = fma2(r.y, t[col][m / 2 + 1], acc[col][1]);
                 }
             }
-            float lo, hi;
 #pragma unroll
             for (int col = 0; col < 2; ++col) {
-                const float x = (i == j + col ? 1.0f : 0.0f) - sum_pairs(acc[col]);
+                float lo, hi;
+                unpack2(add2(acc[col][0], acc[col][1]), lo, hi);
+                const float x = (i == j + col ? 1.0f : 0.0f) - (lo + hi);
                 unpack2(t[col][i / 2], lo, hi);
                 t[col][i / 2] = (i & 1) ? pack2(lo, x) : pack2(x, hi);
             }
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
             float a0, a1, b0, b1;
             unpack2(t[0][i], a0, a1);
             unpack2(t[1][i], b0, b1);
@@ -168,29 +194,23 @@ __device__ __forceinline__ void invert(float *matrices, int tid) {
         }
     }
     __syncthreads();
-    // Two products of 32 x 32 blocks, 8 rows of two columns a thread: X = A21 T11, then -T22 X.
-    const int group = (tid >> 4) & 3, j = (tid & 15) * 2;
-    float *a = matrices + (tid >> 6) * (C * kLd);
-#pragma unroll 1
-    for (int step = 0; step < 2; ++step) {
-        const float *left = a + (32 + 8 * group) * kLd + 32 * step;
-        const float *right = a + 32 * step + j;
-        float *out = a + (8 * group + 32 * step) * kLd + 32 * (1 - step) + j;
-        const float sign = step ? -1.0f : 1.0f;
+    float *a = matrices + (warp >> 1) * (C * kLd);
+    {  // to 32 x 32, a warp a block; the product goes through the block's upper right quarter, zero again at the end
+        float *d = a + (warp & 1) * (32 * kLd + 32);
+        multiply_block<2, 2>(d + 16 * kLd, d, d + 16, 1.0f, lane);
+        __syncwarp();
+        multiply_block<2, 2>(d + 16 * kLd + 16, d + 16, d + 16 * kLd, -1.0f, lane);
+        __syncwarp();
 #pragma unroll
-        for (int m = 0; m < 16; ++m) {
-            const float2 x = *reinterpret_cast<const float2 *>(right + 2 * m * kLd), y = *reinterpret_cast<const float2 *>(right + (2 * m + 1) * kLd);
-            t[0][m] = pack2(x.x, y.x);
-            t[1][m] = pack2(x.y, y.y);
-        }
-#pragma unroll 2
-        for (int i = 0; i < 8; ++i) {
-            f32x2 acc[2][2] = {{0ull, 0ull}, {0ull, 0ull}};
-            dot2<32>(left + i * kLd, t, acc);
-            *reinterpret_cast<float2 *>(out + i * kLd) = make_float2(sign * sum_pairs(acc[0]), sign * sum_pairs(acc[1]));
-        }
-        __syncthreads();
+        for (int i = 0; i < 2; ++i) *reinterpret_cast<float4 *>(d + (i * 8 + (lane >> 2)) * kLd + 16 + (lane & 3) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    __syncthreads();
+    // to 64 x 64, half of the rows a warp
+    const int r = 16 * (warp & 1);
+    multiply_block<4, 4>(a + (32 + r) * kLd, a, a + r * kLd + 32, 1.0f, lane);
+    __syncthreads();
+    multiply_block<4, 4>(a + (32 + r) * kLd + 32, a + 32, a + (32 + r) * kLd, -1.0f, lane);
+    __syncthreads();
 }
 
 // PANELS: dim_k rounded up to 64 PANELS.  V: rows of q and k allow 16-byte vectors.

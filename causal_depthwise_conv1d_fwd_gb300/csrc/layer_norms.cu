@@ -81,48 +81,62 @@ struct GatedArgs {
     int activation, before;
 };
 
-template <int LPR, int VEC, int NV>
+// R: rows a thread has in flight at once.  One row of 128 values is 64 bytes a lane, x and gate together, which leaves HBM
+// waiting on block turnover: 16384 x 32 rows take GATED_R1 us with 1 row a thread and GATED_R4 with 4.
+template <int LPR, int VEC, int NV, int R>
 __global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) gated_rms_norm_kernel(const __grid_constant__ GatedArgs a) {
     __shared__ float warp_sums[32];
     wait_prior_grid();
     release_next_grid();
     constexpr int kThreads = LPR > kNormThreads ? LPR : kNormThreads;
+    constexpr int kRows = kThreads / LPR;  // rows of a block's pass
     const int lane = threadIdx.x % LPR;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
-    const bool live = row < a.rows;
-    const int64_t tok = live ? row / a.heads : 0, head = live ? row % a.heads : 0;
-    const int dim = live ? a.dim : 0;
-    const uint16_t *xp = static_cast<const uint16_t *>(a.x.data) + tok * a.x.stride_tok + head * a.x.stride_head;
-    const uint16_t *gp = static_cast<const uint16_t *>(a.gate.data) + tok * a.gate.stride_tok + head * a.gate.stride_head;
-    uint16_t *op = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + tok * a.out.stride_tok + head * a.out.stride_head;
-    float x[NV][VEC], z[NV][VEC];
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRows * R) + threadIdx.x / LPR;
+    float x[R][NV][VEC], z[R][NV][VEC];
+    uint16_t *op[R];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int d = (j * LPR + lane) * VEC;
-        load_row<VEC>(xp, a.x.stride_dim, d, dim, x[j]);
-        load_row<VEC>(gp, a.gate.stride_dim, d, dim, z[j]);
-    }
-    float sum = 0.0f;
+    for (int r = 0; r < R; ++r) {
+        const int64_t row = first + r * kRows;
+        const bool live = row < a.rows;
+        const int64_t tok = live ? row / a.heads : 0, head = live ? row % a.heads : 0;
+        const int dim = live ? a.dim : 0;
+        const uint16_t *xp = static_cast<const uint16_t *>(a.x.data) + tok * a.x.stride_tok + head * a.x.stride_head;
+        const uint16_t *gp = static_cast<const uint16_t *>(a.gate.data) + tok * a.gate.stride_tok + head * a.gate.stride_head;
+        op[r] = live ? static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + tok * a.out.stride_tok + head * a.out.stride_head
+                     : nullptr;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            z[j][i] = gate_act(z[j][i], a.activation);
-            if (!a.before) {  // past the row's end x is 0 and the gate finite
-                x[j][i] *= z[j][i];
-                z[j][i] = 1.0f;
-            }
-            sum = fmaf(x[j][i], x[j][i], sum);
+        for (int j = 0; j < NV; ++j) {
+            const int d = (j * LPR + lane) * VEC;
+            load_row<VEC>(xp, a.x.stride_dim, d, dim, x[r][j]);
+            load_row<VEC>(gp, a.gate.stride_dim, d, dim, z[r][j]);
         }
-    const float scale = rsqrtf(row_sum<LPR>(sum, warp_sums) / a.dim + a.eps);
+    }
+    float w[NV][VEC];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int d = (j * LPR + lane) * VEC;
-        float w[VEC];
-        load_row<VEC>(a.weight, 1, d, dim, w);
+    for (int j = 0; j < NV; ++j) load_row<VEC>(a.weight, 1, (j * LPR + lane) * VEC, a.dim, w[j]);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) w[i] = x[j][i] * scale * w[i] * z[j][i];
-        store_row<VEC>(op, a.out.stride_dim, d, dim, w);
+    for (int r = 0; r < R; ++r) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                z[r][j][i] = gate_act(z[r][j][i], a.activation);
+                if (!a.before) {  // past the row's end x is 0 and the gate finite
+                    x[r][j][i] *= z[r][j][i];
+                    z[r][j][i] = 1.0f;
+                }
+                sum = fmaf(x[r][j][i], x[r][j][i], sum);
+            }
+        const float scale = rsqrtf(row_sum<LPR>(sum, warp_sums) / a.dim + a.eps);
+        const int dim = op[r] != nullptr ? a.dim : 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float y[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) y[i] = x[r][j][i] * scale * w[j][i] * z[r][j][i];
+            store_row<VEC>(op[r], a.out.stride_dim, (j * LPR + lane) * VEC, dim, y);
+        }
     }
 }
 
@@ -231,7 +245,14 @@ struct GatedLaunch {
     cudaStream_t stream;
     template <int LPR, int VEC, int NV>
     int operator()() const {
-        return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV>, dim3(row_blocks(a.rows, LPR)),
+        // Four rows a thread once there are enough rows for every SM's threads to have four: below that one row each
+        // spreads the call over more SMs.
+        if constexpr (LPR <= 32 && VEC == 8 && NV == 1) {
+            if (a.rows * LPR >= 4ll * 2048 * current_device_sms())
+                return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV, 4>, dim3(row_blocks((a.rows + 3) / 4, LPR)),
+                                  dim3(kNormThreads), 0, stream, a);
+        }
+        return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV, 1>, dim3(row_blocks(a.rows, LPR)),
                           dim3(LPR > kNormThreads ? LPR : kNormThreads), 0, stream, a);
     }
 };

@@ -11,11 +11,12 @@
 namespace ccv {
 namespace {
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
+constexpr int kVectors = 4;                               // vectors of 8 logits a thread holds
+constexpr int kSplit = kVerifyThreads * kVectors * 8;     // a block's share of a row: 8192 logits
 
 struct VerifyArgs {
     const void *logits;
-    int logits_fp32;
     int64_t tb, tp;
     const int32_t *tokens;
     int64_t db, dp;
@@ -28,17 +29,46 @@ struct VerifyArgs {
     const float *noise;
     int64_t nb;
     int32_t *out_tokens, *num_accepted;
-    int batch, drafts, vocab;
-    float *stats;  // (batch, drafts + 1, 4): maximum, its index's bits, sum of exponentials
+    int batch, drafts, vocab, splits;
+    float4 *stats;     // (batch, drafts + 1, splits): maximum, its index's bits, sum of exponentials
+    float2 *best;      // (batch, splits): a share's best score and its index's bits
+    unsigned *done;    // (batch): shares finished
     int *err_count;
 };
 
 // A logit: NaN is masked like -inf, +inf is the largest finite value.
 __device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
+__device__ __forceinline__ float widen(uint16_t x) { return bf16_bits(x); }
+__device__ __forceinline__ float widen(float x) { return x; }
 
-__device__ __forceinline__ float logit(const VerifyArgs &a, int64_t off) {
-    return clean(a.logits_fp32 ? static_cast<const float *>(a.logits)[off]
-                               : bf16_bits(static_cast<const uint16_t *>(a.logits)[off]));
+// 8 logits from row[i..], of which those in [0, end) are real; the others come back as -inf.  `aligned`: row + i is on a
+// 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ void load8(const T *row, int i, int end, bool aligned, float (&f)[8]) {
+    if (aligned && i >= 0 && i + 8 <= end) {
+        if constexpr (sizeof(T) == 2) {
+            Raw<8> r;
+            r.v = *reinterpret_cast<const uint4 *>(row + i);
+            r.to_float(f);
+        } else {
+            const float4 x = *reinterpret_cast<const float4 *>(row + i), y = *reinterpret_cast<const float4 *>(row + i + 4);
+            f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w; f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = clean(f[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = i + k >= 0 && i + k < end ? clean(widen(row[i + k])) : -INFINITY;
+    }
+}
+__device__ __forceinline__ void load8_plain(const float *row, int i, int end, bool aligned, float (&f)[8]) {
+    if (aligned && i + 8 <= end) {
+        const float4 x = *reinterpret_cast<const float4 *>(row + i), y = *reinterpret_cast<const float4 *>(row + i + 4);
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w; f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = i + k >= 0 && i + k < end ? row[i + k] : 1.0f;
+    }
 }
 
 // The larger value, and of equal ones the lower index.
@@ -48,21 +78,21 @@ __device__ __forceinline__ void take_best(float &v, int &i, float ov, int oi) {
         i = oi;
     }
 }
-
-template <int kThreads>
-__device__ __forceinline__ void block_best(float &v, int &i, float *sv, int *si) {
+__device__ __forceinline__ void warp_best(float &v, int &i) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) take_best(v, i, __shfl_xor_sync(kFullMask, v, m), __shfl_xor_sync(kFullMask, i, m));
+}
+__device__ __forceinline__ void block_best(float &v, int &i, float *sv, int *si) {
+    warp_best(v, i);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (lane == 0) {
         sv[warp] = v;
         si[warp] = i;
     }
     __syncthreads();
-    v = lane < kThreads / 32 ? sv[lane] : -INFINITY;
-    i = lane < kThreads / 32 ? si[lane] : INT32_MAX;
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) take_best(v, i, __shfl_xor_sync(kFullMask, v, m), __shfl_xor_sync(kFullMask, i, m));
+    v = lane < kVerifyThreads / 32 ? sv[lane] : -INFINITY;
+    i = lane < kVerifyThreads / 32 ? si[lane] : INT32_MAX;
+    warp_best(v, i);
     __syncthreads();
 }
 
@@ -70,32 +100,49 @@ __device__ __forceinline__ void block_best(float &v, int &i, float *sv, int *si)
 __device__ __forceinline__ float weight_of(float x, float best, float inv_temp) {
     return x == -INFINITY ? 0.0f : expf((x - best) * inv_temp);
 }
+__device__ __forceinline__ float inverse_temperature(const VerifyArgs &a, int b) {
+    const float t = a.temperature != nullptr ? a.temperature[b] : 1.0f;
+    return t > 0.0f ? 1.0f / t : 0.0f;  // 0 marks a greedy row
+}
 
+// Maximum, its first index and the sum of exponentials of one share of one position.  Rows may start at any element: the
+// shares count from the 16-byte boundary at or before the row's start, so that all but the edges are whole vectors.
+template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads) verify_stats_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ float sv[32];
     __shared__ int si[32];
     wait_prior_grid();
-    const int pos = blockIdx.x % (a.drafts + 1), b = blockIdx.x / (a.drafts + 1);
+    release_next_grid();
+    const int split = blockIdx.x % a.splits, row = blockIdx.x / a.splits;
+    const int pos = row % (a.drafts + 1), b = row / (a.drafts + 1);
+    if (pos == 0 && split == 0 && threadIdx.x == 0) a.done[b] = 0;
     const int n = a.num_drafts != nullptr ? a.num_drafts[b] : a.drafts;
     if (pos > n) return;
-    const float temp = a.temperature != nullptr ? a.temperature[b] : 1.0f;
-    const float inv = temp > 0.0f ? 1.0f / temp : 1.0f;
-    const int64_t at = b * a.tb + pos * a.tp;
-    float best = -INFINITY, sum = 0.0f;
+    const float inv = inverse_temperature(a, b);
+    const T *logits = static_cast<const T *>(a.logits) + b * a.tb + pos * a.tp;
+    const int before = static_cast<int>(reinterpret_cast<uintptr_t>(logits) % 16 / sizeof(T));
+    const int start = split * kSplit - before;
+    float x[kVectors][8];
+#pragma unroll
+    for (int j = 0; j < kVectors; ++j) load8(logits, start + (j * kVerifyThreads + threadIdx.x) * 8, a.vocab, true, x[j]);
+    float best = -INFINITY;
     int index = INT32_MAX;
-    for (int v = threadIdx.x; v < a.vocab; v += kVerifyThreads) {
-        const float x = logit(a, at + v);
-        if (x > best) {
-            sum = sum * weight_of(best, x, inv) + 1.0f;
-            best = x;
-            index = v;
-        } else {
-            sum += weight_of(x, best, inv);
-        }
+#pragma unroll
+    for (int j = 0; j < kVectors; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (x[j][k] > best) {
+                best = x[j][k];
+                index = start + (j * kVerifyThreads + threadIdx.x) * 8 + k;
+            }
+    block_best(best, index, sv, si);
+    float sum = 0.0f;
+    if (inv > 0.0f) {
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += weight_of(x[j][k], best, inv);
     }
-    const float mine = best;
-    block_best<kVerifyThreads>(best, index, sv, si);
-    sum *= weight_of(mine, best, inv);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(kFullMask, sum, m);
     if (threadIdx.x % 32 == 0) sv[threadIdx.x / 32] = sum;
@@ -103,77 +150,149 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_stats_kernel(const __gr
     if (threadIdx.x == 0) {
         float z = 0.0f;
         for (int w = 0; w < kVerifyThreads / 32; ++w) z += sv[w];
-        float *out = a.stats + static_cast<int64_t>(blockIdx.x) * 4;
-        out[0] = best;
-        out[1] = __int_as_float(index);
-        out[2] = z;
+        a.stats[blockIdx.x] = make_float4(best, __int_as_float(index), z, 0.0f);
     }
 }
 
+// Every share of a row repeats the acceptance (a few values), then races its part of the vocabulary; the share that ends
+// last joins them.
+template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ float sv[32];
     __shared__ int si[32];
-    __shared__ int s_kept;
+    __shared__ int s_kept, s_top;
+    __shared__ float s_best, s_z;
+    __shared__ bool s_last;
     wait_prior_grid();
-    const int b = blockIdx.x;
-    int n = a.num_drafts != nullptr ? a.num_drafts[b] : a.drafts;
+    release_next_grid();
+    const int split = blockIdx.x % a.splits, b = blockIdx.x / a.splits;
+    const int n = min(a.num_drafts != nullptr ? a.num_drafts[b] : a.drafts, a.drafts);
     int32_t *out = a.out_tokens + static_cast<int64_t>(b) * (a.drafts + 1);
     if (n < 0) {
-        for (int i = threadIdx.x; i <= a.drafts; i += kVerifyThreads) out[i] = -1;
-        if (threadIdx.x == 0) a.num_accepted[b] = 0;
+        if (split == 0) {
+            for (int i = threadIdx.x; i <= a.drafts; i += kVerifyThreads) out[i] = -1;
+            if (threadIdx.x == 0) a.num_accepted[b] = 0;
+        }
         return;
     }
-    if (n > a.drafts) n = a.drafts;
-    const float temp = a.temperature != nullptr ? a.temperature[b] : 1.0f;
-    const bool greedy = !(temp > 0.0f);
-    const float inv = greedy ? 1.0f : 1.0f / temp;
-    const float *stats = a.stats + static_cast<int64_t>(b) * (a.drafts + 1) * 4;
-    if (threadIdx.x == 0) {
-        int kept = 0;
-        for (; kept < n; ++kept) {
-            const int token = a.tokens[b * a.db + kept * a.dp];
-            if (token < 0 || token >= a.vocab) {
-                count_error(a.err_count);
+    const float inv = inverse_temperature(a, b);
+    const bool greedy = inv == 0.0f;
+    const T *row = static_cast<const T *>(a.logits) + b * a.tb;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        for (int i0 = 0;; i0 += 32) {  // positions i0 + lane; the row's last one (n) has no draft and ends the search
+            const int i = i0 + lane;
+            float best = -INFINITY, z = 0.0f;
+            int top = INT32_MAX;
+            bool keep = false;
+            if (i <= n) {
+                const float4 *st = a.stats + (static_cast<int64_t>(b) * (a.drafts + 1) + i) * a.splits;
+                for (int k = 0; k < a.splits; ++k) {
+                    const float4 x = st[k];
+                    if (x.x > best) {
+                        z *= weight_of(best, x.x, inv);
+                        best = x.x;
+                        top = __float_as_int(x.y);
+                    }
+                    z += x.x == -INFINITY ? 0.0f : x.z * weight_of(x.x, best, inv);
+                }
+            }
+            if (i < n) {
+                const int token = a.tokens[b * a.db + i * a.dp];
+                if (token >= 0 && token < a.vocab) {
+                    float p = greedy && token == top && best > -INFINITY ? 1.0f : 0.0f;
+                    if (!greedy && z > 0.0f) p = weight_of(clean(widen(row[i * a.tp + token])), best, inv) / z;
+                    const float q = a.probs != nullptr ? a.probs[b * a.pb + i * a.pp + token] : 1.0f;
+                    keep = a.uniform[b * a.ub + i * a.up] * q < p;
+                }
+            }
+            const unsigned stop = __ballot_sync(kFullMask, !keep);
+            if (stop != 0) {
+                const int at = __ffs(stop) - 1;
+                if (lane == at) {
+                    s_kept = i;
+                    s_best = best;
+                    s_z = z;
+                    s_top = top;
+                    if (split == 0 && i < n) {
+                        const int token = a.tokens[b * a.db + i * a.dp];
+                        if (token < 0 || token >= a.vocab) count_error(a.err_count);
+                    }
+                }
                 break;
             }
-            const float *st = stats + kept * 4;
-            float p;
-            if (greedy) p = st[0] > -INFINITY && token == __float_as_int(st[1]) ? 1.0f : 0.0f;
-            else p = st[2] > 0.0f ? weight_of(logit(a, b * a.tb + kept * a.tp + token), st[0], inv) / st[2] : 0.0f;
-            const float q = a.probs != nullptr ? a.probs[b * a.pb + kept * a.pp + token] : 1.0f;
-            if (!(a.uniform[b * a.ub + kept * a.up] * q < p)) break;
         }
-        s_kept = kept;
     }
     __syncthreads();
     const int kept = s_kept;
-    const float best = stats[kept * 4], z = stats[kept * 4 + 2];
+    const float best = s_best, z = s_z;
     float top = 0.0f;  // a score has to be above 0
     int index = INT32_MAX;
-    if (greedy) {
-        if (best > -INFINITY) {
-            top = 1.0f;
-            index = __float_as_int(stats[kept * 4 + 1]);
-        }
-    } else if (z > 0.0f) {
-        const int64_t at = b * a.tb + kept * a.tp;
+    const bool race = !greedy && z > 0.0f;
+    if (race) {
+        const T *logits = row + kept * a.tp;
         const float *q = kept < n && a.probs != nullptr ? a.probs + b * a.pb + kept * a.pp : nullptr;
+        const float *noise = a.noise + b * a.nb;
         const int sure = kept < n && a.probs == nullptr ? a.tokens[b * a.db + kept * a.dp] : -1;
-        for (int v = threadIdx.x; v < a.vocab; v += kVerifyThreads) {
-            float r = weight_of(logit(a, at + v), best, inv) / z;
-            if (q != nullptr) r -= q[v];
-            if (v == sure) r = 0.0f;
-            const float score = r / a.noise[b * a.nb + v];
-            if (r > 0.0f && score > top) {
-                top = score;
-                index = v;
+        // whole vectors where all three rows allow them
+        const int before = static_cast<int>(reinterpret_cast<uintptr_t>(logits) % 16 / sizeof(T));
+        const int start = split * kSplit - before;
+        const bool vn = reinterpret_cast<uintptr_t>(noise + start) % 16 == 0;
+        const bool vq = q != nullptr && reinterpret_cast<uintptr_t>(q + start) % 16 == 0;
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j) {
+            const int v0 = start + (j * kVerifyThreads + threadIdx.x) * 8;
+            float x[8], w[8], y[8] = {};
+            load8(logits, v0, a.vocab, true, x);
+            load8_plain(noise, v0, a.vocab, vn && v0 >= 0, w);
+            if (q != nullptr) load8_plain(q, v0, a.vocab, vq && v0 >= 0, y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float r = weight_of(x[k], best, inv) / z - y[k];
+                if (v0 + k == sure) r = 0.0f;
+                if (r > 0.0f) {
+                    const float score = r / w[k];
+                    if (score > top) {
+                        top = score;
+                        index = v0 + k;
+                    }
+                }
             }
         }
-        block_best<kVerifyThreads>(top, index, sv, si);
+        block_best(top, index, sv, si);
+        if (threadIdx.x == 0) {
+            a.best[static_cast<int64_t>(b) * a.splits + split] = make_float2(top, __int_as_float(index));
+            __threadfence();
+            s_last = atomicAdd(a.done + b, 1u) == static_cast<unsigned>(a.splits) - 1;
+        }
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+        top = 0.0f;
+        index = INT32_MAX;
+        for (int k = threadIdx.x % 32; k < a.splits; k += 32) {
+            const float2 x = __ldcg(a.best + static_cast<int64_t>(b) * a.splits + k);
+            take_best(top, index, x.x, __float_as_int(x.y));
+        }
+        warp_best(top, index);
+    } else {
+        if (split != 0) return;
+        if (greedy && best > -INFINITY) index = s_top;
     }
     for (int i = threadIdx.x; i <= a.drafts; i += kVerifyThreads)
         out[i] = i < kept ? a.tokens[b * a.db + i * a.dp] : i == kept && index != INT32_MAX ? index : -1;
     if (threadIdx.x == 0) a.num_accepted[b] = kept + 1;
+}
+
+// Shares of a row: its logits and up to 7 before them (see verify_stats_kernel).
+int64_t verify_splits(int vocab) { return (static_cast<int64_t>(vocab) + 7 + kSplit - 1) / kSplit; }
+
+template <typename T>
+int launch_verify(const VerifyArgs &a, cudaStream_t stream) {
+    const int status = launch_pdl(verify_stats_kernel<T>, dim3(static_cast<unsigned>(a.batch) * (a.drafts + 1) * a.splits),
+                                  dim3(kVerifyThreads), 0, stream, a);
+    if (status != CCV_OK) return status;
+    return launch_pdl(verify_pick_kernel<T>, dim3(static_cast<unsigned>(a.batch) * a.splits), dim3(kVerifyThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -181,7 +300,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(const __gri
 
 extern "C" int64_t spec_verify_workspace(int batch, int drafts, int vocab) {
     if (batch <= 0 || drafts < 0 || vocab <= 0) return 0;
-    return static_cast<int64_t>(batch) * (drafts + 1) * 16;
+    const int64_t shares = static_cast<int64_t>(batch) * ccv::verify_splits(vocab);
+    return shares * (drafts + 1) * 16 + shares * 8 + static_cast<int64_t>(batch) * 4;
 }
 
 extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t_stride_b, int64_t t_stride_pos,
@@ -196,7 +316,7 @@ extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t
                       n_stride_b})
         if (s < 0) return CCV_ERR_STRIDE;
     if (batch == 0) return CCV_OK;
-    if (vocab == 0 || static_cast<int64_t>(batch) * (drafts + 1) > 0x7fffffff) return CCV_ERR_SIZE;
+    if (vocab == 0 || static_cast<int64_t>(batch) * (drafts + 1) * verify_splits(vocab) > 0x7fffffff) return CCV_ERR_SIZE;
     if (target_logits == nullptr || noise == nullptr || out_tokens == nullptr || num_accepted == nullptr ||
         (drafts > 0 && (draft_tokens == nullptr || uniform == nullptr)))
         return CCV_ERR_NULL_POINTER;
@@ -213,12 +333,12 @@ extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t
         (num_drafts != nullptr &&
          (overlaps(et, extent(num_drafts, batch, 1, 1, 0)) || overlaps(ea, extent(num_drafts, batch, 1, 1, 0)))))
         return CCV_ERR_ALIAS;
-    const VerifyArgs a{target_logits, logits_fp32, t_stride_b, t_stride_pos, draft_tokens, d_stride_b, d_stride_pos,
-                       draft_probs, p_stride_b, p_stride_pos, num_drafts, temperature, uniform, u_stride_b, u_stride_pos,
-                       noise, n_stride_b, out_tokens, num_accepted, batch, drafts, vocab,
-                       static_cast<float *>(workspace), err_count};
-    const int status = launch_pdl(verify_stats_kernel, dim3(static_cast<unsigned>(batch * (drafts + 1))),
-                                  dim3(kVerifyThreads), 0, stream, a);
-    if (status != CCV_OK) return status;
-    return launch_pdl(verify_pick_kernel, dim3(static_cast<unsigned>(batch)), dim3(kVerifyThreads), 0, stream, a);
+    const int64_t shares = static_cast<int64_t>(batch) * verify_splits(vocab);
+    uint8_t *space = static_cast<uint8_t *>(workspace);
+    const VerifyArgs a{target_logits, t_stride_b, t_stride_pos, draft_tokens, d_stride_b, d_stride_pos, draft_probs, p_stride_b,
+                       p_stride_pos, num_drafts, temperature, uniform, u_stride_b, u_stride_pos, noise, n_stride_b, out_tokens,
+                       num_accepted, batch, drafts, vocab, static_cast<int>(verify_splits(vocab)),
+                       reinterpret_cast<float4 *>(space), reinterpret_cast<float2 *>(space + shares * (drafts + 1) * 16),
+                       reinterpret_cast<unsigned *>(space + shares * (drafts + 1) * 16 + shares * 8), err_count};
+    return logits_fp32 ? launch_verify<float>(a, stream) : launch_verify<uint16_t>(a, stream);
 }

@@ -3,21 +3,53 @@ runs next to the causal convolution (gated delta rule, norms, draft
 verification).  Argument marshalling only, as in :mod:`.api`."""
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import Optional, Tuple
 
 import torch
 
 from . import _lib
-from .api import PAD_SLOT_ID, Launch, _index_vector, _need_cuda, _ptr
+from .api import PAD_SLOT_ID, Launch, _check, _stream
 
 _ACTIVATIONS = {None: 0, "silu": 1, "swish": 1, "sigmoid": 2}
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+# struct ccv_heads_view and struct ccv_gdr_args of include/ccv_layer.h.  A call
+# passes them packed into bytes: building ctypes structures field by field costs
+# more than the launch of a decode step.
+_VIEW = struct.Struct("<Qqqqq")
+_GDR = struct.Struct("<" + "Qqqqq" * 4 + "QQqqq" + "QQQqqqq" + "iiiiifii")
+
+_FUNCTIONS = {}
+
+
+def _call(name: str, args: tuple, device: int, stream, scratch: Optional[torch.Tensor] = None):
+    """One call of an entry point on the tensors' device and the given or that
+    device's current stream."""
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(_lib.load(), name)
+    if torch._C._cuda_getDevice() != device:
+        with torch.cuda.device(device):
+            return _call(name, args, device, stream, scratch)
+    if stream is None:
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(device)), name)
+    else:
+        _check(fn(*args, _stream(stream, device)), name)
+        if scratch is not None:
+            _used_on(scratch, stream, device)
+
+
+def _used_on(scratch: torch.Tensor, stream, device: int):
+    """Tell the allocator that a workspace of the current stream is in use on another one."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    scratch.record_stream(stream)
 
 
 class ScratchLaunch(Launch):
     """A Launch whose call uses a workspace.  One that the binding allocated
-    belongs to the plan: on a stream other than its own the allocator is told,
-    and the plan must not run on two streams at once."""
+    belongs to the plan: the plan must not run on two streams at once."""
 
     def __init__(self, name, args, result, keep, scratch: torch.Tensor):
         super().__init__(name, args, result, keep)
@@ -26,75 +58,108 @@ class ScratchLaunch(Launch):
     def _launch(self, stream):
         result = super()._launch(stream)
         if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-            self._scratch.record_stream(stream)
+            _used_on(self._scratch, stream, self.device)
         return result
 
 
-def _workspace(given: Optional[torch.Tensor], size: int, device) -> torch.Tensor:
+def _need(dev: int, t: torch.Tensor, name: str, *dtypes):
+    """t is a tensor of the call's CUDA device and of one of the types."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0 or t.device.type != "cuda":
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"all tensors of a call must be on one device, got cuda:{dev} and "
+                         f"{t.device} ({name})")
+    return t
+
+
+def _first(t, name: str, *dtypes) -> int:
+    """The call's device: that of its first tensor."""
+    _need(t.get_device() if isinstance(t, torch.Tensor) else -1, t, name, *dtypes)
+    return t.get_device()
+
+
+def _vector(dev: int, t: Optional[torch.Tensor], name: str, dtype, length: int):
+    """Pointer of a contiguous vector of at least `length` entries, or None."""
+    if t is None:
+        return None
+    _need(dev, t, name, dtype)
+    if t.dim() != 1 or t.stride(0) != 1:
+        raise ValueError(f"{name} must be a contiguous 1-D tensor")
+    if t.shape[0] < length:
+        raise ValueError(f"{name} has {t.shape[0]} entries, needs {length}")
+    return t.data_ptr()
+
+
+def _err(dev: int, t: Optional[torch.Tensor]):
+    return None if t is None else _need(dev, t, "err_count", _I32).data_ptr()
+
+
+def _workspace(dev: int, given: Optional[torch.Tensor], size: int, like: torch.Tensor):
     if given is None:
-        return torch.empty(size, dtype=torch.uint8, device=device)
-    _need_cuda(given, "workspace", torch.uint8)
-    if given.dim() != 1 or (given.numel() and given.stride(0) != 1):
+        return torch.empty(size, dtype=_U8, device=like.device)
+    _need(dev, given, "workspace", _U8)
+    if given.dim() != 1 or (given.shape[0] and given.stride(0) != 1):
         raise ValueError("workspace must be a contiguous 1-D tensor")
     return given
 
 
-def _view(t: torch.Tensor, has_row: bool) -> _lib.HeadsView:
-    st = t.stride()
-    return _lib.HeadsView(t.data_ptr(), *(st if has_row else (0, *st)))
-
-
-def _gdr_args(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slot_id, out,
-              has_row: bool):
-    """Checks shared by gdr_fwd and gdr_update; (..., heads, dim) tensors."""
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _need_cuda(t, name, torch.bfloat16)
-        if t.dim() != (4 if has_row else 3):
-            raise ValueError(f"{name} must be ({'batch, seqlen' if has_row else 'total_tokens'}, "
-                             "heads, dim)")
-    lead = v.shape[:-2]
-    hv, dv = v.shape[-2:]
-    hk, dk = k.shape[-2:]
-    if q.shape != k.shape or k.shape[:-2] != lead:
+def _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slot_id, out, mode):
+    """Checks shared by gdr_fwd and gdr_update.  mode: "tokens" for (tokens,
+    heads, dim) tensors, "rows" for (batch, heads, dim), "steps" for (batch,
+    seqlen, heads, dim).  Returns (device, packed ccv_gdr_args, out, sizes)."""
+    dev = _first(v, "v", _BF16)
+    _need(dev, k, "k", _BF16)
+    _need(dev, q, "q", _BF16)
+    lead = 2 if mode == "steps" else 1
+    vs, ks = v.shape, k.shape
+    if len(vs) != lead + 2:
+        raise ValueError(f"v must have {lead + 2} dimensions, got {len(vs)}")
+    if q.shape != ks or ks[:lead] != vs[:lead] or len(ks) != lead + 2:
         raise ValueError("q and k must have the same shape, and v the same tokens")
+    hv, dv = vs[lead:]
+    hk, dk = ks[lead:]
     if (a_log is None) != (dt_bias is None):
         raise ValueError("a_log and dt_bias go together")
-    gate_dtype = torch.float32 if a_log is None else torch.bfloat16
-    for t, name in ((g, "g"), (beta, "beta")):
-        _need_cuda(t, name, gate_dtype)
-        if t.shape != (*lead, hv):
-            raise ValueError(f"{name} must have shape {(*lead, hv)}, got {tuple(t.shape)}")
-    if beta.stride() != g.stride():
+    dtype = _F32 if a_log is None else _BF16
+    _need(dev, g, "g", dtype)
+    _need(dev, beta, "beta", dtype)
+    if g.shape != vs[:-1] or beta.shape != vs[:-1]:
+        raise ValueError(f"g and beta must have shape {tuple(vs[:-1])}")
+    gs = g.stride()
+    if beta.stride() != gs:
         raise ValueError("g and beta must have the same strides")
+    al = db = sp = lines = 0
+    ss = (0, 0, 0, 0)
     if a_log is not None:
-        for t, name in ((a_log, "a_log"), (dt_bias, "dt_bias")):
-            _index_vector(t, name, torch.float32, hv)
-            if t.numel() != hv:
-                raise ValueError(f"{name} must have {hv} entries, got {t.numel()}")
+        al, db = (_vector(dev, t, n, _F32, hv) for t, n in ((a_log, "a_log"), (dt_bias, "dt_bias")))
+        if a_log.shape[0] != hv or dt_bias.shape[0] != hv:
+            raise ValueError(f"a_log and dt_bias must have {hv} entries")
     if state is not None:
-        _need_cuda(state, "state", torch.float32)
-        if state.dim() != 4 or state.shape[1:] != (hv, dv, dk):
+        _need(dev, state, "state", _F32)
+        lines = state.shape[0]
+        if state.shape != (lines, hv, dv, dk):
             raise ValueError("state must be (num_lines, num_v_heads, dim_v, dim_k)")
-        ss, lines = state.stride(), state.shape[0]
-    else:
-        ss, lines = (0, 0, 0, 0), 0
+        ss, sp = state.stride(), state.data_ptr()
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        out = torch.empty(vs, dtype=_BF16, device=v.device)
     else:
-        _need_cuda(out, "out", torch.bfloat16)
-        if out.shape != v.shape:
+        _need(dev, out, "out", _BF16)
+        if out.shape != vs:
             raise ValueError("out must have v's shape")
-    gs = g.stride() if has_row else (0, *g.stride())
-    args = _lib.GdrArgs(_view(q, has_row), _view(k, has_row), _view(v, has_row),
-                        _view(out, has_row), g.data_ptr(), beta.data_ptr(), *gs,
-                        a_log.data_ptr() if a_log is not None else None,
-                        dt_bias.data_ptr() if dt_bias is not None else None,
-                        state.data_ptr() if state is not None else None, *ss, lines, hk, hv, dk, dv,
-                        dk ** -0.5 if scale is None and dk else float(scale or 0.0),
-                        int(bool(qk_l2norm)), pad_slot_id)
-    return args, out
+    qs, ks_, vst, os_ = q.stride(), k.stride(), v.stride(), out.stride()
+    if mode == "tokens":
+        qs, ks_, vst, os_, gs = (0, *qs), (0, *ks_), (0, *vst), (0, *os_), (0, *gs)
+    elif mode == "rows":
+        qs, ks_, vst, os_ = ((t[0], 0, t[1], t[2]) for t in (qs, ks_, vst, os_))
+        gs = (gs[0], 0, gs[1])
+    if scale is None:
+        scale = dk ** -0.5 if dk else 0.0
+    packed = _GDR.pack(q.data_ptr(), *qs, k.data_ptr(), *ks_, v.data_ptr(), *vst, out.data_ptr(),
+                       *os_, g.data_ptr(), beta.data_ptr(), *gs, al, db, sp, *ss, lines, hk, hv, dk,
+                       dv, scale, 1 if qk_l2norm else 0, pad_slot_id)
+    return dev, packed, out, (hk, hv, dk, dv)
 
 
 def gdr_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
@@ -114,33 +179,46 @@ def gdr_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
     bf16 projections they come from.  state is (num_lines, num_v_heads, dim_v,
     dim_k) fp32.  scale defaults to dim_k ** -0.5.  Returns out.
     """
-    return prepare_gdr_fwd(q, k, v, g, beta, state, query_start_loc, cache_indices,
-                           has_initial_state, scale, qk_l2norm, a_log, dt_bias, pad_slot_id, out,
-                           workspace, err_count)(stream)
+    dev, args, out, scratch, _ = _marshal_gdr_fwd(q, k, v, g, beta, state, query_start_loc,
+                                                  cache_indices, has_initial_state, scale,
+                                                  qk_l2norm, a_log, dt_bias, pad_slot_id, out,
+                                                  workspace, err_count)
+    _call("gdr_fwd", args, dev, stream, scratch)
+    return out
 
 
 def prepare_gdr_fwd(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
                     has_initial_state=None, scale=None, qk_l2norm=True, a_log=None, dt_bias=None,
                     pad_slot_id=PAD_SLOT_ID, out=None, workspace=None, err_count=None) -> Launch:
     """Validate and marshal a gdr_fwd call once; returns a reusable Launch."""
-    args, out = _gdr_args(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slot_id,
-                          out, has_row=False)
-    qsl = _index_vector(query_start_loc, "query_start_loc", torch.int32, 1)
-    batch, total = qsl.numel() - 1, v.shape[0]
-    ci = _index_vector(cache_indices, "cache_indices", torch.int32, batch)
+    _, args, out, scratch, keep = _marshal_gdr_fwd(q, k, v, g, beta, state, query_start_loc,
+                                                   cache_indices, has_initial_state, scale,
+                                                   qk_l2norm, a_log, dt_bias, pad_slot_id, out,
+                                                   workspace, err_count)
+    return ScratchLaunch("gdr_fwd", args, out, keep, scratch)
+
+
+def _marshal_gdr_fwd(q, k, v, g, beta, state, query_start_loc, cache_indices, has_initial_state,
+                     scale, qk_l2norm, a_log, dt_bias, pad_slot_id, out, workspace, err_count):
+    dev, packed, out, sizes = _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias,
+                                        pad_slot_id, out, "tokens")
+    qsl = _vector(dev, query_start_loc, "query_start_loc", _I32, 1)
+    if qsl is None:
+        raise TypeError("query_start_loc must be a CUDA tensor")
+    batch, total = query_start_loc.shape[0] - 1, v.shape[0]
+    ci = _vector(dev, cache_indices, "cache_indices", _I32, batch)
     hi = has_initial_state
     if hi is not None:
-        if hi.dtype not in (torch.bool, torch.uint8):
+        if hi.dtype not in (torch.bool, _U8):
             raise TypeError("has_initial_state must be bool or uint8")
-        hi = _index_vector(hi, "has_initial_state", hi.dtype, batch)
-    _need_cuda(err_count, "err_count", torch.int32)
-    size = _lib.load().gdr_fwd_workspace(total, batch, args.num_k_heads, args.num_v_heads,
-                                         args.dim_k, args.dim_v)
-    scratch = _workspace(workspace, size, v.device)
-    call = (ctypes.byref(args), _ptr(qsl), batch, _ptr(ci), _ptr(hi), total, _ptr(scratch),
-            scratch.numel(), _ptr(err_count))
-    return ScratchLaunch("gdr_fwd", call, out, (args, q, k, v, g, beta, state, qsl, ci, hi, a_log,
-                                                dt_bias, out, scratch, err_count), scratch)
+        hi = _vector(dev, hi, "has_initial_state", hi.dtype, batch)
+    size = _lib.load().gdr_fwd_workspace(total, batch, *sizes)
+    scratch = _workspace(dev, workspace, size, v)
+    args = (packed, qsl, batch, ci, hi, total, scratch.data_ptr(), scratch.shape[0],
+            _err(dev, err_count))
+    keep = (q, k, v, g, beta, state, query_start_loc, cache_indices, has_initial_state, a_log,
+            dt_bias, out, scratch, err_count)
+    return dev, args, out, scratch, keep
 
 
 def gdr_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
@@ -162,36 +240,45 @@ def gdr_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     starts from line [b, num_accepted_tokens[b] - 1].  Returns out with v's
     rank.
     """
-    return prepare_gdr_update(q, k, v, g, beta, state, state_indices, num_accepted_tokens,
-                              output_state_indices, scale, qk_l2norm, a_log, dt_bias, pad_slot_id,
-                              out, err_count)(stream)
+    dev, args, out, _ = _marshal_gdr_update(q, k, v, g, beta, state, state_indices,
+                                            num_accepted_tokens, output_state_indices, scale,
+                                            qk_l2norm, a_log, dt_bias, pad_slot_id, out, err_count)
+    _call("gdr_update", args, dev, stream)
+    return out
 
 
 def prepare_gdr_update(q, k, v, g, beta, state, state_indices=None, num_accepted_tokens=None,
                        output_state_indices=None, scale=None, qk_l2norm=True, a_log=None,
                        dt_bias=None, pad_slot_id=PAD_SLOT_ID, out=None, err_count=None) -> Launch:
     """Validate and marshal a gdr_update call once; returns a reusable Launch."""
-    squeeze = v.dim() == 3
-    if squeeze:
-        q, k, v, g, beta = (t.unsqueeze(1) for t in (q, k, v, g, beta))
-        out = out.unsqueeze(1) if out is not None else None
+    _, args, out, keep = _marshal_gdr_update(q, k, v, g, beta, state, state_indices,
+                                             num_accepted_tokens, output_state_indices, scale,
+                                             qk_l2norm, a_log, dt_bias, pad_slot_id, out,
+                                             err_count)
+    return Launch("gdr_update", args, out, keep)
+
+
+def _marshal_gdr_update(q, k, v, g, beta, state, state_indices, num_accepted_tokens,
+                        output_state_indices, scale, qk_l2norm, a_log, dt_bias, pad_slot_id, out,
+                        err_count):
     if state is None:
         raise TypeError("state must be a CUDA tensor")
-    args, out = _gdr_args(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slot_id,
-                          out, has_row=True)
-    batch, seqlen = v.shape[:2]
-    idx = _index_vector(state_indices, "state_indices", torch.int32, batch)
-    nacc = _index_vector(num_accepted_tokens, "num_accepted_tokens", torch.int32, batch)
-    oidx = output_state_indices
-    _need_cuda(oidx, "output_state_indices", torch.int32)
-    if oidx is not None and (oidx.dim() != 2 or oidx.shape[0] != batch):
-        raise ValueError("output_state_indices must be (batch, steps)")
-    _need_cuda(err_count, "err_count", torch.int32)
-    ost = oidx.stride() if oidx is not None else (0, 0)
-    call = (ctypes.byref(args), _ptr(idx), _ptr(nacc), _ptr(oidx), *ost,
-            oidx.shape[1] if oidx is not None else 0, batch, seqlen, _ptr(err_count))
-    return Launch("gdr_update", call, out.squeeze(1) if squeeze else out,
-                  (args, q, k, v, g, beta, state, idx, nacc, oidx, a_log, dt_bias, out, err_count))
+    rows = v.dim() == 3
+    dev, packed, out, _ = _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias,
+                                    pad_slot_id, out, "rows" if rows else "steps")
+    batch, seqlen = v.shape[0], 1 if rows else v.shape[1]
+    oidx, ost, steps = output_state_indices, (0, 0), 0
+    if oidx is not None:
+        _need(dev, oidx, "output_state_indices", _I32)
+        if oidx.dim() != 2 or oidx.shape[0] != batch:
+            raise ValueError("output_state_indices must be (batch, steps)")
+        oidx, ost, steps = oidx.data_ptr(), oidx.stride(), oidx.shape[1]
+    args = (packed, _vector(dev, state_indices, "state_indices", _I32, batch),
+            _vector(dev, num_accepted_tokens, "num_accepted_tokens", _I32, batch), oidx, *ost,
+            steps, batch, seqlen, _err(dev, err_count))
+    keep = (q, k, v, g, beta, state, state_indices, num_accepted_tokens, output_state_indices,
+            a_log, dt_bias, out, err_count)
+    return dev, args, out, keep
 
 
 def gated_rms_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -201,44 +288,52 @@ def gated_rms_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, ep
     or norm(x act(gate)) weight with norm_before_gate=False.  x, gate
     (tokens, heads, dim) or (tokens, dim) bf16; activation "silu", "sigmoid"
     or None.  Returns out."""
-    return prepare_gated_rms_norm(x, gate, weight, eps, activation, norm_before_gate, out)(stream)
+    dev, args, out, _ = _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out)
+    _call("gated_rms_norm", args, dev, stream)
+    return out
 
 
 def prepare_gated_rms_norm(x, gate, weight, eps=1e-6, activation="silu", norm_before_gate=True,
                            out=None) -> Launch:
     """Validate and marshal a gated_rms_norm call once; returns a reusable Launch."""
-    _need_cuda(x, "x", torch.bfloat16)
-    _need_cuda(gate, "gate", torch.bfloat16)
+    _, args, out, keep = _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out)
+    return Launch("gated_rms_norm", args, out, keep)
+
+
+def _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out):
+    dev = _first(x, "x", _BF16)
+    _need(dev, gate, "gate", _BF16)
     if activation not in _ACTIVATIONS:
         raise ValueError(f"unsupported activation: {activation!r}")
-    if x.dim() not in (2, 3) or gate.shape != x.shape:
+    shape = x.shape
+    if len(shape) not in (2, 3) or gate.shape != shape:
         raise ValueError("x and gate must be (tokens, heads, dim) or (tokens, dim), one shape")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(shape, dtype=_BF16, device=x.device)
     else:
-        _need_cuda(out, "out", torch.bfloat16)
-        if out.shape != x.shape:
+        _need(dev, out, "out", _BF16)
+        if out.shape != shape:
             raise ValueError("out must have x's shape")
-    weight = _norm_weight(weight, "weight", x.shape[-1])
-    tokens, heads, dim = x.shape if x.dim() == 3 else (x.shape[0], 1, x.shape[1])
+    if weight is None:
+        raise TypeError("weight must be a CUDA tensor")
+    w = _norm_weight(dev, weight, "weight", shape[-1])
+    xs, gs, os_ = x.stride(), gate.stride(), out.stride()
+    if len(shape) == 2:
+        xs, gs, os_ = ((s[0], 0, s[1]) for s in (xs, gs, os_))
+        shape = (shape[0], 1, shape[1])
+    args = (_VIEW.pack(x.data_ptr(), 0, *xs), _VIEW.pack(gate.data_ptr(), 0, *gs), w,
+            _VIEW.pack(out.data_ptr(), 0, *os_), *shape, eps, _ACTIVATIONS[activation],
+            1 if norm_before_gate else 0)
+    return dev, args, out, (x, gate, weight, out)
 
-    def view(t):
-        st = t.stride()
-        return _lib.HeadsView(t.data_ptr(), 0, st[0], st[1] if t.dim() == 3 else 0, st[-1])
 
-    vx, vg, vo = view(x), view(gate), view(out)
-    call = (ctypes.byref(vx), ctypes.byref(vg), _ptr(weight), ctypes.byref(vo), tokens, heads, dim,
-            float(eps), _ACTIVATIONS[activation], int(bool(norm_before_gate)))
-    return Launch("gated_rms_norm", call, out, (vx, vg, vo, x, gate, weight, out))
-
-
-def _norm_weight(w: Optional[torch.Tensor], name: str, dim: int):
+def _norm_weight(dev: int, w: Optional[torch.Tensor], name: str, dim: int):
     if w is None:
         return None
-    _need_cuda(w, name, torch.bfloat16)
+    _need(dev, w, name, _BF16)
     if w.shape != (dim,) or (dim > 1 and w.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {dim}")
-    return w
+    return w.data_ptr()
 
 
 def residual_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
@@ -254,44 +349,54 @@ def residual_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Ten
     x (tokens, dim) bf16; residual bf16 or fp32; gate (dim,) or (tokens, dim).
     residual_out may be residual and out may be x (in place).
     """
-    return prepare_residual_rms_norm(x, residual, weight, post_weight, gate, scale, eps,
-                                     weight_offset, out, residual_out)(stream)
+    dev, args, result, _ = _marshal_residual(x, residual, weight, post_weight, gate, scale, eps,
+                                             weight_offset, out, residual_out)
+    _call("residual_rms_norm", args, dev, stream)
+    return result
 
 
 def prepare_residual_rms_norm(x, residual, weight, post_weight=None, gate=None, scale=1.0,
                               eps=1e-6, weight_offset=0.0, out=None, residual_out=None) -> Launch:
     """Validate and marshal a residual_rms_norm call once; returns a reusable Launch."""
-    _need_cuda(x, "x", torch.bfloat16)
-    _need_cuda(residual, "residual")
-    if residual.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"residual must be bfloat16 or float32, got {residual.dtype}")
-    if x.dim() != 2 or residual.shape != x.shape:
+    _, args, result, keep = _marshal_residual(x, residual, weight, post_weight, gate, scale, eps,
+                                              weight_offset, out, residual_out)
+    return Launch("residual_rms_norm", args, result, keep)
+
+
+def _marshal_residual(x, residual, weight, post_weight, gate, scale, eps, weight_offset, out,
+                      residual_out):
+    dev = _first(x, "x", _BF16)
+    _need(dev, residual, "residual", _BF16, _F32)
+    shape, kind = x.shape, residual.dtype
+    if len(shape) != 2 or residual.shape != shape:
         raise ValueError("x and residual must be (tokens, dim), one shape")
-    tokens, dim = x.shape
+    tokens, dim = shape
     if weight is None:
         raise TypeError("weight must be a CUDA tensor")
-    weight = _norm_weight(weight, "weight", dim)
-    post_weight = _norm_weight(post_weight, "post_weight", dim)
-    gst = (0, 0)
+    w, pw = (_norm_weight(dev, weight, "weight", dim),
+             _norm_weight(dev, post_weight, "post_weight", dim))
+    gp, gs = None, (0, 0)
     if gate is not None:
-        _need_cuda(gate, "gate", torch.bfloat16)
+        _need(dev, gate, "gate", _BF16)
         if gate.shape not in ((dim,), (tokens, dim)):
             raise ValueError("gate must be (dim,) or (tokens, dim)")
-        gst = (0, gate.stride(0)) if gate.dim() == 1 else gate.stride()
+        gp, gs = gate.data_ptr(), gate.stride() if gate.dim() == 2 else (0, gate.stride(0))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(shape, dtype=_BF16, device=x.device)
+    else:
+        _need(dev, out, "out", _BF16)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
-    _need_cuda(out, "out", torch.bfloat16)
-    _need_cuda(residual_out, "residual_out", residual.dtype)
-    if out.shape != x.shape or residual_out.shape != x.shape:
+        residual_out = torch.empty(shape, dtype=kind, device=x.device)
+    else:
+        _need(dev, residual_out, "residual_out", kind)
+    if out.shape != shape or residual_out.shape != shape:
         raise ValueError("out and residual_out must have x's shape")
-    call = (_ptr(x), *x.stride(), _ptr(residual), *residual.stride(),
-            int(residual.dtype == torch.float32), _ptr(weight), _ptr(post_weight), _ptr(gate), *gst,
-            _ptr(out), *out.stride(), _ptr(residual_out), *residual_out.stride(), tokens, dim,
-            float(scale), float(eps), float(weight_offset))
-    return Launch("residual_rms_norm", call, (out, residual_out),
-                  (x, residual, weight, post_weight, gate, out, residual_out))
+    args = (x.data_ptr(), *x.stride(), residual.data_ptr(), *residual.stride(),
+            1 if kind is _F32 else 0, w, pw, gp, *gs, out.data_ptr(), *out.stride(),
+            residual_out.data_ptr(), *residual_out.stride(), tokens, dim, scale, eps,
+            weight_offset)
+    return (dev, args, (out, residual_out),
+            (x, residual, weight, post_weight, gate, out, residual_out))
 
 
 def spec_verify(target_logits: torch.Tensor, draft_tokens: torch.Tensor, uniform: torch.Tensor,
@@ -314,56 +419,68 @@ def spec_verify(target_logits: torch.Tensor, draft_tokens: torch.Tensor, uniform
     and int32 (batch) kept drafts + 1 -- the num_accepted_tokens of the next
     ccv_update_spec and gdr_update.
     """
-    return prepare_spec_verify(target_logits, draft_tokens, uniform, noise, draft_probs, num_drafts,
-                               temperature, out_tokens, num_accepted, workspace, err_count)(stream)
+    dev, args, result, scratch, _ = _marshal_verify(target_logits, draft_tokens, uniform, noise,
+                                                    draft_probs, num_drafts, temperature,
+                                                    out_tokens, num_accepted, workspace, err_count)
+    _call("spec_verify", args, dev, stream, scratch)
+    return result
 
 
 def prepare_spec_verify(target_logits, draft_tokens, uniform, noise, draft_probs=None,
                         num_drafts=None, temperature=None, out_tokens=None, num_accepted=None,
                         workspace=None, err_count=None) -> Launch:
     """Validate and marshal a spec_verify call once; returns a reusable Launch."""
-    _need_cuda(target_logits, "target_logits")
-    if target_logits.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"target_logits must be bfloat16 or float32, got {target_logits.dtype}")
-    _need_cuda(draft_tokens, "draft_tokens", torch.int32)
-    _need_cuda(uniform, "uniform", torch.float32)
-    _need_cuda(noise, "noise", torch.float32)
-    _need_cuda(draft_probs, "draft_probs", torch.float32)
+    _, args, result, scratch, keep = _marshal_verify(target_logits, draft_tokens, uniform, noise,
+                                                     draft_probs, num_drafts, temperature,
+                                                     out_tokens, num_accepted, workspace,
+                                                     err_count)
+    return ScratchLaunch("spec_verify", args, result, keep, scratch)
+
+
+def _marshal_verify(target_logits, draft_tokens, uniform, noise, draft_probs, num_drafts,
+                    temperature, out_tokens, num_accepted, workspace, err_count):
+    dev = _first(target_logits, "target_logits", _BF16, _F32)
+    _need(dev, draft_tokens, "draft_tokens", _I32)
+    _need(dev, uniform, "uniform", _F32)
+    _need(dev, noise, "noise", _F32)
     if target_logits.dim() != 3 or draft_tokens.dim() != 2:
         raise ValueError("target_logits must be (batch, drafts + 1, vocab), draft_tokens "
                          "(batch, drafts)")
-    (batch, drafts), vocab = draft_tokens.shape, target_logits.shape[2]
-    if target_logits.shape[:2] != (batch, drafts + 1):
+    batch, drafts = draft_tokens.shape
+    vocab = target_logits.shape[2]
+    if target_logits.shape != (batch, drafts + 1, vocab):
         raise ValueError("target_logits must have one position more than there are drafts")
-    if uniform.shape != draft_tokens.shape:
+    if uniform.shape != (batch, drafts):
         raise ValueError("uniform must have draft_tokens' shape")
     if noise.shape != (batch, vocab):
         raise ValueError("noise must be (batch, vocab)")
-    if draft_probs is not None and draft_probs.shape != (batch, drafts, vocab):
-        raise ValueError("draft_probs must be (batch, drafts, vocab)")
-    for t, name in ((target_logits, "target_logits"), (noise, "noise"),
-                    (draft_probs, "draft_probs")):
-        if t is not None and vocab > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name} must have stride 1 along vocab")
-    nd = _index_vector(num_drafts, "num_drafts", torch.int32, batch)
-    temp = _index_vector(temperature, "temperature", torch.float32, batch)
+    ts, ns = target_logits.stride(), noise.stride()
+    pp, ps = None, (0, 0, 1)
+    if draft_probs is not None:
+        _need(dev, draft_probs, "draft_probs", _F32)
+        if draft_probs.shape != (batch, drafts, vocab):
+            raise ValueError("draft_probs must be (batch, drafts, vocab)")
+        pp, ps = draft_probs.data_ptr(), draft_probs.stride()
+    if vocab > 1 and not ts[2] == ns[1] == ps[2] == 1:
+        raise ValueError("target_logits, noise and draft_probs must have stride 1 along vocab")
+    nd = _vector(dev, num_drafts, "num_drafts", _I32, batch)
+    temp = _vector(dev, temperature, "temperature", _F32, batch)
     if out_tokens is None:
-        out_tokens = torch.empty(batch, drafts + 1, dtype=torch.int32, device=draft_tokens.device)
+        out_tokens = torch.empty((batch, drafts + 1), dtype=_I32, device=noise.device)
+    else:
+        _need(dev, out_tokens, "out_tokens", _I32)
+        if out_tokens.shape != (batch, drafts + 1) or not out_tokens.is_contiguous():
+            raise ValueError("out_tokens must be a contiguous (batch, drafts + 1)")
     if num_accepted is None:
-        num_accepted = torch.empty(batch, dtype=torch.int32, device=draft_tokens.device)
-    _need_cuda(out_tokens, "out_tokens", torch.int32)
-    if out_tokens.shape != (batch, drafts + 1) or not out_tokens.is_contiguous():
-        raise ValueError("out_tokens must be a contiguous (batch, drafts + 1)")
-    _index_vector(num_accepted, "num_accepted", torch.int32, batch)
-    _need_cuda(err_count, "err_count", torch.int32)
+        num_accepted = torch.empty(batch, dtype=_I32, device=noise.device)
+    count = _vector(dev, num_accepted, "num_accepted", _I32, batch)
     size = _lib.load().spec_verify_workspace(batch, drafts, vocab)
-    scratch = _workspace(workspace, size, draft_tokens.device)
-    pst = draft_probs.stride()[:2] if draft_probs is not None else (0, 0)
-    call = (_ptr(target_logits), int(target_logits.dtype == torch.float32),
-            *target_logits.stride()[:2], _ptr(draft_tokens), *draft_tokens.stride(),
-            _ptr(draft_probs), *pst, _ptr(nd), _ptr(temp), _ptr(uniform), *uniform.stride(),
-            _ptr(noise), noise.stride(0), _ptr(out_tokens), _ptr(num_accepted), batch, drafts,
-            vocab, _ptr(scratch), scratch.numel(), _ptr(err_count))
-    return ScratchLaunch("spec_verify", call, (out_tokens, num_accepted),
-                         (target_logits, draft_tokens, uniform, noise, draft_probs, nd, temp,
-                          out_tokens, num_accepted, scratch, err_count), scratch)
+    scratch = _workspace(dev, workspace, size, noise)
+    args = (target_logits.data_ptr(), 1 if target_logits.dtype is _F32 else 0, ts[0], ts[1],
+            draft_tokens.data_ptr(), *draft_tokens.stride(), pp, ps[0], ps[1], nd, temp,
+            uniform.data_ptr(), *uniform.stride(), noise.data_ptr(), ns[0], out_tokens.data_ptr(),
+            count, batch, drafts, vocab, scratch.data_ptr(), scratch.shape[0],
+            _err(dev, err_count))
+    keep = (target_logits, draft_tokens, uniform, noise, draft_probs, num_drafts, temperature,
+            out_tokens, num_accepted, scratch, err_count)
+    return dev, args, (out_tokens, num_accepted), scratch, keep

@@ -174,7 +174,8 @@ int residual_rms_norm(const void *x, int64_t x_stride_tok, int64_t x_stride_dim,
  *               next token, then -1.
  * num_accepted  int32 [batch]: kept drafts + 1, what num_accepted_tokens of
  *               ccv_update_spec and gdr_update takes for the next step.
- * A draft token outside [0, vocab) is rejected and counted in err_count.
+ * A draft token outside [0, vocab) is rejected; the first one met is counted in
+ * err_count.
  * workspace     spec_verify_workspace(...) bytes, 16-byte aligned.
  */
 int spec_verify(const void *target_logits, int logits_fp32, int64_t t_stride_b, int64_t t_stride_pos,

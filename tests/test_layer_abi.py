@@ -29,6 +29,19 @@ def test_every_declared_function_is_exported(lib):
     assert names <= set(re.findall(r" T (\w+)$", out, flags=re.M))
 
 
+def test_packed_structures_match_the_header(lib):
+    """The binding packs the C structures itself: sizes and the order of the fields."""
+    from causal_depthwise_conv1d_fwd_gb300 import layer
+
+    assert layer._VIEW.size == ctypes.sizeof(_lib.HeadsView)
+    assert layer._GDR.size == ctypes.sizeof(_lib.GdrArgs)
+    numbers = list(range(1, 33)) + [0.5 if i == 5 else 40 + i for i in range(8)]
+    got = _lib.GdrArgs.from_buffer_copy(layer._GDR.pack(*numbers))
+    assert (got.q.data, got.k.stride_row, got.v.stride_tok, got.out.stride_dim) == (1, 7, 13, 20)
+    assert (got.g, got.beta, got.gate_stride_head, got.a_log, got.state, got.s_stride_k) == (21, 22, 25, 26, 28, 32)
+    assert (got.num_lines, got.dim_v, got.scale, got.qk_l2norm, got.pad_slot_id) == (40, 44, 0.5, 46, 47)
+
+
 def test_status_strings(lib):
     for code in (DIM, HEADS, WORK):
         assert "unknown" not in _lib.status_string(code)
