@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 
 #include "ccv_common.cuh"
 #include "ccv_math2.cuh"
@@ -22,15 +23,16 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
 __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
+// Whether the barrier's phase `parity` is complete.  kSleep: the hardware may hold the thread for a while if it is not.
+template <bool kSleep>
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+    if constexpr (kSleep)
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return done != 0;
 }
 
@@ -43,12 +45,13 @@ constexpr uint64_t kMaxWaitNs = 2000000000ull;  // far beyond any wait of a heal
 
 // Waits until the barrier's phase `parity` is complete.  False when two seconds ran out or another thread of the block
 // gave up (`*abort` set): the caller then leaves its loop and goes to the kernel's common end.
+template <bool kSleep = true>
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_test<kSleep>(bar, parity)) return true;
     const uint64_t start = timer_ns();
     for (int i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 15) == 0) {
+        if (mbar_test<kSleep>(bar, parity)) return true;
+        if ((i & 63) == 0) {
             if (*abort) return false;
             if (timer_ns() - start > kMaxWaitNs) {
                 *abort = 1;
@@ -58,8 +61,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 // The same for a whole warp, with one answer for all its lanes (tensor-memory accesses are warp-wide).
+template <bool kSleep = true>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+    return __all_sync(0xffffffffu, mbar_wait<kSleep>(bar, parity, abort));
 }
 
 // --------------------------------------------------------- bulk copies ----
@@ -69,6 +73,20 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
+}
+// One box of a tensor (coordinates innermost first) into swizzled shared memory, counted in bytes on `bar`.
+__device__ __forceinline__ void tensor_load(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+                 : "memory");
+}
+// Brings a contiguous range, or a tensor's box, into L2.
+__device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tensor_prefetch(const CUtensorMap *map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
 }
 // 16-byte asynchronous copy, or 16 zero bytes when `real` is false (src is not read then).
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool real) {
@@ -96,6 +114,12 @@ __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::
 
 // N consecutive columns of this thread's lane (lane base in the address' upper half).  Loads are asynchronous: the values
 // are there after tmem_wait_load(), which the caller places before their first use.
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(addr));
+}
 __device__ __forceinline__ void tmem_load(uint32_t addr, float (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
                  "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -112,6 +136,11 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&r)[32]) {
                    "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
                    "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
                  : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
@@ -165,54 +194,31 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t lane) {
         : "memory");
 }
 
-// ------------------------------------------------------- 8 x 8 transposes ----
-
-// Four 8 x 8 blocks of 16-bit values from shared memory, transposed: lane l gives the address of row l % 8 of block l / 8
-// (16-byte aligned) and receives in r[b] the pair (row 2 (l % 4), + 1) of column l / 4 of block b.
-__device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-// r[i] of lane j of every four lanes becomes r[j] of lane i.
-__device__ __forceinline__ void transpose_quad(uint32_t (&r)[4]) {
-    const int lane = threadIdx.x;
-#pragma unroll
-    for (int m = 1; m < 4; m <<= 1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if ((i & m) == 0) {
-                const bool up = (lane & m) != 0;
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? r[i] : r[i | m], m);
-                if (up) r[i] = got;
-                else r[i | m] = got;
-            }
-}
-
-// Two floats as pairs of bf16 parts, by truncation: each part takes the next 8 bits, so three hold a float exactly and two
-// hold 16 bits of it.  (Rounded parts would need conversions at half the rate of these.)
-__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
-    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-}
-__device__ __forceinline__ f32x2 below_upper(float a, float b) {  // what upper_halves leaves
-    return sub2(pack2(a, b), pack2(__uint_as_float(__float_as_uint(a) & 0xffff0000u), __uint_as_float(__float_as_uint(b) & 0xffff0000u)));
+// Two floats as pairs of bf16 parts: each part is what the parts before it leave, rounded to 8 bits, so two parts hold 16
+// bits of a float and three hold all 24.  The remainder is one mixed-precision FMA (exact) a value: unpacking the parts with
+// masks and shifts instead keeps the integer pipe, which has half the rate, busy for twice as long.
+__device__ __forceinline__ void take_part(float &a, float &b, uint32_t &part) {
+    part = pack_bf16x2(a, b);
+    asm("{\n\t.reg .b16 lo, hi, one;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "mov.b16 one, 0xbf80;\n\t"  // -1
+        "fma.rn.f32.bf16 %0, lo, one, %0;\n\t"
+        "fma.rn.f32.bf16 %1, hi, one, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(part));
 }
 __device__ __forceinline__ void split_bf16x2(f32x2 x, uint32_t &hi, uint32_t &mid) {
     float a, b;
     unpack2(x, a, b);
-    hi = upper_halves(a, b);
-    unpack2(below_upper(a, b), a, b);
-    mid = upper_halves(a, b);
+    take_part(a, b, hi);
+    mid = pack_bf16x2(a, b);
 }
 __device__ __forceinline__ void split_bf16x3(f32x2 x, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
     float a, b;
     unpack2(x, a, b);
-    hi = upper_halves(a, b);
-    unpack2(below_upper(a, b), a, b);
-    mid = upper_halves(a, b);
-    unpack2(below_upper(a, b), a, b);
-    lo = upper_halves(a, b);
+    take_part(a, b, hi);
+    take_part(a, b, mid);
+    lo = pack_bf16x2(a, b);
 }
 
 }  // namespace ccv

@@ -40,6 +40,13 @@ struct FwdArgs {
     int *err_count;
 };
 
+// Tensor maps (dim, head, token) of q, k and v with boxes of 64 values x 64 tokens; `use` is false where the tensors'
+// strides do not allow them.
+struct FwdMaps {
+    CUtensorMap q, k, v;
+    bool use;
+};
+
 // Chunk j of sequence i is in slot first_slot(i) + j.  floor(s / 64) + i leaves every sequence room for its
 // ceil(n / 64) chunks, needs no sum over the lengths, and total / 64 + batch slots in all.
 __device__ __forceinline__ int first_slot(int start, int i) { return (start >> 6) + i; }
@@ -428,42 +435,45 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
 
 // ----------------------------------------------------------------- chunks ----
 
-constexpr int kCompute = 256;                 // two warpgroups, each half of the columns of every row
-constexpr int kLoaders = 64;                  // two warps that load, beside one that stores and one that issues the MMAs
+constexpr int kCompute = 512;       // four warpgroups, each a quarter of the columns of every row
 constexpr int kChunkThreads = kCompute + 128;
+constexpr int kIssueWarp = 16, kStoreWarp = 17, kLoadWarp = 18;
+constexpr int kLoaders = 64;
 constexpr int kStages = 2;
-constexpr int kIssueWarp = 8, kStoreWarp = 9, kLoadWarp = 10;
-// Registers a thread: 384 threads launch with 168 each, 64512 in all; the compute warpgroups take 208 and the other 88.
-constexpr int kComputeRegs = 208, kOtherRegs = 88;
-static_assert(kCompute * kComputeRegs + 128 * kOtherRegs <= kChunkThreads * 168, "register split");
+// Registers a thread: 640 threads launch with 96 each, 61440 in all; the compute warpgroups take 104 and the other 64.
+constexpr int kComputeRegs = 104, kOtherRegs = 64;
+static_assert(kCompute * kComputeRegs + 128 * kOtherRegs <= kChunkThreads * 96, "register split");
 
-// Columns of tensor memory.  Operands in parts keep each warpgroup's share together, so that a thread overwrites only
-// columns that it alone has read.
+// Columns of tensor memory.  A thread overwrites only columns that it alone reads, or that a barrier says are free.
 enum : uint32_t {
-    kColS = 0,       // 192: S^T in 3 parts (a warpgroup: 32 columns each); then what the chunk adds to S^T
-    kColP = 192,     // 64: S^T k^T
+    kColS = 0,       // 192: S^T in 3 parts, and in the same columns what the chunk adds to S^T (see s_part)
+    kColP = 192,     // 64: S^T k^T, then d in 2 parts
     kColO = 256,     // 64: S^T q^T, then d P^T
-    kColR = 320,     // 96: R in 3 parts (a warpgroup: 16 columns each), then the decayed d in 3 parts
-    kColN = 416,     // 64: d, then d in 2 parts
+    kColR = 320,     // 96: R in 3 parts, then the decayed d in 3 parts
+    kColN = 416,     // 64: d
 };
-
-// V and the output cross shared memory as rows of 64 tokens (144 bytes apart, which spreads them over the banks): the
-// compute threads own a row each.  The loader warps turn them from and to rows of values.
-constexpr int kRowBytes = 144;
-constexpr int kRawBytes = 272;  // a token's 128 values on the way in
+// Warpgroup q holds 16 PANELS keys of every row of S.  They have 24 PANELS columns: 8 PANELS for each part (a column is two
+// bf16 values), or 16 PANELS for what is added to them.
+template <int PANELS>
+__device__ __forceinline__ constexpr uint32_t s_part(int q, int part) { return kColS + q * 24 * PANELS + part * 8 * PANELS; }
+// It also holds tokens 8 q .. + 7 and 32 + 8 q .. + 7 of every row of R and d, so that two warpgroups make up the 16 tokens of
+// an inner step of the tensor cores, and the steps of tokens 0 .. 31 can run while the others are prepared.
+__device__ __forceinline__ constexpr uint32_t r_part(int step, int part) { return kColR + step * 24 + part * 8; }
+__device__ __forceinline__ constexpr uint32_t d_part(int step, int part) { return kColP + step * 16 + part * 8; }
 
 template <int PANELS>
 struct Stage {
     static constexpr int kq = PANELS * 2 * kTile;  // per panel: 64 rows of K, 64 of Q
-    static constexpr int v = kq;
-    static constexpr int head = v + 128 * kRowBytes;
+    static constexpr int v = kq;                   // two swizzled tiles of 64 values
+    static constexpr int head = v + 2 * kTile;
     static constexpr int bytes = (head + kHeadBytes + 1023) / 1024 * 1024;
 };
 
 struct ChunkSmem {
     uint64_t full[kStages], empty[kStages];               // a stage is loaded; its chunk's MMAs, the last to use it, are done
-    uint64_t mma_p, mma_o, mma_n, mma_delta, mma_out;     // completed by the tensor cores
-    uint64_t have_s, have_read, have_r, have_vs, have_d;  // arrived on by the compute threads
+    uint64_t mma_p, mma_o, mma_n, mma_delta[2], mma_out;  // completed by the tensor cores
+    uint64_t have_s[2], have_r[2], have_vs[2];            // arrived on by the compute threads, by halves
+    uint64_t have_read, have_d;
     uint64_t out_full, out_free;                          // the output tile: written by them, stored by one warp
     uint64_t drain;
     uint32_t tmem;
@@ -472,13 +482,13 @@ struct ChunkSmem {
 
 // V: the state allows 16-byte vectors.  VIO: rows of q, k, v and out do.
 template <int PANELS, bool V, bool VIO>
-__global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __grid_constant__ FwdArgs p, int slices) {
+__global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __grid_constant__ FwdArgs p,
+                                                                     const __grid_constant__ FwdMaps maps, int slices) {
     using St = Stage<PANELS>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *out_tile = base + kStages * St::bytes;
-    uint8_t *raw_v = out_tile + 128 * kRowBytes;
-    ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(raw_v + C * kRawBytes);
+    uint16_t *out_tile = reinterpret_cast<uint16_t *>(base + kStages * St::bytes);  // 64 rows of 128 values
+    ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(base + kStages * St::bytes + 2 * kTile);
     const ccv_gdr_args &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFullMask, tid >> 5, 0);
@@ -506,9 +516,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     if (tid == 0) {
         sm.abort = 0;
         for (uint64_t &b : sm.full) mbar_init(&b, kLoaders + 1);
-        for (uint64_t &b : sm.empty) mbar_init(&b, 1);
-        for (uint64_t *b : {&sm.mma_p, &sm.mma_o, &sm.mma_n, &sm.mma_delta, &sm.mma_out, &sm.drain}) mbar_init(b, 1);
-        for (uint64_t *b : {&sm.have_s, &sm.have_read, &sm.have_r, &sm.have_vs, &sm.have_d, &sm.out_full}) mbar_init(b, kCompute);
+        for (uint64_t *b : {&sm.empty[0], &sm.empty[1], &sm.mma_p, &sm.mma_o, &sm.mma_n, &sm.mma_delta[0], &sm.mma_delta[1], &sm.mma_out,
+                            &sm.drain})
+            mbar_init(b, 1);
+        for (uint64_t *b : {&sm.have_s[0], &sm.have_s[1]}) mbar_init(b, kCompute / 2);
+        for (uint64_t *b : {&sm.have_r[0], &sm.have_r[1], &sm.have_vs[0], &sm.have_vs[1], &sm.have_read, &sm.have_d, &sm.out_full})
+            mbar_init(b, kCompute);
         mbar_init(&sm.out_free, 32);
         mbar_init_fence();
     }
@@ -523,74 +536,95 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         if (warp == kIssueWarp) {
             const uint32_t el = elect_lane();
             const uint32_t smem0 = __shfl_sync(kFullMask, smem_u32(base), 0);
-            auto s_col = [](int ks, int part) {
-                return PANELS == 2 ? (ks / 4) * 96 + (ks % 4) * 8 + part * 32 : (ks / 2) * 48 + (ks % 2) * 8 + part * 16;
+            // keys of warpgroup q from step j on: their place in the rows of K and Q
+            auto key_at = [](int q, int j) {
+                const int key = q * 16 * PANELS + j * 16;
+                return (key / 64) * 2 * kTile + (key % 64) * 2;
             };
             int c = 0;
             for (; c < chunks; ++c) {
                 const uint32_t par = c & 1;
                 const uint32_t kq = smem0 + (c % kStages) * St::bytes;
                 const uint32_t head = kq + St::head;
-                if (!mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort)) break;
-                if (!mbar_wait_warp(&sm.have_s, par, &sm.abort)) break;
-                tc_fence_after();
+                if (!mbar_wait_warp<false>(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort)) break;
+                if (c > 0 && !mbar_wait_warp<false>(&sm.mma_out, par ^ 1, &sm.abort)) break;  // it read d where P goes
+                bool ok = true;
                 // S^T k^T, three parts of S; the keys are exact
 #pragma unroll
-                for (int part = 0; part < 3; ++part)
+                for (int g = 0; g < 2; ++g) {
+                    if (!(ok = mbar_wait_warp<false>(&sm.have_s[g], par, &sm.abort))) break;
+                    tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < PANELS * 4; ++ks)
-                        mma_ts(tmem + kColP, tmem + kColS + s_col(ks, part),
-                               smem_desc(kq + (ks / 4) * 2 * kTile + (ks % 4) * 32, 0, 1024), mma_desc(128, C, false), part + ks > 0, el);
+                    for (int part = 0; part < 3; ++part)
+#pragma unroll
+                        for (int q = 2 * g; q < 2 * g + 2; ++q)
+#pragma unroll
+                            for (int j = 0; j < PANELS; ++j)
+                                mma_ts(tmem + kColP, tmem + s_part<PANELS>(q, part) + j * 8, smem_desc(kq + key_at(q, j), 0, 1024),
+                                       mma_desc(128, C, false), part + q + j > 0, el);
+                }
+                if (!ok) break;
                 mma_commit(&sm.mma_p, el);
+                // d^T = R^T T^T: the six products of parts above 2^-24, for tokens 0 .. 31 of the sum, then the others
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = mbar_wait_warp<false>(&sm.have_r[half], par, &sm.abort))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int sum = 0; sum < 3; ++sum)
+#pragma unroll
+                        for (int part = 0; part <= sum; ++part)
+#pragma unroll
+                            for (int ks = 2 * half; ks < 2 * half + 2; ++ks)
+                                mma_ts(tmem + kColN, tmem + r_part(ks, part), smem_desc(head + kT + (sum - part) * kTile + ks * 32, 0, 1024),
+                                       mma_desc(128, C, false), sum + part + ks > 0, el);
+                }
+                if (!ok) break;
+                mma_commit(&sm.mma_n, el);
                 // S^T q^T, once the previous chunk's output has left these columns
-                if (!mbar_wait_warp(&sm.have_read, par, &sm.abort)) break;
+                if (!mbar_wait_warp<false>(&sm.have_read, par, &sm.abort)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int ks = 0; ks < PANELS * 4; ++ks)
-                        mma_ts(tmem + kColO, tmem + kColS + s_col(ks, part),
-                               smem_desc(kq + (ks / 4) * 2 * kTile + kTile + (ks % 4) * 32, 0, 1024), mma_desc(128, C, false),
-                               part + ks > 0, el);
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int j = 0; j < PANELS; ++j)
+                            mma_ts(tmem + kColO, tmem + s_part<PANELS>(q, part) + j * 8, smem_desc(kq + kTile + key_at(q, j), 0, 1024),
+                                   mma_desc(128, C, false), part + q + j > 0, el);
                 mma_commit(&sm.mma_o, el);
-                if (!mbar_wait_warp(&sm.have_r, par, &sm.abort)) break;
+                if (!mbar_wait_warp<false>(&sm.have_vs[0], par, &sm.abort)) break;
+                if (!mbar_wait_warp<false>(&sm.mma_o, par, &sm.abort)) break;  // S is about to be overwritten
+                // what the chunk adds to S^T: tokens are the inner axis, so the keys are read MN-major; each warpgroup's keys
+                // into its own columns
+                auto add = [&](int g, int half) {
+#pragma unroll
+                    for (int q = 2 * g; q < 2 * g + 2; ++q)
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+#pragma unroll
+                            for (int ks = 2 * half; ks < 2 * half + 2; ++ks)
+                                mma_ts(tmem + s_part<PANELS>(q, 0), tmem + r_part(ks, part), smem_desc(kq + key_at(q, 0) + ks * 2048, 0, 1024),
+                                       mma_desc(128, 16 * PANELS, true), part + ks > 0, el);
+                };
                 tc_fence_after();
-                // d^T = R^T T^T: the six products of parts above 2^-24, largest first
-#pragma unroll
-                for (int sum = 0; sum < 3; ++sum)
-#pragma unroll
-                    for (int part = 0; part <= sum; ++part)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(tmem + kColN, tmem + kColR + (ks / 2) * 48 + (ks % 2) * 8 + part * 16,
-                                   smem_desc(head + kT + (sum - part) * kTile + ks * 32, 0, 1024), mma_desc(128, C, false),
-                                   sum + part + ks > 0, el);
-                mma_commit(&sm.mma_n, el);
-                if (!mbar_wait_warp(&sm.have_vs, par, &sm.abort)) break;
-                if (!mbar_wait_warp(&sm.mma_o, par, &sm.abort)) break;  // S is about to be overwritten
+                add(0, 0);
+                add(1, 0);
+                if (!mbar_wait_warp<false>(&sm.have_vs[1], par, &sm.abort)) break;
                 tc_fence_after();
-                // what the chunk adds to S^T: tokens are the inner axis, so the keys are read MN-major; half of the keys a
-                // time, each half into the columns of the warpgroup that holds them
-#pragma unroll
-                for (int w = 0; w < 2; ++w)
-#pragma unroll
-                    for (int part = 0; part < 3; ++part)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(tmem + kColS + w * 48 * PANELS, tmem + kColR + (ks / 2) * 48 + (ks % 2) * 8 + part * 16,
-                                   smem_desc(kq + (PANELS == 2 ? w * 2 * kTile : w * 64) + ks * 2048, 0, 1024),
-                                   mma_desc(128, 32 * PANELS, true), part + ks > 0, el);
-                mma_commit(&sm.mma_delta, el);
-                if (!mbar_wait_warp(&sm.have_d, par, &sm.abort)) break;
+                add(0, 1);
+                mma_commit(&sm.mma_delta[0], el);
+                add(1, 1);
+                mma_commit(&sm.mma_delta[1], el);
+                if (!mbar_wait_warp<false>(&sm.have_d, par, &sm.abort)) break;
                 tc_fence_after();
                 // d P^T: the three products of parts above 2^-16
 #pragma unroll
                 for (int term = 0; term < 3; ++term)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_ts(tmem + kColO, tmem + kColN + (ks / 2) * 32 + (ks % 2) * 8 + (term == 1 ? 16 : 0),
-                               smem_desc(head + kP + (term == 2 ? kTile : 0) + ks * 32, 0, 1024), mma_desc(128, C, false),
-                               term + ks > 0, el);
+                        mma_ts(tmem + kColO, tmem + d_part(ks, term == 1), smem_desc(head + kP + (term == 2 ? kTile : 0) + ks * 32, 0, 1024),
+                               mma_desc(128, C, false), term + ks > 0, el);
                 mma_commit(&sm.mma_out, el);
                 mma_commit(&sm.empty[c % kStages], el);
             }
@@ -606,82 +640,64 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             for (int c = 0; c < chunks; ++c) {
                 if (!mbar_wait_warp(&sm.out_full, c & 1, &sm.abort)) break;
                 const int t0 = s + c * C, n = min(C, e - t0);
-                if constexpr (VIO) {
-                    // tokens 8 g .. + 7, values 32 m .. + 31
-#pragma unroll 2
-                    for (int g = 0; g < 8; ++g) {
-                        uint32_t r[4][4];
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) load_transposed(smem_u32(out_tile) + (m * 32 + lane) * kRowBytes + g * 16, r[m]);
-                        const int row = g * 8 + (lane >> 2);
-                        uint16_t *dst = out + (t0 + row) * a.out.stride_tok + (lane & 3) * 8;
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            transpose_quad(r[m]);
-                            if (row < n && m * 32 + (lane & 3) * 8 < width)
-                                *reinterpret_cast<uint4 *>(dst + m * 32) = make_uint4(r[m][0], r[m][1], r[m][2], r[m][3]);
-                        }
+                if constexpr (VIO) {  // two rows a pass, 16 bytes a lane
+                    uint16_t *dst = out + (t0 + (lane >> 4)) * a.out.stride_tok + (lane & 15) * 8;
+                    const bool wide = (lane & 15) * 8 < width;
+#pragma unroll 8
+                    for (int r = lane >> 4; r < C; r += 2) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(out_tile + r * 128 + (lane & 15) * 8);
+                        if (wide && r < n) *reinterpret_cast<uint4 *>(dst) = x;
+                        dst += 2 * a.out.stride_tok;
                     }
                 } else {
                     for (int i = lane; i < n * 128; i += 32)
-                        if ((i & 127) < width)
-                            out[(t0 + (i >> 7)) * a.out.stride_tok + (i & 127) * a.out.stride_dim] =
-                                reinterpret_cast<const uint16_t *>(out_tile + (i & 127) * kRowBytes)[i >> 7];
+                        if ((i & 127) < width) out[(t0 + (i >> 7)) * a.out.stride_tok + (i & 127) * a.out.stride_dim] = out_tile[i];
                 }
                 mbar_arrive(&sm.out_free);
             }
         } else {
-            const int id = tid - kLoadWarp * 32, lw = warp - kLoadWarp;
-            auto sync_loaders = [] { asm volatile("bar.sync 1, %0;" ::"n"(kLoaders) : "memory"); };
+            const int id = tid - kLoadWarp * 32;
             const int width = min(128, a.dim_v - slice * 128);
-            const uint16_t *vsrc = static_cast<const uint16_t *>(a.v.data) + h * a.v.stride_head + slice * 128 * a.v.stride_dim;
+            ccv_heads_view vv = a.v;
+            vv.data = static_cast<const uint16_t *>(a.v.data) + slice * 128 * a.v.stride_dim;
+            const uint8_t *heads = p.heads + (static_cast<int64_t>(slot0) * a.num_v_heads + h) * kHeadBytes;
+            const int64_t heads_step = static_cast<int64_t>(a.num_v_heads) * kHeadBytes;
             int c = 0;
             for (; c < chunks; ++c) {
+                const int t0 = s + c * C, n = min(C, e - t0);
+                // Whole chunks come as tensor tiles; a sequence's last rows, which need zeros after them, piece by piece.
+                const bool whole = VIO && maps.use && n == C;
+                if (id == 0 && c + 1 < chunks) {  // the stage frees up late: let L2 have the next chunk's part by then
+                    bulk_prefetch(heads + (c + 1) * heads_step, kHeadBytes);
+                    if (VIO && maps.use) {
+                        for (int i = 0; i < 2; ++i) tensor_prefetch(&maps.v, slice * 128 + i * 64, h, t0 + C);
+                        for (int i = 0; i < PANELS; ++i) {
+                            tensor_prefetch(&maps.k, i * 64, hk, t0 + C);
+                            tensor_prefetch(&maps.q, i * 64, hk, t0 + C);
+                        }
+                    }
+                }
                 if (c >= kStages && !mbar_wait_warp(&sm.empty[c % kStages], (c / kStages - 1) & 1, &sm.abort)) break;
                 uint8_t *st = base + (c % kStages) * St::bytes;
                 uint64_t *bar = &sm.full[c % kStages];
-                const int t0 = s + c * C, n = min(C, e - t0);
                 if (id == 0) {
-                    mbar_expect_tx(bar, kHeadBytes);
-                    bulk_load(st + St::head, p.heads + (static_cast<int64_t>(slot0 + c) * a.num_v_heads + h) * kHeadBytes, kHeadBytes, bar);
+                    mbar_expect_tx(bar, kHeadBytes + (whole ? St::head : 0));
+                    if (whole) {
+                        for (int i = 0; i < PANELS; ++i) tensor_load(st + i * 2 * kTile, &maps.k, i * 64, hk, t0, bar);
+                        for (int i = 0; i < 2; ++i) tensor_load(st + St::v + i * kTile, &maps.v, slice * 128 + i * 64, h, t0, bar);
+                    }
+                    bulk_load(st + St::head, heads + c * heads_step, kHeadBytes, bar);
+                    if (whole)
+                        for (int i = 0; i < PANELS; ++i) tensor_load(st + i * 2 * kTile + kTile, &maps.q, i * 64, hk, t0, bar);
                 }
-                if constexpr (VIO) {
-                    const int piece = id & 15;
-                    const uint16_t *src = vsrc + (t0 + (id >> 4)) * a.v.stride_tok + piece * 8;
-                    const uint32_t to = smem_u32(raw_v + (id >> 4) * kRawBytes + piece * 16);
-#pragma unroll
-                    for (int i = 0; i < C / 4; ++i) {
-                        const bool real = (id >> 4) + 4 * i < n && piece * 8 < width;
-                        cp_async16_or_zero(to + i * 4 * kRawBytes, real ? src : vsrc, real);
-                        src += 4 * a.v.stride_tok;
-                    }
-                } else {
-                    const uint16_t *src = vsrc + t0 * a.v.stride_tok;
-                    for (int i = id; i < C * 128; i += kLoaders) {
-                        const int row = i >> 7, dv = i & 127;
-                        reinterpret_cast<uint16_t *>(st + St::v + dv * kRowBytes)[row] =
-                            row < n && dv < width ? src[row * a.v.stride_tok + dv * a.v.stride_dim] : uint16_t(0);
-                    }
-                }
-                cp_async_commit();
-                stage_rows<PANELS, VIO, kLoaders>(st, 2 * kTile, a.k, t0, hk, n, a.dim_k, id);
-                stage_rows<PANELS, VIO, kLoaders>(st + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, id);
-                cp_async_commit();
-                if constexpr (VIO) {
-                    cp_async_wait<1>();
-                    sync_loaders();
-#pragma unroll 4
-                    for (int g = lw; g < 32; g += kLoaders / 32) {  // values 8 (g / 2), tokens 32 (g % 2)
-                        uint32_t r[4];
-                        load_transposed(smem_u32(raw_v) + ((g & 1) * 32 + lane) * kRawBytes + (g >> 1) * 16, r);
-                        uint8_t *dst = st + St::v + ((g >> 1) * 8 + (lane >> 2)) * kRowBytes + (g & 1) * 64 + (lane & 3) * 4;
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) *reinterpret_cast<uint32_t *>(dst + m * 16) = r[m];
-                    }
+                if (!whole) {
+                    stage_rows<2, VIO, kLoaders>(st + St::v, kTile, vv, t0, h, n, width, id);
+                    stage_rows<PANELS, VIO, kLoaders>(st, 2 * kTile, a.k, t0, hk, n, a.dim_k, id);
+                    stage_rows<PANELS, VIO, kLoaders>(st + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, id);
+                    cp_async_commit();
                     cp_async_wait<0>();
-                    sync_loaders();  // raw_v is read: the next chunk may overwrite it
+                    fence_async_shared();
                 }
-                fence_async_shared();
                 mbar_arrive(bar);
             }
             if (c < chunks) {  // gave up: let the copies land before the shared memory goes
@@ -691,18 +707,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
-        constexpr int KH = 32 * PANELS;  // keys of the state a thread holds
-        const int wg = warp >> 2, d = (warp & 3) * 32 + lane, row = slice * 128 + d;
+        constexpr int KH = 16 * PANELS;  // keys of the state a thread holds
+        const int q = warp >> 2, d = (warp & 3) * 32 + lane, row = slice * 128 + d;
         const bool live = row < a.dim_v;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t col_s = lanes + kColS + wg * 48 * PANELS, col_r = lanes + kColR + wg * 48, col_n = lanes + kColN + wg * 32;
+        const uint32_t col_s = lanes + s_part<PANELS>(q, 0);
         const bool init = a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
         float *sp = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + row * a.s_stride_v : nullptr;
 
         f32x2 st[KH / 2];  // this thread's part of row d of S
 #pragma unroll
         for (int k = 0; k < KH; k += 4) {
-            const int kk = wg * KH + k;
+            const int kk = q * KH + k;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (init && live) {
                 if constexpr (V) {
@@ -718,30 +734,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             st[k / 2 + 1] = pack2(x.z, x.w);
         }
         auto stage = [&](int c) { return base + (c % kStages) * St::bytes; };
-        // S^T <- gamma S^T + what the chunk added, 16 keys a time
-        auto add_delta = [&](float gamma, int k0) {
-            float x[16];
-            tmem_load(col_s + k0, x);
-            tmem_wait_load();
+        // S^T <- gamma S^T + what the chunk added
+        auto add_delta = [&](float gamma) {
             const f32x2 g2 = pack2(gamma, gamma);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) st[k0 / 2 + k] = fma2(g2, st[k0 / 2 + k], pack2(x[2 * k], x[2 * k + 1]));
+            for (int k0 = 0; k0 < KH; k0 += 16) {
+                float x[16];
+                tmem_load(col_s + k0, x);
+                tmem_wait_load();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) st[k0 / 2 + k] = fma2(g2, st[k0 / 2 + k], pack2(x[2 * k], x[2 * k + 1]));
+            }
         };
         // d P^T of chunk c onto oi, into the output tile
-        f32x2 oi[16];
+        f32x2 oi[8];
         auto finish = [&](int c) {
-            float x[32];
-            tmem_load(lanes + kColO + wg * 32, x);
+            float x[2][8];
+            tmem_load(lanes + kColO + 8 * q, x[0]);
+            tmem_load(lanes + kColO + 32 + 8 * q, x[1]);
             tmem_wait_load();
             tc_fence_before();
             mbar_arrive(&sm.have_read);
-            if (c > 0 && !mbar_wait_warp(&sm.out_free, (c - 1) & 1, &sm.abort)) return false;
-            uint32_t w[16];
+            if (c > 0 && !mbar_wait_warp<false>(&sm.out_free, (c - 1) & 1, &sm.abort)) return false;
+            uint16_t *o = out_tile + 8 * q * 128 + d;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = f32x2_to_bf16x2(add2(oi[i], pack2(x[2 * i], x[2 * i + 1])));
-            uint4 *o = reinterpret_cast<uint4 *>(out_tile + d * kRowBytes + wg * 64);
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = f32x2_to_bf16x2(add2(oi[4 * half + i], pack2(x[half][2 * i], x[half][2 * i + 1])));
+                    o[(32 * half + 2 * i) * 128] = static_cast<uint16_t>(w);
+                    o[(32 * half + 2 * i + 1) * 128] = static_cast<uint16_t>(w >> 16);
+                }
             mbar_arrive(&sm.out_full);
             return true;
         };
@@ -750,31 +773,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         float gamma = 1.0f;
         for (int c = 0; c < chunks; ++c) {
             const uint32_t par = c & 1;
-            // b v of this thread's 32 tokens, while the tensor cores add up the last chunk
-            if (!(ok = mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
-            const float *f = reinterpret_cast<const float *>(stage(c) + St::head + kVec) + wg * 32;
-            auto vec2 = [&](int which, int i) { return *reinterpret_cast<const ulonglong2 *>(f + which * C + i); };
-            f32x2 vb[16];
-            {
-                const uint4 *v = reinterpret_cast<const uint4 *>(stage(c) + St::v + d * kRowBytes + wg * 64);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 x = v[i];
-                    const ulonglong2 b0 = vec2(kBeta, 8 * i), b1 = vec2(kBeta, 8 * i + 4);
-                    vb[4 * i] = mul2(pack2(bf16_lo(x.x), bf16_hi(x.x)), b0.x);
-                    vb[4 * i + 1] = mul2(pack2(bf16_lo(x.y), bf16_hi(x.y)), b0.y);
-                    vb[4 * i + 2] = mul2(pack2(bf16_lo(x.z), bf16_hi(x.z)), b1.x);
-                    vb[4 * i + 3] = mul2(pack2(bf16_lo(x.w), bf16_hi(x.w)), b1.y);
-                }
-            }
             if (c > 0) {
-                if (!(ok = mbar_wait_warp(&sm.mma_delta, par ^ 1, &sm.abort))) break;
+                if (!(ok = mbar_wait_warp<false>(&sm.mma_delta[q >> 1], par ^ 1, &sm.abort))) break;
                 tc_fence_after();
-            }
-            // All of S is read before any of it is overwritten by its parts (they are wider).
-            if (c > 0) {
-#pragma unroll
-                for (int k0 = 0; k0 < KH; k0 += 16) add_delta(gamma, k0);
+                add_delta(gamma);  // all of it is read before its parts, which are wider, overwrite it
             }
 #pragma unroll
             for (int k0 = 0; k0 < KH; k0 += 16) {
@@ -787,101 +789,117 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             }
             tmem_wait_store();
             tc_fence_before();
-            mbar_arrive(&sm.have_s);
+            mbar_arrive(&sm.have_s[q >> 1]);
 
-            if (c > 0) {  // the output of the chunk before
-                if (!(ok = mbar_wait_warp(&sm.mma_out, par ^ 1, &sm.abort))) break;
+            // b v of this thread's tokens
+            if (!(ok = mbar_wait_warp<false>(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
+            const float *f = reinterpret_cast<const float *>(stage(c) + St::head + kVec) + 8 * q;
+            auto vec2 = [&](int which, int half, int i) { return *reinterpret_cast<const f32x2 *>(f + which * C + 32 * half + 2 * i); };
+            f32x2 vb[8];
+            {
+                const uint8_t *v = stage(c) + St::v + (d >> 6) * kTile + 8 * q * 128 + (d & 7) * 2;
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        auto at = [&](int r) {  // row 8 q + r of the half, whose place within 8 rows is r
+                            return bf16_bits(*reinterpret_cast<const uint16_t *>(v + (32 * half + r) * 128 + ((((d & 63) >> 3) ^ r) << 4)));
+                        };
+                        vb[4 * half + i] = mul2(pack2(at(2 * i), at(2 * i + 1)), vec2(kBeta, half, i));
+                    }
+            }
+
+            // R = b v - b e^G S k
+            if (!(ok = mbar_wait_warp<false>(&sm.mma_p, par, &sm.abort))) break;
+            tc_fence_after();
+            {
+                float x[2][8];
+                tmem_load(lanes + kColP + 8 * q, x[0]);
+                tmem_load(lanes + kColP + 32 + 8 * q, x[1]);
+                tmem_wait_load();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        split_bf16x3(fma2(vec2(kKey, half, i), pack2(x[half][2 * i], x[half][2 * i + 1]), vb[4 * half + i]), hi[i], mid[i], lo[i]);
+                    const uint32_t at = lanes + r_part(2 * half + (q >> 1), 0) + (q & 1) * 4;
+                    tmem_store(at, hi);
+                    tmem_store(at + 8, mid);
+                    tmem_store(at + 16, lo);
+                    tmem_wait_store();
+                    tc_fence_before();
+                    mbar_arrive(&sm.have_r[half]);
+                }
+            }
+
+            if (c > 0) {  // the output of the chunk before, while the tensor cores are at d
+                if (!(ok = mbar_wait_warp<false>(&sm.mma_out, par ^ 1, &sm.abort))) break;
                 tc_fence_after();
                 if (!(ok = finish(c - 1))) break;
             } else {
                 mbar_arrive(&sm.have_read);
             }
 
-            // R = b v - b e^G S k
-            if (!(ok = mbar_wait_warp(&sm.mma_p, par, &sm.abort))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int i0 = 0; i0 < 32; i0 += 16) {
-                float x[16];
-                tmem_load(lanes + kColP + wg * 32 + i0, x);
-                tmem_wait_load();
-                uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const ulonglong2 key = vec2(kKey, i0 + 2 * i);
-                    split_bf16x3(fma2(key.x, pack2(x[2 * i], x[2 * i + 1]), vb[i0 / 2 + i]), hi[i], mid[i], lo[i]);
-                    split_bf16x3(fma2(key.y, pack2(x[2 * i + 2], x[2 * i + 3]), vb[i0 / 2 + i + 1]), hi[i + 1], mid[i + 1], lo[i + 1]);
-                }
-                tmem_store(col_r + i0 / 2, hi);
-                tmem_store(col_r + 16 + i0 / 2, mid);
-                tmem_store(col_r + 32 + i0 / 2, lo);
-            }
-            tmem_wait_store();
-            tc_fence_before();
-            mbar_arrive(&sm.have_r);
-
             // d, decayed for the state (3 parts) and for the output (2)
-            if (!(ok = mbar_wait_warp(&sm.mma_n, par, &sm.abort))) break;
-            tc_fence_after();
-            f32x2 x[16];
-#pragma unroll
-            for (int i0 = 0; i0 < 32; i0 += 16) {
-                float y[16];
-                tmem_load(col_n + i0, y);
-                tmem_wait_load();
-                uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const ulonglong2 left = vec2(kState, i0 + 2 * i);
-                    x[i0 / 2 + i] = pack2(y[2 * i], y[2 * i + 1]);
-                    x[i0 / 2 + i + 1] = pack2(y[2 * i + 2], y[2 * i + 3]);
-                    split_bf16x3(mul2(left.x, x[i0 / 2 + i]), hi[i], mid[i], lo[i]);
-                    split_bf16x3(mul2(left.y, x[i0 / 2 + i + 1]), hi[i + 1], mid[i + 1], lo[i + 1]);
-                }
-                tmem_store(col_r + i0 / 2, hi);
-                tmem_store(col_r + 16 + i0 / 2, mid);
-                tmem_store(col_r + 32 + i0 / 2, lo);
-            }
-            tmem_wait_store();
-            tc_fence_before();
-            mbar_arrive(&sm.have_vs);
-#pragma unroll
-            for (int i0 = 0; i0 < 16; i0 += 8) {
-                uint32_t hi[8], mid[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) split_bf16x2(x[i0 + i], hi[i], mid[i]);
-                tmem_store(col_n + i0, hi);
-                tmem_store(col_n + 16 + i0, mid);
-            }
-            if (!(ok = mbar_wait_warp(&sm.mma_o, par, &sm.abort))) break;
+            if (!(ok = mbar_wait_warp<false>(&sm.mma_n, par, &sm.abort))) break;
             tc_fence_after();
             {
-                float y[32];
-                tmem_load(lanes + kColO + wg * 32, y);
+                float x[2][8];
+                tmem_load(lanes + kColN + 8 * q, x[0]);
+                tmem_load(lanes + kColN + 32 + 8 * q, x[1]);
                 tmem_wait_load();
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const ulonglong2 q = vec2(kQuery, 2 * i);
-                    oi[i] = mul2(q.x, pack2(y[2 * i], y[2 * i + 1]));
-                    oi[i + 1] = mul2(q.y, pack2(y[2 * i + 2], y[2 * i + 3]));
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        split_bf16x3(mul2(vec2(kState, half, i), pack2(x[half][2 * i], x[half][2 * i + 1])), hi[i], mid[i], lo[i]);
+                    const uint32_t at = lanes + r_part(2 * half + (q >> 1), 0) + (q & 1) * 4;
+                    tmem_store(at, hi);
+                    tmem_store(at + 8, mid);
+                    tmem_store(at + 16, lo);
+                    tmem_wait_store();
+                    tc_fence_before();
+                    mbar_arrive(&sm.have_vs[half]);
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t hi[4], mid[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) split_bf16x2(pack2(x[half][2 * i], x[half][2 * i + 1]), hi[i], mid[i]);
+                    const uint32_t at = lanes + d_part(2 * half + (q >> 1), 0) + (q & 1) * 4;
+                    tmem_store(at, hi);
+                    tmem_store(at + 8, mid);
                 }
             }
-            gamma = f[kMisc * C - wg * 32];
+            if (!(ok = mbar_wait_warp<false>(&sm.mma_o, par, &sm.abort))) break;
+            tc_fence_after();
+            {
+                float x[2][8];
+                tmem_load(lanes + kColO + 8 * q, x[0]);
+                tmem_load(lanes + kColO + 32 + 8 * q, x[1]);
+                tmem_wait_load();
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) oi[4 * half + i] = mul2(vec2(kQuery, half, i), pack2(x[half][2 * i], x[half][2 * i + 1]));
+            }
+            gamma = f[kMisc * C - 8 * q];
             tmem_wait_store();
             tc_fence_before();
             mbar_arrive(&sm.have_d);
         }
         // the last chunk's output and the final state
-        if (ok) ok = mbar_wait_warp(&sm.mma_out, (chunks - 1) & 1, &sm.abort);
+        if (ok) ok = mbar_wait_warp<false>(&sm.mma_out, (chunks - 1) & 1, &sm.abort);
         if (ok) {
             tc_fence_after();
             finish(chunks - 1);
-#pragma unroll
-            for (int k0 = 0; k0 < KH; k0 += 16) add_delta(gamma, k0);
+            add_delta(gamma);
             if (sp != nullptr && live) {
 #pragma unroll
                 for (int k = 0; k < KH; k += 4) {
-                    const int kk = wg * KH + k;
+                    const int kk = q * KH + k;
                     float4 x;
                     unpack2(st[k / 2], x.x, x.y);
                     unpack2(st[k / 2 + 1], x.z, x.w);
@@ -907,7 +925,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 template <int PANELS>
 constexpr size_t prep_smem() { return 1024 + kMatrixBytes + sizeof(PrepSmem); }
 template <int PANELS>
-constexpr size_t chunk_smem() { return 1024 + kStages * Stage<PANELS>::bytes + 128 * kRowBytes + C * kRawBytes + sizeof(ChunkSmem); }
+constexpr size_t chunk_smem() { return 1024 + kStages * Stage<PANELS>::bytes + 2 * kTile + sizeof(ChunkSmem); }
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder, looked up once (the library links no driver symbols).
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+bool encode_map(CUtensorMap *map, const ccv_heads_view &v, int dim, int heads, int tokens) {
+    const cuuint64_t size[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t stride[2] = {static_cast<cuuint64_t>(v.stride_head) * 2, static_cast<cuuint64_t>(v.stride_tok) * 2};
+    if ((stride[0] == 0 && heads > 1) || stride[1] == 0 || stride[0] >= 1ull << 40 || stride[1] >= 1ull << 40) return false;
+    const cuuint64_t strides[2] = {heads > 1 ? stride[0] : 16, stride[1]};
+    const cuuint32_t box[3] = {64, 1, C}, one[3] = {1, 1, 1};
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(v.data), size, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int PANELS, bool VS, bool VIO>
 int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
@@ -924,8 +972,12 @@ int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
     const int status = launch_pdl(gdr_prep_kernel<PANELS, VIO>, dim3(static_cast<unsigned>(prep)), dim3(kPrepThreads),
                                   prep_smem<PANELS>(), stream, p);
     if (status != CCV_OK) return status;
+    FwdMaps maps;
+    maps.use = VIO && encoder() != nullptr && encode_map(&maps.q, p.a.q, p.a.dim_k, p.a.num_k_heads, p.total_tokens) &&
+               encode_map(&maps.k, p.a.k, p.a.dim_k, p.a.num_k_heads, p.total_tokens) &&
+               encode_map(&maps.v, p.a.v, p.a.dim_v, p.a.num_v_heads, p.total_tokens);
     return launch_pdl(gdr_chunk_kernel<PANELS, VS, VIO>, dim3(static_cast<unsigned>(blocks)), dim3(kChunkThreads),
-                      chunk_smem<PANELS>(), stream, p, slices);
+                      chunk_smem<PANELS>(), stream, p, maps, slices);
 }
 
 template <int PANELS>

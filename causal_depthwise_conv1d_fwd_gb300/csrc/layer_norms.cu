@@ -4,6 +4,7 @@
 // Both read each element once, keep the row in registers in fp32, reduce it, and write once: 6 bytes an element for the
 // first, 8 to 14 for the second, so HBM bounds them at any size that fills the card and one launch's latency below.
 // A row belongs to LPR lanes: within a warp the reductions are shuffles; longer rows reduce over the block's warps.
+#include <cstdlib>
 #include "ccv_common.cuh"
 #include "ccv_layer.h"
 
@@ -248,7 +249,10 @@ struct GatedLaunch {
         // Four rows a thread once there are enough rows for every SM's threads to have four: below that one row each
         // spreads the call over more SMs.
         if constexpr (LPR <= 32 && VEC == 8 && NV == 1) {
-            if (a.rows * LPR >= 4ll * 2048 * current_device_sms())
+            if (std::getenv("GN_R2") && a.rows * LPR >= 4ll * 2048 * current_device_sms())
+                return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV, 2>, dim3(row_blocks((a.rows + 1) / 2, LPR)),
+                                  dim3(kNormThreads), 0, stream, a);
+            if (std::getenv("GN_R4") && a.rows * LPR >= 4ll * 2048 * current_device_sms())
                 return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV, 4>, dim3(row_blocks((a.rows + 3) / 4, LPR)),
                                   dim3(kNormThreads), 0, stream, a);
         }

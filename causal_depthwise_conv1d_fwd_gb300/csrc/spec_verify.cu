@@ -41,11 +41,11 @@ __device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINIT
 __device__ __forceinline__ float widen(uint16_t x) { return bf16_bits(x); }
 __device__ __forceinline__ float widen(float x) { return x; }
 
-// 8 logits from row[i..], of which those in [0, end) are real; the others come back as -inf.  `aligned`: row + i is on a
-// 16-byte boundary.
+// 8 logits from row[i..], of which those in [0, end) are real; the others come back as -inf.  row + i is on a 16-byte
+// boundary.
 template <typename T>
-__device__ __forceinline__ void load8(const T *row, int i, int end, bool aligned, float (&f)[8]) {
-    if (aligned && i >= 0 && i + 8 <= end) {
+__device__ __forceinline__ void load8(const T *row, int i, int end, float (&f)[8]) {
+    if (i >= 0 && i + 8 <= end) {
         if constexpr (sizeof(T) == 2) {
             Raw<8> r;
             r.v = *reinterpret_cast<const uint4 *>(row + i);
@@ -54,11 +54,9 @@ __device__ __forceinline__ void load8(const T *row, int i, int end, bool aligned
             const float4 x = *reinterpret_cast<const float4 *>(row + i), y = *reinterpret_cast<const float4 *>(row + i + 4);
             f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w; f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = clean(f[k]);
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = i + k >= 0 && i + k < end ? clean(widen(row[i + k])) : -INFINITY;
+        for (int k = 0; k < 8; ++k) f[k] = i + k >= 0 && i + k < end ? widen(row[i + k]) : -INFINITY;
     }
 }
 __device__ __forceinline__ void load8_plain(const float *row, int i, int end, bool aligned, float (&f)[8]) {
@@ -96,13 +94,21 @@ __device__ __forceinline__ void block_best(float &v, int &i, float *sv, int *si)
     __syncthreads();
 }
 
-// e^((x - best) / temp) for x <= best; 0 where x is masked, whatever best is.
-__device__ __forceinline__ float weight_of(float x, float best, float inv_temp) {
-    return x == -INFINITY ? 0.0f : expf((x - best) * inv_temp);
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-__device__ __forceinline__ float inverse_temperature(const VerifyArgs &a, int b) {
+// e^((x - best) / temp) as 2^((x - best) rate), rate = log2(e) / temp.  A masked x gives 0, also when best is -inf.
+struct Weigh {
+    float rate, best;
+    __device__ __forceinline__ Weigh(float rate_, float best_) : rate(rate_), best(best_ == -INFINITY ? 0.0f : best_) {}
+    __device__ __forceinline__ float operator()(float x) const { return ex2((x - best) * rate); }
+};
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float rate_of(const VerifyArgs &a, int b) {
     const float t = a.temperature != nullptr ? a.temperature[b] : 1.0f;
-    return t > 0.0f ? 1.0f / t : 0.0f;  // 0 marks a greedy row
+    return t > 0.0f ? kLog2e / t : 0.0f;  // 0 marks a greedy row
 }
 
 // Maximum, its first index and the sum of exponentials of one share of one position.  Rows may start at any element: the
@@ -118,38 +124,69 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_stats_kernel(const __gr
     if (pos == 0 && split == 0 && threadIdx.x == 0) a.done[b] = 0;
     const int n = a.num_drafts != nullptr ? a.num_drafts[b] : a.drafts;
     if (pos > n) return;
-    const float inv = inverse_temperature(a, b);
+    const float rate = rate_of(a, b);
     const T *logits = static_cast<const T *>(a.logits) + b * a.tb + pos * a.tp;
     const int before = static_cast<int>(reinterpret_cast<uintptr_t>(logits) % 16 / sizeof(T));
     const int start = split * kSplit - before;
     float x[kVectors][8];
 #pragma unroll
-    for (int j = 0; j < kVectors; ++j) load8(logits, start + (j * kVerifyThreads + threadIdx.x) * 8, a.vocab, true, x[j]);
+    for (int j = 0; j < kVectors; ++j) load8(logits, start + (j * kVerifyThreads + threadIdx.x) * 8, a.vocab, x[j]);
     float best = -INFINITY;
-    int index = INT32_MAX;
+    bool odd = false;  // a NaN or +inf among them: then all are cleaned first
 #pragma unroll
     for (int j = 0; j < kVectors; ++j)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (x[j][k] > best) {
-                best = x[j][k];
-                index = start + (j * kVerifyThreads + threadIdx.x) * 8 + k;
-            }
-    block_best(best, index, sv, si);
-    float sum = 0.0f;
-    if (inv > 0.0f) {
+        for (int k = 0; k < 8; ++k) {
+            odd |= !(x[j][k] < INFINITY);
+            best = fmaxf(best, x[j][k]);
+        }
+    if (__syncthreads_or(odd)) {
+        best = -INFINITY;
 #pragma unroll
         for (int j = 0; j < kVectors; ++j)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum += weight_of(x[j][k], best, inv);
+            for (int k = 0; k < 8; ++k) {
+                x[j][k] = clean(x[j][k]);
+                best = fmaxf(best, x[j][k]);
+            }
     }
+    const float mine = best;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) best = fmaxf(best, __shfl_xor_sync(kFullMask, best, m));
+    if (threadIdx.x % 32 == 0) sv[threadIdx.x / 32] = best;
+    __syncthreads();
+    best = sv[threadIdx.x % (kVerifyThreads / 32)];
+#pragma unroll
+    for (int m = kVerifyThreads / 64; m > 0; m >>= 1) best = fmaxf(best, __shfl_xor_sync(kFullMask, best, m));
+    int index = INT32_MAX;
+    if (mine == best) {
+#pragma unroll
+        for (int j = kVectors - 1; j >= 0; --j)
+#pragma unroll
+            for (int k = 7; k >= 0; --k)
+                if (x[j][k] == best) index = start + (j * kVerifyThreads + threadIdx.x) * 8 + k;
+    }
+    float sum = 0.0f;
+    if (rate > 0.0f) {
+        const Weigh weigh(rate, best);
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += weigh(x[j][k]);
+    }
+    index = __reduce_min_sync(kFullMask, index);
+    if (threadIdx.x % 32 == 0) si[threadIdx.x / 32] = index;
+    __syncthreads();
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(kFullMask, sum, m);
     if (threadIdx.x % 32 == 0) sv[threadIdx.x / 32] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
         float z = 0.0f;
-        for (int w = 0; w < kVerifyThreads / 32; ++w) z += sv[w];
+        for (int w = 0; w < kVerifyThreads / 32; ++w) {
+            z += sv[w];
+            index = min(index, si[w]);
+        }
         a.stats[blockIdx.x] = make_float4(best, __int_as_float(index), z, 0.0f);
     }
 }
@@ -175,8 +212,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(const __gri
         }
         return;
     }
-    const float inv = inverse_temperature(a, b);
-    const bool greedy = inv == 0.0f;
+    const float rate = rate_of(a, b);
+    const bool greedy = rate == 0.0f;
     const T *row = static_cast<const T *>(a.logits) + b * a.tb;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
@@ -190,18 +227,18 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(const __gri
                 for (int k = 0; k < a.splits; ++k) {
                     const float4 x = st[k];
                     if (x.x > best) {
-                        z *= weight_of(best, x.x, inv);
+                        z *= Weigh(rate, x.x)(best);
                         best = x.x;
                         top = __float_as_int(x.y);
                     }
-                    z += x.x == -INFINITY ? 0.0f : x.z * weight_of(x.x, best, inv);
+                    z += x.z * Weigh(rate, best)(x.x);
                 }
             }
             if (i < n) {
                 const int token = a.tokens[b * a.db + i * a.dp];
                 if (token >= 0 && token < a.vocab) {
                     float p = greedy && token == top && best > -INFINITY ? 1.0f : 0.0f;
-                    if (!greedy && z > 0.0f) p = weight_of(clean(widen(row[i * a.tp + token])), best, inv) / z;
+                    if (!greedy && z > 0.0f) p = Weigh(rate, best)(clean(widen(row[i * a.tp + token]))) / z;
                     const float q = a.probs != nullptr ? a.probs[b * a.pb + i * a.pp + token] : 1.0f;
                     keep = a.uniform[b * a.ub + i * a.up] * q < p;
                 }
@@ -237,25 +274,25 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(const __gri
         // whole vectors where all three rows allow them
         const int before = static_cast<int>(reinterpret_cast<uintptr_t>(logits) % 16 / sizeof(T));
         const int start = split * kSplit - before;
+        const Weigh weigh(rate, best);
+        const float inv_z = 1.0f / z;
         const bool vn = reinterpret_cast<uintptr_t>(noise + start) % 16 == 0;
         const bool vq = q != nullptr && reinterpret_cast<uintptr_t>(q + start) % 16 == 0;
 #pragma unroll
         for (int j = 0; j < kVectors; ++j) {
             const int v0 = start + (j * kVerifyThreads + threadIdx.x) * 8;
             float x[8], w[8], y[8] = {};
-            load8(logits, v0, a.vocab, true, x);
+            load8(logits, v0, a.vocab, x);
             load8_plain(noise, v0, a.vocab, vn && v0 >= 0, w);
             if (q != nullptr) load8_plain(q, v0, a.vocab, vq && v0 >= 0, y);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                float r = weight_of(x[k], best, inv) / z - y[k];
+                float r = fmaf(weigh(clean(x[k])), inv_z, -y[k]);
                 if (v0 + k == sure) r = 0.0f;
-                if (r > 0.0f) {
-                    const float score = r / w[k];
-                    if (score > top) {
-                        top = score;
-                        index = v0 + k;
-                    }
+                const float score = r * rcp_approx(w[k]);
+                if (score > top) {  // never so for r <= 0
+                    top = score;
+                    index = v0 + k;
                 }
             }
         }
