@@ -23,16 +23,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
 __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-// Whether the barrier's phase `parity` is complete.  kSleep: the hardware may hold the thread for a while if it is not.
-template <bool kSleep>
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+// Whether the barrier's phase `parity` is complete; the hardware may hold the thread for a while if it is not, which leaves
+// the issue slots to the warps that work (polling without it made the chunk kernel of gdr_fwd 4% slower).
+__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     uint32_t done;
-    if constexpr (kSleep)
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return done != 0;
 }
 
@@ -45,25 +41,23 @@ constexpr uint64_t kMaxWaitNs = 2000000000ull;  // far beyond any wait of a heal
 
 // Waits until the barrier's phase `parity` is complete.  False when two seconds ran out or another thread of the block
 // gave up (`*abort` set): the caller then leaves its loop and goes to the kernel's common end.
-template <bool kSleep = true>
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    if (mbar_test<kSleep>(bar, parity)) return true;
-    const uint64_t start = timer_ns();
-    for (int i = 1;; ++i) {
-        if (mbar_test<kSleep>(bar, parity)) return true;
-        if ((i & 63) == 0) {
-            if (*abort) return false;
-            if (timer_ns() - start > kMaxWaitNs) {
-                *abort = 1;
-                return false;
-            }
+    uint64_t start = 0;
+    for (int i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 63) != 0) continue;
+        if (*abort) return false;
+        const uint64_t now = timer_ns();
+        if (start == 0) start = now;
+        if (now - start > kMaxWaitNs) {
+            *abort = 1;
+            return false;
         }
     }
+    return true;
 }
 // The same for a whole warp, with one answer for all its lanes (tensor-memory accesses are warp-wide).
-template <bool kSleep = true>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait<kSleep>(bar, parity, abort));
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
 // --------------------------------------------------------- bulk copies ----
@@ -151,12 +145,11 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[8]
 // ----------------------------------------------------------- tcgen05.mma ----
 
 // Shared-memory operand in 128-byte swizzled rows: rows of 64 bf16 values, 16-byte piece c of row r at piece c ^ (r & 7),
-// 8 rows (1024 bytes) a group.  K-major: a row is one M/N index, groups are `stride` bytes apart.  MN-major: a row is one
-// K index and 64 M/N indices, groups of 8 K indices are `stride` apart, groups of 64 M/N indices `lead` apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((lead >> 4) & 0x3fffu) << 16) |
-           (static_cast<uint64_t>((stride >> 4) & 0x3fffu) << 32) | (1ull << 46) | (2ull << 61);
-}
+// 8 rows (1024 bytes) a group, groups one after the other.  K-major: a row is one M/N index.  MN-major (up to 64 M/N
+// indices): a row is one K index.  The upper word of its descriptor is kDescHigh, the lower one the address; addresses and
+// descriptors add, byte offsets as offset / 16.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return (addr >> 4) & 0x3fffu; }
 // bf16 x bf16 -> fp32; b_mn: B is MN-major.
 constexpr uint32_t mma_desc(int m, int n, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
@@ -170,19 +163,20 @@ __device__ __forceinline__ uint32_t elect_lane() {
 // D[tmem] (+)= A B^T, issued by the lane whose `lane` flag is set, with A in tensor memory (lane = row, a 32-bit column = 2
 // K indices) ...  Called by the whole warp with uniform operands: from inside a one-lane branch each issue took 52 cycles
 // (measured, any N up to 64), this way 16, so that 128 x 64 x 16 takes the tensor cores' own 32.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lane) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate, uint32_t lane) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lane)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 bd;\n\tmov.b64 bd, {%2, %6};\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lane), "n"(kDescHigh)
         : "memory");
 }
 // ... or in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lane) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate, uint32_t lane) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lane)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 ad, bd;\n\tmov.b64 ad, {%1, %6};\n\tmov.b64 bd, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lane), "n"(kDescHigh)
         : "memory");
 }
 // Arrives on `bar` when every MMA that lane issued so far is complete.
@@ -206,6 +200,17 @@ __device__ __forceinline__ void take_part(float &a, float &b, uint32_t &part) {
         "fma.rn.f32.bf16 %1, hi, one, %1;\n\t}"
         : "+f"(a), "+f"(b)
         : "r"(part));
+}
+// x plus a bf16 value a half, exact to one rounding; the values need no unpacking.
+__device__ __forceinline__ f32x2 add_bf16(f32x2 x, uint16_t lo, uint16_t hi) {
+    float a, b;
+    unpack2(x, a, b);
+    asm("{\n\t.reg .b16 one;\n\tmov.b16 one, 0x3f80;\n\t"
+        "fma.rn.f32.bf16 %0, %2, one, %0;\n\t"
+        "fma.rn.f32.bf16 %1, %3, one, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "h"(lo), "h"(hi));
+    return pack2(a, b);
 }
 __device__ __forceinline__ void split_bf16x2(f32x2 x, uint32_t &hi, uint32_t &mid) {
     float a, b;

@@ -9,6 +9,10 @@
 //   gdr_prep_kernel   for every chunk and key head at once: the two products, the decays, T = (I + A)^-1, P, and what each
 //                     token multiplies by; written to the workspace in the layout the tensor cores read.
 //   gdr_chunk_kernel  for every sequence and value head: the chunks in order with S^T kept on chip.
+// Where sequences and heads are too few for the card, each sequence is cut into segments of chunks.  A segment takes its
+// first state to S M + N; gdr_chunk_kernel first finds N (the segment from a zero state) and M (from the identity, without
+// values) of all segments at once, gdr_join_kernel goes through them for each segment's first state, and gdr_chunk_kernel
+// then runs all segments from there.  That is three times the work on as many more SMs as there are segments.
 //
 // Precision.  The state is fp32, so every product that reaches it is formed to 24 bits: k and q enter as their own bf16
 // values (exact; their norms are factors of a token, applied to sums), and each inexact operand (S, R, T, d) as three bf16
@@ -38,6 +42,8 @@ struct FwdArgs {
     int batch, total_tokens, slots;
     uint8_t *heads;  // (slots, num_v_heads) blocks of kHeadBytes
     int *err_count;
+    int seg_chunks;  // chunks of a segment; 0: sequences are not cut
+    float *seg_state, *seg_step;  // (segment slots, num_v_heads, dim_v or dim_k, 64 panels): first states, and M
 };
 
 // Tensor maps (dim, head, token) of q, k and v with boxes of 64 values x 64 tokens; `use` is false where the tensors'
@@ -47,11 +53,36 @@ struct FwdMaps {
     bool use;
 };
 
-// Chunk j of sequence i is in slot first_slot(i) + j.  floor(s / 64) + i leaves every sequence room for its
-// ceil(n / 64) chunks, needs no sum over the lengths, and total / 64 + batch slots in all.
-__device__ __forceinline__ int first_slot(int start, int i) { return (start >> 6) + i; }
+// Chunk (or segment) j of sequence i is in slot first_slot(i) + j.  floor(s / u) + i, with u the tokens of a chunk, leaves
+// every sequence room for its ceil(n / u) chunks, needs no sum over the lengths, and total / u + batch slots in all.
+__device__ __forceinline__ int first_slot(int start, int i, int unit) { return start / unit + i; }
+
+// The sequence of a slot, the last i with first_slot(i) <= slot, and its tokens; by a whole warp, 32 candidates at a time.
+__device__ __forceinline__ void find_sequence(const int32_t *query_start_loc, int batch, int slot, int unit, int lane, int &seq, int &start,
+                                              int &end) {
+    int lo = 0, hi = batch;  // the answer is in [lo, hi)
+    do {
+        const int step = (hi - lo + 31) / 32;
+        const int i = min(lo + lane * step, batch), next = max(i, min(i + step, hi));
+        const int at = query_start_loc[i], to = query_start_loc[next];
+        const bool below = i < hi && first_slot(at, i, unit) <= slot;
+        const int last = 31 - __clz(__ballot_sync(kFullMask, below) | 1);
+        lo += last * step;
+        hi = min(hi, lo + step);
+        start = __shfl_sync(kFullMask, at, last);
+        end = __shfl_sync(kFullMask, to, last);
+    } while (hi - lo > 1);
+    seq = lo;
+}
 
 __device__ __forceinline__ bool sequence_ok(int s, int e, int total) { return s >= 0 && e >= s && e <= total; }
+
+// Swizzled tiles need shared memory on a 1024-byte boundary.
+__device__ __forceinline__ bool misplaced(const void *smem, int *err_count) {
+    const bool bad = (smem_u32(smem) & 1023u) != 0;
+    if (bad && threadIdx.x == 0) count_error(err_count);
+    return bad;
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -224,7 +255,7 @@ __device__ __forceinline__ void invert(float *matrices, int tid) {
 template <int PANELS, bool V>
 __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_constant__ FwdArgs p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *ab = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *ab = smem_raw;  // on a 1024-byte boundary, since the kernel has no static shared memory (checked below)
     float *matrices = reinterpret_cast<float *>(ab);
     PrepSmem &sm = *reinterpret_cast<PrepSmem *>(ab + kMatrixBytes);
     static_assert(kMatrixBytes >= PANELS * 2 * kTile && kMatrixBytes % 16 == 0, "");
@@ -232,23 +263,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hk = blockIdx.x % a.num_k_heads, slot = blockIdx.x / a.num_k_heads;
     wait_prior_grid();
+    if (misplaced(smem_raw, p.err_count)) return;
 
-    // The sequence of this slot: the last i with first_slot(i) <= slot, found by a warp 32 candidates at a time.
     if (warp == 0) {
-        int lo = 0, hi = p.batch, s = 0, e = 0;  // the answer is in [lo, hi)
-        do {
-            const int step = (hi - lo + 31) / 32;
-            const int i = min(lo + lane * step, p.batch), next = max(i, min(i + step, hi));
-            const int at = p.query_start_loc[i], to = p.query_start_loc[next];
-            const bool below = i < hi && first_slot(at, i) <= slot;
-            const int last = 31 - __clz(__ballot_sync(kFullMask, below) | 1);
-            lo += last * step;
-            hi = min(hi, lo + step);
-            s = __shfl_sync(kFullMask, at, last);
-            e = __shfl_sync(kFullMask, to, last);
-        } while (hi - lo > 1);
+        int seq, s, e;
+        find_sequence(p.query_start_loc, p.batch, slot, C, lane, seq, s, e);
         if (lane == 0) {
-            sm.seq = lo;
+            sm.seq = seq;
             sm.start = s;
             sm.end = e;
         }
@@ -261,7 +282,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
     __syncthreads();
     const int seq = sm.seq, s = sm.start, e = sm.end;
     if (!sequence_ok(s, e, p.total_tokens)) return;  // counted by the chunk kernel
-    const int chunk = slot - first_slot(s, seq);
+    const int chunk = slot - first_slot(s, seq, C);
     if (chunk < 0 || chunk * C >= e - s) return;
     if (p.cache_indices != nullptr && p.cache_indices[seq] == a.pad_slot_id) return;
     const int t0 = s + chunk * C, n = min(C, e - t0);
@@ -307,7 +328,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
     if (tid == 0) {  // [K; Q] K^T, 128 x 64
 #pragma unroll
         for (int ks = 0; ks < PANELS * 4; ++ks) {
-            const uint64_t d = smem_desc(smem_u32(ab) + (ks / 4) * 2 * kTile + (ks % 4) * 32, 0, 1024);
+            const uint32_t d = desc_low(smem_u32(ab)) + ((ks / 4) * 2 * kTile + (ks % 4) * 32) / 16;
             mma_ss(tmem, d, d, mma_desc(128, C, false), ks > 0, 1);
         }
         mma_commit(&sm.bar, 1);
@@ -452,10 +473,13 @@ enum : uint32_t {
     kColR = 320,     // 96: R in 3 parts, then the decayed d in 3 parts
     kColN = 416,     // 64: d
 };
-// Warpgroup q holds 16 PANELS keys of every row of S.  They have 24 PANELS columns: 8 PANELS for each part (a column is two
-// bf16 values), or 16 PANELS for what is added to them.
+// Warpgroup q holds 16 PANELS keys of every row of S.  They have 24 PANELS columns, 8 PANELS for each part (a column is two
+// bf16 values); what is added to them comes in the last 16 PANELS of those where q is even and the first where it is odd, so
+// that two warpgroups' are next to each other and one MMA adds to both.
 template <int PANELS>
 __device__ __forceinline__ constexpr uint32_t s_part(int q, int part) { return kColS + q * 24 * PANELS + part * 8 * PANELS; }
+template <int PANELS>
+__device__ __forceinline__ constexpr uint32_t s_added(int q) { return s_part<PANELS>(q, 0) + (q & 1 ? 0 : 8 * PANELS); }
 // It also holds tokens 8 q .. + 7 and 32 + 8 q .. + 7 of every row of R and d, so that two warpgroups make up the 16 tokens of
 // an inner step of the tensor cores, and the steps of tokens 0 .. 31 can run while the others are prepared.
 __device__ __forceinline__ constexpr uint32_t r_part(int step, int part) { return kColR + step * 24 + part * 8; }
@@ -478,40 +502,71 @@ struct ChunkSmem {
     uint64_t drain;
     uint32_t tmem;
     int abort;
+    int seq, start, end;
 };
 
-// V: the state allows 16-byte vectors.  VIO: rows of q, k, v and out do.
-template <int PANELS, bool V, bool VIO>
+// FULL: outputs and final states.  Otherwise the first pass over segments: N of all but the last, and M of those between
+// (the last block of every group of slices + 1).  V: the state allows 16-byte vectors.  VIO: rows of q, k, v and out do.
+template <int PANELS, bool FULL, bool V, bool VIO>
 __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __grid_constant__ FwdArgs p,
                                                                      const __grid_constant__ FwdMaps maps, int slices) {
     using St = Stage<PANELS>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *base = smem_raw;  // on a 1024-byte boundary, since the kernel has no static shared memory (checked below)
     uint16_t *out_tile = reinterpret_cast<uint16_t *>(base + kStages * St::bytes);  // 64 rows of 128 values
     ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(base + kStages * St::bytes + 2 * kTile);
     const ccv_gdr_args &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFullMask, tid >> 5, 0);
-    const int slice = blockIdx.x % slices;
-    const int bh = blockIdx.x / slices;
-    const int h = bh % a.num_v_heads, seq = bh / a.num_v_heads;
+    const int types = FULL ? slices : slices + 1;
+    const int slice = blockIdx.x % types;
+    const bool step_only = !FULL && slice == slices;  // M
+    const int bh = blockIdx.x / types;
+    const int h = bh % a.num_v_heads, slot = bh / a.num_v_heads;
     const int hk = h / (a.num_v_heads / a.num_k_heads);
     wait_prior_grid();
+    if (misplaced(smem_raw, p.err_count)) return;
 
-    const int s = p.query_start_loc[seq], e = p.query_start_loc[seq + 1];
+    int seq = slot, segment = 0, s, e;
+    if (p.seg_chunks > 0) {
+        if (warp == 0) {
+            find_sequence(p.query_start_loc, p.batch, slot, p.seg_chunks * C, lane, seq, s, e);
+            if (lane == 0) {
+                sm.seq = seq;
+                sm.start = s;
+                sm.end = e;
+            }
+        }
+        __syncthreads();
+        seq = sm.seq;
+        s = sm.start;
+        e = sm.end;
+    } else {
+        s = p.query_start_loc[seq];
+        e = p.query_start_loc[seq + 1];
+    }
     const int line = p.cache_indices != nullptr ? p.cache_indices[seq] : seq;
-    const bool counts = tid == 0 && slice == 0 && h == 0;
-    if (!sequence_ok(s, e, p.total_tokens)) {
-        if (counts) count_error(p.err_count);
+    const bool good = sequence_ok(s, e, p.total_tokens) && (a.state == nullptr || line == a.pad_slot_id || (line >= 0 && line < a.num_lines));
+    if (p.seg_chunks > 0) segment = slot - first_slot(s, seq, p.seg_chunks * C);
+    if (!good) {
+        if (FULL && p.seg_chunks == 0 && tid == 0 && slice == 0 && h == 0) count_error(p.err_count);
         return;
     }
     if (e == s || line == a.pad_slot_id) return;
-    if (a.state != nullptr && (line < 0 || line >= a.num_lines)) {
-        if (counts) count_error(p.err_count);
-        return;
+    int chunks = (e - s + C - 1) / C;
+    int slot0 = first_slot(s, seq, C);
+    bool last = true;  // segment of the sequence
+    if (p.seg_chunks > 0) {
+        const int segments = (chunks + p.seg_chunks - 1) / p.seg_chunks;
+        if (segment < 0 || segment >= segments) return;
+        last = segment == segments - 1;
+        if (!FULL && (last || (step_only && segment == 0))) return;
+        const int c0 = segment * p.seg_chunks;
+        chunks = min(p.seg_chunks, chunks - c0);
+        slot0 += c0;
+        s += c0 * C;
+        if (!last) e = s + chunks * C;
     }
-    const int chunks = (e - s + C - 1) / C;
-    const int slot0 = first_slot(s, seq);
 
     if (tid == 0) {
         sm.abort = 0;
@@ -535,24 +590,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kIssueWarp) {
             const uint32_t el = elect_lane();
-            const uint32_t smem0 = __shfl_sync(kFullMask, smem_u32(base), 0);
+            const uint32_t smem0 = desc_low(__shfl_sync(kFullMask, smem_u32(base), 0));  // all below in units of 16 bytes
             // keys of warpgroup q from step j on: their place in the rows of K and Q
             auto key_at = [](int q, int j) {
                 const int key = q * 16 * PANELS + j * 16;
-                return (key / 64) * 2 * kTile + (key % 64) * 2;
+                return ((key / 64) * 2 * kTile + (key % 64) * 2) / 16;
             };
+            constexpr uint32_t kTokens = mma_desc(128, C, false), kKeys = mma_desc(128, 32 * PANELS, true);
             int c = 0;
             for (; c < chunks; ++c) {
                 const uint32_t par = c & 1;
-                const uint32_t kq = smem0 + (c % kStages) * St::bytes;
-                const uint32_t head = kq + St::head;
-                if (!mbar_wait_warp<false>(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort)) break;
-                if (c > 0 && !mbar_wait_warp<false>(&sm.mma_out, par ^ 1, &sm.abort)) break;  // it read d where P goes
+                const uint32_t kq = smem0 + (c % kStages) * (St::bytes / 16);
+                const uint32_t head = kq + St::head / 16;
+                if (!mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort)) break;
+                if (FULL && c > 0 && !mbar_wait_warp(&sm.mma_out, par ^ 1, &sm.abort)) break;  // it read d where P goes
                 bool ok = true;
                 // S^T k^T, three parts of S; the keys are exact
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    if (!(ok = mbar_wait_warp<false>(&sm.have_s[g], par, &sm.abort))) break;
+                    if (!(ok = mbar_wait_warp(&sm.have_s[g], par, &sm.abort))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int part = 0; part < 3; ++part)
@@ -560,15 +616,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                         for (int q = 2 * g; q < 2 * g + 2; ++q)
 #pragma unroll
                             for (int j = 0; j < PANELS; ++j)
-                                mma_ts(tmem + kColP, tmem + s_part<PANELS>(q, part) + j * 8, smem_desc(kq + key_at(q, j), 0, 1024),
-                                       mma_desc(128, C, false), part + q + j > 0, el);
+                                mma_ts(tmem + kColP, tmem + s_part<PANELS>(q, part) + j * 8, kq + key_at(q, j), kTokens,
+                                       part + q + j > 0, el);
                 }
                 if (!ok) break;
                 mma_commit(&sm.mma_p, el);
                 // d^T = R^T T^T: the six products of parts above 2^-24, for tokens 0 .. 31 of the sum, then the others
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    if (!(ok = mbar_wait_warp<false>(&sm.have_r[half], par, &sm.abort))) break;
+                    if (!(ok = mbar_wait_warp(&sm.have_r[half], par, &sm.abort))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int sum = 0; sum < 3; ++sum)
@@ -576,56 +632,58 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                         for (int part = 0; part <= sum; ++part)
 #pragma unroll
                             for (int ks = 2 * half; ks < 2 * half + 2; ++ks)
-                                mma_ts(tmem + kColN, tmem + r_part(ks, part), smem_desc(head + kT + (sum - part) * kTile + ks * 32, 0, 1024),
-                                       mma_desc(128, C, false), sum + part + ks > 0, el);
+                                mma_ts(tmem + kColN, tmem + r_part(ks, part), head + (kT + (sum - part) * kTile + ks * 32) / 16, kTokens,
+                                       sum + part + ks > 0, el);
                 }
                 if (!ok) break;
                 mma_commit(&sm.mma_n, el);
                 // S^T q^T, once the previous chunk's output has left these columns
-                if (!mbar_wait_warp<false>(&sm.have_read, par, &sm.abort)) break;
-                tc_fence_after();
+                if constexpr (FULL) {
+                    if (!mbar_wait_warp(&sm.have_read, par, &sm.abort)) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < 4; ++q)
 #pragma unroll
-                        for (int j = 0; j < PANELS; ++j)
-                            mma_ts(tmem + kColO, tmem + s_part<PANELS>(q, part) + j * 8, smem_desc(kq + kTile + key_at(q, j), 0, 1024),
-                                   mma_desc(128, C, false), part + q + j > 0, el);
-                mma_commit(&sm.mma_o, el);
-                if (!mbar_wait_warp<false>(&sm.have_vs[0], par, &sm.abort)) break;
-                if (!mbar_wait_warp<false>(&sm.mma_o, par, &sm.abort)) break;  // S is about to be overwritten
-                // what the chunk adds to S^T: tokens are the inner axis, so the keys are read MN-major; each warpgroup's keys
-                // into its own columns
+                            for (int j = 0; j < PANELS; ++j)
+                                mma_ts(tmem + kColO, tmem + s_part<PANELS>(q, part) + j * 8, kq + kTile / 16 + key_at(q, j), kTokens,
+                                       part + q + j > 0, el);
+                    mma_commit(&sm.mma_o, el);
+                }
+                if (!mbar_wait_warp(&sm.have_vs[0], par, &sm.abort)) break;
+                if (FULL && !mbar_wait_warp(&sm.mma_o, par, &sm.abort)) break;  // S is about to be overwritten
+                // what the chunk adds to S^T: tokens are the inner axis, so the keys are read MN-major; those of two
+                // warpgroups at a time
                 auto add = [&](int g, int half) {
 #pragma unroll
-                    for (int q = 2 * g; q < 2 * g + 2; ++q)
+                    for (int part = 0; part < 3; ++part)
 #pragma unroll
-                        for (int part = 0; part < 3; ++part)
-#pragma unroll
-                            for (int ks = 2 * half; ks < 2 * half + 2; ++ks)
-                                mma_ts(tmem + s_part<PANELS>(q, 0), tmem + r_part(ks, part), smem_desc(kq + key_at(q, 0) + ks * 2048, 0, 1024),
-                                       mma_desc(128, 16 * PANELS, true), part + ks > 0, el);
+                        for (int ks = 2 * half; ks < 2 * half + 2; ++ks)
+                            mma_ts(tmem + s_added<PANELS>(2 * g), tmem + r_part(ks, part), kq + key_at(2 * g, 0) + ks * 2048 / 16, kKeys,
+                                   part + ks > 0, el);
                 };
                 tc_fence_after();
                 add(0, 0);
                 add(1, 0);
-                if (!mbar_wait_warp<false>(&sm.have_vs[1], par, &sm.abort)) break;
+                if (!mbar_wait_warp(&sm.have_vs[1], par, &sm.abort)) break;
                 tc_fence_after();
                 add(0, 1);
                 mma_commit(&sm.mma_delta[0], el);
                 add(1, 1);
                 mma_commit(&sm.mma_delta[1], el);
-                if (!mbar_wait_warp<false>(&sm.have_d, par, &sm.abort)) break;
-                tc_fence_after();
-                // d P^T: the three products of parts above 2^-16
+                if constexpr (FULL) {
+                    if (!mbar_wait_warp(&sm.have_d, par, &sm.abort)) break;
+                    tc_fence_after();
+                    // d P^T: the three products of parts above 2^-16
 #pragma unroll
-                for (int term = 0; term < 3; ++term)
+                    for (int term = 0; term < 3; ++term)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_ts(tmem + kColO, tmem + d_part(ks, term == 1), smem_desc(head + kP + (term == 2 ? kTile : 0) + ks * 32, 0, 1024),
-                               mma_desc(128, C, false), term + ks > 0, el);
-                mma_commit(&sm.mma_out, el);
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts(tmem + kColO, tmem + d_part(ks, term == 1), head + (kP + (term == 2 ? kTile : 0) + ks * 32) / 16, kTokens,
+                                   term + ks > 0, el);
+                    mma_commit(&sm.mma_out, el);
+                }
                 mma_commit(&sm.empty[c % kStages], el);
             }
             if (c < chunks) {  // gave up: let the MMAs end before their memories go
@@ -637,7 +695,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         } else if (warp == kStoreWarp) {
             const int width = min(128, a.dim_v - slice * 128);
             uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + slice * 128 * a.out.stride_dim;
-            for (int c = 0; c < chunks; ++c) {
+            for (int c = 0; FULL && c < chunks; ++c) {
                 if (!mbar_wait_warp(&sm.out_full, c & 1, &sm.abort)) break;
                 const int t0 = s + c * C, n = min(C, e - t0);
                 if constexpr (VIO) {  // two rows a pass, 16 bytes a lane
@@ -659,7 +717,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             const int id = tid - kLoadWarp * 32;
             const int width = min(128, a.dim_v - slice * 128);
             ccv_heads_view vv = a.v;
-            vv.data = static_cast<const uint16_t *>(a.v.data) + slice * 128 * a.v.stride_dim;
+            if (!step_only) vv.data = static_cast<const uint16_t *>(a.v.data) + slice * 128 * a.v.stride_dim;
             const uint8_t *heads = p.heads + (static_cast<int64_t>(slot0) * a.num_v_heads + h) * kHeadBytes;
             const int64_t heads_step = static_cast<int64_t>(a.num_v_heads) * kHeadBytes;
             int c = 0;
@@ -670,10 +728,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 if (id == 0 && c + 1 < chunks) {  // the stage frees up late: let L2 have the next chunk's part by then
                     bulk_prefetch(heads + (c + 1) * heads_step, kHeadBytes);
                     if (VIO && maps.use) {
-                        for (int i = 0; i < 2; ++i) tensor_prefetch(&maps.v, slice * 128 + i * 64, h, t0 + C);
+                        if (!step_only)
+                            for (int i = 0; i < 2; ++i) tensor_prefetch(&maps.v, slice * 128 + i * 64, h, t0 + C);
                         for (int i = 0; i < PANELS; ++i) {
                             tensor_prefetch(&maps.k, i * 64, hk, t0 + C);
-                            tensor_prefetch(&maps.q, i * 64, hk, t0 + C);
+                            if (FULL) tensor_prefetch(&maps.q, i * 64, hk, t0 + C);
                         }
                     }
                 }
@@ -681,19 +740,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 uint8_t *st = base + (c % kStages) * St::bytes;
                 uint64_t *bar = &sm.full[c % kStages];
                 if (id == 0) {
-                    mbar_expect_tx(bar, kHeadBytes + (whole ? St::head : 0));
+                    const int tiles = whole ? PANELS * (FULL ? 2 : 1) + (step_only ? 0 : 2) : 0;
+                    mbar_expect_tx(bar, (FULL ? kHeadBytes : kHeadBytes - 2 * kTile) + tiles * kTile);
                     if (whole) {
                         for (int i = 0; i < PANELS; ++i) tensor_load(st + i * 2 * kTile, &maps.k, i * 64, hk, t0, bar);
-                        for (int i = 0; i < 2; ++i) tensor_load(st + St::v + i * kTile, &maps.v, slice * 128 + i * 64, h, t0, bar);
+                        if (!step_only)
+                            for (int i = 0; i < 2; ++i) tensor_load(st + St::v + i * kTile, &maps.v, slice * 128 + i * 64, h, t0, bar);
                     }
-                    bulk_load(st + St::head, heads + c * heads_step, kHeadBytes, bar);
-                    if (whole)
-                        for (int i = 0; i < PANELS; ++i) tensor_load(st + i * 2 * kTile + kTile, &maps.q, i * 64, hk, t0, bar);
+                    const uint8_t *src = heads + c * heads_step;
+                    if constexpr (FULL) {
+                        bulk_load(st + St::head, src, kHeadBytes, bar);
+                        if (whole)
+                            for (int i = 0; i < PANELS; ++i) tensor_load(st + i * 2 * kTile + kTile, &maps.q, i * 64, hk, t0, bar);
+                    } else {  // without P
+                        bulk_load(st + St::head + kT, src + kT, kP - kT, bar);
+                        bulk_load(st + St::head + kVec, src + kVec, kHeadBytes - kVec, bar);
+                    }
                 }
                 if (!whole) {
-                    stage_rows<2, VIO, kLoaders>(st + St::v, kTile, vv, t0, h, n, width, id);
+                    if (!step_only) stage_rows<2, VIO, kLoaders>(st + St::v, kTile, vv, t0, h, n, width, id);
                     stage_rows<PANELS, VIO, kLoaders>(st, 2 * kTile, a.k, t0, hk, n, a.dim_k, id);
-                    stage_rows<PANELS, VIO, kLoaders>(st + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, id);
+                    if (FULL) stage_rows<PANELS, VIO, kLoaders>(st + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, id);
                     cp_async_commit();
                     cp_async_wait<0>();
                     fence_async_shared();
@@ -708,27 +775,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
         constexpr int KH = 16 * PANELS;  // keys of the state a thread holds
-        const int q = warp >> 2, d = (warp & 3) * 32 + lane, row = slice * 128 + d;
-        const bool live = row < a.dim_v;
+        const int q = warp >> 2, d = (warp & 3) * 32 + lane, row = step_only ? d : slice * 128 + d;
+        const bool live = row < (step_only ? a.dim_k : a.dim_v);
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t col_s = lanes + s_part<PANELS>(q, 0);
+        // Row d of the state this block starts from and ends with: a pool line's, or a segment's in the workspace.
+        constexpr int kLdS = 64 * PANELS;
+        auto in_segment = [&](float *at, int which, int rows) {
+            return at + ((static_cast<int64_t>(which) * a.num_v_heads + h) * rows + row) * kLdS;
+        };
+        float *pool = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + row * a.s_stride_v : nullptr;
         const bool init = a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
-        float *sp = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + row * a.s_stride_v : nullptr;
+        const float *from = segment == 0 ? (init ? pool : nullptr) : FULL ? in_segment(p.seg_state, slot, a.dim_v) : nullptr;
 
         f32x2 st[KH / 2];  // this thread's part of row d of S
 #pragma unroll
         for (int k = 0; k < KH; k += 4) {
             const int kk = q * KH + k;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (init && live) {
-                if constexpr (V) {
-                    if (kk < a.dim_k) x = *reinterpret_cast<const float4 *>(sp + kk);
+            if (from != nullptr && live) {
+                if (V || segment > 0) {
+                    if (kk < a.dim_k) x = *reinterpret_cast<const float4 *>(from + kk);
                 } else {
-                    if (kk < a.dim_k) x.x = sp[kk * a.s_stride_k];
-                    if (kk + 1 < a.dim_k) x.y = sp[(kk + 1) * a.s_stride_k];
-                    if (kk + 2 < a.dim_k) x.z = sp[(kk + 2) * a.s_stride_k];
-                    if (kk + 3 < a.dim_k) x.w = sp[(kk + 3) * a.s_stride_k];
+                    if (kk < a.dim_k) x.x = from[kk * a.s_stride_k];
+                    if (kk + 1 < a.dim_k) x.y = from[(kk + 1) * a.s_stride_k];
+                    if (kk + 2 < a.dim_k) x.z = from[(kk + 2) * a.s_stride_k];
+                    if (kk + 3 < a.dim_k) x.w = from[(kk + 3) * a.s_stride_k];
                 }
+            } else if (step_only && live) {
+                x = make_float4(kk == row, kk + 1 == row, kk + 2 == row, kk + 3 == row);
             }
             st[k / 2] = pack2(x.x, x.y);
             st[k / 2 + 1] = pack2(x.z, x.w);
@@ -740,7 +815,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 #pragma unroll
             for (int k0 = 0; k0 < KH; k0 += 16) {
                 float x[16];
-                tmem_load(col_s + k0, x);
+                tmem_load(lanes + s_added<PANELS>(q) + k0, x);
                 tmem_wait_load();
 #pragma unroll
                 for (int k = 0; k < 8; ++k) st[k0 / 2 + k] = fma2(g2, st[k0 / 2 + k], pack2(x[2 * k], x[2 * k + 1]));
@@ -755,7 +830,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             tmem_wait_load();
             tc_fence_before();
             mbar_arrive(&sm.have_read);
-            if (c > 0 && !mbar_wait_warp<false>(&sm.out_free, (c - 1) & 1, &sm.abort)) return false;
+            if (c > 0 && !mbar_wait_warp(&sm.out_free, (c - 1) & 1, &sm.abort)) return false;
             uint16_t *o = out_tile + 8 * q * 128 + d;
 #pragma unroll
             for (int half = 0; half < 2; ++half)
@@ -774,7 +849,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         for (int c = 0; c < chunks; ++c) {
             const uint32_t par = c & 1;
             if (c > 0) {
-                if (!(ok = mbar_wait_warp<false>(&sm.mma_delta[q >> 1], par ^ 1, &sm.abort))) break;
+                if (!(ok = mbar_wait_warp(&sm.mma_delta[q >> 1], par ^ 1, &sm.abort))) break;
                 tc_fence_after();
                 add_delta(gamma);  // all of it is read before its parts, which are wider, overwrite it
             }
@@ -792,11 +867,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             mbar_arrive(&sm.have_s[q >> 1]);
 
             // b v of this thread's tokens
-            if (!(ok = mbar_wait_warp<false>(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
+            if (!(ok = mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
             const float *f = reinterpret_cast<const float *>(stage(c) + St::head + kVec) + 8 * q;
             auto vec2 = [&](int which, int half, int i) { return *reinterpret_cast<const f32x2 *>(f + which * C + 32 * half + 2 * i); };
             f32x2 vb[8];
-            {
+            if (step_only) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) vb[i] = 0ull;
+            } else {
                 const uint8_t *v = stage(c) + St::v + (d >> 6) * kTile + 8 * q * 128 + (d & 7) * 2;
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
@@ -810,7 +888,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             }
 
             // R = b v - b e^G S k
-            if (!(ok = mbar_wait_warp<false>(&sm.mma_p, par, &sm.abort))) break;
+            if (!(ok = mbar_wait_warp(&sm.mma_p, par, &sm.abort))) break;
             tc_fence_after();
             {
                 float x[2][8];
@@ -833,16 +911,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 }
             }
 
-            if (c > 0) {  // the output of the chunk before, while the tensor cores are at d
-                if (!(ok = mbar_wait_warp<false>(&sm.mma_out, par ^ 1, &sm.abort))) break;
-                tc_fence_after();
-                if (!(ok = finish(c - 1))) break;
-            } else {
-                mbar_arrive(&sm.have_read);
+            if constexpr (FULL) {
+                if (c > 0) {  // the output of the chunk before, while the tensor cores are at d
+                    if (!(ok = mbar_wait_warp(&sm.mma_out, par ^ 1, &sm.abort))) break;
+                    tc_fence_after();
+                    if (!(ok = finish(c - 1))) break;
+                } else {
+                    mbar_arrive(&sm.have_read);
+                }
             }
 
             // d, decayed for the state (3 parts) and for the output (2)
-            if (!(ok = mbar_wait_warp<false>(&sm.mma_n, par, &sm.abort))) break;
+            if (!(ok = mbar_wait_warp(&sm.mma_n, par, &sm.abort))) break;
             tc_fence_after();
             {
                 float x[2][8];
@@ -863,53 +943,69 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                     tc_fence_before();
                     mbar_arrive(&sm.have_vs[half]);
                 }
+                if constexpr (FULL) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t hi[4], mid[4];
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t hi[4], mid[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) split_bf16x2(pack2(x[half][2 * i], x[half][2 * i + 1]), hi[i], mid[i]);
-                    const uint32_t at = lanes + d_part(2 * half + (q >> 1), 0) + (q & 1) * 4;
-                    tmem_store(at, hi);
-                    tmem_store(at + 8, mid);
+                        for (int i = 0; i < 4; ++i) split_bf16x2(pack2(x[half][2 * i], x[half][2 * i + 1]), hi[i], mid[i]);
+                        const uint32_t at = lanes + d_part(2 * half + (q >> 1), 0) + (q & 1) * 4;
+                        tmem_store(at, hi);
+                        tmem_store(at + 8, mid);
+                    }
                 }
             }
-            if (!(ok = mbar_wait_warp<false>(&sm.mma_o, par, &sm.abort))) break;
-            tc_fence_after();
-            {
-                float x[2][8];
-                tmem_load(lanes + kColO + 8 * q, x[0]);
-                tmem_load(lanes + kColO + 32 + 8 * q, x[1]);
-                tmem_wait_load();
+            if constexpr (FULL) {
+                if (!(ok = mbar_wait_warp(&sm.mma_o, par, &sm.abort))) break;
+                tc_fence_after();
+                {
+                    float x[2][8];
+                    tmem_load(lanes + kColO + 8 * q, x[0]);
+                    tmem_load(lanes + kColO + 32 + 8 * q, x[1]);
+                    tmem_wait_load();
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                    for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) oi[4 * half + i] = mul2(vec2(kQuery, half, i), pack2(x[half][2 * i], x[half][2 * i + 1]));
+                        for (int i = 0; i < 4; ++i) oi[4 * half + i] = mul2(vec2(kQuery, half, i), pack2(x[half][2 * i], x[half][2 * i + 1]));
+                }
             }
             gamma = f[kMisc * C - 8 * q];
-            tmem_wait_store();
-            tc_fence_before();
-            mbar_arrive(&sm.have_d);
+            if constexpr (FULL) {
+                tmem_wait_store();
+                tc_fence_before();
+                mbar_arrive(&sm.have_d);
+            }
         }
         // the last chunk's output and the final state
-        if (ok) ok = mbar_wait_warp<false>(&sm.mma_out, (chunks - 1) & 1, &sm.abort);
+        if (ok && FULL) {
+            ok = mbar_wait_warp(&sm.mma_out, (chunks - 1) & 1, &sm.abort);
+            if (ok) {
+                tc_fence_after();
+                finish(chunks - 1);
+            }
+        }
+        if (ok) ok = mbar_wait_warp(&sm.mma_delta[q >> 1], (chunks - 1) & 1, &sm.abort);
         if (ok) {
             tc_fence_after();
-            finish(chunks - 1);
             add_delta(gamma);
-            if (sp != nullptr && live) {
+            float *to = FULL ? (last ? pool : nullptr)
+                             : step_only ? in_segment(p.seg_step, slot, a.dim_k) : in_segment(p.seg_state, slot + 1, a.dim_v);
+            if (to != nullptr && live) {
 #pragma unroll
                 for (int k = 0; k < KH; k += 4) {
                     const int kk = q * KH + k;
                     float4 x;
                     unpack2(st[k / 2], x.x, x.y);
                     unpack2(st[k / 2 + 1], x.z, x.w);
-                    if constexpr (V) {
-                        if (kk < a.dim_k) *reinterpret_cast<float4 *>(sp + kk) = x;
+                    if (!FULL) {
+                        *reinterpret_cast<float4 *>(to + kk) = x;
+                    } else if constexpr (V) {
+                        if (kk < a.dim_k) *reinterpret_cast<float4 *>(to + kk) = x;
                     } else {
-                        if (kk < a.dim_k) sp[kk * a.s_stride_k] = x.x;
-                        if (kk + 1 < a.dim_k) sp[(kk + 1) * a.s_stride_k] = x.y;
-                        if (kk + 2 < a.dim_k) sp[(kk + 2) * a.s_stride_k] = x.z;
-                        if (kk + 3 < a.dim_k) sp[(kk + 3) * a.s_stride_k] = x.w;
+                        if (kk < a.dim_k) to[kk * a.s_stride_k] = x.x;
+                        if (kk + 1 < a.dim_k) to[(kk + 1) * a.s_stride_k] = x.y;
+                        if (kk + 2 < a.dim_k) to[(kk + 2) * a.s_stride_k] = x.z;
+                        if (kk + 3 < a.dim_k) to[(kk + 3) * a.s_stride_k] = x.w;
                     }
                 }
             }
@@ -920,12 +1016,112 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     if (warp == kIssueWarp) tmem_free<512>(tmem);
 }
 
+// ------------------------------------------------------------------- join ----
+
+constexpr int kJoinThreads = 128, kJoinRows = 4;  // rows of S a warp carries
+
+// First states of the segments from the third on: S_{j+1} = S_j M_j + N_j, whose N the first pass left in S_{j+1}'s place.
+// Rows are independent: a warp takes 4 of them through a whole sequence, 4 columns a lane, S by shuffles, while the next M
+// is on its way to shared memory.  In fp32 throughout.
+template <int PANELS>
+__global__ void __launch_bounds__(kJoinThreads) gdr_join_kernel(const __grid_constant__ FwdArgs p) {
+    constexpr int kLdS = 64 * PANELS;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    float *steps = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));  // two of M
+    __shared__ uint64_t full[2];
+    __shared__ int abort;
+    const ccv_gdr_args &a = p.a;
+    const int lane = threadIdx.x & 31;
+    const int groups = (a.dim_v + kJoinRows * 4 - 1) / (kJoinRows * 4);
+    const int first = (blockIdx.x % groups) * kJoinRows * 4, row0 = first + (threadIdx.x >> 5) * kJoinRows;
+    const int bh = blockIdx.x / groups;
+    const int h = bh % a.num_v_heads, seq = bh / a.num_v_heads;
+    wait_prior_grid();
+    const int s = p.query_start_loc[seq], e = p.query_start_loc[seq + 1];
+    const int line = p.cache_indices != nullptr ? p.cache_indices[seq] : seq;
+    if (!sequence_ok(s, e, p.total_tokens) || (a.state != nullptr && line != a.pad_slot_id && (line < 0 || line >= a.num_lines))) {
+        if (threadIdx.x == 0 && first == 0 && h == 0) count_error(p.err_count);  // the passes cannot tell whose block would
+        return;
+    }
+    const int unit = p.seg_chunks * C;
+    const int segments = (e - s + unit - 1) / unit, slot0 = first_slot(s, seq, unit);
+    if (line == a.pad_slot_id || segments < 3) return;
+
+    if (threadIdx.x == 0) {
+        abort = 0;
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    const uint32_t bytes = a.dim_k * kLdS * 4;
+    auto fetch = [&](int j) {  // M of segment j, by one thread
+        mbar_expect_tx(&full[j & 1], bytes);
+        bulk_load(steps + (j & 1) * kLdS * kLdS, p.seg_step + (static_cast<int64_t>(slot0 + j) * a.num_v_heads + h) * a.dim_k * kLdS, bytes,
+                  &full[j & 1]);
+    };
+    if (threadIdx.x == 0) fetch(1);
+    const int column = lane * 4 % kLdS;  // with one panel the upper lanes repeat the lower ones
+    auto row_at = [&](int j, int r) {
+        return p.seg_state + ((static_cast<int64_t>(slot0 + j) * a.num_v_heads + h) * a.dim_v + min(row0 + r, a.dim_v - 1)) * kLdS + column;
+    };
+    float4 x[kJoinRows];
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) x[r] = *reinterpret_cast<const float4 *>(row_at(1, r));
+    for (int j = 1; j + 1 < segments; ++j) {
+        if (threadIdx.x == 0 && j + 2 < segments) fetch(j + 1);
+        float4 y[kJoinRows];
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) y[r] = *reinterpret_cast<const float4 *>(row_at(j + 1, r));
+        const bool ok = mbar_wait_warp(&full[j & 1], ((j - 1) >> 1) & 1, &abort);
+        const float *m = steps + (j & 1) * kLdS * kLdS + column;
+#pragma unroll 2
+        for (int k0 = 0; k0 < kLdS; k0 += 4) {
+            float4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const float4 *>(m + min(k0 + k, a.dim_k - 1) * kLdS);  // S is 0 past dim_k
+#pragma unroll
+            for (int r = 0; r < kJoinRows; ++r) {
+                const float s4[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float v = __shfl_sync(kFullMask, s4[k], k0 >> 2);
+                    y[r].x = fmaf(v, w[k].x, y[r].x);
+                    y[r].y = fmaf(v, w[k].y, y[r].y);
+                    y[r].z = fmaf(v, w[k].z, y[r].z);
+                    y[r].w = fmaf(v, w[k].w, y[r].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+            x[r] = y[r];
+            if (row0 + r < a.dim_v) *reinterpret_cast<float4 *>(row_at(j + 1, r)) = y[r];
+        }
+        if (!__syncthreads_and(ok)) {  // also: this M may be overwritten
+            if (threadIdx.x == 0) {
+                count_error(p.err_count);
+                int quiet = 0;
+                if (j + 2 < segments) mbar_wait(&full[(j + 1) & 1], (j >> 1) & 1, &quiet);
+            }
+            return;
+        }
+    }
+}
+template <int PANELS>
+constexpr size_t join_smem() { return 128 + 2 * (64 * PANELS) * (64 * PANELS) * 4; }
+
 // ------------------------------------------------------------------- host ----
 
+int64_t slot_count(int total_tokens, int batch) { return static_cast<int64_t>(total_tokens / C) + batch; }
+int64_t segment_slots(int total_tokens, int batch, int seg_chunks) {
+    return static_cast<int64_t>(total_tokens) / (static_cast<int64_t>(seg_chunks) * C) + batch;
+}
+
 template <int PANELS>
-constexpr size_t prep_smem() { return 1024 + kMatrixBytes + sizeof(PrepSmem); }
+constexpr size_t prep_smem() { return kMatrixBytes + sizeof(PrepSmem); }
 template <int PANELS>
-constexpr size_t chunk_smem() { return 1024 + kStages * Stage<PANELS>::bytes + 2 * kTile + sizeof(ChunkSmem); }
+constexpr size_t chunk_smem() { return kStages * Stage<PANELS>::bytes + 2 * kTile + sizeof(ChunkSmem); }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                  const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -957,27 +1153,44 @@ bool encode_map(CUtensorMap *map, const ccv_heads_view &v, int dim, int heads, i
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int PANELS, bool FULL, bool VS, bool VIO>
+int launch_chunks(const FwdArgs &p, const FwdMaps &maps, int64_t units, cudaStream_t stream) {
+    int dev = 0;
+    current_device_sms(&dev);
+    cudaError_t err;
+    if (resident_blocks<gdr_chunk_kernel<PANELS, FULL, VS, VIO>>(kChunkThreads, chunk_smem<PANELS>(), dev, &err) == 0)
+        return static_cast<int>(err);
+    const int slices = (p.a.dim_v + 127) / 128;
+    const int64_t blocks = units * p.a.num_v_heads * (FULL ? slices : slices + 1);
+    if (blocks > 0x7fffffff) return CCV_ERR_SIZE;
+    return launch_pdl(gdr_chunk_kernel<PANELS, FULL, VS, VIO>, dim3(static_cast<unsigned>(blocks)), dim3(kChunkThreads),
+                      chunk_smem<PANELS>(), stream, p, maps, slices);
+}
+
 template <int PANELS, bool VS, bool VIO>
 int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
     int dev = 0;
     current_device_sms(&dev);
     cudaError_t err;
-    if (resident_blocks<gdr_prep_kernel<PANELS, VIO>>(kPrepThreads, prep_smem<PANELS>(), dev, &err) == 0 ||
-        resident_blocks<gdr_chunk_kernel<PANELS, VS, VIO>>(kChunkThreads, chunk_smem<PANELS>(), dev, &err) == 0)
-        return static_cast<int>(err);
+    if (resident_blocks<gdr_prep_kernel<PANELS, VIO>>(kPrepThreads, prep_smem<PANELS>(), dev, &err) == 0) return static_cast<int>(err);
     const int64_t prep = static_cast<int64_t>(p.slots) * p.a.num_k_heads;
-    const int slices = (p.a.dim_v + 127) / 128;
-    const int64_t blocks = static_cast<int64_t>(p.batch) * p.a.num_v_heads * slices;
-    if (prep > 0x7fffffff || blocks > 0x7fffffff) return CCV_ERR_SIZE;
-    const int status = launch_pdl(gdr_prep_kernel<PANELS, VIO>, dim3(static_cast<unsigned>(prep)), dim3(kPrepThreads),
-                                  prep_smem<PANELS>(), stream, p);
-    if (status != CCV_OK) return status;
+    const int64_t rows = static_cast<int64_t>(p.batch) * p.a.num_v_heads * ((p.a.dim_v + 15) / 16);
+    if (prep > 0x7fffffff || rows > 0x7fffffff) return CCV_ERR_SIZE;
     FwdMaps maps;
     maps.use = VIO && encoder() != nullptr && encode_map(&maps.q, p.a.q, p.a.dim_k, p.a.num_k_heads, p.total_tokens) &&
                encode_map(&maps.k, p.a.k, p.a.dim_k, p.a.num_k_heads, p.total_tokens) &&
                encode_map(&maps.v, p.a.v, p.a.dim_v, p.a.num_v_heads, p.total_tokens);
-    return launch_pdl(gdr_chunk_kernel<PANELS, VS, VIO>, dim3(static_cast<unsigned>(blocks)), dim3(kChunkThreads),
-                      chunk_smem<PANELS>(), stream, p, maps, slices);
+    int status = launch_pdl(gdr_prep_kernel<PANELS, VIO>, dim3(static_cast<unsigned>(prep)), dim3(kPrepThreads),
+                            prep_smem<PANELS>(), stream, p);
+    if (status != CCV_OK) return status;
+    if (p.seg_chunks == 0) return launch_chunks<PANELS, true, VS, VIO>(p, maps, p.batch, stream);
+    const int64_t segments = segment_slots(p.total_tokens, p.batch, p.seg_chunks);
+    status = launch_chunks<PANELS, false, VS, VIO>(p, maps, segments, stream);
+    if (status != CCV_OK) return status;
+    if (resident_blocks<gdr_join_kernel<PANELS>>(kJoinThreads, join_smem<PANELS>(), dev, &err) == 0) return static_cast<int>(err);
+    status = launch_pdl(gdr_join_kernel<PANELS>, dim3(static_cast<unsigned>(rows)), dim3(kJoinThreads), join_smem<PANELS>(), stream, p);
+    if (status != CCV_OK) return status;
+    return launch_chunks<PANELS, true, VS, VIO>(p, maps, segments, stream);
 }
 
 template <int PANELS>
@@ -997,7 +1210,31 @@ bool use_chunked(const ccv_gdr_args &a, int batch, int total) {
     return true;
 }
 
-int64_t slot_count(int total_tokens, int batch) { return static_cast<int64_t>(total_tokens / C) + batch; }
+// Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device).  In
+// chunk times of a block (3.2 us): the first pass takes 0.85 of one a chunk, a join 0.6 a segment, and the two launches more
+// take 6.  Each pass runs in waves of one block an SM.
+int segment_chunks(int total_tokens, int batch, int num_v_heads, int dim_v) {
+    constexpr int kSms = 152;
+    const int chunks = static_cast<int>((static_cast<int64_t>(total_tokens) + batch * C - 1) / (static_cast<int64_t>(batch) * C));
+    const int slices = (dim_v + 127) / 128;
+    const int64_t heads = static_cast<int64_t>(batch) * num_v_heads;
+    auto waves = [](int64_t blocks) { return static_cast<double>((blocks + kSms - 1) / kSms); };
+    const char *forced = std::getenv("CCV_GDR_SEGMENT");  // chunks of a segment (for testing and tuning)
+    if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;
+    double best = waves(heads * slices) * chunks;
+    int choice = 0;
+    for (int n = 3; n <= 64 && n <= chunks; ++n) {
+        const int length = (chunks + n - 1) / n;
+        const double cost = 6 + waves(heads * ((n - 1) * slices + n - 2)) * length * 0.85 + (n - 2) * 0.6 + waves(heads * n * slices) * length;
+        if (cost < best) {
+            best = cost;
+            choice = length;
+        }
+    }
+    return choice;
+}
+
+int64_t heads_bytes(int total_tokens, int batch, int num_v_heads) { return slot_count(total_tokens, batch) * num_v_heads * kHeadBytes; }
 
 }  // namespace
 }  // namespace ccv
@@ -1005,7 +1242,11 @@ int64_t slot_count(int total_tokens, int batch) { return static_cast<int64_t>(to
 extern "C" int64_t gdr_fwd_workspace(int total_tokens, int batch, int num_k_heads, int num_v_heads, int dim_k, int dim_v) {
     using namespace ccv;
     if (total_tokens <= 0 || batch <= 0 || num_k_heads <= 0 || num_v_heads <= 0 || dim_k <= 0 || dim_v <= 0) return 0;
-    return chunked_dims(dim_k) ? slot_count(total_tokens, batch) * num_v_heads * kHeadBytes : 0;
+    if (!chunked_dims(dim_k)) return 0;
+    int64_t bytes = heads_bytes(total_tokens, batch, num_v_heads);
+    if (const int seg = segment_chunks(total_tokens, batch, num_v_heads, dim_v))
+        bytes += segment_slots(total_tokens, batch, seg) * num_v_heads * (dim_v + dim_k) * (dim_k <= 64 ? 256 : 512);
+    return bytes;
 }
 
 extern "C" int gdr_fwd(const ccv_gdr_args *args, const int32_t *query_start_loc, int batch, const int32_t *cache_indices,
@@ -1028,9 +1269,12 @@ extern "C" int gdr_fwd(const ccv_gdr_args *args, const int32_t *query_start_loc,
         return gdr_launch_recurrent(a, rows, stream);
     }
     const int64_t slots = slot_count(total_tokens, batch);
-    if (slots > 0x7fffffff) return CCV_ERR_SIZE;
-    const FwdArgs p{a, query_start_loc, cache_indices, has_initial_state, batch, total_tokens, static_cast<int>(slots),
-                    static_cast<uint8_t *>(workspace), err_count};
+    FwdArgs p{a, query_start_loc, cache_indices, has_initial_state, batch, total_tokens, static_cast<int>(slots),
+              static_cast<uint8_t *>(workspace), err_count, segment_chunks(total_tokens, batch, a.num_v_heads, a.dim_v), nullptr, nullptr};
+    if (p.seg_chunks > 0) {
+        p.seg_state = reinterpret_cast<float *>(p.heads + heads_bytes(total_tokens, batch, a.num_v_heads));
+        p.seg_step = p.seg_state + segment_slots(total_tokens, batch, p.seg_chunks) * a.num_v_heads * a.dim_v * (a.dim_k <= 64 ? 64 : 128);
+    }
     auto vec = [](const ccv_heads_view &v) {
         return aligned16(v.data) && v.stride_dim == 1 && v.stride_tok % 8 == 0 && v.stride_head % 8 == 0;
     };

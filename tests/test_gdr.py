@@ -20,9 +20,12 @@ def ccv():
     return module
 
 
-@pytest.fixture(params=["chunked", "recurrent"])
+@pytest.fixture(params=["chunked", "recurrent", "segments1", "segments2"])
 def path(request, monkeypatch):
-    monkeypatch.setenv("CCV_GDR_PATH", request.param)
+    """The chunked form with sequences whole or cut into segments of 1 or 2 chunks, and the recurrent form."""
+    cut = request.param.startswith("segments")
+    monkeypatch.setenv("CCV_GDR_PATH", "chunked" if cut else request.param)
+    monkeypatch.setenv("CCV_GDR_SEGMENT", request.param[-1] if cut else "0")
     return request.param
 
 
@@ -341,6 +344,13 @@ def test_fwd_is_deterministic(ccv, path):
             first = out, state
         assert_bits(out, first[0])
         assert torch.equal(state, first[1])
+
+
+def test_fwd_cut_by_itself(ccv):
+    """A long prompt with few heads, which the host cuts into segments without being told to."""
+    d, g = inputs(2500, 1, 1, 128, 128, 22, raw=True)
+    pool = 0.3 * torch.randn(3, 1, 128, 128, generator=g)
+    check_fwd(ccv, d, pool, [2300, 0, 200], lines=[2, 1, 0], init=[True, True, False])
 
 
 def test_fwd_split_is_continuation(ccv):
