@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
             const float ghi = sm.ghi[side][i], glo = sm.glo[side][i], beta = sm.beta[side][i];
             const float decay = ex2(ghi + glo), rk = sm.rk[i];
             vec[kBeta * C + i] = beta;
-            vec[kKey * C + i] = -beta * rk * decay;
+                        vec[kKey * C + i] = -beta * rk * decay;
             vec[kState * C + i] = ex2((sm.ghi[side][C - 1] - ghi) + (sm.glo[side][C - 1] - glo)) * rk;
             vec[kQuery * C + i] = sm.rq[i] * decay;
             if (i == 0) vec[kMisc * C] = ex2(sm.ghi[side][C - 1] + sm.glo[side][C - 1]);
@@ -468,10 +468,11 @@ static_assert(kCompute * kComputeRegs + 128 * kOtherRegs <= kChunkThreads * 96, 
 // Columns of tensor memory.  A thread overwrites only columns that it alone reads, or that a barrier says are free.
 enum : uint32_t {
     kColS = 0,       // 192: S^T in 3 parts, and in the same columns what the chunk adds to S^T (see s_part)
-    kColP = 192,     // 64: S^T k^T, then d in 2 parts
+    kColP = 192,     // 64: S^T k^T
     kColO = 256,     // 64: S^T q^T, then d P^T
     kColR = 320,     // 96: R in 3 parts, then the decayed d in 3 parts
-    kColN = 416,     // 64: d
+    kColN = 416,     // 64: d; then, 8 of every 16, its second part
+    kColD = 480,     // 32: its first part
 };
 // Warpgroup q holds 16 PANELS keys of every row of S.  They have 24 PANELS columns, 8 PANELS for each part (a column is two
 // bf16 values); what is added to them comes in the last 16 PANELS of those where q is even and the first where it is odd, so
@@ -483,7 +484,9 @@ __device__ __forceinline__ constexpr uint32_t s_added(int q) { return s_part<PAN
 // It also holds tokens 8 q .. + 7 and 32 + 8 q .. + 7 of every row of R and d, so that two warpgroups make up the 16 tokens of
 // an inner step of the tensor cores, and the steps of tokens 0 .. 31 can run while the others are prepared.
 __device__ __forceinline__ constexpr uint32_t r_part(int step, int part) { return kColR + step * 24 + part * 8; }
-__device__ __forceinline__ constexpr uint32_t d_part(int step, int part) { return kColP + step * 16 + part * 8; }
+// The second part of d goes into the middle 8 of the step's 16 columns of d: the upper half of the even warpgroup's own and
+// the lower half of the odd one's.
+__device__ __forceinline__ constexpr uint32_t d_part(int step, int part) { return part ? kColN + step * 16 + 4 : kColD + step * 8; }
 
 template <int PANELS>
 struct Stage {
@@ -603,7 +606,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 const uint32_t kq = smem0 + (c % kStages) * (St::bytes / 16);
                 const uint32_t head = kq + St::head / 16;
                 if (!mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort)) break;
-                if (FULL && c > 0 && !mbar_wait_warp(&sm.mma_out, par ^ 1, &sm.abort)) break;  // it read d where P goes
                 bool ok = true;
                 // S^T k^T, three parts of S; the keys are exact
 #pragma unroll
@@ -621,6 +623,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 }
                 if (!ok) break;
                 mma_commit(&sm.mma_p, el);
+                if (FULL && c > 0 && !mbar_wait_warp(&sm.mma_out, par ^ 1, &sm.abort)) break;  // it reads d's second part
                 // d^T = R^T T^T: the six products of parts above 2^-24, for tokens 0 .. 31 of the sum, then the others
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -869,7 +872,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             // b v of this thread's tokens
             if (!(ok = mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
             const float *f = reinterpret_cast<const float *>(stage(c) + St::head + kVec) + 8 * q;
-            auto vec2 = [&](int which, int half, int i) { return *reinterpret_cast<const f32x2 *>(f + which * C + 32 * half + 2 * i); };
+            // 4 of a token's factors, as pairs
+            auto vec4 = [&](int which, int half, int i) { return *reinterpret_cast<const ulonglong2 *>(f + which * C + 32 * half + 4 * i); };
             f32x2 vb[8];
             if (step_only) {
 #pragma unroll
@@ -880,10 +884,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        const ulonglong2 beta = vec4(kBeta, half, i / 2);
                         auto at = [&](int r) {  // row 8 q + r of the half, whose place within 8 rows is r
                             return bf16_bits(*reinterpret_cast<const uint16_t *>(v + (32 * half + r) * 128 + ((((d & 63) >> 3) ^ r) << 4)));
                         };
-                        vb[4 * half + i] = mul2(pack2(at(2 * i), at(2 * i + 1)), vec2(kBeta, half, i));
+                        vb[4 * half + i] = mul2(pack2(at(2 * i), at(2 * i + 1)), (i & 1 ? beta.y : beta.x));
                     }
             }
 
@@ -899,8 +904,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 for (int half = 0; half < 2; ++half) {
                     uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        split_bf16x3(fma2(vec2(kKey, half, i), pack2(x[half][2 * i], x[half][2 * i + 1]), vb[4 * half + i]), hi[i], mid[i], lo[i]);
+                    for (int i = 0; i < 4; i += 2) {
+                        const ulonglong2 key = vec4(kKey, half, i / 2);
+                        const float *y = &x[half][2 * i];
+                        split_bf16x3(fma2(key.x, pack2(y[0], y[1]), vb[4 * half + i]), hi[i], mid[i], lo[i]);
+                        split_bf16x3(fma2(key.y, pack2(y[2], y[3]), vb[4 * half + i + 1]), hi[i + 1], mid[i + 1], lo[i + 1]);
+                    }
                     const uint32_t at = lanes + r_part(2 * half + (q >> 1), 0) + (q & 1) * 4;
                     tmem_store(at, hi);
                     tmem_store(at + 8, mid);
@@ -933,8 +942,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 for (int half = 0; half < 2; ++half) {
                     uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        split_bf16x3(mul2(vec2(kState, half, i), pack2(x[half][2 * i], x[half][2 * i + 1])), hi[i], mid[i], lo[i]);
+                    for (int i = 0; i < 4; i += 2) {
+                        const ulonglong2 left = vec4(kState, half, i / 2);
+                        const float *y = &x[half][2 * i];
+                        split_bf16x3(mul2(left.x, pack2(y[0], y[1])), hi[i], mid[i], lo[i]);
+                        split_bf16x3(mul2(left.y, pack2(y[2], y[3])), hi[i + 1], mid[i + 1], lo[i + 1]);
+                    }
                     const uint32_t at = lanes + r_part(2 * half + (q >> 1), 0) + (q & 1) * 4;
                     tmem_store(at, hi);
                     tmem_store(at + 8, mid);
@@ -949,9 +962,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                         uint32_t hi[4], mid[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) split_bf16x2(pack2(x[half][2 * i], x[half][2 * i + 1]), hi[i], mid[i]);
-                        const uint32_t at = lanes + d_part(2 * half + (q >> 1), 0) + (q & 1) * 4;
-                        tmem_store(at, hi);
-                        tmem_store(at + 8, mid);
+                        tmem_store(lanes + d_part(2 * half + (q >> 1), 0) + (q & 1) * 4, hi);
+                        tmem_store(lanes + d_part(2 * half + (q >> 1), 1) + (q & 1) * 4, mid);
                     }
                 }
             }
@@ -966,7 +978,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) oi[4 * half + i] = mul2(vec2(kQuery, half, i), pack2(x[half][2 * i], x[half][2 * i + 1]));
+                        for (int i = 0; i < 4; i += 2) {
+                            const ulonglong2 left = vec4(kQuery, half, i / 2);
+                            const float *y = &x[half][2 * i];
+                            oi[4 * half + i] = mul2(left.x, pack2(y[0], y[1]));
+                            oi[4 * half + i + 1] = mul2(left.y, pack2(y[2], y[3]));
+                        }
                 }
             }
             gamma = f[kMisc * C - 8 * q];
