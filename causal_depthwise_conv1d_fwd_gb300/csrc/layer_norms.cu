@@ -4,7 +4,6 @@
 // Both read each element once, keep the row in registers in fp32, reduce it, and write once: 6 bytes an element for the
 // first, 8 to 14 for the second, so HBM bounds them at any size that fills the card and one launch's latency below.
 // A row belongs to LPR lanes: within a warp the reductions are shuffles; longer rows reduce over the block's warps.
-#include <cstdlib>
 #include "ccv_common.cuh"
 #include "ccv_layer.h"
 
@@ -54,7 +53,7 @@ template <int VEC>
 __device__ __forceinline__ void store_row(uint16_t *p, int64_t stride, int d, int dim, const float (&f)[VEC]) {
     Raw<VEC> r;
     r.from_float(f);
-    if (d < dim) store_plain<VEC>(p + (VEC == 8 ? d : d * stride), r);
+    if (d < dim) store_stream<VEC>(p + (VEC == 8 ? d : d * stride), r);
 }
 template <int VEC>
 __device__ __forceinline__ void store_row(float *p, int64_t stride, int d, int dim, const float (&f)[VEC]) {
@@ -82,8 +81,8 @@ struct GatedArgs {
     int activation, before;
 };
 
-// R: rows a thread has in flight at once.  One row of 128 values is 64 bytes a lane, x and gate together, which leaves HBM
-// waiting on block turnover: 16384 x 32 rows take GATED_R1 us with 1 row a thread and GATED_R4 with 4.
+// R: rows a thread has in flight at once.  One row of 128 values is 32 bytes a lane, x and gate together; with two, 16384 x 32
+// rows take 67 us (6.0 TB/s) instead of 75, with four 73 (registers).
 template <int LPR, int VEC, int NV, int R>
 __global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) gated_rms_norm_kernel(const __grid_constant__ GatedArgs a) {
     __shared__ float warp_sums[32];
@@ -99,7 +98,11 @@ __global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) gated
     for (int r = 0; r < R; ++r) {
         const int64_t row = first + r * kRows;
         const bool live = row < a.rows;
-        const int64_t tok = live ? row / a.heads : 0, head = live ? row % a.heads : 0;
+        unsigned tok = live ? static_cast<unsigned>(row) : 0u, head = 0;
+        if (a.heads > 1) {
+            head = tok % a.heads;
+            tok /= a.heads;
+        }
         const int dim = live ? a.dim : 0;
         const uint16_t *xp = static_cast<const uint16_t *>(a.x.data) + tok * a.x.stride_tok + head * a.x.stride_head;
         const uint16_t *gp = static_cast<const uint16_t *>(a.gate.data) + tok * a.gate.stride_tok + head * a.gate.stride_head;
@@ -246,14 +249,11 @@ struct GatedLaunch {
     cudaStream_t stream;
     template <int LPR, int VEC, int NV>
     int operator()() const {
-        // Four rows a thread once there are enough rows for every SM's threads to have four: below that one row each
-        // spreads the call over more SMs.
+        // Two rows a thread once there are enough rows for every SM's threads to have two: below that one row each spreads
+        // the call over more SMs.
         if constexpr (LPR <= 32 && VEC == 8 && NV == 1) {
-            if (std::getenv("GN_R2") && a.rows * LPR >= 4ll * 2048 * current_device_sms())
+            if (a.rows * LPR >= 2ll * 2048 * current_device_sms())
                 return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV, 2>, dim3(row_blocks((a.rows + 1) / 2, LPR)),
-                                  dim3(kNormThreads), 0, stream, a);
-            if (std::getenv("GN_R4") && a.rows * LPR >= 4ll * 2048 * current_device_sms())
-                return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV, 4>, dim3(row_blocks((a.rows + 3) / 4, LPR)),
                                   dim3(kNormThreads), 0, stream, a);
         }
         return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV, 1>, dim3(row_blocks(a.rows, LPR)),
@@ -310,7 +310,14 @@ extern "C" int gated_rms_norm(const ccv_heads_view *x, const ccv_heads_view *gat
     if (rows > 0x7fffffff) return CCV_ERR_SIZE;
     bool vec = dim % 8 == 0 && aligned16(weight);
     for (const ccv_heads_view *v : {x, gate, out}) vec = vec && vec_view(v->data, v->stride_tok, v->stride_head, v->stride_dim);
-    const GatedArgs a{*x, *gate, *out, static_cast<const uint16_t *>(weight), rows, heads, dim, eps, activation, norm_before_gate};
+    // Heads that follow each other like tokens do are rows of one axis: no division in the kernel.
+    GatedArgs a{*x, *gate, *out, static_cast<const uint16_t *>(weight), rows, heads, dim, eps, activation, norm_before_gate};
+    bool flat = true;
+    for (const ccv_heads_view *v : {x, gate, out}) flat = flat && v->stride_tok == heads * v->stride_head;
+    if (flat) {
+        a.heads = 1;
+        for (ccv_heads_view *v : {&a.x, &a.gate, &a.out}) v->stride_tok = v->stride_head;
+    }
     return for_row(dim, vec, GatedLaunch{a, stream});
 }
 

@@ -12,8 +12,10 @@ namespace ccv {
 namespace {
 
 constexpr int kVerifyThreads = 256;
-constexpr int kVectors = 4;                               // vectors of 8 logits a thread holds
-constexpr int kSplit = kVerifyThreads * kVectors * 8;     // a block's share of a row: 8192 logits
+constexpr int kStep = kVerifyThreads * 8;  // logits of one pass of a block, 8 a thread
+constexpr int kVectors = 4;                // passes that a thread has in flight
+constexpr int kShare = kVectors * kStep;   // a block's share of a row in the draw, and in the statistics of small calls
+constexpr int kLongShare = 2 * kShare;     // in the statistics of large ones
 
 struct VerifyArgs {
     const void *logits;
@@ -29,9 +31,11 @@ struct VerifyArgs {
     const float *noise;
     int64_t nb;
     int32_t *out_tokens, *num_accepted;
-    int batch, drafts, vocab, splits;
+    int batch, drafts, vocab;
+    int share, splits;  // logits of a block of the statistics, and such blocks a row
+    int shares;         // blocks a row of the draw
     float4 *stats;     // (batch, drafts + 1, splits): maximum, its index's bits, sum of exponentials
-    float2 *best;      // (batch, splits): a share's best score and its index's bits
+    float2 *best;      // (batch, shares): a share's best score and its index's bits
     unsigned *done;    // (batch): shares finished
     int *err_count;
 };
@@ -41,23 +45,44 @@ __device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINIT
 __device__ __forceinline__ float widen(uint16_t x) { return bf16_bits(x); }
 __device__ __forceinline__ float widen(float x) { return x; }
 
-// 8 logits from row[i..], of which those in [0, end) are real; the others come back as -inf.  row + i is on a 16-byte
-// boundary.
+// 8 logits from row[i..] as they are in memory, of which those in [0, end) are real; the others are -inf.  row + i is on a
+// 16-byte boundary.
+template <typename T> struct Logits;
+template <> struct Logits<uint16_t> {
+    Raw<8> r;
+    __device__ __forceinline__ void load(const uint16_t *row, int i, int end) {
+        if (i >= 0 && i + 8 <= end) {
+            r.v = *reinterpret_cast<const uint4 *>(row + i);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) r.set_elem(k, i + k >= 0 && i + k < end ? row[i + k] : uint16_t(0xff80));
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const { r.to_float(f); }
+};
+template <> struct Logits<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *row, int i, int end) {
+        if (i >= 0 && i + 8 <= end) {
+            a = *reinterpret_cast<const float4 *>(row + i);
+            b = *reinterpret_cast<const float4 *>(row + i + 4);
+        } else {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = i + k >= 0 && i + k < end ? row[i + k] : -INFINITY;
+            a = make_float4(f[0], f[1], f[2], f[3]);
+            b = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
 template <typename T>
 __device__ __forceinline__ void load8(const T *row, int i, int end, float (&f)[8]) {
-    if (i >= 0 && i + 8 <= end) {
-        if constexpr (sizeof(T) == 2) {
-            Raw<8> r;
-            r.v = *reinterpret_cast<const uint4 *>(row + i);
-            r.to_float(f);
-        } else {
-            const float4 x = *reinterpret_cast<const float4 *>(row + i), y = *reinterpret_cast<const float4 *>(row + i + 4);
-            f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w; f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = i + k >= 0 && i + k < end ? widen(row[i + k]) : -INFINITY;
-    }
+    Logits<T> l;
+    l.load(row, i, end);
+    l.get(f);
 }
 __device__ __forceinline__ void load8_plain(const float *row, int i, int end, bool aligned, float (&f)[8]) {
     if (aligned && i + 8 <= end) {
@@ -112,11 +137,15 @@ __device__ __forceinline__ float rate_of(const VerifyArgs &a, int b) {
 }
 
 // Maximum, its first index and the sum of exponentials of one share of one position.  Rows may start at any element: the
-// shares count from the 16-byte boundary at or before the row's start, so that all but the edges are whole vectors.
+// shares count from the 16-byte boundary at or before the row's start, so that all but the edges are whole vectors.  Each
+// thread keeps a running maximum and sum, one more exponential for every 8 logits, so nothing waits for the block until the
+// end and the next vectors are always on their way: 64 x 5 rows of 131072 bf16 logits take 23 us (3.6 TB/s; the exponentials
+// and the arithmetic around them are the bound) against 33 with a block-wide maximum first.
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_stats_kernel(const __grid_constant__ VerifyArgs a) {
-    __shared__ float sv[32];
-    __shared__ int si[32];
+__global__ void __launch_bounds__(kVerifyThreads, 5) verify_stats_kernel(const __grid_constant__ VerifyArgs a) {
+    constexpr int kWarps = kVerifyThreads / 32;
+    __shared__ float sv[kWarps], ss[kWarps];
+    __shared__ int si[kWarps];
     wait_prior_grid();
     release_next_grid();
     const int split = blockIdx.x % a.splits, row = blockIdx.x / a.splits;
@@ -127,64 +156,83 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_stats_kernel(const __gr
     const float rate = rate_of(a, b);
     const T *logits = static_cast<const T *>(a.logits) + b * a.tb + pos * a.tp;
     const int before = static_cast<int>(reinterpret_cast<uintptr_t>(logits) % 16 / sizeof(T));
-    const int start = split * kSplit - before;
-    float x[kVectors][8];
-#pragma unroll
-    for (int j = 0; j < kVectors; ++j) load8(logits, start + (j * kVerifyThreads + threadIdx.x) * 8, a.vocab, x[j]);
-    float best = -INFINITY;
-    bool odd = false;  // a NaN or +inf among them: then all are cleaned first
-#pragma unroll
-    for (int j = 0; j < kVectors; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            odd |= !(x[j][k] < INFINITY);
-            best = fmaxf(best, x[j][k]);
+    const int first = split * a.share - before, end = min(a.vocab, first + a.share);
+    float best = -INFINITY, sum = 0.0f;
+    int where = 0;  // the vector that holds `best`
+    auto take = [&](const float (&x)[8], int at) {
+        float m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        if (m > best) {
+            if (rate > 0.0f) sum *= Weigh(rate, m)(best);
+            best = m;
+            where = at;
         }
-    if (__syncthreads_or(odd)) {
-        best = -INFINITY;
+        if (rate > 0.0f) {
+            const Weigh weigh(rate, best);
+            float part[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < kVectors; ++j)
+            for (int k = 0; k < 8; ++k) part[k & 1] += weigh(x[k]);
+            sum += part[0] + part[1];
+        }
+    };
+    const int mine = first + static_cast<int>(threadIdx.x) * 8;
+    Logits<T> now[kVectors], next[kVectors];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                x[j][k] = clean(x[j][k]);
-                best = fmaxf(best, x[j][k]);
-            }
+    for (int j = 0; j < kVectors; ++j) now[j].load(logits, mine + j * kStep, end);
+    for (int v0 = mine; v0 < end; v0 += kVectors * kStep) {
+        const int v1 = v0 + kVectors * kStep;
+        if (v1 < end) {
+#pragma unroll
+            for (int j = 0; j < kVectors; ++j) next[j].load(logits, v1 + j * kStep, end);
+        }
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j) {
+            float x[8];
+            now[j].get(x);
+            take(x, v0 + j * kStep);
+            now[j] = next[j];
+        }
     }
-    const float mine = best;
+    if (!(sum < INFINITY) || best == INFINITY) {  // a NaN or +inf among them: once more, cleaned
+        best = -INFINITY;
+        sum = 0.0f;
+        for (int v0 = mine; v0 < end; v0 += kStep) {
+            float x[8];
+            load8(logits, v0, end, x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = clean(x[k]);
+            take(x, v0);
+        }
+    }
+    int index = INT32_MAX;
+    const float top = best;
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) best = fmaxf(best, __shfl_xor_sync(kFullMask, best, m));
-    if (threadIdx.x % 32 == 0) sv[threadIdx.x / 32] = best;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (lane == 0) sv[warp] = best;
     __syncthreads();
-    best = sv[threadIdx.x % (kVerifyThreads / 32)];
+    best = sv[lane % kWarps];
 #pragma unroll
-    for (int m = kVerifyThreads / 64; m > 0; m >>= 1) best = fmaxf(best, __shfl_xor_sync(kFullMask, best, m));
-    int index = INT32_MAX;
-    if (mine == best) {
+    for (int m = kWarps / 2; m > 0; m >>= 1) best = fmaxf(best, __shfl_xor_sync(kFullMask, best, m));
+    if (top == best && best > -INFINITY) {
+        float x[8];
+        load8(logits, where, end, x);
 #pragma unroll
-        for (int j = kVectors - 1; j >= 0; --j)
-#pragma unroll
-            for (int k = 7; k >= 0; --k)
-                if (x[j][k] == best) index = start + (j * kVerifyThreads + threadIdx.x) * 8 + k;
+        for (int k = 7; k >= 0; --k)
+            if (clean(x[k]) == best) index = where + k;
     }
-    float sum = 0.0f;
-    if (rate > 0.0f) {
-        const Weigh weigh(rate, best);
-#pragma unroll
-        for (int j = 0; j < kVectors; ++j)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += weigh(x[j][k]);
-    }
-    index = __reduce_min_sync(kFullMask, index);
-    if (threadIdx.x % 32 == 0) si[threadIdx.x / 32] = index;
-    __syncthreads();
+    sum *= Weigh(rate, best)(top);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(kFullMask, sum, m);
-    if (threadIdx.x % 32 == 0) sv[threadIdx.x / 32] = sum;
+    index = __reduce_min_sync(kFullMask, index);
+    if (lane == 0) {
+        ss[warp] = sum;
+        si[warp] = index;
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
         float z = 0.0f;
-        for (int w = 0; w < kVerifyThreads / 32; ++w) {
-            z += sv[w];
+        for (int w = 0; w < kWarps; ++w) {
+            z += ss[w];
             index = min(index, si[w]);
         }
         a.stats[blockIdx.x] = make_float4(best, __int_as_float(index), z, 0.0f);
@@ -192,17 +240,19 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_stats_kernel(const __gr
 }
 
 // Every share of a row repeats the acceptance (a few values), then races its part of the vocabulary; the share that ends
-// last joins them.
+// last joins them.  Bound by HBM and by the chain that opens it (sums, drafted tokens, their logits): 24 us for 84 MB at
+// 64 x 131072.
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_pick_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ float sv[32];
     __shared__ int si[32];
-    __shared__ int s_kept, s_top;
-    __shared__ float s_best, s_z;
-    __shared__ bool s_last;
+    constexpr int kWarps = kVerifyThreads / 32;
+    __shared__ float s_best[kWarps], s_z[kWarps];
+    __shared__ int s_top[kWarps];
+    __shared__ bool s_keep[kWarps], s_last;
     wait_prior_grid();
     release_next_grid();
-    const int split = blockIdx.x % a.splits, b = blockIdx.x / a.splits;
+    const int split = blockIdx.x % a.shares, b = blockIdx.x / a.shares;
     const int n = min(a.num_drafts != nullptr ? a.num_drafts[b] : a.drafts, a.drafts);
     int32_t *out = a.out_tokens + static_cast<int64_t>(b) * (a.drafts + 1);
     if (n < 0) {
@@ -215,72 +265,88 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(const __gri
     const float rate = rate_of(a, b);
     const bool greedy = rate == 0.0f;
     const T *row = static_cast<const T *>(a.logits) + b * a.tb;
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        for (int i0 = 0;; i0 += 32) {  // positions i0 + lane; the row's last one (n) has no draft and ends the search
-            const int i = i0 + lane;
-            float best = -INFINITY, z = 0.0f;
-            int top = INT32_MAX;
-            bool keep = false;
-            if (i <= n) {
-                const float4 *st = a.stats + (static_cast<int64_t>(b) * (a.drafts + 1) + i) * a.splits;
-                for (int k = 0; k < a.splits; ++k) {
-                    const float4 x = st[k];
-                    if (x.x > best) {
-                        z *= Weigh(rate, x.x)(best);
-                        best = x.x;
-                        top = __float_as_int(x.y);
-                    }
-                    z += x.z * Weigh(rate, best)(x.x);
-                }
-            }
+    const float *noise = a.noise + b * a.nb;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    int kept = 0;
+    float best, z;
+    int first;  // of the largest logits of position `kept`
+    for (int i0 = 0;; i0 += kWarps) {  // a warp a position; the last one (n) has no draft and ends the search
+        const int i = i0 + warp;
+        if (i <= n) {
+            // what the decision takes beside the sums, on its way before them
+            float logit = -INFINITY, q = 1.0f, u = 0.0f;
+            int token = -1;
             if (i < n) {
-                const int token = a.tokens[b * a.db + i * a.dp];
+                token = a.tokens[b * a.db + i * a.dp];
+                u = a.uniform[b * a.ub + i * a.up];
                 if (token >= 0 && token < a.vocab) {
-                    float p = greedy && token == top && best > -INFINITY ? 1.0f : 0.0f;
-                    if (!greedy && z > 0.0f) p = Weigh(rate, best)(clean(widen(row[i * a.tp + token]))) / z;
-                    const float q = a.probs != nullptr ? a.probs[b * a.pb + i * a.pp + token] : 1.0f;
-                    keep = a.uniform[b * a.ub + i * a.up] * q < p;
+                    logit = clean(widen(row[i * a.tp + token]));
+                    if (a.probs != nullptr) q = a.probs[b * a.pb + i * a.pp + token];
                 }
             }
-            const unsigned stop = __ballot_sync(kFullMask, !keep);
-            if (stop != 0) {
-                const int at = __ffs(stop) - 1;
-                if (lane == at) {
-                    s_kept = i;
-                    s_best = best;
-                    s_z = z;
-                    s_top = top;
-                    if (split == 0 && i < n) {
-                        const int token = a.tokens[b * a.db + i * a.dp];
-                        if (token < 0 || token >= a.vocab) count_error(a.err_count);
-                    }
+            const float4 *st = a.stats + (static_cast<int64_t>(b) * (a.drafts + 1) + i) * a.splits;
+            float m = -INFINITY, sum = 0.0f;
+            int at = INT32_MAX;
+            for (int k = lane; k < a.splits; k += 32) {
+                const float4 x = st[k];
+                if (x.x > m) {
+                    sum *= Weigh(rate, x.x)(m);
+                    m = x.x;
+                    at = __float_as_int(x.y);
                 }
-                break;
+                sum += x.z * Weigh(rate, m)(x.x);
+            }
+            const float mine = m;
+            warp_best(m, at);
+            sum *= Weigh(rate, m)(mine);
+#pragma unroll
+            for (int j = 16; j > 0; j >>= 1) sum += __shfl_xor_sync(kFullMask, sum, j);
+            if (lane == 0) {
+                bool keep = false;
+                if (token >= 0 && token < a.vocab) {
+                    float p = greedy && token == at && m > -INFINITY ? 1.0f : 0.0f;
+                    if (!greedy && sum > 0.0f) p = Weigh(rate, m)(logit) / sum;
+                    keep = u * q < p;
+                }
+                s_best[warp] = m;
+                s_z[warp] = sum;
+                s_top[warp] = at;
+                s_keep[warp] = keep;
             }
         }
+        __syncthreads();
+        int w = 0;
+        while (w < kWarps && i0 + w < n && s_keep[w]) ++w;
+        kept = i0 + w;
+        if (w < kWarps) {
+            best = s_best[w];
+            z = s_z[w];
+            first = s_top[w];
+            break;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const int kept = s_kept;
-    const float best = s_best, z = s_z;
+    if (split == 0 && threadIdx.x == 0 && kept < n) {
+        const int token = a.tokens[b * a.db + kept * a.dp];
+        if (token < 0 || token >= a.vocab) count_error(a.err_count);
+    }
     float top = 0.0f;  // a score has to be above 0
     int index = INT32_MAX;
     const bool race = !greedy && z > 0.0f;
     if (race) {
         const T *logits = row + kept * a.tp;
         const float *q = kept < n && a.probs != nullptr ? a.probs + b * a.pb + kept * a.pp : nullptr;
-        const float *noise = a.noise + b * a.nb;
         const int sure = kept < n && a.probs == nullptr ? a.tokens[b * a.db + kept * a.dp] : -1;
         // whole vectors where all three rows allow them
         const int before = static_cast<int>(reinterpret_cast<uintptr_t>(logits) % 16 / sizeof(T));
-        const int start = split * kSplit - before;
+        const int start = split * kShare - before;
         const Weigh weigh(rate, best);
         const float inv_z = 1.0f / z;
         const bool vn = reinterpret_cast<uintptr_t>(noise + start) % 16 == 0;
         const bool vq = q != nullptr && reinterpret_cast<uintptr_t>(q + start) % 16 == 0;
 #pragma unroll
         for (int j = 0; j < kVectors; ++j) {
-            const int v0 = start + (j * kVerifyThreads + threadIdx.x) * 8;
+            const int v0 = start + j * kStep + threadIdx.x * 8;
             float x[8], w[8], y[8] = {};
             load8(logits, v0, a.vocab, x);
             load8_plain(noise, v0, a.vocab, vn && v0 >= 0, w);
@@ -298,38 +364,47 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(const __gri
         }
         block_best(top, index, sv, si);
         if (threadIdx.x == 0) {
-            a.best[static_cast<int64_t>(b) * a.splits + split] = make_float2(top, __int_as_float(index));
+            a.best[static_cast<int64_t>(b) * a.shares + split] = make_float2(top, __int_as_float(index));
             __threadfence();
-            s_last = atomicAdd(a.done + b, 1u) == static_cast<unsigned>(a.splits) - 1;
+            s_last = atomicAdd(a.done + b, 1u) == static_cast<unsigned>(a.shares) - 1;
         }
         __syncthreads();
         if (!s_last) return;
         __threadfence();
         top = 0.0f;
         index = INT32_MAX;
-        for (int k = threadIdx.x % 32; k < a.splits; k += 32) {
-            const float2 x = __ldcg(a.best + static_cast<int64_t>(b) * a.splits + k);
+        for (int k = threadIdx.x % 32; k < a.shares; k += 32) {
+            const float2 x = __ldcg(a.best + static_cast<int64_t>(b) * a.shares + k);
             take_best(top, index, x.x, __float_as_int(x.y));
         }
         warp_best(top, index);
     } else {
         if (split != 0) return;
-        if (greedy && best > -INFINITY) index = s_top;
+        if (greedy && best > -INFINITY) index = first;
     }
     for (int i = threadIdx.x; i <= a.drafts; i += kVerifyThreads)
         out[i] = i < kept ? a.tokens[b * a.db + i * a.dp] : i == kept && index != INT32_MAX ? index : -1;
     if (threadIdx.x == 0) a.num_accepted[b] = kept + 1;
 }
 
-// Shares of a row: its logits and up to 7 before them (see verify_stats_kernel).
-int64_t verify_splits(int vocab) { return (static_cast<int64_t>(vocab) + 7 + kSplit - 1) / kSplit; }
+// Shares of a row: its logits and what is before them up to a 16-byte boundary (see verify_stats_kernel), `before` at most.
+int64_t shares_of(int vocab, int share, int before = 7) { return (static_cast<int64_t>(vocab) + before + share - 1) / share; }
+
+// A block of the statistics takes a long share once that still fills the card (8 blocks an SM): each thread then loads its
+// second 4 vectors under the first 4's arithmetic.  Below that, shorter shares spread a row over more SMs.
+int stats_share(int64_t rows, int vocab) { return rows * shares_of(vocab, kLongShare) >= 8 * 152 ? kLongShare : kShare; }
+
+int64_t stats_blocks(int batch, int drafts, int vocab) {
+    const int64_t rows = static_cast<int64_t>(batch) * (drafts + 1);
+    return rows * shares_of(vocab, stats_share(rows, vocab));
+}
 
 template <typename T>
 int launch_verify(const VerifyArgs &a, cudaStream_t stream) {
-    const int status = launch_pdl(verify_stats_kernel<T>, dim3(static_cast<unsigned>(a.batch) * (a.drafts + 1) * a.splits),
+    const int status = launch_pdl(verify_stats_kernel<T>, dim3(static_cast<unsigned>(a.batch * (a.drafts + 1)) * a.splits),
                                   dim3(kVerifyThreads), 0, stream, a);
     if (status != CCV_OK) return status;
-    return launch_pdl(verify_pick_kernel<T>, dim3(static_cast<unsigned>(a.batch) * a.splits), dim3(kVerifyThreads), 0, stream, a);
+    return launch_pdl(verify_pick_kernel<T>, dim3(static_cast<unsigned>(a.batch) * a.shares), dim3(kVerifyThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -337,8 +412,7 @@ int launch_verify(const VerifyArgs &a, cudaStream_t stream) {
 
 extern "C" int64_t spec_verify_workspace(int batch, int drafts, int vocab) {
     if (batch <= 0 || drafts < 0 || vocab <= 0) return 0;
-    const int64_t shares = static_cast<int64_t>(batch) * ccv::verify_splits(vocab);
-    return shares * (drafts + 1) * 16 + shares * 8 + static_cast<int64_t>(batch) * 4;
+    return ccv::stats_blocks(batch, drafts, vocab) * 16 + batch * ccv::shares_of(vocab, ccv::kShare) * 8 + static_cast<int64_t>(batch) * 4;
 }
 
 extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t_stride_b, int64_t t_stride_pos,
@@ -353,7 +427,7 @@ extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t
                       n_stride_b})
         if (s < 0) return CCV_ERR_STRIDE;
     if (batch == 0) return CCV_OK;
-    if (vocab == 0 || static_cast<int64_t>(batch) * (drafts + 1) * verify_splits(vocab) > 0x7fffffff) return CCV_ERR_SIZE;
+    if (vocab == 0 || static_cast<int64_t>(batch) * (drafts + 1) * shares_of(vocab, kShare) > 0x7fffffff) return CCV_ERR_SIZE;
     if (target_logits == nullptr || noise == nullptr || out_tokens == nullptr || num_accepted == nullptr ||
         (drafts > 0 && (draft_tokens == nullptr || uniform == nullptr)))
         return CCV_ERR_NULL_POINTER;
@@ -370,12 +444,15 @@ extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t
         (num_drafts != nullptr &&
          (overlaps(et, extent(num_drafts, batch, 1, 1, 0)) || overlaps(ea, extent(num_drafts, batch, 1, 1, 0)))))
         return CCV_ERR_ALIAS;
-    const int64_t shares = static_cast<int64_t>(batch) * verify_splits(vocab);
-    uint8_t *space = static_cast<uint8_t *>(workspace);
+    const int share = stats_share(static_cast<int64_t>(batch) * (drafts + 1), vocab);
+    const int size = logits_fp32 ? 4 : 2;
+    const int before = aligned16(target_logits) && t_stride_b * size % 16 == 0 && t_stride_pos * size % 16 == 0 ? 0 : 7;
+    const int64_t shares = shares_of(vocab, kShare, before), splits = shares_of(vocab, share, before);
+    uint8_t *space = static_cast<uint8_t *>(workspace), *best = space + stats_blocks(batch, drafts, vocab) * 16;
     const VerifyArgs a{target_logits, t_stride_b, t_stride_pos, draft_tokens, d_stride_b, d_stride_pos, draft_probs, p_stride_b,
                        p_stride_pos, num_drafts, temperature, uniform, u_stride_b, u_stride_pos, noise, n_stride_b, out_tokens,
-                       num_accepted, batch, drafts, vocab, static_cast<int>(verify_splits(vocab)),
-                       reinterpret_cast<float4 *>(space), reinterpret_cast<float2 *>(space + shares * (drafts + 1) * 16),
-                       reinterpret_cast<unsigned *>(space + shares * (drafts + 1) * 16 + shares * 8), err_count};
+                       num_accepted, batch, drafts, vocab, share, static_cast<int>(splits),
+                       static_cast<int>(shares), reinterpret_cast<float4 *>(space), reinterpret_cast<float2 *>(best),
+                       reinterpret_cast<unsigned *>(best + batch * shares * 8), err_count};
     return logits_fp32 ? launch_verify<float>(a, stream) : launch_verify<uint16_t>(a, stream);
 }

@@ -62,29 +62,32 @@ class ScratchLaunch(Launch):
         return result
 
 
+# The checks below run on every call of a decode step, so the common case is one
+# expression per function and _need only finds out what to say.
+
 def _need(dev: int, t: torch.Tensor, name: str, *dtypes):
     """t is a tensor of the call's CUDA device and of one of the types."""
-    if not isinstance(t, torch.Tensor) or t.get_device() < 0 or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.get_device() != dev:
+    if dev >= 0 and t.get_device() != dev:
         raise ValueError(f"all tensors of a call must be on one device, got cuda:{dev} and "
                          f"{t.device} ({name})")
     return t
 
 
-def _first(t, name: str, *dtypes) -> int:
-    """The call's device: that of its first tensor."""
-    _need(t.get_device() if isinstance(t, torch.Tensor) else -1, t, name, *dtypes)
-    return t.get_device()
+def _device(t) -> int:
+    """The device index of a call's first tensor (-1: not a CUDA tensor)."""
+    return t.get_device() if isinstance(t, torch.Tensor) else -1
 
 
 def _vector(dev: int, t: Optional[torch.Tensor], name: str, dtype, length: int):
     """Pointer of a contiguous vector of at least `length` entries, or None."""
     if t is None:
         return None
-    _need(dev, t, name, dtype)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _need(dev, t, name, dtype)
     if t.dim() != 1 or t.stride(0) != 1:
         raise ValueError(f"{name} must be a contiguous 1-D tensor")
     if t.shape[0] < length:
@@ -109,9 +112,18 @@ def _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slo
     """Checks shared by gdr_fwd and gdr_update.  mode: "tokens" for (tokens,
     heads, dim) tensors, "rows" for (batch, heads, dim), "steps" for (batch,
     seqlen, heads, dim).  Returns (device, packed ccv_gdr_args, out, sizes)."""
-    dev = _first(v, "v", _BF16)
-    _need(dev, k, "k", _BF16)
-    _need(dev, q, "q", _BF16)
+    if (a_log is None) != (dt_bias is None):
+        raise ValueError("a_log and dt_bias go together")
+    dev = _device(v)
+    dtype = _F32 if a_log is None else _BF16
+    if not (dev >= 0 and v.dtype is _BF16 and isinstance(k, torch.Tensor) and k.dtype is _BF16
+            and isinstance(q, torch.Tensor) and q.dtype is _BF16 and isinstance(g, torch.Tensor)
+            and g.dtype is dtype and isinstance(beta, torch.Tensor) and beta.dtype is dtype
+            and k.get_device() == q.get_device() == g.get_device() == beta.get_device() == dev):
+        for t, name in ((v, "v"), (k, "k"), (q, "q")):
+            _need(dev, t, name, _BF16)
+        for t, name in ((g, "g"), (beta, "beta")):
+            _need(dev, t, name, dtype)
     lead = 2 if mode == "steps" else 1
     vs, ks = v.shape, k.shape
     if len(vs) != lead + 2:
@@ -120,11 +132,6 @@ def _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slo
         raise ValueError("q and k must have the same shape, and v the same tokens")
     hv, dv = vs[lead:]
     hk, dk = ks[lead:]
-    if (a_log is None) != (dt_bias is None):
-        raise ValueError("a_log and dt_bias go together")
-    dtype = _F32 if a_log is None else _BF16
-    _need(dev, g, "g", dtype)
-    _need(dev, beta, "beta", dtype)
     if g.shape != vs[:-1] or beta.shape != vs[:-1]:
         raise ValueError(f"g and beta must have shape {tuple(vs[:-1])}")
     gs = g.stride()
@@ -133,17 +140,18 @@ def _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slo
     al = db = sp = lines = 0
     ss = (0, 0, 0, 0)
     if a_log is not None:
-        al, db = (_vector(dev, t, n, _F32, hv) for t, n in ((a_log, "a_log"), (dt_bias, "dt_bias")))
+        al, db = _vector(dev, a_log, "a_log", _F32, hv), _vector(dev, dt_bias, "dt_bias", _F32, hv)
         if a_log.shape[0] != hv or dt_bias.shape[0] != hv:
             raise ValueError(f"a_log and dt_bias must have {hv} entries")
     if state is not None:
-        _need(dev, state, "state", _F32)
+        if not isinstance(state, torch.Tensor) or state.dtype is not _F32 or state.get_device() != dev:
+            _need(dev, state, "state", _F32)
         lines = state.shape[0]
         if state.shape != (lines, hv, dv, dk):
             raise ValueError("state must be (num_lines, num_v_heads, dim_v, dim_k)")
         ss, sp = state.stride(), state.data_ptr()
     if out is None:
-        out = torch.empty(vs, dtype=_BF16, device=v.device)
+        out = torch.empty_like(v)
     else:
         _need(dev, out, "out", _BF16)
         if out.shape != vs:
@@ -152,7 +160,8 @@ def _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slo
     if mode == "tokens":
         qs, ks_, vst, os_, gs = (0, *qs), (0, *ks_), (0, *vst), (0, *os_), (0, *gs)
     elif mode == "rows":
-        qs, ks_, vst, os_ = ((t[0], 0, t[1], t[2]) for t in (qs, ks_, vst, os_))
+        qs, ks_ = (qs[0], 0, qs[1], qs[2]), (ks_[0], 0, ks_[1], ks_[2])
+        vst, os_ = (vst[0], 0, vst[1], vst[2]), (os_[0], 0, os_[1], os_[2])
         gs = (gs[0], 0, gs[1])
     if scale is None:
         scale = dk ** -0.5 if dk else 0.0
@@ -301,15 +310,18 @@ def prepare_gated_rms_norm(x, gate, weight, eps=1e-6, activation="silu", norm_be
 
 
 def _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out):
-    dev = _first(x, "x", _BF16)
-    _need(dev, gate, "gate", _BF16)
+    dev = _device(x)
+    if not (dev >= 0 and x.dtype is _BF16 and isinstance(gate, torch.Tensor)
+            and gate.dtype is _BF16 and gate.get_device() == dev):
+        _need(dev, x, "x", _BF16)
+        _need(dev, gate, "gate", _BF16)
     if activation not in _ACTIVATIONS:
         raise ValueError(f"unsupported activation: {activation!r}")
     shape = x.shape
     if len(shape) not in (2, 3) or gate.shape != shape:
         raise ValueError("x and gate must be (tokens, heads, dim) or (tokens, dim), one shape")
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=x.device)
+        out = torch.empty_like(x)
     else:
         _need(dev, out, "out", _BF16)
         if out.shape != shape:
@@ -330,7 +342,8 @@ def _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out):
 def _norm_weight(dev: int, w: Optional[torch.Tensor], name: str, dim: int):
     if w is None:
         return None
-    _need(dev, w, name, _BF16)
+    if not isinstance(w, torch.Tensor) or w.dtype is not _BF16 or w.get_device() != dev:
+        _need(dev, w, name, _BF16)
     if w.shape != (dim,) or (dim > 1 and w.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {dim}")
     return w.data_ptr()
@@ -365,8 +378,11 @@ def prepare_residual_rms_norm(x, residual, weight, post_weight=None, gate=None, 
 
 def _marshal_residual(x, residual, weight, post_weight, gate, scale, eps, weight_offset, out,
                       residual_out):
-    dev = _first(x, "x", _BF16)
-    _need(dev, residual, "residual", _BF16, _F32)
+    dev = _device(x)
+    if not (dev >= 0 and x.dtype is _BF16 and isinstance(residual, torch.Tensor)
+            and residual.dtype in (_BF16, _F32) and residual.get_device() == dev):
+        _need(dev, x, "x", _BF16)
+        _need(dev, residual, "residual", _BF16, _F32)
     shape, kind = x.shape, residual.dtype
     if len(shape) != 2 or residual.shape != shape:
         raise ValueError("x and residual must be (tokens, dim), one shape")
@@ -382,11 +398,11 @@ def _marshal_residual(x, residual, weight, post_weight, gate, scale, eps, weight
             raise ValueError("gate must be (dim,) or (tokens, dim)")
         gp, gs = gate.data_ptr(), gate.stride() if gate.dim() == 2 else (0, gate.stride(0))
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=x.device)
+        out = torch.empty_like(x)
     else:
         _need(dev, out, "out", _BF16)
     if residual_out is None:
-        residual_out = torch.empty(shape, dtype=kind, device=x.device)
+        residual_out = torch.empty_like(residual)
     else:
         _need(dev, residual_out, "residual_out", kind)
     if out.shape != shape or residual_out.shape != shape:
@@ -439,10 +455,16 @@ def prepare_spec_verify(target_logits, draft_tokens, uniform, noise, draft_probs
 
 def _marshal_verify(target_logits, draft_tokens, uniform, noise, draft_probs, num_drafts,
                     temperature, out_tokens, num_accepted, workspace, err_count):
-    dev = _first(target_logits, "target_logits", _BF16, _F32)
-    _need(dev, draft_tokens, "draft_tokens", _I32)
-    _need(dev, uniform, "uniform", _F32)
-    _need(dev, noise, "noise", _F32)
+    dev = _device(target_logits)
+    if not (dev >= 0 and target_logits.dtype in (_BF16, _F32)
+            and isinstance(draft_tokens, torch.Tensor) and draft_tokens.dtype is _I32
+            and isinstance(uniform, torch.Tensor) and uniform.dtype is _F32
+            and isinstance(noise, torch.Tensor) and noise.dtype is _F32
+            and draft_tokens.get_device() == uniform.get_device() == noise.get_device() == dev):
+        _need(dev, target_logits, "target_logits", _BF16, _F32)
+        _need(dev, draft_tokens, "draft_tokens", _I32)
+        _need(dev, uniform, "uniform", _F32)
+        _need(dev, noise, "noise", _F32)
     if target_logits.dim() != 3 or draft_tokens.dim() != 2:
         raise ValueError("target_logits must be (batch, drafts + 1, vocab), draft_tokens "
                          "(batch, drafts)")
@@ -465,14 +487,15 @@ def _marshal_verify(target_logits, draft_tokens, uniform, noise, draft_probs, nu
         raise ValueError("target_logits, noise and draft_probs must have stride 1 along vocab")
     nd = _vector(dev, num_drafts, "num_drafts", _I32, batch)
     temp = _vector(dev, temperature, "temperature", _F32, batch)
+    device = noise.device
     if out_tokens is None:
-        out_tokens = torch.empty((batch, drafts + 1), dtype=_I32, device=noise.device)
+        out_tokens = torch.empty((batch, drafts + 1), dtype=_I32, device=device)
     else:
         _need(dev, out_tokens, "out_tokens", _I32)
         if out_tokens.shape != (batch, drafts + 1) or not out_tokens.is_contiguous():
             raise ValueError("out_tokens must be a contiguous (batch, drafts + 1)")
     if num_accepted is None:
-        num_accepted = torch.empty(batch, dtype=_I32, device=noise.device)
+        num_accepted = torch.empty(batch, dtype=_I32, device=device)
     count = _vector(dev, num_accepted, "num_accepted", _I32, batch)
     size = _lib.load().spec_verify_workspace(batch, drafts, vocab)
     scratch = _workspace(dev, workspace, size, noise)
