@@ -136,7 +136,9 @@ constexpr int kLd = 68;  // floats of a row of A in shared memory: 16-byte rows,
 struct PrepSmem {
     float ghi[2][C], glo[2][C];    // G log2(e) as a float pair
     float beta[2][C];
+    float from[2][C / 2];          // e^{G_31 - G_j} times the factor of row j of K, j < 32
     float rk[C], rq[C];            // factors of the rows of K and Q
+    uint4 rows[2][32 * 8];         // one part of 32 rows of P on its way out, a warp each
     int64_t carry[2];
     uint64_t bar;
     uint32_t tmem;
@@ -370,57 +372,79 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
             vec[kQuery * C + i] = sm.rq[i] * decay;
             if (i == 0) vec[kMisc * C] = ex2(sm.ghi[side][C - 1] + sm.glo[side][C - 1]);
         }
+        if (side < nh && i < C / 2)
+            sm.from[side][i] = ex2((sm.ghi[side][31] - sm.ghi[side][i]) + (sm.glo[side][31] - sm.glo[side][i])) * sm.rk[i];
+        __syncthreads();
         // Rows of A (threads of K rows, to shared memory) and of P (threads of Q rows, to the workspace).
         for (int w = 0; w < nh; ++w) {
             const float ghi = sm.ghi[w][i], glo = sm.glo[w][i];
             const float own = side ? sm.rq[i] : sm.beta[w][i] * sm.rk[i];
-            uint8_t *out_p = block(r0 + w) + kP + i * 128;
             float *out_a = matrices + w * (C * kLd) + i * kLd;
+            uint4 hi[8], mid[8];  // of P
 #pragma unroll
             for (int j0 = 0; j0 < C; j0 += 32) {
-                if (j0 >= (warp & 1) * 32 + 32) {  // above the diagonal for this warp's rows
-                    if (side) {
+                float f[32];
+                if (j0 == 0 && (warp & 1)) {
+                    // Rows 32 .. 63, columns 0 .. 31: the decay is a factor of the row times one of the column, both <= 1.
+                    const float left = own * ex2((ghi - sm.ghi[w][31]) + (glo - sm.glo[w][31]));
+                    tmem_load(addr + j0, f);
+                    tmem_wait_load();
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int at = ((j0 / 8 + c) ^ (i & 7)) << 4;
-                            *reinterpret_cast<uint4 *>(out_p + at) = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4 *>(out_p + kTile + at) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 r = *reinterpret_cast<const float4 *>(&sm.from[w][j]);
+                        f[j] *= left * r.x;
+                        f[j + 1] *= left * r.y;
+                        f[j + 2] *= left * r.z;
+                        f[j + 3] *= left * r.w;
+                    }
+                } else if (j0 == 0 || (warp & 1)) {  // on the diagonal
+                    tmem_load(addr + j0, f);
+                    tmem_wait_load();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 gh = *reinterpret_cast<const float4 *>(&sm.ghi[w][j0 + j]);
+                        const float4 gl = *reinterpret_cast<const float4 *>(&sm.glo[w][j0 + j]);
+                        const float4 rh = *reinterpret_cast<const float4 *>(&sm.rk[j0 + j]);
+                        const float gj[4] = {gh.x, gh.y, gh.z, gh.w}, lj[4] = {gl.x, gl.y, gl.z, gl.w};
+                        const float rj[4] = {rh.x, rh.y, rh.z, rh.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const bool in = j0 + j + u < i + side;
+                            f[j + u] = in ? f[j + u] * (own * rj[u]) * ex2((ghi - gj[u]) + (glo - lj[u])) : 0.0f;
                         }
                     }
-                    continue;  // of A nothing there is read
-                }
-                float f[32];
-                tmem_load(addr + j0, f);
-                tmem_wait_load();
+                } else {  // rows 0 .. 31, columns 32 .. 63: nothing, and of A not even read
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 gh = *reinterpret_cast<const float4 *>(&sm.ghi[w][j0 + j]);
-                    const float4 gl = *reinterpret_cast<const float4 *>(&sm.glo[w][j0 + j]);
-                    const float4 rh = *reinterpret_cast<const float4 *>(&sm.rk[j0 + j]);
-                    const float gj[4] = {gh.x, gh.y, gh.z, gh.w}, lj[4] = {gl.x, gl.y, gl.z, gl.w};
-                    const float rj[4] = {rh.x, rh.y, rh.z, rh.w};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const bool in = j0 + j + u < i + side;
-                        f[j + u] = in ? f[j + u] * (own * rj[u]) * ex2((ghi - gj[u]) + (glo - lj[u])) : 0.0f;
-                    }
+                    for (int j = 0; j < 32; ++j) f[j] = 0.0f;
+                    if (!side) continue;
                 }
                 if (side) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint4 hi, mid;
-                        split_bf16x2(pack2(f[8 * c], f[8 * c + 1]), hi.x, mid.x);
-                        split_bf16x2(pack2(f[8 * c + 2], f[8 * c + 3]), hi.y, mid.y);
-                        split_bf16x2(pack2(f[8 * c + 4], f[8 * c + 5]), hi.z, mid.z);
-                        split_bf16x2(pack2(f[8 * c + 6], f[8 * c + 7]), hi.w, mid.w);
-                        const int at = ((j0 / 8 + c) ^ (i & 7)) << 4;
-                        *reinterpret_cast<uint4 *>(out_p + at) = hi;
-                        *reinterpret_cast<uint4 *>(out_p + kTile + at) = mid;
+                        uint4 &h = hi[j0 / 8 + c], &m = mid[j0 / 8 + c];
+                        split_bf16x2(pack2(f[8 * c], f[8 * c + 1]), h.x, m.x);
+                        split_bf16x2(pack2(f[8 * c + 2], f[8 * c + 3]), h.y, m.y);
+                        split_bf16x2(pack2(f[8 * c + 4], f[8 * c + 5]), h.z, m.z);
+                        split_bf16x2(pack2(f[8 * c + 6], f[8 * c + 7]), h.w, m.w);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
                         *reinterpret_cast<float4 *>(out_a + j0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                }
+            }
+            if (side) {
+                // A row a thread would touch 32 lines a store: through shared memory 4 rows go out at once.
+                uint4 *rows = sm.rows[warp & 1];
+                uint4 *out_p = reinterpret_cast<uint4 *>(block(r0 + w) + kP) + (warp & 1) * 256;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) rows[lane * 8 + (c ^ (lane & 7))] = part ? mid[c] : hi[c];
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) out_p[part * (kTile / 16) + c * 32 + lane] = rows[c * 32 + lane];
                 }
             }
         }
@@ -434,8 +458,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
                 const int row = it * 8 + (i >> 3);
                 uint4 hi = make_uint4(0u, 0u, 0u, 0u), mid = hi, lo = hi;
                 if (row >= 32 || c < 4) {
+                    // 32 bytes apart, 8 lanes would meet in the banks: half of them read their second 16 bytes first
                     const float *x = matrices + side * (C * kLd) + row * kLd + c * 8;
-                    const ulonglong2 x0 = *reinterpret_cast<const ulonglong2 *>(x), x1 = *reinterpret_cast<const ulonglong2 *>(x + 4);
+                    const ulonglong2 y0 = *reinterpret_cast<const ulonglong2 *>(x + (c & 4)), y1 = *reinterpret_cast<const ulonglong2 *>(x + 4 - (c & 4));
+                    const ulonglong2 x0 = c & 4 ? y1 : y0, x1 = c & 4 ? y0 : y1;
                     split_bf16x3(x0.x, hi.x, mid.x, lo.x);
                     split_bf16x3(x0.y, hi.y, mid.y, lo.y);
                     split_bf16x3(x1.x, hi.z, mid.z, lo.z);

@@ -142,7 +142,7 @@ __device__ __forceinline__ float rate_of(const VerifyArgs &a, int b) {
 // end and the next vectors are always on their way: 64 x 5 rows of 131072 bf16 logits take 23 us (3.6 TB/s; the exponentials
 // and the arithmetic around them are the bound) against 33 with a block-wide maximum first.
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads, 5) verify_stats_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 5 : 2) verify_stats_kernel(const __grid_constant__ VerifyArgs a) {
     constexpr int kWarps = kVerifyThreads / 32;
     __shared__ float sv[kWarps], ss[kWarps];
     __shared__ int si[kWarps];
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 5) verify_stats_kernel(const _
 // last joins them.  Bound by HBM and by the chain that opens it (sums, drafted tokens, their logits): 24 us for 84 MB at
 // 64 x 131072.
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads, 4) verify_pick_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify_pick_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ float sv[32];
     __shared__ int si[32];
     constexpr int kWarps = kVerifyThreads / 32;
