@@ -1061,12 +1061,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 
 // ------------------------------------------------------------------- join ----
 
-constexpr int kJoinThreads = 128, kJoinRows = 4;  // rows of S a warp carries
+constexpr int kJoinThreads = 128;
 
 // First states of the segments from the third on: S_{j+1} = S_j M_j + N_j, whose N the first pass left in S_{j+1}'s place.
-// Rows are independent: a warp takes 4 of them through a whole sequence, 4 columns a lane, S by shuffles, while the next M
-// is on its way to shared memory.  In fp32 throughout.
-template <int PANELS>
+// Rows are independent: a warp takes ROWS of them through a whole sequence, 4 columns a lane, S by shuffles, while the next M
+// is on its way to shared memory.  In fp32 throughout.  Bound by the shared-memory pipe (M and the shuffles): fewer rows a
+// warp are faster as long as the blocks still fit on the card at once.
+template <int PANELS, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) gdr_join_kernel(const __grid_constant__ FwdArgs p) {
     constexpr int kLdS = 64 * PANELS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1075,8 +1076,8 @@ __global__ void __launch_bounds__(kJoinThreads) gdr_join_kernel(const __grid_con
     __shared__ int abort;
     const ccv_gdr_args &a = p.a;
     const int lane = threadIdx.x & 31;
-    const int groups = (a.dim_v + kJoinRows * 4 - 1) / (kJoinRows * 4);
-    const int first = (blockIdx.x % groups) * kJoinRows * 4, row0 = first + (threadIdx.x >> 5) * kJoinRows;
+    const int groups = (a.dim_v + ROWS * 4 - 1) / (ROWS * 4);
+    const int first = (blockIdx.x % groups) * ROWS * 4, row0 = first + (threadIdx.x >> 5) * ROWS;
     const int bh = blockIdx.x / groups;
     const int h = bh % a.num_v_heads, seq = bh / a.num_v_heads;
     wait_prior_grid();
@@ -1108,23 +1109,22 @@ __global__ void __launch_bounds__(kJoinThreads) gdr_join_kernel(const __grid_con
     auto row_at = [&](int j, int r) {
         return p.seg_state + ((static_cast<int64_t>(slot0 + j) * a.num_v_heads + h) * a.dim_v + min(row0 + r, a.dim_v - 1)) * kLdS + column;
     };
-    float4 x[kJoinRows];
+    float4 x[ROWS];
 #pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) x[r] = *reinterpret_cast<const float4 *>(row_at(1, r));
+    for (int r = 0; r < ROWS; ++r) x[r] = *reinterpret_cast<const float4 *>(row_at(1, r));
     for (int j = 1; j + 1 < segments; ++j) {
         if (threadIdx.x == 0 && j + 2 < segments) fetch(j + 1);
-        float4 y[kJoinRows];
+        float4 y[ROWS];
 #pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) y[r] = *reinterpret_cast<const float4 *>(row_at(j + 1, r));
+        for (int r = 0; r < ROWS; ++r) y[r] = *reinterpret_cast<const float4 *>(row_at(j + 1, r));
         const bool ok = mbar_wait_warp(&full[j & 1], ((j - 1) >> 1) & 1, &abort);
         const float *m = steps + (j & 1) * kLdS * kLdS + column;
-#pragma unroll 2
-        for (int k0 = 0; k0 < kLdS; k0 += 4) {
+        auto add = [&](int k0, int step) {  // rows k0 .. + 3 of M; past dim_k S is 0, and M's last row stands in
             float4 w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const float4 *>(m + min(k0 + k, a.dim_k - 1) * kLdS);  // S is 0 past dim_k
+            for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const float4 *>(m + k0 * kLdS + (step > k ? k : step - 1) * kLdS);
 #pragma unroll
-            for (int r = 0; r < kJoinRows; ++r) {
+            for (int r = 0; r < ROWS; ++r) {
                 const float s4[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -1135,9 +1135,13 @@ __global__ void __launch_bounds__(kJoinThreads) gdr_join_kernel(const __grid_con
                     y[r].w = fmaf(v, w[k].w, y[r].w);
                 }
             }
-        }
+        };
+        const int whole = a.dim_k & ~3;
+#pragma unroll 4
+        for (int k0 = 0; k0 < whole; k0 += 4) add(k0, 4);
+        if (whole < a.dim_k) add(whole, a.dim_k - whole);
 #pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
             x[r] = y[r];
             if (row0 + r < a.dim_v) *reinterpret_cast<float4 *>(row_at(j + 1, r)) = y[r];
         }
@@ -1210,6 +1214,17 @@ int launch_chunks(const FwdArgs &p, const FwdMaps &maps, int64_t units, cudaStre
                       chunk_smem<PANELS>(), stream, p, maps, slices);
 }
 
+template <int PANELS, int ROWS>
+int launch_join(const FwdArgs &p, cudaStream_t stream) {
+    int dev = 0;
+    current_device_sms(&dev);
+    cudaError_t err;
+    if (resident_blocks<gdr_join_kernel<PANELS, ROWS>>(kJoinThreads, join_smem<PANELS>(), dev, &err) == 0) return static_cast<int>(err);
+    const int64_t blocks = static_cast<int64_t>(p.batch) * p.a.num_v_heads * ((p.a.dim_v + 4 * ROWS - 1) / (4 * ROWS));
+    if (blocks > 0x7fffffff) return CCV_ERR_SIZE;
+    return launch_pdl(gdr_join_kernel<PANELS, ROWS>, dim3(static_cast<unsigned>(blocks)), dim3(kJoinThreads), join_smem<PANELS>(), stream, p);
+}
+
 template <int PANELS, bool VS, bool VIO>
 int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
     int dev = 0;
@@ -1217,8 +1232,7 @@ int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
     cudaError_t err;
     if (resident_blocks<gdr_prep_kernel<PANELS, VIO>>(kPrepThreads, prep_smem<PANELS>(), dev, &err) == 0) return static_cast<int>(err);
     const int64_t prep = static_cast<int64_t>(p.slots) * p.a.num_k_heads;
-    const int64_t rows = static_cast<int64_t>(p.batch) * p.a.num_v_heads * ((p.a.dim_v + 15) / 16);
-    if (prep > 0x7fffffff || rows > 0x7fffffff) return CCV_ERR_SIZE;
+    if (prep > 0x7fffffff) return CCV_ERR_SIZE;
     FwdMaps maps;
     maps.use = VIO && encoder() != nullptr && encode_map(&maps.q, p.a.q, p.a.dim_k, p.a.num_k_heads, p.total_tokens) &&
                encode_map(&maps.k, p.a.k, p.a.dim_k, p.a.num_k_heads, p.total_tokens) &&
@@ -1230,8 +1244,11 @@ int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
     const int64_t segments = segment_slots(p.total_tokens, p.batch, p.seg_chunks);
     status = launch_chunks<PANELS, false, VS, VIO>(p, maps, segments, stream);
     if (status != CCV_OK) return status;
-    if (resident_blocks<gdr_join_kernel<PANELS>>(kJoinThreads, join_smem<PANELS>(), dev, &err) == 0) return static_cast<int>(err);
-    status = launch_pdl(gdr_join_kernel<PANELS>, dim3(static_cast<unsigned>(rows)), dim3(kJoinThreads), join_smem<PANELS>(), stream, p);
+    const int64_t row_sets = static_cast<int64_t>(p.batch) * p.a.num_v_heads;
+    const int sms = current_device_sms();
+    status = row_sets * ((p.a.dim_v + 3) / 4) <= sms   ? launch_join<PANELS, 1>(p, stream)
+             : row_sets * ((p.a.dim_v + 7) / 8) <= sms ? launch_join<PANELS, 2>(p, stream)
+                                                       : launch_join<PANELS, 4>(p, stream);
     if (status != CCV_OK) return status;
     return launch_chunks<PANELS, true, VS, VIO>(p, maps, segments, stream);
 }
@@ -1244,18 +1261,24 @@ int launch_chunked(const FwdArgs &p, bool vs, bool vio, cudaStream_t stream) {
 
 bool chunked_dims(int dim_k) { return dim_k <= 128; }
 
+// The recurrent form takes 0.85 us a token of the longest sequence, the chunked one 22 us for up to a chunk of each (1
+// sequence of 32 heads; 7.6 + 2.2 us a token against 35 us for 8, 45 + 13 us against 215 us for 64): they meet at 12 to 22
+// tokens a sequence.  8 on average leaves room for lengths that differ, which only the device knows.
+constexpr int kRecurrentTokens = 8;
+
 // CCV_GDR_PATH=recurrent or =chunked, read at each call, forces one form (for testing and tuning).
-bool use_chunked(const ccv_gdr_args &a, int batch, int total) {
-    if (!chunked_dims(a.dim_k)) return false;
+bool use_chunked(int batch, int total_tokens, int dim_k) {
+    if (!chunked_dims(dim_k)) return false;
     const char *path = std::getenv("CCV_GDR_PATH");
     if (path != nullptr && std::strcmp(path, "recurrent") == 0) return false;
     if (path != nullptr && std::strcmp(path, "chunked") == 0) return true;
-    return true;
+    return total_tokens > static_cast<int64_t>(kRecurrentTokens) * batch;
 }
 
 // Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device).  In
-// chunk times of a block (3.2 us): the first pass takes 0.85 of one a chunk, a join 0.6 a segment, and the two launches more
-// take 6.  Each pass runs in waves of one block an SM.
+// chunk times of a block (2.5 us): the first pass takes 0.95 of one a chunk, a join 0.8 a segment (2.5 where its blocks take
+// 4 rows a warp), and the two launches more take 3.5.  Each pass runs in waves of one block an SM.  11027 tokens take 232 us
+// with 16 heads and 124 with 4, against 475 and 446 whole; 1000 tokens and 4 heads, 58 against 59.
 int segment_chunks(int total_tokens, int batch, int num_v_heads, int dim_v) {
     constexpr int kSms = 152;
     const int chunks = static_cast<int>((static_cast<int64_t>(total_tokens) + batch * C - 1) / (static_cast<int64_t>(batch) * C));
@@ -1264,11 +1287,12 @@ int segment_chunks(int total_tokens, int batch, int num_v_heads, int dim_v) {
     auto waves = [](int64_t blocks) { return static_cast<double>((blocks + kSms - 1) / kSms); };
     const char *forced = std::getenv("CCV_GDR_SEGMENT");  // chunks of a segment (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;
+    const double join = heads * ((dim_v + 7) / 8) <= kSms ? 0.8 : 2.5;
     double best = waves(heads * slices) * chunks;
     int choice = 0;
     for (int n = 3; n <= 64 && n <= chunks; ++n) {
         const int length = (chunks + n - 1) / n;
-        const double cost = 6 + waves(heads * ((n - 1) * slices + n - 2)) * length * 0.85 + (n - 2) * 0.6 + waves(heads * n * slices) * length;
+        const double cost = 3.5 + waves(heads * ((n - 1) * slices + n - 2)) * length * 0.95 + (n - 2) * join + waves(heads * n * slices) * length;
         if (cost < best) {
             best = cost;
             choice = length;
@@ -1285,7 +1309,7 @@ int64_t heads_bytes(int total_tokens, int batch, int num_v_heads) { return slot_
 extern "C" int64_t gdr_fwd_workspace(int total_tokens, int batch, int num_k_heads, int num_v_heads, int dim_k, int dim_v) {
     using namespace ccv;
     if (total_tokens <= 0 || batch <= 0 || num_k_heads <= 0 || num_v_heads <= 0 || dim_k <= 0 || dim_v <= 0) return 0;
-    if (!chunked_dims(dim_k)) return 0;
+    if (!use_chunked(batch, total_tokens, dim_k)) return 0;
     int64_t bytes = heads_bytes(total_tokens, batch, num_v_heads);
     if (const int seg = segment_chunks(total_tokens, batch, num_v_heads, dim_v))
         bytes += segment_slots(total_tokens, batch, seg) * num_v_heads * (dim_v + dim_k) * (dim_k <= 64 ? 256 : 512);
@@ -1306,7 +1330,7 @@ extern "C" int gdr_fwd(const ccv_gdr_args *args, const int32_t *query_start_loc,
     const int64_t need = gdr_fwd_workspace(total_tokens, batch, a.num_k_heads, a.num_v_heads, a.dim_k, a.dim_v);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 127u) != 0))
         return CCV_ERR_WORKSPACE;
-    if (!use_chunked(a, batch, total_tokens)) {
+    if (!use_chunked(batch, total_tokens, a.dim_k)) {
         const GdrRows rows{query_start_loc, cache_indices, has_initial_state, nullptr, nullptr, 0, 0, 0, batch, 0,
                            total_tokens, err_count};
         return gdr_launch_recurrent(a, rows, stream);
