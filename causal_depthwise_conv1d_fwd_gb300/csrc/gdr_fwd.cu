@@ -192,7 +192,7 @@ __device__ __forceinline__ void multiply_block(const float *a, const float *b, f
 // block's 128 threads: forward substitution of the diagonal 16 x 16 blocks, then twice T21 = -T22 (A21 T11), which doubles
 // the blocks.  Substitution and not a power series: its error stays at the rounding of T however alike the keys are.
 // Substitution reads a value of A for every column, and a broadcast load fills the shared-memory pipe like any other: done
-// for all 64 columns it took 17400 cycles a block (4 blocks an SM) against INVERT_CLK this way, the products on the tensor
+// for all 64 columns it took 17400 cycles a block (4 blocks an SM), and takes 8000 this way with the products on the tensor
 // cores.  The upper right 32 x 32 blocks hold scratch at the end.
 __device__ __forceinline__ void invert(float *matrices, int tid) {
     const int warp = tid >> 5, lane = tid & 31;
@@ -815,7 +815,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         };
         float *pool = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + row * a.s_stride_v : nullptr;
         const bool init = a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
-        const float *from = segment == 0 ? (init ? pool : nullptr) : FULL ? in_segment(p.seg_state, slot, a.dim_v) : nullptr;
+        // In the second pass another block may already have written the pool's line when a cut sequence's first segment starts:
+        // the first pass keeps the state it read for it.
+        const bool kept = FULL && !(segment == 0 && last);
+        const float *from = kept ? in_segment(p.seg_state, slot, a.dim_v) : segment == 0 && init ? pool : nullptr;
 
         f32x2 st[KH / 2];  // this thread's part of row d of S
 #pragma unroll
@@ -823,7 +826,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             const int kk = q * KH + k;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (from != nullptr && live) {
-                if (V || segment > 0) {
+                if (V || kept) {
                     if (kk < a.dim_k) x = *reinterpret_cast<const float4 *>(from + kk);
                 } else {
                     if (kk < a.dim_k) x.x = from[kk * a.s_stride_k];
@@ -834,6 +837,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             } else if (step_only && live) {
                 x = make_float4(kk == row, kk + 1 == row, kk + 2 == row, kk + 3 == row);
             }
+            if (!FULL && segment == 0 && live) *reinterpret_cast<float4 *>(in_segment(p.seg_state, slot, a.dim_v) + kk) = x;
             st[k / 2] = pack2(x.x, x.y);
             st[k / 2 + 1] = pack2(x.z, x.w);
         }
@@ -1063,7 +1067,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 
 constexpr int kJoinThreads = 128;
 
-// First states of the segments from the third on: S_{j+1} = S_j M_j + N_j, whose N the first pass left in S_{j+1}'s place.
+// First states of the segments from the third on (the first pass left the first two): S_{j+1} = S_j M_j + N_j, whose N the first pass left in S_{j+1}'s place.
 // Rows are independent: a warp takes ROWS of them through a whole sequence, 4 columns a lane, S by shuffles, while the next M
 // is on its way to shared memory.  In fp32 throughout.  Bound by the shared-memory pipe (M and the shuffles): fewer rows a
 // warp are faster as long as the blocks still fit on the card at once.
@@ -1320,7 +1324,7 @@ extern "C" int gdr_fwd(const ccv_gdr_args *args, const int32_t *query_start_loc,
                        const uint8_t *has_initial_state, int total_tokens, void *workspace, int64_t workspace_bytes,
                        int *err_count, ccv_stream_t stream) {
     using namespace ccv;
-    if (batch < 0 || total_tokens < 0) return CCV_ERR_SIZE;
+    if (batch < 0 || total_tokens < 0 || total_tokens > (1 << 30)) return CCV_ERR_SIZE;
     const int status = gdr_check(args, 1, total_tokens);
     if (status != CCV_OK) return status;
     if (has_initial_state != nullptr && args->state == nullptr) return CCV_ERR_ARGUMENT;

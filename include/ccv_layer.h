@@ -72,11 +72,19 @@ typedef struct ccv_gdr_args {
  * ccv_fwd: sequence i owns tokens [qsl[i], qsl[i+1]) and state line
  * cache_indices[i] (line i when NULL); a line equal to pad_slot_id skips the
  * sequence; without an initial state the state starts at zero, and the final
- * state is written to the line either way.  Offsets must not decrease: a
- * sequence whose own offsets do, or leave [0, total_tokens], is skipped and
- * counted in err_count, and the others' results are then undefined.  args->state may be NULL (zero
+ * state is written to the line either way.  args->state may be NULL (zero
  * start, no write-back; then has_initial_state must be NULL:
- * CCV_ERR_ARGUMENT).  A sequence of no tokens writes nothing.
+ * CCV_ERR_ARGUMENT).  A sequence of no tokens writes nothing.  Offsets must not
+ * decrease: a sequence whose own offsets do, or leave [0, total_tokens], is
+ * skipped and counted in err_count, and the other sequences' results are then
+ * undefined.
+ * With dim_k <= 128 and more than 8 tokens a sequence on average the call runs
+ * in chunks of 64 tokens on the tensor cores, and where sequences and heads are
+ * too few to fill the card also cuts sequences into segments that run side by
+ * side; otherwise token by token.  The forms differ in rounding alone.  The
+ * choice follows from the integer sizes.  The environment variables
+ * CCV_GDR_PATH=chunked or =recurrent and CCV_GDR_SEGMENT=<chunks of a segment,
+ * 0: none>, read at each call, force it (for testing and tuning).
  * workspace     gdr_fwd_workspace(...) bytes, 128-byte aligned, not shared
  *               with another call in flight.
  */
