@@ -138,7 +138,7 @@ struct PrepSmem {
     float beta[2][C];
     float from[2][C / 2];          // e^{G_31 - G_j} times the factor of row j of K, j < 32
     float rk[C], rq[C];            // factors of the rows of K and Q
-    uint4 rows[2][32 * 8];         // one part of 32 rows of P on its way out, a warp each
+    uint4 rows[2][2][32 * 8];      // 32 rows of P in two parts, on their way out, a warp each
     int64_t carry[2];
     uint64_t bar;
     uint32_t tmem;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
     stage_rows<PANELS, V, kPrepThreads>(ab, 2 * kTile, a.k, t0, hk, n, a.dim_k, tid);
     stage_rows<PANELS, V, kPrepThreads>(ab + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, tid);
     cp_async_commit();
-    if (warp == 0) tmem_alloc<64>(&sm.tmem);
+    if (warp == 0) tmem_alloc<2 * C>(&sm.tmem);
 
     // The value heads of this key head go two at a time, 64 threads each.
     const int i = tid & (C - 1), side = tid >> 6;
@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
         const int h = hk * rep + min(r0 + side, rep - 1);
         float g = 0.0f, beta = 0.0f;
         if (i < n) gdr_gates(a, (t0 + i) * a.gate_stride_tok + h * a.gate_stride_head, h, g, beta);
-        if (g < -200.0f) g = -200.0f;  // e^-200 is 0 in fp32; keeps -inf - -inf out of the differences
+        // e^-200 is 0 in fp32 and e^1000 infinite: keeps inf - inf out of the differences and the sums in range, and NaN as it is
+        g = g < -200.0f ? -200.0f : g > 1000.0f ? 1000.0f : g;
         constexpr float kOne = 1099511627776.0f;  // 2^40
         int64_t sum = __float2ll_rn(g * 1.4426950408889634f * kOne);
 #pragma unroll
@@ -327,35 +328,32 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    if (tid == 0) {  // [K; Q] K^T, 128 x 64
+    if (warp == 0) {  // [K; Q] [K; Q]^T: K K^T, Q K^T, and the rows' squares on the diagonal
+        const uint32_t one = elect_lane();
 #pragma unroll
         for (int ks = 0; ks < PANELS * 4; ++ks) {
             const uint32_t d = desc_low(smem_u32(ab)) + ((ks / 4) * 2 * kTile + (ks % 4) * 32) / 16;
-            mma_ss(tmem, d, d, mma_desc(128, C, false), ks > 0, 1);
+            mma_ss(tmem, d, d, mma_desc(2 * C, 2 * C, false), ks > 0, one);
         }
-        mma_commit(&sm.bar, 1);
-    }
-    // Meanwhile the rows' norms, a row a thread.
-    {
-        float ss = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 8 * PANELS; ++c) {
-            Raw<8> r;
-            r.v = *reinterpret_cast<const uint4 *>(ab + (c >> 3) * 2 * kTile + tid * 128 + (((c & 7) ^ (tid & 7)) << 4));
-            float f[8];
-            r.to_float(f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
-        }
-        const float r = a.qk_l2norm ? rsqrtf(ss + kGdrNormEps) : 1.0f;
-        if (side) sm.rq[i] = r * a.scale;
-        else sm.rk[i] = r;
+        mma_commit(&sm.bar, one);
     }
     if (!mbar_wait_warp(&sm.bar, 0, &sm.abort) && lane == 0) count_error(p.err_count);
     tc_fence_after();
-    __syncthreads();  // the rows of K and Q are no longer needed: A takes their place
 
     const uint32_t addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    {
+        float r = 1.0f;
+        if (a.qk_l2norm) {
+            float f[32], square = 0.0f;
+            tmem_load(addr + warp * 32, f);
+            tmem_wait_load();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) square = lane == j ? f[j] : square;
+            r = rsqrtf(square + kGdrNormEps);
+        }
+        (side ? sm.rq : sm.rk)[i] = side ? r * a.scale : r;
+    }
+    __syncthreads();  // the rows of K and Q are no longer needed: A takes their place
     for (int r0 = 0; r0 < rep; r0 += 2) {
         const int nh = min(2, rep - r0);
         if (r0 > 0) {
@@ -367,7 +365,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
             const float ghi = sm.ghi[side][i], glo = sm.glo[side][i], beta = sm.beta[side][i];
             const float decay = ex2(ghi + glo), rk = sm.rk[i];
             vec[kBeta * C + i] = beta;
-                        vec[kKey * C + i] = -beta * rk * decay;
+            vec[kKey * C + i] = -beta * rk * decay;
             vec[kState * C + i] = ex2((sm.ghi[side][C - 1] - ghi) + (sm.glo[side][C - 1] - glo)) * rk;
             vec[kQuery * C + i] = sm.rq[i] * decay;
             if (i == 0) vec[kMisc * C] = ex2(sm.ghi[side][C - 1] + sm.glo[side][C - 1]);
@@ -380,7 +378,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
             const float ghi = sm.ghi[w][i], glo = sm.glo[w][i];
             const float own = side ? sm.rq[i] : sm.beta[w][i] * sm.rk[i];
             float *out_a = matrices + w * (C * kLd) + i * kLd;
-            uint4 hi[8], mid[8];  // of P
+            uint4 (&rows)[2][32 * 8] = sm.rows[warp & 1];
+            if (side && r0 + w > 0) {
+                bulk_wait_read();
+                __syncwarp();
+            }
 #pragma unroll
             for (int j0 = 0; j0 < C; j0 += 32) {
                 float f[32];
@@ -421,11 +423,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
                 if (side) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint4 &h = hi[j0 / 8 + c], &m = mid[j0 / 8 + c];
+                        uint4 h, m;
                         split_bf16x2(pack2(f[8 * c], f[8 * c + 1]), h.x, m.x);
                         split_bf16x2(pack2(f[8 * c + 2], f[8 * c + 3]), h.y, m.y);
                         split_bf16x2(pack2(f[8 * c + 4], f[8 * c + 5]), h.z, m.z);
                         split_bf16x2(pack2(f[8 * c + 6], f[8 * c + 7]), h.w, m.w);
+                        const int at = lane * 8 + ((j0 / 8 + c) ^ (lane & 7));
+                        rows[0][at] = h;
+                        rows[1][at] = m;
                     }
                 } else {
 #pragma unroll
@@ -434,17 +439,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
                 }
             }
             if (side) {
-                // A row a thread would touch 32 lines a store: through shared memory 4 rows go out at once.
-                uint4 *rows = sm.rows[warp & 1];
-                uint4 *out_p = reinterpret_cast<uint4 *>(block(r0 + w) + kP) + (warp & 1) * 256;
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) rows[lane * 8 + (c ^ (lane & 7))] = part ? mid[c] : hi[c];
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) out_p[part * (kTile / 16) + c * 32 + lane] = rows[c * 32 + lane];
+                // Out by bulk copies: a row a thread would touch 32 lines a store.
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    uint8_t *to = block(r0 + w) + kP + (warp & 1) * (kTile / 2);
+                    bulk_store(to, rows[0], kTile / 2);
+                    bulk_store(to + kTile, rows[1], kTile / 2);
+                    bulk_commit();
                 }
             }
         }
@@ -475,9 +477,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
         }
         __syncthreads();
     }
+    bulk_wait();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_free<64>(tmem);
+    if (warp == 0) tmem_free<2 * C>(tmem);
 }
 
 // ----------------------------------------------------------------- chunks ----
