@@ -146,46 +146,76 @@ struct PrepSmem {
 };
 constexpr int kMatrixBytes = 2 * C * kLd * 4;  // A, then T, of two value heads; over the rows of K and Q once they are used
 
-// C = sign A B for a 16 x 8 NT block of fp32 matrices in shared memory (leading dimension kLd), inner length 8 KS, by a warp
-// on the tensor cores.  Each value goes in as two tf32 parts (11 bits each; the second by the unit's own truncation) and
-// three of their products are added, so the result is good to 2^-21.
-template <int KS, int NT>
-__device__ __forceinline__ void multiply_block(const float *a, const float *b, float *c, float sign, int lane) {
+// T21 = -T22 (A21 T11) in columns l .. l + 15 of the lower left quarter of the 16 S x 16 S block at d (leading dimension kLd),
+// over A21, by a warp on the tensor cores; `sync` comes between the last read and the first write.  Each value goes in as two
+// tf32 parts (11 bits each; the second by the unit's own truncation) and three of their products are added, so the result is
+// good to 2^-21.  (A21 T11)^T leaves the first product as the second one takes its operand: a lane's accumulators, of two
+// rows next to each other, are its two values of an inner step.
+template <int S, typename Sync>
+__device__ __forceinline__ void multiply_lower(float *d, int l, int lane, Sync sync) {
     const int g = lane >> 2, t = lane & 3;
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+    const float *t11 = d, *t22 = d + 8 * S * kLd + 8 * S;
+    float *a21 = d + 8 * S * kLd;
     auto parts = [](float x, uint32_t &hi, uint32_t &lo) {
         hi = __float_as_uint(x) & 0xffffe000u;
         lo = __float_as_uint(x - __uint_as_float(hi));
     };
-    auto mma = [](float (&d)[4], const uint32_t (&x)[4], const uint32_t (&y)[2]) {
+    auto mma = [](float (&c)[4], const uint32_t (&x)[4], const uint32_t (&y)[2]) {
         asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y[0]), "r"(y[1]));
     };
+    float x[S][4], y[S / 2][2][4];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
+    for (int n = 0; n < S; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[n][i] = y[n / 2][n & 1][i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+        if (8 * k < l) continue;  // T11 has zeros there
         uint32_t ah[4], al[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) parts(a[(g + 8 * (i & 1)) * kLd + 8 * k + t + 4 * (i >> 1)], ah[i], al[i]);
+        for (int i = 0; i < 4; ++i) parts(t11[(8 * k + t + 4 * (i >> 1)) * kLd + l + g + 8 * (i & 1)], ah[i], al[i]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < S; ++n) {
             uint32_t bh[2], bl[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) parts(b[(8 * k + t + 4 * i) * kLd + 8 * n + g], bh[i], bl[i]);
-            mma(acc[n], al, bh);
-            mma(acc[n], ah, bl);
-            mma(acc[n], ah, bh);
+            for (int i = 0; i < 2; ++i) parts(a21[(8 * n + g) * kLd + 8 * k + t + 4 * i], bh[i], bl[i]);
+            mma(x[n], al, bh);
+            mma(x[n], ah, bl);
+            mma(x[n], ah, bh);
         }
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int k = 0; k < S; ++k) {
+        uint32_t bh[2][2], bl[2][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float2 *>(c + (g + 8 * i) * kLd + 8 * n + 2 * t) = make_float2(sign * acc[n][2 * i], sign * acc[n][2 * i + 1]);
+        for (int i = 0; i < 4; ++i) parts(x[k][i], bh[i >> 1][i & 1], bl[i >> 1][i & 1]);
+#pragma unroll
+        for (int m = k / 2; m < S / 2; ++m) {  // T22 has zeros in the rows before
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 v = *reinterpret_cast<const float2 *>(t22 + (16 * m + g + 8 * h) * kLd + 8 * k + 2 * t);
+                parts(v.x, ah[h], al[h]);
+                parts(v.y, ah[h + 2], al[h + 2]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                mma(y[m][c], al, bh[c]);
+                mma(y[m][c], ah, bl[c]);
+                mma(y[m][c], ah, bh[c]);
+            }
+        }
+    }
+    sync();
+#pragma unroll
+    for (int m = 0; m < S / 2; ++m)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2 *>(a21 + (16 * m + g + 8 * h) * kLd + l + 8 * c + 2 * t) = make_float2(-y[m][c][2 * h], -y[m][c][2 * h + 1]);
 }
 
 // T = (I + A)^-1 for the unit lower triangular 64 x 64 matrices of two heads (strictly lower part A, zeros above), by the
@@ -193,7 +223,7 @@ __device__ __forceinline__ void multiply_block(const float *a, const float *b, f
 // the blocks.  Substitution and not a power series: its error stays at the rounding of T however alike the keys are.
 // Substitution reads a value of A for every column, and a broadcast load fills the shared-memory pipe like any other: done
 // for all 64 columns it took 17400 cycles a block (4 blocks an SM), and takes 8000 this way with the products on the tensor
-// cores.  The upper right 32 x 32 blocks hold scratch at the end.
+// cores.
 __device__ __forceinline__ void invert(float *matrices, int tid) {
     const int warp = tid >> 5, lane = tid & 31;
     if (tid < 64) {  // 8 blocks, two columns a thread, pairs of rows
@@ -235,21 +265,9 @@ __device__ __forceinline__ void invert(float *matrices, int tid) {
     }
     __syncthreads();
     float *a = matrices + (warp >> 1) * (C * kLd);
-    {  // to 32 x 32, a warp a block; the product goes through the block's upper right quarter, zero again at the end
-        float *d = a + (warp & 1) * (32 * kLd + 32);
-        multiply_block<2, 2>(d + 16 * kLd, d, d + 16, 1.0f, lane);
-        __syncwarp();
-        multiply_block<2, 2>(d + 16 * kLd + 16, d + 16, d + 16 * kLd, -1.0f, lane);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) *reinterpret_cast<float4 *>(d + (i * 8 + (lane >> 2)) * kLd + 16 + (lane & 3) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    multiply_lower<2>(a + (warp & 1) * (32 * kLd + 32), 0, lane, [] { __syncwarp(); });  // to 32 x 32, a warp a block
     __syncthreads();
-    // to 64 x 64, half of the rows a warp
-    const int r = 16 * (warp & 1);
-    multiply_block<4, 4>(a + (32 + r) * kLd, a, a + r * kLd + 32, 1.0f, lane);
-    __syncthreads();
-    multiply_block<4, 4>(a + (32 + r) * kLd + 32, a + 32, a + (32 + r) * kLd, -1.0f, lane);
+    multiply_lower<4>(a, 16 * (warp & 1), lane, [] { __syncthreads(); });  // to 64 x 64, half of the columns a warp
     __syncthreads();
 }
 
