@@ -1086,102 +1086,126 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 
 // ------------------------------------------------------------------- join ----
 
-constexpr int kJoinThreads = 128;
-
-// First states of the segments from the third on (the first pass left the first two): S_{j+1} = S_j M_j + N_j, whose N the first pass left in S_{j+1}'s place.
-// Rows are independent: a warp takes ROWS of them through a whole sequence, 4 columns a lane, S by shuffles, while the next M
-// is on its way to shared memory.  In fp32 throughout.  Bound by the shared-memory pipe (M and the shuffles): fewer rows a
-// warp are faster as long as the blocks still fit on the card at once.
+// First states of the segments from the third on (the first pass left the first two): S_{j+1} = S_j M_j + N_j, whose N the
+// first pass left in S_{j+1}'s place.  In fp32 throughout.  Rows of S are independent: a block takes ROWS of them through a
+// whole sequence, with the next M on its way to shared memory.  A thread has 4 columns of up to 8 rows and a part of the
+// inner length, so that a value of M serves 8 rows and 16 warps hide one another's loads; the parts are added in order.  Bound
+// by latency: 2.4 us a segment with 16 rows a block, 1 us with up to 8 (a warp for 4 whole rows took 6.6).
 template <int PANELS, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) gdr_join_kernel(const __grid_constant__ FwdArgs p) {
-    constexpr int kLdS = 64 * PANELS;
+struct Join {
+    static constexpr int kLdS = 64 * PANELS, kColumns = kLdS / 4;  // threads for a row
+    static constexpr int threads = 256 * PANELS;
+    static constexpr int rows = ROWS < 8 ? ROWS : 8;               // of a thread
+    static constexpr int row_groups = ROWS / rows;
+    static constexpr int splits = threads / kColumns / row_groups, inner = kLdS / splits;
+    static_assert(inner % 4 == 0 && ROWS * kColumns <= threads, "");
+    static constexpr int step = 0, sums = step + 2 * kLdS * kLdS, state = sums + splits * ROWS * kLdS;  // floats from the start
+    static constexpr size_t smem = 128 + (state + ROWS * kLdS) * 4;
+};
+
+template <int PANELS, int ROWS>
+__global__ void __launch_bounds__(256 * PANELS) gdr_join_kernel(const __grid_constant__ FwdArgs p) {
+    using J = Join<PANELS, ROWS>;
+    constexpr int kLdS = J::kLdS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    float *steps = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));  // two of M
+    float *base = reinterpret_cast<float *>(smem_raw);
+    float *steps = base + J::step, *sums = base + J::sums, *state = base + J::state;
     __shared__ uint64_t full[2];
     __shared__ int abort;
     const ccv_gdr_args &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int groups = (a.dim_v + ROWS * 4 - 1) / (ROWS * 4);
-    const int first = (blockIdx.x % groups) * ROWS * 4, row0 = first + (threadIdx.x >> 5) * ROWS;
+    const int tid = threadIdx.x;
+    const int groups = (a.dim_v + ROWS - 1) / ROWS;
+    const int first = (blockIdx.x % groups) * ROWS;
     const int bh = blockIdx.x / groups;
     const int h = bh % a.num_v_heads, seq = bh / a.num_v_heads;
     wait_prior_grid();
     const int s = p.query_start_loc[seq], e = p.query_start_loc[seq + 1];
     const int line = p.cache_indices != nullptr ? p.cache_indices[seq] : seq;
     if (!sequence_ok(s, e, p.total_tokens) || (a.state != nullptr && line != a.pad_slot_id && (line < 0 || line >= a.num_lines))) {
-        if (threadIdx.x == 0 && first == 0 && h == 0) count_error(p.err_count);  // the passes cannot tell whose block would
+        if (tid == 0 && first == 0 && h == 0) count_error(p.err_count);  // the passes cannot tell whose block would
         return;
     }
     const int unit = p.seg_chunks * C;
     const int segments = (e - s + unit - 1) / unit, slot0 = first_slot(s, seq, unit);
     if (line == a.pad_slot_id || segments < 3) return;
 
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         abort = 0;
         mbar_init(&full[0], 1);
         mbar_init(&full[1], 1);
         mbar_init_fence();
     }
-    __syncthreads();
+    // S is zero past dim_k; M has no rows there.
+    for (int i = a.dim_k * kLdS + tid; i < kLdS * kLdS; i += J::threads) steps[i] = steps[kLdS * kLdS + i] = 0.0f;
     const uint32_t bytes = a.dim_k * kLdS * 4;
     auto fetch = [&](int j) {  // M of segment j, by one thread
         mbar_expect_tx(&full[j & 1], bytes);
         bulk_load(steps + (j & 1) * kLdS * kLdS, p.seg_step + (static_cast<int64_t>(slot0 + j) * a.num_v_heads + h) * a.dim_k * kLdS, bytes,
                   &full[j & 1]);
     };
-    if (threadIdx.x == 0) fetch(1);
-    const int column = lane * 4 % kLdS;  // with one panel the upper lanes repeat the lower ones
-    auto row_at = [&](int j, int r) {
-        return p.seg_state + ((static_cast<int64_t>(slot0 + j) * a.num_v_heads + h) * a.dim_v + min(row0 + r, a.dim_v - 1)) * kLdS + column;
+    // As one of the products' threads, and as one that adds up a row's sums.
+    const int column = tid % J::kColumns * 4, group = tid / J::kColumns;
+    const int row0 = group % J::row_groups * J::rows, split = group / J::row_groups;
+    const bool adds = group < ROWS, real = adds && first + group < a.dim_v;
+    auto row_at = [&](int j) {
+        return reinterpret_cast<float4 *>(p.seg_state + ((static_cast<int64_t>(slot0 + j) * a.num_v_heads + h) * a.dim_v + first + group) * kLdS + column);
     };
-    float4 x[ROWS];
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) x[r] = *reinterpret_cast<const float4 *>(row_at(1, r));
+    if (adds) *reinterpret_cast<float4 *>(state + group * kLdS + column) = real ? *row_at(1) : make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    if (tid == 0) fetch(1);
     for (int j = 1; j + 1 < segments; ++j) {
-        if (threadIdx.x == 0 && j + 2 < segments) fetch(j + 1);
-        float4 y[ROWS];
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) y[r] = *reinterpret_cast<const float4 *>(row_at(j + 1, r));
+        if (tid == 0 && j + 2 < segments) fetch(j + 1);
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (real) y = *row_at(j + 1);
         const bool ok = mbar_wait_warp(&full[j & 1], ((j - 1) >> 1) & 1, &abort);
-        const float *m = steps + (j & 1) * kLdS * kLdS + column;
-        auto add = [&](int k0, int step) {  // rows k0 .. + 3 of M; past dim_k S is 0, and M's last row stands in
-            float4 w[4];
+        const float *m = steps + ((j & 1) * kLdS + split * J::inner) * kLdS + column;
+        const float *x = state + row0 * kLdS + split * J::inner;
+        f32x2 acc[J::rows][2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const float4 *>(m + k0 * kLdS + (step > k ? k : step - 1) * kLdS);
+        for (int r = 0; r < J::rows; ++r) acc[r][0] = acc[r][1] = 0ull;
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                const float s4[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+        for (int k0 = 0; k0 < J::inner; k0 += 4) {
+            ulonglong2 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const ulonglong2 *>(m + (k0 + k) * kLdS);
+#pragma unroll
+            for (int r = 0; r < J::rows; ++r) {
+                const float4 v = *reinterpret_cast<const float4 *>(x + r * kLdS + k0);
+                const float s4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float v = __shfl_sync(kFullMask, s4[k], k0 >> 2);
-                    y[r].x = fmaf(v, w[k].x, y[r].x);
-                    y[r].y = fmaf(v, w[k].y, y[r].y);
-                    y[r].z = fmaf(v, w[k].z, y[r].z);
-                    y[r].w = fmaf(v, w[k].w, y[r].w);
+                    const f32x2 both = pack2(s4[k], s4[k]);
+                    acc[r][0] = fma2(both, w[k].x, acc[r][0]);
+                    acc[r][1] = fma2(both, w[k].y, acc[r][1]);
                 }
             }
-        };
-        const int whole = a.dim_k & ~3;
-#pragma unroll 4
-        for (int k0 = 0; k0 < whole; k0 += 4) add(k0, 4);
-        if (whole < a.dim_k) add(whole, a.dim_k - whole);
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            x[r] = y[r];
-            if (row0 + r < a.dim_v) *reinterpret_cast<float4 *>(row_at(j + 1, r)) = y[r];
         }
+#pragma unroll
+        for (int r = 0; r < J::rows; ++r)
+            *reinterpret_cast<ulonglong2 *>(sums + (split * ROWS + row0 + r) * kLdS + column) = make_ulonglong2(acc[r][0], acc[r][1]);
         if (!__syncthreads_and(ok)) {  // also: this M may be overwritten
-            if (threadIdx.x == 0) {
+            if (tid == 0) {
                 count_error(p.err_count);
                 int quiet = 0;
                 if (j + 2 < segments) mbar_wait(&full[(j + 1) & 1], (j >> 1) & 1, &quiet);
             }
             return;
         }
+        if (adds) {
+#pragma unroll
+            for (int i = 0; i < J::splits; ++i) {
+                const float4 v = *reinterpret_cast<const float4 *>(sums + (i * ROWS + group) * kLdS + column);
+                y.x += v.x;
+                y.y += v.y;
+                y.z += v.z;
+                y.w += v.w;
+            }
+            *reinterpret_cast<float4 *>(state + group * kLdS + column) = y;
+            if (real) *row_at(j + 1) = y;
+        }
+        __syncthreads();
     }
 }
-template <int PANELS>
-constexpr size_t join_smem() { return 128 + 2 * (64 * PANELS) * (64 * PANELS) * 4; }
 
 // ------------------------------------------------------------------- host ----
 
@@ -1241,13 +1265,14 @@ int launch_chunks(const FwdArgs &p, const FwdMaps &maps, int64_t units, cudaStre
 
 template <int PANELS, int ROWS>
 int launch_join(const FwdArgs &p, cudaStream_t stream) {
+    using J = Join<PANELS, ROWS>;
     int dev = 0;
     current_device_sms(&dev);
     cudaError_t err;
-    if (resident_blocks<gdr_join_kernel<PANELS, ROWS>>(kJoinThreads, join_smem<PANELS>(), dev, &err) == 0) return static_cast<int>(err);
-    const int64_t blocks = static_cast<int64_t>(p.batch) * p.a.num_v_heads * ((p.a.dim_v + 4 * ROWS - 1) / (4 * ROWS));
+    if (resident_blocks<gdr_join_kernel<PANELS, ROWS>>(J::threads, J::smem, dev, &err) == 0) return static_cast<int>(err);
+    const int64_t blocks = static_cast<int64_t>(p.batch) * p.a.num_v_heads * ((p.a.dim_v + ROWS - 1) / ROWS);
     if (blocks > 0x7fffffff) return CCV_ERR_SIZE;
-    return launch_pdl(gdr_join_kernel<PANELS, ROWS>, dim3(static_cast<unsigned>(blocks)), dim3(kJoinThreads), join_smem<PANELS>(), stream, p);
+    return launch_pdl(gdr_join_kernel<PANELS, ROWS>, dim3(static_cast<unsigned>(blocks)), dim3(J::threads), J::smem, stream, p);
 }
 
 template <int PANELS, bool VS, bool VIO>
@@ -1271,9 +1296,9 @@ int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
     if (status != CCV_OK) return status;
     const int64_t row_sets = static_cast<int64_t>(p.batch) * p.a.num_v_heads;
     const int sms = current_device_sms();
-    status = row_sets * ((p.a.dim_v + 3) / 4) <= sms   ? launch_join<PANELS, 1>(p, stream)
-             : row_sets * ((p.a.dim_v + 7) / 8) <= sms ? launch_join<PANELS, 2>(p, stream)
-                                                       : launch_join<PANELS, 4>(p, stream);
+    status = row_sets * ((p.a.dim_v + 3) / 4) <= sms   ? launch_join<PANELS, 4>(p, stream)
+             : row_sets * ((p.a.dim_v + 7) / 8) <= sms ? launch_join<PANELS, 8>(p, stream)
+                                                       : launch_join<PANELS, 16>(p, stream);
     if (status != CCV_OK) return status;
     return launch_chunks<PANELS, true, VS, VIO>(p, maps, segments, stream);
 }
@@ -1301,18 +1326,19 @@ bool use_chunked(int batch, int total_tokens, int dim_k) {
 }
 
 // Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device).  In
-// chunk times of a block (2.5 us): the first pass takes 0.95 of one a chunk, a join 0.8 a segment (2.5 where its blocks take
-// 4 rows a warp), and the two launches more take 3.5.  Each pass runs in waves of one block an SM.  11027 tokens take 232 us
-// with 16 heads and 124 with 4, against 475 and 446 whole; 1000 tokens and 4 heads, 58 against 59.
+// chunk times of a block (2.5 us): the first pass takes 0.95 of one a chunk, a join 0.4 a segment (1 where its blocks take 16
+// rows), and the two launches more take 3.5.  Each pass runs in waves of one block an SM.  11027 tokens take 210 us with 16
+// heads and 97 with 4, against 468 and 443 whole; 1000 tokens and 4 heads, 50 against 58; 4 x 2000 tokens and 8 heads, 103
+// against 106.
 int segment_chunks(int total_tokens, int batch, int num_v_heads, int dim_v) {
     constexpr int kSms = 152;
-    const int chunks = static_cast<int>((static_cast<int64_t>(total_tokens) + batch * C - 1) / (static_cast<int64_t>(batch) * C));
+    const int chunks = static_cast<int>((static_cast<int64_t>(total_tokens) + static_cast<int64_t>(batch) * C - 1) / (static_cast<int64_t>(batch) * C));
     const int slices = (dim_v + 127) / 128;
     const int64_t heads = static_cast<int64_t>(batch) * num_v_heads;
     auto waves = [](int64_t blocks) { return static_cast<double>((blocks + kSms - 1) / kSms); };
     const char *forced = std::getenv("CCV_GDR_SEGMENT");  // chunks of a segment (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;
-    const double join = heads * ((dim_v + 7) / 8) <= kSms ? 0.8 : 2.5;
+    const double join = heads * ((dim_v + 7) / 8) <= kSms ? 0.4 : 1.0;
     double best = waves(heads * slices) * chunks;
     int choice = 0;
     for (int n = 3; n <= 64 && n <= chunks; ++n) {
