@@ -3,6 +3,7 @@
 // The probabilities are never written: position i's are exp((l - m) / T) / z with the position's maximum m and sum z.
 // The draw is a race (the largest r_v / noise_v) and not a walk along cumulative sums, so the answer does not depend on
 // the order in which any sum is formed and every split of the vocabulary gives the same token.
+#include <algorithm>
 #include <cfloat>
 
 #include "ccv_common.cuh"
@@ -16,6 +17,7 @@ constexpr int kStep = kVerifyThreads * 8;  // logits of one pass of a block, 8 a
 constexpr int kVectors = 4;                // passes that a thread has in flight
 constexpr int kShare = kVectors * kStep;   // a block's share of a row in the draw, and in the statistics of small calls
 constexpr int kLongShare = 2 * kShare;     // in the statistics of large ones
+constexpr int kPickBlocks = 4, kPickBlocks32 = 3;  // blocks an SM of the draw, for bf16 and fp32 logits (2, 3, 5, 6 were slower)
 
 struct VerifyArgs {
     const void *logits;
@@ -33,7 +35,7 @@ struct VerifyArgs {
     int32_t *out_tokens, *num_accepted;
     int batch, drafts, vocab;
     int share, splits;  // logits of a block of the statistics, and such blocks a row
-    int shares;         // blocks a row of the draw
+    int shares, rounds;  // blocks a row of the draw, and how often each takes kShare logits
     float4 *stats;     // (batch, drafts + 1, splits): maximum, its index's bits, sum of exponentials
     float2 *best;      // (batch, shares): a share's best score and its index's bits
     unsigned *done;    // (batch): shares finished
@@ -239,23 +241,25 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 5 : 2) verify
     }
 }
 
-// Every share of a row repeats the acceptance (a few values), then races its part of the vocabulary; the share that ends
-// last joins them.  Bound by HBM and by the chain that opens it (sums, drafted tokens, their logits): 24 us for 84 MB at
-// 64 x 131072.
+// Every block of a row repeats the acceptance (a few values), then races its part of the vocabulary; the block that ends
+// last joins them.  Bound by HBM and by the chain around the race (sums, decision, logits, join): 20 us for 84 MB at
+// 64 x 131072, with all blocks on the card at once; 24 with a block for every 8192 logits.
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify_pick_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? kPickBlocks : kPickBlocks32) verify_pick_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ float sv[32];
     __shared__ int si[32];
     constexpr int kWarps = kVerifyThreads / 32;
     __shared__ float s_best[kWarps], s_z[kWarps];
     __shared__ int s_top[kWarps];
     __shared__ bool s_keep[kWarps], s_last;
-    wait_prior_grid();
-    release_next_grid();
+    // The statistics kernel lets this one start only after its own wait for what came before, so the caller's inputs are there
+    // already: the drafts' values are on their way while it ends.
     const int split = blockIdx.x % a.shares, b = blockIdx.x / a.shares;
     const int n = min(a.num_drafts != nullptr ? a.num_drafts[b] : a.drafts, a.drafts);
     int32_t *out = a.out_tokens + static_cast<int64_t>(b) * (a.drafts + 1);
     if (n < 0) {
+        wait_prior_grid();
+        release_next_grid();
         if (split == 0) {
             for (int i = threadIdx.x; i <= a.drafts; i += kVerifyThreads) out[i] = -1;
             if (threadIdx.x == 0) a.num_accepted[b] = 0;
@@ -267,23 +271,29 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify
     const T *row = static_cast<const T *>(a.logits) + b * a.tb;
     const float *noise = a.noise + b * a.nb;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // What the decision on a draft takes beside the sums.
+    int token = -1;
+    float logit = -INFINITY, q_token = 1.0f, u = 0.0f;
+    auto draft = [&](int i) {
+        token = -1;
+        if (i >= n) return;
+        token = a.tokens[b * a.db + i * a.dp];
+        u = a.uniform[b * a.ub + i * a.up];
+        if (token >= 0 && token < a.vocab) {
+            logit = clean(widen(row[i * a.tp + token]));
+            if (a.probs != nullptr) q_token = a.probs[b * a.pb + i * a.pp + token];
+        }
+    };
+    draft(warp);
+    wait_prior_grid();
+    release_next_grid();
     int kept = 0;
     float best, z;
     int first;  // of the largest logits of position `kept`
     for (int i0 = 0;; i0 += kWarps) {  // a warp a position; the last one (n) has no draft and ends the search
         const int i = i0 + warp;
         if (i <= n) {
-            // what the decision takes beside the sums, on its way before them
-            float logit = -INFINITY, q = 1.0f, u = 0.0f;
-            int token = -1;
-            if (i < n) {
-                token = a.tokens[b * a.db + i * a.dp];
-                u = a.uniform[b * a.ub + i * a.up];
-                if (token >= 0 && token < a.vocab) {
-                    logit = clean(widen(row[i * a.tp + token]));
-                    if (a.probs != nullptr) q = a.probs[b * a.pb + i * a.pp + token];
-                }
-            }
+            if (i0 > 0) draft(i);
             const float4 *st = a.stats + (static_cast<int64_t>(b) * (a.drafts + 1) + i) * a.splits;
             float m = -INFINITY, sum = 0.0f;
             int at = INT32_MAX;
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify
                 if (token >= 0 && token < a.vocab) {
                     float p = greedy && token == at && m > -INFINITY ? 1.0f : 0.0f;
                     if (!greedy && sum > 0.0f) p = Weigh(rate, m)(logit) / sum;
-                    keep = u * q < p;
+                    keep = u * q_token < p;
                 }
                 s_best[warp] = m;
                 s_z[warp] = sum;
@@ -339,26 +349,28 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify
         const int sure = kept < n && a.probs == nullptr ? a.tokens[b * a.db + kept * a.dp] : -1;
         // whole vectors where all three rows allow them
         const int before = static_cast<int>(reinterpret_cast<uintptr_t>(logits) % 16 / sizeof(T));
-        const int start = split * kShare - before;
+        const int start = split * a.rounds * kShare - before;
         const Weigh weigh(rate, best);
         const float inv_z = 1.0f / z;
         const bool vn = reinterpret_cast<uintptr_t>(noise + start) % 16 == 0;
         const bool vq = q != nullptr && reinterpret_cast<uintptr_t>(q + start) % 16 == 0;
+        for (int round = 0; round < a.rounds; ++round) {
 #pragma unroll
-        for (int j = 0; j < kVectors; ++j) {
-            const int v0 = start + j * kStep + threadIdx.x * 8;
-            float x[8], w[8], y[8] = {};
-            load8(logits, v0, a.vocab, x);
-            load8_plain(noise, v0, a.vocab, vn && v0 >= 0, w);
-            if (q != nullptr) load8_plain(q, v0, a.vocab, vq && v0 >= 0, y);
+            for (int j = 0; j < kVectors; ++j) {
+                const int v0 = start + (round * kVectors + j) * kStep + threadIdx.x * 8;
+                float x[8], w[8], y[8] = {};
+                load8(logits, v0, a.vocab, x);
+                load8_plain(noise, v0, a.vocab, vn && v0 >= 0, w);
+                if (q != nullptr) load8_plain(q, v0, a.vocab, vq && v0 >= 0, y);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float r = fmaf(weigh(clean(x[k])), inv_z, -y[k]);
-                if (v0 + k == sure) r = 0.0f;
-                const float score = r * rcp_approx(w[k]);
-                if (score > top) {  // never so for r <= 0
-                    top = score;
-                    index = v0 + k;
+                for (int k = 0; k < 8; ++k) {
+                    float r = fmaf(weigh(clean(x[k])), inv_z, -y[k]);
+                    if (v0 + k == sure) r = 0.0f;
+                    const float score = r * rcp_approx(w[k]);
+                    if (score > top) {  // never so for r <= 0
+                        top = score;
+                        index = v0 + k;
+                    }
                 }
             }
         }
@@ -388,11 +400,18 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify
 }
 
 // Shares of a row: its logits and what is before them up to a 16-byte boundary (see verify_stats_kernel), `before` at most.
-int64_t shares_of(int vocab, int share, int before = 7) { return (static_cast<int64_t>(vocab) + before + share - 1) / share; }
+int64_t shares_of(int vocab, int64_t share, int before = 7) { return (static_cast<int64_t>(vocab) + before + share - 1) / share; }
 
 // A block of the statistics takes a long share once that still fills the card (8 blocks an SM): each thread then loads its
 // second 4 vectors under the first 4's arithmetic.  Below that, shorter shares spread a row over more SMs.
 int stats_share(int64_t rows, int vocab) { return rows * shares_of(vocab, kLongShare) >= 8 * 152 ? kLongShare : kShare; }
+
+// How often a block of the draw takes kShare logits: as often as keeps all rows' blocks on the card at once, since each repeats
+// the chain up to the race.
+int64_t pick_rounds(int batch, int64_t shares, int resident) {
+    const int64_t blocks = std::max<int64_t>(1, resident * 152 / batch);
+    return (shares + blocks - 1) / blocks;
+}
 
 int64_t stats_blocks(int batch, int drafts, int vocab) {
     const int64_t rows = static_cast<int64_t>(batch) * (drafts + 1);
@@ -447,12 +466,13 @@ extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t
     const int share = stats_share(static_cast<int64_t>(batch) * (drafts + 1), vocab);
     const int size = logits_fp32 ? 4 : 2;
     const int before = aligned16(target_logits) && t_stride_b * size % 16 == 0 && t_stride_pos * size % 16 == 0 ? 0 : 7;
-    const int64_t shares = shares_of(vocab, kShare, before), splits = shares_of(vocab, share, before);
+    const int64_t rounds = pick_rounds(batch, shares_of(vocab, kShare, before), logits_fp32 ? kPickBlocks32 : kPickBlocks);
+    const int64_t shares = shares_of(vocab, rounds * kShare, before), splits = shares_of(vocab, share, before);
     uint8_t *space = static_cast<uint8_t *>(workspace), *best = space + stats_blocks(batch, drafts, vocab) * 16;
     const VerifyArgs a{target_logits, t_stride_b, t_stride_pos, draft_tokens, d_stride_b, d_stride_pos, draft_probs, p_stride_b,
                        p_stride_pos, num_drafts, temperature, uniform, u_stride_b, u_stride_pos, noise, n_stride_b, out_tokens,
                        num_accepted, batch, drafts, vocab, share, static_cast<int>(splits),
-                       static_cast<int>(shares), reinterpret_cast<float4 *>(space), reinterpret_cast<float2 *>(best),
+                       static_cast<int>(shares), static_cast<int>(rounds), reinterpret_cast<float4 *>(space), reinterpret_cast<float2 *>(best),
                        reinterpret_cast<unsigned *>(best + batch * shares * 8), err_count};
     return logits_fp32 ? launch_verify<float>(a, stream) : launch_verify<uint16_t>(a, stream);
 }
