@@ -446,7 +446,7 @@ extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t
                       n_stride_b})
         if (s < 0) return CCV_ERR_STRIDE;
     if (batch == 0) return CCV_OK;
-    if (vocab == 0 || static_cast<int64_t>(batch) * (drafts + 1) * shares_of(vocab, kShare) > 0x7fffffff) return CCV_ERR_SIZE;
+    if (vocab == 0 || vocab > (1 << 30) || static_cast<int64_t>(batch) * (drafts + 1) * shares_of(vocab, kShare) > 0x7fffffff) return CCV_ERR_SIZE;
     if (target_logits == nullptr || noise == nullptr || out_tokens == nullptr || num_accepted == nullptr ||
         (drafts > 0 && (draft_tokens == nullptr || uniform == nullptr)))
         return CCV_ERR_NULL_POINTER;

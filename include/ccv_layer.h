@@ -158,7 +158,7 @@ int residual_rms_norm(const void *x, int64_t x_stride_tok, int64_t x_stride_dim,
 /*
  * spec_verify -- accepts or rejects drafted tokens against the target model's
  * probabilities, from given random numbers.
- * target_logits (batch, num_positions = drafts + 1, vocab), vocab stride 1,
+ * target_logits (batch, num_positions = drafts + 1, vocab <= 2^30), stride 1,
  *               bf16 or (logits_fp32) fp32: position i predicts the token
  *               after draft i-1.  p_i = softmax(logits_i / temperature).
  *               -inf and NaN logits have probability 0; +inf counts as the

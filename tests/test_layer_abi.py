@@ -236,3 +236,9 @@ def test_binding_refusals_on_gpu_tensors():
     refuse(ValueError, ccv.spec_verify, f32(2, 9, 3).transpose(1, 2), t, u, n)
     refuse(TypeError, ccv.spec_verify, lg, t.long(), u, n)
     refuse(ccv.CcvError, ccv.spec_verify, lg, t, u, n, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))
+
+
+def test_size_limits(lib):
+    assert verify(lib, vocab=(1 << 30) + 1, wsb=1 << 62) == SIZE
+    args = _lib.GdrArgs()
+    assert lib.gdr_fwd(ctypes.byref(args), Q, 1, None, None, (1 << 30) + 1, S, 1 << 62, None, None) == SIZE

@@ -56,6 +56,13 @@ def test_rows_and_drafts(ccv, b, s):
     check(ccv, make(b, s, 513, b + s, draft=False))
 
 
+@pytest.mark.parametrize("b,v,dtype", [(128, 40000, torch.bfloat16), (131, 39999, torch.bfloat16), (250, 20004, torch.float32),
+                                       (700, 9001, torch.bfloat16)])
+def test_many_rows(ccv, b, v, dtype):
+    """More shares of the vocabulary than blocks fit on the card: a block of the draw goes round several times."""
+    check(ccv, make(b, 1, v, b, dtype))
+
+
 def test_ragged_and_padded(ccv):
     d = make(9, 4, 1001, 3)
     check(ccv, d, num_drafts=torch.tensor([4, 0, 1, 2, 3, -1, 4, -5, 2], dtype=torch.int32))
