@@ -545,7 +545,7 @@ struct Stage {
 
 struct ChunkSmem {
     uint64_t full[kStages], empty[kStages];               // a stage is loaded; its chunk's MMAs, the last to use it, are done
-    uint64_t mma_p, mma_o, mma_n, mma_delta[2], mma_out;  // completed by the tensor cores
+    uint64_t mma_p, mma_o, mma_n[2], mma_delta[2], mma_out;  // completed by the tensor cores
     uint64_t have_s[2], have_r[2], have_vs[2];            // arrived on by the compute threads, by halves
     uint64_t have_read, have_d;
     uint64_t out_full, out_free;                          // the output tile: written by them, stored by one warp
@@ -621,8 +621,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     if (tid == 0) {
         sm.abort = 0;
         for (uint64_t &b : sm.full) mbar_init(&b, kLoaders + 1);
-        for (uint64_t *b : {&sm.empty[0], &sm.empty[1], &sm.mma_p, &sm.mma_o, &sm.mma_n, &sm.mma_delta[0], &sm.mma_delta[1], &sm.mma_out,
-                            &sm.drain})
+        for (uint64_t *b : {&sm.empty[0], &sm.empty[1], &sm.mma_p, &sm.mma_o, &sm.mma_n[0], &sm.mma_n[1], &sm.mma_delta[0],
+                            &sm.mma_delta[1], &sm.mma_out, &sm.drain})
             mbar_init(b, 1);
         for (uint64_t *b : {&sm.have_s[0], &sm.have_s[1]}) mbar_init(b, kCompute / 2);
         for (uint64_t *b : {&sm.have_r[0], &sm.have_r[1], &sm.have_vs[0], &sm.have_vs[1], &sm.have_read, &sm.have_d, &sm.out_full})
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 const int key = q * 16 * PANELS + j * 16;
                 return ((key / 64) * 2 * kTile + (key % 64) * 2) / 16;
             };
-            constexpr uint32_t kTokens = mma_desc(128, C, false), kKeys = mma_desc(128, 32 * PANELS, true);
+            constexpr uint32_t kTokens = mma_desc(128, C, false), kLateTokens = mma_desc(128, C / 2, false), kKeys = mma_desc(128, 32 * PANELS, true);
             int c = 0;
             for (; c < chunks; ++c) {
                 const uint32_t par = c & 1;
@@ -670,24 +670,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 }
                 if (!ok) break;
                 mma_commit(&sm.mma_p, el);
-                if (FULL && c > 0 && !mbar_wait_warp(&sm.mma_out, par ^ 1, &sm.abort)) break;  // it reads d's second part
-                // d^T = R^T T^T: the six products of parts above 2^-24, for tokens 0 .. 31 of the sum, then the others
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!(ok = mbar_wait_warp(&sm.have_r[half], par, &sm.abort))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int sum = 0; sum < 3; ++sum)
-#pragma unroll
-                        for (int part = 0; part <= sum; ++part)
-#pragma unroll
-                            for (int ks = 2 * half; ks < 2 * half + 2; ++ks)
-                                mma_ts(tmem + kColN, tmem + r_part(ks, part), head + (kT + (sum - part) * kTile + ks * 32) / 16, kTokens,
-                                       sum + part + ks > 0, el);
-                }
-                if (!ok) break;
-                mma_commit(&sm.mma_n, el);
-                // S^T q^T, once the previous chunk's output has left these columns
+                // S^T q^T, once the previous chunk's output has left these columns, while R is made
                 if constexpr (FULL) {
                     if (!mbar_wait_warp(&sm.have_read, par, &sm.abort)) break;
                     tc_fence_after();
@@ -701,8 +684,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                                        part + q + j > 0, el);
                     mma_commit(&sm.mma_o, el);
                 }
+                // d^T = R^T T^T: the six products of parts above 2^-24, for tokens 0 .. 31 of the sum, then the others, which are
+                // parts of d's last 32 tokens alone.  (d's second part of the chunk before, in these columns, is out with its output.)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = mbar_wait_warp(&sm.have_r[half], par, &sm.abort))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int sum = 0; sum < 3; ++sum)
+#pragma unroll
+                        for (int part = 0; part <= sum; ++part)
+#pragma unroll
+                            for (int ks = 2 * half; ks < 2 * half + 2; ++ks)
+                                mma_ts(tmem + kColN + 32 * half, tmem + r_part(ks, part),
+                                       head + (kT + (sum - part) * kTile + ks * 32 + half * (kTile / 2)) / 16, half ? kLateTokens : kTokens,
+                                       sum + part + ks > 0, el);
+                    mma_commit(&sm.mma_n[half], el);
+                }
+                if (!ok) break;
                 if (!mbar_wait_warp(&sm.have_vs[0], par, &sm.abort)) break;
-                if (FULL && !mbar_wait_warp(&sm.mma_o, par, &sm.abort)) break;  // S is about to be overwritten
                 // what the chunk adds to S^T: tokens are the inner axis, so the keys are read MN-major; those of two
                 // warpgroups at a time
                 auto add = [&](int g, int half) {
@@ -729,9 +729,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 #pragma unroll
                     for (int term = 0; term < 3; ++term)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(tmem + kColO, tmem + d_part(ks, term == 1), head + (kP + (term == 2 ? kTile : 0) + ks * 32) / 16, kTokens,
+                        for (int ks = 0; ks < 4; ++ks) {
+                            const int half = ks / 2;
+                            mma_ts(tmem + kColO + 32 * half, tmem + d_part(ks, term == 1),
+                                   head + (kP + (term == 2 ? kTile : 0) + ks * 32 + half * (kTile / 2)) / 16, half ? kLateTokens : kTokens,
                                    term + ks > 0, el);
+                        }
                     mma_commit(&sm.mma_out, el);
                 }
                 mma_commit(&sm.empty[c % kStages], el);
@@ -920,6 +923,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             tc_fence_before();
             mbar_arrive(&sm.have_s[q >> 1]);
 
+            if constexpr (FULL) {
+                if (c > 0) {  // the output of the chunk before, while the tensor cores are at S k
+                    if (!(ok = mbar_wait_warp(&sm.mma_out, par ^ 1, &sm.abort))) break;
+                    tc_fence_after();
+                    if (!(ok = finish(c - 1))) break;
+                } else {
+                    mbar_arrive(&sm.have_read);
+                }
+            }
+
             // b v of this thread's tokens
             if (!(ok = mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
             const float *f = reinterpret_cast<const float *>(stage(c) + St::head + kVec) + 8 * q;
@@ -971,26 +984,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 }
             }
 
-            if constexpr (FULL) {
-                if (c > 0) {  // the output of the chunk before, while the tensor cores are at d
-                    if (!(ok = mbar_wait_warp(&sm.mma_out, par ^ 1, &sm.abort))) break;
-                    tc_fence_after();
-                    if (!(ok = finish(c - 1))) break;
-                } else {
-                    mbar_arrive(&sm.have_read);
-                }
-            }
-
             // d, decayed for the state (3 parts) and for the output (2)
-            if (!(ok = mbar_wait_warp(&sm.mma_n, par, &sm.abort))) break;
-            tc_fence_after();
             {
                 float x[2][8];
-                tmem_load(lanes + kColN + 8 * q, x[0]);
-                tmem_load(lanes + kColN + 32 + 8 * q, x[1]);
-                tmem_wait_load();
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
+                    if (!(ok = mbar_wait_warp(&sm.mma_n[half], par, &sm.abort))) break;
+                    tc_fence_after();
+                    tmem_load(lanes + kColN + 32 * half + 8 * q, x[half]);
+                    tmem_wait_load();
                     uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
@@ -1007,6 +1009,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                     tc_fence_before();
                     mbar_arrive(&sm.have_vs[half]);
                 }
+                if (!ok) break;
                 if constexpr (FULL) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
