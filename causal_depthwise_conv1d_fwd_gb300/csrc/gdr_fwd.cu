@@ -9,6 +9,7 @@
 //   gdr_prep_kernel   for every chunk and key head at once: the two products, the decays, T = (I + A)^-1, P, and what each
 //                     token multiplies by; written to the workspace in the layout the tensor cores read.
 //   gdr_chunk_kernel  for every sequence and value head: the chunks in order with S^T kept on chip.
+// 4 x 4096 tokens with 32 value heads take 271 us: 95 + 172, and what the launches cost.
 // Where sequences and heads are too few for the card, each sequence is cut into segments of chunks.  A segment takes its
 // first state to S M + N; gdr_chunk_kernel first finds N (the segment from a zero state) and M (from the identity, without
 // values) of all segments at once, gdr_join_kernel goes through them for each segment's first state, and gdr_chunk_kernel
@@ -271,6 +272,9 @@ __device__ __forceinline__ void invert(float *matrices, int tid) {
     __syncthreads();
 }
 
+// A block of 4 warps a (chunk, key head), 4 blocks an SM: 4096 of them (4 x 4096 tokens, 16 key and 32 value heads) take 95 us.
+// It writes 344 MB, 3.6 TB/s; what bounds it is latency (44% of the issue slots, 50% of the shared-memory pipe): loads that
+// wait on the search, 14 barriers, and forward substitution.  3, 5 and 6 blocks an SM and 8 warps a block were slower.
 // PANELS: dim_k rounded up to 64 PANELS.  V: rows of q and k allow 16-byte vectors.
 template <int PANELS, bool V>
 __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_constant__ FwdArgs p) {
@@ -555,6 +559,14 @@ struct ChunkSmem {
     int seq, start, end;
 };
 
+// S^T (128 rows of values on the lanes of tensor memory) stays in registers; its three bf16 parts, R's and d's go to tensor
+// memory as the A operands.  16 warps do the arithmetic, one issues MMAs, two load the next chunk and one stores the output.
+// The chunks are a chain of product, split into parts, product: S k^T, R, d = T R, decayed d, what is added to S.  Of the
+// 2.7 us (5150 cycles) of a chunk the tensor cores work 3200: 24 + 24 products of 32 cycles for S k and d, 16 for S q, 24 for
+// the state, 12 for the output.  The rest is splitting (the sixteen warps' integer and conversion pipes: 1200 cycles for S,
+// 350 for each half of R and d) and 240 cycles from each commit to the waiting warps; halves of R, d and S overlap the two.
+// 4 x 4096 tokens, 32 heads: 128 blocks, 172 us; a block is 640 threads with all registers and all tensor memory of its SM.
+//
 // FULL: outputs and final states.  Otherwise the first pass over segments: N of all but the last, and M of those between
 // (the last block of every group of slices + 1).  V: the state allows 16-byte vectors.  VIO: rows of q, k, v and out do.
 template <int PANELS, bool FULL, bool V, bool VIO>
@@ -684,8 +696,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                                        part + q + j > 0, el);
                     mma_commit(&sm.mma_o, el);
                 }
-                // d^T = R^T T^T: the six products of parts above 2^-24, for tokens 0 .. 31 of the sum, then the others, which are
-                // parts of d's last 32 tokens alone.  (d's second part of the chunk before, in these columns, is out with its output.)
+                // d^T = R^T T^T: the six products of parts above 2^-24, for tokens 0 .. 31 of the sum, then the others.  T is lower
+                // triangular: these are parts of d's last 32 tokens alone, and the compute threads take up the first 32 meanwhile.
+                // (N = 32 costs the tensor cores what N = 64 does.  What had these columns left with the last output.)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (!(ok = mbar_wait_warp(&sm.have_r[half], par, &sm.abort))) break;
@@ -729,12 +742,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 #pragma unroll
                     for (int term = 0; term < 3; ++term)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            const int half = ks / 2;
-                            mma_ts(tmem + kColO + 32 * half, tmem + d_part(ks, term == 1),
-                                   head + (kP + (term == 2 ? kTile : 0) + ks * 32 + half * (kTile / 2)) / 16, half ? kLateTokens : kTokens,
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts(tmem + kColO, tmem + d_part(ks, term == 1), head + (kP + (term == 2 ? kTile : 0) + ks * 32) / 16, kTokens,
                                    term + ks > 0, el);
-                        }
                     mma_commit(&sm.mma_out, el);
                 }
                 mma_commit(&sm.empty[c % kStages], el);

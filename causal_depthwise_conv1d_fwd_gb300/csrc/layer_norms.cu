@@ -2,7 +2,8 @@
 // and scale, the residual addition, and the norm that opens the next block).
 //
 // Both read each element once, keep the row in registers in fp32, reduce it, and write once: 6 bytes an element for the
-// first, 8 to 14 for the second, so HBM bounds them at any size that fills the card and one launch's latency below.
+// first, 8 to 14 for the second, so HBM bounds them at any size that fills the card (16384 x 32 x 128 with gate: 66 us,
+// 6.1 TB/s; 8191 x 4096 with a post norm, channel gate and fp32 residual: 65 us, 6.2 TB/s) and one launch's latency below.
 // A row belongs to LPR lanes: within a warp the reductions are shuffles; longer rows reduce over the block's warps.
 #include "ccv_common.cuh"
 #include "ccv_layer.h"
