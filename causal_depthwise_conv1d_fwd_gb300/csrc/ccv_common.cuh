@@ -108,7 +108,9 @@ __device__ __forceinline__ void store_plain(uint16_t *p, const Raw<VEC> &r) {
 // kernel has completed and its writes are visible.  release_next_grid() lets
 // the next kernel of the stream be scheduled; it only ever starts early, and
 // it waits in its own wait_prior_grid() for this kernel to complete.  Without
-// a programmatic predecessor the wait returns at once.
+// a programmatic predecessor the wait returns at once.  The later kernels of
+// one call may read the caller's inputs before their wait: they start once
+// every block before them is past its own, and the call writes no input.
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_next_grid() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -81,7 +81,10 @@ __device__ __forceinline__ bool sequence_ok(int s, int e, int total) { return s 
 // Swizzled tiles need shared memory on a 1024-byte boundary.
 __device__ __forceinline__ bool misplaced(const void *smem, int *err_count) {
     const bool bad = (smem_u32(smem) & 1023u) != 0;
-    if (bad && threadIdx.x == 0) count_error(err_count);
+    if (bad) {
+        wait_prior_grid();
+        if (threadIdx.x == 0) count_error(err_count);
+    }
     return bad;
 }
 
@@ -287,6 +290,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hk = blockIdx.x % a.num_k_heads, slot = blockIdx.x / a.num_k_heads;
     wait_prior_grid();
+    release_next_grid();
     if (misplaced(smem_raw, p.err_count)) return;
 
     if (warp == 0) {
@@ -586,7 +590,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     const int bh = blockIdx.x / types;
     const int h = bh % a.num_v_heads, slot = bh / a.num_v_heads;
     const int hk = h / (a.num_v_heads / a.num_k_heads);
-    wait_prior_grid();
+    // The kernels before this one let it start only after their own wait, so the caller's tensors are as they will stay: this
+    // one reads them, and waits before it reads what those wrote or writes anything.
     if (misplaced(smem_raw, p.err_count)) return;
 
     int seq = slot, segment = 0, s, e;
@@ -611,18 +616,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     const bool good = sequence_ok(s, e, p.total_tokens) && (a.state == nullptr || line == a.pad_slot_id || (line >= 0 && line < a.num_lines));
     if (p.seg_chunks > 0) segment = slot - first_slot(s, seq, p.seg_chunks * C);
     if (!good) {
+        wait_prior_grid();
         if (FULL && p.seg_chunks == 0 && tid == 0 && slice == 0 && h == 0) count_error(p.err_count);
         return;
     }
-    if (e == s || line == a.pad_slot_id) return;
+    if (e == s || line == a.pad_slot_id) {
+        wait_prior_grid();
+        return;
+    }
     int chunks = (e - s + C - 1) / C;
     int slot0 = first_slot(s, seq, C);
     bool last = true;  // segment of the sequence
     if (p.seg_chunks > 0) {
         const int segments = (chunks + p.seg_chunks - 1) / p.seg_chunks;
-        if (segment < 0 || segment >= segments) return;
         last = segment == segments - 1;
-        if (!FULL && (last || (step_only && segment == 0))) return;
+        if (segment < 0 || segment >= segments || (!FULL && (last || (step_only && segment == 0)))) {
+            wait_prior_grid();
+            return;
+        }
         const int c0 = segment * p.seg_chunks;
         chunks = min(p.seg_chunks, chunks - c0);
         slot0 += c0;
@@ -756,6 +767,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 mbar_wait_warp(&sm.drain, 0, &quiet);
             }
         } else if (warp == kStoreWarp) {
+            wait_prior_grid();
+            release_next_grid();
             const int width = min(128, a.dim_v - slice * 128);
             uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + slice * 128 * a.out.stride_dim;
             for (int c = 0; FULL && c < chunks; ++c) {
@@ -789,7 +802,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 // Whole chunks come as tensor tiles; a sequence's last rows, which need zeros after them, piece by piece.
                 const bool whole = VIO && maps.use && n == C;
                 if (id == 0 && c + 1 < chunks) {  // the stage frees up late: let L2 have the next chunk's part by then
-                    bulk_prefetch(heads + (c + 1) * heads_step, kHeadBytes);
+                    if (c > 0) bulk_prefetch(heads + (c + 1) * heads_step, kHeadBytes);
                     if (VIO && maps.use) {
                         if (!step_only)
                             for (int i = 0; i < 2; ++i) tensor_prefetch(&maps.v, slice * 128 + i * 64, h, t0 + C);
@@ -811,10 +824,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                             for (int i = 0; i < 2; ++i) tensor_load(st + St::v + i * kTile, &maps.v, slice * 128 + i * 64, h, t0, bar);
                     }
                     const uint8_t *src = heads + c * heads_step;
+                    if (FULL && whole)
+                        for (int i = 0; i < PANELS; ++i) tensor_load(st + i * 2 * kTile + kTile, &maps.q, i * 64, hk, t0, bar);
+                    if (c == 0) {
+                        wait_prior_grid();
+                        if (chunks > 1) bulk_prefetch(heads + heads_step, kHeadBytes);
+                    }
                     if constexpr (FULL) {
                         bulk_load(st + St::head, src, kHeadBytes, bar);
-                        if (whole)
-                            for (int i = 0; i < PANELS; ++i) tensor_load(st + i * 2 * kTile + kTile, &maps.q, i * 64, hk, t0, bar);
                     } else {  // without P
                         bulk_load(st + St::head + kT, src + kT, kP - kT, bar);
                         bulk_load(st + St::head + kVec, src + kVec, kHeadBytes - kVec, bar);
@@ -853,6 +870,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         // the first pass keeps the state it read for it.
         const bool kept = FULL && !(segment == 0 && last);
         const float *from = kept ? in_segment(p.seg_state, slot, a.dim_v) : segment == 0 && init ? pool : nullptr;
+
+        if (kept || (!FULL && segment == 0)) wait_prior_grid();  // the join's states; and the first segment's goes to the workspace
 
         f32x2 st[KH / 2];  // this thread's part of row d of S
 #pragma unroll
@@ -1132,6 +1151,7 @@ __global__ void __launch_bounds__(256 * PANELS) gdr_join_kernel(const __grid_con
     const int bh = blockIdx.x / groups;
     const int h = bh % a.num_v_heads, seq = bh / a.num_v_heads;
     wait_prior_grid();
+    release_next_grid();
     const int s = p.query_start_loc[seq], e = p.query_start_loc[seq + 1];
     const int line = p.cache_indices != nullptr ? p.cache_indices[seq] : seq;
     if (!sequence_ok(s, e, p.total_tokens) || (a.state != nullptr && line != a.pad_slot_id && (line < 0 || line >= a.num_lines))) {
@@ -1340,9 +1360,9 @@ bool use_chunked(int batch, int total_tokens, int dim_k) {
 
 // Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device).  In
 // chunk times of a block (2.5 us): the first pass takes 0.95 of one a chunk, a join 0.4 a segment (1 where its blocks take 16
-// rows), and the two launches more take 3.5.  Each pass runs in waves of one block an SM.  11027 tokens take 210 us with 16
-// heads and 97 with 4, against 468 and 443 whole; 1000 tokens and 4 heads, 50 against 58; 4 x 2000 tokens and 8 heads, 103
-// against 106.
+// rows), and the two launches more take 3.5.  Each pass runs in waves of one block an SM.  11027 tokens take 200 us with 16
+// heads and 92 with 4, against 457 and 433 whole; 1000 tokens and 4 heads, 48 against 51; 4 x 2000 tokens and 8 heads, 97
+// against 102.
 int segment_chunks(int total_tokens, int batch, int num_v_heads, int dim_v) {
     constexpr int kSms = 152;
     const int chunks = static_cast<int>((static_cast<int64_t>(total_tokens) + static_cast<int64_t>(batch) * C - 1) / (static_cast<int64_t>(batch) * C));
