@@ -13,6 +13,7 @@ from .api import PAD_SLOT_ID, Launch, _check, _stream
 
 _ACTIVATIONS = {None: 0, "silu": 1, "swish": 1, "sigmoid": 2}
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_Tensor, _empty, _empty_like, _ONE = torch.Tensor, torch.empty, torch.empty_like, (1,)
 
 # struct ccv_heads_view and struct ccv_gdr_args of include/ccv_layer.h.  A call
 # passes them packed into bytes: building ctypes structures field by field costs
@@ -67,7 +68,7 @@ class ScratchLaunch(Launch):
 
 def _need(dev: int, t: torch.Tensor, name: str, *dtypes):
     """t is a tensor of the call's CUDA device and of one of the types."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, _Tensor) or t.device.type != "cuda":
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
@@ -79,18 +80,18 @@ def _need(dev: int, t: torch.Tensor, name: str, *dtypes):
 
 def _device(t) -> int:
     """The device index of a call's first tensor (-1: not a CUDA tensor)."""
-    return t.get_device() if isinstance(t, torch.Tensor) else -1
+    return t.get_device() if isinstance(t, _Tensor) else -1
 
 
 def _vector(dev: int, t: Optional[torch.Tensor], name: str, dtype, length: int):
     """Pointer of a contiguous vector of at least `length` entries, or None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
         _need(dev, t, name, dtype)
-    if t.dim() != 1 or t.stride(0) != 1:
+    if t.stride() != _ONE:
         raise ValueError(f"{name} must be a contiguous 1-D tensor")
-    if t.shape[0] < length:
+    if t.numel() < length:
         raise ValueError(f"{name} has {t.shape[0]} entries, needs {length}")
     return t.data_ptr()
 
@@ -101,7 +102,7 @@ def _err(dev: int, t: Optional[torch.Tensor]):
 
 def _workspace(dev: int, given: Optional[torch.Tensor], size: int, like: torch.Tensor):
     if given is None:
-        return torch.empty(size, dtype=_U8, device=like.device)
+        return _empty(size, dtype=_U8, device=like.device)
     _need(dev, given, "workspace", _U8)
     if given.dim() != 1 or (given.shape[0] and given.stride(0) != 1):
         raise ValueError("workspace must be a contiguous 1-D tensor")
@@ -116,9 +117,9 @@ def _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slo
         raise ValueError("a_log and dt_bias go together")
     dev = _device(v)
     dtype = _F32 if a_log is None else _BF16
-    if not (dev >= 0 and v.dtype is _BF16 and isinstance(k, torch.Tensor) and k.dtype is _BF16
-            and isinstance(q, torch.Tensor) and q.dtype is _BF16 and isinstance(g, torch.Tensor)
-            and g.dtype is dtype and isinstance(beta, torch.Tensor) and beta.dtype is dtype
+    if not (dev >= 0 and v.dtype is _BF16 and isinstance(k, _Tensor) and k.dtype is _BF16
+            and isinstance(q, _Tensor) and q.dtype is _BF16 and isinstance(g, _Tensor)
+            and g.dtype is dtype and isinstance(beta, _Tensor) and beta.dtype is dtype
             and k.get_device() == q.get_device() == g.get_device() == beta.get_device() == dev):
         for t, name in ((v, "v"), (k, "k"), (q, "q")):
             _need(dev, t, name, _BF16)
@@ -132,8 +133,9 @@ def _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slo
         raise ValueError("q and k must have the same shape, and v the same tokens")
     hv, dv = vs[lead:]
     hk, dk = ks[lead:]
-    if g.shape != vs[:-1] or beta.shape != vs[:-1]:
-        raise ValueError(f"g and beta must have shape {tuple(vs[:-1])}")
+    heads = vs[:-1]
+    if g.shape != heads or beta.shape != heads:
+        raise ValueError(f"g and beta must have shape {tuple(heads)}")
     gs = g.stride()
     if beta.stride() != gs:
         raise ValueError("g and beta must have the same strides")
@@ -144,30 +146,34 @@ def _pack_gdr(q, k, v, g, beta, state, scale, qk_l2norm, a_log, dt_bias, pad_slo
         if a_log.shape[0] != hv or dt_bias.shape[0] != hv:
             raise ValueError(f"a_log and dt_bias must have {hv} entries")
     if state is not None:
-        if not isinstance(state, torch.Tensor) or state.dtype is not _F32 or state.get_device() != dev:
+        if not isinstance(state, _Tensor) or state.dtype is not _F32 or state.get_device() != dev:
             _need(dev, state, "state", _F32)
         lines = state.shape[0]
         if state.shape != (lines, hv, dv, dk):
             raise ValueError("state must be (num_lines, num_v_heads, dim_v, dim_k)")
         ss, sp = state.stride(), state.data_ptr()
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty_like(v)
     else:
         _need(dev, out, "out", _BF16)
         if out.shape != vs:
             raise ValueError("out must have v's shape")
-    qs, ks_, vst, os_ = q.stride(), k.stride(), v.stride(), out.stride()
-    if mode == "tokens":
-        qs, ks_, vst, os_, gs = (0, *qs), (0, *ks_), (0, *vst), (0, *os_), (0, *gs)
-    elif mode == "rows":
-        qs, ks_ = (qs[0], 0, qs[1], qs[2]), (ks_[0], 0, ks_[1], ks_[2])
-        vst, os_ = (vst[0], 0, vst[1], vst[2]), (os_[0], 0, os_[1], os_[2])
-        gs = (gs[0], 0, gs[1])
     if scale is None:
         scale = dk ** -0.5 if dk else 0.0
-    packed = _GDR.pack(q.data_ptr(), *qs, k.data_ptr(), *ks_, v.data_ptr(), *vst, out.data_ptr(),
-                       *os_, g.data_ptr(), beta.data_ptr(), *gs, al, db, sp, *ss, lines, hk, hv, dk,
-                       dv, scale, 1 if qk_l2norm else 0, pad_slot_id)
+    end = (al, db, sp, *ss, lines, hk, hv, dk, dv, scale, 1 if qk_l2norm else 0, pad_slot_id)
+    pq, pk, pv, po, pg, pb = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                              g.data_ptr(), beta.data_ptr())
+    if mode == "tokens":
+        packed = _GDR.pack(pq, 0, *q.stride(), pk, 0, *k.stride(), pv, 0, *v.stride(), po, 0,
+                           *out.stride(), pg, pb, 0, *gs, *end)
+    elif mode == "steps":
+        packed = _GDR.pack(pq, *q.stride(), pk, *k.stride(), pv, *v.stride(), po, *out.stride(),
+                           pg, pb, *gs, *end)
+    else:
+        (q0, q1, q2), (k0, k1, k2), (v0, v1, v2) = q.stride(), k.stride(), v.stride()
+        o0, o1, o2 = out.stride()
+        packed = _GDR.pack(pq, q0, 0, q1, q2, pk, k0, 0, k1, k2, pv, v0, 0, v1, v2, po, o0, 0, o1,
+                           o2, pg, pb, gs[0], 0, gs[1], *end)
     return dev, packed, out, (hk, hv, dk, dv)
 
 
@@ -311,7 +317,7 @@ def prepare_gated_rms_norm(x, gate, weight, eps=1e-6, activation="silu", norm_be
 
 def _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out):
     dev = _device(x)
-    if not (dev >= 0 and x.dtype is _BF16 and isinstance(gate, torch.Tensor)
+    if not (dev >= 0 and x.dtype is _BF16 and isinstance(gate, _Tensor)
             and gate.dtype is _BF16 and gate.get_device() == dev):
         _need(dev, x, "x", _BF16)
         _need(dev, gate, "gate", _BF16)
@@ -321,7 +327,7 @@ def _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out):
     if len(shape) not in (2, 3) or gate.shape != shape:
         raise ValueError("x and gate must be (tokens, heads, dim) or (tokens, dim), one shape")
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty_like(x)
     else:
         _need(dev, out, "out", _BF16)
         if out.shape != shape:
@@ -342,7 +348,7 @@ def _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out):
 def _norm_weight(dev: int, w: Optional[torch.Tensor], name: str, dim: int):
     if w is None:
         return None
-    if not isinstance(w, torch.Tensor) or w.dtype is not _BF16 or w.get_device() != dev:
+    if not isinstance(w, _Tensor) or w.dtype is not _BF16 or w.get_device() != dev:
         _need(dev, w, name, _BF16)
     if w.shape != (dim,) or (dim > 1 and w.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {dim}")
@@ -379,7 +385,7 @@ def prepare_residual_rms_norm(x, residual, weight, post_weight=None, gate=None, 
 def _marshal_residual(x, residual, weight, post_weight, gate, scale, eps, weight_offset, out,
                       residual_out):
     dev = _device(x)
-    if not (dev >= 0 and x.dtype is _BF16 and isinstance(residual, torch.Tensor)
+    if not (dev >= 0 and x.dtype is _BF16 and isinstance(residual, _Tensor)
             and residual.dtype in (_BF16, _F32) and residual.get_device() == dev):
         _need(dev, x, "x", _BF16)
         _need(dev, residual, "residual", _BF16, _F32)
@@ -398,11 +404,11 @@ def _marshal_residual(x, residual, weight, post_weight, gate, scale, eps, weight
             raise ValueError("gate must be (dim,) or (tokens, dim)")
         gp, gs = gate.data_ptr(), gate.stride() if gate.dim() == 2 else (0, gate.stride(0))
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty_like(x)
     else:
         _need(dev, out, "out", _BF16)
     if residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = _empty_like(residual)
     else:
         _need(dev, residual_out, "residual_out", kind)
     if out.shape != shape or residual_out.shape != shape:
@@ -457,9 +463,9 @@ def _marshal_verify(target_logits, draft_tokens, uniform, noise, draft_probs, nu
                     temperature, out_tokens, num_accepted, workspace, err_count):
     dev = _device(target_logits)
     if not (dev >= 0 and target_logits.dtype in (_BF16, _F32)
-            and isinstance(draft_tokens, torch.Tensor) and draft_tokens.dtype is _I32
-            and isinstance(uniform, torch.Tensor) and uniform.dtype is _F32
-            and isinstance(noise, torch.Tensor) and noise.dtype is _F32
+            and isinstance(draft_tokens, _Tensor) and draft_tokens.dtype is _I32
+            and isinstance(uniform, _Tensor) and uniform.dtype is _F32
+            and isinstance(noise, _Tensor) and noise.dtype is _F32
             and draft_tokens.get_device() == uniform.get_device() == noise.get_device() == dev):
         _need(dev, target_logits, "target_logits", _BF16, _F32)
         _need(dev, draft_tokens, "draft_tokens", _I32)
@@ -489,13 +495,13 @@ def _marshal_verify(target_logits, draft_tokens, uniform, noise, draft_probs, nu
     temp = _vector(dev, temperature, "temperature", _F32, batch)
     device = noise.device
     if out_tokens is None:
-        out_tokens = torch.empty((batch, drafts + 1), dtype=_I32, device=device)
+        out_tokens = _empty((batch, drafts + 1), dtype=_I32, device=device)
     else:
         _need(dev, out_tokens, "out_tokens", _I32)
         if out_tokens.shape != (batch, drafts + 1) or not out_tokens.is_contiguous():
             raise ValueError("out_tokens must be a contiguous (batch, drafts + 1)")
     if num_accepted is None:
-        num_accepted = torch.empty(batch, dtype=_I32, device=device)
+        num_accepted = _empty(batch, dtype=_I32, device=device)
     count = _vector(dev, num_accepted, "num_accepted", _I32, batch)
     size = _lib.load().spec_verify_workspace(batch, drafts, vocab)
     scratch = _workspace(dev, workspace, size, noise)
