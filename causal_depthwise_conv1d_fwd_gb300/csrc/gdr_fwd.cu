@@ -1013,6 +1013,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 }
             }
 
+            gamma = f[kMisc * C - 8 * q];  // before the last arrival, after which the stage may be filled again
             // d, decayed for the state (3 parts) and for the output (2)
             {
                 float x[2][8];
@@ -1069,7 +1070,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                         }
                 }
             }
-            gamma = f[kMisc * C - 8 * q];
             if constexpr (FULL) {
                 tmem_wait_store();
                 tc_fence_before();
