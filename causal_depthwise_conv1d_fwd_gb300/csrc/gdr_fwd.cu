@@ -9,7 +9,7 @@
 //   gdr_prep_kernel   for every chunk and key head at once: the two products, the decays, T = (I + A)^-1, P, and what each
 //                     token multiplies by; written to the workspace in the layout the tensor cores read.
 //   gdr_chunk_kernel  for every sequence and value head: the chunks in order with S^T kept on chip.
-// 4 x 4096 tokens with 32 value heads take 271 us: 95 + 172, and what the launches cost.
+// 4 x 4096 tokens with 32 value heads take 268 us: 95 + 172 and the launches, less what overlaps.
 // Where sequences and heads are too few for the card, each sequence is cut into segments of chunks.  A segment takes its
 // first state to S M + N; gdr_chunk_kernel first finds N (the segment from a zero state) and M (from the identity, without
 // values) of all segments at once, gdr_join_kernel goes through them for each segment's first state, and gdr_chunk_kernel
