@@ -538,3 +538,45 @@ def test_update_past_32_bits(ccv):
         o, om, st, sm = ref.gdr_tokens(*split(d, i, i + 1), start[i].double(), 128 ** -0.5, True)
         ref.assert_out(out[i:i + 1], o, om)
         ref.assert_state(state[line], st, sm)
+
+
+@pytest.mark.parametrize("heads", [(1, 2), (16, 32)])
+def test_fwd_calls_in_a_row(ccv, path, heads):
+    """Kernels start before the ones ahead of them end: calls that go on from each other's states, with one workspace and
+    with inputs and indices written just before each, give the bits that they give one at a time."""
+    hk, hv = heads
+    d, g = inputs(700, hk, hv, 64, 64, 31)
+    dd = dev(d)
+    seed = torch.randn(4, hv, 64, 64, generator=g).cuda()
+    starts = torch.tensor([0, 300, 300, 429, 700], dtype=torch.int32, device="cuda")
+    lines = torch.tensor([2, 0, 3, 1], dtype=torch.int32, device="cuda")
+    init = torch.tensor([True, True, False, True], device="cuda")
+    space = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        state, outs = seed.clone(), []
+        q, k, v = (torch.empty_like(dd[n]) for n in "qkv")
+        qsl, idx, flags = torch.zeros_like(starts), torch.full_like(lines, -1), torch.zeros_like(init)
+        for step in range(6):
+            for to, of in ((q, dd["q"]), (k, dd["k"]), (v, dd["v"])):
+                to.copy_(of.roll(step, 0))
+            qsl.copy_(starts)
+            idx.copy_(lines.roll(step))
+            flags.copy_(init | (step % 2 == 1))
+            outs.append(ccv.gdr_fwd(q, k, v, dd["g"], dd["beta"], state, qsl, idx, flags, workspace=space))
+            if wait:
+                torch.cuda.synchronize()
+            for t in (q, k, v):
+                t.fill_(float("nan"))
+            qsl.zero_()
+            idx.fill_(-1)
+            if wait:
+                torch.cuda.synchronize()
+        return outs, state
+
+    one_by_one = run(True)
+    for _ in range(3):
+        outs, state = run(False)
+        assert torch.equal(state, one_by_one[1])
+        for got, want in zip(outs, one_by_one[0]):
+            assert torch.equal(got.view(torch.int16), want.view(torch.int16))

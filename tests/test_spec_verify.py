@@ -176,6 +176,26 @@ def test_streams_graphs_and_repeats(ccv):
         assert torch.equal(plan.result[0], want[0]) and torch.equal(plan.result[1], want[1])
 
 
+def test_calls_in_a_row(ccv):
+    """The draw starts before the statistics end: with all inputs written just before each call and overwritten just
+    after it, calls in a row give what they give one at a time."""
+    cases = [make(40, 3, 70000, seed) for seed in (21, 22, 23)]
+    wants = [check(ccv, d) for d in cases]
+    on = [{n: t.cuda() for n, t in d.items()} for d in cases]
+    now = {n: torch.zeros_like(t) for n, t in on[0].items()}
+    space = torch.empty(8 << 20, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        got = []
+        for d in on:
+            for n, t in d.items():
+                now[n].copy_(t)
+            got.append(ccv.spec_verify(now["logits"], now["tokens"], now["uniform"], now["noise"], now["probs"], workspace=space))
+            for t in now.values():
+                t.zero_()
+        for a, b in zip(got, wants):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_counts_feed_the_next_step(ccv):
     """The counts are gdr_update's num_accepted_tokens: a verify step of tokens [last, drafts] keeps `count` states."""
     b, s, v = 3, 3, 200
