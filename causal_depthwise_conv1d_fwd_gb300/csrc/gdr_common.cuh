@@ -12,20 +12,40 @@ constexpr float kGdrNormEps = 1e-6f;
 constexpr int kGdrMaxDk = 256;
 constexpr int kGdrMaxDv = 1024;
 
-// The decay's logarithm and the write strength of one (token, value head).  `raw` selects the projections' bf16
-// values; expf and log1pf rather than the approximations, since the logarithm is summed over a chunk and the decay
+// The decay's logarithm and the write strength of one (token, value head), as they are in memory.  Raw projections are
+// bf16; expf and log1pf rather than the approximations, since the logarithm is summed over a chunk and the decay
 // multiplies an fp32 state.
-__device__ __forceinline__ void gdr_gates(const ccv_gdr_args &a, int64_t off, int h, float &g, float &beta) {
-    if (a.a_log != nullptr) {
-        const float x = bf16_bits(static_cast<const uint16_t *>(a.g)[off]) + a.dt_bias[h];
-        const float y = bf16_bits(static_cast<const uint16_t *>(a.beta)[off]);
-        const float softplus = x > 20.0f ? x : log1pf(expf(x));
-        g = -expf(a.a_log[h]) * softplus;
-        beta = 1.0f / (1.0f + expf(-y));
-    } else {
-        g = static_cast<const float *>(a.g)[off];
-        beta = static_cast<const float *>(a.beta)[off];
+struct GdrGates {
+    uint32_t g, beta;  // bits
+    float bias, a_log;
+    __device__ __forceinline__ void load(const ccv_gdr_args &a, int64_t off, int h) {
+        if (a.a_log != nullptr) {
+            g = static_cast<const uint16_t *>(a.g)[off];
+            beta = static_cast<const uint16_t *>(a.beta)[off];
+            bias = a.dt_bias[h];
+            a_log = a.a_log[h];
+        } else {
+            g = static_cast<const uint32_t *>(a.g)[off];
+            beta = static_cast<const uint32_t *>(a.beta)[off];
+        }
     }
+    __device__ __forceinline__ void get(bool raw, float &decay, float &strength) const {
+        if (raw) {
+            const float x = bf16_bits(static_cast<uint16_t>(g)) + bias;
+            const float y = bf16_bits(static_cast<uint16_t>(beta));
+            const float softplus = x > 20.0f ? x : log1pf(expf(x));
+            decay = -expf(a_log) * softplus;
+            strength = 1.0f / (1.0f + expf(-y));
+        } else {
+            decay = __uint_as_float(g);
+            strength = __uint_as_float(beta);
+        }
+    }
+};
+__device__ __forceinline__ void gdr_gates(const ccv_gdr_args &a, int64_t off, int h, float &g, float &beta) {
+    GdrGates gates;
+    gates.load(a, off, h);
+    gates.get(a.a_log != nullptr, g, beta);
 }
 
 // ------------------------------------------------------------ host side ----

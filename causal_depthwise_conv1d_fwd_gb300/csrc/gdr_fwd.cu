@@ -9,7 +9,7 @@
 //   gdr_prep_kernel   for every chunk and key head at once: the two products, the decays, T = (I + A)^-1, P, and what each
 //                     token multiplies by; written to the workspace in the layout the tensor cores read.
 //   gdr_chunk_kernel  for every sequence and value head: the chunks in order with S^T kept on chip.
-// 4 x 4096 tokens with 32 value heads take 268 us: 95 + 172 and the launches, less what overlaps.
+// 4 x 4096 tokens with 32 value heads take 268 us: 93 + 172 and the launches, less what overlaps.
 // Where sequences and heads are too few for the card, each sequence is cut into segments of chunks.  A segment takes its
 // first state to S M + N; gdr_chunk_kernel first finds N (the segment from a zero state) and M (from the identity, without
 // values) of all segments at once, gdr_join_kernel goes through them for each segment's first state, and gdr_chunk_kernel
@@ -230,7 +230,8 @@ __device__ __forceinline__ void multiply_lower(float *d, int l, int lane, Sync s
 // cores.
 __device__ __forceinline__ void invert(float *matrices, int tid) {
     const int warp = tid >> 5, lane = tid & 31;
-    if (tid < 64) {  // 8 blocks, two columns a thread, pairs of rows
+    if (tid < 64) {  // 8 blocks, two columns a thread, pairs of rows; by the warps that wrote A, while the others are at P
+        asm volatile("bar.sync 1, 64;" ::: "memory");
         const int which = tid >> 3, j = (tid & 7) * 2;
         float *d = matrices + (which >> 2) * (C * kLd) + (which & 3) * (16 * kLd + 16);
         f32x2 t[2][8];
@@ -275,8 +276,8 @@ __device__ __forceinline__ void invert(float *matrices, int tid) {
     __syncthreads();
 }
 
-// A block of 4 warps a (chunk, key head), 4 blocks an SM: 4096 of them (4 x 4096 tokens, 16 key and 32 value heads) take 95 us.
-// It writes 344 MB, 3.6 TB/s; what bounds it is latency (44% of the issue slots, 50% of the shared-memory pipe): loads that
+// A block of 4 warps a (chunk, key head), 4 blocks an SM: 4096 of them (4 x 4096 tokens, 16 key and 32 value heads) take 93 us.
+// It writes 344 MB, 3.7 TB/s; what bounds it is latency (44% of the issue slots, 50% of the shared-memory pipe): loads that
 // wait on the search, 14 barriers, and forward substitution.  3, 5 and 6 blocks an SM and 8 warps a block were slower.
 // PANELS: dim_k rounded up to 64 PANELS.  V: rows of q and k allow 16-byte vectors.
 template <int PANELS, bool V>
@@ -315,21 +316,27 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
     if (p.cache_indices != nullptr && p.cache_indices[seq] == a.pad_slot_id) return;
     const int t0 = s + chunk * C, n = min(C, e - t0);
 
+    // The value heads of this key head go two at a time, 64 threads each.
+    const int i = tid & (C - 1), side = tid >> 6;
+    const int rep = a.num_v_heads / a.num_k_heads;
+    GdrGates gates;
+    auto load_gates = [&](int r0) {
+        const int h = hk * rep + min(r0 + side, rep - 1);
+        if (i < n) gates.load(a, (t0 + i) * a.gate_stride_tok + h * a.gate_stride_head, h);
+    };
+    load_gates(0);  // on their way before the larger copies
+
     // Panels of 128 rows: the chunk's keys, then its queries.
     stage_rows<PANELS, V, kPrepThreads>(ab, 2 * kTile, a.k, t0, hk, n, a.dim_k, tid);
     stage_rows<PANELS, V, kPrepThreads>(ab + kTile, 2 * kTile, a.q, t0, hk, n, a.dim_k, tid);
     cp_async_commit();
     if (warp == 0) tmem_alloc<2 * C>(&sm.tmem);
 
-    // The value heads of this key head go two at a time, 64 threads each.
-    const int i = tid & (C - 1), side = tid >> 6;
-    const int rep = a.num_v_heads / a.num_k_heads;
     auto block = [&](int w) { return p.heads + (static_cast<int64_t>(slot) * a.num_v_heads + hk * rep + w) * kHeadBytes; };
     // Gates, and G by a scan in 64-bit fixed point: a difference of two sums has to be exact to its own rounding.
-    auto scan_gates = [&](int r0) {
-        const int h = hk * rep + min(r0 + side, rep - 1);
+    auto scan_gates = [&] {
         float g = 0.0f, beta = 0.0f;
-        if (i < n) gdr_gates(a, (t0 + i) * a.gate_stride_tok + h * a.gate_stride_head, h, g, beta);
+        if (i < n) gates.get(a.a_log != nullptr, g, beta);
         // e^-200 is 0 in fp32 and e^1000 infinite: keeps inf - inf out of the differences and the sums in range, and NaN as it is
         g = g < -200.0f ? -200.0f : g > 1000.0f ? 1000.0f : g;
         constexpr float kOne = 1099511627776.0f;  // 2^40
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
         sm.glo[side][i] = __ll2float_rn(sum - __float2ll_rn(hi)) / kOne;
         sm.beta[side][i] = g != g ? g : beta;
     };
-    scan_gates(0);
+    scan_gates();
     cp_async_wait<0>();
     fence_async_shared();
     tc_fence_before();
@@ -383,7 +390,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
     for (int r0 = 0; r0 < rep; r0 += 2) {
         const int nh = min(2, rep - r0);
         if (r0 > 0) {
-            scan_gates(r0);
+            load_gates(r0);
+            scan_gates();
             __syncthreads();
         }
         if (side < nh) {
@@ -476,7 +484,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
                 }
             }
         }
-        __syncthreads();
         invert(matrices, tid);
         if (side < nh) {
             uint8_t *out = block(r0 + side) + kT;
