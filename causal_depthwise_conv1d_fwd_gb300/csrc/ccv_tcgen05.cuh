@@ -209,17 +209,6 @@ __device__ __forceinline__ void take_part(float &a, float &b, uint32_t &part) {
         : "+f"(a), "+f"(b)
         : "r"(part));
 }
-// x plus a bf16 value a half, exact to one rounding; the values need no unpacking.
-__device__ __forceinline__ f32x2 add_bf16(f32x2 x, uint16_t lo, uint16_t hi) {
-    float a, b;
-    unpack2(x, a, b);
-    asm("{\n\t.reg .b16 one;\n\tmov.b16 one, 0x3f80;\n\t"
-        "fma.rn.f32.bf16 %0, %2, one, %0;\n\t"
-        "fma.rn.f32.bf16 %1, %3, one, %1;\n\t}"
-        : "+f"(a), "+f"(b)
-        : "h"(lo), "h"(hi));
-    return pack2(a, b);
-}
 __device__ __forceinline__ void split_bf16x2(f32x2 x, uint32_t &hi, uint32_t &mid) {
     float a, b;
     unpack2(x, a, b);
