@@ -71,6 +71,27 @@ def _stream(stream, device: int) -> ctypes.c_void_p:
     return ctypes.c_void_p(handle)
 
 
+def _elsewhere(stream, like: torch.Tensor, call, *args):
+    """call(*args) on `stream`, which is made current: what the call allocates
+    then follows that stream's own work, and the tensors that it made and
+    returns are kept from reuse until the caller's stream is past them, too."""
+    _need_cuda(like, "the first tensor")
+    home = torch.cuda.current_stream(like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream, like.device.index).value or 0
+        # 0 and 1 are both CUDA's legacy default stream
+        stream = (torch.cuda.ExternalStream(handle, device=like.device) if handle > 1
+                  else torch.cuda.default_stream(like.device))
+    if stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {like.device}")
+    with torch.cuda.stream(stream):
+        result = call(*args)
+    for t in result if isinstance(result, tuple) else (result,):
+        if not any(t is a for a in args):
+            t.record_stream(home)
+    return result
+
+
 def _silu_flag(activation) -> int:
     if activation is None or activation is False:
         return 0

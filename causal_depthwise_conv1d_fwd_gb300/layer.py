@@ -9,7 +9,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from .api import PAD_SLOT_ID, Launch, _check, _stream
+from .api import PAD_SLOT_ID, Launch, _check, _elsewhere
 
 _ACTIVATIONS = {None: 0, "silu": 1, "swish": 1, "sigmoid": 2}
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -24,21 +24,16 @@ _GDR = struct.Struct("<" + "Qqqqq" * 4 + "QQqqq" + "QQQqqqq" + "iiiiifii")
 _FUNCTIONS = {}
 
 
-def _call(name: str, args: tuple, device: int, stream, scratch: Optional[torch.Tensor] = None):
-    """One call of an entry point on the tensors' device and the given or that
-    device's current stream."""
+def _call(name: str, args: tuple, device: int):
+    """One call of an entry point on the tensors' device and that device's
+    current stream."""
     fn = _FUNCTIONS.get(name)
     if fn is None:
         fn = _FUNCTIONS[name] = getattr(_lib.load(), name)
     if torch._C._cuda_getDevice() != device:
         with torch.cuda.device(device):
-            return _call(name, args, device, stream, scratch)
-    if stream is None:
-        _check(fn(*args, torch._C._cuda_getCurrentRawStream(device)), name)
-    else:
-        _check(fn(*args, _stream(stream, device)), name)
-        if scratch is not None:
-            _used_on(scratch, stream, device)
+            return _call(name, args, device)
+    _check(fn(*args, torch._C._cuda_getCurrentRawStream(device)), name)
 
 
 def _used_on(scratch: torch.Tensor, stream, device: int):
@@ -194,11 +189,15 @@ def gdr_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
     bf16 projections they come from.  state is (num_lines, num_v_heads, dim_v,
     dim_k) fp32.  scale defaults to dim_k ** -0.5.  Returns out.
     """
+    if stream is not None:
+        return _elsewhere(stream, v, gdr_fwd, q, k, v, g, beta, state, query_start_loc,
+                          cache_indices, has_initial_state, scale, qk_l2norm, a_log, dt_bias,
+                          pad_slot_id, out, workspace, err_count)
     dev, args, out, scratch, _ = _marshal_gdr_fwd(q, k, v, g, beta, state, query_start_loc,
                                                   cache_indices, has_initial_state, scale,
                                                   qk_l2norm, a_log, dt_bias, pad_slot_id, out,
                                                   workspace, err_count)
-    _call("gdr_fwd", args, dev, stream, scratch)
+    _call("gdr_fwd", args, dev)
     return out
 
 
@@ -255,10 +254,14 @@ def gdr_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     starts from line [b, num_accepted_tokens[b] - 1].  Returns out with v's
     rank.
     """
+    if stream is not None:
+        return _elsewhere(stream, v, gdr_update, q, k, v, g, beta, state, state_indices,
+                          num_accepted_tokens, output_state_indices, scale, qk_l2norm, a_log,
+                          dt_bias, pad_slot_id, out, err_count)
     dev, args, out, _ = _marshal_gdr_update(q, k, v, g, beta, state, state_indices,
                                             num_accepted_tokens, output_state_indices, scale,
                                             qk_l2norm, a_log, dt_bias, pad_slot_id, out, err_count)
-    _call("gdr_update", args, dev, stream)
+    _call("gdr_update", args, dev)
     return out
 
 
@@ -303,8 +306,11 @@ def gated_rms_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, ep
     or norm(x act(gate)) weight with norm_before_gate=False.  x, gate
     (tokens, heads, dim) or (tokens, dim) bf16; activation "silu", "sigmoid"
     or None.  Returns out."""
+    if stream is not None:
+        return _elsewhere(stream, x, gated_rms_norm, x, gate, weight, eps, activation,
+                          norm_before_gate, out)
     dev, args, out, _ = _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out)
-    _call("gated_rms_norm", args, dev, stream)
+    _call("gated_rms_norm", args, dev)
     return out
 
 
@@ -368,9 +374,12 @@ def residual_rms_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Ten
     x (tokens, dim) bf16; residual bf16 or fp32; gate (dim,) or (tokens, dim).
     residual_out may be residual and out may be x (in place).
     """
+    if stream is not None:
+        return _elsewhere(stream, x, residual_rms_norm, x, residual, weight, post_weight, gate,
+                          scale, eps, weight_offset, out, residual_out)
     dev, args, result, _ = _marshal_residual(x, residual, weight, post_weight, gate, scale, eps,
                                              weight_offset, out, residual_out)
-    _call("residual_rms_norm", args, dev, stream)
+    _call("residual_rms_norm", args, dev)
     return result
 
 
@@ -441,10 +450,14 @@ def spec_verify(target_logits: torch.Tensor, draft_tokens: torch.Tensor, uniform
     and int32 (batch) kept drafts + 1 -- the num_accepted_tokens of the next
     ccv_update_spec and gdr_update.
     """
+    if stream is not None:
+        return _elsewhere(stream, target_logits, spec_verify, target_logits, draft_tokens, uniform,
+                          noise, draft_probs, num_drafts, temperature, out_tokens, num_accepted,
+                          workspace, err_count)
     dev, args, result, scratch, _ = _marshal_verify(target_logits, draft_tokens, uniform, noise,
                                                     draft_probs, num_drafts, temperature,
                                                     out_tokens, num_accepted, workspace, err_count)
-    _call("spec_verify", args, dev, stream, scratch)
+    _call("spec_verify", args, dev)
     return result
 
 
