@@ -86,7 +86,7 @@ def _elsewhere(stream, like: torch.Tensor, call, *args):
         raise ValueError(f"stream is on {stream.device}, the tensors are on {like.device}")
     with torch.cuda.stream(stream):
         result = call(*args)
-    for t in result if isinstance(result, tuple) else (result,):
+    for t in result if isinstance(result, (tuple, list)) else (result,):
         if not any(t is a for a in args):
             t.record_stream(home)
     return result
@@ -143,6 +143,9 @@ def ccv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
     an empty tensor with x's strides.  conv_states (num_lines, dim, >= W-1) is
     updated in place.  Returns out.
     """
+    if stream is not None and out is None:
+        return _elsewhere(stream, x, ccv_fwd, x, weight, bias, conv_states, query_start_loc,
+                          cache_indices, has_initial_state, activation, pad_slot_id, out, err_count)
     return prepare_ccv_fwd(x, weight, bias, conv_states, query_start_loc, cache_indices,
                            has_initial_state, activation, pad_slot_id, out, err_count)(stream)
 
@@ -345,6 +348,10 @@ def paged_sconv_fwd(x: torch.Tensor, weight: torch.Tensor, cache: torch.Tensor,
                     out: Optional[torch.Tensor] = None,
                     err_count: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Single-launch paged insert + depthwise causal conv.  Returns out [T, H*ws]."""
+    if stream is not None and out is None:
+        return _elsewhere(stream, x, paged_sconv_fwd, x, weight, cache, positions, block_table,
+                          seq_idx, slot_mapping, query_start, off_s, ws, block_size, activation,
+                          use_residual, out, err_count)
     return prepare_paged_sconv_fwd(x, weight, cache, positions, block_table, seq_idx,
                                    slot_mapping, query_start, off_s, ws, block_size,
                                    activation, use_residual, out, err_count)(stream)
@@ -405,6 +412,11 @@ def paged_sconv_fwd_with_metadata(x: torch.Tensor, weight: torch.Tensor, cache: 
     """paged_sconv_fwd in one launch that resolves each token's request and
     first x-row from query_start_loc itself (and writes them to seq_idx_out
     / query_start_out when given).  Returns out [T, H*ws]."""
+    if stream is not None and out is None:
+        return _elsewhere(stream, x, paged_sconv_fwd_with_metadata, x, weight, cache, positions,
+                          block_table, query_start_loc, num_reqs, num_actual_tokens, slot_mapping,
+                          off_s, ws, block_size, activation, use_residual, out, seq_idx_out,
+                          query_start_out, err_count)
     return prepare_paged_sconv_fwd_with_metadata(
         x, weight, cache, positions, block_table, query_start_loc, num_reqs, num_actual_tokens,
         slot_mapping, off_s, ws, block_size, activation, use_residual, out, seq_idx_out,
@@ -466,6 +478,10 @@ def paged_sconv_fwd_streams(streams, cache: torch.Tensor, positions: torch.Tenso
 
     streams: list of dicts with keys x, weight, off_s, ws and optionally out
     (created when missing).  Returns the list of outputs."""
+    if stream is not None and any(st.get("out") is None for st in streams):
+        return _elsewhere(stream, cache, paged_sconv_fwd_streams, streams, cache, positions,
+                          block_table, seq_idx, slot_mapping, query_start, block_size, activation,
+                          use_residual, err_count)
     return prepare_paged_sconv_fwd_streams(streams, cache, positions, block_table, seq_idx,
                                            slot_mapping, query_start, block_size, activation,
                                            use_residual, err_count)(stream)
