@@ -71,17 +71,27 @@ def _stream(stream, device: int) -> ctypes.c_void_p:
     return ctypes.c_void_p(handle)
 
 
+def _torch_stream(stream, device: torch.device) -> torch.cuda.Stream:
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream, device.index).value or 0
+    # 0 and 1 are both CUDA's legacy default stream
+    return (torch.cuda.ExternalStream(handle, device=device) if handle > 1
+            else torch.cuda.default_stream(device))
+
+
+def _capturing(stream: torch.cuda.Stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _elsewhere(stream, like: torch.Tensor, call, *args):
     """call(*args) on `stream`, which is made current: what the call allocates
     then follows that stream's own work, and the tensors that it made and
     returns are kept from reuse until the caller's stream is past them, too."""
     _need_cuda(like, "the first tensor")
     home = torch.cuda.current_stream(like.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream, like.device.index).value or 0
-        # 0 and 1 are both CUDA's legacy default stream
-        stream = (torch.cuda.ExternalStream(handle, device=like.device) if handle > 1
-                  else torch.cuda.default_stream(like.device))
+    stream = _torch_stream(stream, like.device)
     if stream.device != like.device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on {like.device}")
     with torch.cuda.stream(stream):
@@ -110,15 +120,26 @@ class Launch:
     and sizes are converted once, so each call costs one ctypes call.  The
     tensors must stay alive and keep their storage while the plan is used.
     The call runs on the tensors' device (made current for the call if it is
-    not) and, by default, on that device's current stream."""
+    not) and, by default, on that device's current stream.
 
-    def __init__(self, name: str, args: tuple, result, keep: tuple):
+    `owned` are the tensors that the plan allocated (its output, a workspace).
+    They belong to the stream that was current then.  The first call on another
+    stream makes that one wait for what the owner had queued by then, which may
+    still use their memory; a call that is captured into a graph does not (a
+    capture may not wait for work outside it), and torch.cuda.graph synchronises
+    before it begins.  A plan must not run on two streams at once."""
+
+    def __init__(self, name: str, args: tuple, result, keep: tuple, owned: tuple = ()):
         self.name = name
         self._fn = getattr(_lib.load(), name)
         self._args = args
         self.result = result
         self._keep = keep
         self.device = _device_of(keep).index
+        self._owned = owned
+        if owned:
+            self._home = torch._C._cuda_getCurrentRawStream(self.device)
+            self._known = {self._home}
 
     def __call__(self, stream=None):
         if torch.cuda.current_device() != self.device:
@@ -127,8 +148,20 @@ class Launch:
         return self._launch(stream)
 
     def _launch(self, stream):
-        _check(self._fn(*self._args, _stream(stream, self.device)), self.name)
+        handle = _stream(stream, self.device)
+        if self._owned and (handle.value or 0) not in self._known:
+            self._hand_over(handle.value or 0)
+        _check(self._fn(*self._args, handle), self.name)
         return self.result
+
+    def _hand_over(self, handle: int):
+        device = self._owned[0].device
+        stream, home = _torch_stream(handle, device), _torch_stream(self._home, device)
+        for t in self._owned:
+            t.record_stream(stream)
+        if not (_capturing(stream) or _capturing(home)):
+            stream.wait_stream(home)
+            self._known.add(handle)
 
 
 def ccv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
@@ -182,7 +215,9 @@ def prepare_ccv_fwd(x, weight, bias, conv_states, query_start_loc, cache_indices
         ss, nl, sl = (0, 0, 0), 0, 0
     if out is None:
         out = torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=x.device)
+        owned = (out,)
     else:
+        owned = ()
         _need_cuda(out, "out", torch.bfloat16)
         if out.shape != x.shape:
             raise ValueError("out must have x's shape")
@@ -193,7 +228,7 @@ def prepare_ccv_fwd(x, weight, bias, conv_states, query_start_loc, cache_indices
             _ptr(qsl), batch, _ptr(ci), _ptr(hi), dim, total, width, pad_slot_id,
             _silu_flag(activation), _ptr(err_count))
     return Launch("ccv_fwd", args, out,
-                  (x, weight, bias, conv_states, qsl, ci, hi, out, err_count))
+                  (x, weight, bias, conv_states, qsl, ci, hi, out, err_count), owned)
 
 
 def ccv_update(x: torch.Tensor, conv_state: torch.Tensor, weight: torch.Tensor,
@@ -384,7 +419,9 @@ def prepare_paged_sconv_fwd(x, weight, cache, positions, block_table, seq_idx, s
         raise ValueError("block_table must be [num_reqs, max_blocks] with stride 1 along blocks")
     if out is None:
         out = torch.empty_like(x)
+        owned = (out,)
     else:
+        owned = ()
         _need_cuda(out, "out", torch.bfloat16)
         if out.shape != x.shape or out.stride(1) != 1:
             raise ValueError("out must be [T, C] with channel stride 1")
@@ -396,7 +433,7 @@ def prepare_paged_sconv_fwd(x, weight, cache, positions, block_table, seq_idx, s
             block_table.shape[0], block_table.shape[1], _ptr(qs), T, off_s, ws, width,
             _silu_flag(activation), int(bool(use_residual)), _ptr(err_count))
     return Launch("paged_sconv_fwd", args, out,
-                  (x, weight, cache, pos, sidx, slots, block_table, qs, out, err_count))
+                  (x, weight, cache, pos, sidx, slots, block_table, qs, out, err_count), owned)
 
 
 def paged_sconv_fwd_with_metadata(x: torch.Tensor, weight: torch.Tensor, cache: torch.Tensor,
@@ -453,7 +490,9 @@ def prepare_paged_sconv_fwd_with_metadata(x, weight, cache, positions, block_tab
         raise ValueError("block_table must be [num_reqs, max_blocks] with stride 1 along blocks")
     if out is None:
         out = torch.empty_like(x)
+        owned = (out,)
     else:
+        owned = ()
         _need_cuda(out, "out", torch.bfloat16)
         if out.shape != x.shape or out.stride(1) != 1:
             raise ValueError("out must be [T, C] with channel stride 1")
@@ -466,7 +505,8 @@ def prepare_paged_sconv_fwd_with_metadata(x, weight, cache, positions, block_tab
             block_table.shape[1], T, off_s, ws, width, _silu_flag(activation),
             int(bool(use_residual)), _ptr(err_count))
     return Launch("paged_sconv_fwd_with_metadata", args, out,
-                  (x, weight, cache, pos, qsl, seq_o, qs_o, slots, block_table, out, err_count))
+                  (x, weight, cache, pos, qsl, seq_o, qs_o, slots, block_table, out, err_count),
+                  owned)
 
 
 def paged_sconv_fwd_streams(streams, cache: torch.Tensor, positions: torch.Tensor,
@@ -502,7 +542,7 @@ def prepare_paged_sconv_fwd_streams(streams, cache, positions, block_table, seq_
     T = streams[0]["x"].shape[0]
     width = streams[0]["weight"].shape[1]
     descs = (_lib.PagedStream * len(streams))()
-    outs, keep = [], []
+    outs, keep, owned = [], [], []
     for i, st in enumerate(streams):
         x, w, ws = st["x"], st["weight"], int(st["ws"])
         _need_cuda(x, f"streams[{i}].x", torch.bfloat16)
@@ -514,6 +554,7 @@ def prepare_paged_sconv_fwd_streams(streams, cache, positions, block_table, seq_
         out = st.get("out")
         if out is None:
             out = torch.empty_like(x)
+            owned.append(out)
         else:
             _need_cuda(out, f"streams[{i}].out", torch.bfloat16)
             if out.shape != x.shape or out.stride(1) != 1:
@@ -537,4 +578,5 @@ def prepare_paged_sconv_fwd_streams(streams, cache, positions, block_table, seq_
             block_table.stride(0), block_table.shape[0], block_table.shape[1], _ptr(qs), T,
             width, _silu_flag(activation), int(bool(use_residual)), _ptr(err_count))
     return Launch("paged_sconv_fwd_streams", args, outs,
-                  (descs, cache, pos, sidx, slots, block_table, qs, err_count, *keep))
+                  (descs, cache, pos, sidx, slots, block_table, qs, err_count, *keep),
+                  tuple(owned))

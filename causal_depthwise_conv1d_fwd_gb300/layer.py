@@ -36,26 +36,9 @@ def _call(name: str, args: tuple, device: int):
     _check(fn(*args, torch._C._cuda_getCurrentRawStream(device)), name)
 
 
-def _used_on(scratch: torch.Tensor, stream, device: int):
-    """Tell the allocator that a workspace of the current stream is in use on another one."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    scratch.record_stream(stream)
-
-
-class ScratchLaunch(Launch):
-    """A Launch whose call uses a workspace.  One that the binding allocated
-    belongs to the plan: the plan must not run on two streams at once."""
-
-    def __init__(self, name, args, result, keep, scratch: torch.Tensor):
-        super().__init__(name, args, result, keep)
-        self._scratch = scratch
-
-    def _launch(self, stream):
-        result = super()._launch(stream)
-        if stream is not None:
-            _used_on(self._scratch, stream, self.device)
-        return result
+def _made(tensors: tuple, given: tuple) -> tuple:
+    """Those of a plan's tensors that it allocated: the ones not given to it."""
+    return tuple(t for t, g in zip(tensors, given) if t is not g)
 
 
 # The checks below run on every call of a decode step, so the common case is one
@@ -205,11 +188,11 @@ def prepare_gdr_fwd(q, k, v, g, beta, state, query_start_loc, cache_indices=None
                     has_initial_state=None, scale=None, qk_l2norm=True, a_log=None, dt_bias=None,
                     pad_slot_id=PAD_SLOT_ID, out=None, workspace=None, err_count=None) -> Launch:
     """Validate and marshal a gdr_fwd call once; returns a reusable Launch."""
-    _, args, out, scratch, keep = _marshal_gdr_fwd(q, k, v, g, beta, state, query_start_loc,
-                                                   cache_indices, has_initial_state, scale,
-                                                   qk_l2norm, a_log, dt_bias, pad_slot_id, out,
-                                                   workspace, err_count)
-    return ScratchLaunch("gdr_fwd", args, out, keep, scratch)
+    _, args, result, scratch, keep = _marshal_gdr_fwd(q, k, v, g, beta, state, query_start_loc,
+                                                      cache_indices, has_initial_state, scale,
+                                                      qk_l2norm, a_log, dt_bias, pad_slot_id, out,
+                                                      workspace, err_count)
+    return Launch("gdr_fwd", args, result, keep, _made((result, scratch), (out, workspace)))
 
 
 def _marshal_gdr_fwd(q, k, v, g, beta, state, query_start_loc, cache_indices, has_initial_state,
@@ -269,11 +252,11 @@ def prepare_gdr_update(q, k, v, g, beta, state, state_indices=None, num_accepted
                        output_state_indices=None, scale=None, qk_l2norm=True, a_log=None,
                        dt_bias=None, pad_slot_id=PAD_SLOT_ID, out=None, err_count=None) -> Launch:
     """Validate and marshal a gdr_update call once; returns a reusable Launch."""
-    _, args, out, keep = _marshal_gdr_update(q, k, v, g, beta, state, state_indices,
-                                             num_accepted_tokens, output_state_indices, scale,
-                                             qk_l2norm, a_log, dt_bias, pad_slot_id, out,
-                                             err_count)
-    return Launch("gdr_update", args, out, keep)
+    _, args, result, keep = _marshal_gdr_update(q, k, v, g, beta, state, state_indices,
+                                                num_accepted_tokens, output_state_indices, scale,
+                                                qk_l2norm, a_log, dt_bias, pad_slot_id, out,
+                                                err_count)
+    return Launch("gdr_update", args, result, keep, _made((result,), (out,)))
 
 
 def _marshal_gdr_update(q, k, v, g, beta, state, state_indices, num_accepted_tokens,
@@ -317,8 +300,8 @@ def gated_rms_norm(x: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, ep
 def prepare_gated_rms_norm(x, gate, weight, eps=1e-6, activation="silu", norm_before_gate=True,
                            out=None) -> Launch:
     """Validate and marshal a gated_rms_norm call once; returns a reusable Launch."""
-    _, args, out, keep = _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out)
-    return Launch("gated_rms_norm", args, out, keep)
+    _, args, result, keep = _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out)
+    return Launch("gated_rms_norm", args, result, keep, _made((result,), (out,)))
 
 
 def _marshal_gated(x, gate, weight, eps, activation, norm_before_gate, out):
@@ -388,7 +371,7 @@ def prepare_residual_rms_norm(x, residual, weight, post_weight=None, gate=None, 
     """Validate and marshal a residual_rms_norm call once; returns a reusable Launch."""
     _, args, result, keep = _marshal_residual(x, residual, weight, post_weight, gate, scale, eps,
                                               weight_offset, out, residual_out)
-    return Launch("residual_rms_norm", args, result, keep)
+    return Launch("residual_rms_norm", args, result, keep, _made(result, (out, residual_out)))
 
 
 def _marshal_residual(x, residual, weight, post_weight, gate, scale, eps, weight_offset, out,
@@ -469,7 +452,8 @@ def prepare_spec_verify(target_logits, draft_tokens, uniform, noise, draft_probs
                                                      draft_probs, num_drafts, temperature,
                                                      out_tokens, num_accepted, workspace,
                                                      err_count)
-    return ScratchLaunch("spec_verify", args, result, keep, scratch)
+    return Launch("spec_verify", args, result, keep,
+                  _made((*result, scratch), (out_tokens, num_accepted, workspace)))
 
 
 def _marshal_verify(target_logits, draft_tokens, uniform, noise, draft_probs, num_drafts,
