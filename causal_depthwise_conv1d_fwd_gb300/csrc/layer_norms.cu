@@ -2,8 +2,13 @@
 // and scale, the residual addition, and the norm that opens the next block).
 //
 // Both read each element once, keep the row in registers in fp32, reduce it, and write once: 6 bytes an element for the
-// first, 8 to 14 for the second, so HBM bounds them at any size that fills the card (16384 x 32 x 128 with gate: 66 us,
-// 6.1 TB/s; 8191 x 4096 with a post norm, channel gate and fp32 residual: 65 us, 6.2 TB/s) and one launch's latency below.
+// first, 8 to 14 for the second.  Rows that allow 16-byte vectors are bound by HBM up to 16384 elements where they fill the
+// card (16384 x 32 x 128 with gate: 66 us, 6.1 TB/s; 8191 x 4096 with a post norm, channel gate and fp32 residual: 65 us,
+// 6.2 TB/s), and by one launch's latency below.  Above 16384 a block of 1024 threads has the SM to itself and waits on its
+// loads (1677 x 20000: gated 64 us, 3.1 TB/s).  Rows that go element by element (a length that is not a multiple of 8, other
+// strides, an address off 16 bytes) are bound by the count of loads and stores: 8191 x 2500 takes 74 us plain and 122 with
+// post norm, token gate and fp32 residual (2.2 and 2.3 TB/s), gated 83 (1.5); 8191 x 4096 one element off 16 bytes, gated, 98
+// against 36 on it.
 // A row belongs to LPR lanes: within a warp the reductions are shuffles; longer rows reduce over the block's warps.
 #include "ccv_common.cuh"
 #include "ccv_layer.h"
@@ -13,6 +18,18 @@ namespace {
 
 constexpr int kMaxRow = 32768;
 constexpr int kNormThreads = 128;  // threads of a block when a row needs no more
+
+constexpr int norm_threads(int lanes) { return lanes > kNormThreads ? lanes : kNormThreads; }
+
+// A thread with up to 8 single elements or 2 vectors of a row has both operands' in flight at once and in registers.  With
+// more, two operands and their addresses pass the 64 registers that a thread of 1024 may have: it keeps one, and reads the
+// other after the sum, a few at a time.  (The bf16 residual's 4 vectors wait unwidened and fit: 1023 rows of 32768 take 46 us
+// so and 57 the other way; gated rows of that length, 48 us, took 177 with both.)
+constexpr bool holds_both(int vec, int count) { return count <= (vec == 1 ? 8 : 2); }
+template <int VEC>
+__device__ __forceinline__ void pause_loads(int j, float &used) {  // later loads come after `used` is there, and after stores
+    if ((j + 1) * VEC % 8 == 0) asm volatile("" : "+f"(used)::"memory");
+}
 
 // Sum over the LPR lanes of a row; the block is one row when LPR > 32.
 template <int LPR>
@@ -85,15 +102,17 @@ struct GatedArgs {
 // R: rows a thread has in flight at once.  One row of 128 values is 32 bytes a lane, x and gate together; with two, 16384 x 32
 // rows take 67 us (6.0 TB/s) instead of 75, with four 73 (registers).
 template <int LPR, int VEC, int NV, int R>
-__global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) gated_rms_norm_kernel(const __grid_constant__ GatedArgs a) {
+__global__ void __launch_bounds__(norm_threads(LPR), LPR == 1024 ? 1 : 0) gated_rms_norm_kernel(const __grid_constant__ GatedArgs a) {
     __shared__ float warp_sums[32];
     wait_prior_grid();
     release_next_grid();
-    constexpr int kThreads = LPR > kNormThreads ? LPR : kNormThreads;
+    constexpr int kThreads = norm_threads(LPR);
     constexpr int kRows = kThreads / LPR;  // rows of a block's pass
     const int lane = threadIdx.x % LPR;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRows * R) + threadIdx.x / LPR;
-    float x[R][NV][VEC], z[R][NV][VEC];
+    constexpr bool kBoth = holds_both(VEC, NV);
+    float x[R][NV][VEC], z[R][kBoth ? NV : 1][VEC];
+    const uint16_t *gp[R];
     uint16_t *op[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -106,41 +125,56 @@ __global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) gated
         }
         const int dim = live ? a.dim : 0;
         const uint16_t *xp = static_cast<const uint16_t *>(a.x.data) + tok * a.x.stride_tok + head * a.x.stride_head;
-        const uint16_t *gp = static_cast<const uint16_t *>(a.gate.data) + tok * a.gate.stride_tok + head * a.gate.stride_head;
+        gp[r] = static_cast<const uint16_t *>(a.gate.data) + tok * a.gate.stride_tok + head * a.gate.stride_head;
         op[r] = live ? static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + tok * a.out.stride_tok + head * a.out.stride_head
                      : nullptr;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int d = (j * LPR + lane) * VEC;
             load_row<VEC>(xp, a.x.stride_dim, d, dim, x[r][j]);
-            load_row<VEC>(gp, a.gate.stride_dim, d, dim, z[r][j]);
+            if constexpr (kBoth) load_row<VEC>(gp[r], a.gate.stride_dim, d, dim, z[r][j]);
         }
     }
-    float w[NV][VEC];
+    float w[kBoth ? NV : 1][VEC];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_row<VEC>(a.weight, 1, (j * LPR + lane) * VEC, a.dim, w[j]);
+    for (int j = 0; j < NV && kBoth; ++j) load_row<VEC>(a.weight, 1, (j * LPR + lane) * VEC, a.dim, w[j]);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+        const int dim = op[r] != nullptr ? a.dim : 0;
         float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            float(&gate)[VEC] = z[r][kBoth ? j : 0];
+            if constexpr (!kBoth)
+                if (!a.before) load_row<VEC>(gp[r], a.gate.stride_dim, (j * LPR + lane) * VEC, dim, gate);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                z[r][j][i] = gate_act(z[r][j][i], a.activation);
+                if (kBoth || !a.before) gate[i] = gate_act(gate[i], a.activation);
                 if (!a.before) {  // past the row's end x is 0 and the gate finite
-                    x[r][j][i] *= z[r][j][i];
-                    z[r][j][i] = 1.0f;
+                    x[r][j][i] *= gate[i];
+                    gate[i] = 1.0f;
                 }
                 sum = fmaf(x[r][j][i], x[r][j][i], sum);
             }
+            if constexpr (!kBoth) pause_loads<VEC>(j, sum);
+        }
         const float scale = rsqrtf(row_sum<LPR>(sum, warp_sums) / a.dim + a.eps);
-        const int dim = op[r] != nullptr ? a.dim : 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
+            const int d = (j * LPR + lane) * VEC;
+            float(&gate)[VEC] = z[r][kBoth ? j : 0], (&weight)[VEC] = w[kBoth ? j : 0];
+            if constexpr (!kBoth) {
+                load_row<VEC>(a.weight, 1, d, a.dim, weight);
+                if (a.before) load_row<VEC>(gp[r], a.gate.stride_dim, d, dim, gate);
+            }
             float y[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) y[i] = x[r][j][i] * scale * w[j][i] * z[r][j][i];
-            store_row<VEC>(op[r], a.out.stride_dim, (j * LPR + lane) * VEC, dim, y);
+            for (int i = 0; i < VEC; ++i) {
+                if (!kBoth) gate[i] = a.before ? gate_act(gate[i], a.activation) : 1.0f;
+                y[i] = x[r][j][i] * scale * weight[i] * gate[i];
+            }
+            store_row<VEC>(op[r], a.out.stride_dim, d, dim, y);
+            if constexpr (!kBoth) pause_loads<VEC>(j, x[r][j][0]);
         }
     }
 }
@@ -157,23 +191,24 @@ struct ResidualArgs {
 };
 
 template <int LPR, int VEC, int NV, typename Res>
-__global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) residual_rms_norm_kernel(const __grid_constant__ ResidualArgs a) {
+__global__ void __launch_bounds__(norm_threads(LPR), LPR == 1024 ? 1 : 0) residual_rms_norm_kernel(const __grid_constant__ ResidualArgs a) {
     __shared__ float warp_sums[32];
     wait_prior_grid();
     release_next_grid();
-    constexpr int kThreads = LPR > kNormThreads ? LPR : kNormThreads;
+    constexpr int kThreads = norm_threads(LPR);
     const int lane = threadIdx.x % LPR;
     int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
     const int dim = row < a.tokens ? a.dim : 0;
     if (row >= a.tokens) row = 0;
     const uint16_t *xp = a.x + row * a.xt;
     const Res *rp = static_cast<const Res *>(a.residual) + row * a.rt;
-    float x[NV][VEC], h[NV][VEC];
+    constexpr bool kBoth = holds_both(VEC, NV) || (VEC == 8 && sizeof(Res) == 2);
+    float x[NV][VEC], residual[kBoth ? NV : 1][VEC];  // x, then h
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int d = (j * LPR + lane) * VEC;
         load_row<VEC>(xp, a.xd, d, dim, x[j]);
-        load_row<VEC>(rp, a.rd, d, dim, h[j]);
+        if constexpr (kBoth) load_row<VEC>(rp, a.rd, d, dim, residual[j]);
     }
     float post = a.scale;
     if (a.post_weight != nullptr) {
@@ -199,11 +234,14 @@ __global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) resid
 #pragma unroll
             for (int i = 0; i < VEC; ++i) x[j][i] *= f[i];
         }
+        float(&res)[VEC] = residual[kBoth ? j : 0];
+        if constexpr (!kBoth) load_row<VEC>(rp, a.rd, d, dim, res);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            h[j][i] = fmaf(post, x[j][i], h[j][i]);
-            sum = fmaf(h[j][i], h[j][i], sum);
+            x[j][i] = fmaf(post, x[j][i], res[i]);
+            sum = fmaf(x[j][i], x[j][i], sum);
         }
+        if constexpr (!kBoth) pause_loads<VEC>(j, sum);
     }
     const float scale = rsqrtf(row_sum<LPR>(sum, warp_sums) / a.dim + a.eps);
     Res *hp = static_cast<Res *>(a.residual_out) + row * a.rot;
@@ -211,17 +249,20 @@ __global__ void __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) resid
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int d = (j * LPR + lane) * VEC;
-        store_row<VEC>(hp, a.rod, d, dim, h[j]);
+        store_row<VEC>(hp, a.rod, d, dim, x[j]);
         float w[VEC];
         load_row<VEC>(a.weight, 1, d, dim, w);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) w[i] = h[j][i] * scale * (w[i] + a.offset);
+        for (int i = 0; i < VEC; ++i) w[i] = x[j][i] * scale * (w[i] + a.offset);
         store_row<VEC>(op, a.od, d, dim, w);
+        if constexpr (!kBoth) pause_loads<VEC>(j, x[j][0]);
     }
 }
 
 // Calls f.template operator()<LPR, VEC, NV>() with the least lanes a row of `dim` elements needs.  With vectors of 8 a
 // lane holds 1 vector up to 256 elements (a warp's 32 lanes), 2 vectors a lane up to 512, then whole blocks with 2 or 4.
+// Single elements (a length that is not a multiple of 8, a stride, or an address off 16 bytes) go 8 to a lane up to a
+// block's 1024 lanes, then 16 and 32.
 template <typename F>
 int for_row(int dim, bool vec, F f) {
     if (vec) {
@@ -237,6 +278,9 @@ int for_row(int dim, bool vec, F f) {
     }
     if (dim <= 256) return f.template operator()<32, 1, 8>();
     if (dim <= 2048) return f.template operator()<256, 1, 8>();
+    if (dim <= 4096) return f.template operator()<512, 1, 8>();
+    if (dim <= 8192) return f.template operator()<1024, 1, 8>();
+    if (dim <= 16384) return f.template operator()<1024, 1, 16>();
     return f.template operator()<1024, 1, 32>();
 }
 
@@ -258,7 +302,7 @@ struct GatedLaunch {
                                   dim3(kNormThreads), 0, stream, a);
         }
         return launch_pdl(gated_rms_norm_kernel<LPR, VEC, NV, 1>, dim3(row_blocks(a.rows, LPR)),
-                          dim3(LPR > kNormThreads ? LPR : kNormThreads), 0, stream, a);
+                          dim3(norm_threads(LPR)), 0, stream, a);
     }
 };
 
@@ -269,7 +313,7 @@ struct ResidualLaunch {
     template <int LPR, int VEC, int NV>
     int operator()() const {
         return launch_pdl(residual_rms_norm_kernel<LPR, VEC, NV, Res>, dim3(row_blocks(a.tokens, LPR)),
-                          dim3(LPR > kNormThreads ? LPR : kNormThreads), 0, stream, a);
+                          dim3(norm_threads(LPR)), 0, stream, a);
     }
 };
 
