@@ -20,6 +20,14 @@
 // parts, of whose products the ones above 2^-24 are kept: 3 with an exact operand, 6 without.  Products that reach the
 // output alone keep 16 bits (the output has 8).  bf16 parts span the range of fp32, so nothing needs scaling and nothing
 // overflows or vanishes that would not in fp32, however far e^G falls inside a chunk.
+//
+// What is not finite.  A sum over a chunk takes zeros for the tokens after its own, and 0 * NaN is NaN.  So a token whose key or
+// gates are not finite, and a value that is not, are left out of the products; the outputs of the rows that they reach are NaN
+// from that token on, and so is the rows' final state, and tokens before it are what they are without it.  A row of the state
+// that starts with something not finite is NaN throughout.  (What overflows on the way, from finite inputs, can reach all of
+// its chunk.)  The loading warps look at each chunk's values while the one before is worked on, which costs nothing that can
+// be measured on 4 x 4096 tokens and 1% on 11027 (the same look by the computing warps cost 2 to 4%).
+#include <climits>
 #include <cstdlib>
 #include <cstring>
 
@@ -147,6 +155,7 @@ struct PrepSmem {
     uint64_t bar;
     uint32_t tmem;
     int seq, start, end, abort;
+    int odd;  // a token's key or a strength is not finite
 };
 constexpr int kMatrixBytes = 2 * C * kLd * 4;  // A, then T, of two value heads; over the rows of K and Q once they are used
 
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
         }
     }
     if (tid == 32) {
-        sm.abort = 0;
+        sm.abort = sm.odd = 0;
         mbar_init(&sm.bar, 1);
         mbar_init_fence();
     }
@@ -337,8 +346,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
     auto scan_gates = [&] {
         float g = 0.0f, beta = 0.0f;
         if (i < n) gates.get(a.a_log != nullptr, g, beta);
-        // e^-200 is 0 in fp32 and e^1000 infinite: keeps inf - inf out of the differences and the sums in range, and NaN as it is
-        g = g < -200.0f ? -200.0f : g > 1000.0f ? 1000.0f : g;
+        sm.beta[side][i] = g != g ? g : beta;
+        // e^-200 is 0 in fp32 and e^1000 infinite: keeps inf - inf out of the differences and the sums in range
+        g = g < -200.0f ? -200.0f : g > 1000.0f ? 1000.0f : g == g ? g : 0.0f;
         constexpr float kOne = 1099511627776.0f;  // 2^40
         int64_t sum = __float2ll_rn(g * 1.4426950408889634f * kOne);
 #pragma unroll
@@ -352,7 +362,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
         const float hi = __ll2float_rn(sum);
         sm.ghi[side][i] = hi / kOne;
         sm.glo[side][i] = __ll2float_rn(sum - __float2ll_rn(hi)) / kOne;
-        sm.beta[side][i] = g != g ? g : beta;
     };
     scan_gates();
     cp_async_wait<0>();
@@ -375,16 +384,13 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
 
     const uint32_t addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     {
-        float r = 1.0f;
-        if (a.qk_l2norm) {
-            float f[32], square = 0.0f;
-            tmem_load(addr + warp * 32, f);
-            tmem_wait_load();
+        float f[32], square = 0.0f;
+        tmem_load(addr + warp * 32, f);
+        tmem_wait_load();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) square = lane == j ? f[j] : square;
-            r = rsqrtf(square + kGdrNormEps);
-        }
-        (side ? sm.rq : sm.rk)[i] = side ? r * a.scale : r;
+        for (int j = 0; j < 32; ++j) square = lane == j ? f[j] : square;
+        const float r = a.qk_l2norm ? rsqrtf(square + kGdrNormEps) : 1.0f;
+        (side ? sm.rq : sm.rk)[i] = side ? r * a.scale : square < INFINITY ? r : NAN;
     }
     __syncthreads();  // the rows of K and Q are no longer needed: A takes their place
     for (int r0 = 0; r0 < rep; r0 += 2) {
@@ -394,18 +400,21 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
             scan_gates();
             __syncthreads();
         }
+        bool bad = false;  // a key or a strength that is not finite
         if (side < nh) {
             float *vec = reinterpret_cast<float *>(block(r0 + side) + kVec);
             const float ghi = sm.ghi[side][i], glo = sm.glo[side][i], beta = sm.beta[side][i];
             const float decay = ex2(ghi + glo), rk = sm.rk[i];
-            vec[kBeta * C + i] = beta;
-            vec[kKey * C + i] = -beta * rk * decay;
+            bad = !(fabsf(beta * rk) < INFINITY);
+            vec[kBeta * C + i] = bad ? NAN : beta;
+            vec[kKey * C + i] = bad ? 0.0f : -beta * rk * decay;
             vec[kState * C + i] = ex2((sm.ghi[side][C - 1] - ghi) + (sm.glo[side][C - 1] - glo)) * rk;
             vec[kQuery * C + i] = sm.rq[i] * decay;
             if (i == 0) vec[kMisc * C] = ex2(sm.ghi[side][C - 1] + sm.glo[side][C - 1]);
         }
         if (side < nh && i < C / 2)
             sm.from[side][i] = ex2((sm.ghi[side][31] - sm.ghi[side][i]) + (sm.glo[side][31] - sm.glo[side][i])) * sm.rk[i];
+        if (bad) sm.odd = 1;
         __syncthreads();
         // Rows of A (threads of K rows, to shared memory) and of P (threads of Q rows, to the workspace).
         for (int w = 0; w < nh; ++w) {
@@ -471,6 +480,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
                     for (int j = 0; j < 32; j += 4)
                         *reinterpret_cast<float4 *>(out_a + j0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
                 }
+            }
+            if (!side && sm.odd) {  // T has to be finite in the other tokens' rows
+#pragma unroll 1
+                for (int j = 0; j < i; ++j)
+                    if (!(fabsf(out_a[j]) < INFINITY)) out_a[j] = 0.0f;
             }
             if (side) {
                 // Out by bulk copies: a row a thread would touch 32 lines a store.
@@ -560,6 +574,7 @@ struct Stage {
 
 struct ChunkSmem {
     uint64_t full[kStages], empty[kStages];               // a stage is loaded; its chunk's MMAs, the last to use it, are done
+    uint64_t keys_ok[kStages], values_ok[kStages];        // ... and has nothing in its keys, in its values, that is not finite
     uint64_t mma_p, mma_o, mma_n[2], mma_delta[2], mma_out;  // completed by the tensor cores
     uint64_t have_s[2], have_r[2], have_vs[2];            // arrived on by the compute threads, by halves
     uint64_t have_read, have_d;
@@ -568,7 +583,46 @@ struct ChunkSmem {
     uint32_t tmem;
     int abort;
     int seq, start, end;
+    int first_bad[128];  // of every row of S: the first token, from the block's first, that is not finite
+    int any_bad;         // the least of them
 };
+__device__ __forceinline__ void note_bad(ChunkSmem &sm, int row, int token) {
+    atomicMin(&sm.first_bad[row], token);
+    atomicMin(&sm.any_bad, token);
+}
+
+// What is not finite of a chunk in shared memory is left out, by the kLoaders threads `id`.  A token whose strength the
+// preparation has set to NaN loses its key and its strength, and is noted for all rows ...
+template <int PANELS>
+__device__ __forceinline__ void leave_out_keys(ChunkSmem &sm, uint8_t *keys, float *strength, int first_token, int id) {
+    if (fabsf(strength[id]) < INFINITY) return;
+    strength[id] = 0.0f;
+    for (int row = 0; row < 128; ++row) note_bad(sm, row, first_token + id);
+    for (int i = 0; i < PANELS * 8; ++i)
+        *reinterpret_cast<uint4 *>(keys + (i >> 3) * 2 * kTile + id * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_shared();  // for the products, and for the next copy to these places
+}
+// ... a value is set to 0, and noted for its row.
+__device__ __forceinline__ void leave_out_values(ChunkSmem &sm, uint8_t *values, int first_token, int id) {
+    constexpr int kPieces = 2 * kTile / 16 / kLoaders;
+    uint32_t odd = 0u;  // NaN in a half if one of those added to it is not finite
+#pragma unroll 8
+    for (int i = 0; i < kPieces; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(values + (i * kLoaders + id) * 16);
+        for (uint32_t w : {x.x, x.y, x.z, x.w}) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(w), "r"(0u));
+    }
+    if (odd == 0u) return;
+    for (int i = id * 8; i < 2 * kTile / 2; i += kLoaders * 8) {
+        uint16_t *v = reinterpret_cast<uint16_t *>(values) + i;
+        const int row = (i >> 6) & (C - 1), column = (i >> 12) * 64 + (((i >> 3) ^ row) & 7) * 8;
+        for (int k = 0; k < 8; ++k)
+            if ((v[k] & 0x7f80u) == 0x7f80u) {
+                v[k] = 0;
+                note_bad(sm, column + k, first_token + row);
+            }
+    }
+    fence_async_shared();
+}
 
 // S^T (128 rows of values on the lanes of tensor memory) stays in registers; its three bf16 parts, R's and d's go to tensor
 // memory as the A operands.  16 warps do the arithmetic, one issues MMAs, two load the next chunk and one stores the output.
@@ -651,6 +705,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     if (tid == 0) {
         sm.abort = 0;
         for (uint64_t &b : sm.full) mbar_init(&b, kLoaders + 1);
+        for (uint64_t *b : {&sm.keys_ok[0], &sm.keys_ok[1], &sm.values_ok[0], &sm.values_ok[1]}) mbar_init(b, kLoaders);
+        sm.any_bad = INT_MAX;
         for (uint64_t *b : {&sm.empty[0], &sm.empty[1], &sm.mma_p, &sm.mma_o, &sm.mma_n[0], &sm.mma_n[1], &sm.mma_delta[0],
                             &sm.mma_delta[1], &sm.mma_out, &sm.drain})
             mbar_init(b, 1);
@@ -660,6 +716,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
         mbar_init(&sm.out_free, 32);
         mbar_init_fence();
     }
+    if (tid < 128) sm.first_bad[tid] = INT_MAX;
     if (warp == kIssueWarp) tmem_alloc<512>(&sm.tmem);
     tc_fence_before();
     __syncthreads();
@@ -682,7 +739,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                 const uint32_t par = c & 1;
                 const uint32_t kq = smem0 + (c % kStages) * (St::bytes / 16);
                 const uint32_t head = kq + St::head / 16;
-                if (!mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort)) break;
+                if (!mbar_wait_warp(&(FULL ? sm.keys_ok : sm.full)[c % kStages], (c / kStages) & 1, &sm.abort)) break;
                 bool ok = true;
                 // S^T k^T, three parts of S; the keys are exact
 #pragma unroll
@@ -781,6 +838,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             for (int c = 0; FULL && c < chunks; ++c) {
                 if (!mbar_wait_warp(&sm.out_full, c & 1, &sm.abort)) break;
                 const int t0 = s + c * C, n = min(C, e - t0);
+                if (*const_cast<volatile int *>(&sm.any_bad) < (c + 1) * C) {
+                    for (int i = lane; i < C * 128; i += 32)
+                        if (*const_cast<volatile int *>(&sm.first_bad[i & 127]) <= c * C + (i >> 7)) out_tile[i] = 0x7fffu;
+                    __syncwarp();
+                }
                 if constexpr (VIO) {  // two rows a pass, 16 bytes a lane
                     uint16_t *dst = out + (t0 + (lane >> 4)) * a.out.stride_tok + (lane & 15) * 8;
                     const bool wide = (lane & 15) * 8 < width;
@@ -803,7 +865,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             if (!step_only) vv.data = static_cast<const uint16_t *>(a.v.data) + slice * 128 * a.v.stride_dim;
             const uint8_t *heads = p.heads + (static_cast<int64_t>(slot0) * a.num_v_heads + h) * kHeadBytes;
             const int64_t heads_step = static_cast<int64_t>(a.num_v_heads) * kHeadBytes;
-            int c = 0;
+            int c = 0, issued = 0;
             for (; c < chunks; ++c) {
                 const int t0 = s + c * C, n = min(C, e - t0);
                 // Whole chunks come as tensor tiles; a sequence's last rows, which need zeros after them, piece by piece.
@@ -853,10 +915,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                     fence_async_shared();
                 }
                 mbar_arrive(bar);
+                issued = c + 1;
+                if constexpr (FULL) {  // in the first pass a row that is not finite becomes NaN by itself, and that is all it has to
+                    if (!mbar_wait_warp(bar, (c / kStages) & 1, &sm.abort)) break;
+                    leave_out_keys<PANELS>(sm, st, reinterpret_cast<float *>(st + St::head + kVec) + kBeta * C, c * C, id);
+                    mbar_arrive(&sm.keys_ok[c % kStages]);
+                    leave_out_values(sm, st + St::v, c * C, id);
+                    mbar_arrive(&sm.values_ok[c % kStages]);
+                }
             }
             if (c < chunks) {  // gave up: let the copies land before the shared memory goes
                 int quiet = 0;
-                for (int i = max(0, c - kStages); i < c; ++i) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1, &quiet);
+                for (int i = max(0, issued - kStages); i < issued; ++i) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1, &quiet);
             }
         }
     } else {
@@ -880,7 +950,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 
         if (kept || (!FULL && segment == 0)) wait_prior_grid();  // the join's states; and the first segment's goes to the workspace
 
-        f32x2 st[KH / 2];  // this thread's part of row d of S
+        f32x2 st[KH / 2], odd = 0ull;  // this thread's part of row d of S; NaN where it holds a value that is not finite
 #pragma unroll
         for (int k = 0; k < KH; k += 4) {
             const int kk = q * KH + k;
@@ -900,7 +970,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             if (!FULL && segment == 0 && live) *reinterpret_cast<float4 *>(in_segment(p.seg_state, slot, a.dim_v) + kk) = x;
             st[k / 2] = pack2(x.x, x.y);
             st[k / 2 + 1] = pack2(x.z, x.w);
+            if constexpr (FULL) odd = fma2(st[k / 2], 0ull, fma2(st[k / 2 + 1], 0ull, odd));
         }
+        if (odd != 0ull) note_bad(sm, d, 0);
         auto stage = [&](int c) { return base + (c % kStages) * St::bytes; };
         // S^T <- gamma S^T + what the chunk added
         auto add_delta = [&](float gamma) {
@@ -970,7 +1042,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             }
 
             // b v of this thread's tokens
-            if (!(ok = mbar_wait_warp(&sm.full[c % kStages], (c / kStages) & 1, &sm.abort))) break;
+            if (!(ok = mbar_wait_warp(&(FULL ? sm.values_ok : sm.full)[c % kStages], (c / kStages) & 1, &sm.abort))) break;
             const float *f = reinterpret_cast<const float *>(stage(c) + St::head + kVec) + 8 * q;
             // 4 of a token's factors, as pairs
             auto vec4 = [&](int which, int half, int i) { return *reinterpret_cast<const ulonglong2 *>(f + which * C + 32 * half + 4 * i); };
@@ -1097,6 +1169,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
             add_delta(gamma);
             float *to = FULL ? (last ? pool : nullptr)
                              : step_only ? in_segment(p.seg_step, slot, a.dim_k) : in_segment(p.seg_state, slot + 1, a.dim_v);
+            const bool bad = FULL && *const_cast<volatile int *>(&sm.first_bad[d]) != INT_MAX;
             if (to != nullptr && live) {
 #pragma unroll
                 for (int k = 0; k < KH; k += 4) {
@@ -1104,6 +1177,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
                     float4 x;
                     unpack2(st[k / 2], x.x, x.y);
                     unpack2(st[k / 2 + 1], x.z, x.w);
+                    if (bad) x = make_float4(NAN, NAN, NAN, NAN);
                     if (!FULL) {
                         *reinterpret_cast<float4 *>(to + kk) = x;
                     } else if constexpr (V) {

@@ -81,8 +81,13 @@ typedef struct ccv_gdr_args {
  * With dim_k <= 128 and more than 8 tokens a sequence on average the call runs
  * in chunks of 64 tokens on the tensor cores, and where sequences and heads are
  * too few to fill the card also cuts sequences into segments that run side by
- * side; otherwise token by token.  The forms differ in rounding alone.  The
- * choice follows from the integer sizes.  The environment variables
+ * side; otherwise token by token.  On finite inputs the forms differ in
+ * rounding alone.  A value, key, gate or state row that is not finite makes
+ * the outputs of the rows it reaches, from its token on, and their final state
+ * not finite (a query: its own token's), in every form; tokens before it, other
+ * rows and other sequences are as without it.  Finite inputs whose sums leave
+ * fp32's range can in the chunked form also reach the tokens before them in
+ * their 64-token chunk.  The choice follows from the integer sizes.  The environment variables
  * CCV_GDR_PATH=chunked or =recurrent and CCV_GDR_SEGMENT=<chunks of a segment,
  * 0: none>, read at each call, force it (for testing and tuning).
  * workspace     gdr_fwd_workspace(...) bytes, 128-byte aligned, not shared
