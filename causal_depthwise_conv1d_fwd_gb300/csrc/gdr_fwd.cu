@@ -379,7 +379,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
         }
         mma_commit(&sm.bar, one);
     }
-    if (!mbar_wait_warp(&sm.bar, 0, &sm.abort) && lane == 0) count_error(p.err_count);
+    const bool done = mbar_wait_warp(&sm.bar, 0, &sm.abort);
+    if (!done && lane == 0) count_error(p.err_count);
     tc_fence_after();
 
     const uint32_t addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdr_prep_kernel(const __grid_
         tmem_wait_load();
 #pragma unroll
         for (int j = 0; j < 32; ++j) square = lane == j ? f[j] : square;
-        const float r = a.qk_l2norm ? rsqrtf(square + kGdrNormEps) : 1.0f;
+        const float r = !done ? NAN : a.qk_l2norm ? rsqrtf(square + kGdrNormEps) : 1.0f;  // NaN from here to the outputs
         (side ? sm.rq : sm.rk)[i] = side ? r * a.scale : square < INFINITY ? r : NAN;
     }
     __syncthreads();  // the rows of K and Q are no longer needed: A takes their place
@@ -583,6 +584,7 @@ struct ChunkSmem {
     uint32_t tmem;
     int abort;
     int seq, start, end;
+    int first, last, line;  // the block's tokens, and the line that it writes its last state to (-1: none)
     int first_bad[128];  // of every row of S: the first token, from the block's first, that is not finite
     int any_bad;         // the least of them
 };
@@ -704,6 +706,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
 
     if (tid == 0) {
         sm.abort = 0;
+        sm.first = s;
+        sm.last = e;
+        sm.line = last && a.state != nullptr ? line : -1;
         for (uint64_t &b : sm.full) mbar_init(&b, kLoaders + 1);
         for (uint64_t *b : {&sm.keys_ok[0], &sm.keys_ok[1], &sm.values_ok[0], &sm.values_ok[1]}) mbar_init(b, kLoaders);
         sm.any_bad = INT_MAX;
@@ -1195,6 +1200,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) gdr_chunk_kernel(const __gri
     }
     __syncthreads();
     if (warp == kIssueWarp) tmem_free<512>(tmem);
+    if (sm.abort) {  // a wait ran out: nothing that this block should have written may pass for a result
+        unsigned block = blockIdx.x;
+        asm volatile("" : "+r"(block));  // what follows is worked out again, not kept in registers meanwhile
+        const int part = block % types, head = block / types % a.num_v_heads;
+        const bool step = !FULL && part == slices;
+        const int rows = step ? a.dim_k : min(128, a.dim_v - part * 128), row0 = step ? 0 : part * 128;
+        if constexpr (FULL) {
+            uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + head * a.out.stride_head + row0 * a.out.stride_dim;
+            for (int t = sm.first + threadIdx.x / 128; t < sm.last; t += kChunkThreads / 128)
+                if (threadIdx.x % 128 < rows) out[t * a.out.stride_tok + threadIdx.x % 128 * a.out.stride_dim] = 0x7fffu;
+            float *state = a.state + sm.line * a.s_stride_line + head * a.s_stride_head + row0 * a.s_stride_v;
+            for (int i = threadIdx.x; sm.line >= 0 && i < rows * a.dim_k; i += kChunkThreads)
+                state[i / a.dim_k * a.s_stride_v + i % a.dim_k * a.s_stride_k] = NAN;
+        } else {
+            const int64_t at = (static_cast<int64_t>(block / types / a.num_v_heads + (step ? 0 : 1)) * a.num_v_heads + head) * (step ? a.dim_k : a.dim_v) + row0;
+            for (int i = threadIdx.x; i < rows * 64 * PANELS; i += kChunkThreads) (step ? p.seg_step : p.seg_state)[at * 64 * PANELS + i] = NAN;
+        }
+    }
 }
 
 // ------------------------------------------------------------------- join ----
@@ -1303,6 +1326,7 @@ __global__ void __launch_bounds__(256 * PANELS) gdr_join_kernel(const __grid_con
                 int quiet = 0;
                 if (j + 2 < segments) mbar_wait(&full[(j + 1) & 1], (j >> 1) & 1, &quiet);
             }
+            for (++j; real && j < segments; ++j) *row_at(j) = make_float4(NAN, NAN, NAN, NAN);
             return;
         }
         if (adds) {

@@ -90,6 +90,8 @@ typedef struct ccv_gdr_args {
  * their 64-token chunk.  The choice follows from the integer sizes.  The environment variables
  * CCV_GDR_PATH=chunked or =recurrent and CCV_GDR_SEGMENT=<chunks of a segment,
  * 0: none>, read at each call, force it (for testing and tuning).
+ * A wait inside a kernel that runs out (2 s, on work of the same block) is
+ * counted in err_count, and what its block should have written is NaN.
  * workspace     gdr_fwd_workspace(...) bytes, 128-byte aligned, not shared
  *               with another call in flight.
  */
