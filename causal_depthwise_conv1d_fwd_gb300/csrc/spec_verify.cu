@@ -135,7 +135,9 @@ struct Weigh {
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float rate_of(const VerifyArgs &a, int b) {
     const float t = a.temperature != nullptr ? a.temperature[b] : 1.0f;
-    return t > 0.0f ? kLog2e / t : 0.0f;  // 0 marks a greedy row
+    // 0 marks a greedy row.  Any other rate stays finite and above 0: 0 * infinity is NaN, for the largest logit with a
+    // temperature below 4.3e-39 and for masked logits with an infinite one.
+    return t > 0.0f ? fminf(fmaxf(kLog2e / t, __int_as_float(1)), FLT_MAX) : 0.0f;
 }
 
 // Maximum, its first index and the sum of exponentials of one share of one position.  Rows may start at any element: the

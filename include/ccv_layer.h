@@ -176,8 +176,9 @@ int residual_rms_norm(const void *x, int64_t x_stride_tok, int64_t x_stride_dim,
  * num_drafts    int32 [batch] or NULL (all `drafts`): the row's drafts, at
  *               most `drafts`; negative: a padded row, which gets count 0 and
  *               tokens -1.
- * temperature   fp32 [batch] or NULL (1).  0: greedy, p is 1 at the largest
- *               logit (the lowest index on ties).
+ * temperature   fp32 [batch] or NULL (1).  0 (or anything else that is not
+ *               above 0): greedy, p is 1 at the largest logit (the lowest
+ *               index on ties).
  * uniform       fp32 (batch, drafts) in [0, 1); noise fp32 (batch, vocab),
  *               vocab stride 1, > 0, exponentially distributed.
  * Draft i is kept while every earlier one is and uniform_i q_i(x_i) <
