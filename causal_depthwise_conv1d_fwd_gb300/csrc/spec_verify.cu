@@ -415,8 +415,13 @@ int64_t pick_rounds(int batch, int64_t shares, int resident) {
     return (shares + blocks - 1) / blocks;
 }
 
-int64_t stats_blocks(int batch, int drafts, int vocab) {
-    const int64_t rows = static_cast<int64_t>(batch) * (drafts + 1);
+// Rows of logits, or -1 where their blocks would pass a grid's limit.
+int64_t logit_rows(int batch, int drafts, int vocab) {
+    const int64_t positions = static_cast<int64_t>(drafts) + 1, shares = shares_of(vocab, kShare);
+    return vocab > (1 << 30) || positions > 0x7fffffff / batch || batch * positions > 0x7fffffff / shares ? -1 : batch * positions;
+}
+
+int64_t stats_blocks(int64_t rows, int vocab) {
     return rows * shares_of(vocab, stats_share(rows, vocab));
 }
 
@@ -433,7 +438,9 @@ int launch_verify(const VerifyArgs &a, cudaStream_t stream) {
 
 extern "C" int64_t spec_verify_workspace(int batch, int drafts, int vocab) {
     if (batch <= 0 || drafts < 0 || vocab <= 0) return 0;
-    return ccv::stats_blocks(batch, drafts, vocab) * 16 + batch * ccv::shares_of(vocab, ccv::kShare) * 8 + static_cast<int64_t>(batch) * 4;
+    const int64_t rows = ccv::logit_rows(batch, drafts, vocab);
+    if (rows < 0) return 0;
+    return ccv::stats_blocks(rows, vocab) * 16 + batch * ccv::shares_of(vocab, ccv::kShare) * 8 + static_cast<int64_t>(batch) * 4;
 }
 
 extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t_stride_b, int64_t t_stride_pos,
@@ -448,7 +455,8 @@ extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t
                       n_stride_b})
         if (s < 0) return CCV_ERR_STRIDE;
     if (batch == 0) return CCV_OK;
-    if (vocab == 0 || vocab > (1 << 30) || static_cast<int64_t>(batch) * (drafts + 1) * shares_of(vocab, kShare) > 0x7fffffff) return CCV_ERR_SIZE;
+    const int64_t rows = vocab > 0 ? logit_rows(batch, drafts, vocab) : -1;
+    if (rows < 0) return CCV_ERR_SIZE;
     if (target_logits == nullptr || noise == nullptr || out_tokens == nullptr || num_accepted == nullptr ||
         (drafts > 0 && (draft_tokens == nullptr || uniform == nullptr)))
         return CCV_ERR_NULL_POINTER;
@@ -465,12 +473,12 @@ extern "C" int spec_verify(const void *target_logits, int logits_fp32, int64_t t
         (num_drafts != nullptr &&
          (overlaps(et, extent(num_drafts, batch, 1, 1, 0)) || overlaps(ea, extent(num_drafts, batch, 1, 1, 0)))))
         return CCV_ERR_ALIAS;
-    const int share = stats_share(static_cast<int64_t>(batch) * (drafts + 1), vocab);
+    const int share = stats_share(rows, vocab);
     const int size = logits_fp32 ? 4 : 2;
     const int before = aligned16(target_logits) && t_stride_b * size % 16 == 0 && t_stride_pos * size % 16 == 0 ? 0 : 7;
     const int64_t rounds = pick_rounds(batch, shares_of(vocab, kShare, before), logits_fp32 ? kPickBlocks32 : kPickBlocks);
     const int64_t shares = shares_of(vocab, rounds * kShare, before), splits = shares_of(vocab, share, before);
-    uint8_t *space = static_cast<uint8_t *>(workspace), *best = space + stats_blocks(batch, drafts, vocab) * 16;
+    uint8_t *space = static_cast<uint8_t *>(workspace), *best = space + stats_blocks(rows, vocab) * 16;
     const VerifyArgs a{target_logits, t_stride_b, t_stride_pos, draft_tokens, d_stride_b, d_stride_pos, draft_probs, p_stride_b,
                        p_stride_pos, num_drafts, temperature, uniform, u_stride_b, u_stride_pos, noise, n_stride_b, out_tokens,
                        num_accepted, batch, drafts, vocab, share, static_cast<int>(splits),

@@ -204,7 +204,8 @@ int spec_verify(const void *target_logits, int logits_fp32, int64_t t_stride_b, 
                 int batch, int drafts, int vocab, void *workspace, int64_t workspace_bytes,
                 int *err_count, ccv_stream_t stream);
 
-/* Bytes of workspace spec_verify needs for these sizes. */
+/* Bytes of workspace spec_verify needs for these sizes (0: sizes that it
+ * refuses). */
 int64_t spec_verify_workspace(int batch, int drafts, int vocab);
 
 #ifdef __cplusplus
