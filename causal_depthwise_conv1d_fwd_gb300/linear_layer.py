@@ -15,7 +15,9 @@ pool and one of the delta rule's.  While it decodes speculatively it also owns
 one delta-rule line for each token of a step (`step_lines`): a step writes the
 state after every token, and the next one starts from the state after the last
 token that spec_verify kept -- its counts go to ccv_update_spec and gdr_update
-as num_accepted_tokens.
+as num_accepted_tokens.  The sequence's own lines stay as they were before the
+first step; `settle` brings them up to date, for decode, another prefill, or a
+step together with sequences that have not begun to speculate.
 """
 from __future__ import annotations
 
@@ -74,7 +76,8 @@ class LinearAttentionLayer:
 
     def prefill(self, x: torch.Tensor, residual: torch.Tensor, query_start_loc: torch.Tensor,
                 lines: torch.Tensor, has_initial_state: torch.Tensor):
-        """Varlen prompts: x, residual (total_tokens, hidden)."""
+        """Varlen prompts, or their next parts: x, residual (total_tokens, hidden).
+        After speculative steps a sequence is settled first."""
         mixed, z, b, a = self._project(x)
         mixed = api.ccv_fwd(mixed.t(), self.conv_weight, None, self.conv_state, query_start_loc,
                             lines, has_initial_state).t()
@@ -83,7 +86,8 @@ class LinearAttentionLayer:
         return self._finish(o, z, residual)
 
     def decode(self, x: torch.Tensor, residual: torch.Tensor, lines: torch.Tensor):
-        """One token a row: x, residual (batch, hidden)."""
+        """One token a row: x, residual (batch, hidden).  After speculative steps a
+        row is settled first."""
         mixed, z, b, a = self._project(x)
         mixed = api.ccv_update(mixed, self.conv_state, self.conv_weight, None, "silu", lines)
         o = layer.gdr_update(*self._heads(mixed), a, b, self.state, lines, a_log=self.a_log,
@@ -94,7 +98,8 @@ class LinearAttentionLayer:
                num_accepted_tokens: Optional[torch.Tensor]):
         """A speculative step: x, residual (batch, steps, hidden) hold the last
         token and the drafts after it.  num_accepted_tokens is what the step
-        before kept of its own tokens (None: the first step after a prefill)."""
+        before kept of its own tokens (None: the first step after a prefill, a
+        decode or a settle)."""
         batch, steps = x.shape[:2]
         mixed, z, b, a = self._project(x)
         mixed = api.ccv_update_spec(mixed.transpose(1, 2), self.conv_state, self.conv_weight, None,
@@ -103,6 +108,15 @@ class LinearAttentionLayer:
                              self.step_lines[lines.long()], a_log=self.a_log, dt_bias=self.dt_bias)
         x, residual = self._finish(o, z, residual.flatten(0, 1))
         return x.unflatten(0, (batch, steps)), residual.unflatten(0, (batch, steps))
+
+    def settle(self, lines: torch.Tensor, num_accepted_tokens: torch.Tensor):
+        """Ends the rows' speculative steps: their lines become what they are
+        after the tokens that the last step kept (1 or more of them)."""
+        rows, last = lines.long(), num_accepted_tokens.long() - 1
+        self.state[rows] = self.state[self.step_lines[rows, last].long()]
+        window = last[:, None] + torch.arange(self.width - 1, device=last.device)
+        self.conv_state[rows, :, :self.width - 1] = self.conv_state[rows].gather(
+            2, window[:, None].expand(-1, self.mixed, -1))
 
 
 def serve(device="cuda", hidden: int = 256, vocab: int = 1000, rounds: int = 3, seed: int = 0):
