@@ -1354,8 +1354,18 @@ int64_t segment_slots(int total_tokens, int batch, int seg_chunks) {
 
 template <int PANELS>
 constexpr size_t prep_smem() { return kMatrixBytes + sizeof(PrepSmem); }
+// A chunk block takes all tensor memory of its SM and then waits for the preparation, whose blocks may still be about to take
+// theirs: the two must not meet on an SM.  With 64 keys their sizes would let them, so the chunk block asks for the rest.
+// (Their registers do not let them either: 61440 and 16384 of 65536.)
+constexpr size_t kSmShared = 228 * 1024, kBlockShared = 1024;  // of an SM, and what each block takes beside its own
 template <int PANELS>
-constexpr size_t chunk_smem() { return kStages * Stage<PANELS>::bytes + 2 * kTile + sizeof(ChunkSmem); }
+constexpr size_t chunk_smem() {
+    constexpr size_t used = kStages * Stage<PANELS>::bytes + 2 * kTile + sizeof(ChunkSmem);
+    constexpr size_t rest = kSmShared - 2 * kBlockShared - prep_smem<PANELS>() + 16;
+    constexpr size_t bytes = used > rest ? used : rest;
+    static_assert(bytes + prep_smem<PANELS>() + 2 * kBlockShared > kSmShared && bytes + kBlockShared <= kSmShared, "");
+    return bytes;
+}
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                  const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
