@@ -3,7 +3,8 @@
 Every function takes CUDA tensors, reads their pointers and strides, and
 calls the entry point of the same name in libccv.so on the current (or given)
 stream.  No arithmetic of the method happens here and there is no CPU path:
-CPU tensors are rejected.
+CPU tensors are rejected.  An output that a call makes is allocated on the
+stream that it runs on.
 """
 from __future__ import annotations
 

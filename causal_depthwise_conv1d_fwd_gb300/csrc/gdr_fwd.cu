@@ -9,7 +9,7 @@
 //   gdr_prep_kernel   for every chunk and key head at once: the two products, the decays, T = (I + A)^-1, P, and what each
 //                     token multiplies by; written to the workspace in the layout the tensor cores read.
 //   gdr_chunk_kernel  for every sequence and value head: the chunks in order with S^T kept on chip.
-// 4 x 4096 tokens with 32 value heads take 268 us: 93 + 172 and the launches, less what overlaps.
+// 4 x 4096 tokens with 32 value heads take 267 us: 95 + 174 and the launches, less what overlaps.
 // Where sequences and heads are too few for the card, each sequence is cut into segments of chunks.  A segment takes its
 // first state to S M + N; gdr_chunk_kernel first finds N (the segment from a zero state) and M (from the identity, without
 // values) of all segments at once, gdr_join_kernel goes through them for each segment's first state, and gdr_chunk_kernel
@@ -289,8 +289,8 @@ __device__ __forceinline__ void invert(float *matrices, int tid) {
     __syncthreads();
 }
 
-// A block of 4 warps a (chunk, key head), 4 blocks an SM: 4096 of them (4 x 4096 tokens, 16 key and 32 value heads) take 93 us.
-// It writes 344 MB, 3.7 TB/s; what bounds it is latency (44% of the issue slots, 50% of the shared-memory pipe): loads that
+// A block of 4 warps a (chunk, key head), 4 blocks an SM: 4096 of them (4 x 4096 tokens, 16 key and 32 value heads) take 95 us.
+// It writes 344 MB, 3.6 TB/s; what bounds it is latency (44% of the issue slots, 50% of the shared-memory pipe): loads that
 // wait on the search, 14 barriers, and forward substitution.  3, 5 and 6 blocks an SM and 8 warps a block were slower.
 // PANELS: dim_k rounded up to 64 PANELS.  V: rows of q and k allow 16-byte vectors.
 template <int PANELS, bool V>
@@ -631,12 +631,12 @@ __device__ __forceinline__ void leave_out_values(ChunkSmem &sm, uint8_t *values,
 }
 
 // S^T (128 rows of values on the lanes of tensor memory) stays in registers; its three bf16 parts, R's and d's go to tensor
-// memory as the A operands.  16 warps do the arithmetic, one issues MMAs, two load the next chunk and one stores the output.
+// memory as the A operands.  16 warps do the arithmetic, one issues MMAs, two load the next chunk and look at its values, and one stores the output.
 // The chunks are a chain of product, split into parts, product: S k^T, R, d = T R, decayed d, what is added to S.  Of the
 // 2.7 us (5150 cycles) of a chunk the tensor cores work 3200: 24 + 24 products of 32 cycles for S k and d, 16 for S q, 24 for
 // the state, 12 for the output.  The rest is splitting (the sixteen warps' integer and conversion pipes: 1200 cycles for S,
 // 350 for each half of R and d) and 240 cycles from each commit to the waiting warps; halves of R, d and S overlap the two.
-// 4 x 4096 tokens, 32 heads: 128 blocks, 172 us; a block is 640 threads with all registers and all tensor memory of its SM.
+// 4 x 4096 tokens, 32 heads: 128 blocks, 174 us; a block is 640 threads with all registers and all tensor memory of its SM.
 //
 // FULL: outputs and final states.  Otherwise the first pass over segments: N of all but the last, and M of those between
 // (the last block of every group of slices + 1).  V: the state allows 16-byte vectors.  VIO: rows of q, k, v and out do.
@@ -1465,7 +1465,9 @@ bool chunked_dims(int dim_k) { return dim_k <= 128; }
 
 // The recurrent form takes 0.85 us a token of the longest sequence, the chunked one 22 us for up to a chunk of each (1
 // sequence of 32 heads; 7.6 + 2.2 us a token against 35 us for 8, 45 + 13 us against 215 us for 64): they meet at 12 to 22
-// tokens a sequence.  8 on average leaves room for lengths that differ, which only the device knows.
+// tokens a sequence.  8 on average leaves room for lengths that differ, which only the device knows.  It is an average: with 16
+// heads a sequence of 2000 tokens takes 68 us by itself and 1430 in a batch filled up to 256 with empty ones, and one of 1500
+// takes 62 by itself and 1220 beside 255 single tokens (which take 69 by themselves).
 constexpr int kRecurrentTokens = 8;
 
 // CCV_GDR_PATH=recurrent or =chunked, read at each call, forces one form (for testing and tuning).
@@ -1477,13 +1479,14 @@ bool use_chunked(int batch, int total_tokens, int dim_k) {
     return total_tokens > static_cast<int64_t>(kRecurrentTokens) * batch;
 }
 
-// Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device).  In
+// Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device; 11027
+// tokens and 23 sequences of 1 or 40, which the average leaves whole, take 470 us instead of 200 and 40).  In
 // chunk times of a block (2.5 us): the first pass takes 0.95 of one a chunk, a join 0.4 a segment (1 where its blocks take 16
 // rows), and the two launches more take 3.5.  Each pass runs in waves of one block an SM.  11027 tokens take 200 us with 16
 // heads and 92 with 4, against 457 and 433 whole; 1000 tokens and 4 heads, 48 against 51; 4 x 2000 tokens and 8 heads, 97
 // against 102.
 int segment_chunks(int total_tokens, int batch, int num_v_heads, int dim_v) {
-    constexpr int kSms = 152;
+    constexpr int kSms = 152;  // a GB300's: the workspace's size may not depend on the device that is current
     const int chunks = static_cast<int>((static_cast<int64_t>(total_tokens) + static_cast<int64_t>(batch) * C - 1) / (static_cast<int64_t>(batch) * C));
     const int slices = (dim_v + 127) / 128;
     const int64_t heads = static_cast<int64_t>(batch) * num_v_heads;

@@ -5,8 +5,9 @@
 //     d = b (v - a p),  o = a r + d (k.q),  S <- a S + d k^T
 // so both products come out of one pass over the old state, which then stays in registers for the next token.  The
 // state dominates the traffic: 4 dim_k dim_v bytes read and written per head against 2 (2 dim_k + 2 dim_v) for the
-// rest, so the kernel is bound by HBM for more than a few rows (256 rows of 32 heads of 128 x 128: 167 us, 6.4 TB/s; 64 rows
-// of 4 tokens with a state stored after each: 108 us, 6.3 TB/s) and by one memory round trip below that.
+// rest, so the kernel is bound by HBM for more than a few rows (256 rows of 32 heads of 128 x 128: 167 to 177 us on
+// different cards, 6.1 to 6.45 TB/s, and of 256 x 128: 350 us, 6.2 TB/s; 64 rows of 4 tokens with a state stored after each:
+// 107 to 110 us, 6.2 to 6.3 TB/s) and by one memory round trip below that.
 //
 // A row of S (dim_k values, contiguous) belongs to 8 lanes, each holding every eighth group of 4 values: a warp's load
 // of 4 rows covers whole 128-byte lines, the dot products take 3 shuffles, and no shared memory or barrier is needed.

@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? kPickBlocks :
 // Shares of a row: its logits and what is before them up to a 16-byte boundary (see verify_stats_kernel), `before` at most.
 int64_t shares_of(int vocab, int64_t share, int before = 7) { return (static_cast<int64_t>(vocab) + before + share - 1) / share; }
 
-// A block of the statistics takes a long share once that still fills the card (8 blocks an SM): each thread then loads its
+// A block of the statistics takes a long share once that still fills the card (8 blocks on each of its 152 SMs): each thread then loads its
 // second 4 vectors under the first 4's arithmetic.  Below that, shorter shares spread a row over more SMs.
 int stats_share(int64_t rows, int vocab) { return rows * shares_of(vocab, kLongShare) >= 8 * 152 ? kLongShare : kShare; }
 

@@ -1,6 +1,10 @@
 """Python binding of include/ccv_layer.h: the operators a linear-attention layer
 runs next to the causal convolution (gated delta rule, norms, draft
-verification).  Argument marshalling only, as in :mod:`.api`."""
+verification).  Argument marshalling only, as in :mod:`.api`.
+
+A call with `stream` runs on that stream and allocates its workspace and what it
+returns there; its inputs have to be ready on it.  The outputs may be used on the
+caller's stream once that one waits for the given one."""
 from __future__ import annotations
 
 import struct
