@@ -87,17 +87,18 @@ typedef struct ccv_gdr_args {
  * not finite (a query: its own token's), in every form; tokens before it, other
  * rows and other sequences are as without it.  Finite inputs whose sums leave
  * fp32's range can in the chunked form also reach the tokens before them in
- * their 64-token chunk.  The choice follows from the integer sizes.  The environment variables
- * CCV_GDR_PATH=chunked or =recurrent and CCV_GDR_SEGMENT=<chunks of a segment,
- * 0: none>, read at each call, force it (for testing and tuning).
+ * their 64-token chunk.
+ * The choice of form follows from the integer sizes, and so from the average
+ * length: one long sequence among many short or empty ones runs as the average
+ * would.  The environment variables CCV_GDR_PATH=chunked or =recurrent and
+ * CCV_GDR_SEGMENT=<chunks of a segment, 0: none>, read at each call, force it
+ * (for testing and tuning).
+ * Where q, k, v and out have a contiguous dim axis of a multiple of 8 elements,
+ * and strides and addresses that are multiples of 16 bytes, the chunked form
+ * copies whole tiles; otherwise (the (dim, tokens) layout, say) it copies
+ * elements, several times as slow.
  * A wait inside a kernel that runs out (2 s, on work of the same block) is
  * counted in err_count, and what its block should have written is NaN.
- * The choice sees averages: one long sequence among many short or empty ones
- * runs in the form, and as whole as, the average would.  Tensors of q, k, v
- * and out whose dim axis is contiguous, with a multiple of 8 elements and all
- * strides and addresses multiples of 16 bytes, are copied in whole tiles; any
- * others (the (dim, tokens) layout too) element by element, several times as
- * slow.
  * workspace     gdr_fwd_workspace(...) bytes, 128-byte aligned, not shared
  *               with another call in flight.
  */
