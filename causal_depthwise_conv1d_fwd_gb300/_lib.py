@@ -1,5 +1,4 @@
-"""ctypes loader for libccv.so, the CUDA library behind include/ccv.h and
-include/ccv_layer.h.
+"""ctypes loader for libccv.so, the CUDA library behind the headers of include/.
 
 There is no fallback: if the library has not been built, loading raises.
 """
@@ -13,6 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libccv.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "ccv.h")
 LAYER_HEADER = os.path.join(os.path.dirname(HERE), "include", "ccv_layer.h")
+SSM_HEADER = os.path.join(os.path.dirname(HERE), "include", "ccv_ssm.h")
+LOGITS_HEADER = os.path.join(os.path.dirname(HERE), "include", "ccv_logits.h")
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
@@ -84,6 +85,42 @@ LAYER_SIGNATURES = {
     "spec_verify_workspace": ([I32, I32, I32], I64),
 }
 
+
+class SsmArgs(ctypes.Structure):
+    """struct ccv_ssm_args of include/ccv_ssm.h."""
+    _fields_ = [("x", HeadsView), ("z", HeadsView), ("out", HeadsView), ("B", HeadsView),
+                ("C", HeadsView), ("dt", P), ("dt_stride_row", I64), ("dt_stride_tok", I64),
+                ("dt_stride_head", I64), ("A", P), ("D", P), ("dt_bias", P), ("state", P),
+                ("s_stride_line", I64), ("s_stride_head", I64), ("s_stride_dim", I64),
+                ("s_stride_state", I64), ("dt_min", F32), ("dt_max", F32), ("dt_fp32", I32),
+                ("dt_softplus", I32), ("a_per_state", I32), ("num_lines", I32),
+                ("num_heads", I32), ("num_groups", I32), ("head_dim", I32), ("dim_state", I32),
+                ("pad_slot_id", I32)]
+
+
+class LogitsArgs(ctypes.Structure):
+    """struct ccv_logits_args of include/ccv_logits.h."""
+    _fields_ = [("logits", P), ("l_stride_b", I64), ("l_stride_pos", I64), ("out", P),
+                ("o_stride_b", I64), ("o_stride_pos", I64), ("history", P), ("h_stride_line", I64),
+                ("history_indices", P), ("history_lengths", P), ("prompt_lengths", P),
+                ("draft_tokens", P), ("d_stride_b", I64), ("d_stride_pos", I64),
+                ("repetition", P), ("frequency", P), ("presence", P), ("bias_ids", P),
+                ("bias", P), ("b_stride_b", I64), ("mask", P), ("m_stride_b", I64),
+                ("m_stride_pos", I64), ("logits_fp32", I32), ("out_fp32", I32), ("batch", I32),
+                ("num_positions", I32), ("vocab", I32), ("num_lines", I32),
+                ("history_size", I32), ("bias_size", I32), ("pad_slot_id", I32)]
+
+
+# Argument lists of include/ccv_ssm.h and include/ccv_logits.h.
+SSM_SIGNATURES = {
+    "ssm_fwd": ([P, P, I32, P, P, I32, P, I64, P, P], I32),
+    "ssm_fwd_workspace": ([I32, I32, I32, I32, I32, I32, I32], I64),
+    "ssm_update": ([P, P, P, P, I64, I64, I32, I32, I32, P, P], I32),
+}
+LOGITS_SIGNATURES = {
+    "logits_process": ([P, P, P], I32),
+}
+
 _LIB = None
 
 
@@ -102,7 +139,8 @@ def load():
                 f"libccv.so is not built ({LIB_PATH} missing); build it with "
                 "`python -c 'import __graft_entry__ as g; g.build()'`")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in (*SIGNATURES.items(), *LAYER_SIGNATURES.items()):
+        for name, (args, res) in (*SIGNATURES.items(), *LAYER_SIGNATURES.items(),
+                                  *SSM_SIGNATURES.items(), *LOGITS_SIGNATURES.items()):
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res

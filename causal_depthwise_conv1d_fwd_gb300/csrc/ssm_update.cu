@@ -1,0 +1,252 @@
+// Selective state space scan, recurrent form: decode rows, speculative-verify rows, and short varlen sequences.
+//
+// One token of one row of the state (head h, channel p) is
+//     s <- exp(d A) s + (d x) B,   y = s . C
+// over dim_state values.  The state dominates the traffic: 8 bytes a value read and written against 2 for x, z and out over
+// a whole row of it, so the kernel is bound by HBM for more than a few rows and by one memory round trip below that.
+//
+// A row of S (contiguous) belongs to LANES lanes, each holding every LANES-th group of 4 values: a warp's load covers whole
+// 128-byte lines, the sum over the row takes 2 or 3 shuffles, and no shared memory or barrier is needed.
+#include "ssm_common.cuh"
+
+namespace ccv {
+namespace {
+
+constexpr int kSsmThreads = 128;
+
+// 4 values at d..d+3 of a row of `dim`, zeros past its end.  V: one aligned vector load.
+template <bool V>
+__device__ __forceinline__ void load4(const float *p, int64_t stride, int d, int dim, float (&f)[4]) {
+    if constexpr (V) {
+        const float4 x = d < dim ? __ldcs(reinterpret_cast<const float4 *>(p + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = d + i < dim ? p[(d + i) * stride] : 0.0f;
+    }
+}
+template <bool V>
+__device__ __forceinline__ void store4(float *p, int64_t stride, int d, int dim, const float (&f)[4]) {
+    if constexpr (V) {
+        if (d < dim) __stcs(reinterpret_cast<float4 *>(p + d), make_float4(f[0], f[1], f[2], f[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (d + i < dim) p[(d + i) * stride] = f[i];
+    }
+}
+template <bool V>
+__device__ __forceinline__ void load_bf16x4(const uint16_t *p, int64_t stride, int d, int dim, float (&f)[4]) {
+    if constexpr (V) {
+        const uint2 x = d < dim ? *reinterpret_cast<const uint2 *>(p + d) : make_uint2(0u, 0u);
+        f[0] = bf16_lo(x.x); f[1] = bf16_hi(x.x); f[2] = bf16_lo(x.y); f[3] = bf16_hi(x.y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = d + i < dim ? bf16_bits(p[(d + i) * stride]) : 0.0f;
+    }
+}
+
+// LANES x NV x 4: dim_state rounded up.  R: rows of the state a group of lanes has.  PER: A has a value a state.
+// V: dim_state and every stride and pointer allow 16-byte vectors of the state and 8-byte vectors of B and C.
+template <int LANES, int NV, int R, bool PER, bool V>
+__global__ void __launch_bounds__(kSsmThreads) ssm_recurrent_kernel(const __grid_constant__ ccv_ssm_args a,
+                                                                    const __grid_constant__ SsmRows rw, int slices) {
+    constexpr int kGroups = kSsmThreads / LANES;
+    wait_prior_grid();
+    release_next_grid();
+    const int slice = blockIdx.x % slices, b = blockIdx.x / slices;
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const bool first = threadIdx.x == 0 && slice == 0;  // counts a row's error once
+
+    int64_t t0 = 0, row = b;
+    int n = rw.seqlen;
+    if (rw.query_start_loc != nullptr) {
+        const int s = rw.query_start_loc[b], e = rw.query_start_loc[b + 1];
+        if (s < 0 || e < s || e > rw.total_tokens) {
+            if (first) count_error(rw.err_count);
+            return;
+        }
+        t0 = s;
+        n = e - s;
+        row = 0;
+    }
+    if (n == 0) return;
+    const int line = rw.state_indices != nullptr ? rw.state_indices[b] : b;
+    if (line == a.pad_slot_id) return;
+    const bool fresh = a.state == nullptr || (rw.query_start_loc != nullptr &&
+                                              (rw.has_initial_state == nullptr || rw.has_initial_state[b] == 0));
+    bool good = a.state == nullptr || (line >= 0 && line < a.num_lines);
+    int64_t from = line;
+    if (rw.num_accepted != nullptr) {
+        const int kept = rw.num_accepted[b];
+        if (kept >= 1 && kept <= rw.oidx_steps) {
+            from = rw.out_indices[b * rw.oi_stride_b + (kept - 1) * rw.oi_stride_step];
+            good = from >= 0 && from < a.num_lines;
+        } else {
+            good = false;
+        }
+    }
+    if (!good) {
+        if (first) count_error(rw.err_count);
+        return;
+    }
+
+    const int rows = a.num_heads * a.head_dim, rep = a.num_heads / a.num_groups;
+    float s[R][NV][4], decay[R][PER ? NV : 1][PER ? 4 : 1], bias[R], skip[R];
+    int head[R], chan[R], grp[R];
+    bool use[R];
+    int64_t off[R];  // of the row in a state line
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int at = slice * kGroups * R + r * kGroups + group;
+        use[r] = at < rows;
+        head[r] = use[r] ? at / a.head_dim : 0;
+        chan[r] = use[r] ? at - head[r] * a.head_dim : 0;
+        grp[r] = head[r] / rep;
+        off[r] = head[r] * a.s_stride_head + chan[r] * a.s_stride_dim;
+        const float *p = a.state + from * a.s_stride_line + off[r];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            load4<V>(fresh ? a.A : p, a.s_stride_state, (j * LANES + lane) * 4, use[r] && !fresh ? a.dim_state : 0, s[r][j]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if constexpr (PER) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                load4<false>(a.A + static_cast<int64_t>(head[r]) * a.dim_state, 1, (j * LANES + lane) * 4, a.dim_state, decay[r][j]);
+        } else {
+            decay[r][0][0] = a.A[head[r]];
+        }
+        bias[r] = a.dt_bias != nullptr ? a.dt_bias[head[r]] : 0.0f;
+        skip[r] = a.D != nullptr ? a.D[head[r]] : 0.0f;
+    }
+
+    auto at = [&](const ccv_heads_view &v) { return static_cast<const uint16_t *>(v.data) + row * v.stride_row + t0 * v.stride_tok; };
+    const uint16_t *xp = at(a.x), *zp = at(a.z), *bp = at(a.B), *cp = at(a.C);
+    uint16_t *op = const_cast<uint16_t *>(at(a.out));
+    int64_t step = row * a.dt_stride_row + t0 * a.dt_stride_tok;
+
+    for (int t = 0; t < n; ++t) {
+        float y[R], x[R], d[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            x[r] = bf16_bits(xp[head[r] * a.x.stride_head + chan[r] * a.x.stride_dim]);
+            d[r] = ssm_raw_step(a, step + head[r] * a.dt_stride_head);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            d[r] = ssm_step(d[r], bias[r], a);
+            const float dx = d[r] * x[r];
+            const float same = PER ? 0.0f : expf(d[r] * decay[r][0][0]);
+            y[r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                float bv[4], cv[4];
+                load_bf16x4<V>(bp + grp[r] * a.B.stride_head, a.B.stride_dim, (j * LANES + lane) * 4, a.dim_state, bv);
+                load_bf16x4<V>(cp + grp[r] * a.C.stride_head, a.C.stride_dim, (j * LANES + lane) * 4, a.dim_state, cv);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = PER ? expf(d[r] * decay[r][PER ? j : 0][PER ? i : 0]) : same;
+                    s[r][j][i] = fmaf(e, s[r][j][i], dx * bv[i]);
+                    y[r] = fmaf(s[r][j][i], cv[i], y[r]);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 1; m < LANES; m <<= 1)
+#pragma unroll
+            for (int r = 0; r < R; ++r) y[r] += __shfl_xor_sync(kFullMask, y[r], m);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (lane != 0 || !use[r]) continue;
+            float o = fmaf(skip[r], x[r], y[r]);
+            if (a.z.data != nullptr) o *= silu(bf16_bits(zp[head[r] * a.z.stride_head + chan[r] * a.z.stride_dim]));
+            op[head[r] * a.out.stride_head + chan[r] * a.out.stride_dim] = round_bf16(o);
+        }
+        if (rw.out_indices != nullptr) {
+            const int64_t to = rw.out_indices[b * rw.oi_stride_b + t * rw.oi_stride_step];
+            if (to >= a.num_lines) {
+                if (first) count_error(rw.err_count);
+            } else if (to >= 0) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int j = 0; j < NV; ++j)
+                        store4<V>(a.state + to * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
+                                  use[r] ? a.dim_state : 0, s[r][j]);
+            }
+        }
+        xp += a.x.stride_tok;
+        zp += a.z.stride_tok;
+        bp += a.B.stride_tok;
+        cp += a.C.stride_tok;
+        op += a.out.stride_tok;
+        step += a.dt_stride_tok;
+    }
+    if (rw.out_indices == nullptr && a.state != nullptr) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                store4<V>(a.state + line * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
+                          use[r] ? a.dim_state : 0, s[r][j]);
+    }
+}
+
+template <int LANES, int NV, int R, bool PER, bool V>
+int launch(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
+    constexpr int kRows = kSsmThreads / LANES * R;
+    const int slices = (a.num_heads * a.head_dim + kRows - 1) / kRows;
+    const int64_t blocks = static_cast<int64_t>(slices) * rows.batch;
+    if (blocks > 0x7fffffff) return CCV_ERR_SIZE;
+    return launch_pdl(ssm_recurrent_kernel<LANES, NV, R, PER, V>, dim3(static_cast<unsigned>(blocks)), dim3(kSsmThreads), 0, stream,
+                      a, rows, slices);
+}
+
+template <bool PER, bool V>
+int launch_states(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
+    if (a.dim_state <= 16) return launch<4, 1, 2, PER, V>(a, rows, stream);
+    if (a.dim_state <= 32) return launch<8, 1, 2, PER, V>(a, rows, stream);
+    if (a.dim_state <= 64) return launch<8, 2, 2, PER, V>(a, rows, stream);
+    if (a.dim_state <= 128) return launch<8, 4, 2, PER, V>(a, rows, stream);
+    return launch<8, 8, PER ? 1 : 2, PER, V>(a, rows, stream);
+}
+
+bool vector_ok(const ccv_ssm_args &a) {
+    auto bf = [](const ccv_heads_view &v) {
+        return (reinterpret_cast<uintptr_t>(v.data) & 7u) == 0 && v.stride_dim == 1 && v.stride_row % 4 == 0 &&
+               v.stride_tok % 4 == 0 && v.stride_head % 4 == 0;
+    };
+    if (a.dim_state % 4 != 0 || !bf(a.B) || !bf(a.C)) return false;
+    return a.state == nullptr || (aligned16(a.state) && a.s_stride_state == 1 && a.s_stride_line % 4 == 0 &&
+                                  a.s_stride_head % 4 == 0 && a.s_stride_dim % 4 == 0);
+}
+
+}  // namespace
+
+int ssm_launch_recurrent(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
+    const bool vec = vector_ok(a);
+    if (a.a_per_state) return vec ? launch_states<true, true>(a, rows, stream) : launch_states<true, false>(a, rows, stream);
+    return vec ? launch_states<false, true>(a, rows, stream) : launch_states<false, false>(a, rows, stream);
+}
+
+}  // namespace ccv
+
+extern "C" int ssm_update(const ccv_ssm_args *args, const int32_t *state_indices, const int32_t *num_accepted_tokens,
+                          const int32_t *output_state_indices, int64_t oi_stride_b, int64_t oi_stride_step, int oidx_steps,
+                          int batch, int seqlen, int *err_count, ccv_stream_t stream) {
+    using namespace ccv;
+    if (batch < 0 || seqlen < 0) return CCV_ERR_SIZE;
+    const int status = ssm_check(args, batch, seqlen);
+    if (status != CCV_OK) return status;
+    if (oi_stride_b < 0 || oi_stride_step < 0) return CCV_ERR_STRIDE;
+    if (num_accepted_tokens != nullptr && output_state_indices == nullptr) return CCV_ERR_ARGUMENT;
+    if (output_state_indices != nullptr && oidx_steps < seqlen) return CCV_ERR_CAPACITY;
+    if (batch == 0 || seqlen == 0 || args->num_heads == 0 || args->head_dim == 0 || args->dim_state == 0) return CCV_OK;
+    if (args->state == nullptr) return CCV_ERR_NULL_POINTER;
+    const SsmRows rows{nullptr,     state_indices,  nullptr,    num_accepted_tokens, output_state_indices,
+                       oi_stride_b, oi_stride_step, oidx_steps, batch,               seqlen,
+                       0,           err_count};
+    return ssm_launch_recurrent(*args, rows, stream);
+}
