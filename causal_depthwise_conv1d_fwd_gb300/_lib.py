@@ -114,7 +114,7 @@ class LogitsArgs(ctypes.Structure):
 # Argument lists of include/ccv_ssm.h and include/ccv_logits.h.
 SSM_SIGNATURES = {
     "ssm_fwd": ([P, P, I32, P, P, I32, P, I64, P, P], I32),
-    "ssm_fwd_workspace": ([I32, I32, I32, I32, I32, I32, I32], I64),
+    "ssm_fwd_workspace": ([I32, I32, I32, I32, I32, I32, I32, I32], I64),
     "ssm_update": ([P, P, P, P, I64, I64, I32, I32, I32, P, P], I32),
 }
 LOGITS_SIGNATURES = {

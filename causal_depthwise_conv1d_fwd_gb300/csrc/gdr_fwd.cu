@@ -35,7 +35,7 @@
 #include <cstdlib>
 #include <cstring>
 
-#include "ccv_tcgen05.cuh"
+#include "ccv_varlen.cuh"
 #include "gdr_common.cuh"
 
 namespace ccv {
@@ -65,30 +65,6 @@ struct FwdMaps {
     CUtensorMap q, k, v;
     bool use;
 };
-
-// Chunk (or segment) j of sequence i is in slot first_slot(i) + j.  floor(s / u) + i, with u the tokens of a chunk, leaves
-// every sequence room for its ceil(n / u) chunks, needs no sum over the lengths, and total / u + batch slots in all.
-__device__ __forceinline__ int first_slot(int start, int i, int unit) { return start / unit + i; }
-
-// The sequence of a slot, the last i with first_slot(i) <= slot, and its tokens; by a whole warp, 32 candidates at a time.
-__device__ __forceinline__ void find_sequence(const int32_t *query_start_loc, int batch, int slot, int unit, int lane, int &seq, int &start,
-                                              int &end) {
-    int lo = 0, hi = batch;  // the answer is in [lo, hi)
-    do {
-        const int step = (hi - lo + 31) / 32;
-        const int i = min(lo + lane * step, batch), next = max(i, min(i + step, hi));
-        const int at = query_start_loc[i], to = query_start_loc[next];
-        const bool below = i < hi && first_slot(at, i, unit) <= slot;
-        const int last = 31 - __clz(__ballot_sync(kFullMask, below) | 1);
-        lo += last * step;
-        hi = min(hi, lo + step);
-        start = __shfl_sync(kFullMask, at, last);
-        end = __shfl_sync(kFullMask, to, last);
-    } while (hi - lo > 1);
-    seq = lo;
-}
-
-__device__ __forceinline__ bool sequence_ok(int s, int e, int total) { return s >= 0 && e >= s && e <= total; }
 
 // Swizzled tiles need shared memory on a 1024-byte boundary.
 __device__ __forceinline__ bool misplaced(const void *smem, int *err_count) {
@@ -1371,36 +1347,6 @@ constexpr size_t chunk_smem() {
     return bytes;
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's encoder, looked up once (the library links no driver symbols).
-EncodeTiled encoder() {
-    static const EncodeTiled fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            f = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(f);
-    }();
-    return fn;
-}
-
-bool encode_map(CUtensorMap *map, const ccv_heads_view &v, int dim, int heads, int tokens) {
-    const cuuint64_t size[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
-    const cuuint64_t stride[2] = {static_cast<cuuint64_t>(v.stride_head) * 2, static_cast<cuuint64_t>(v.stride_tok) * 2};
-    if ((stride[0] == 0 && heads > 1) || stride[1] == 0 || stride[0] >= 1ull << 40 || stride[1] >= 1ull << 40) return false;
-    const cuuint64_t strides[2] = {heads > 1 ? stride[0] : 16, stride[1]};
-    const cuuint32_t box[3] = {64, 1, C}, one[3] = {1, 1, 1};
-    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(v.data), size, strides, box, one,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int PANELS, bool FULL, bool VS, bool VIO>
 int launch_chunks(const FwdArgs &p, const FwdMaps &maps, int64_t units, cudaStream_t stream) {
     int dev = 0;
@@ -1436,9 +1382,9 @@ int launch_chunked(const FwdArgs &p, cudaStream_t stream) {
     const int64_t prep = static_cast<int64_t>(p.slots) * p.a.num_k_heads;
     if (prep > 0x7fffffff) return CCV_ERR_SIZE;
     FwdMaps maps;
-    maps.use = VIO && encoder() != nullptr && encode_map(&maps.q, p.a.q, p.a.dim_k, p.a.num_k_heads, p.total_tokens) &&
-               encode_map(&maps.k, p.a.k, p.a.dim_k, p.a.num_k_heads, p.total_tokens) &&
-               encode_map(&maps.v, p.a.v, p.a.dim_v, p.a.num_v_heads, p.total_tokens);
+    maps.use = VIO && encode_heads_map(&maps.q, p.a.q, p.a.dim_k, p.a.num_k_heads, p.total_tokens, C) &&
+               encode_heads_map(&maps.k, p.a.k, p.a.dim_k, p.a.num_k_heads, p.total_tokens, C) &&
+               encode_heads_map(&maps.v, p.a.v, p.a.dim_v, p.a.num_v_heads, p.total_tokens, C);
     int status = launch_pdl(gdr_prep_kernel<PANELS, VIO>, dim3(static_cast<unsigned>(prep)), dim3(kPrepThreads),
                             prep_smem<PANELS>(), stream, p);
     if (status != CCV_OK) return status;

@@ -91,6 +91,13 @@ def _pack_ssm(x, dt, A, B, C, state, D, z, dt_bias, dt_softplus, dt_limit, pad_s
     return dev, packed, out, (h, g, p, n, 1 if per_state else 0)
 
 
+def _mapped(t: torch.Tensor, channels: bool = False) -> bool:
+    """Whether the chunked form reads a (tokens, heads, dim) tensor as it is (ssm_fwd_workspace)."""
+    st = t.stride()
+    return (not channels and st[2] == 1 and t.data_ptr() % 16 == 0 and st[0] > 0 and st[0] % 8 == 0
+            and (t.shape[1] == 1 or (st[1] > 0 and st[1] % 8 == 0)))
+
+
 def ssm_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
             state: Optional[torch.Tensor], query_start_loc: torch.Tensor,
             cache_indices: Optional[torch.Tensor] = None,
@@ -152,7 +159,8 @@ def _marshal_fwd(x, dt, A, B, C, state, query_start_loc, cache_indices, has_init
         if hi.dtype not in (torch.bool, _U8):
             raise TypeError("has_initial_state must be bool or uint8")
         hi = _vector(dev, hi, "has_initial_state", hi.dtype, batch)
-    size = _lib.load().ssm_fwd_workspace(total, batch, *sizes)
+    copies = not (_mapped(x, x.dim() == 2) and _mapped(B) and _mapped(C))
+    size = _lib.load().ssm_fwd_workspace(total, batch, *sizes, 1 if copies else 0)
     scratch = _workspace(dev, workspace, size, x)
     args = (packed, qsl, batch, ci, hi, total, scratch.data_ptr(), scratch.shape[0],
             _err(dev, err_count))

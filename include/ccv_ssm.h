@@ -70,9 +70,12 @@ int ssm_fwd(const ccv_ssm_args *args, const int32_t *query_start_loc, int batch,
             void *workspace, int64_t workspace_bytes, int *err_count, ccv_stream_t stream);
 
 /* Bytes of workspace ssm_fwd needs for these sizes (0: none, or sizes that it
- * refuses). */
+ * refuses).  copies: whether x, B or C have to be copied for the chunked form,
+ * which reads rows of 16-byte pieces: they need not where each has stride_dim 1,
+ * its address on 16 bytes, and strides of tokens and (of more than one) heads
+ * that are multiples of 8 and above 0. */
 int64_t ssm_fwd_workspace(int total_tokens, int batch, int num_heads, int num_groups, int head_dim,
-                          int dim_state, int a_per_state);
+                          int dim_state, int a_per_state, int copies);
 
 /*
  * ssm_update -- the scan over `seqlen` new tokens of each of `batch` rows

@@ -103,8 +103,8 @@ def test_ssm_workspace(lib):
     """What ssm_fwd needs is refused when it is missing, too small or misaligned; sizes that it refuses need none."""
     for sizes in ((1 << 14, 4, 8, 2, 64, 128, 0), (1 << 14, 1, 2, 1, 64, 128, 0), (5000, 1, 512, 1, 1, 16, 1)):
         total, batch, heads, groups, dim, states, per = sizes
-        need = lib.ssm_fwd_workspace(*sizes)
-        assert need >= 0
+        need = lib.ssm_fwd_workspace(*sizes, 0)
+        assert 0 <= need <= lib.ssm_fwd_workspace(*sizes, 1)
         if need:
             kw = dict(total=total, batch=batch, heads=heads, groups=groups, dim=dim, states=states, per=per)
             if dim == 1:  # (tokens, channels)
@@ -116,7 +116,7 @@ def test_ssm_workspace(lib):
             assert fwd(lib, ws=0xA0000008, **kw) == WORK
     for sizes in ((-1, 1, 8, 2, 64, 128, 0), (1 << 14, 1, 8, 3, 64, 128, 0), (1 << 14, 1, 8, 2, 64, 257, 0), (1 << 14, -1, 8, 2, 64, 128, 0),
                   (0, 1, 8, 2, 64, 128, 0), ((1 << 30) + 1, 1, 8, 2, 64, 128, 0), (1 << 14, 1, 0, 0, 64, 128, 0)):
-        assert lib.ssm_fwd_workspace(*sizes) == 0
+        assert lib.ssm_fwd_workspace(*sizes, 1) == 0
 
 
 def test_ssm_update_refusals(lib):
