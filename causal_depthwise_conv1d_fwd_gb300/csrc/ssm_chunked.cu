@@ -6,12 +6,13 @@
 //     S  <- e^{G_Q} S + sum_j B_j^T (e^{G_Q - G_j} d_j x_j)
 // and C B^T is the same for all heads of a group.  Nothing but S is sequential, and S only by its own multiply-add, so all
 // products of a chunk run beside those of its neighbours.  A block has two heads of a group of one sequence (or segment) and
-// goes through its chunks:
-//   warpgroups 0, 1  a head each: M from C B^T (tensor memory to tensor memory), then the head's outputs
-//   warpgroups 2, 3  a head each: the state in registers (thread n has row n), its parts to shared memory for C S, and the
-//                    weighted tokens' parts for the state's sum
-//   four warps       copies and steps; products C B^T and M x; products of the state's sum; products C S
-// Heads wider than 64 are cut into panels of 64 that share steps and decays.
+// goes through its chunks with four warpgroups, two a head, which all run the same code on a half each:
+//   M from C B^T (tensor memory to tensor memory), 64 of its columns;
+//   the state in registers (thread n has half of row n), its parts to shared memory for C S, and its multiply-add;
+//   the weighted tokens' parts for the state's sum; and the outputs, 32 channels.
+// Four more warps copy tiles and sum the steps, and issue products: C B^T and M x, the state's sum, C S.
+// Heads wider than 64 are cut into panels of 64 that share steps and decays.  With a role a warpgroup the hot instructions were
+// twice as many and missed the instruction cache: a third of all stalls.
 //
 // Precision.  The state is fp32, so the operands of what reaches it keep 24 bits: B enters as its own bf16 values (exact), the
 // weighted tokens as three bf16 parts, and the sum over chunks is an fp32 multiply-add.  Products that reach the output alone
@@ -56,20 +57,35 @@ struct Smem {
     uint8_t w[2][3][kQuarter];  // head, part: weighted tokens
     uint8_t s[2][kTile];        // part: the state of the head whose turn it is
     Gates gates[2][2];          // stage, head
-    float weight[2][Q];         // head: what tokens count for in the state's sum
     float factor[2][192];       // head: what the 32, 64, 96 tokens before warps 1, 2, 3 count for in their rows of M
+    float since[2][Q];          // head: G of a token since its warp's first
     // A barrier's phase is waited for by the same threads each time, or by ones that know the phase before it to be over: a wait
     // tells a phase from the next one only.
     uint64_t xb_full[2], xb_free[2], c_full, c_free, gates_full[2], gates_free[2];
     uint64_t cb_full, cb_free, m_full[2], m_free[2], mx_full[2], mx_free, cs_full[2], cs_free, s_full, s_free[2];
-    uint64_t w_full[2], w_free[2], sum_full[2], x_ok[2][2], together[2], cleared[2], drain[3];
-    int first_bad[2][2][64];    // stage, head, channel: the first token whose x is not finite
-    int any_bad[2][2];
+    uint64_t w_full[2], w_free[2], sum_full[2], x_ok[2][2], drain[3];
+    int first_bad[2][64];       // head, channel: the first of the block's tokens whose x is not finite
+    int any_bad[2];
     int seq, start, end, abort;
     uint32_t tmem;
 };
 constexpr size_t kSmemBytes = sizeof(Smem);
 static_assert(kSmemBytes <= 227 * 1024, "");
+
+// mbar_wait for a whole warp whose lanes stay together.
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    uint64_t start = 0;
+    for (int i = 1; !__all_sync(kFullMask, mbar_try_wait(bar, parity)); ++i) {
+        if ((i & 63) != 0) continue;
+        const uint64_t now = timer_ns();
+        if (start == 0) start = now;
+        if (__any_sync(kFullMask, *abort != 0 || now - start > kMaxWaitNs)) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
 
 // The warp's own arrival, after all its lanes are done.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
@@ -77,19 +93,22 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
+// Called and not inlined: eight copies of it would be a tenth of the kernel's instructions, which have to fit the SM's cache.
+__device__ __noinline__ float step_of(float raw, float bias, const ccv_ssm_args &a) { return ssm_step(raw, bias, a); }
+
 __device__ __forceinline__ f32x2 same2(float x) { return pack2(x, x); }
 __device__ __forceinline__ bool odd_bf16x2(uint32_t w) {  // either is not finite
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
 // FULL: outputs and the sequences' final states; otherwise segments' own states for the join.
-// NP: panels of 64 states.  VO: rows of out (and z) allow 16-byte vectors.
-template <bool FULL, int NP>
+// NP: panels of 64 states.  GATED: with z.  vec_out: rows of out (and z) allow 16-byte vectors.
+template <bool FULL, int NP, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_constant__ SsmFwd p, const __grid_constant__ Maps maps, int vec_out) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const ccv_ssm_args &a = p.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
     const int panels = (a.head_dim + 63) / 64, rep = a.num_heads / a.num_groups;
     const int per_group = (rep * panels + 1) / 2, pairs = a.num_groups * per_group;
     const int unit = blockIdx.x / pairs, pair = blockIdx.x % pairs;
@@ -153,33 +172,31 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         const auto init = [](uint64_t &b, int n) { mbar_init(&b, n); };
         for (int i = 0; i < 2; ++i) {
             init(sm.xb_full[i], 1);
-            init(sm.xb_free[i], FULL ? 2 + 4 * nh : 1);  // both issuers of products, and the outputs' warps
+            init(sm.xb_free[i], FULL ? 2 + 8 * nh : 1);  // both issuers of products, and the outputs' warps
             init(sm.gates_full[i], 1);
-            init(sm.gates_free[i], FULL ? 8 * nh : 4 * nh);
+            init(sm.gates_free[i], 8 * nh);
             init(sm.m_full[i], 4);
             init(sm.m_free[i], 1);
-            init(sm.w_full[i], 4);
+            init(sm.w_full[i], 8);
             init(sm.w_free[i], 1);
             init(sm.sum_full[i], 1);
             init(sm.mx_full[i], 1);
             init(sm.cs_full[i], 1);
             init(sm.s_free[i], 1);
-            for (int k = 0; k < 2; ++k) init(sm.x_ok[i][k], 4);
-            init(sm.together[i], 4);
-            init(sm.cleared[i], 4);
+            for (int k = 0; k < 2; ++k) init(sm.x_ok[i][k], 8);
         }
         init(sm.c_full, 1);
         init(sm.c_free, 2);
         init(sm.cb_full, 1);
-        init(sm.cb_free, 4 * nh);
-        init(sm.mx_free, 4);
-        init(sm.cs_free, 4);
-        init(sm.s_full, 4);
+        init(sm.cb_free, 8 * nh);
+        init(sm.mx_free, 8);
+        init(sm.cs_free, 8);
+        init(sm.s_full, 8);
         for (uint64_t &b : sm.drain) init(b, 1);
         mbar_init_fence();
     }
-    if (tid < 256) (&sm.first_bad[0][0][0])[tid] = INT_MAX;
-    if (tid < 4) (&sm.any_bad[0][0])[tid] = 0;
+    if (tid < 128) sm.first_bad[tid >> 6][tid & 63] = INT_MAX;
+    if (tid < 2) sm.any_bad[tid] = 0;
     if (warp == kCopyWarp) tmem_alloc<512>(&sm.tmem);
     tc_fence_before();
     __syncthreads();
@@ -210,14 +227,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         fetch(0);
         for (; c < chunks; ++c) {
             const int st = c & 1, t0 = s + c * Q;
-            if (c >= 2 && !mbar_wait_warp(&sm.xb_free[st], (c / 2 - 1) & 1, abort)) break;
+            if (c >= 2 && !wait_all(&sm.xb_free[st], (c / 2 - 1) & 1, abort)) break;
             if (lane == 0) {
                 mbar_expect_tx(&sm.xb_full[st], (2 + nh) * kTile);
                 for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.xb_full[st]);
                 for (int k = 0; k < nh; ++k) tensor_load(sm.x[st][k], &maps.x, ((v0 + k) % panels) * 64, head[k], t0, &sm.xb_full[st]);
             }
             issued = c + 1;
-            if (c >= 2 && !mbar_wait_warp(&sm.gates_free[st], (c / 2 - 1) & 1, abort)) break;
+            if (c >= 2 && !wait_all(&sm.gates_free[st], (c / 2 - 1) & 1, abort)) break;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 if (k >= nh) break;
@@ -226,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const bool real = t0 + lane * 4 + i < e;
-                    d[i] = real ? ssm_step(raw[k][i], bias[k], a) : 0.0f;
+                    d[i] = real ? step_of(raw[k][i], bias[k], a) : 0.0f;
                     // e^-200 is 0 in fp32 and e^1000 infinite: keeps the sums in range
                     float u = d[i] * scale[k];
                     u = u < -200.0f ? -200.0f : u > 1000.0f ? 1000.0f : u == u ? u : 0.0f;
@@ -254,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             warp_arrive(&sm.gates_full[st], lane);
             if (c + 1 < chunks) fetch(c + 1);
             if constexpr (FULL) {
-                if (c >= 1 && !mbar_wait_warp(&sm.c_free, (c - 1) & 1, abort)) break;
+                if (c >= 1 && !wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
                 if (lane == 0) {
                     mbar_expect_tx(&sm.c_full, NP * kTile);
                     for (int i = 0; i < NP; ++i) tensor_load(sm.c[i], &maps.c, i * 64, group, t0, &sm.c_full);
@@ -263,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         }
         if (c < chunks) {  // gave up: let the copies land before the shared memory goes
             int quiet = 0;
-            for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait_warp(&sm.xb_full[i & 1], (i / 2) & 1, &quiet);
-            if (FULL && c > 0) mbar_wait_warp(&sm.c_full, (c - 1) & 1, &quiet);
+            for (int i = max(0, issued - 2); i < issued; ++i) wait_all(&sm.xb_full[i & 1], (i / 2) & 1, &quiet);
+            if (FULL && c > 0) wait_all(&sm.c_full, (c - 1) & 1, &quiet);
         }
     } else if (warp == kOutWarp) {
         if constexpr (FULL) {
@@ -273,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             for (; c < chunks; ++c) {
                 const int st = c & 1;
                 const uint32_t b = desc_low(smem_u32(sm.b[st][0])), cc = desc_low(smem_u32(sm.c[0]));
-                if (!mbar_wait_warp(&sm.xb_full[st], (c / 2) & 1, abort) || !mbar_wait_warp(&sm.c_full, c & 1, abort)) break;
-                if (c >= 1 && !mbar_wait_warp(&sm.cb_free, (c - 1) & 1, abort)) break;
+                if (!wait_all(&sm.xb_full[st], (c / 2) & 1, abort) || !wait_all(&sm.c_full, c & 1, abort)) break;
+                if (c >= 1 && !wait_all(&sm.cb_free, (c - 1) & 1, abort)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 4 * NP; ++ks) {
@@ -286,11 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 for (k = 0; k < nh; ++k) {
                     const int u = c * nh + k;
                     const uint32_t x = desc_low(smem_u32(sm.x[st][k]));
-                    if (!mbar_wait_warp(&sm.x_ok[st][k], (c / 2) & 1, abort)) break;
-                    if (u >= 1 && !mbar_wait_warp(&sm.mx_free, (u - 1) & 1, abort)) break;
+                    if (!wait_all(&sm.x_ok[st][k], (c / 2) & 1, abort)) break;
+                    if (u >= 1 && !wait_all(&sm.mx_free, (u - 1) & 1, abort)) break;
                     int half = 0;
                     for (; half < 2; ++half) {
-                        if (!mbar_wait_warp(&sm.m_full[half], u & 1, abort)) break;
+                        if (!wait_all(&sm.m_full[half], u & 1, abort)) break;
                         tc_fence_after();
 #pragma unroll
                         for (int part = 1; part >= 0; --part)
@@ -310,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 if (el) count_error(p.err_count);
                 int quiet = 0;
                 mma_commit(&sm.drain[0], el);
-                mbar_wait_warp(&sm.drain[0], 0, &quiet);
+                wait_all(&sm.drain[0], 0, &quiet);
             }
         }
     } else if (warp == kSumWarp) {
@@ -319,10 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         for (int c = 0; ok && c < chunks; ++c) {
             const int st = c & 1;
             const uint32_t b = desc_low(smem_u32(sm.b[st][0])) | ((kTile / 16) << 16);  // MN-major: its panels are kTile apart
-            if (!(ok = mbar_wait_warp(&sm.xb_full[st], (c / 2) & 1, abort))) break;
+            if (!(ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort))) break;
             for (int q = 0; ok && q < 4; ++q)
                 for (int k = 0; k < nh; ++k) {
-                    if (!(ok = mbar_wait_warp(&sm.w_full[k], q & 1, abort))) break;
+                    if (!(ok = wait_all(&sm.w_full[k], q & 1, abort))) break;
                     tc_fence_after();
                     const uint32_t w = desc_low(smem_u32(sm.w[k][0]));
 #pragma unroll
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             if (el) count_error(p.err_count);
             int quiet = 0;
             mma_commit(&sm.drain[1], el);
-            mbar_wait_warp(&sm.drain[1], 0, &quiet);
+            wait_all(&sm.drain[1], 0, &quiet);
         }
     } else if (warp == kStateWarp) {
         if constexpr (FULL) {
@@ -348,11 +365,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             const uint32_t cc = desc_low(smem_u32(sm.c[0])), s0 = desc_low(smem_u32(sm.s[0]));
             bool ok = true;
             for (int c = 0; ok && c < chunks; ++c) {
-                if (!(ok = mbar_wait_warp(&sm.c_full, c & 1, abort))) break;
+                if (!(ok = wait_all(&sm.c_full, c & 1, abort))) break;
                 for (int k = 0; k < nh; ++k) {
                     const int u = c * nh + k;
-                    if (!(ok = mbar_wait_warp(&sm.s_full, u & 1, abort))) break;
-                    if (u >= 1 && !(ok = mbar_wait_warp(&sm.cs_free, (u - 1) & 1, abort))) break;
+                    if (!(ok = wait_all(&sm.s_full, u & 1, abort))) break;
+                    if (u >= 1 && !(ok = wait_all(&sm.cs_free, (u - 1) & 1, abort))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int part = 1; part >= 0; --part)
@@ -369,205 +386,144 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 if (el) count_error(p.err_count);
                 int quiet = 0;
                 mma_commit(&sm.drain[2], el);
-                mbar_wait_warp(&sm.drain[2], 0, &quiet);
+                wait_all(&sm.drain[2], 0, &quiet);
             }
         }
-    } else if (warp >= 8) {
-        // The state of one head: thread n has its row n.
-        const int k = (warp >> 2) & 1, n = tid & 127;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        if (k < nh) {
-            const int h = group * rep + (v0 + k) / panels, panel = (v0 + k) % panels, width = min(64, a.head_dim - panel * 64);
-            const int64_t v = static_cast<int64_t>(group) * rep * panels + v0 + k;  // among all panels of all heads
-            float *pool = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + panel * 64 * a.s_stride_dim +
-                                                   n * a.s_stride_state
-                                             : nullptr;
-            float *slot = p.seg_chunks > 0 ? p.seg_state + (unit * static_cast<int64_t>(a.num_heads) * panels + v) * kStateFloats + n : nullptr;
-            f32x2 st2[32];
-            {
-                const bool init = FULL && segments == 1 && a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
+    } else if ((warp >> 3) < nh) {
+        // Thread i of a warpgroup has token i and row i of the state; the warpgroup has half `hf` of head k's channels, and of M.
+        const int k = warp >> 3, hf = (warp >> 2) & 1, w = warp & 3, i = tid & 127;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
+        const uint32_t col_cb = lanes + kColCB + hf * 64, col_m = lanes + kColM + hf * 64, col_sum = lanes + kColSum + k * 64 + hf * 32;
+        const uint32_t col_mx = lanes + kColMX + hf * 32, col_cs = lanes + kColCS + hf * 32;
+        const int h = group * rep + (v0 + k) / panels, panel = (v0 + k) % panels;
+        const int first = panel * 64 + hf * 32, width = max(0, min(32, a.head_dim - first));  // channels of the head
+        const int64_t v = static_cast<int64_t>(group) * rep * panels + v0 + k;                // among all panels of all heads
+        float *pool = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + first * a.s_stride_dim + i * a.s_stride_state
+                                         : nullptr;
+        float *slot = p.seg_chunks > 0 ? p.seg_state + (unit * static_cast<int64_t>(a.num_heads) * panels + v) * kStateFloats + hf * 32 * 128 + i : nullptr;
+        f32x2 st2[16];  // two channels each
+        {
+            const bool kept = FULL && segments > 1, init = a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
+            const float *from = kept ? slot : pool;
+            const int64_t step = kept ? 128 : a.s_stride_dim;
+            const int count = kept ? 32 : FULL && init && i < a.dim_state ? width : 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float f[2];
+            for (int j = 0; j < 16; ++j) {
+                float f[2];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int ch = 2 * i + j;
-                        f[j] = 0.0f;
-                        if (FULL && segments > 1) f[j] = slot[ch * 128];
-                        else if (init && ch < width && n < a.dim_state) f[j] = pool[ch * a.s_stride_dim];
-                    }
-                    st2[i] = pack2(f[0], f[1]);
-                }
+                for (int l = 0; l < 2; ++l) f[l] = 2 * j + l < count ? from[(2 * j + l) * step] : 0.0f;
+                st2[j] = pack2(f[0], f[1]);
             }
-            float whole = 1.0f;  // decay over all tokens
-            int cleared = 0;
-            bool ok = true;
-            for (int c = 0; c < chunks; ++c) {
-                const int stage = c & 1, rows = min(Q, e - s - c * Q);
-                if (!(ok = mbar_wait_warp(&sm.gates_full[stage], (c / 2) & 1, abort))) break;
-                const Gates &g = sm.gates[stage][k];
-                const float ghi = g.hi[Q - 1], glo = g.lo[Q - 1];
-                const float gamma = ex2_approx(ghi + glo);
-                sm.weight[k][n] = g.d[n] * ex2_approx((ghi - g.hi[n]) + (glo - g.lo[n]));
-                warp_arrive(&sm.gates_free[stage], lane);
-                if constexpr (FULL) {
-                    // the state's parts for C S, once the other head's (or the last chunk's) are used
-                    const int from = k == 0 ? nh - 1 : 0, turn = k == 0 ? c - 1 : c;
-                    if (turn >= 0 && !(ok = mbar_wait_warp(&sm.s_free[from], turn & 1, abort))) break;
+        }
+        const float skip = FULL && a.D != nullptr ? a.D[h] : 0.0f;
+        uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + first * a.out.stride_dim;
+        const uint16_t *z = static_cast<const uint16_t *>(a.z.data) + h * a.z.stride_head + first * a.z.stride_dim;
+        // M's columns of tokens after a warp's own are zero, and nothing writes them again.
+        if constexpr (FULL) {
+            const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint32_t hi[4], mid[4];
+            for (int b = 0; b < 2; ++b)
+                if (k == 0 && 2 * hf + b > w) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) split_bf16x2(st2[4 * i + j], hi[j], mid[j]);
-                        const int at = n * 128 + ((i ^ (n & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(sm.s[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(sm.s[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    }
-                    fence_async_shared();
-                    warp_arrive(&sm.s_full, lane);
+                    for (int j = 0; j < 4; ++j) tmem_store(col_m + (j & 1) * 32 + b * 16 + (j >> 1) * 8, none);
                 }
-                // the tokens' parts, and what is wrong with the tile: rows of another sequence, values that are not finite
-                if (!(ok = mbar_wait_warp(&sm.xb_full[stage], (c / 2) & 1, abort))) break;
-                const bool stale = sm.any_bad[stage][k] != 0;  // of two chunks ago, whose readers are done (the stage was free)
-                warp_arrive(&sm.together[k], lane);            // the weights are there, and all have looked
-                if (!(ok = mbar_wait_warp(&sm.together[k], c & 1, abort))) break;
-                if (stale) {
-                    if (n < 64) sm.first_bad[stage][k][n] = INT_MAX;
-                    if (n == 64) sm.any_bad[stage][k] = 0;
-                    warp_arrive(&sm.cleared[k], lane);
-                    if (!(ok = mbar_wait_warp(&sm.cleared[k], cleared & 1, abort))) break;
-                    ++cleared;
+            tmem_wait_store();
+        }
+        float whole = 1.0f;  // decay over all tokens
+        bool ok = true;
+        int c = 0;
+        for (; c < chunks; ++c) {
+            const int stage = c & 1, u = c * nh + k, rows = min(Q, e - s - c * Q);
+            if (!(ok = wait_all(&sm.gates_full[stage], (c / 2) & 1, abort))) break;
+            const Gates &g = sm.gates[stage][k];
+            const float end_hi = g.hi[Q - 1], end_lo = g.lo[Q - 1], ghi = g.hi[i], glo = g.lo[i];
+            const float gamma = ex2_approx(end_hi + end_lo);
+            float here = 0.0f, own = 0.0f, row_decay = 0.0f;
+            float *before = sm.factor[k] + 16 * w * (w - 1);
+            if constexpr (FULL) {
+                const float base_hi = w > 0 ? g.hi[w * 32 - 1] : 0.0f, base_lo = w > 0 ? g.lo[w * 32 - 1] : 0.0f;
+                own = (ghi - base_hi) + (glo - base_lo);  // since the warp's first token
+                here = ex2_approx(own);
+                row_decay = ex2_approx(ghi + glo);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int j = (2 * hf + b) * 32 + lane;
+                    if (2 * hf + b < w) before[j] = g.d[j] * ex2_approx((base_hi - g.hi[j]) + (base_lo - g.lo[j]));
+                    if (2 * hf + b == w) sm.since[k][i] = own;
                 }
-                uint8_t *xt = sm.x[stage][k];
-                const int piece = n & 7;
+                // the state's parts for C S, once the other head's (or the last chunk's) are used
+                const int from = k == 0 ? nh - 1 : 0, turn = k == 0 ? c - 1 : c;
+                if (turn >= 0 && !(ok = wait_all(&sm.s_free[from], turn & 1, abort))) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t hi[4], mid[4];
+#pragma unroll
+                    for (int l = 0; l < 4; ++l) split_bf16x2(st2[4 * j + l], hi[l], mid[l]);
+                    const int at = i * 128 + (((hf * 4 + j) ^ (i & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(sm.s[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(sm.s[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                }
+                fence_async_shared();
+                warp_arrive(&sm.s_full, lane);
+            }
+            // the tokens' parts, and what is wrong with the tile: rows of another sequence, values that are not finite
+            if (!(ok = wait_all(&sm.xb_full[stage], (c / 2) & 1, abort))) break;
+            uint8_t *xt = sm.x[stage][k];
+            {
+                const int piece = i & 7, in = hf * 16 + (i >> 3), sw = (piece ^ (in & 7)) << 4;
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
-                    if ((c > 0 || q > 0) && !(ok = mbar_wait_warp(&sm.w_free[k], (q - 1) & 1, abort))) break;
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int in = r * 16 + (n >> 3), row = q * 32 + in, sw = (piece ^ (row & 7)) << 4;
-                        uint4 x = *reinterpret_cast<const uint4 *>(xt + row * 128 + sw);
-                        if (row >= rows) {
-                            x = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4 *>(xt + row * 128 + sw) = x;
-                            if (k == 0) {
-                                *reinterpret_cast<uint4 *>(sm.b[stage][0] + row * 128 + sw) = x;
-                                *reinterpret_cast<uint4 *>(sm.b[stage][1] + row * 128 + sw) = x;
-                            }
+                    if ((c > 0 || q > 0) && !(ok = wait_all(&sm.w_free[k], (q - 1) & 1, abort))) break;
+                    const int row = q * 32 + in;
+                    const float wt = g.d[row] * ex2_approx((end_hi - g.hi[row]) + (end_lo - g.lo[row]));
+                    uint4 x = *reinterpret_cast<const uint4 *>(xt + row * 128 + sw);
+                    if (row >= rows) {
+                        x = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(xt + row * 128 + sw) = x;
+                        if (k == 0) {
+                            *reinterpret_cast<uint4 *>(sm.b[stage][0] + row * 128 + sw) = x;
+                            *reinterpret_cast<uint4 *>(sm.b[stage][1] + row * 128 + sw) = x;
                         }
-                        uint32_t word[4] = {x.x, x.y, x.z, x.w};
-                        if (odd_bf16x2(word[0]) || odd_bf16x2(word[1]) || odd_bf16x2(word[2]) || odd_bf16x2(word[3])) {
-                            sm.any_bad[stage][k] = 1;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const uint32_t bits = (j & 1) ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
-                                if ((bits & 0x7f80u) != 0x7f80u) continue;
-                                atomicMin(&sm.first_bad[stage][k][piece * 8 + j], row);
-                                word[j / 2] &= (j & 1) ? 0xffffu : 0xffff0000u;
-                            }
-                            *reinterpret_cast<uint4 *>(xt + row * 128 + sw) = make_uint4(word[0], word[1], word[2], word[3]);
-                        }
-                        const f32x2 wt = same2(sm.weight[k][row]);
-                        uint32_t part[3][4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            split_bf16x3(mul2(pack2(bf16_lo(word[j]), bf16_hi(word[j])), wt), part[0][j], part[1][j], part[2][j]);
-#pragma unroll
-                        for (int i = 0; i < 3; ++i)
-                            *reinterpret_cast<uint4 *>(sm.w[k][i] + in * 128 + sw) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
                     }
+                    uint32_t word[4] = {x.x, x.y, x.z, x.w};
+                    if (odd_bf16x2(word[0]) || odd_bf16x2(word[1]) || odd_bf16x2(word[2]) || odd_bf16x2(word[3])) {
+                        sm.any_bad[k] = 1;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t bits = (j & 1) ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
+                            if ((bits & 0x7f80u) != 0x7f80u) continue;
+                            atomicMin(&sm.first_bad[k][piece * 8 + j], c * Q + row);
+                            word[j / 2] &= (j & 1) ? 0xffffu : 0xffff0000u;
+                        }
+                        *reinterpret_cast<uint4 *>(xt + row * 128 + sw) = make_uint4(word[0], word[1], word[2], word[3]);
+                    }
+                    const f32x2 wt2 = same2(wt);
+                    uint32_t part[3][4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        split_bf16x3(mul2(pack2(bf16_lo(word[j]), bf16_hi(word[j])), wt2), part[0][j], part[1][j], part[2][j]);
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        *reinterpret_cast<uint4 *>(sm.w[k][j] + in * 128 + sw) = make_uint4(part[j][0], part[j][1], part[j][2], part[j][3]);
                     fence_async_shared();
                     warp_arrive(&sm.w_full[k], lane);
                 }
-                if (!ok) break;
+            }
+            if (!ok) break;
+            if constexpr (FULL) {
                 warp_arrive(&sm.x_ok[stage][k], lane);
-                if (!(ok = mbar_wait_warp(&sm.sum_full[k], c & 1, abort))) break;
-                tc_fence_after();
-                const f32x2 g2 = same2(gamma);
-#pragma unroll
-                for (int i0 = 0; i0 < 64; i0 += 16) {
-                    float f[16];
-                    tmem_load(lanes + kColSum + k * 64 + i0, f);
-                    tmem_wait_load();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) st2[i0 / 2 + i] = fma2(g2, st2[i0 / 2 + i], pack2(f[2 * i], f[2 * i + 1]));
-                }
-                tc_fence_before();
-                whole *= gamma;
-                if (sm.any_bad[stage][k]) {  // all of the group's arrivals are before sum_full
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float f0, f1;
-                        unpack2(st2[i], f0, f1);
-                        if (sm.first_bad[stage][k][2 * i] < Q) f0 = NAN;
-                        if (sm.first_bad[stage][k][2 * i + 1] < Q) f1 = NAN;
-                        st2[i] = pack2(f0, f1);
-                    }
-                }
-            }
-            if (!FULL || (last && a.state != nullptr)) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float f[2];
-                    unpack2(st2[i], f[0], f[1]);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int ch = 2 * i + j;
-                        const float x = ok ? f[j] : NAN;
-                        if (!FULL) slot[ch * 128] = x;
-                        else if (ch < width && n < a.dim_state) pool[ch * a.s_stride_dim] = x;
-                    }
-                }
-                if (!FULL && n == 0) p.seg_decay[static_cast<int64_t>(unit) * a.num_heads * panels + v] = whole;
-            }
-        }
-    } else if constexpr (FULL) {
-        // M and the outputs of one head: thread i has token i.
-        const int k = warp >> 2, i = tid & 127, w = warp & 3;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
-        if (k < nh) {
-            const int h = group * rep + (v0 + k) / panels, panel = (v0 + k) % panels, width = min(64, a.head_dim - panel * 64);
-            const float skip = a.D != nullptr ? a.D[h] : 0.0f;
-            uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + panel * 64 * a.out.stride_dim;
-            const uint16_t *z = static_cast<const uint16_t *>(a.z.data) + h * a.z.stride_head + panel * 64 * a.z.stride_dim;
-            // The columns of tokens after a warp's own are zero in both halves, and nothing writes them again.
-            const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            if (k == 0)
-                for (int blk = w + 1; blk < 4; ++blk)
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) tmem_store(lanes + kColM + (blk >> 1) * 64 + part * 32 + (blk & 1) * 16 + j * 8, none);
-            tmem_wait_store();
-            int c = 0;
-            for (; c < chunks; ++c) {
-                const int stage = c & 1, u = c * nh + k, rows = min(Q, e - s - c * Q);
-                if (!mbar_wait_warp(&sm.gates_full[stage], (c / 2) & 1, abort)) break;
-                const Gates &g = sm.gates[stage][k];
-                const float ghi = g.hi[i], glo = g.lo[i];
-                const float base_hi = w > 0 ? g.hi[w * 32 - 1] : 0.0f, base_lo = w > 0 ? g.lo[w * 32 - 1] : 0.0f;
-                const float own = (ghi - base_hi) + (glo - base_lo);  // since the warp's first token
-                const float here = ex2_approx(own), row_decay = ex2_approx(ghi + glo);
-                float *before = sm.factor[k] + 16 * w * (w - 1);
-#pragma unroll
-                for (int b = 0; b < 3; ++b)
-                    if (b < w) {
-                        const int j = b * 32 + lane;
-                        before[j] = g.d[j] * ex2_approx((base_hi - g.hi[j]) + (base_lo - g.lo[j]));
-                    }
-                const float own_d = g.d[i];
-                warp_arrive(&sm.gates_free[stage], lane);
-                bool ok = mbar_wait_warp(&sm.cb_full, c & 1, abort);
-                if (!ok) break;
+                if (!(ok = wait_all(&sm.cb_full, c & 1, abort))) break;
+                if (u >= 1 && !(ok = wait_all(&sm.m_free[hf], (u - 1) & 1, abort))) break;
                 tc_fence_after();
                 const f32x2 here2 = same2(here);
 #pragma unroll
-                for (int blk = 0; blk < 4; ++blk) {
-                    if ((blk & 1) == 0 && u >= 1 && !(ok = mbar_wait_warp(&sm.m_free[blk >> 1], (u - 1) & 1, abort))) break;
+                for (int b = 0; b < 2; ++b) {
+                    const int blk = 2 * hf + b;
                     if (blk <= w) {
 #pragma unroll
                         for (int j0 = 0; j0 < 32; j0 += 16) {
                             float f[16];
-                            tmem_load(lanes + kColCB + blk * 32 + j0, f);
+                            tmem_load(col_cb + b * 32 + j0, f);
                             tmem_wait_load();
                             uint32_t hi[8], mid[8];
                             if (blk < w) {
@@ -579,48 +535,74 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                                 }
                             } else {
 #pragma unroll
-                                for (int j = 0; j < 16; j += 2) {
-                                    float m[2];
+                                for (int j = 0; j < 16; j += 4) {
+                                    const float4 gj = *reinterpret_cast<const float4 *>(&sm.since[k][w * 32 + j0 + j]);
+                                    const ulonglong2 dj = *reinterpret_cast<const ulonglong2 *>(&g.d[w * 32 + j0 + j]);
+                                    const float at[4] = {gj.x, gj.y, gj.z, gj.w};
+                                    float m[4];
 #pragma unroll
-                                    for (int l = 0; l < 2; ++l) {
-                                        const int t = j0 + j + l;
-                                        const float gj = __shfl_sync(kFullMask, own, t), dj = __shfl_sync(kFullMask, own_d, t);
-                                        m[l] = t <= lane ? f[j + l] * (dj * ex2_approx(own - gj)) : 0.0f;
-                                    }
+                                    for (int l = 0; l < 4; ++l) m[l] = ex2_approx(own - at[l]);
+                                    unpack2(mul2(mul2(pack2(m[0], m[1]), dj.x), pack2(f[j], f[j + 1])), m[0], m[1]);
+                                    unpack2(mul2(mul2(pack2(m[2], m[3]), dj.y), pack2(f[j + 2], f[j + 3])), m[2], m[3]);
+#pragma unroll
+                                    for (int l = 0; l < 4; ++l) m[l] = j0 + j + l <= lane ? m[l] : 0.0f;
                                     split_bf16x2(pack2(m[0], m[1]), hi[j / 2], mid[j / 2]);
+                                    split_bf16x2(pack2(m[2], m[3]), hi[j / 2 + 1], mid[j / 2 + 1]);
                                 }
                             }
-                            const uint32_t to = lanes + kColM + (blk >> 1) * 64 + (blk & 1) * 16 + j0 / 2;
-                            tmem_store(to, hi);
-                            tmem_store(to + 32, mid);
+                            tmem_store(col_m + b * 16 + j0 / 2, hi);
+                            tmem_store(col_m + 32 + b * 16 + j0 / 2, mid);
                         }
                     }
-                    if (blk & 1) {
-                        tmem_wait_store();
-                        tc_fence_before();
-                        warp_arrive(&sm.m_full[blk >> 1], lane);
-                    }
                 }
-                if (!ok) break;
+                tmem_wait_store();
+                tc_fence_before();
+                warp_arrive(&sm.m_full[hf], lane);
                 warp_arrive(&sm.cb_free, lane);
+            }
+            warp_arrive(&sm.gates_free[stage], lane);
 
-                // out_i = e^{G_i} (C S)_i + (M x)_i + D x_i, with the gate
-                if (!mbar_wait_warp(&sm.xb_full[stage], (c / 2) & 1, abort) || !mbar_wait_warp(&sm.cs_full[k], c & 1, abort) ||
-                    !mbar_wait_warp(&sm.mx_full[k], c & 1, abort))
-                    break;
+            // S <- e^{G_Q} S + the chunk's sum
+            if (!(ok = wait_all(&sm.sum_full[k], c & 1, abort))) break;
+            tc_fence_after();
+            const f32x2 g2 = same2(gamma);
+#pragma unroll
+            for (int j0 = 0; j0 < 32; j0 += 16) {
+                float f[16];
+                tmem_load(col_sum + j0, f);
+                tmem_wait_load();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) st2[j0 / 2 + j] = fma2(g2, st2[j0 / 2 + j], pack2(f[2 * j], f[2 * j + 1]));
+            }
+            tc_fence_before();
+            whole *= gamma;
+            const bool bad = sm.any_bad[k] != 0;  // what this chunk has is noted before sum_full
+            if (bad) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float f[2];
+                    unpack2(st2[j], f[0], f[1]);
+#pragma unroll
+                    for (int l = 0; l < 2; ++l) f[l] = sm.first_bad[k][hf * 32 + 2 * j + l] < (c + 1) * Q ? NAN : f[l];
+                    st2[j] = pack2(f[0], f[1]);
+                }
+            }
+
+            // out_i = e^{G_i} (C S)_i + (M x)_i + D x_i, with the gate
+            if constexpr (FULL) {
+                if (!(ok = wait_all(&sm.cs_full[k], c & 1, abort)) || !(ok = wait_all(&sm.mx_full[k], c & 1, abort))) break;
                 tc_fence_after();
-                const uint8_t *xt = sm.x[stage][k] + i * 128;
-                const bool bad = sm.any_bad[stage][k] != 0;
+                const bool fast = vec_out && !bad;
                 const int64_t t = s + c * Q + i;
                 const f32x2 decay2 = same2(row_decay), skip2 = same2(skip);
 #pragma unroll
-                for (int j0 = 0; j0 < 64; j0 += 16) {
+                for (int j0 = 0; j0 < 32; j0 += 16) {
                     float mx[16], cs[16];
                     __syncwarp();
-                    tmem_load(lanes + kColMX + j0, mx);
-                    tmem_load(lanes + kColCS + j0, cs);
+                    tmem_load(col_mx + j0, mx);
+                    tmem_load(col_cs + j0, cs);
                     tmem_wait_load();
-                    if (j0 == 48) {
+                    if (j0 == 16) {
                         tc_fence_before();
                         warp_arrive(&sm.mx_free, lane);
                         warp_arrive(&sm.cs_free, lane);
@@ -628,8 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int ch = j0 + half * 8;
-                        const uint4 x = *reinterpret_cast<const uint4 *>(xt + (((ch >> 3) ^ (i & 7)) << 4));
-                        const uint32_t word[4] = {x.x, x.y, x.z, x.w};
+                        uint4 *x = reinterpret_cast<uint4 *>(xt + i * 128 + (((hf * 4 + (ch >> 3)) ^ (i & 7)) << 4));
+                        const uint32_t word[4] = {x->x, x->y, x->z, x->w};
                         f32x2 y[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -637,44 +619,54 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                             y[j] = fma2(decay2, pack2(cs[at], cs[at + 1]), pack2(mx[at], mx[at + 1]));
                             y[j] = fma2(skip2, pack2(bf16_lo(word[j]), bf16_hi(word[j])), y[j]);
                         }
-                        if (bad) {
+                        if constexpr (GATED) {
+                            if (i < rows && ch < width) {
+                                if (vec_out) {
+                                    const uint4 zz = __ldg(reinterpret_cast<const uint4 *>(z + t * a.z.stride_tok + ch));
+                                    const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                float f0, f1;
-                                unpack2(y[j], f0, f1);
-                                if (sm.first_bad[stage][k][ch + 2 * j] <= i) f0 = NAN;
-                                if (sm.first_bad[stage][k][ch + 2 * j + 1] <= i) f1 = NAN;
-                                y[j] = pack2(f0, f1);
+                                    for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], silu2(pack2(bf16_lo(zw[j]), bf16_hi(zw[j]))));
+                                } else {
+                                    const auto at = [&](int j) { return ch + j < width ? bf16_bits(z[t * a.z.stride_tok + (ch + j) * a.z.stride_dim]) : 0.0f; };
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], silu2(pack2(at(2 * j), at(2 * j + 1))));
+                                }
                             }
                         }
-                        if (i >= rows || ch >= width) {
-                        } else if (vec_out) {
-                            if (a.z.data != nullptr) {
-                                const uint4 zz = __ldg(reinterpret_cast<const uint4 *>(z + t * a.z.stride_tok + ch));
-                                const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], silu2(pack2(bf16_lo(zw[j]), bf16_hi(zw[j]))));
-                            }
-                            *reinterpret_cast<uint4 *>(out + t * a.out.stride_tok + ch) =
-                                make_uint4(f32x2_to_bf16x2(y[0]), f32x2_to_bf16x2(y[1]), f32x2_to_bf16x2(y[2]), f32x2_to_bf16x2(y[3]));
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                if (ch + j >= width) continue;
-                                float f0, f1;
-                                unpack2(y[j / 2], f0, f1);
-                                float f = (j & 1) ? f1 : f0;
-                                if (a.z.data != nullptr) f *= silu(bf16_bits(z[t * a.z.stride_tok + (ch + j) * a.z.stride_dim]));
-                                out[t * a.out.stride_tok + (ch + j) * a.out.stride_dim] = round_bf16(f);
-                            }
-                        }
+                        const uint4 packed = make_uint4(f32x2_to_bf16x2(y[0]), f32x2_to_bf16x2(y[1]), f32x2_to_bf16x2(y[2]), f32x2_to_bf16x2(y[3]));
+                        if (!fast) *x = packed;  // the thread's own values, which nothing reads any more
+                        else if (i < rows && ch < width) *reinterpret_cast<uint4 *>(out + t * a.out.stride_tok + ch) = packed;
                     }
+                }
+                if (!fast) {
+#pragma unroll 1
+                    for (int ch = 0; i < rows && ch < width; ++ch) {
+                        uint16_t f = *reinterpret_cast<const uint16_t *>(xt + i * 128 + (((hf * 4 + (ch >> 3)) ^ (i & 7)) << 4) + (ch & 7) * 2);
+                        if (bad && sm.first_bad[k][hf * 32 + ch] <= c * Q + i) f = 0x7fffu;
+                        out[t * a.out.stride_tok + ch * a.out.stride_dim] = f;
+                    }
+                    fence_async_shared();
                 }
                 warp_arrive(&sm.xb_free[stage], lane);
             }
-            for (; c < chunks; ++c)  // gave up
+        }
+        if (FULL && !ok)  // gave up
+            for (; c < chunks; ++c)
                 if (s + c * Q + i < e)
                     for (int ch = 0; ch < width; ++ch) out[(s + c * Q + i) * a.out.stride_tok + ch * a.out.stride_dim] = 0x7fffu;
+        if (!FULL || (last && a.state != nullptr)) {
+            float *to = FULL ? pool : slot;
+            const int64_t step = FULL ? a.s_stride_dim : 128;
+            const int count = !FULL ? 32 : i < a.dim_state ? width : 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float f[2];
+                unpack2(st2[j], f[0], f[1]);
+#pragma unroll
+                for (int l = 0; l < 2; ++l)
+                    if (2 * j + l < count) to[(2 * j + l) * step] = ok ? f[l] : NAN;
+            }
+            if (!FULL && i == 0 && hf == 0) p.seg_decay[static_cast<int64_t>(unit) * a.num_heads * panels + v] = whole;
         }
     }
     tc_fence_before();
@@ -722,30 +714,30 @@ int64_t segment_slots(int total_tokens, int batch, int seg_chunks) {
     return static_cast<int64_t>(total_tokens) / (static_cast<int64_t>(seg_chunks) * Q) + batch;
 }
 
-template <bool FULL, int NP>
+template <bool FULL, int NP, bool GATED>
 int launch_chunks(const SsmFwd &p, const Maps &maps, int64_t units, int vec_out, cudaStream_t stream) {
     int dev = 0;
     current_device_sms(&dev);
     cudaError_t err;
-    if (resident_blocks<ssm_chunk_kernel<FULL, NP>>(kThreads, kSmemBytes, dev, &err) == 0) return static_cast<int>(err);
+    if (resident_blocks<ssm_chunk_kernel<FULL, NP, GATED>>(kThreads, kSmemBytes, dev, &err) == 0) return static_cast<int>(err);
     const int panels = (p.a.head_dim + 63) / 64, rep = p.a.num_heads / p.a.num_groups;
     const int64_t blocks = units * p.a.num_groups * ((static_cast<int64_t>(rep) * panels + 1) / 2);
     if (blocks > 0x7fffffff) return CCV_ERR_SIZE;
-    return launch_pdl(ssm_chunk_kernel<FULL, NP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kSmemBytes, stream, p, maps, vec_out);
+    return launch_pdl(ssm_chunk_kernel<FULL, NP, GATED>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kSmemBytes, stream, p, maps, vec_out);
 }
 
-template <int NP>
+template <int NP, bool GATED>
 int launch_all(const SsmFwd &p, const Maps &maps, int vec_out, cudaStream_t stream) {
-    if (p.seg_chunks == 0) return launch_chunks<true, NP>(p, maps, p.batch, vec_out, stream);
+    if (p.seg_chunks == 0) return launch_chunks<true, NP, GATED>(p, maps, p.batch, vec_out, stream);
     const int64_t units = segment_slots(p.total_tokens, p.batch, p.seg_chunks);
-    int status = launch_chunks<false, NP>(p, maps, units, vec_out, stream);
+    int status = launch_chunks<false, 2, false>(p, maps, units, vec_out, stream);
     if (status != CCV_OK) return status;
     const int panels = (p.a.head_dim + 63) / 64;
     const int64_t joins = static_cast<int64_t>(p.batch) * p.a.num_heads * panels * (kStateFloats / 1024);
     if (joins > 0x7fffffff) return CCV_ERR_SIZE;
     status = launch_pdl(ssm_join_kernel, dim3(static_cast<unsigned>(joins)), dim3(256), 0, stream, p, panels);
     if (status != CCV_OK) return status;
-    return launch_chunks<true, NP>(p, maps, units, vec_out, stream);
+    return launch_chunks<true, NP, GATED>(p, maps, units, vec_out, stream);
 }
 
 }  // namespace
@@ -799,7 +791,9 @@ int ssm_launch_chunked(const SsmFwd &call, void *workspace, cudaStream_t stream)
         return aligned16(v.data) && v.stride_dim == 1 && v.stride_tok % 8 == 0 && v.stride_head % 8 == 0;
     };
     const int vec_out = a.head_dim % 8 == 0 && rows(a.out) && (a.z.data == nullptr || rows(a.z));
-    return a.dim_state <= 64 ? launch_all<1>(p, maps, vec_out, stream) : launch_all<2>(p, maps, vec_out, stream);
+    if (a.z.data != nullptr)
+        return a.dim_state <= 64 ? launch_all<1, true>(p, maps, vec_out, stream) : launch_all<2, true>(p, maps, vec_out, stream);
+    return a.dim_state <= 64 ? launch_all<1, false>(p, maps, vec_out, stream) : launch_all<2, false>(p, maps, vec_out, stream);
 }
 
 }  // namespace ccv
