@@ -53,16 +53,17 @@ bool mapped(const ccv_heads_view &v, int heads) {
 
 // -------------------------------------------------------------------- form ----
 
-enum Form { kRecurrent, kChunked };
+enum Form { kRecurrent, kChunked, kScan };
 
-// CCV_SSM_PATH=recurrent or =chunked, read at each call, forces a form where it can run (for testing and tuning).
+// CCV_SSM_PATH=recurrent, =chunked or =scan, read at each call, forces a form where it can run (for testing and tuning).
 Form choose(int total_tokens, int batch, int head_dim, int dim_state, int a_per_state) {
     const char *path = std::getenv("CCV_SSM_PATH");
+    const bool chunks = ssm_chunked_dims(dim_state, a_per_state);
     if (path != nullptr && std::strcmp(path, "recurrent") == 0) return kRecurrent;
-    if (ssm_chunked_dims(dim_state, a_per_state) &&
-        ((path != nullptr && std::strcmp(path, "chunked") == 0) || (head_dim >= 16 && total_tokens > static_cast<int64_t>(8) * batch)))
-        return kChunked;
-    return kRecurrent;
+    if (path != nullptr && std::strcmp(path, "scan") == 0) return kScan;
+    if (path != nullptr && std::strcmp(path, "chunked") == 0 && chunks) return kChunked;
+    if (total_tokens <= static_cast<int64_t>(8) * batch) return kRecurrent;
+    return chunks && head_dim >= 16 ? kChunked : kScan;
 }
 
 }  // namespace
@@ -74,7 +75,11 @@ extern "C" int64_t ssm_fwd_workspace(int total_tokens, int batch, int num_heads,
     if (total_tokens <= 0 || total_tokens > (1 << 30) || batch <= 0 || num_heads <= 0 || num_groups <= 0 || num_heads % num_groups != 0 ||
         head_dim <= 0 || head_dim > kSsmMaxDim || dim_state <= 0 || dim_state > kSsmMaxStates)
         return 0;
-    if (choose(total_tokens, batch, head_dim, dim_state, a_per_state) != kChunked) return 0;
+    const Form form = choose(total_tokens, batch, head_dim, dim_state, a_per_state);
+    if (form == kRecurrent) return 0;
+    if (form == kScan)
+        return ssm_scan_workspace(total_tokens, batch, num_heads, head_dim, dim_state,
+                                  ssm_scan_segments(total_tokens, batch, num_heads, num_groups, head_dim, dim_state));
     int64_t bytes = ssm_chunked_workspace(total_tokens, batch, num_heads, head_dim,
                                           ssm_chunked_segments(total_tokens, batch, num_heads, num_groups, head_dim));
     if (copies) bytes += copy_bytes(total_tokens, num_heads, head_dim) + 2 * copy_bytes(total_tokens, num_groups, dim_state);
@@ -96,12 +101,16 @@ extern "C" int ssm_fwd(const ccv_ssm_args *args, const int32_t *query_start_loc,
     const int64_t need = ssm_fwd_workspace(total_tokens, batch, a.num_heads, a.num_groups, a.head_dim, a.dim_state, a.a_per_state, copies);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 127u) != 0))
         return CCV_ERR_WORKSPACE;
-    if (choose(total_tokens, batch, a.head_dim, a.dim_state, a.a_per_state) != kChunked) {
+    const Form form = choose(total_tokens, batch, a.head_dim, a.dim_state, a.a_per_state);
+    if (form == kRecurrent) {
         const SsmRows rows{query_start_loc, cache_indices, has_initial_state, nullptr, nullptr, 0, 0, 0, batch, 0, total_tokens, err_count};
         return ssm_launch_recurrent(a, rows, stream);
     }
     SsmFwd p{a, query_start_loc, cache_indices, has_initial_state, batch, total_tokens, err_count,
-             ssm_chunked_segments(total_tokens, batch, a.num_heads, a.num_groups, a.head_dim), nullptr, nullptr};
+             form == kScan ? ssm_scan_segments(total_tokens, batch, a.num_heads, a.num_groups, a.head_dim, a.dim_state)
+                           : ssm_chunked_segments(total_tokens, batch, a.num_heads, a.num_groups, a.head_dim),
+             nullptr, nullptr};
+    if (form == kScan) return ssm_launch_scan(p, workspace, stream);
     if (copies) {
         uint8_t *to = static_cast<uint8_t *>(workspace) + ssm_chunked_workspace(total_tokens, batch, a.num_heads, a.head_dim, p.seg_chunks);
         if ((status = copy_view(p.a.x, to, total_tokens, a.num_heads, a.head_dim, stream)) != CCV_OK) return status;
