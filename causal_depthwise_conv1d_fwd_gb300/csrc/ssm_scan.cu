@@ -11,8 +11,9 @@
 //
 // What bounds it is the exponential: 16 lanes of one a cycle and SM, 465 us for 4 x 4096 tokens of 8192 channels with 16 states,
 // where the copies take 160.
+#include <algorithm>
+#include <cmath>
 #include <cstdlib>
-#include <cstring>
 
 #include "ccv_varlen.cuh"
 #include "ssm_fwd.cuh"
@@ -20,29 +21,33 @@
 namespace ccv {
 namespace {
 
-constexpr int kThreads = 128;
 constexpr int kUnit = 128;    // tokens of a segment's unit
 
-// log(1 + e^x) = max(x, 0) + log1p(e^{-|x|}), the latter as t times a polynomial in t = e^{-|x|} (least largest relative error on
-// [0, 1], 3e-8; with its own rounding 2.3e-7).  A step's relative error is what counts, however small the step is.
-__device__ __forceinline__ float softplus_fast(float x) {
-    const float t = ex2_approx(-1.4426950408889634f * fabsf(x));
-    float q = 0.005232623778283596f;
-    q = fmaf(q, t, -0.029504956677556038f);
-    q = fmaf(q, t, 0.07822549343109131f);
-    q = fmaf(q, t, -0.1366320699453354f);
-    q = fmaf(q, t, 0.1910598874092102f);
-    q = fmaf(q, t, -0.2484297752380371f);
-    q = fmaf(q, t, 0.3331909477710724f);
-    q = fmaf(q, t, -0.4999949336051941f);
-    q = fmaf(q, t, 0.9999999403953552f);
-    return fmaf(q, t, fmaxf(x, 0.0f));
+// log(1 + e^x) = max(x, 0) + log1p(e^{-|x|}) of a pair, the latter as t times a polynomial in t = e^{-|x|} (least largest relative
+// error on [0, 1], 3e-8; with its own rounding 2.3e-7).  A step's relative error is what counts, however small the step is.
+__device__ __forceinline__ f32x2 softplus2(f32x2 x) {
+    float x0, x1;
+    unpack2(x, x0, x1);
+    const f32x2 t = pack2(ex2_approx(-1.4426950408889634f * fabsf(x0)), ex2_approx(-1.4426950408889634f * fabsf(x1)));
+    const auto both = [](float c) { return pack2(c, c); };
+    f32x2 q = fma2(both(0.005232623778283596f), t, both(-0.029504956677556038f));
+    q = fma2(q, t, both(0.07822549343109131f));
+    q = fma2(q, t, both(-0.1366320699453354f));
+    q = fma2(q, t, both(0.1910598874092102f));
+    q = fma2(q, t, both(-0.2484297752380371f));
+    q = fma2(q, t, both(0.3331909477710724f));
+    q = fma2(q, t, both(-0.4999949336051941f));
+    q = fma2(q, t, both(0.9999999403953552f));
+    return fma2(q, t, pack2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
 }
 
-template <int LANES, int NS>
+template <int LANES, int NS, int R, int ROWS, int TOKENS>
 struct ScanSmem {
-    static constexpr int rows = kThreads / LANES, states = LANES * NS, T = states > 128 ? 16 : 32;
-    float2 step[T][rows];        // d, d x
+    static constexpr int rows = ROWS, states = LANES * NS, T = TOKENS, threads = LANES * ROWS / R;
+    float2 step[T][rows];        // d, d x; two rows' pairs (16 bytes) are at place_of(row / 2)
+    // A thread writes eight rows of a token, so the eight threads of a token write 64 bytes apart: the places' low bits spread
+    // them over the banks, and leave the rows of a warp's loads side by side.
+    static __device__ __forceinline__ int place_of(int pair) { return pair ^ ((pair >> 3) & (rows / 16 - 1)); }
     float b[T][states], c[T][states];
     uint16_t x[T][rows], z[T][rows];  // outputs take the place of x
     int seq, start, end;
@@ -72,15 +77,17 @@ __device__ __forceinline__ uint4 load8(const ccv_heads_view &v, int64_t tok, int
 
 // FULL: outputs and the sequences' final states; otherwise segments' own states and the sums of their steps, for the join.
 // LANES x NS: dim_state rounded up.  PER: A has a value a state.
-template <int LANES, int NS, bool PER, bool FULL>
-__global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const __grid_constant__ SsmFwd p, const __grid_constant__ ScanVec vec) {
-    using S = ScanSmem<LANES, NS>;
-    constexpr int T = S::T, kRows = S::rows, kPieces = kRows / 8, kLoads = T * kPieces / kThreads > 0 ? T * kPieces / kThreads : 1;
-    constexpr int kQuads = T * S::states / 4 / kThreads;  // groups of 4 states that a thread brings
-    static_assert(kPieces >= 1 && kQuads >= 1 && T % LANES == 0, "");
+template <int LANES, int NS, int R, int ROWS, int TOKENS, bool PER, bool FULL>
+__global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan_kernel(const __grid_constant__ SsmFwd p, const __grid_constant__ ScanVec vec) {
+    using S = ScanSmem<LANES, NS, R, ROWS, TOKENS>;
+    constexpr int T = S::T, kRows = S::rows, kThreads = S::threads, kPieces = kRows / 8;
+    constexpr int kLoads = (T * kPieces + kThreads - 1) / kThreads;              // groups of 8 rows that a thread brings
+    constexpr int kAllQuads = T * S::states / 4, kQuads = (kAllQuads + kThreads - 1) / kThreads;  // and of 4 states
+    static_assert(kPieces >= 1 && kThreads % kPieces == 0 && T % LANES == 0 && LANES % R == 0 && ROWS % R == 0, "");
     __shared__ S sm;
     const ccv_ssm_args &a = p.a;
-    const int tid = threadIdx.x, lane = tid % LANES, row = tid / LANES;
+    const int tid = threadIdx.x, lane = tid % 32 / (32 / LANES);
+    const int row = (tid / 32 * (32 / LANES) + tid % (32 / LANES)) * R;  // the first of the lane's rows
     const int rep = a.num_heads / a.num_groups, group_rows = rep * a.head_dim;
     const int per_group = (group_rows + kRows - 1) / kRows, blocks = a.num_groups * per_group;
     const int unit = blockIdx.x / blocks, rest = blockIdx.x % blocks;
@@ -132,34 +139,38 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const __grid_constan
         if (!last) e = s + unit_tokens;
     }
 
-    // The thread's row of the state: states j * 4 LANES + 4 lane + i.
-    const int r = r0 + row;
-    const bool real = r < group_rows;
-    const int h = head0 + (real ? r / a.head_dim : 0), ch = real ? r % a.head_dim : 0;
+    // The lane's R rows of the state: states j * 4 LANES + 4 lane + i.
     const int all_rows = a.num_heads * a.head_dim;
-    float *pool = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + ch * a.s_stride_dim : nullptr;
-    float *slot = p.seg_chunks > 0 ? p.seg_state + (static_cast<int64_t>(unit) * all_rows + head0 * a.head_dim + (real ? r : 0)) * S::states : nullptr;
-    f32x2 st[NS / 2], decay[PER ? NS / 2 : 1];
-    {
-        const bool kept = FULL && segments > 1, init = a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
-        const float *from = kept ? slot : pool;
+    const auto pool_at = [&](int r) {
+        const int h = r / a.head_dim;
+        return a.state + line * a.s_stride_line + (head0 + h) * a.s_stride_head + (r - h * a.head_dim) * a.s_stride_dim;
+    };
+    const auto slot_at = [&](int r) { return p.seg_state + (static_cast<int64_t>(unit) * all_rows + head0 * a.head_dim + r) * S::states; };
+    f32x2 st[R][NS / 2], decay[R][PER ? NS / 2 : 1];
+    const bool kept = FULL && segments > 1, init = FULL && a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int r = r0 + row + q;
+        const bool real = r < group_rows, some = real && (kept || init);
+        const float *from = !some ? a.A : kept ? slot_at(r) : pool_at(r);
         const int64_t step = kept ? 1 : a.s_stride_state;
-        const bool some = FULL && real && (kept || init);
-        const float *rates = a.A + static_cast<int64_t>(h) * (PER ? a.dim_state : 1);
+        const float *rates = a.A + static_cast<int64_t>(head0 + (real ? r / a.head_dim : 0)) * (PER ? a.dim_state : 1);
         constexpr float kLog2e = 1.4426950408889634f;
 #pragma unroll
         for (int j = 0; j < NS; j += 2) {
             const int n = (j / 4) * 4 * LANES + lane * 4 + (j & 3);
-            st[j / 2] = pack2(some && n < a.dim_state ? from[n * step] : 0.0f, some && n + 1 < a.dim_state ? from[(n + 1) * step] : 0.0f);
-            if (PER) decay[j / 2] = pack2(n < a.dim_state ? rates[n] * kLog2e : 0.0f, n + 1 < a.dim_state ? rates[n + 1] * kLog2e : 0.0f);
+            st[q][j / 2] = pack2(some && n < a.dim_state ? from[n * step] : 0.0f, some && n + 1 < a.dim_state ? from[(n + 1) * step] : 0.0f);
+            if (PER) decay[q][j / 2] = pack2(n < a.dim_state ? rates[n] * kLog2e : 0.0f, n + 1 < a.dim_state ? rates[n + 1] * kLog2e : 0.0f);
         }
-        if (!PER) decay[0] = pack2(rates[0] * kLog2e, rates[0] * kLog2e);
+        if (!PER) decay[q][0] = pack2(rates[0] * kLog2e, rates[0] * kLog2e);
     }
-    const float skip = FULL && a.D != nullptr ? a.D[h] : 0.0f;
+    // The row whose outputs the lane ends with, of every LANES / R-th token.
+    const int out_row = row + lane % R, out_tok = lane / R;
+    const float skip = FULL && a.D != nullptr && r0 + out_row < group_rows ? a.D[head0 + (r0 + out_row) / a.head_dim] : 0.0f;
 
     // The next tile's inputs: token tid / kPieces (+ ..), 8 rows.
     const int piece = tid % kPieces, tok = tid / kPieces, at = r0 + piece * 8;
-    const bool loads = tok < T;
+    const auto loads = [&](int l) { return tok + l * (kThreads / kPieces) < T; };
     constexpr int kStep = kThreads / kPieces;  // tokens between a thread's loads
     uint4 xr[kLoads], zr[kLoads], dr[kLoads][2];
     constexpr bool kAhead = kQuads <= 4;
@@ -176,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const __grid_constan
 #pragma unroll
         for (int l = 0; l < kLoads; ++l) {
             const int64_t t = t0 + tok + l * kStep;
-            const bool in = loads && t < e;
+            const bool in = loads(l) && t < e;
             xr[l] = zr[l] = dr[l][0] = dr[l][1] = make_uint4(0u, 0u, 0u, 0u);
             if (!in) continue;
             xr[l] = load8(a.x, t, head0, a.head_dim, at, group_rows, vec.x);
@@ -212,16 +223,27 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const __grid_constan
             for (int i = 0; i < kQuads; ++i) {
                 const int quad = tid + i * kThreads, n = quad % (S::states / 4) * 4;
                 const int64_t t = t0 + quad / (S::states / 4);
-                br[i] = t < e ? load_quad(a.B, t, n) : make_uint2(0u, 0u);
-                if (FULL) cr[i] = t < e ? load_quad(a.C, t, n) : make_uint2(0u, 0u);
+                const bool in = t < e && (kAllQuads % kThreads == 0 || quad < kAllQuads);
+                br[i] = in ? load_quad(a.B, t, n) : make_uint2(0u, 0u);
+                if (FULL) cr[i] = in ? load_quad(a.C, t, n) : make_uint2(0u, 0u);
             }
         }
     };
-    float bias[8];
+    f32x2 bias[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) bias[i] = a.dt_bias != nullptr && at + i < group_rows ? a.dt_bias[head0 + (at + i) / a.head_dim] : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        const auto of = [&](int r) { return a.dt_bias != nullptr && r < group_rows ? a.dt_bias[head0 + r / a.head_dim] : 0.0f; };
+        bias[i] = pack2(of(at + 2 * i), of(at + 2 * i + 1));
+    }
+    const bool limits = a.dt_max < INFINITY || !(a.dt_min <= (a.dt_softplus ? 0.0f : -INFINITY));
     auto widen = [](uint2 w) { return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)); };
-    float sum_d = 0.0f;  // of the row's steps
+    float sum_d[R];  // of the rows' steps
+    int row_at[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        sum_d[q] = 0.0f;
+        row_at[q] = 2 * S::place_of((row + q) / 2) + ((row + q) & 1);
+    }
 
     fetch(s);
     for (int t0 = s; t0 < e; t0 += T) {
@@ -230,17 +252,26 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const __grid_constan
 #pragma unroll
         for (int l = 0; l < kLoads; ++l) {
             const int t = tok + l * kStep;
-            if (!loads) continue;
+            if (!loads(l)) continue;
             const uint32_t xw[4] = {xr[l].x, xr[l].y, xr[l].z, xr[l].w};
             const uint32_t d0[4] = {dr[l][0].x, dr[l][0].y, dr[l][0].z, dr[l][0].w}, d1[4] = {dr[l][1].x, dr[l][1].y, dr[l][1].z, dr[l][1].w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float d = a.dt_fp32 ? __uint_as_float(i < 4 ? d0[i & 3] : d1[i & 3]) : (i & 1) ? bf16_hi(d0[i / 2]) : bf16_lo(d0[i / 2]);
-                d += bias[i];
-                if (a.dt_softplus) d = softplus_fast(d);
-                d = d < a.dt_min ? a.dt_min : d > a.dt_max ? a.dt_max : d;
-                const float x = (i & 1) ? bf16_hi(xw[i / 2]) : bf16_lo(xw[i / 2]);
-                sm.step[t][piece * 8 + i] = t < n ? make_float2(d, d * x) : make_float2(0.0f, 0.0f);
+            for (int i = 0; i < 4; ++i) {
+                f32x2 d = a.dt_fp32 ? pack2(__uint_as_float(i < 2 ? d0[2 * (i & 1)] : d1[2 * (i & 1)]),
+                                            __uint_as_float(i < 2 ? d0[2 * (i & 1) + 1] : d1[2 * (i & 1) + 1]))
+                                    : pack2(bf16_lo(d0[i]), bf16_hi(d0[i]));
+                d = add2(d, bias[i]);
+                if (a.dt_softplus) d = softplus2(d);
+                float f0, f1, g0, g1;
+                unpack2(d, f0, f1);
+                if (limits) {
+                    f0 = f0 < a.dt_min ? a.dt_min : f0 > a.dt_max ? a.dt_max : f0;
+                    f1 = f1 < a.dt_min ? a.dt_min : f1 > a.dt_max ? a.dt_max : f1;
+                    d = pack2(f0, f1);
+                }
+                unpack2(mul2(d, pack2(bf16_lo(xw[i]), bf16_hi(xw[i]))), g0, g1);
+                *reinterpret_cast<float4 *>(&sm.step[t][2 * S::place_of(piece * 4 + i)]) =
+                    t < n ? make_float4(f0, g0, f1, g1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
             if (FULL) {
                 *reinterpret_cast<uint4 *>(&sm.x[t][piece * 8]) = xr[l];
@@ -250,6 +281,7 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
             const int quad = tid + i * kThreads, at_n = quad % (S::states / 4) * 4, t = quad / (S::states / 4);
+            if (kAllQuads % kThreads != 0 && quad >= kAllQuads) continue;
             uint2 bw = make_uint2(0u, 0u), cw = bw;
             if constexpr (kAhead) {
                 bw = br[i];
@@ -264,56 +296,93 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const __grid_constan
         __syncthreads();
         if (t0 + T < e) fetch(t0 + T);
 
-#pragma unroll 1
-        for (int g = 0; g < n; g += LANES) {
+        // Sums first and outputs after them: a store to shared memory would keep the next tokens' loads behind it.
+        constexpr int kTogether = LANES / R;  // tokens whose sums are taken together
+        float sums[T / kTogether];
+#pragma unroll
+        for (int g = 0; g < T; g += kTogether) {
             float y[LANES];
 #pragma unroll
-            for (int l = 0; l < LANES; ++l) {
-                const float2 step = sm.step[g + l][row];
-                const f32x2 d2 = pack2(step.x, step.x), dx2 = pack2(step.y, step.y);
-                f32x2 acc = 0ull, same = 0ull;
-                if constexpr (!PER) {
-                    const float a1 = ex2_approx(step.x * __uint_as_float(static_cast<uint32_t>(decay[0])));
-                    same = pack2(a1, a1);
+            for (int l = 0; l < kTogether; ++l) {
+                f32x2 d2[R], dx2[R], acc[R], same[R];
+                if constexpr (R % 2 == 0) {
+#pragma unroll
+                    for (int q = 0; q < R; q += 2) {
+                        const float4 step = *reinterpret_cast<const float4 *>(&sm.step[g + l][row_at[q]]);
+                        d2[q] = pack2(step.x, step.x);
+                        dx2[q] = pack2(step.y, step.y);
+                        d2[q + 1] = pack2(step.z, step.z);
+                        dx2[q + 1] = pack2(step.w, step.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < R; ++q) {
+                        const float2 step = sm.step[g + l][row_at[q]];
+                        d2[q] = pack2(step.x, step.x);
+                        dx2[q] = pack2(step.y, step.y);
+                    }
                 }
-                if (!FULL) sum_d += step.x;
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    acc[q] = same[q] = 0ull;
+                    if constexpr (!PER) {
+                        float u0, u1;
+                        unpack2(mul2(d2[q], decay[q][0]), u0, u1);
+                        const float a1 = ex2_approx(u0);
+                        same[q] = pack2(a1, a1);
+                    }
+                    if (!FULL) sum_d[q] += __uint_as_float(static_cast<uint32_t>(d2[q]));
+                }
 #pragma unroll
                 for (int j = 0; j < NS; j += 4) {
                     const ulonglong2 b2 = *reinterpret_cast<const ulonglong2 *>(&sm.b[g + l][j * LANES + lane * 4]);
-                    f32x2 e0 = same, e1 = same;
-                    if constexpr (PER) {
-                        float u0, u1, u2, u3;
-                        unpack2(mul2(d2, decay[j / 2]), u0, u1);
-                        unpack2(mul2(d2, decay[j / 2 + 1]), u2, u3);
-                        e0 = pack2(ex2_approx(u0), ex2_approx(u1));
-                        e1 = pack2(ex2_approx(u2), ex2_approx(u3));
-                    }
-                    st[j / 2] = fma2(e0, st[j / 2], mul2(dx2, b2.x));
-                    st[j / 2 + 1] = fma2(e1, st[j / 2 + 1], mul2(dx2, b2.y));
-                    if constexpr (FULL) {
-                        const ulonglong2 c2 = *reinterpret_cast<const ulonglong2 *>(&sm.c[g + l][j * LANES + lane * 4]);
-                        acc = fma2(st[j / 2], c2.x, acc);
-                        acc = fma2(st[j / 2 + 1], c2.y, acc);
+                    ulonglong2 c2 = make_ulonglong2(0ull, 0ull);
+                    if (FULL) c2 = *reinterpret_cast<const ulonglong2 *>(&sm.c[g + l][j * LANES + lane * 4]);
+#pragma unroll
+                    for (int q = 0; q < R; ++q) {
+                        f32x2 e0 = same[q], e1 = same[q];
+                        if constexpr (PER) {
+                            float u0, u1, u2, u3;
+                            unpack2(mul2(d2[q], decay[q][j / 2]), u0, u1);
+                            unpack2(mul2(d2[q], decay[q][j / 2 + 1]), u2, u3);
+                            e0 = pack2(ex2_approx(u0), ex2_approx(u1));
+                            e1 = pack2(ex2_approx(u2), ex2_approx(u3));
+                        }
+                        st[q][j / 2] = fma2(e0, st[q][j / 2], mul2(dx2[q], b2.x));
+                        st[q][j / 2 + 1] = fma2(e1, st[q][j / 2 + 1], mul2(dx2[q], b2.y));
+                        if constexpr (FULL) {
+                            acc[q] = j == 0 ? mul2(st[q][0], c2.x) : fma2(st[q][j / 2], c2.x, acc[q]);
+                            acc[q] = fma2(st[q][j / 2 + 1], c2.y, acc[q]);
+                        }
                     }
                 }
-                float lo, hi;
-                unpack2(acc, lo, hi);
-                y[l] = lo + hi;
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    float lo, hi;
+                    unpack2(acc[q], lo, hi);
+                    y[l * R + q] = lo + hi;
+                }
             }
             if constexpr (FULL) {
-                // y[l] summed over the lanes for token g + l: at each step a lane keeps the half of the tokens that has its bit
+                // y[i] summed over the lanes for lane i: at each step a lane keeps the half of the sums that has its bit
 #pragma unroll
                 for (int m = LANES / 2; m > 0; m >>= 1)
 #pragma unroll
                     for (int l = 0; l < m; ++l) {
                         const bool upper = (lane & m) != 0;
                         const float keep = upper ? y[l + m] : y[l], give = upper ? y[l] : y[l + m];
-                        y[l] = keep + __shfl_xor_sync(kFullMask, give, m);
+                        y[l] = keep + __shfl_xor_sync(kFullMask, give, m * (32 / LANES));
                     }
-                const int t = g + lane;
-                float o = fmaf(skip, bf16_bits(sm.x[t][row]), y[0]);
-                if (a.z.data != nullptr) o *= silu(bf16_bits(sm.z[t][row]));
-                sm.x[t][row] = round_bf16(o);
+                sums[g / kTogether] = y[0];
+            }
+        }
+        if constexpr (FULL) {
+#pragma unroll
+            for (int g = 0; g < T; g += kTogether) {
+                const int t = g + out_tok;
+                float o = fmaf(skip, bf16_bits(sm.x[t][out_row]), sums[g / kTogether]);
+                if (a.z.data != nullptr) o *= silu(bf16_bits(sm.z[t][out_row]));
+                sm.x[t][out_row] = round_bf16(o);
             }
         }
         __syncthreads();
@@ -321,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const __grid_constan
 #pragma unroll
             for (int l = 0; l < kLoads; ++l) {
                 const int t = tok + l * kStep;
-                if (!loads || t >= n) continue;
+                if (!loads(l) || t >= n) continue;
                 uint16_t *to = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + (t0 + t) * a.out.stride_tok;
                 if (vec.out && at + 8 <= group_rows) {
                     const int oh = at / a.head_dim;
@@ -340,20 +409,24 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const __grid_constan
         }
     }
 
-    if (!real) return;
-    if (!FULL || (last && a.state != nullptr)) {
-        float *to = FULL ? pool : slot;
-        const int64_t step = FULL ? a.s_stride_state : 1;
 #pragma unroll
-        for (int j = 0; j < NS; j += 2) {
-            const int n = (j / 4) * 4 * LANES + lane * 4 + (j & 3);
-            float f0, f1;
-            unpack2(st[j / 2], f0, f1);
-            if (n < a.dim_state) to[n * step] = f0;
-            if (n + 1 < a.dim_state) to[(n + 1) * step] = f1;
+    for (int q = 0; q < R; ++q) {
+        const int r = r0 + row + q;
+        if (r >= group_rows) continue;
+        if (!FULL || (last && a.state != nullptr)) {
+            float *to = FULL ? pool_at(r) : slot_at(r);
+            const int64_t step = FULL ? a.s_stride_state : 1;
+#pragma unroll
+            for (int j = 0; j < NS; j += 2) {
+                const int n = (j / 4) * 4 * LANES + lane * 4 + (j & 3);
+                float f0, f1;
+                unpack2(st[q][j / 2], f0, f1);
+                if (n < a.dim_state) to[n * step] = f0;
+                if (n + 1 < a.dim_state) to[(n + 1) * step] = f1;
+            }
         }
+        if (!FULL && lane == 0) p.seg_decay[static_cast<int64_t>(unit) * all_rows + head0 * a.head_dim + r] = sum_d[q];
     }
-    if (!FULL && lane == 0) p.seg_decay[static_cast<int64_t>(unit) * all_rows + head0 * a.head_dim + r] = sum_d;
 }
 
 // The segments' first states, one after the other, from their own: F <- e^{A sum of d} F + own, a thread a row and state; the
@@ -394,32 +467,32 @@ int64_t segment_slots(int total_tokens, int batch, int seg_units) {
 // States that a row has room for.
 int padded_states(int dim_state) { return dim_state <= 16 ? 16 : dim_state <= 32 ? 32 : dim_state <= 64 ? 64 : dim_state <= 128 ? 128 : 256; }
 
-template <int LANES, int NS, bool PER>
+template <int LANES, int NS, int R, int ROWS, int TOKENS, bool PER>
 int launch_scan(const SsmFwd &p, const ScanVec &vec, cudaStream_t stream) {
-    const int rows = kThreads / LANES, group_rows = p.a.num_heads / p.a.num_groups * p.a.head_dim;
+    const int rows = ROWS, group_rows = p.a.num_heads / p.a.num_groups * p.a.head_dim;
     const int64_t blocks = static_cast<int64_t>(p.a.num_groups) * ((group_rows + rows - 1) / rows);
     const int64_t units = p.seg_chunks > 0 ? segment_slots(p.total_tokens, p.batch, p.seg_chunks) : p.batch;
     if (blocks * units > 0x7fffffff) return CCV_ERR_SIZE;
-    const dim3 grid(static_cast<unsigned>(blocks * units)), block(kThreads);
+    const dim3 grid(static_cast<unsigned>(blocks * units)), block(LANES * ROWS / R);
     if (p.seg_chunks > 0) {
-        int status = launch_pdl(ssm_scan_kernel<LANES, NS, PER, false>, grid, block, 0, stream, p, vec);
+        int status = launch_pdl(ssm_scan_kernel<LANES, NS, R, ROWS, TOKENS, PER, false>, grid, block, 0, stream, p, vec);
         if (status != CCV_OK) return status;
         const int64_t joins = p.batch * ((static_cast<int64_t>(p.a.num_heads) * p.a.head_dim * p.a.dim_state + 255) / 256);
         if (joins > 0x7fffffff) return CCV_ERR_SIZE;
         status = launch_pdl(ssm_scan_join_kernel, dim3(static_cast<unsigned>(joins)), dim3(256), 0, stream, p, LANES * NS);
         if (status != CCV_OK) return status;
     }
-    return launch_pdl(ssm_scan_kernel<LANES, NS, PER, true>, grid, block, 0, stream, p, vec);
+    return launch_pdl(ssm_scan_kernel<LANES, NS, R, ROWS, TOKENS, PER, true>, grid, block, 0, stream, p, vec);
 }
 
 template <bool PER>
 int launch_states(const SsmFwd &p, const ScanVec &vec, cudaStream_t stream) {
     const int n = p.a.dim_state;
-    if (n <= 16) return launch_scan<4, 4, PER>(p, vec, stream);
-    if (n <= 32) return launch_scan<8, 4, PER>(p, vec, stream);
-    if (n <= 64) return launch_scan<8, 8, PER>(p, vec, stream);
-    if (n <= 128) return launch_scan<16, 8, PER>(p, vec, stream);
-    return launch_scan<16, 16, PER>(p, vec, stream);
+    if (n <= 16) return launch_scan<4, 4, 1, 32, 32, PER>(p, vec, stream);
+    if (n <= 32) return launch_scan<8, 4, 1, 16, 32, PER>(p, vec, stream);
+    if (n <= 64) return launch_scan<8, 8, 1, 16, 32, PER>(p, vec, stream);
+    if (n <= 128) return launch_scan<16, 8, 1, 8, 32, PER>(p, vec, stream);
+    return launch_scan<16, 16, 1, 8, 16, PER>(p, vec, stream);
 }
 
 }  // namespace
@@ -430,12 +503,27 @@ int64_t ssm_scan_workspace(int total_tokens, int batch, int num_heads, int head_
     return rows * padded_states(dim_state) * 4 + (rows * 4 + 127) / 128 * 128;
 }
 
-// Units of 128 tokens of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the
-// device).  Cutting does the states' work twice.
+// Units of 128 tokens of a segment, or 0 to leave sequences whole.  Offsets are on the device, so the longest sequence is taken to
+// be halfway between the average and all tokens.  In cycles: a token takes 140 in a block with an SM to itself, and 57 of the SM's
+// throughput; cutting does three quarters of the work once more, a segment of the join takes 700 and the two launches 20000.
 int ssm_scan_segments(int total_tokens, int batch, int num_heads, int num_groups, int head_dim, int dim_state) {
     const char *forced = std::getenv("CCV_SSM_SEGMENT");  // (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;
-    return 0;
+    constexpr double kSms = 152;  // a GB300's: the workspace's size may not depend on the device that is current
+    const double rows = dim_state <= 16 ? 32 : dim_state <= 64 ? 16 : 8;
+    const double blocks = num_groups * std::ceil(static_cast<double>(num_heads / num_groups) * head_dim / rows);
+    const double longest = 0.5 * (static_cast<double>(total_tokens) / batch + total_tokens);
+    const double work = total_tokens * blocks / kSms * 57;
+    double best = std::max(work, longest * 140);
+    int choice = 0;
+    for (int units = 1; units <= 64 && units * kUnit < longest; units *= 2) {
+        const double cost = std::max(1.75 * work, 1.75 * 140 * units * kUnit) + longest / (units * kUnit) * 700 + 20000;
+        if (cost < best) {
+            best = cost;
+            choice = units;
+        }
+    }
+    return choice;
 }
 
 int ssm_launch_scan(const SsmFwd &call, void *workspace, cudaStream_t stream) {
