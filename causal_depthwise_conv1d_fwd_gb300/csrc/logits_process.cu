@@ -1,9 +1,15 @@
 // Adjustment of logits before tokens are chosen: penalties for what a request has said, a bias list, a grammar's mask.
 //
 // A block has a share of one row's vocabulary for all of the row's positions.  It counts the share's tokens in the history into
-// a table in shared memory (a word a token: how often it was said, whether it is in the prompt, whether it has a bias), then
-// goes through the positions, adding the draft that each one follows.  A row's history is read by all of its blocks, from L2
-// after the first.
+// a table in shared memory (a word a token: how often it was said, whether it is in the prompt, whether it has a bias) and notes
+// them in a bitmap, then goes through the positions, adding the draft that each one follows, eight logits at a time.  Where no
+// lane of a warp has more than two bits they are stored once more, one by one; else all of the warp's logits go through the
+// penalties' arithmetic, which has no branches.  A row's history is read by all of its blocks, from L2 after the first.
+//
+// In place and without a mask only the tokens that were seen matter.  Where they are few enough for a hash table in shared memory
+// a block takes a whole row: it counts the history there, lists the slots in use, and goes through the list at each position.
+#include <algorithm>
+
 #include "ccv_common.cuh"
 #include "ccv_logits.h"
 
@@ -12,29 +18,86 @@ namespace {
 
 constexpr int kLogitsThreads = 256;
 constexpr int kShare = 8192;  // tokens of a block's table: 32 KB
+constexpr int kAhead = 8;     // history tokens that a thread has in flight
 constexpr uint32_t kPrompt = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3fffffffu;
 
 struct Penalties {
-    float repetition, frequency, presence;
+    float repetition, inverse, frequency, presence;  // the quotient is a product with 1 / repetition: 2 units of fp32 off at most
+    const int32_t *ids;  // the row's bias list
+    const float *bias;
+    int size;
 };
 
-// One logit's penalties and bias.  `bias` are the row's entries.
-__device__ __forceinline__ float adjust(float x, uint32_t entry, int token, const Penalties &p, const int32_t *ids, const float *bias,
-                                        int size) {
+// One logit's penalties and bias.
+__device__ __forceinline__ float adjust(float x, uint32_t entry, int token, const Penalties &p) {
     const float n = static_cast<float>(entry & kCount);
-    if ((entry & (kPrompt | kCount)) != 0) {
-        x = x > 0.0f ? x / p.repetition : x * p.repetition;
-        if (n > 0.0f) x = x - p.frequency * n - p.presence;
-    }
+    x = (entry & (kPrompt | kCount)) != 0u ? x * (x > 0.0f ? p.inverse : p.repetition) : x;
+    x = n > 0.0f ? fmaf(-p.frequency, n, x) - p.presence : x;
     if (entry & kBiased) {
         float sum = 0.0f;
-        for (int i = 0; i < size; ++i)
-            if (ids[i] == token) sum += bias[i];
+        for (int i = 0; i < p.size; ++i)
+            if (p.ids[i] == token) sum += p.bias[i];
         x += sum;
     }
     return x;
 }
 
+// Eight logits as they are in memory: 16 bytes of bf16, or 32 of fp32.
+template <bool F32> struct Eight;
+template <> struct Eight<false> {
+    uint4 v;
+    __device__ __forceinline__ void load(const void *p, int64_t i) { v = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i)); }
+    __device__ __forceinline__ void store(void *p, int64_t i) const { __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i), v); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        Raw<8> r;
+        r.v = v;
+        r.to_float(f);
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        Raw<8> r;
+        r.from_float(f);
+        v = r.v;
+    }
+    __device__ __forceinline__ float one(int i) const { return bf16_bits(Raw<8>{v}.elem(i)); }
+    // -inf where a bit of `may` is not set
+    __device__ __forceinline__ void mask(uint32_t may) {
+        const auto half = [&](int i, uint32_t w) {
+            const uint32_t keep = ((may >> (2 * i)) & 1u) * 0xffffu + ((may >> (2 * i + 1)) & 1u) * 0xffff0000u;
+            return (w & keep) | (0xff80ff80u & ~keep);
+        };
+        v = make_uint4(half(0, v.x), half(1, v.y), half(2, v.z), half(3, v.w));
+    }
+};
+template <> struct Eight<true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        a = __ldcs(q);
+        b = __ldcs(q + 1);
+    }
+    __device__ __forceinline__ void store(void *p, int64_t i) const {
+        float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+        __stcs(q, a);
+        __stcs(q + 1, b);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        a = make_float4(f[0], f[1], f[2], f[3]);
+        b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ float one(int i) const {
+        const float4 h = i < 4 ? a : b;
+        return (i & 3) == 0 ? h.x : (i & 3) == 1 ? h.y : (i & 3) == 2 ? h.z : h.w;
+    }
+    __device__ __forceinline__ void mask(uint32_t may) {
+        const auto one = [&](int i, float x) { return ((may >> i) & 1u) != 0u ? x : -INFINITY; };
+        a = make_float4(one(0, a.x), one(1, a.y), one(2, a.z), one(3, a.w));
+        b = make_float4(one(4, b.x), one(5, b.y), one(6, b.z), one(7, b.w));
+    }
+};
 template <bool F32>
 __device__ __forceinline__ float load_logit(const void *p, int64_t i) {
     if constexpr (F32) return static_cast<const float *>(p)[i];
@@ -45,14 +108,22 @@ __device__ __forceinline__ void store_logit(void *p, int64_t i, float x) {
     if constexpr (F32) static_cast<float *>(p)[i] = x;
     else static_cast<uint16_t *>(p)[i] = round_bf16(x);
 }
+// Elements from address p on to the next 16-byte boundary.
+template <bool F32>
+__device__ __forceinline__ int to_boundary(const void *p, int64_t i) {
+    constexpr int kSize = F32 ? 4 : 2;
+    return static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) + i * kSize) % 16) % 16 / kSize);
+}
 
 // IN, OUT: fp32 logits and results.  PLACE: out is logits.
 template <bool IN, bool OUT, bool PLACE>
-__global__ void __launch_bounds__(kLogitsThreads) logits_kernel(const __grid_constant__ ccv_logits_args a, int shares, int *err_count) {
-    __shared__ uint32_t table[kShare];
+__global__ void __launch_bounds__(kLogitsThreads, IN ? 1 : 4) logits_kernel(const __grid_constant__ ccv_logits_args a, int shares, int *err_count) {
+    __shared__ __align__(16) uint32_t table[kShare];
+    __shared__ uint32_t touched[kShare / 32 + 1];
     const int tid = threadIdx.x;
     const int b = blockIdx.x / shares, first = (blockIdx.x % shares) * kShare, n = min(kShare, a.vocab - first);
-    for (int i = tid; i < kShare; i += kLogitsThreads) table[i] = 0;
+    for (int i = tid; i < kShare / 4; i += kLogitsThreads) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < kShare / 32 + 1; i += kLogitsThreads) touched[i] = 0u;
     wait_prior_grid();
     release_next_grid();
     const int line = a.history_indices != nullptr ? a.history_indices[b] : b;
@@ -63,13 +134,13 @@ __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(const __grid_con
     }
     __syncthreads();
     bool odd = false;
-    auto add = [&](int token, bool said) {
+    const auto note = [&](int token, uint32_t flag) {  // flag 0: said
         odd |= token >= a.vocab;
-        const unsigned at = static_cast<unsigned>(token - first);
-        if (token >= 0 && at < static_cast<unsigned>(n)) {
-            if (said) atomicAdd(&table[at], 1u);
-            else atomicOr(&table[at], kPrompt);
-        }
+        const unsigned at = static_cast<unsigned>(token) - static_cast<unsigned>(first);
+        if (at >= static_cast<unsigned>(n)) return;
+        if (flag == 0u) atomicAdd(&table[at], 1u);
+        else atomicOr(&table[at], flag);
+        atomicOr(&touched[at / 32], 1u << (at % 32));
     };
     if (a.history != nullptr) {
         int told = a.history_lengths[line], prompt = a.prompt_lengths != nullptr ? a.prompt_lengths[line] : 0;
@@ -77,34 +148,225 @@ __global__ void __launch_bounds__(kLogitsThreads) logits_kernel(const __grid_con
         told = min(max(told, 0), a.history_size);
         prompt = min(max(prompt, 0), a.history_size);
         const int32_t *ids = a.history + line * a.h_stride_line;
-        for (int i = tid; i < told; i += kLogitsThreads) add(ids[i], i >= prompt);
+        for (int i0 = tid; i0 < told; i0 += kLogitsThreads * kAhead) {
+            int token[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) token[j] = i0 + j * kLogitsThreads < told ? __ldg(ids + i0 + j * kLogitsThreads) : -1;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) note(token[j], i0 + j * kLogitsThreads < prompt ? kPrompt : 0u);
+        }
     }
-    const int32_t *bias_ids = a.bias_ids + b * a.b_stride_b;
-    const float *bias = a.bias + b * a.b_stride_b;
-    for (int i = tid; i < a.bias_size; i += kLogitsThreads) {
-        const int token = bias_ids[i];
-        odd |= token >= a.vocab;
-        const unsigned at = static_cast<unsigned>(token - first);
-        if (token >= 0 && at < static_cast<unsigned>(n)) atomicOr(&table[at], kBiased);
-    }
-    const Penalties p{a.repetition != nullptr ? a.repetition[b] : 1.0f, a.frequency != nullptr ? a.frequency[b] : 0.0f,
-                      a.presence != nullptr ? a.presence[b] : 0.0f};
+    const float repetition = a.repetition != nullptr ? a.repetition[b] : 1.0f;
+    const Penalties p{repetition,
+                      1.0f / repetition,
+                      a.frequency != nullptr ? a.frequency[b] : 0.0f,
+                      a.presence != nullptr ? a.presence[b] : 0.0f,
+                      a.bias_ids + b * a.b_stride_b,
+                      a.bias + b * a.b_stride_b,
+                      a.bias_size};
+    for (int i = tid; i < p.size; i += kLogitsThreads) note(p.ids[i], kBiased);
+
     for (int pos = 0; pos < a.num_positions; ++pos) {
-        if (pos > 0 && a.draft_tokens != nullptr && tid == 0) add(a.draft_tokens[b * a.d_stride_b + (pos - 1) * a.d_stride_pos], true);
-        __syncthreads();
+        if (pos > 0 && a.draft_tokens != nullptr) {
+            __syncthreads();  // the last position's threads are done with the table
+            if (tid == 0) note(a.draft_tokens[b * a.d_stride_b + (pos - 1) * a.d_stride_pos], 0u);
+        }
         const int64_t from = b * a.l_stride_b + pos * a.l_stride_pos + first, to = b * a.o_stride_b + pos * a.o_stride_pos + first;
         const int32_t *mask = a.mask != nullptr ? a.mask + b * a.m_stride_b + pos * a.m_stride_pos + first / 32 : nullptr;
-        for (int i = tid; i < n; i += kLogitsThreads) {
-            const uint32_t entry = table[i];
-            const bool may = mask == nullptr || ((static_cast<uint32_t>(mask[i / 32]) >> (i & 31)) & 1u) != 0;
-            if (PLACE && may && entry == 0) continue;
-            float x = -INFINITY;
-            if (may) x = adjust(load_logit<IN>(a.logits, from + i), entry, first + i, p, bias_ids, bias, a.bias_size);
-            store_logit<OUT>(a.out, to + i, x);
+        const int words = (n + 31) / 32;
+        // Elements up to 16 bytes' boundary and past the last vector go one by one; all do where input and output never meet one.
+        int head = to_boundary<IN>(a.logits, from);
+        if (to_boundary<OUT>(a.out, to + head) != 0) head = n;
+        head = min(head, n);
+        const int vectors = (n - head) / 8, rest = n - head - vectors * 8;
+        constexpr int kVectors = kShare / 8 / kLogitsThreads;
+        if (!PLACE || mask != nullptr) {
+            uint32_t may[kVectors];  // eight bits each
+            Eight<IN> x[PLACE ? 1 : kVectors];
+#pragma unroll
+            for (int j = 0; j < kVectors; ++j) {
+                const int at = head + (tid + j * kLogitsThreads) * 8;
+                may[j] = 0xffu;
+                if (tid + j * kLogitsThreads >= vectors) continue;
+                if constexpr (!PLACE) x[j].load(a.logits, from + at);
+                if (mask != nullptr)
+                    may[j] = __funnelshift_r(__ldg(mask + at / 32), at / 32 + 1 < words ? __ldg(mask + at / 32 + 1) : 0, at % 32) & 0xffu;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kVectors; ++j) {
+                const int at = head + (tid + j * kLogitsThreads) * 8;
+                const bool mine = tid + j * kLogitsThreads < vectors;
+                const uint32_t bits = mine ? __funnelshift_r(touched[at / 32], touched[at / 32 + 1], at % 32) & may[j] : 0u;
+                Eight<IN> in;
+                if constexpr (PLACE) {
+                    if (mine && may[j] != 0u && (may[j] != 0xffu || bits != 0u)) in.load(a.logits, from + at);
+                } else {
+                    in = x[j];
+                }
+                const bool many = __any_sync(kFullMask, __popc(bits) > 2);
+                if (!mine || (PLACE && may[j] == 0xffu && bits == 0u)) continue;
+                Eight<OUT> result;
+                if (many || IN != OUT) {
+                    float f[8];
+                    in.get(f);
+                    if (many) {
+                        uint32_t entry[8];
+                        if (head % 4 == 0) {
+                            const uint4 e0 = *reinterpret_cast<const uint4 *>(&table[at]), e1 = *reinterpret_cast<const uint4 *>(&table[at + 4]);
+                            entry[0] = e0.x; entry[1] = e0.y; entry[2] = e0.z; entry[3] = e0.w;
+                            entry[4] = e1.x; entry[5] = e1.y; entry[6] = e1.z; entry[7] = e1.w;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) entry[i] = table[at + i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = adjust(f[i], entry[i], first + at + i, p);
+                    }
+                    result.set(f);
+                } else if constexpr (IN == OUT) {
+                    result = in;
+                }
+                if (mask != nullptr) result.mask(may[j]);
+                result.store(a.out, to + at);
+                if (many) continue;
+                for (uint32_t left = bits; left != 0u; left &= left - 1u) {
+                    const int i = __ffs(left) - 1;
+                    store_logit<OUT>(a.out, to + at + i, adjust(in.one(i), table[at + i], first + at + i, p));
+                }
+            }
+            for (int k = tid; k < head + rest; k += kLogitsThreads) {
+                const int at = k < head ? k : k + vectors * 8;
+                const uint32_t entry = table[at];
+                const bool can = mask == nullptr || ((static_cast<uint32_t>(mask[at / 32]) >> (at % 32)) & 1u) != 0;
+                if (PLACE && can && entry == 0u) continue;
+                store_logit<OUT>(a.out, to + at, can ? adjust(load_logit<IN>(a.logits, from + at), entry, first + at, p) : -INFINITY);
+            }
+        } else {
+            __syncthreads();
+            for (int word = tid; word < words; word += kLogitsThreads)
+                for (uint32_t bits = touched[word]; bits != 0u;) {
+                    int at[4];
+                    float f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        at[i] = bits != 0u ? word * 32 + __ffs(bits) - 1 : -1;
+                        bits &= bits - 1u;
+                        f[i] = at[i] >= 0 ? load_logit<IN>(a.logits, from + at[i]) : 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (at[i] >= 0) store_logit<OUT>(a.out, to + at[i], adjust(f[i], table[at[i]], first + at[i], p));
+                }
+        }
+    }
+    if (__syncthreads_or(odd) && tid == 0) count_error(err_count);
+}
+
+constexpr int kRowThreads = 1024;
+constexpr int kMaxSlots = 16384;
+constexpr uint32_t kNone = 0xffffffffu;
+
+// Slots of the hash table: a quarter stays empty even if all of a row's tokens differ; 0 where they are too many for it.
+int hash_slots(const ccv_logits_args &a) {
+    const int64_t tokens = static_cast<int64_t>(a.history != nullptr ? a.history_size : 0) + (a.draft_tokens != nullptr ? a.num_positions - 1 : 0) + a.bias_size;
+    int slots = 1024;
+    while (3 * static_cast<int64_t>(slots) < 4 * tokens && slots <= kMaxSlots) slots *= 2;
+    return slots <= kMaxSlots ? slots : 0;
+}
+size_t hash_bytes(int slots) { return static_cast<size_t>(slots) * 9; }
+
+// A block a row, in place and without a mask.  slots: a power of two, at most three quarters of them used.
+template <bool F32>
+__global__ void __launch_bounds__(kRowThreads) logits_row_kernel(const __grid_constant__ ccv_logits_args a, int slots, int *err_count) {
+    extern __shared__ __align__(16) uint32_t hash[];
+    uint32_t *key = hash, *entry = hash + slots;
+    uint16_t *list = reinterpret_cast<uint16_t *>(entry + slots);
+    __shared__ int used;
+    const int tid = threadIdx.x, b = blockIdx.x, shift = 32 - (31 - __clz(slots));
+    for (int i = tid; i < slots / 4; i += kRowThreads) {
+        reinterpret_cast<uint4 *>(key)[i] = make_uint4(kNone, kNone, kNone, kNone);
+        reinterpret_cast<uint4 *>(entry)[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (tid == 0) used = 0;
+    wait_prior_grid();
+    release_next_grid();
+    const int line = a.history_indices != nullptr ? a.history_indices[b] : b;
+    if (a.history_indices != nullptr && line == a.pad_slot_id) return;
+    if (a.history != nullptr && (line < 0 || line >= a.num_lines)) {
+        if (tid == 0) count_error(err_count);
+        return;
+    }
+    __syncthreads();
+    bool odd = false;
+    const auto note = [&](int token, uint32_t flag) {  // flag 0: said
+        odd |= token >= a.vocab;
+        if (static_cast<unsigned>(token) >= static_cast<unsigned>(a.vocab)) return;
+        uint32_t at = (static_cast<uint32_t>(token) * 2654435769u) >> shift;  // multiplicative hashing (Knuth)
+        for (;; at = (at + 1) & (slots - 1)) {  // some slots stay empty, so it ends
+            const uint32_t old = atomicCAS(&key[at], kNone, static_cast<uint32_t>(token));
+            if (old == kNone) list[atomicAdd(&used, 1)] = static_cast<uint16_t>(at);
+            if (old == kNone || old == static_cast<uint32_t>(token)) break;
+        }
+        if (flag == 0u) atomicAdd(&entry[at], 1u);
+        else atomicOr(&entry[at], flag);
+    };
+    if (a.history != nullptr) {
+        int told = a.history_lengths[line], prompt = a.prompt_lengths != nullptr ? a.prompt_lengths[line] : 0;
+        odd |= told < 0 || told > a.history_size || prompt < 0 || prompt > a.history_size;
+        told = min(max(told, 0), a.history_size);
+        prompt = min(max(prompt, 0), a.history_size);
+        const int32_t *ids = a.history + line * a.h_stride_line;
+        for (int i0 = tid; i0 < told; i0 += kRowThreads * kAhead) {
+            int token[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) token[j] = i0 + j * kRowThreads < told ? __ldg(ids + i0 + j * kRowThreads) : -1;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) note(token[j], i0 + j * kRowThreads < prompt ? kPrompt : 0u);
+        }
+    }
+    const float repetition = a.repetition != nullptr ? a.repetition[b] : 1.0f;
+    const Penalties p{repetition,
+                      1.0f / repetition,
+                      a.frequency != nullptr ? a.frequency[b] : 0.0f,
+                      a.presence != nullptr ? a.presence[b] : 0.0f,
+                      a.bias_ids + b * a.b_stride_b,
+                      a.bias + b * a.b_stride_b,
+                      a.bias_size};
+    for (int i = tid; i < p.size; i += kRowThreads) note(p.ids[i], kBiased);
+    for (int pos = 0; pos < a.num_positions; ++pos) {
+        if (pos > 0 && a.draft_tokens != nullptr) {
+            __syncthreads();  // the last position's threads are done with the table
+            if (tid == 0) note(a.draft_tokens[b * a.d_stride_b + (pos - 1) * a.d_stride_pos], 0u);
         }
         __syncthreads();
+        const int count = used;
+        const int64_t from = b * a.l_stride_b + pos * a.l_stride_pos;
+        for (int i0 = tid; i0 < count; i0 += kRowThreads * 4) {
+            uint32_t at[4], token[4];
+            float f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j * kRowThreads;
+                at[j] = i < count ? list[i] : 0u;
+                token[j] = i < count ? key[at[j]] : kNone;
+                f[j] = i < count ? load_logit<F32>(a.logits, from + token[j]) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (token[j] != kNone) store_logit<F32>(a.out, from + token[j], adjust(f[j], entry[at[j]], static_cast<int>(token[j]), p));
+        }
     }
-    if (odd) count_error(err_count);
+    if (__syncthreads_or(odd) && tid == 0) count_error(err_count);
+}
+
+template <bool F32>
+int launch_rows(const ccv_logits_args &a, int slots, int *err_count, cudaStream_t stream) {
+    int dev = 0;
+    current_device_sms(&dev);
+    cudaError_t err;
+    if (resident_blocks<logits_row_kernel<F32>>(kRowThreads, hash_bytes(kMaxSlots), dev, &err) == 0) return static_cast<int>(err);
+    return launch_pdl(logits_row_kernel<F32>, dim3(static_cast<unsigned>(a.batch)), dim3(kRowThreads), hash_bytes(slots), stream, a, slots, err_count);
 }
 
 int check(const ccv_logits_args *a) {
@@ -147,11 +409,13 @@ extern "C" int logits_process(const ccv_logits_args *args, int *err_count, ccv_s
     const int status = check(args);
     if (status != CCV_OK) return status;
     if (args->batch == 0 || args->num_positions == 0 || args->vocab == 0) return CCV_OK;
+    const bool place = args->out == args->logits;
+    if (const int slots = place && args->mask == nullptr ? hash_slots(*args) : 0)
+        return args->logits_fp32 ? launch_rows<true>(*args, slots, err_count, stream) : launch_rows<false>(*args, slots, err_count, stream);
     const int shares = (args->vocab + kShare - 1) / kShare;
     const int64_t blocks = static_cast<int64_t>(shares) * args->batch;
     if (blocks > 0x7fffffff) return CCV_ERR_SIZE;
     const dim3 grid(static_cast<unsigned>(blocks)), block(kLogitsThreads);
-    const bool place = args->out == args->logits;
     auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, stream, *args, shares, err_count); };
     if (args->logits_fp32) {
         if (place) return go(logits_kernel<true, true, true>);
