@@ -6,7 +6,9 @@
 // a whole row of it, so the kernel is bound by HBM for more than a few rows and by one memory round trip below that.
 //
 // A row of S (contiguous) belongs to LANES lanes, each holding every LANES-th group of 4 values: a warp's load covers whole
-// 128-byte lines, the sum over the row takes 2 or 3 shuffles, and no shared memory or barrier is needed.
+// 128-byte lines, and no shared memory or barrier is needed.  A group of lanes has R rows next to each other; what goes by the row
+// (x, the step, the decay where a head has one, the output) is one lane's work and reaches the others by shuffles, and the sums
+// over the lanes are taken for all rows at once, so that each ends with the lane that its row belongs to.
 #include "ssm_common.cuh"
 
 namespace ccv {
@@ -49,7 +51,7 @@ __device__ __forceinline__ void load_bf16x4(const uint16_t *p, int64_t stride, i
 // LANES x NV x 4: dim_state rounded up.  R: rows of the state a group of lanes has.  PER: A has a value a state.
 // V: dim_state and every stride and pointer allow 16-byte vectors of the state and 8-byte vectors of B and C.
 template <int LANES, int NV, int R, bool PER, bool V>
-__global__ void __launch_bounds__(kSsmThreads) ssm_recurrent_kernel(const __grid_constant__ ccv_ssm_args a,
+__global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6) ssm_recurrent_kernel(const __grid_constant__ ccv_ssm_args a,
                                                                     const __grid_constant__ SsmRows rw, int slices) {
     constexpr int kGroups = kSsmThreads / LANES;
     wait_prior_grid();
@@ -92,77 +94,103 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_recurrent_kernel(const __grid
     }
 
     const int rows = a.num_heads * a.head_dim, rep = a.num_heads / a.num_groups;
-    float s[R][NV][4], decay[R][PER ? NV : 1][PER ? 4 : 1], bias[R], skip[R];
-    int head[R], chan[R], grp[R];
-    bool use[R];
+    const int first_row = (slice * kGroups + group) * R;
+    float s[R][NV][4], decay[PER ? R : 1][PER ? NV : 1][PER ? 4 : 1];
     int64_t off[R];  // of the row in a state line
+    int grp[R];
+    const int own_row = first_row + lane % R;  // the lane's
+    const bool own = lane < R && own_row < rows;
+    int own_h = 0, own_ch = 0;
+    {
+        // one division for the first row; the others follow it
+        int h = min(first_row, rows - 1) / a.head_dim, ch = min(first_row, rows - 1) - h * a.head_dim, g = h / rep, in_group = h - g * rep;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int at = slice * kGroups * R + r * kGroups + group;
-        use[r] = at < rows;
-        head[r] = use[r] ? at / a.head_dim : 0;
-        chan[r] = use[r] ? at - head[r] * a.head_dim : 0;
-        grp[r] = head[r] / rep;
-        off[r] = head[r] * a.s_stride_head + chan[r] * a.s_stride_dim;
-        const float *p = a.state + from * a.s_stride_line + off[r];
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            load4<V>(fresh ? a.A : p, a.s_stride_state, (j * LANES + lane) * 4, use[r] && !fresh ? a.dim_state : 0, s[r][j]);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if constexpr (PER) {
+        for (int r = 0; r < R; ++r) {
+            const bool use = first_row + r < rows;
+            off[r] = h * a.s_stride_head + ch * a.s_stride_dim;
+            grp[r] = g;
+            if (lane % R == r) {
+                own_h = h;
+                own_ch = ch;
+            }
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                load4<false>(a.A + static_cast<int64_t>(head[r]) * a.dim_state, 1, (j * LANES + lane) * 4, a.dim_state, decay[r][j]);
-        } else {
-            decay[r][0][0] = a.A[head[r]];
-        }
-        bias[r] = a.dt_bias != nullptr ? a.dt_bias[head[r]] : 0.0f;
-        skip[r] = a.D != nullptr ? a.D[head[r]] : 0.0f;
-    }
-
-    auto at = [&](const ccv_heads_view &v) { return static_cast<const uint16_t *>(v.data) + row * v.stride_row + t0 * v.stride_tok; };
-    const uint16_t *xp = at(a.x), *zp = at(a.z), *bp = at(a.B), *cp = at(a.C);
-    uint16_t *op = const_cast<uint16_t *>(at(a.out));
-    int64_t step = row * a.dt_stride_row + t0 * a.dt_stride_tok;
-
-    for (int t = 0; t < n; ++t) {
-        float y[R], x[R], d[R];
+                load4<V>(fresh ? a.A : a.state + from * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
+                         use && !fresh ? a.dim_state : 0, s[r][j]);
+            if constexpr (PER) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            x[r] = bf16_bits(xp[head[r] * a.x.stride_head + chan[r] * a.x.stride_dim]);
-            d[r] = ssm_raw_step(a, step + head[r] * a.dt_stride_head);
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            d[r] = ssm_step(d[r], bias[r], a);
-            const float dx = d[r] * x[r];
-            const float same = PER ? 0.0f : expf(d[r] * decay[r][0][0]);
-            y[r] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                float bv[4], cv[4];
-                load_bf16x4<V>(bp + grp[r] * a.B.stride_head, a.B.stride_dim, (j * LANES + lane) * 4, a.dim_state, bv);
-                load_bf16x4<V>(cp + grp[r] * a.C.stride_head, a.C.stride_dim, (j * LANES + lane) * 4, a.dim_state, cv);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = PER ? expf(d[r] * decay[r][PER ? j : 0][PER ? i : 0]) : same;
-                    s[r][j][i] = fmaf(e, s[r][j][i], dx * bv[i]);
-                    y[r] = fmaf(s[r][j][i], cv[i], y[r]);
+                for (int j = 0; j < NV; ++j) {
+                    const float *rates = a.A + static_cast<int64_t>(h) * a.dim_state;
+                    const int d = (j * LANES + lane) * 4;
+                    if constexpr (V) {
+                        const float4 f = d < a.dim_state ? __ldg(reinterpret_cast<const float4 *>(rates + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        decay[r][j][0] = f.x; decay[r][j][1] = f.y; decay[r][j][2] = f.z; decay[r][j][3] = f.w;
+                    } else {
+                        load4<false>(rates, 1, d, a.dim_state, decay[r][j]);
+                    }
+                }
+            }
+            if (first_row + r + 1 < rows && ++ch == a.head_dim) {
+                ch = 0;
+                ++h;
+                if (++in_group == rep) {
+                    in_group = 0;
+                    ++g;
                 }
             }
         }
-#pragma unroll
-        for (int m = 1; m < LANES; m <<= 1)
-#pragma unroll
-            for (int r = 0; r < R; ++r) y[r] += __shfl_xor_sync(kFullMask, y[r], m);
+    }
+    const int h = own_h, ch = own_ch;
+    const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f, skip = a.D != nullptr ? a.D[h] : 0.0f;
+    const float rate = PER ? 0.0f : a.A[h];
+
+    const auto at = [&](const ccv_heads_view &v, int64_t head, int64_t dim) {
+        return static_cast<const uint16_t *>(v.data) + row * v.stride_row + t0 * v.stride_tok + head * v.stride_head + dim * v.stride_dim;
+    };
+    const uint16_t *xp = at(a.x, h, ch), *zp = at(a.z, h, ch), *bp = at(a.B, 0, 0), *cp = at(a.C, 0, 0);
+    uint16_t *op = const_cast<uint16_t *>(at(a.out, h, ch));
+    int64_t step = row * a.dt_stride_row + t0 * a.dt_stride_tok + h * a.dt_stride_head;
+
+    for (int t = 0; t < n; ++t) {
+        const float x = bf16_bits(*xp), d = ssm_step(ssm_raw_step(a, step), bias, a);
+        const float z = a.z.data != nullptr ? bf16_bits(*zp) : 0.0f;
+        const float dx = d * x, same = PER ? d : expf(d * rate);
+        float y[R], bv[NV][4], cv[NV][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (lane != 0 || !use[r]) continue;
-            float o = fmaf(skip[r], x[r], y[r]);
-            if (a.z.data != nullptr) o *= silu(bf16_bits(zp[head[r] * a.z.stride_head + chan[r] * a.z.stride_dim]));
-            op[head[r] * a.out.stride_head + chan[r] * a.out.stride_dim] = round_bf16(o);
+            const float e_or_d = __shfl_sync(kFullMask, same, r, LANES), w = __shfl_sync(kFullMask, dx, r, LANES);
+            if (r == 0 || grp[r] != grp[r - 1]) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    load_bf16x4<V>(bp + grp[r] * a.B.stride_head, a.B.stride_dim, (j * LANES + lane) * 4, a.dim_state, bv[j]);
+                    load_bf16x4<V>(cp + grp[r] * a.C.stride_head, a.C.stride_dim, (j * LANES + lane) * 4, a.dim_state, cv[j]);
+                }
+            }
+            y[r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = PER ? expf(e_or_d * decay[PER ? r : 0][PER ? j : 0][PER ? i : 0]) : e_or_d;
+                    s[r][j][i] = fmaf(e, s[r][j][i], w * bv[j][i]);
+                    y[r] = fmaf(s[r][j][i], cv[j][i], y[r]);
+                }
+        }
+        // halving: after the steps that the rows' count allows each lane has one row's sum over some lanes, then over all
+#pragma unroll
+        for (int m = R / 2; m > 0; m >>= 1)
+#pragma unroll
+            for (int r = 0; r < m; ++r) {
+                const bool upper = (lane & m) != 0;
+                const float keep = upper ? y[r + m] : y[r], give = upper ? y[r] : y[r + m];
+                y[r] = keep + __shfl_xor_sync(kFullMask, give, m);
+            }
+#pragma unroll
+        for (int m = R; m < LANES; m <<= 1) y[0] += __shfl_xor_sync(kFullMask, y[0], m);
+        if (own) {
+            float o = fmaf(skip, x, y[0]);
+            if (a.z.data != nullptr) o *= silu(z);
+            *op = round_bf16(o);
         }
         if (rw.out_indices != nullptr) {
             const int64_t to = rw.out_indices[b * rw.oi_stride_b + t * rw.oi_stride_step];
@@ -174,7 +202,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_recurrent_kernel(const __grid
 #pragma unroll
                     for (int j = 0; j < NV; ++j)
                         store4<V>(a.state + to * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
-                                  use[r] ? a.dim_state : 0, s[r][j]);
+                                  first_row + r < rows ? a.dim_state : 0, s[r][j]);
             }
         }
         xp += a.x.stride_tok;
@@ -190,7 +218,7 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_recurrent_kernel(const __grid
 #pragma unroll
             for (int j = 0; j < NV; ++j)
                 store4<V>(a.state + line * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
-                          use[r] ? a.dim_state : 0, s[r][j]);
+                          first_row + r < rows ? a.dim_state : 0, s[r][j]);
     }
 }
 
@@ -206,10 +234,10 @@ int launch(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
 
 template <bool PER, bool V>
 int launch_states(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
-    if (a.dim_state <= 16) return launch<4, 1, 2, PER, V>(a, rows, stream);
-    if (a.dim_state <= 32) return launch<8, 1, 2, PER, V>(a, rows, stream);
-    if (a.dim_state <= 64) return launch<8, 2, 2, PER, V>(a, rows, stream);
-    if (a.dim_state <= 128) return launch<8, 4, 2, PER, V>(a, rows, stream);
+    if (a.dim_state <= 16) return launch<4, 1, 4, PER, V>(a, rows, stream);
+    if (a.dim_state <= 32) return launch<8, 1, 4, PER, V>(a, rows, stream);
+    if (a.dim_state <= 64) return launch<8, 2, 4, PER, V>(a, rows, stream);
+    if (a.dim_state <= 128) return launch<8, 4, 1, PER, V>(a, rows, stream);
     return launch<8, 8, PER ? 1 : 2, PER, V>(a, rows, stream);
 }
 
@@ -218,7 +246,7 @@ bool vector_ok(const ccv_ssm_args &a) {
         return (reinterpret_cast<uintptr_t>(v.data) & 7u) == 0 && v.stride_dim == 1 && v.stride_row % 4 == 0 &&
                v.stride_tok % 4 == 0 && v.stride_head % 4 == 0;
     };
-    if (a.dim_state % 4 != 0 || !bf(a.B) || !bf(a.C)) return false;
+    if (a.dim_state % 4 != 0 || !bf(a.B) || !bf(a.C) || (a.a_per_state && !aligned16(a.A))) return false;
     return a.state == nullptr || (aligned16(a.state) && a.s_stride_state == 1 && a.s_stride_line % 4 == 0 &&
                                   a.s_stride_head % 4 == 0 && a.s_stride_dim % 4 == 0);
 }
