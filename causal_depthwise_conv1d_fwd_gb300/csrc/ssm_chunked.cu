@@ -10,14 +10,16 @@
 //   M from C B^T (tensor memory to tensor memory), 64 of its columns;
 //   the state in registers (thread n has half of row n), its parts to shared memory for C S, and its multiply-add;
 //   the weighted tokens' parts for the state's sum; and the outputs, 32 channels.
-// Four more warps copy tiles and sum the steps, and issue products: C B^T and M x, the state's sum, C S.
+// Four more warps copy tiles and sum the steps, and issue products: what leads to the outputs, and each head's sum for the state.
 // Heads wider than 64 are cut into panels of 64 that share steps and decays.  With a role a warpgroup the hot instructions were
 // twice as many and missed the instruction cache: a third of all stalls.
 //
-// Precision.  The state is fp32, so the operands of what reaches it keep 24 bits: B enters as its own bf16 values (exact), the
-// weighted tokens as three bf16 parts, and the sum over chunks is an fp32 multiply-add.  Products that reach the output alone
-// (M, S) keep 16 bits an operand, two parts; x and C are exact.  Smaller parts are added first, since the tensor cores' sums
-// truncate.  G is summed in 64-bit fixed point, and differences of it are taken as pairs of floats.
+// Precision.  Every operand that is not bf16 from the start (M, the state in C S, the weighted tokens) enters the tensor cores as
+// two bf16 parts, which hold 16 bits of it: 2^-17 of each term of a sum whose other factors, x, B and C, are exact.  Sums and the
+// state are fp32: the tensor cores' accumulators within a chunk, a multiply-add from chunk to chunk.  The state is 3e-6 of itself
+// off that way, 500 times less than by one part; a third part for the weighted tokens would leave 1e-7 and costs half as many
+// products and instructions again.  Smaller parts are added first, since the tensor cores' sums truncate.  G is summed in pairs
+// of floats, and so are its differences.
 //
 // What is not finite.  A sum over a chunk takes zeros for the tokens after its own, and 0 * NaN is NaN.  So an x that is not
 // finite is left out of the products, and its channel is NaN from that token on, the final state too; a step that is not finite
@@ -37,7 +39,7 @@ constexpr int Q = 128;              // tokens of a chunk
 constexpr int kTile = Q * 128;      // bytes of 128 rows of 64 bf16 values
 constexpr int kQuarter = kTile / 4; // of 32 rows
 constexpr int kThreads = 640;
-constexpr int kCopyWarp = 16, kOutWarp = 17, kSumWarp = 18, kStateWarp = 19;
+constexpr int kCopyWarp = 16, kOutWarp = 17, kSumWarp = 18;  // the last has one warp a head
 // Columns of tensor memory: C B^T; M in two halves of 64 tokens, each in two parts; M x; C S; the heads' sums for the state.
 constexpr uint32_t kColCB = 0, kColM = 128, kColMX = 256, kColCS = 320, kColSum = 384;
 constexpr int kStateFloats = 128 * 64;  // of a head's panel in the workspace
@@ -46,23 +48,22 @@ struct Maps {
     CUtensorMap x, b, c;
 };
 
-struct Gates {  // of a chunk's tokens and a head: G log2(e) as a pair of floats, and the steps
-    float hi[Q], lo[Q], d[Q];
+struct Gates {  // of a chunk's tokens and a head: G log2(e) as a pair of floats, the steps, and e^{G_Q - G_j} d_j
+    float hi[Q], lo[Q], d[Q], weight[Q];
 };
 
 struct Smem {
     uint8_t x[2][2][kTile];     // stage, head
     uint8_t b[2][2][kTile];     // stage, panel of 64 states
     uint8_t c[2][kTile];        // panel
-    uint8_t w[2][3][kQuarter];  // head, part: weighted tokens
+    uint8_t w[2][2][kQuarter];  // head, part: weighted tokens, 32 at a time
     uint8_t s[2][kTile];        // part: the state of the head whose turn it is
     Gates gates[2][2];          // stage, head
-    float factor[2][192];       // head: what the 32, 64, 96 tokens before warps 1, 2, 3 count for in their rows of M
-    float since[2][Q];          // head: G of a token since its warp's first
+    float since[2][4][Q];       // head, 32 rows of M: G of the tokens up to them, counted from the rows' first
     // A barrier's phase is waited for by the same threads each time, or by ones that know the phase before it to be over: a wait
     // tells a phase from the next one only.
-    uint64_t xb_full[2], xb_free[2], c_full, c_free, gates_full[2], gates_free[2];
-    uint64_t cb_full, cb_free, m_full[2], m_free[2], mx_full[2], mx_free, cs_full[2], cs_free, s_full, s_free[2];
+    uint64_t xb_full[2], xb_free[2], c_full, c_free, gates_full[2][2], gates_free[2][2];
+    uint64_t cb_full, cb_free, m_full[2], m_free[2], mx_full[2], cs_full[2], cs_free, s_full, s_free[2];
     uint64_t w_full[2], w_free[2], sum_full[2], x_ok[2][2], drain[3];
     int first_bad[2][64];       // head, channel: the first of the block's tokens whose x is not finite
     int any_bad[2];
@@ -93,13 +94,39 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
-// Called and not inlined: eight copies of it would be a tenth of the kernel's instructions, which have to fit the SM's cache.
-__device__ __noinline__ float step_of(float raw, float bias, const ccv_ssm_args &a) { return ssm_step(raw, bias, a); }
+// Sums of pairs of floats (hi, lo) with |lo| within half a unit of hi: good to 2^-44 or so.
+__device__ __forceinline__ float2 add_pairs(float2 a, float2 b) {
+    const float s = a.x + b.x, t = s - a.x;
+    const float e = ((a.x - (s - t)) + (b.x - t)) + (a.y + b.y);
+    const float hi = s + e;
+    return make_float2(hi, e - (hi - s));
+}
+
+// Four steps from their inputs with the bias, and the logarithms (base 2) of their decays.
+__device__ __forceinline__ void steps_of(float (&d)[4], float2 (&g)[4], float bias, float scale, int real, const ccv_ssm_args &a) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        f32x2 x = add2(pack2(d[i], d[i + 1]), pack2(bias, bias));
+        if (a.dt_softplus) x = softplus2(x);
+        unpack2(x, d[i], d[i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        d[i] = i >= real ? 0.0f : d[i] < a.dt_min ? a.dt_min : d[i] > a.dt_max ? a.dt_max : d[i];
+        constexpr float kHi = 1.4426950216293335f, kLo = 1.9259629911266175e-8f;  // log2(e)
+        float u = d[i] * scale, rest = fmaf(d[i], scale, -u);
+        // e^-200 is 0 in fp32 and e^1000 infinite
+        if (!(u >= -200.0f && u <= 1000.0f)) {
+            u = u < -200.0f ? -200.0f : u > 1000.0f ? 1000.0f : 0.0f;
+            rest = 0.0f;
+        }
+        g[i].x = u * kHi;
+        g[i].y = fmaf(u, kHi, -g[i].x) + fmaf(u, kLo, rest * kHi);
+        if (!(fabsf(d[i]) < INFINITY)) d[i] = NAN;
+    }
+}
 
 __device__ __forceinline__ f32x2 same2(float x) { return pack2(x, x); }
-__device__ __forceinline__ bool odd_bf16x2(uint32_t w) {  // either is not finite
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
 
 // FULL: outputs and the sequences' final states; otherwise segments' own states for the join.
 // NP: panels of 64 states.  GATED: with z.  vec_out: rows of out (and z) allow 16-byte vectors.
@@ -172,9 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         const auto init = [](uint64_t &b, int n) { mbar_init(&b, n); };
         for (int i = 0; i < 2; ++i) {
             init(sm.xb_full[i], 1);
-            init(sm.xb_free[i], FULL ? 2 + 8 * nh : 1);  // both issuers of products, and the outputs' warps
-            init(sm.gates_full[i], 1);
-            init(sm.gates_free[i], 8 * nh);
+            init(sm.xb_free[i], FULL ? 1 + 9 * nh : nh);  // the issuers of products, and the outputs' warps
+            for (int k = 0; k < 2; ++k) init(sm.gates_full[i][k], 1);
+            for (int k = 0; k < 2; ++k) init(sm.gates_free[i][k], 8);
             init(sm.m_full[i], 4);
             init(sm.m_free[i], 1);
             init(sm.w_full[i], 8);
@@ -186,10 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             for (int k = 0; k < 2; ++k) init(sm.x_ok[i][k], 8);
         }
         init(sm.c_full, 1);
-        init(sm.c_free, 2);
+        init(sm.c_free, 1);
         init(sm.cb_full, 1);
         init(sm.cb_free, 8 * nh);
-        init(sm.mx_free, 8);
         init(sm.cs_free, 8);
         init(sm.s_full, 8);
         for (uint64_t &b : sm.drain) init(b, 1);
@@ -205,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     volatile int *abort = &sm.abort;
 
     if (warp == kCopyWarp) {
-        // Copies of a chunk's tiles, then its steps and their sums; four tokens a lane.
+        // Copies of a chunk's tiles, and its steps and their sums; four tokens a lane.
         int issued = 0, c = 0;
         float raw[2][4], scale[2], bias[2];
         int head[2];
@@ -233,42 +259,41 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.xb_full[st]);
                 for (int k = 0; k < nh; ++k) tensor_load(sm.x[st][k], &maps.x, ((v0 + k) % panels) * 64, head[k], t0, &sm.xb_full[st]);
             }
+            __syncwarp();
             issued = c + 1;
-            if (c >= 2 && !wait_all(&sm.gates_free[st], (c / 2 - 1) & 1, abort)) break;
+            bool ok = true;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                if (k >= nh) break;
-                float d[4];
-                int64_t sum[4], run = 0;
+                if (k >= nh || !ok) continue;
+                float d[4] = {raw[k][0], raw[k][1], raw[k][2], raw[k][3]};
+                float2 sum[4];
+                steps_of(d, sum, bias[k], scale[k], e - t0 - lane * 4, a);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool real = t0 + lane * 4 + i < e;
-                    d[i] = real ? step_of(raw[k][i], bias[k], a) : 0.0f;
-                    // e^-200 is 0 in fp32 and e^1000 infinite: keeps the sums in range
-                    float u = d[i] * scale[k];
-                    u = u < -200.0f ? -200.0f : u > 1000.0f ? 1000.0f : u == u ? u : 0.0f;
-                    if (!(fabsf(d[i]) < INFINITY)) d[i] = NAN;
-                    constexpr float kOne = 1099511627776.0f;  // 2^40
-                    run += real ? __float2ll_rn(u * 1.4426950408889634f * kOne) : 0ll;
-                    sum[i] = run;
-                }
-                int64_t total = run;
+                for (int i = 1; i < 4; ++i) sum[i] = add_pairs(sum[i - 1], sum[i]);
+                float2 total = sum[3];
 #pragma unroll
                 for (int m = 1; m < 32; m <<= 1) {
-                    const int64_t o = __shfl_up_sync(kFullMask, total, m);
-                    if (lane >= m) total += o;
+                    const float2 o = make_float2(__shfl_up_sync(kFullMask, total.x, m), __shfl_up_sync(kFullMask, total.y, m));
+                    if (lane >= m) total = add_pairs(o, total);
                 }
-                const int64_t before = total - run;
-                Gates &g = sm.gates[st][k];
+                const float2 end = make_float2(__shfl_sync(kFullMask, total.x, 31), __shfl_sync(kFullMask, total.y, 31));
+                float2 before = make_float2(__shfl_up_sync(kFullMask, total.x, 1), __shfl_up_sync(kFullMask, total.y, 1));
+                if (lane == 0) before = make_float2(0.0f, 0.0f);
+                float weight[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float hi = __ll2float_rn(sum[i] + before);
-                    g.hi[lane * 4 + i] = hi * 0x1p-40f;
-                    g.lo[lane * 4 + i] = __ll2float_rn(sum[i] + before - __float2ll_rn(hi)) * 0x1p-40f;
-                    g.d[lane * 4 + i] = d[i];
+                    sum[i] = i < 3 ? add_pairs(before, sum[i]) : total;
+                    weight[i] = d[i] * ex2_approx((end.x - sum[i].x) + (end.y - sum[i].y));
                 }
+                if (c >= 2 && !(ok = wait_all(&sm.gates_free[st][k], (c / 2 - 1) & 1, abort))) continue;
+                Gates &g = sm.gates[st][k];
+                *reinterpret_cast<float4 *>(g.hi + lane * 4) = make_float4(sum[0].x, sum[1].x, sum[2].x, sum[3].x);
+                *reinterpret_cast<float4 *>(g.lo + lane * 4) = make_float4(sum[0].y, sum[1].y, sum[2].y, sum[3].y);
+                *reinterpret_cast<float4 *>(g.d + lane * 4) = make_float4(d[0], d[1], d[2], d[3]);
+                *reinterpret_cast<float4 *>(g.weight + lane * 4) = make_float4(weight[0], weight[1], weight[2], weight[3]);
+                warp_arrive(&sm.gates_full[st][k], lane);
             }
-            warp_arrive(&sm.gates_full[st], lane);
+            if (!ok) break;
             if (c + 1 < chunks) fetch(c + 1);
             if constexpr (FULL) {
                 if (c >= 1 && !wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
@@ -276,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     mbar_expect_tx(&sm.c_full, NP * kTile);
                     for (int i = 0; i < NP; ++i) tensor_load(sm.c[i], &maps.c, i * 64, group, t0, &sm.c_full);
                 }
+                __syncwarp();
             }
         }
         if (c < chunks) {  // gave up: let the copies land before the shared memory goes
@@ -286,12 +312,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     } else if (warp == kOutWarp) {
         if constexpr (FULL) {
             const uint32_t el = elect_lane();
-            int c = 0, k = 0;
-            for (; c < chunks; ++c) {
+            const uint32_t cc = desc_low(smem_u32(sm.c[0])), s0 = desc_low(smem_u32(sm.s[0]));
+            bool ok = true;
+            for (int c = 0; ok && c < chunks; ++c) {
                 const int st = c & 1;
-                const uint32_t b = desc_low(smem_u32(sm.b[st][0])), cc = desc_low(smem_u32(sm.c[0]));
-                if (!wait_all(&sm.xb_full[st], (c / 2) & 1, abort) || !wait_all(&sm.c_full, c & 1, abort)) break;
-                if (c >= 1 && !wait_all(&sm.cb_free, (c - 1) & 1, abort)) break;
+                const uint32_t b = desc_low(smem_u32(sm.b[st][0]));
+                ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort) && wait_all(&sm.c_full, c & 1, abort) &&
+                     (c == 0 || wait_all(&sm.cb_free, (c - 1) & 1, abort));
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 4 * NP; ++ks) {
@@ -299,77 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     mma_ss(tmem + kColCB, cc + at, b + at, mma_desc(128, 128, false), ks > 0, el);
                 }
                 mma_commit(&sm.cb_full, el);
-                mma_commit(&sm.c_free, el);
-                for (k = 0; k < nh; ++k) {
+                for (int k = 0; k < nh; ++k) {
                     const int u = c * nh + k;
                     const uint32_t x = desc_low(smem_u32(sm.x[st][k]));
-                    if (!wait_all(&sm.x_ok[st][k], (c / 2) & 1, abort)) break;
-                    if (u >= 1 && !wait_all(&sm.mx_free, (u - 1) & 1, abort)) break;
-                    int half = 0;
-                    for (; half < 2; ++half) {
-                        if (!wait_all(&sm.m_full[half], u & 1, abort)) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int part = 1; part >= 0; --part)
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_ts(tmem + kColMX, tmem + kColM + half * 64 + part * 32 + ks * 8, x + (half * 4 + ks) * 2048 / 16,
-                                       mma_desc(128, 64, true), half + (1 - part) + ks > 0, el);
-                        mma_commit(&sm.m_free[half], el);
-                    }
-                    if (half < 2) break;
-                    mma_commit(&sm.mx_full[k], el);
-                }
-                if (k < nh) break;
-                mma_commit(&sm.xb_free[st], el);
-            }
-            if (c < chunks) {  // gave up: let the products end before their memories go
-                if (el) count_error(p.err_count);
-                int quiet = 0;
-                mma_commit(&sm.drain[0], el);
-                wait_all(&sm.drain[0], 0, &quiet);
-            }
-        }
-    } else if (warp == kSumWarp) {
-        const uint32_t el = elect_lane();
-        bool ok = true;
-        for (int c = 0; ok && c < chunks; ++c) {
-            const int st = c & 1;
-            const uint32_t b = desc_low(smem_u32(sm.b[st][0])) | ((kTile / 16) << 16);  // MN-major: its panels are kTile apart
-            if (!(ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort))) break;
-            for (int q = 0; ok && q < 4; ++q)
-                for (int k = 0; k < nh; ++k) {
-                    if (!(ok = wait_all(&sm.w_full[k], q & 1, abort))) break;
-                    tc_fence_after();
-                    const uint32_t w = desc_low(smem_u32(sm.w[k][0]));
-#pragma unroll
-                    for (int part = 2; part >= 0; --part)
-#pragma unroll
-                        for (int ks = 0; ks < 2; ++ks)
-                            mma_ss(tmem + kColSum + k * 64, b + (q * 2 + ks) * 2048 / 16, w + (part * kQuarter + ks * 2048) / 16,
-                                   mma_desc(128, 64, true) | (1u << 15), q > 0 || part < 2 || ks > 0, el);
-                    mma_commit(&sm.w_free[k], el);
-                    if (q == 3) mma_commit(&sm.sum_full[k], el);
-                }
-            if (ok) mma_commit(&sm.xb_free[st], el);
-        }
-        if (!ok) {
-            if (el) count_error(p.err_count);
-            int quiet = 0;
-            mma_commit(&sm.drain[1], el);
-            wait_all(&sm.drain[1], 0, &quiet);
-        }
-    } else if (warp == kStateWarp) {
-        if constexpr (FULL) {
-            const uint32_t el = elect_lane();
-            const uint32_t cc = desc_low(smem_u32(sm.c[0])), s0 = desc_low(smem_u32(sm.s[0]));
-            bool ok = true;
-            for (int c = 0; ok && c < chunks; ++c) {
-                if (!(ok = wait_all(&sm.c_full, c & 1, abort))) break;
-                for (int k = 0; k < nh; ++k) {
-                    const int u = c * nh + k;
-                    if (!(ok = wait_all(&sm.s_full, u & 1, abort))) break;
-                    if (u >= 1 && !(ok = wait_all(&sm.cs_free, (u - 1) & 1, abort))) break;
+                    // C S, where the last outputs have left the accumulators
+                    ok = wait_all(&sm.s_full, u & 1, abort) && (u == 0 || wait_all(&sm.cs_free, (u - 1) & 1, abort));
+                    if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int part = 1; part >= 0; --part)
@@ -379,15 +342,62 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                                    mma_desc(128, 64, true), part < 1 || ks > 0, el);
                     mma_commit(&sm.cs_full[k], el);
                     mma_commit(&sm.s_free[k], el);
+                    if (k == nh - 1) mma_commit(&sm.c_free, el);
+                    // M x (what left C S's accumulators left its, too)
+                    if (!(ok = wait_all(&sm.x_ok[st][k], (c / 2) & 1, abort))) break;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (!(ok = wait_all(&sm.m_full[half], u & 1, abort))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int part = 1; part >= 0; --part)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_ts(tmem + kColMX, tmem + kColM + half * 64 + part * 32 + ks * 8, x + (half * 4 + ks) * 2048 / 16,
+                                       mma_desc(128, 64, true), half + (1 - part) + ks > 0, el);
+                        mma_commit(&sm.m_free[half], el);
+                    }
+                    if (!ok) break;
+                    mma_commit(&sm.mx_full[k], el);
                 }
-                if (ok) mma_commit(&sm.c_free, el);
+                if (ok) mma_commit(&sm.xb_free[st], el);
             }
-            if (!ok) {
+            if (!ok) {  // gave up: let the products end before their memories go
                 if (el) count_error(p.err_count);
                 int quiet = 0;
-                mma_commit(&sm.drain[2], el);
-                wait_all(&sm.drain[2], 0, &quiet);
+                mma_commit(&sm.drain[0], el);
+                wait_all(&sm.drain[0], 0, &quiet);
             }
+        }
+    } else if (warp >= kSumWarp) {
+        const int k = warp - kSumWarp;
+        const uint32_t el = elect_lane(), w = desc_low(smem_u32(sm.w[k][0]));
+        bool ok = true;
+        for (int c = 0; k < nh && ok && c < chunks; ++c) {
+            const int st = c & 1;
+            const uint32_t b = desc_low(smem_u32(sm.b[st][0])) | ((kTile / 16) << 16);  // MN-major: its panels are kTile apart
+            if (!(ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort))) break;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (!(ok = wait_all(&sm.w_full[k], q & 1, abort))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int part = 1; part >= 0; --part)
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks)
+                        mma_ss(tmem + kColSum + k * 64, b + (q * 2 + ks) * 2048 / 16, w + (part * kQuarter + ks * 2048) / 16,
+                               mma_desc(128, 64, true) | (1u << 15), q > 0 || part < 1 || ks > 0, el);
+                mma_commit(&sm.w_free[k], el);
+            }
+            if (!ok) break;
+            mma_commit(&sm.sum_full[k], el);
+            mma_commit(&sm.xb_free[st], el);
+        }
+        if (!ok) {
+            if (el) count_error(p.err_count);
+            int quiet = 0;
+            mma_commit(&sm.drain[1 + k], el);
+            wait_all(&sm.drain[1 + k], 0, &quiet);
         }
     } else if ((warp >> 3) < nh) {
         // Thread i of a warpgroup has token i and row i of the state; the warpgroup has half `hf` of head k's channels, and of M.
@@ -432,24 +442,100 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         float whole = 1.0f;  // decay over all tokens
         bool ok = true;
         int c = 0;
+        // The parts of 32 weighted tokens, and what is wrong with the tile: rows of another sequence, values that are not finite.
+        const int piece = i & 7, in = hf * 16 + (i >> 3), sw = (piece ^ (in & 7)) << 4;
+        const auto weigh = [&](int chunk, int q) {
+            if ((chunk > 0 || q > 0) && !wait_all(&sm.w_free[k], (q - 1) & 1, abort)) return false;
+            const int stage = chunk & 1, row = q * 32 + in;
+            uint4 *at = reinterpret_cast<uint4 *>(sm.x[stage][k] + row * 128 + sw);
+            uint4 x = *at;
+            const f32x2 wt = same2(sm.gates[stage][k].weight[row]);
+            if (row >= e - s - chunk * Q) {
+                x = make_uint4(0u, 0u, 0u, 0u);
+                *at = x;
+                if (k == 0) {
+                    *reinterpret_cast<uint4 *>(sm.b[stage][0] + row * 128 + sw) = x;
+                    *reinterpret_cast<uint4 *>(sm.b[stage][1] + row * 128 + sw) = x;
+                }
+            }
+            uint32_t word[4] = {x.x, x.y, x.z, x.w};
+            f32x2 f[4], odd = 0ull;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
+                odd = fma2(f[j], 0ull, odd);
+            }
+            if ((odd & 0x7fffffff7fffffffull) != 0ull) {  // 0 x is NaN
+                sm.any_bad[k] = 1;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t bits = (j & 1) ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
+                    if ((bits & 0x7f80u) != 0x7f80u) continue;
+                    atomicMin(&sm.first_bad[k][piece * 8 + j], chunk * Q + row);
+                    word[j / 2] &= (j & 1) ? 0xffffu : 0xffff0000u;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
+                *at = make_uint4(word[0], word[1], word[2], word[3]);
+            }
+            uint32_t hi[4], mid[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split_bf16x2(mul2(f[j], wt), hi[j], mid[j]);
+            *reinterpret_cast<uint4 *>(sm.w[k][0] + in * 128 + sw) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(sm.w[k][1] + in * 128 + sw) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            fence_async_shared();
+            warp_arrive(&sm.w_full[k], lane);
+            return true;
+        };
+        // M's columns of 32 tokens, from C B^T: times d_j and e^{G_i - G_j}, G counted from the first token of the warp's rows
+        // (where the decays are weak that is as exact as it needs, and where they are strong the difference is large).
+        float own = 0.0f;
+        float *since = sm.since[k][w];
+        const auto make_m = [&](const float *steps, int b) {
+            const int blk = 2 * hf + b;
+            if (blk > w) return;
+            const int limit = blk < w ? 32 : lane;
+#pragma unroll
+            for (int j0 = 0; j0 < 32; j0 += 16) {
+                float f[16];
+                tmem_load(col_cb + b * 32 + j0, f);
+                tmem_wait_load();
+                uint32_t hi[8], mid[8];
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 gj = *reinterpret_cast<const float4 *>(since + blk * 32 + j0 + j);
+                    const ulonglong2 dj = *reinterpret_cast<const ulonglong2 *>(steps + blk * 32 + j0 + j);
+                    const float at[4] = {gj.x, gj.y, gj.z, gj.w};
+                    float m[4];
+#pragma unroll
+                    for (int l = 0; l < 4; ++l) m[l] = ex2_approx(own - at[l]);
+                    unpack2(mul2(mul2(pack2(m[0], m[1]), dj.x), pack2(f[j], f[j + 1])), m[0], m[1]);
+                    unpack2(mul2(mul2(pack2(m[2], m[3]), dj.y), pack2(f[j + 2], f[j + 3])), m[2], m[3]);
+#pragma unroll
+                    for (int l = 0; l < 4; ++l) m[l] = j0 + j + l <= limit ? m[l] : 0.0f;
+                    split_bf16x2(pack2(m[0], m[1]), hi[j / 2], mid[j / 2]);
+                    split_bf16x2(pack2(m[2], m[3]), hi[j / 2 + 1], mid[j / 2 + 1]);
+                }
+                tmem_store(col_m + b * 16 + j0 / 2, hi);
+                tmem_store(col_m + 32 + b * 16 + j0 / 2, mid);
+            }
+        };
         for (; c < chunks; ++c) {
             const int stage = c & 1, u = c * nh + k, rows = min(Q, e - s - c * Q);
-            if (!(ok = wait_all(&sm.gates_full[stage], (c / 2) & 1, abort))) break;
+            if (!(ok = wait_all(&sm.gates_full[stage][k], (c / 2) & 1, abort) && wait_all(&sm.xb_full[stage], (c / 2) & 1, abort))) break;
             const Gates &g = sm.gates[stage][k];
-            const float end_hi = g.hi[Q - 1], end_lo = g.lo[Q - 1], ghi = g.hi[i], glo = g.lo[i];
-            const float gamma = ex2_approx(end_hi + end_lo);
-            float here = 0.0f, own = 0.0f, row_decay = 0.0f;
-            float *before = sm.factor[k] + 16 * w * (w - 1);
+            const float gamma = ex2_approx(g.hi[Q - 1] + g.lo[Q - 1]);
+            float row_decay = 0.0f;
+            uint8_t *xt = sm.x[stage][k];
             if constexpr (FULL) {
+                const float ghi = g.hi[i], glo = g.lo[i];
                 const float base_hi = w > 0 ? g.hi[w * 32 - 1] : 0.0f, base_lo = w > 0 ? g.lo[w * 32 - 1] : 0.0f;
-                own = (ghi - base_hi) + (glo - base_lo);  // since the warp's first token
-                here = ex2_approx(own);
+                own = (ghi - base_hi) + (glo - base_lo);
                 row_decay = ex2_approx(ghi + glo);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const int j = (2 * hf + b) * 32 + lane;
-                    if (2 * hf + b < w) before[j] = g.d[j] * ex2_approx((base_hi - g.hi[j]) + (base_lo - g.lo[j]));
-                    if (2 * hf + b == w) sm.since[k][i] = own;
+                    if (2 * hf + b <= w) since[j] = (g.hi[j] - base_hi) + (g.lo[j] - base_lo);
                 }
                 // the state's parts for C S, once the other head's (or the last chunk's) are used
                 const int from = k == 0 ? nh - 1 : 0, turn = k == 0 ? c - 1 : c;
@@ -466,101 +552,22 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 fence_async_shared();
                 warp_arrive(&sm.s_full, lane);
             }
-            // the tokens' parts, and what is wrong with the tile: rows of another sequence, values that are not finite
-            if (!(ok = wait_all(&sm.xb_full[stage], (c / 2) & 1, abort))) break;
-            uint8_t *xt = sm.x[stage][k];
-            {
-                const int piece = i & 7, in = hf * 16 + (i >> 3), sw = (piece ^ (in & 7)) << 4;
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    if ((c > 0 || q > 0) && !(ok = wait_all(&sm.w_free[k], (q - 1) & 1, abort))) break;
-                    const int row = q * 32 + in;
-                    const float wt = g.d[row] * ex2_approx((end_hi - g.hi[row]) + (end_lo - g.lo[row]));
-                    uint4 x = *reinterpret_cast<const uint4 *>(xt + row * 128 + sw);
-                    if (row >= rows) {
-                        x = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(xt + row * 128 + sw) = x;
-                        if (k == 0) {
-                            *reinterpret_cast<uint4 *>(sm.b[stage][0] + row * 128 + sw) = x;
-                            *reinterpret_cast<uint4 *>(sm.b[stage][1] + row * 128 + sw) = x;
-                        }
-                    }
-                    uint32_t word[4] = {x.x, x.y, x.z, x.w};
-                    if (odd_bf16x2(word[0]) || odd_bf16x2(word[1]) || odd_bf16x2(word[2]) || odd_bf16x2(word[3])) {
-                        sm.any_bad[k] = 1;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t bits = (j & 1) ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
-                            if ((bits & 0x7f80u) != 0x7f80u) continue;
-                            atomicMin(&sm.first_bad[k][piece * 8 + j], c * Q + row);
-                            word[j / 2] &= (j & 1) ? 0xffffu : 0xffff0000u;
-                        }
-                        *reinterpret_cast<uint4 *>(xt + row * 128 + sw) = make_uint4(word[0], word[1], word[2], word[3]);
-                    }
-                    const f32x2 wt2 = same2(wt);
-                    uint32_t part[3][4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        split_bf16x3(mul2(pack2(bf16_lo(word[j]), bf16_hi(word[j])), wt2), part[0][j], part[1][j], part[2][j]);
-#pragma unroll
-                    for (int j = 0; j < 3; ++j)
-                        *reinterpret_cast<uint4 *>(sm.w[k][j] + in * 128 + sw) = make_uint4(part[j][0], part[j][1], part[j][2], part[j][3]);
-                    fence_async_shared();
-                    warp_arrive(&sm.w_full[k], lane);
-                }
-            }
+            for (int q = 0; ok && q < 4; ++q) ok = weigh(c, q);
             if (!ok) break;
             if constexpr (FULL) {
                 warp_arrive(&sm.x_ok[stage][k], lane);
                 if (!(ok = wait_all(&sm.cb_full, c & 1, abort))) break;
                 if (u >= 1 && !(ok = wait_all(&sm.m_free[hf], (u - 1) & 1, abort))) break;
                 tc_fence_after();
-                const f32x2 here2 = same2(here);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int blk = 2 * hf + b;
-                    if (blk <= w) {
-#pragma unroll
-                        for (int j0 = 0; j0 < 32; j0 += 16) {
-                            float f[16];
-                            tmem_load(col_cb + b * 32 + j0, f);
-                            tmem_wait_load();
-                            uint32_t hi[8], mid[8];
-                            if (blk < w) {
-#pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
-                                    const ulonglong2 b2 = *reinterpret_cast<const ulonglong2 *>(before + blk * 32 + j0 + j);
-                                    split_bf16x2(mul2(mul2(pack2(f[j], f[j + 1]), b2.x), here2), hi[j / 2], mid[j / 2]);
-                                    split_bf16x2(mul2(mul2(pack2(f[j + 2], f[j + 3]), b2.y), here2), hi[j / 2 + 1], mid[j / 2 + 1]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
-                                    const float4 gj = *reinterpret_cast<const float4 *>(&sm.since[k][w * 32 + j0 + j]);
-                                    const ulonglong2 dj = *reinterpret_cast<const ulonglong2 *>(&g.d[w * 32 + j0 + j]);
-                                    const float at[4] = {gj.x, gj.y, gj.z, gj.w};
-                                    float m[4];
-#pragma unroll
-                                    for (int l = 0; l < 4; ++l) m[l] = ex2_approx(own - at[l]);
-                                    unpack2(mul2(mul2(pack2(m[0], m[1]), dj.x), pack2(f[j], f[j + 1])), m[0], m[1]);
-                                    unpack2(mul2(mul2(pack2(m[2], m[3]), dj.y), pack2(f[j + 2], f[j + 3])), m[2], m[3]);
-#pragma unroll
-                                    for (int l = 0; l < 4; ++l) m[l] = j0 + j + l <= lane ? m[l] : 0.0f;
-                                    split_bf16x2(pack2(m[0], m[1]), hi[j / 2], mid[j / 2]);
-                                    split_bf16x2(pack2(m[2], m[3]), hi[j / 2 + 1], mid[j / 2 + 1]);
-                                }
-                            }
-                            tmem_store(col_m + b * 16 + j0 / 2, hi);
-                            tmem_store(col_m + 32 + b * 16 + j0 / 2, mid);
-                        }
-                    }
-                }
+                make_m(g.d, 0);
+                make_m(g.d, 1);
                 tmem_wait_store();
                 tc_fence_before();
                 warp_arrive(&sm.m_full[hf], lane);
                 warp_arrive(&sm.cb_free, lane);
             }
-            warp_arrive(&sm.gates_free[stage], lane);
+            warp_arrive(&sm.gates_free[stage][k], lane);
 
             // S <- e^{G_Q} S + the chunk's sum
             if (!(ok = wait_all(&sm.sum_full[k], c & 1, abort))) break;
@@ -604,7 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     tmem_wait_load();
                     if (j0 == 16) {
                         tc_fence_before();
-                        warp_arrive(&sm.mx_free, lane);
                         warp_arrive(&sm.cs_free, lane);
                     }
 #pragma unroll
