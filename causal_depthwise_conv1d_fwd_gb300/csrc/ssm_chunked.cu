@@ -250,6 +250,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     raw[k][i] = t < e && k < nh ? ssm_raw_step(a, t * a.dt_stride_tok + head[k] * a.dt_stride_head) : 0.0f;
                 }
         };
+        const auto load_c = [&](int t0) {
+            if (lane == 0) {
+                mbar_expect_tx(&sm.c_full, NP * kTile);
+                for (int i = 0; i < NP; ++i) tensor_load(sm.c[i], &maps.c, i * 64, group, t0, &sm.c_full);
+            }
+            __syncwarp();
+        };
         fetch(0);
         for (; c < chunks; ++c) {
             const int st = c & 1, t0 = s + c * Q;
@@ -261,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             }
             __syncwarp();
             issued = c + 1;
+            if (FULL && c == 0) load_c(t0);
             bool ok = true;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -296,12 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             if (!ok) break;
             if (c + 1 < chunks) fetch(c + 1);
             if constexpr (FULL) {
-                if (c >= 1 && !wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
-                if (lane == 0) {
-                    mbar_expect_tx(&sm.c_full, NP * kTile);
-                    for (int i = 0; i < NP; ++i) tensor_load(sm.c[i], &maps.c, i * 64, group, t0, &sm.c_full);
+                if (c >= 1) {
+                    if (!wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
+                    load_c(t0);
                 }
-                __syncwarp();
             }
         }
         if (c < chunks) {  // gave up: let the copies land before the shared memory goes
@@ -640,11 +646,20 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                             }
                         }
                         const uint4 packed = make_uint4(f32x2_to_bf16x2(y[0]), f32x2_to_bf16x2(y[1]), f32x2_to_bf16x2(y[2]), f32x2_to_bf16x2(y[3]));
-                        if (!fast) *x = packed;  // the thread's own values, which nothing reads any more
-                        else if (i < rows && ch < width) *reinterpret_cast<uint4 *>(out + t * a.out.stride_tok + ch) = packed;
+                        *x = packed;  // the thread's own values, which nothing reads any more
                     }
                 }
-                if (!fast) {
+                if (fast) {  // four lanes a row: a store of whole rows a lane takes four times as many of L1's cycles
+                    __syncwarp();
+                    const int part = lane & 3;
+#pragma unroll
+                    for (int r8 = 0; r8 < 4; ++r8) {
+                        const int tr = w * 32 + r8 * 8 + (lane >> 2);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(xt + tr * 128 + (((hf * 4 + part) ^ (tr & 7)) << 4));
+                        if (tr < rows && part * 8 < width) *reinterpret_cast<uint4 *>(out + (t - i + tr) * a.out.stride_tok + part * 8) = v;
+                    }
+                    fence_async_shared();
+                } else {
 #pragma unroll 1
                     for (int ch = 0; i < rows && ch < width; ++ch) {
                         uint16_t f = *reinterpret_cast<const uint16_t *>(xt + i * 128 + (((hf * 4 + (ch >> 3)) ^ (i & 7)) << 4) + (ch & 7) * 2);
@@ -751,8 +766,9 @@ int launch_all(const SsmFwd &p, const Maps &maps, int vec_out, cudaStream_t stre
 bool ssm_chunked_dims(int dim_state, int a_per_state) { return !a_per_state && dim_state <= 128; }
 
 // Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device).  In
-// chunk times of a block: the first pass takes 0.6 of one a chunk, the two launches more take 4.  Each pass runs in waves of
-// one block an SM.
+// chunk times of a block (7 us): the first pass takes 0.6 of one a chunk, a block 0.8 to start and end, the two launches more 3.
+// Each pass runs in waves of one block an SM.  11027 tokens of 32 heads take 136 us so and 600 whole; 2 x 4000 of 64 heads 191
+// in two segments, 199 whole, and 222 in segments of 4 chunks.
 int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int num_groups, int head_dim) {
     const char *forced = std::getenv("CCV_SSM_SEGMENT");  // chunks of a segment (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;
@@ -761,11 +777,11 @@ int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int num_gro
     const int chunks = static_cast<int>((total_tokens + each - 1) / each);
     const int64_t blocks = static_cast<int64_t>(batch) * num_groups * ((static_cast<int64_t>(num_heads / num_groups) * ((head_dim + 63) / 64) + 1) / 2);
     auto waves = [](int64_t n) { return static_cast<double>((n + kSms - 1) / kSms); };
-    double best = waves(blocks) * chunks;
+    double best = waves(blocks) * (chunks + 0.8);
     int choice = 0;
     for (int n = 2; n <= 64 && n <= chunks; ++n) {
         const int length = (chunks + n - 1) / n;
-        const double cost = 4 + waves(blocks * (n - 1)) * length * 0.6 + waves(blocks * n) * length;
+        const double cost = 3 + waves(blocks * (n - 1)) * (length * 0.6 + 0.8) + waves(blocks * n) * (length + 0.8);
         if (cost < best) {
             best = cost;
             choice = length;
