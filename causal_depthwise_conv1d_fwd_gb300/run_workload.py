@@ -13,7 +13,7 @@ varlen (8 sequences of 1..512 tokens, dim 4096, channel-last), paged_single
 (the paged workload as one paged_sconv_fwd_with_metadata launch), many (--batch
 channel-first sequences of --tokens tokens each at --dim, all with initial state),
 linear_layer (a layer on the convolution and the operators around it: two prompts, then
-speculative rounds).
+speculative rounds), ssm_layer (the same with a selective state space layer).
 The process exits 0 after a device synchronize; it times nothing.
 """
 from __future__ import annotations
@@ -22,11 +22,11 @@ import argparse
 
 import torch
 
-from . import api, linear_layer
+from . import api, linear_layer, ssm_layer
 from . import workloads as wl
 
 PARTS = ("prefill_tokens_dim", "prefill_dim_tokens", "decode", "paged", "spec", "atrex",
-         "paged_streams", "varlen", "paged_single", "many", "linear_layer")
+         "paged_streams", "varlen", "paged_single", "many", "linear_layer", "ssm_layer")
 
 
 def _dev(kwargs, dev):
@@ -100,6 +100,8 @@ def make_launch(part: str, dev, tokens: int = 1024, dim: int = 4096, width: int 
         return lambda: launch()
     if part == "linear_layer":
         return lambda: linear_layer.serve(dev)
+    if part == "ssm_layer":
+        return lambda: ssm_layer.serve(dev)
     if part == "varlen":
         d = _dev(wl.config_varlen().kwargs(), dev)
         out = torch.empty_strided(d["x"].shape, d["x"].stride(), dtype=torch.bfloat16,
