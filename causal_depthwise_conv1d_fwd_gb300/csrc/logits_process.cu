@@ -274,7 +274,7 @@ int hash_slots(const ccv_logits_args &a) {
     while (3 * static_cast<int64_t>(slots) < 4 * tokens && slots <= kMaxSlots) slots *= 2;
     return slots <= kMaxSlots ? slots : 0;
 }
-size_t hash_bytes(int slots) { return static_cast<size_t>(slots) * 9; }
+size_t hash_bytes(int slots) { return static_cast<size_t>(slots) * 10; }  // key, entry, and a place in the list for each
 
 // A block a row, in place and without a mask.  slots: a power of two, at most three quarters of them used.
 template <bool F32>

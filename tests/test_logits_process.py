@@ -234,3 +234,33 @@ def test_drafts_are_verified_after_it(ccv):
         for i in range(kept):
             token = int(tokens[r, i])
             assert (int(d["mask"][r, i, token // 32]) >> (token % 32)) & 1 == 1
+
+
+@pytest.mark.parametrize("size", [12000, 13000, 40000])
+def test_long_histories(ccv, size):
+    """Histories around what a row's hash table takes in place, and far beyond; many different tokens, and few."""
+    d = make(2, 2, 20000, size, 15, F32, mask=False)
+    d["lengths"][:] = size
+    d["history"][0] = torch.arange(size, dtype=torch.int32) % 20000
+    check(ccv, d)
+
+
+def test_dense_and_sparse_shares(ccv):
+    """Every token of a share seen, and shares with one: both ways that a warp treats its vectors."""
+    for kind in (BF16, F32):
+        d = make(3, 2, 30000, 9000, 16, kind)
+        d["lengths"][:] = 9000
+        d["history"][0] = 8192 + torch.arange(9000, dtype=torch.int32) % 8192
+        d["history"][1] = 77
+        check(ccv, d)
+        check(ccv, {**d, "x": d["x"]}, kind=BF16 if kind is F32 else F32)
+
+
+def test_offsets_past_32_bits(ccv):
+    d = make(2, 1, 5000, 30, 17)
+    want = call(ccv, d)
+    far = torch.empty(2 ** 31 + 2 ** 20, dtype=BF16, device="cuda").as_strided((2, 1, 5000), (2 ** 31 + 64, 5000, 1))
+    far.copy_(d["x"])
+    out = torch.empty(2 ** 31 + 2 ** 20, dtype=BF16, device="cuda").as_strided((2, 1, 5000), (2 ** 31 + 64, 5000, 1))
+    assert torch.equal(call(ccv, d, logits=far, out=out), want)
+    assert torch.equal(call(ccv, d, logits=far, out=far), want)

@@ -417,3 +417,39 @@ def test_results_do_not_change_from_call_to_call(ccv):
         runs.append((ccv.ssm_fwd(*(t[k] for k in ("x", "dt", "A", "B", "C")), state, starts, D=t["D"], dt_bias=t["dt_bias"]), state))
     for out, state in runs[1:]:
         assert torch.equal(out, runs[0][0]) and torch.equal(state, runs[0][1])
+
+
+def far(shape, stride0, dtype, seed):
+    """(2, *shape) values, the second 2^31 and more elements after the first."""
+    base = torch.empty(stride0 + 2 ** 20, dtype=dtype, device="cuda")
+    inner = torch.empty(shape).stride()
+    view = base.as_strided((2, *shape), (stride0, *inner))
+    view.copy_(torch.randn(2, *shape, generator=torch.Generator().manual_seed(seed)))
+    return view
+
+
+def test_offsets_past_32_bits(ccv):
+    """State lines and rows more than 2^31 elements apart."""
+    for h, p, n, per in ((3, 64, 128, False), (70, 1, 16, True)):
+        t = cuda(make(2, h, p, 1, n, 33, per_state=per))
+        state = far((h, p, n), 2 ** 31 + 64, torch.float32, 34)
+        x = far((h, p), 2 ** 31 + 64, BF16, 35)
+        near, dense = state.clone(), x.contiguous()
+        args = (t["dt"], t["A"], t["B"], t["C"])
+        for call, tail in ((ccv.ssm_update, ()), (ccv.ssm_fwd, (torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"), None,
+                                                                torch.tensor([True, True], device="cuda")))):
+            want = call(dense, *args, near, *tail)
+            got = call(x, *args, state, *tail)
+            assert torch.equal(got, want) and torch.equal(state, near)
+        del state, x
+        torch.cuda.empty_cache()
+
+
+def test_one_chunk_of_many_sequences(ccv):
+    """More sequences than a search looks at in one step, many of them empty, in segments and whole."""
+    g = torch.Generator().manual_seed(36)
+    lengths = [int(v) for v in torch.randint(0, 40, (300,), generator=g)]
+    lengths[7] = 900
+    for heads, dim, states, per in ((2, 64, 64, False), (40, 1, 16, True)):
+        t = make(sum(lengths), heads, dim, 1, states, 37, per_state=per)
+        check_fwd(ccv, t, lengths, init=[i % 3 == 0 for i in range(300)], channels=per)
