@@ -137,7 +137,6 @@ __global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan
         const float *from = !some ? a.A : kept ? slot_at(r) : pool_at(r);
         const int64_t step = kept ? 1 : a.s_stride_state;
         const float *rates = a.A + static_cast<int64_t>(head0 + (real ? r / a.head_dim : 0)) * (PER ? a.dim_state : 1);
-        constexpr float kLog2e = 1.4426950408889634f;
 #pragma unroll
         for (int j = 0; j < NS; j += 2) {
             const int n = (j / 4) * 4 * LANES + lane * 4 + (j & 3);

@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6
     constexpr int kGroups = kSsmThreads / LANES;
     wait_prior_grid();
     release_next_grid();
-    const int slice = blockIdx.x % slices, b = blockIdx.x / slices;
+    const int b = blockIdx.x / static_cast<unsigned>(slices), slice = blockIdx.x - b * slices;
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const bool first = threadIdx.x == 0 && slice == 0;  // counts a row's error once
 
@@ -103,7 +103,14 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6
     int own_h = 0, own_ch = 0;
     {
         // one division for the first row; the others follow it
-        int h = min(first_row, rows - 1) / a.head_dim, ch = min(first_row, rows - 1) - h * a.head_dim, g = h / rep, in_group = h - g * rep;
+        int h = min(first_row, rows - 1), ch = 0, g = 0;
+        if (a.head_dim != 1) {
+            ch = h;
+            h /= a.head_dim;
+            ch -= h * a.head_dim;
+        }
+        if (a.num_groups != 1) g = h / rep;
+        int in_group = h - g * rep;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const bool use = first_row + r < rows;
@@ -128,6 +135,8 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6
                     } else {
                         load4<false>(rates, 1, d, a.dim_state, decay[r][j]);
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) decay[r][j][i] *= kLog2e;
                 }
             }
             if (first_row + r + 1 < rows && ++ch == a.head_dim) {
@@ -142,7 +151,7 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6
     }
     const int h = own_h, ch = own_ch;
     const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f, skip = a.D != nullptr ? a.D[h] : 0.0f;
-    const float rate = PER ? 0.0f : a.A[h];
+    const float rate = PER ? 0.0f : a.A[h] * kLog2e;
 
     const auto at = [&](const ccv_heads_view &v, int64_t head, int64_t dim) {
         return static_cast<const uint16_t *>(v.data) + row * v.stride_row + t0 * v.stride_tok + head * v.stride_head + dim * v.stride_dim;
@@ -154,7 +163,7 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6
     for (int t = 0; t < n; ++t) {
         const float x = bf16_bits(*xp), d = ssm_step(ssm_raw_step(a, step), bias, a);
         const float z = a.z.data != nullptr ? bf16_bits(*zp) : 0.0f;
-        const float dx = d * x, same = PER ? d : expf(d * rate);
+        const float dx = d * x, same = PER ? d : ex2_approx(d * rate);
         float y[R], bv[NV][4], cv[NV][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -171,7 +180,7 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float e = PER ? expf(e_or_d * decay[PER ? r : 0][PER ? j : 0][PER ? i : 0]) : e_or_d;
+                    const float e = PER ? ex2_approx(e_or_d * decay[PER ? r : 0][PER ? j : 0][PER ? i : 0]) : e_or_d;
                     s[r][j][i] = fmaf(e, s[r][j][i], w * bv[j][i]);
                     y[r] = fmaf(s[r][j][i], cv[j][i], y[r]);
                 }
