@@ -243,11 +243,11 @@ int launch(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
 
 template <bool PER, bool V>
 int launch_states(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
-    if (a.dim_state <= 16) return launch<4, 1, 4, PER, V>(a, rows, stream);
-    if (a.dim_state <= 32) return launch<8, 1, 4, PER, V>(a, rows, stream);
-    if (a.dim_state <= 64) return launch<8, 2, 4, PER, V>(a, rows, stream);
+    if (a.dim_state <= 16) return launch<4, 1, V ? 4 : 2, PER, V>(a, rows, stream);
+    if (a.dim_state <= 32) return launch<8, 1, V ? 4 : 2, PER, V>(a, rows, stream);
+    if (a.dim_state <= 64) return launch<8, 2, V ? 2 : 1, PER, V>(a, rows, stream);
     if (a.dim_state <= 128) return launch<8, 4, 1, PER, V>(a, rows, stream);
-    return launch<8, 8, PER ? 1 : 2, PER, V>(a, rows, stream);
+    return launch<8, 8, 1, PER, V>(a, rows, stream);
 }
 
 bool vector_ok(const ccv_ssm_args &a) {
