@@ -46,21 +46,21 @@ def _pack_ssm(x, dt, A, B, C, state, D, z, dt_bias, dt_softplus, dt_limit, pad_s
     dp, bp = _vector(dev, D, "D", _F32, h), _vector(dev, dt_bias, "dt_bias", _F32, h)
     if (D is not None and D.shape[0] != h) or (dt_bias is not None and dt_bias.shape[0] != h):
         raise ValueError(f"D and dt_bias must have {h} entries")
-    zp, zs = 0, (0,) * len(xs)
     if z is not None:
-        _need(dev, z, "z", _BF16)
+        if not isinstance(z, _Tensor) or z.dtype is not _BF16 or z.get_device() != dev:
+            _need(dev, z, "z", _BF16)
         if z.shape != xs:
             raise ValueError("z must have x's shape")
-        zp, zs = z.data_ptr(), z.stride()
     sp = lines = 0
     ss = (0, 0, 0, 0)
     if state is not None:
         if not isinstance(state, _Tensor) or state.dtype is not _F32 or state.get_device() != dev:
             _need(dev, state, "state", _F32)
-        if state.dim() < 3 or state.shape[1:] != ((h, n) if channels else (h, p, n)):
+        st = state.shape
+        if len(st) < 3 or st[1:] != ((h, n) if channels else (h, p, n)):
             raise ValueError("state must be (num_lines, heads, head_dim, dim_state), without "
                              "head_dim where x has none")
-        lines, ss, sp = state.shape[0], state.stride(), state.data_ptr()
+        lines, ss, sp = st[0], state.stride(), state.data_ptr()
         if channels:
             ss = (ss[0], ss[1], 0, ss[2])
     if out is None:
@@ -70,31 +70,26 @@ def _pack_ssm(x, dt, A, B, C, state, D, z, dt_bias, dt_softplus, dt_limit, pad_s
         if out.shape != xs:
             raise ValueError("out must have x's shape")
     lo, hi = dt_limit
-
-    def view(ptr, strides, whole):
-        """row, token, head and dim strides of a tensor with `lead` axes before the heads."""
-        if not whole:
-            strides = (*strides, 0)
-        if lead == 2:
-            return (ptr, *strides)
-        # ssm_fwd's tokens are flat (no row); a row of ssm_update has one token
-        return (ptr, strides[0], strides[0], strides[1], strides[2])
-
-    ds = dt.stride()
-    ds = ds if lead == 2 else (ds[0], ds[0], ds[1])
-    packed = _SSM.pack(*view(x.data_ptr(), x.stride(), not channels), *view(zp, zs, not channels),
-                       *view(out.data_ptr(), out.stride(), not channels),
-                       *view(B.data_ptr(), B.stride(), True), *view(C.data_ptr(), C.stride(), True),
-                       dt.data_ptr(), *ds, A.data_ptr(), dp or 0, bp or 0, sp, *ss, lo, hi,
-                       1 if dt.dtype is _F32 else 0, 1 if dt_softplus else 0, 1 if per_state else 0,
-                       lines, h, g, p, n, pad_slot_id)
+    # row, token, head and dim strides: ssm_fwd's tokens are flat (no row), and a row of ssm_update
+    # has one token, or as many as there are
+    v, o, b, c, d = x.stride(), out.stride(), B.stride(), C.stride(), dt.stride()
+    w = z.stride() if z is not None else v
+    if lead == 1:
+        v, w, o, b, c, d = ((t[0], *t) for t in (v, w, o, b, c, d))
+    if channels:
+        v, w, o = (*v, 0), (*w, 0), (*o, 0)
+    packed = _SSM.pack(x.data_ptr(), *v, 0 if z is None else z.data_ptr(), *w, out.data_ptr(), *o,
+                       B.data_ptr(), *b, C.data_ptr(), *c, dt.data_ptr(), *d, A.data_ptr(), dp or 0,
+                       bp or 0, sp, *ss, lo, hi, 1 if dt.dtype is _F32 else 0,
+                       1 if dt_softplus else 0, 1 if per_state else 0, lines, h, g, p, n,
+                       pad_slot_id)
     return dev, packed, out, (h, g, p, n, 1 if per_state else 0)
 
 
-def _mapped(t: torch.Tensor, channels: bool = False) -> bool:
+def _mapped(t: torch.Tensor) -> bool:
     """Whether the chunked form reads a (tokens, heads, dim) tensor as it is (ssm_fwd_workspace)."""
     st = t.stride()
-    return (not channels and st[2] == 1 and t.data_ptr() % 16 == 0 and st[0] > 0 and st[0] % 8 == 0
+    return (st[2] == 1 and t.data_ptr() % 16 == 0 and st[0] > 0 and st[0] % 8 == 0
             and (t.shape[1] == 1 or (st[1] > 0 and st[1] % 8 == 0)))
 
 
@@ -159,11 +154,13 @@ def _marshal_fwd(x, dt, A, B, C, state, query_start_loc, cache_indices, has_init
         if hi.dtype not in (torch.bool, _U8):
             raise TypeError("has_initial_state must be bool or uint8")
         hi = _vector(dev, hi, "has_initial_state", hi.dtype, batch)
-    copies = not (_mapped(x, x.dim() == 2) and _mapped(B) and _mapped(C))
+    copies = x.dim() == 2 or not (_mapped(x) and _mapped(B) and _mapped(C))
     size = _lib.load().ssm_fwd_workspace(total, batch, *sizes, 1 if copies else 0)
-    scratch = _workspace(dev, workspace, size, x)
-    args = (packed, qsl, batch, ci, hi, total, scratch.data_ptr(), scratch.shape[0],
-            _err(dev, err_count))
+    scratch, sp, room = workspace, 0, 0
+    if size or workspace is not None:
+        scratch = _workspace(dev, workspace, size, x)
+        sp, room = scratch.data_ptr(), scratch.shape[0]
+    args = (packed, qsl, batch, ci, hi, total, sp, room, _err(dev, err_count))
     keep = (x, dt, A, B, C, state, query_start_loc, cache_indices, has_initial_state, D, z, dt_bias,
             out, scratch, err_count)
     return dev, args, out, scratch, keep
