@@ -88,6 +88,9 @@ __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
+// Quarters (32 tokens) of a chunk with `rows` tokens from its start on to the sequence's end; the others are left out.
+__device__ __forceinline__ int quarters_of(int rows) { return min(4, (rows + 31) / 32); }
+
 // The warp's own arrival, after all its lanes are done.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     __syncwarp();
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             const uint32_t cc = desc_low(smem_u32(sm.c[0])), s0 = desc_low(smem_u32(sm.s[0]));
             bool ok = true;
             for (int c = 0; ok && c < chunks; ++c) {
-                const int st = c & 1;
+                const int st = c & 1, quarters = quarters_of(e - s - c * Q);
                 const uint32_t b = desc_low(smem_u32(sm.b[st][0]));
                 ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort) && wait_all(&sm.c_full, c & 1, abort) &&
                      (c == 0 || wait_all(&sm.cb_free, (c - 1) & 1, abort));
@@ -359,8 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                         for (int part = 1; part >= 0; --part)
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                mma_ts(tmem + kColMX, tmem + kColM + half * 64 + part * 32 + ks * 8, x + (half * 4 + ks) * 2048 / 16,
-                                       mma_desc(128, 64, true), half + (1 - part) + ks > 0, el);
+                                if (half * 4 + ks < 2 * quarters)
+                                    mma_ts(tmem + kColMX, tmem + kColM + half * 64 + part * 32 + ks * 8, x + (half * 4 + ks) * 2048 / 16,
+                                           mma_desc(128, 64, true), half + (1 - part) + ks > 0, el);
                         mma_commit(&sm.m_free[half], el);
                     }
                     if (!ok) break;
@@ -380,12 +384,12 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         const uint32_t el = elect_lane(), w = desc_low(smem_u32(sm.w[k][0]));
         bool ok = true;
         for (int c = 0; k < nh && ok && c < chunks; ++c) {
-            const int st = c & 1;
+            const int st = c & 1, quarters = quarters_of(e - s - c * Q);
             const uint32_t b = desc_low(smem_u32(sm.b[st][0])) | ((kTile / 16) << 16);  // MN-major: its panels are kTile apart
             if (!(ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort))) break;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if (!(ok = wait_all(&sm.w_full[k], q & 1, abort))) break;
+                if (q >= quarters || !(ok = wait_all(&sm.w_full[k], q & 1, abort))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int part = 1; part >= 0; --part)
@@ -497,9 +501,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         // (where the decays are weak that is as exact as it needs, and where they are strong the difference is large).
         float own = 0.0f;
         float *since = sm.since[k][w];
-        const auto make_m = [&](const float *steps, int b) {
+        const auto make_m = [&](const float *steps, int b, int quarters) {
             const int blk = 2 * hf + b;
-            if (blk > w) return;
+            if (blk > w || blk >= quarters) return;
             const int limit = blk < w ? 32 : lane;
 #pragma unroll
             for (int j0 = 0; j0 < 32; j0 += 16) {
@@ -527,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             }
         };
         for (; c < chunks; ++c) {
-            const int stage = c & 1, u = c * nh + k, rows = min(Q, e - s - c * Q);
+            const int stage = c & 1, u = c * nh + k, rows = min(Q, e - s - c * Q), quarters = quarters_of(rows);
             if (!(ok = wait_all(&sm.gates_full[stage][k], (c / 2) & 1, abort) && wait_all(&sm.xb_full[stage], (c / 2) & 1, abort))) break;
             const Gates &g = sm.gates[stage][k];
             const float gamma = ex2_approx(g.hi[Q - 1] + g.lo[Q - 1]);
@@ -559,15 +563,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 warp_arrive(&sm.s_full, lane);
             }
 #pragma unroll 1
-            for (int q = 0; ok && q < 4; ++q) ok = weigh(c, q);
+            for (int q = 0; ok && q < quarters; ++q) ok = weigh(c, q);
             if (!ok) break;
             if constexpr (FULL) {
                 warp_arrive(&sm.x_ok[stage][k], lane);
                 if (!(ok = wait_all(&sm.cb_full, c & 1, abort))) break;
                 if (u >= 1 && !(ok = wait_all(&sm.m_free[hf], (u - 1) & 1, abort))) break;
                 tc_fence_after();
-                make_m(g.d, 0);
-                make_m(g.d, 1);
+                make_m(g.d, 0, quarters);
+                make_m(g.d, 1, quarters);
                 tmem_wait_store();
                 tc_fence_before();
                 warp_arrive(&sm.m_full[hf], lane);
