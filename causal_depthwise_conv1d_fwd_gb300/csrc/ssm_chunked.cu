@@ -5,14 +5,15 @@
 //     y_i = e^{G_i} C_i S + sum_{j <= i} M_ij x_j,   M_ij = (C_i . B_j) e^{G_i - G_j} d_j
 //     S  <- e^{G_Q} S + sum_j B_j^T (e^{G_Q - G_j} d_j x_j)
 // and C B^T is the same for all heads of a group.  Nothing but S is sequential, and S only by its own multiply-add, so all
-// products of a chunk run beside those of its neighbours.  A block has two heads of a group of one sequence (or segment) and
-// goes through its chunks with four warpgroups, two a head, which all run the same code on a half each:
-//   M from C B^T (tensor memory to tensor memory), 64 of its columns;
-//   the state in registers (thread n has half of row n), its parts to shared memory for C S, and its multiply-add;
-//   the weighted tokens' parts for the state's sum; and the outputs, 32 channels.
-// Four more warps copy tiles and sum the steps, and issue products: what leads to the outputs, and each head's sum for the state.
-// Heads wider than 64 are cut into panels of 64 that share steps and decays.  With a role a warpgroup the hot instructions were
-// twice as many and missed the instruction cache: a third of all stalls.
+// products of a chunk run beside those of its neighbours.  A block has a head of one sequence (or segment) and goes through its
+// chunks with four warpgroups that all run the same code on a quarter each:
+//   the state in registers (thread n has 16 channels of row n), its parts to shared memory for C S, and its multiply-add;
+//   the weighted tokens' parts for the state's sum; M from C B^T (tensor memory to tensor memory), 32 of its columns; and the
+//   outputs, 16 channels.
+// Three more warps copy tiles and sum the steps, issue what leads to the outputs, and issue the sum for the state.
+// Heads wider than 64 are cut into panels of 64.  With a role a warpgroup the hot instructions were twice as many and missed the
+// instruction cache, a third of all stalls; with two heads a block, two warpgroups each, the registers for twice the state left
+// too few to overlap M's arithmetic.
 //
 // Precision.  Every operand that is not bf16 from the start (M, the state in C S, the weighted tokens) enters the tensor cores as
 // two bf16 parts, which hold 16 bits of it: 2^-17 of each term of a sum whose other factors, x, B and C, are exact.  Sums and the
@@ -37,10 +38,10 @@ namespace {
 
 constexpr int Q = 128;              // tokens of a chunk
 constexpr int kTile = Q * 128;      // bytes of 128 rows of 64 bf16 values
-constexpr int kQuarter = kTile / 4; // of 32 rows
 constexpr int kThreads = 640;
-constexpr int kCopyWarp = 16, kOutWarp = 17, kSumWarp = 18;  // the last has one warp a head
-// Columns of tensor memory: C B^T; M in two halves of 64 tokens, each in two parts; M x; C S; the heads' sums for the state.
+constexpr int kCompute = 16;  // warps that compute; the others:
+constexpr int kCopyWarp = kCompute, kOutWarp = kCompute + 1, kSumWarp = kCompute + 2;
+// Columns of tensor memory: C B^T; M in two halves of 64 tokens, each in two parts; M x; C S; the sum for the state.
 constexpr uint32_t kColCB = 0, kColM = 128, kColMX = 256, kColCS = 320, kColSum = 384;
 constexpr int kStateFloats = 128 * 64;  // of a head's panel in the workspace
 
@@ -48,25 +49,24 @@ struct Maps {
     CUtensorMap x, b, c;
 };
 
-struct Gates {  // of a chunk's tokens and a head: G log2(e) as a pair of floats, the steps, and e^{G_Q - G_j} d_j
+struct Gates {  // of a chunk's tokens: G log2(e) as a pair of floats, the steps, and e^{G_Q - G_j} d_j
     float hi[Q], lo[Q], d[Q], weight[Q];
 };
 
 struct Smem {
-    uint8_t x[2][2][kTile];     // stage, head
+    uint8_t x[2][kTile];        // stage
     uint8_t b[2][2][kTile];     // stage, panel of 64 states
     uint8_t c[2][kTile];        // panel
-    uint8_t w[2][2][kQuarter];  // head, part: weighted tokens, 32 at a time
-    uint8_t s[2][kTile];        // part: the state of the head whose turn it is
-    Gates gates[2][2];          // stage, head
-    float since[2][4][Q];       // head, 32 rows of M: G of the tokens up to them, counted from the rows' first
-    // A barrier's phase is waited for by the same threads each time, or by ones that know the phase before it to be over: a wait
-    // tells a phase from the next one only.
-    uint64_t xb_full[2], xb_free[2], c_full, c_free, gates_full[2][2], gates_free[2][2];
-    uint64_t cb_full, cb_free, m_full[2], m_free[2], mx_full[2], cs_full[2], cs_free, s_full, s_free[2];
-    uint64_t w_full[2], w_free[2], sum_full[2], x_ok[2][2], drain[3];
-    int first_bad[2][64];       // head, channel: the first of the block's tokens whose x is not finite
-    int any_bad[2];
+    uint8_t w[2][kTile];        // part: weighted tokens
+    uint8_t s[2][kTile];        // part: the state
+    Gates gates[2];             // stage
+    float since[4][Q];          // 32 rows of M: G of the tokens up to them, counted from the rows' first
+    // What the compute warps produce in a chunk they produce again once all of them are past the products that read it, which
+    // each knows from its own waits; so only what is made ahead has a barrier for its way back.
+    uint64_t xb_full[2], xb_free[2], c_full, c_free, gates_full[2], gates_free[2];
+    uint64_t cb_full, cb_free, m_full[2], mx_full, cs_full, s_full, w_full[2], sum_full, x_ok, drain[2];
+    int first_bad[64];          // channel: the first of the block's tokens whose x is not finite
+    int any_bad;
     int seq, start, end, abort;
     uint32_t tmem;
 };
@@ -139,11 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const ccv_ssm_args &a = p.a;
     const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
-    const int panels = (a.head_dim + 63) / 64, rep = a.num_heads / a.num_groups;
-    const int per_group = (rep * panels + 1) / 2, pairs = a.num_groups * per_group;
-    const int unit = blockIdx.x / pairs, pair = blockIdx.x % pairs;
-    const int group = pair / per_group, v0 = (pair % per_group) * 2;  // first panel of the pair, within the group
-    const int nh = min(2, rep * panels - v0);
+    const int panels = (a.head_dim + 63) / 64, all = a.num_heads * panels;
+    const int unit = blockIdx.x / all, v = blockIdx.x % all;  // panel among all panels of all heads
+    const int h = v / panels, panel = v % panels, group = h / (a.num_heads / a.num_groups);
     wait_prior_grid();
     release_next_grid();
     if ((smem_u32(smem_raw) & 1023u) != 0) {  // swizzled tiles need it
@@ -172,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         s = p.query_start_loc[seq];
         e = p.query_start_loc[seq + 1];
     }
-    const bool told = tid == 0 && pair == 0 && FULL;  // counts a sequence's error
+    const bool told = tid == 0 && v == 0 && FULL;  // counts a sequence's error
     if (!sequence_ok(s, e, p.total_tokens)) {
         if (told) count_error(p.err_count);
         return;
@@ -198,34 +196,29 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     const int chunks = (e - s + Q - 1) / Q;
 
     if (tid == 0) {
-        sm.abort = 0;
+        sm.abort = sm.any_bad = 0;
         const auto init = [](uint64_t &b, int n) { mbar_init(&b, n); };
         for (int i = 0; i < 2; ++i) {
             init(sm.xb_full[i], 1);
-            init(sm.xb_free[i], FULL ? 1 + 9 * nh : nh);  // the issuers of products, and the outputs' warps
-            for (int k = 0; k < 2; ++k) init(sm.gates_full[i][k], 1);
-            for (int k = 0; k < 2; ++k) init(sm.gates_free[i][k], 8);
-            init(sm.m_full[i], 4);
-            init(sm.m_free[i], 1);
-            init(sm.w_full[i], 8);
-            init(sm.w_free[i], 1);
-            init(sm.sum_full[i], 1);
-            init(sm.mx_full[i], 1);
-            init(sm.cs_full[i], 1);
-            init(sm.s_free[i], 1);
-            for (int k = 0; k < 2; ++k) init(sm.x_ok[i][k], 8);
+            init(sm.xb_free[i], FULL ? 2 + kCompute : 1);  // the issuers of products, and the outputs' warps
+            init(sm.gates_full[i], 1);
+            init(sm.gates_free[i], kCompute);
+            init(sm.m_full[i], kCompute / 2);
+            init(sm.w_full[i], kCompute);
+            init(sm.drain[i], 1);
         }
         init(sm.c_full, 1);
         init(sm.c_free, 1);
         init(sm.cb_full, 1);
-        init(sm.cb_free, 8 * nh);
-        init(sm.cs_free, 8);
-        init(sm.s_full, 8);
-        for (uint64_t &b : sm.drain) init(b, 1);
+        init(sm.cb_free, kCompute);
+        init(sm.mx_full, 1);
+        init(sm.cs_full, 1);
+        init(sm.s_full, kCompute);
+        init(sm.sum_full, 1);
+        init(sm.x_ok, kCompute);
         mbar_init_fence();
     }
-    if (tid < 128) sm.first_bad[tid >> 6][tid & 63] = INT_MAX;
-    if (tid < 2) sm.any_bad[tid] = 0;
+    if (tid < 64) sm.first_bad[tid] = INT_MAX;
     if (warp == kCopyWarp) tmem_alloc<512>(&sm.tmem);
     tc_fence_before();
     __syncthreads();
@@ -236,22 +229,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     if (warp == kCopyWarp) {
         // Copies of a chunk's tiles, and its steps and their sums; four tokens a lane.
         int issued = 0, c = 0;
-        float raw[2][4], scale[2], bias[2];
-        int head[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            head[k] = group * rep + min(v0 + k, rep * panels - 1) / panels;
-            scale[k] = a.A[head[k]];
-            bias[k] = a.dt_bias != nullptr ? a.dt_bias[head[k]] : 0.0f;
-        }
+        float raw[4];
+        const float scale = a.A[h], bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
         const auto fetch = [&](int chunk) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = s + chunk * Q + lane * 4 + i;
-                    raw[k][i] = t < e && k < nh ? ssm_raw_step(a, t * a.dt_stride_tok + head[k] * a.dt_stride_head) : 0.0f;
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int t = s + chunk * Q + lane * 4 + i;
+                raw[i] = t < e ? ssm_raw_step(a, t * a.dt_stride_tok + h * a.dt_stride_head) : 0.0f;
+            }
         };
         const auto load_c = [&](int t0) {
             if (lane == 0) {
@@ -265,58 +250,50 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             const int st = c & 1, t0 = s + c * Q;
             if (c >= 2 && !wait_all(&sm.xb_free[st], (c / 2 - 1) & 1, abort)) break;
             if (lane == 0) {
-                mbar_expect_tx(&sm.xb_full[st], (2 + nh) * kTile);
+                mbar_expect_tx(&sm.xb_full[st], 3 * kTile);
+                tensor_load(sm.x[st], &maps.x, panel * 64, h, t0, &sm.xb_full[st]);
                 for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.xb_full[st]);
-                for (int k = 0; k < nh; ++k) tensor_load(sm.x[st][k], &maps.x, ((v0 + k) % panels) * 64, head[k], t0, &sm.xb_full[st]);
             }
             __syncwarp();
             issued = c + 1;
             if (FULL && c == 0) load_c(t0);
-            bool ok = true;
+            float d[4] = {raw[0], raw[1], raw[2], raw[3]};
+            float2 sum[4];
+            steps_of(d, sum, bias, scale, e - t0 - lane * 4, a);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (k >= nh || !ok) continue;
-                float d[4] = {raw[k][0], raw[k][1], raw[k][2], raw[k][3]};
-                float2 sum[4];
-                steps_of(d, sum, bias[k], scale[k], e - t0 - lane * 4, a);
+            for (int i = 1; i < 4; ++i) sum[i] = add_pairs(sum[i - 1], sum[i]);
+            float2 total = sum[3];
 #pragma unroll
-                for (int i = 1; i < 4; ++i) sum[i] = add_pairs(sum[i - 1], sum[i]);
-                float2 total = sum[3];
-#pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const float2 o = make_float2(__shfl_up_sync(kFullMask, total.x, m), __shfl_up_sync(kFullMask, total.y, m));
-                    if (lane >= m) total = add_pairs(o, total);
-                }
-                const float2 end = make_float2(__shfl_sync(kFullMask, total.x, 31), __shfl_sync(kFullMask, total.y, 31));
-                float2 before = make_float2(__shfl_up_sync(kFullMask, total.x, 1), __shfl_up_sync(kFullMask, total.y, 1));
-                if (lane == 0) before = make_float2(0.0f, 0.0f);
-                float weight[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sum[i] = i < 3 ? add_pairs(before, sum[i]) : total;
-                    weight[i] = d[i] * ex2_approx((end.x - sum[i].x) + (end.y - sum[i].y));
-                }
-                if (c >= 2 && !(ok = wait_all(&sm.gates_free[st][k], (c / 2 - 1) & 1, abort))) continue;
-                Gates &g = sm.gates[st][k];
-                *reinterpret_cast<float4 *>(g.hi + lane * 4) = make_float4(sum[0].x, sum[1].x, sum[2].x, sum[3].x);
-                *reinterpret_cast<float4 *>(g.lo + lane * 4) = make_float4(sum[0].y, sum[1].y, sum[2].y, sum[3].y);
-                *reinterpret_cast<float4 *>(g.d + lane * 4) = make_float4(d[0], d[1], d[2], d[3]);
-                *reinterpret_cast<float4 *>(g.weight + lane * 4) = make_float4(weight[0], weight[1], weight[2], weight[3]);
-                warp_arrive(&sm.gates_full[st][k], lane);
+            for (int m = 1; m < 32; m <<= 1) {
+                const float2 o = make_float2(__shfl_up_sync(kFullMask, total.x, m), __shfl_up_sync(kFullMask, total.y, m));
+                if (lane >= m) total = add_pairs(o, total);
             }
-            if (!ok) break;
+            const float2 end = make_float2(__shfl_sync(kFullMask, total.x, 31), __shfl_sync(kFullMask, total.y, 31));
+            float2 before = make_float2(__shfl_up_sync(kFullMask, total.x, 1), __shfl_up_sync(kFullMask, total.y, 1));
+            if (lane == 0) before = make_float2(0.0f, 0.0f);
+            float weight[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum[i] = i < 3 ? add_pairs(before, sum[i]) : total;
+                weight[i] = d[i] * ex2_approx((end.x - sum[i].x) + (end.y - sum[i].y));
+            }
+            if (c >= 2 && !wait_all(&sm.gates_free[st], (c / 2 - 1) & 1, abort)) break;
+            Gates &g = sm.gates[st];
+            *reinterpret_cast<float4 *>(g.hi + lane * 4) = make_float4(sum[0].x, sum[1].x, sum[2].x, sum[3].x);
+            *reinterpret_cast<float4 *>(g.lo + lane * 4) = make_float4(sum[0].y, sum[1].y, sum[2].y, sum[3].y);
+            *reinterpret_cast<float4 *>(g.d + lane * 4) = make_float4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<float4 *>(g.weight + lane * 4) = make_float4(weight[0], weight[1], weight[2], weight[3]);
+            warp_arrive(&sm.gates_full[st], lane);
             if (c + 1 < chunks) fetch(c + 1);
-            if constexpr (FULL) {
-                if (c >= 1) {
-                    if (!wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
-                    load_c(t0);
-                }
+            if (FULL && c >= 1) {
+                if (!wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
+                load_c(t0);
             }
         }
         if (c < chunks) {  // gave up: let the copies land before the shared memory goes
             int quiet = 0;
             for (int i = max(0, issued - 2); i < issued; ++i) wait_all(&sm.xb_full[i & 1], (i / 2) & 1, &quiet);
-            if (FULL && c > 0) wait_all(&sm.c_full, (c - 1) & 1, &quiet);
+            if (FULL) wait_all(&sm.c_full, max(0, c - 1) & 1, &quiet);
         }
     } else if (warp == kOutWarp) {
         if constexpr (FULL) {
@@ -325,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             bool ok = true;
             for (int c = 0; ok && c < chunks; ++c) {
                 const int st = c & 1, quarters = quarters_of(e - s - c * Q);
-                const uint32_t b = desc_low(smem_u32(sm.b[st][0]));
+                const uint32_t b = desc_low(smem_u32(sm.b[st][0])), x = desc_low(smem_u32(sm.x[st]));
+                // C B^T
                 ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort) && wait_all(&sm.c_full, c & 1, abort) &&
                      (c == 0 || wait_all(&sm.cb_free, (c - 1) & 1, abort));
                 if (!ok) break;
@@ -336,41 +314,34 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     mma_ss(tmem + kColCB, cc + at, b + at, mma_desc(128, 128, false), ks > 0, el);
                 }
                 mma_commit(&sm.cb_full, el);
-                for (int k = 0; k < nh; ++k) {
-                    const int u = c * nh + k;
-                    const uint32_t x = desc_low(smem_u32(sm.x[st][k]));
-                    // C S, where the last outputs have left the accumulators
-                    ok = wait_all(&sm.s_full, u & 1, abort) && (u == 0 || wait_all(&sm.cs_free, (u - 1) & 1, abort));
-                    if (!ok) break;
+                // C S: all warps have left the last outputs behind them
+                if (!(ok = wait_all(&sm.s_full, c & 1, abort))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int part = 1; part >= 0; --part)
+#pragma unroll
+                    for (int ks = 0; ks < 4 * NP; ++ks)
+                        mma_ss(tmem + kColCS, cc + ((ks / 4) * kTile + (ks % 4) * 32) / 16, s0 + (part * kTile + ks * 2048) / 16,
+                               mma_desc(128, 64, true), part < 1 || ks > 0, el);
+                mma_commit(&sm.cs_full, el);
+                mma_commit(&sm.c_free, el);
+                // M x
+                if (!(ok = wait_all(&sm.x_ok, c & 1, abort))) break;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = wait_all(&sm.m_full[half], c & 1, abort))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int part = 1; part >= 0; --part)
 #pragma unroll
-                        for (int ks = 0; ks < 4 * NP; ++ks)
-                            mma_ss(tmem + kColCS, cc + ((ks / 4) * kTile + (ks % 4) * 32) / 16, s0 + (part * kTile + ks * 2048) / 16,
-                                   mma_desc(128, 64, true), part < 1 || ks > 0, el);
-                    mma_commit(&sm.cs_full[k], el);
-                    mma_commit(&sm.s_free[k], el);
-                    if (k == nh - 1) mma_commit(&sm.c_free, el);
-                    // M x (what left C S's accumulators left its, too)
-                    if (!(ok = wait_all(&sm.x_ok[st][k], (c / 2) & 1, abort))) break;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (!(ok = wait_all(&sm.m_full[half], u & 1, abort))) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int part = 1; part >= 0; --part)
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                if (half * 4 + ks < 2 * quarters)
-                                    mma_ts(tmem + kColMX, tmem + kColM + half * 64 + part * 32 + ks * 8, x + (half * 4 + ks) * 2048 / 16,
-                                           mma_desc(128, 64, true), half + (1 - part) + ks > 0, el);
-                        mma_commit(&sm.m_free[half], el);
-                    }
-                    if (!ok) break;
-                    mma_commit(&sm.mx_full[k], el);
+                        for (int ks = 0; ks < 4; ++ks)
+                            if (half * 4 + ks < 2 * quarters)
+                                mma_ts(tmem + kColMX, tmem + kColM + half * 64 + part * 32 + ks * 8, x + (half * 4 + ks) * 2048 / 16,
+                                       mma_desc(128, 64, true), half + (1 - part) + ks > 0, el);
                 }
-                if (ok) mma_commit(&sm.xb_free[st], el);
+                if (!ok) break;
+                mma_commit(&sm.mx_full, el);
+                mma_commit(&sm.xb_free[st], el);
             }
             if (!ok) {  // gave up: let the products end before their memories go
                 if (el) count_error(p.err_count);
@@ -379,56 +350,51 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 wait_all(&sm.drain[0], 0, &quiet);
             }
         }
-    } else if (warp >= kSumWarp) {
-        const int k = warp - kSumWarp;
-        const uint32_t el = elect_lane(), w = desc_low(smem_u32(sm.w[k][0]));
+    } else if (warp == kSumWarp) {
+        const uint32_t el = elect_lane(), w = desc_low(smem_u32(sm.w[0]));
         bool ok = true;
-        for (int c = 0; k < nh && ok && c < chunks; ++c) {
-            const int st = c & 1, quarters = quarters_of(e - s - c * Q);
+        for (int c = 0; ok && c < chunks; ++c) {
+            const int st = c & 1, rows = e - s - c * Q;
             const uint32_t b = desc_low(smem_u32(sm.b[st][0])) | ((kTile / 16) << 16);  // MN-major: its panels are kTile apart
             if (!(ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort))) break;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (q >= quarters || !(ok = wait_all(&sm.w_full[k], q & 1, abort))) break;
+            for (int half = 0; half < 2; ++half) {
+                if (half * 64 >= rows || !(ok = wait_all(&sm.w_full[half], c & 1, abort))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int part = 1; part >= 0; --part)
 #pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-                        mma_ss(tmem + kColSum + k * 64, b + (q * 2 + ks) * 2048 / 16, w + (part * kQuarter + ks * 2048) / 16,
-                               mma_desc(128, 64, true) | (1u << 15), q > 0 || part < 1 || ks > 0, el);
-                mma_commit(&sm.w_free[k], el);
+                    for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                        mma_ss(tmem + kColSum, b + ks * 2048 / 16, w + (part * kTile + ks * 2048) / 16, mma_desc(128, 64, true) | (1u << 15),
+                               half > 0 || part < 1 || ks > 0, el);
             }
             if (!ok) break;
-            mma_commit(&sm.sum_full[k], el);
+            mma_commit(&sm.sum_full, el);
             mma_commit(&sm.xb_free[st], el);
         }
         if (!ok) {
             if (el) count_error(p.err_count);
             int quiet = 0;
-            mma_commit(&sm.drain[1 + k], el);
-            wait_all(&sm.drain[1 + k], 0, &quiet);
+            mma_commit(&sm.drain[1], el);
+            wait_all(&sm.drain[1], 0, &quiet);
         }
-    } else if ((warp >> 3) < nh) {
-        // Thread i of a warpgroup has token i and row i of the state; the warpgroup has half `hf` of head k's channels, and of M.
-        const int k = warp >> 3, hf = (warp >> 2) & 1, w = warp & 3, i = tid & 127;
+    } else if (warp < kCompute) {
+        // Thread i of a warpgroup has token i and row i of the state; the warpgroup has 16 channels, and 32 of M's columns.
+        const int qd = warp >> 2, w = warp & 3, i = tid & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
-        const uint32_t col_cb = lanes + kColCB + hf * 64, col_m = lanes + kColM + hf * 64, col_sum = lanes + kColSum + k * 64 + hf * 32;
-        const uint32_t col_mx = lanes + kColMX + hf * 32, col_cs = lanes + kColCS + hf * 32;
-        const int h = group * rep + (v0 + k) / panels, panel = (v0 + k) % panels;
-        const int first = panel * 64 + hf * 32, width = max(0, min(32, a.head_dim - first));  // channels of the head
-        const int64_t v = static_cast<int64_t>(group) * rep * panels + v0 + k;                // among all panels of all heads
+        const uint32_t col_m = lanes + kColM + (qd >> 1) * 64 + (qd & 1) * 16;
+        const int first = panel * 64 + qd * 16, width = max(0, min(16, a.head_dim - first));  // channels of the head
         float *pool = a.state != nullptr ? a.state + line * a.s_stride_line + h * a.s_stride_head + first * a.s_stride_dim + i * a.s_stride_state
                                          : nullptr;
-        float *slot = p.seg_chunks > 0 ? p.seg_state + (unit * static_cast<int64_t>(a.num_heads) * panels + v) * kStateFloats + hf * 32 * 128 + i : nullptr;
-        f32x2 st2[16];  // two channels each
+        float *slot = p.seg_chunks > 0 ? p.seg_state + (unit * static_cast<int64_t>(all) + v) * kStateFloats + qd * 16 * 128 + i : nullptr;
+        f32x2 st2[8];  // two channels each
         {
             const bool kept = FULL && segments > 1, init = a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
             const float *from = kept ? slot : pool;
             const int64_t step = kept ? 128 : a.s_stride_dim;
-            const int count = kept ? 32 : FULL && init && i < a.dim_state ? width : 0;
+            const int count = kept ? 16 : FULL && init && i < a.dim_state ? width : 0;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 float f[2];
 #pragma unroll
                 for (int l = 0; l < 2; ++l) f[l] = 2 * j + l < count ? from[(2 * j + l) * step] : 0.0f;
@@ -439,239 +405,214 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         uint16_t *out = static_cast<uint16_t *>(const_cast<void *>(a.out.data)) + h * a.out.stride_head + first * a.out.stride_dim;
         const uint16_t *z = static_cast<const uint16_t *>(a.z.data) + h * a.z.stride_head + first * a.z.stride_dim;
         // M's columns of tokens after a warp's own are zero, and nothing writes them again.
-        if constexpr (FULL) {
+        if (FULL && qd > w) {
             const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-                if (k == 0 && 2 * hf + b > w) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) tmem_store(col_m + (j & 1) * 32 + b * 16 + (j >> 1) * 8, none);
-                }
+            for (int j = 0; j < 4; ++j) tmem_store(col_m + (j & 1) * 32 + (j >> 1) * 8, none);
             tmem_wait_store();
         }
         float whole = 1.0f;  // decay over all tokens
         bool ok = true;
         int c = 0;
-        // The parts of 32 weighted tokens, and what is wrong with the tile: rows of another sequence, values that are not finite.
-        const int piece = i & 7, in = hf * 16 + (i >> 3), sw = (piece ^ (in & 7)) << 4;
-        const auto weigh = [&](int chunk, int q) {
-            if ((chunk > 0 || q > 0) && !wait_all(&sm.w_free[k], (q - 1) & 1, abort)) return false;
-            const int stage = chunk & 1, row = q * 32 + in;
-            uint4 *at = reinterpret_cast<uint4 *>(sm.x[stage][k] + row * 128 + sw);
-            uint4 x = *at;
-            const f32x2 wt = same2(sm.gates[stage][k].weight[row]);
-            if (row >= e - s - chunk * Q) {
-                x = make_uint4(0u, 0u, 0u, 0u);
-                *at = x;
-                if (k == 0) {
-                    *reinterpret_cast<uint4 *>(sm.b[stage][0] + row * 128 + sw) = x;
-                    *reinterpret_cast<uint4 *>(sm.b[stage][1] + row * 128 + sw) = x;
-                }
-            }
-            uint32_t word[4] = {x.x, x.y, x.z, x.w};
-            f32x2 f[4], odd = 0ull;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
-                odd = fma2(f[j], 0ull, odd);
-            }
-            if ((odd & 0x7fffffff7fffffffull) != 0ull) {  // 0 x is NaN
-                sm.any_bad[k] = 1;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t bits = (j & 1) ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
-                    if ((bits & 0x7f80u) != 0x7f80u) continue;
-                    atomicMin(&sm.first_bad[k][piece * 8 + j], chunk * Q + row);
-                    word[j / 2] &= (j & 1) ? 0xffffu : 0xffff0000u;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
-                *at = make_uint4(word[0], word[1], word[2], word[3]);
-            }
-            uint32_t hi[4], mid[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) split_bf16x2(mul2(f[j], wt), hi[j], mid[j]);
-            *reinterpret_cast<uint4 *>(sm.w[k][0] + in * 128 + sw) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(sm.w[k][1] + in * 128 + sw) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-            fence_async_shared();
-            warp_arrive(&sm.w_full[k], lane);
-            return true;
-        };
-        // M's columns of 32 tokens, from C B^T: times d_j and e^{G_i - G_j}, G counted from the first token of the warp's rows
-        // (where the decays are weak that is as exact as it needs, and where they are strong the difference is large).
-        float own = 0.0f;
-        float *since = sm.since[k][w];
-        const auto make_m = [&](const float *steps, int b, int quarters) {
-            const int blk = 2 * hf + b;
-            if (blk > w || blk >= quarters) return;
-            const int limit = blk < w ? 32 : lane;
-#pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 16) {
-                float f[16];
-                tmem_load(col_cb + b * 32 + j0, f);
-                tmem_wait_load();
-                uint32_t hi[8], mid[8];
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 gj = *reinterpret_cast<const float4 *>(since + blk * 32 + j0 + j);
-                    const ulonglong2 dj = *reinterpret_cast<const ulonglong2 *>(steps + blk * 32 + j0 + j);
-                    const float at[4] = {gj.x, gj.y, gj.z, gj.w};
-                    float m[4];
-#pragma unroll
-                    for (int l = 0; l < 4; ++l) m[l] = ex2_approx(own - at[l]);
-                    unpack2(mul2(mul2(pack2(m[0], m[1]), dj.x), pack2(f[j], f[j + 1])), m[0], m[1]);
-                    unpack2(mul2(mul2(pack2(m[2], m[3]), dj.y), pack2(f[j + 2], f[j + 3])), m[2], m[3]);
-#pragma unroll
-                    for (int l = 0; l < 4; ++l) m[l] = j0 + j + l <= limit ? m[l] : 0.0f;
-                    split_bf16x2(pack2(m[0], m[1]), hi[j / 2], mid[j / 2]);
-                    split_bf16x2(pack2(m[2], m[3]), hi[j / 2 + 1], mid[j / 2 + 1]);
-                }
-                tmem_store(col_m + b * 16 + j0 / 2, hi);
-                tmem_store(col_m + 32 + b * 16 + j0 / 2, mid);
-            }
-        };
+        const int piece = tid & 7;
         for (; c < chunks; ++c) {
-            const int stage = c & 1, u = c * nh + k, rows = min(Q, e - s - c * Q), quarters = quarters_of(rows);
-            if (!(ok = wait_all(&sm.gates_full[stage][k], (c / 2) & 1, abort) && wait_all(&sm.xb_full[stage], (c / 2) & 1, abort))) break;
-            const Gates &g = sm.gates[stage][k];
+            const int stage = c & 1, rows = e - s - c * Q, quarters = quarters_of(rows);
+            if (!(ok = wait_all(&sm.gates_full[stage], (c / 2) & 1, abort) && wait_all(&sm.xb_full[stage], (c / 2) & 1, abort))) break;
+            const Gates &g = sm.gates[stage];
             const float gamma = ex2_approx(g.hi[Q - 1] + g.lo[Q - 1]);
-            float row_decay = 0.0f;
-            uint8_t *xt = sm.x[stage][k];
-            if constexpr (FULL) {
-                const float ghi = g.hi[i], glo = g.lo[i];
-                const float base_hi = w > 0 ? g.hi[w * 32 - 1] : 0.0f, base_lo = w > 0 ? g.lo[w * 32 - 1] : 0.0f;
-                own = (ghi - base_hi) + (glo - base_lo);
-                row_decay = ex2_approx(ghi + glo);
+            uint8_t *xt = sm.x[stage];
+            if constexpr (FULL) {  // the state's parts for C S
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int j = (2 * hf + b) * 32 + lane;
-                    if (2 * hf + b <= w) since[j] = (g.hi[j] - base_hi) + (g.lo[j] - base_lo);
-                }
-                // the state's parts for C S, once the other head's (or the last chunk's) are used
-                const int from = k == 0 ? nh - 1 : 0, turn = k == 0 ? c - 1 : c;
-                if (turn >= 0 && !(ok = wait_all(&sm.s_free[from], turn & 1, abort))) break;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 2; ++j) {
                     uint32_t hi[4], mid[4];
 #pragma unroll
                     for (int l = 0; l < 4; ++l) split_bf16x2(st2[4 * j + l], hi[l], mid[l]);
-                    const int at = i * 128 + (((hf * 4 + j) ^ (i & 7)) << 4);
+                    const int at = i * 128 + (((qd * 2 + j) ^ (i & 7)) << 4);
                     *reinterpret_cast<uint4 *>(sm.s[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(sm.s[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
                 }
                 fence_async_shared();
                 warp_arrive(&sm.s_full, lane);
             }
-#pragma unroll 1
-            for (int q = 0; ok && q < quarters; ++q) ok = weigh(c, q);
-            if (!ok) break;
+            // The weighted tokens' parts, and what is wrong with the tile: rows of another sequence, values that are not finite.
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int row = half * 64 + (tid >> 3), at = row * 128 + ((piece ^ (row & 7)) << 4);
+                if (half * 64 >= rows) break;
+                uint4 x = *reinterpret_cast<const uint4 *>(xt + at);
+                const f32x2 wt = same2(g.weight[row]);
+                if (row >= rows) {
+                    x = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4 *>(xt + at) = x;
+                    *reinterpret_cast<uint4 *>(sm.b[stage][0] + at) = x;
+                    *reinterpret_cast<uint4 *>(sm.b[stage][1] + at) = x;
+                }
+                uint32_t word[4] = {x.x, x.y, x.z, x.w};
+                f32x2 f[4], odd = 0ull;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
+                    odd = fma2(f[j], 0ull, odd);
+                }
+                if ((odd & 0x7fffffff7fffffffull) != 0ull) {  // 0 x is NaN
+                    sm.any_bad = 1;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t bits = (j & 1) ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
+                        if ((bits & 0x7f80u) != 0x7f80u) continue;
+                        atomicMin(&sm.first_bad[piece * 8 + j], c * Q + row);
+                        word[j / 2] &= (j & 1) ? 0xffffu : 0xffff0000u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
+                    *reinterpret_cast<uint4 *>(xt + at) = make_uint4(word[0], word[1], word[2], word[3]);
+                }
+                uint32_t hi[4], mid[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) split_bf16x2(mul2(f[j], wt), hi[j], mid[j]);
+                *reinterpret_cast<uint4 *>(sm.w[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(sm.w[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                fence_async_shared();
+                warp_arrive(&sm.w_full[half], lane);
+            }
+            float row_decay = 0.0f;
             if constexpr (FULL) {
-                warp_arrive(&sm.x_ok[stage][k], lane);
+                warp_arrive(&sm.x_ok, lane);
+                // M's columns of 32 tokens, from C B^T: times d_j and e^{G_i - G_j}, G counted from the first token of the warp's
+                // rows (where the decays are weak that is as exact as it needs, and where they are strong the difference is large).
+                const float ghi = g.hi[i], glo = g.lo[i];
+                row_decay = ex2_approx(ghi + glo);
+                const bool mine = qd <= w && qd < quarters;
+                float own = 0.0f;
+                if (mine) {
+                    const float base_hi = w > 0 ? g.hi[w * 32 - 1] : 0.0f, base_lo = w > 0 ? g.lo[w * 32 - 1] : 0.0f;
+                    own = (ghi - base_hi) + (glo - base_lo);
+                    const int j = qd * 32 + lane;
+                    sm.since[w][j] = (g.hi[j] - base_hi) + (g.lo[j] - base_lo);
+                }
+                __syncwarp();
                 if (!(ok = wait_all(&sm.cb_full, c & 1, abort))) break;
-                if (u >= 1 && !(ok = wait_all(&sm.m_free[hf], (u - 1) & 1, abort))) break;
                 tc_fence_after();
-                make_m(g.d, 0, quarters);
-                make_m(g.d, 1, quarters);
-                tmem_wait_store();
+                if (mine) {
+                    const int limit = qd < w ? 32 : lane;
+                    const float *since = sm.since[w] + qd * 32, *steps = g.d + qd * 32;
+#pragma unroll
+                    for (int j0 = 0; j0 < 32; j0 += 16) {
+                        float f[16];
+                        tmem_load(lanes + kColCB + qd * 32 + j0, f);
+                        tmem_wait_load();
+                        uint32_t hi[8], mid[8];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 gj = *reinterpret_cast<const float4 *>(since + j0 + j);
+                            const ulonglong2 dj = *reinterpret_cast<const ulonglong2 *>(steps + j0 + j);
+                            const float at[4] = {gj.x, gj.y, gj.z, gj.w};
+                            float m[4];
+#pragma unroll
+                            for (int l = 0; l < 4; ++l) m[l] = ex2_approx(own - at[l]);
+                            unpack2(mul2(mul2(pack2(m[0], m[1]), dj.x), pack2(f[j], f[j + 1])), m[0], m[1]);
+                            unpack2(mul2(mul2(pack2(m[2], m[3]), dj.y), pack2(f[j + 2], f[j + 3])), m[2], m[3]);
+#pragma unroll
+                            for (int l = 0; l < 4; ++l) m[l] = j0 + j + l <= limit ? m[l] : 0.0f;
+                            split_bf16x2(pack2(m[0], m[1]), hi[j / 2], mid[j / 2]);
+                            split_bf16x2(pack2(m[2], m[3]), hi[j / 2 + 1], mid[j / 2 + 1]);
+                        }
+                        tmem_store(col_m + j0 / 2, hi);
+                        tmem_store(col_m + 32 + j0 / 2, mid);
+                    }
+                    tmem_wait_store();
+                }
                 tc_fence_before();
-                warp_arrive(&sm.m_full[hf], lane);
+                warp_arrive(&sm.m_full[qd >> 1], lane);
                 warp_arrive(&sm.cb_free, lane);
             }
-            warp_arrive(&sm.gates_free[stage][k], lane);
+            warp_arrive(&sm.gates_free[stage], lane);
 
             // S <- e^{G_Q} S + the chunk's sum
-            if (!(ok = wait_all(&sm.sum_full[k], c & 1, abort))) break;
+            if (!(ok = wait_all(&sm.sum_full, c & 1, abort))) break;
             tc_fence_after();
             const f32x2 g2 = same2(gamma);
-#pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 16) {
+            {
                 float f[16];
-                tmem_load(col_sum + j0, f);
+                tmem_load(lanes + kColSum + qd * 16, f);
                 tmem_wait_load();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) st2[j0 / 2 + j] = fma2(g2, st2[j0 / 2 + j], pack2(f[2 * j], f[2 * j + 1]));
+                for (int j = 0; j < 8; ++j) st2[j] = fma2(g2, st2[j], pack2(f[2 * j], f[2 * j + 1]));
             }
             tc_fence_before();
             whole *= gamma;
-            const bool bad = sm.any_bad[k] != 0;  // what this chunk has is noted before sum_full
+            const bool bad = sm.any_bad != 0;  // what this chunk has is noted before sum_full
             if (bad) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     float f[2];
                     unpack2(st2[j], f[0], f[1]);
 #pragma unroll
-                    for (int l = 0; l < 2; ++l) f[l] = sm.first_bad[k][hf * 32 + 2 * j + l] < (c + 1) * Q ? NAN : f[l];
+                    for (int l = 0; l < 2; ++l) f[l] = sm.first_bad[qd * 16 + 2 * j + l] < (c + 1) * Q ? NAN : f[l];
                     st2[j] = pack2(f[0], f[1]);
                 }
             }
 
             // out_i = e^{G_i} (C S)_i + (M x)_i + D x_i, with the gate
             if constexpr (FULL) {
-                if (!(ok = wait_all(&sm.cs_full[k], c & 1, abort)) || !(ok = wait_all(&sm.mx_full[k], c & 1, abort))) break;
+                if (!(ok = wait_all(&sm.cs_full, c & 1, abort) && wait_all(&sm.mx_full, c & 1, abort))) break;
                 tc_fence_after();
                 const bool fast = vec_out && !bad;
                 const int64_t t = s + c * Q + i;
                 const f32x2 decay2 = same2(row_decay), skip2 = same2(skip);
+                float mx[16], cs[16];
+                __syncwarp();
+                tmem_load(lanes + kColMX + qd * 16, mx);
+                tmem_load(lanes + kColCS + qd * 16, cs);
+                tmem_wait_load();
+                tc_fence_before();
 #pragma unroll
-                for (int j0 = 0; j0 < 32; j0 += 16) {
-                    float mx[16], cs[16];
-                    __syncwarp();
-                    tmem_load(col_mx + j0, mx);
-                    tmem_load(col_cs + j0, cs);
-                    tmem_wait_load();
-                    if (j0 == 16) {
-                        tc_fence_before();
-                        warp_arrive(&sm.cs_free, lane);
+                for (int half = 0; half < 2; ++half) {
+                    const int ch = half * 8;
+                    uint4 *x = reinterpret_cast<uint4 *>(xt + i * 128 + (((qd * 2 + half) ^ (i & 7)) << 4));
+                    const uint32_t word[4] = {x->x, x->y, x->z, x->w};
+                    f32x2 y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int at = ch + 2 * j;
+                        y[j] = fma2(decay2, pack2(cs[at], cs[at + 1]), pack2(mx[at], mx[at + 1]));
+                        y[j] = fma2(skip2, pack2(bf16_lo(word[j]), bf16_hi(word[j])), y[j]);
                     }
+                    if constexpr (GATED) {
+                        if (i < rows && ch < width) {
+                            if (vec_out) {
+                                const uint4 zz = __ldg(reinterpret_cast<const uint4 *>(z + t * a.z.stride_tok + ch));
+                                const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int ch = j0 + half * 8;
-                        uint4 *x = reinterpret_cast<uint4 *>(xt + i * 128 + (((hf * 4 + (ch >> 3)) ^ (i & 7)) << 4));
-                        const uint32_t word[4] = {x->x, x->y, x->z, x->w};
-                        f32x2 y[4];
+                                for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], silu2(pack2(bf16_lo(zw[j]), bf16_hi(zw[j]))));
+                            } else {
+                                const auto at = [&](int j) { return ch + j < width ? bf16_bits(z[t * a.z.stride_tok + (ch + j) * a.z.stride_dim]) : 0.0f; };
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int at = half * 8 + 2 * j;
-                            y[j] = fma2(decay2, pack2(cs[at], cs[at + 1]), pack2(mx[at], mx[at + 1]));
-                            y[j] = fma2(skip2, pack2(bf16_lo(word[j]), bf16_hi(word[j])), y[j]);
-                        }
-                        if constexpr (GATED) {
-                            if (i < rows && ch < width) {
-                                if (vec_out) {
-                                    const uint4 zz = __ldg(reinterpret_cast<const uint4 *>(z + t * a.z.stride_tok + ch));
-                                    const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], silu2(pack2(bf16_lo(zw[j]), bf16_hi(zw[j]))));
-                                } else {
-                                    const auto at = [&](int j) { return ch + j < width ? bf16_bits(z[t * a.z.stride_tok + (ch + j) * a.z.stride_dim]) : 0.0f; };
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], silu2(pack2(at(2 * j), at(2 * j + 1))));
-                                }
+                                for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], silu2(pack2(at(2 * j), at(2 * j + 1))));
                             }
                         }
-                        const uint4 packed = make_uint4(f32x2_to_bf16x2(y[0]), f32x2_to_bf16x2(y[1]), f32x2_to_bf16x2(y[2]), f32x2_to_bf16x2(y[3]));
-                        *x = packed;  // the thread's own values, which nothing reads any more
                     }
+                    // over the thread's own values of x, which nothing reads any more
+                    *x = make_uint4(f32x2_to_bf16x2(y[0]), f32x2_to_bf16x2(y[1]), f32x2_to_bf16x2(y[2]), f32x2_to_bf16x2(y[3]));
                 }
-                if (fast) {  // four lanes a row: a store of whole rows a lane takes four times as many of L1's cycles
+                if (fast) {  // two lanes a row: with a whole row a lane a store takes more of L1's cycles
                     __syncwarp();
-                    const int part = lane & 3;
+                    const int part = lane & 1;
 #pragma unroll
-                    for (int r8 = 0; r8 < 4; ++r8) {
-                        const int tr = w * 32 + r8 * 8 + (lane >> 2);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(xt + tr * 128 + (((hf * 4 + part) ^ (tr & 7)) << 4));
-                        if (tr < rows && part * 8 < width) *reinterpret_cast<uint4 *>(out + (t - i + tr) * a.out.stride_tok + part * 8) = v;
+                    for (int r16 = 0; r16 < 2; ++r16) {
+                        const int tr = w * 32 + r16 * 16 + (lane >> 1);
+                        const uint4 val = *reinterpret_cast<const uint4 *>(xt + tr * 128 + (((qd * 2 + part) ^ (tr & 7)) << 4));
+                        if (tr < rows && part * 8 < width) *reinterpret_cast<uint4 *>(out + (t - i + tr) * a.out.stride_tok + part * 8) = val;
                     }
-                    fence_async_shared();
                 } else {
 #pragma unroll 1
                     for (int ch = 0; i < rows && ch < width; ++ch) {
-                        uint16_t f = *reinterpret_cast<const uint16_t *>(xt + i * 128 + (((hf * 4 + (ch >> 3)) ^ (i & 7)) << 4) + (ch & 7) * 2);
-                        if (bad && sm.first_bad[k][hf * 32 + ch] <= c * Q + i) f = 0x7fffu;
+                        uint16_t f = *reinterpret_cast<const uint16_t *>(xt + i * 128 + (((qd * 2 + (ch >> 3)) ^ (i & 7)) << 4) + (ch & 7) * 2);
+                        if (bad && sm.first_bad[qd * 16 + ch] <= c * Q + i) f = 0x7fffu;
                         out[t * a.out.stride_tok + ch * a.out.stride_dim] = f;
                     }
-                    fence_async_shared();
                 }
+                fence_async_shared();
                 warp_arrive(&sm.xb_free[stage], lane);
             }
         }
@@ -682,16 +623,16 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         if (!FULL || (last && a.state != nullptr)) {
             float *to = FULL ? pool : slot;
             const int64_t step = FULL ? a.s_stride_dim : 128;
-            const int count = !FULL ? 32 : i < a.dim_state ? width : 0;
+            const int count = !FULL ? 16 : i < a.dim_state ? width : 0;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 float f[2];
                 unpack2(st2[j], f[0], f[1]);
 #pragma unroll
                 for (int l = 0; l < 2; ++l)
                     if (2 * j + l < count) to[(2 * j + l) * step] = ok ? f[l] : NAN;
             }
-            if (!FULL && i == 0 && hf == 0) p.seg_decay[static_cast<int64_t>(unit) * a.num_heads * panels + v] = whole;
+            if (!FULL && i == 0 && qd == 0) p.seg_decay[static_cast<int64_t>(unit) * all + v] = whole;
         }
     }
     tc_fence_before();
@@ -745,8 +686,7 @@ int launch_chunks(const SsmFwd &p, const Maps &maps, int64_t units, int vec_out,
     current_device_sms(&dev);
     cudaError_t err;
     if (resident_blocks<ssm_chunk_kernel<FULL, NP, GATED>>(kThreads, kSmemBytes, dev, &err) == 0) return static_cast<int>(err);
-    const int panels = (p.a.head_dim + 63) / 64, rep = p.a.num_heads / p.a.num_groups;
-    const int64_t blocks = units * p.a.num_groups * ((static_cast<int64_t>(rep) * panels + 1) / 2);
+    const int64_t blocks = units * p.a.num_heads * ((p.a.head_dim + 63) / 64);
     if (blocks > 0x7fffffff) return CCV_ERR_SIZE;
     return launch_pdl(ssm_chunk_kernel<FULL, NP, GATED>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kSmemBytes, stream, p, maps, vec_out);
 }
@@ -779,7 +719,7 @@ int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int num_gro
     constexpr int kSms = 152;  // a GB300's: the workspace's size may not depend on the device that is current
     const int64_t each = static_cast<int64_t>(batch) * Q;
     const int chunks = static_cast<int>((total_tokens + each - 1) / each);
-    const int64_t blocks = static_cast<int64_t>(batch) * num_groups * ((static_cast<int64_t>(num_heads / num_groups) * ((head_dim + 63) / 64) + 1) / 2);
+    const int64_t blocks = static_cast<int64_t>(batch) * num_heads * ((head_dim + 63) / 64);
     auto waves = [](int64_t n) { return static_cast<double>((n + kSms - 1) / kSms); };
     double best = waves(blocks) * (chunks + 0.8);
     int choice = 0;
