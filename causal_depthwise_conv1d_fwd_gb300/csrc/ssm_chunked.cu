@@ -42,7 +42,7 @@ constexpr int kThreads = 640;
 constexpr int kCompute = 16;  // warps that compute; the others:
 constexpr int kCopyWarp = kCompute, kOutWarp = kCompute + 1, kSumWarp = kCompute + 2;
 // Columns of tensor memory: C B^T; M in two halves of 64 tokens, each in two parts; M x; C S; the sum for the state.
-constexpr uint32_t kColCB = 0, kColM = 128, kColMX = 256, kColCS = 320, kColSum = 384;
+constexpr uint32_t kColCB = 0, kColM = 128, kColMX = 256, kColCS = 320, kColSum = 448;  // C S twice
 constexpr int kStateFloats = 128 * 64;  // of a head's panel in the workspace
 
 struct Maps {
@@ -54,16 +54,16 @@ struct Gates {  // of a chunk's tokens: G log2(e) as a pair of floats, the steps
 };
 
 struct Smem {
-    uint8_t x[2][kTile];        // stage
+    uint8_t x[3][kTile];        // stage; the outputs are written over it
     uint8_t b[2][2][kTile];     // stage, panel of 64 states
     uint8_t c[2][kTile];        // panel
     uint8_t w[2][kTile];        // part: weighted tokens
     uint8_t s[2][kTile];        // part: the state
     Gates gates[2];             // stage
     float since[4][Q];          // 32 rows of M: G of the tokens up to them, counted from the rows' first
-    // What the compute warps produce in a chunk they produce again once all of them are past the products that read it, which
-    // each knows from its own waits; so only what is made ahead has a barrier for its way back.
-    uint64_t xb_full[2], xb_free[2], c_full, c_free, gates_full[2], gates_free[2];
+    // What the compute warps produce for a chunk's products they produce again only after they waited for these products' end;
+    // so only what is made ahead has a barrier for its way back.
+    uint64_t x_full[3], x_free[3], b_full[2], b_free[2], c_full, c_free, gates_full[2], gates_free[2];
     uint64_t cb_full, cb_free, m_full[2], mx_full, cs_full, s_full, w_full[2], sum_full, x_ok, drain[2];
     int first_bad[64];          // channel: the first of the block's tokens whose x is not finite
     int any_bad;
@@ -199,13 +199,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         sm.abort = sm.any_bad = 0;
         const auto init = [](uint64_t &b, int n) { mbar_init(&b, n); };
         for (int i = 0; i < 2; ++i) {
-            init(sm.xb_full[i], 1);
-            init(sm.xb_free[i], FULL ? 2 + kCompute : 1);  // the issuers of products, and the outputs' warps
+            init(sm.b_full[i], 1);
+            init(sm.b_free[i], FULL ? 2 : 1);  // the products' issuers
             init(sm.gates_full[i], 1);
             init(sm.gates_free[i], kCompute);
             init(sm.m_full[i], kCompute / 2);
             init(sm.w_full[i], kCompute);
             init(sm.drain[i], 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            init(sm.x_full[i], 1);
+            init(sm.x_free[i], kCompute);
         }
         init(sm.c_full, 1);
         init(sm.c_free, 1);
@@ -248,11 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         fetch(0);
         for (; c < chunks; ++c) {
             const int st = c & 1, t0 = s + c * Q;
-            if (c >= 2 && !wait_all(&sm.xb_free[st], (c / 2 - 1) & 1, abort)) break;
+            if (c >= 2 && !wait_all(&sm.b_free[st], (c / 2 - 1) & 1, abort)) break;
+            if (c >= 3 && !wait_all(&sm.x_free[c % 3], (c / 3 - 1) & 1, abort)) break;
             if (lane == 0) {
-                mbar_expect_tx(&sm.xb_full[st], 3 * kTile);
-                tensor_load(sm.x[st], &maps.x, panel * 64, h, t0, &sm.xb_full[st]);
-                for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.xb_full[st]);
+                mbar_expect_tx(&sm.x_full[c % 3], kTile);
+                tensor_load(sm.x[c % 3], &maps.x, panel * 64, h, t0, &sm.x_full[c % 3]);
+                mbar_expect_tx(&sm.b_full[st], 2 * kTile);
+                for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.b_full[st]);
             }
             __syncwarp();
             issued = c + 1;
@@ -292,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         }
         if (c < chunks) {  // gave up: let the copies land before the shared memory goes
             int quiet = 0;
-            for (int i = max(0, issued - 2); i < issued; ++i) wait_all(&sm.xb_full[i & 1], (i / 2) & 1, &quiet);
+            for (int i = max(0, issued - 2); i < issued; ++i) wait_all(&sm.b_full[i & 1], (i / 2) & 1, &quiet);
+            for (int i = max(0, issued - 3); i < issued; ++i) wait_all(&sm.x_full[i % 3], (i / 3) & 1, &quiet);
             if (FULL) wait_all(&sm.c_full, max(0, c - 1) & 1, &quiet);
         }
     } else if (warp == kOutWarp) {
@@ -302,9 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             bool ok = true;
             for (int c = 0; ok && c < chunks; ++c) {
                 const int st = c & 1, quarters = quarters_of(e - s - c * Q);
-                const uint32_t b = desc_low(smem_u32(sm.b[st][0])), x = desc_low(smem_u32(sm.x[st]));
+                const uint32_t b = desc_low(smem_u32(sm.b[st][0])), x = desc_low(smem_u32(sm.x[c % 3]));
                 // C B^T
-                ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort) && wait_all(&sm.c_full, c & 1, abort) &&
+                ok = wait_all(&sm.b_full[st], (c / 2) & 1, abort) && wait_all(&sm.c_full, c & 1, abort) &&
                      (c == 0 || wait_all(&sm.cb_free, (c - 1) & 1, abort));
                 if (!ok) break;
                 tc_fence_after();
@@ -314,18 +321,19 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     mma_ss(tmem + kColCB, cc + at, b + at, mma_desc(128, 128, false), ks > 0, el);
                 }
                 mma_commit(&sm.cb_full, el);
-                // C S: all warps have left the last outputs behind them
+                mma_commit(&sm.b_free[st], el);
+                // C S: all warps have left the outputs before the last behind them
                 if (!(ok = wait_all(&sm.s_full, c & 1, abort))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int part = 1; part >= 0; --part)
 #pragma unroll
                     for (int ks = 0; ks < 4 * NP; ++ks)
-                        mma_ss(tmem + kColCS, cc + ((ks / 4) * kTile + (ks % 4) * 32) / 16, s0 + (part * kTile + ks * 2048) / 16,
+                        mma_ss(tmem + kColCS + (c & 1) * 64, cc + ((ks / 4) * kTile + (ks % 4) * 32) / 16, s0 + (part * kTile + ks * 2048) / 16,
                                mma_desc(128, 64, true), part < 1 || ks > 0, el);
                 mma_commit(&sm.cs_full, el);
                 mma_commit(&sm.c_free, el);
-                // M x
+                // M x: they have left the last
                 if (!(ok = wait_all(&sm.x_ok, c & 1, abort))) break;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -341,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 }
                 if (!ok) break;
                 mma_commit(&sm.mx_full, el);
-                mma_commit(&sm.xb_free[st], el);
             }
             if (!ok) {  // gave up: let the products end before their memories go
                 if (el) count_error(p.err_count);
@@ -356,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         for (int c = 0; ok && c < chunks; ++c) {
             const int st = c & 1, rows = e - s - c * Q;
             const uint32_t b = desc_low(smem_u32(sm.b[st][0])) | ((kTile / 16) << 16);  // MN-major: its panels are kTile apart
-            if (!(ok = wait_all(&sm.xb_full[st], (c / 2) & 1, abort))) break;
+            if (!(ok = wait_all(&sm.b_full[st], (c / 2) & 1, abort))) break;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 if (half * 64 >= rows || !(ok = wait_all(&sm.w_full[half], c & 1, abort))) break;
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             }
             if (!ok) break;
             mma_commit(&sm.sum_full, el);
-            mma_commit(&sm.xb_free[st], el);
+            mma_commit(&sm.b_free[st], el);
         }
         if (!ok) {
             if (el) count_error(p.err_count);
@@ -413,149 +420,162 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         }
         float whole = 1.0f;  // decay over all tokens
         bool ok = true;
-        int c = 0;
+        int c;
         const int piece = tid & 7;
-        for (; c < chunks; ++c) {
-            const int stage = c & 1, rows = e - s - c * Q, quarters = quarters_of(rows);
-            if (!(ok = wait_all(&sm.gates_full[stage], (c / 2) & 1, abort) && wait_all(&sm.xb_full[stage], (c / 2) & 1, abort))) break;
+        // The next chunk's weighted tokens and state are made while M x runs; -1 makes the first's.
+        for (c = -1; c < chunks; ++c) {
+            const int stage = c & 1, rows = e - s - c * Q, quarters = quarters_of(rows), next = c + 1;
             const Gates &g = sm.gates[stage];
-            const float gamma = ex2_approx(g.hi[Q - 1] + g.lo[Q - 1]);
-            uint8_t *xt = sm.x[stage];
-            if constexpr (FULL) {  // the state's parts for C S
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t hi[4], mid[4];
-#pragma unroll
-                    for (int l = 0; l < 4; ++l) split_bf16x2(st2[4 * j + l], hi[l], mid[l]);
-                    const int at = i * 128 + (((qd * 2 + j) ^ (i & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(sm.s[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(sm.s[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                }
-                fence_async_shared();
-                warp_arrive(&sm.s_full, lane);
-            }
-            // The weighted tokens' parts, and what is wrong with the tile: rows of another sequence, values that are not finite.
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int row = half * 64 + (tid >> 3), at = row * 128 + ((piece ^ (row & 7)) << 4);
-                if (half * 64 >= rows) break;
-                uint4 x = *reinterpret_cast<const uint4 *>(xt + at);
-                const f32x2 wt = same2(g.weight[row]);
-                if (row >= rows) {
-                    x = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4 *>(xt + at) = x;
-                    *reinterpret_cast<uint4 *>(sm.b[stage][0] + at) = x;
-                    *reinterpret_cast<uint4 *>(sm.b[stage][1] + at) = x;
-                }
-                uint32_t word[4] = {x.x, x.y, x.z, x.w};
-                f32x2 f[4], odd = 0ull;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
-                    odd = fma2(f[j], 0ull, odd);
-                }
-                if ((odd & 0x7fffffff7fffffffull) != 0ull) {  // 0 x is NaN
-                    sm.any_bad = 1;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t bits = (j & 1) ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
-                        if ((bits & 0x7f80u) != 0x7f80u) continue;
-                        atomicMin(&sm.first_bad[piece * 8 + j], c * Q + row);
-                        word[j / 2] &= (j & 1) ? 0xffffu : 0xffff0000u;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
-                    *reinterpret_cast<uint4 *>(xt + at) = make_uint4(word[0], word[1], word[2], word[3]);
-                }
-                uint32_t hi[4], mid[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) split_bf16x2(mul2(f[j], wt), hi[j], mid[j]);
-                *reinterpret_cast<uint4 *>(sm.w[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(sm.w[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                fence_async_shared();
-                warp_arrive(&sm.w_full[half], lane);
-            }
+            uint8_t *xt = sm.x[(c + 3) % 3];
             float row_decay = 0.0f;
-            if constexpr (FULL) {
-                warp_arrive(&sm.x_ok, lane);
-                // M's columns of 32 tokens, from C B^T: times d_j and e^{G_i - G_j}, G counted from the first token of the warp's
-                // rows (where the decays are weak that is as exact as it needs, and where they are strong the difference is large).
-                const float ghi = g.hi[i], glo = g.lo[i];
-                row_decay = ex2_approx(ghi + glo);
-                const bool mine = qd <= w && qd < quarters;
-                float own = 0.0f;
-                if (mine) {
-                    const float base_hi = w > 0 ? g.hi[w * 32 - 1] : 0.0f, base_lo = w > 0 ? g.lo[w * 32 - 1] : 0.0f;
-                    own = (ghi - base_hi) + (glo - base_lo);
-                    const int j = qd * 32 + lane;
-                    sm.since[w][j] = (g.hi[j] - base_hi) + (g.lo[j] - base_lo);
-                }
-                __syncwarp();
-                if (!(ok = wait_all(&sm.cb_full, c & 1, abort))) break;
-                tc_fence_after();
-                if (mine) {
-                    const int limit = qd < w ? 32 : lane;
-                    const float *since = sm.since[w] + qd * 32, *steps = g.d + qd * 32;
-#pragma unroll
-                    for (int j0 = 0; j0 < 32; j0 += 16) {
-                        float f[16];
-                        tmem_load(lanes + kColCB + qd * 32 + j0, f);
-                        tmem_wait_load();
-                        uint32_t hi[8], mid[8];
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 gj = *reinterpret_cast<const float4 *>(since + j0 + j);
-                            const ulonglong2 dj = *reinterpret_cast<const ulonglong2 *>(steps + j0 + j);
-                            const float at[4] = {gj.x, gj.y, gj.z, gj.w};
-                            float m[4];
-#pragma unroll
-                            for (int l = 0; l < 4; ++l) m[l] = ex2_approx(own - at[l]);
-                            unpack2(mul2(mul2(pack2(m[0], m[1]), dj.x), pack2(f[j], f[j + 1])), m[0], m[1]);
-                            unpack2(mul2(mul2(pack2(m[2], m[3]), dj.y), pack2(f[j + 2], f[j + 3])), m[2], m[3]);
-#pragma unroll
-                            for (int l = 0; l < 4; ++l) m[l] = j0 + j + l <= limit ? m[l] : 0.0f;
-                            split_bf16x2(pack2(m[0], m[1]), hi[j / 2], mid[j / 2]);
-                            split_bf16x2(pack2(m[2], m[3]), hi[j / 2 + 1], mid[j / 2 + 1]);
-                        }
-                        tmem_store(col_m + j0 / 2, hi);
-                        tmem_store(col_m + 32 + j0 / 2, mid);
+            bool bad = false;
+            if (c >= 0) {
+                if constexpr (FULL) {
+                    warp_arrive(&sm.x_ok, lane);
+                    // M's columns of 32 tokens, from C B^T: times d_j and e^{G_i - G_j}, G counted from the first token of the warp's
+                    // rows (where the decays are weak that is as exact as it needs, and where they are strong the difference is large).
+                    const float ghi = g.hi[i], glo = g.lo[i];
+                    row_decay = ex2_approx(ghi + glo);
+                    const bool mine = qd <= w && qd < quarters;
+                    float own = 0.0f;
+                    if (mine) {
+                        const float base_hi = w > 0 ? g.hi[w * 32 - 1] : 0.0f, base_lo = w > 0 ? g.lo[w * 32 - 1] : 0.0f;
+                        own = (ghi - base_hi) + (glo - base_lo);
+                        const int j = qd * 32 + lane;
+                        sm.since[w][j] = (g.hi[j] - base_hi) + (g.lo[j] - base_lo);
                     }
-                    tmem_wait_store();
+                    __syncwarp();
+                    if (!(ok = wait_all(&sm.cb_full, c & 1, abort))) break;
+                    tc_fence_after();
+                    if (mine) {
+                        const int limit = qd < w ? 32 : lane;
+                        const float *since = sm.since[w] + qd * 32, *steps = g.d + qd * 32;
+#pragma unroll
+                        for (int j0 = 0; j0 < 32; j0 += 16) {
+                            float f[16];
+                            tmem_load(lanes + kColCB + qd * 32 + j0, f);
+                            tmem_wait_load();
+                            uint32_t hi[8], mid[8];
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 gj = *reinterpret_cast<const float4 *>(since + j0 + j);
+                                const ulonglong2 dj = *reinterpret_cast<const ulonglong2 *>(steps + j0 + j);
+                                const float at[4] = {gj.x, gj.y, gj.z, gj.w};
+                                float m[4];
+#pragma unroll
+                                for (int l = 0; l < 4; ++l) m[l] = ex2_approx(own - at[l]);
+                                unpack2(mul2(mul2(pack2(m[0], m[1]), dj.x), pack2(f[j], f[j + 1])), m[0], m[1]);
+                                unpack2(mul2(mul2(pack2(m[2], m[3]), dj.y), pack2(f[j + 2], f[j + 3])), m[2], m[3]);
+#pragma unroll
+                                for (int l = 0; l < 4; ++l) m[l] = j0 + j + l <= limit ? m[l] : 0.0f;
+                                split_bf16x2(pack2(m[0], m[1]), hi[j / 2], mid[j / 2]);
+                                split_bf16x2(pack2(m[2], m[3]), hi[j / 2 + 1], mid[j / 2 + 1]);
+                            }
+                            tmem_store(col_m + j0 / 2, hi);
+                            tmem_store(col_m + 32 + j0 / 2, mid);
+                        }
+                        tmem_wait_store();
+                    }
+                    tc_fence_before();
+                    warp_arrive(&sm.m_full[qd >> 1], lane);
+                    warp_arrive(&sm.cb_free, lane);
+                }
+                const float gamma = ex2_approx(g.hi[Q - 1] + g.lo[Q - 1]);
+                warp_arrive(&sm.gates_free[stage], lane);
+
+                // S <- e^{G_Q} S + the chunk's sum
+                if (!(ok = wait_all(&sm.sum_full, c & 1, abort))) break;
+                tc_fence_after();
+                const f32x2 g2 = same2(gamma);
+                {
+                    float f[16];
+                    tmem_load(lanes + kColSum + qd * 16, f);
+                    tmem_wait_load();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) st2[j] = fma2(g2, st2[j], pack2(f[2 * j], f[2 * j + 1]));
                 }
                 tc_fence_before();
-                warp_arrive(&sm.m_full[qd >> 1], lane);
-                warp_arrive(&sm.cb_free, lane);
-            }
-            warp_arrive(&sm.gates_free[stage], lane);
-
-            // S <- e^{G_Q} S + the chunk's sum
-            if (!(ok = wait_all(&sm.sum_full, c & 1, abort))) break;
-            tc_fence_after();
-            const f32x2 g2 = same2(gamma);
-            {
-                float f[16];
-                tmem_load(lanes + kColSum + qd * 16, f);
-                tmem_wait_load();
+                whole *= gamma;
+                bad = sm.any_bad != 0;  // what this chunk has is noted before sum_full
+                if (bad) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) st2[j] = fma2(g2, st2[j], pack2(f[2 * j], f[2 * j + 1]));
-            }
-            tc_fence_before();
-            whole *= gamma;
-            const bool bad = sm.any_bad != 0;  // what this chunk has is noted before sum_full
-            if (bad) {
+                    for (int j = 0; j < 8; ++j) {
+                        float f[2];
+                        unpack2(st2[j], f[0], f[1]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float f[2];
-                    unpack2(st2[j], f[0], f[1]);
-#pragma unroll
-                    for (int l = 0; l < 2; ++l) f[l] = sm.first_bad[qd * 16 + 2 * j + l] < (c + 1) * Q ? NAN : f[l];
-                    st2[j] = pack2(f[0], f[1]);
+                        for (int l = 0; l < 2; ++l) f[l] = sm.first_bad[qd * 16 + 2 * j + l] < (c + 1) * Q ? NAN : f[l];
+                        st2[j] = pack2(f[0], f[1]);
+                    }
                 }
             }
+            if (next < chunks) {
+                const int ns = next & 1, left = e - s - next * Q;
+                if (!(ok = wait_all(&sm.gates_full[ns], (next / 2) & 1, abort) && wait_all(&sm.b_full[ns], (next / 2) & 1, abort) &&
+                           wait_all(&sm.x_full[next % 3], (next / 3) & 1, abort)))
+                    break;
+                uint8_t *nx = sm.x[next % 3];
+                if constexpr (FULL) {  // the state's parts for C S
+                    if (c >= 0 && !(ok = wait_all(&sm.cs_full, c & 1, abort))) break;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t hi[4], mid[4];
+#pragma unroll
+                        for (int l = 0; l < 4; ++l) split_bf16x2(st2[4 * j + l], hi[l], mid[l]);
+                        const int at = i * 128 + (((qd * 2 + j) ^ (i & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(sm.s[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(sm.s[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    }
+                    fence_async_shared();
+                    warp_arrive(&sm.s_full, lane);
+                }
+                // The weighted tokens' parts, and what is wrong with the tile: rows of another sequence, values that are not finite.
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int row = half * 64 + (tid >> 3), at = row * 128 + ((piece ^ (row & 7)) << 4);
+                    if (half * 64 >= left) break;
+                    uint4 x = *reinterpret_cast<const uint4 *>(nx + at);
+                    const f32x2 wt = same2(sm.gates[ns].weight[row]);
+                    if (row >= left) {
+                        x = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(nx + at) = x;
+                        *reinterpret_cast<uint4 *>(sm.b[ns][0] + at) = x;
+                        *reinterpret_cast<uint4 *>(sm.b[ns][1] + at) = x;
+                    }
+                    uint32_t word[4] = {x.x, x.y, x.z, x.w};
+                    f32x2 f[4], odd = 0ull;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
+                        odd = fma2(f[j], 0ull, odd);
+                    }
+                    if ((odd & 0x7fffffff7fffffffull) != 0ull) {  // 0 x is NaN
+                        sm.any_bad = 1;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t bits = (j & 1) ? word[j / 2] >> 16 : word[j / 2] & 0xffffu;
+                            if ((bits & 0x7f80u) != 0x7f80u) continue;
+                            atomicMin(&sm.first_bad[piece * 8 + j], next * Q + row);
+                            word[j / 2] &= (j & 1) ? 0xffffu : 0xffff0000u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
+                        *reinterpret_cast<uint4 *>(nx + at) = make_uint4(word[0], word[1], word[2], word[3]);
+                    }
+                    uint32_t hi[4], mid[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) split_bf16x2(mul2(f[j], wt), hi[j], mid[j]);
+                    *reinterpret_cast<uint4 *>(sm.w[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(sm.w[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    fence_async_shared();
+                    warp_arrive(&sm.w_full[half], lane);
+                }
+                if (!FULL) warp_arrive(&sm.x_free[next % 3], lane);
+            }
+            if (c < 0) continue;
 
             // out_i = e^{G_i} (C S)_i + (M x)_i + D x_i, with the gate
             if constexpr (FULL) {
-                if (!(ok = wait_all(&sm.cs_full, c & 1, abort) && wait_all(&sm.mx_full, c & 1, abort))) break;
+                if (!(ok = wait_all(&sm.mx_full, c & 1, abort))) break;
                 tc_fence_after();
                 const bool fast = vec_out && !bad;
                 const int64_t t = s + c * Q + i;
@@ -563,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 float mx[16], cs[16];
                 __syncwarp();
                 tmem_load(lanes + kColMX + qd * 16, mx);
-                tmem_load(lanes + kColCS + qd * 16, cs);
+                tmem_load(lanes + kColCS + (c & 1) * 64 + qd * 16, cs);
                 tmem_wait_load();
                 tc_fence_before();
 #pragma unroll
@@ -613,11 +633,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     }
                 }
                 fence_async_shared();
-                warp_arrive(&sm.xb_free[stage], lane);
+                warp_arrive(&sm.x_free[c % 3], lane);
             }
         }
         if (FULL && !ok)  // gave up
-            for (; c < chunks; ++c)
+            for (c = max(c, 0); c < chunks; ++c)
                 if (s + c * Q + i < e)
                     for (int ch = 0; ch < width; ++ch) out[(s + c * Q + i) * a.out.stride_tok + ch * a.out.stride_dim] = 0x7fffu;
         if (!FULL || (last && a.state != nullptr)) {
