@@ -10,7 +10,7 @@
 //   the state in registers (thread n has 16 channels of row n), its parts to shared memory for C S, and its multiply-add;
 //   the weighted tokens' parts for the state's sum; M from C B^T (tensor memory to tensor memory), 32 of its columns; and the
 //   outputs, 16 channels.
-// Three more warps copy tiles and sum the steps, issue what leads to the outputs, and issue the sum for the state.
+// Four more warps copy tiles, sum the steps, issue what leads to the outputs, and issue the sum for the state.
 // Heads wider than 64 are cut into panels of 64.  With a role a warpgroup the hot instructions were twice as many and missed the
 // instruction cache, a third of all stalls; with two heads a block, two warpgroups each, the registers for twice the state left
 // too few to overlap M's arithmetic.
@@ -40,7 +40,7 @@ constexpr int Q = 128;              // tokens of a chunk
 constexpr int kTile = Q * 128;      // bytes of 128 rows of 64 bf16 values
 constexpr int kThreads = 640;
 constexpr int kCompute = 16;  // warps that compute; the others:
-constexpr int kCopyWarp = kCompute, kOutWarp = kCompute + 1, kSumWarp = kCompute + 2;
+constexpr int kCopyWarp = kCompute, kOutWarp = kCompute + 1, kSumWarp = kCompute + 2, kStepWarp = kCompute + 3;
 // Columns of tensor memory: C B^T; M in two halves of 64 tokens, each in two parts; M x; C S; the sum for the state.
 constexpr uint32_t kColCB = 0, kColM = 128, kColMX = 256, kColCS = 320, kColSum = 448;  // C S twice
 constexpr int kStateFloats = 128 * 64;  // of a head's panel in the workspace
@@ -231,17 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     volatile int *abort = &sm.abort;
 
     if (warp == kCopyWarp) {
-        // Copies of a chunk's tiles, and its steps and their sums; four tokens a lane.
         int issued = 0, c = 0;
-        float raw[4];
-        const float scale = a.A[h], bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
-        const auto fetch = [&](int chunk) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = s + chunk * Q + lane * 4 + i;
-                raw[i] = t < e ? ssm_raw_step(a, t * a.dt_stride_tok + h * a.dt_stride_head) : 0.0f;
-            }
-        };
         const auto load_c = [&](int t0) {
             if (lane == 0) {
                 mbar_expect_tx(&sm.c_full, NP * kTile);
@@ -249,7 +239,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             }
             __syncwarp();
         };
-        fetch(0);
         for (; c < chunks; ++c) {
             const int st = c & 1, t0 = s + c * Q;
             if (c >= 2 && !wait_all(&sm.b_free[st], (c / 2 - 1) & 1, abort)) break;
@@ -262,10 +251,39 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             }
             __syncwarp();
             issued = c + 1;
-            if (FULL && c == 0) load_c(t0);
-            float d[4] = {raw[0], raw[1], raw[2], raw[3]};
+            if (FULL) {
+                if (c >= 1 && !wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
+                load_c(t0);
+            }
+        }
+        if (c < chunks) {  // gave up: let the copies land before the shared memory goes
+            int quiet = 0;
+            for (int i = max(0, issued - 2); i < issued; ++i) wait_all(&sm.b_full[i & 1], (i / 2) & 1, &quiet);
+            for (int i = max(0, issued - 3); i < issued; ++i) wait_all(&sm.x_full[i % 3], (i / 3) & 1, &quiet);
+            if (FULL) wait_all(&sm.c_full, max(0, c - 1) & 1, &quiet);
+        }
+    } else if (warp == kStepWarp) {
+        // A chunk's steps and their sums, four tokens a lane.  What it loads it converts a chunk later.
+        uint32_t raw[4];
+        const int shift = a.dt_fp32 ? 0 : 16;
+        const float scale = a.A[h], bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
+        const auto fetch = [&](int chunk) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = s + chunk * Q + lane * 4 + i;
+                const int64_t at = t * a.dt_stride_tok + h * a.dt_stride_head;
+                raw[i] = t >= e ? 0u : a.dt_fp32 ? static_cast<const uint32_t *>(a.dt)[at] : static_cast<const uint16_t *>(a.dt)[at];
+            }
+        };
+        fetch(0);
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1;
+            float d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = __uint_as_float(raw[i] << shift);
+            if (c + 1 < chunks) fetch(c + 1);
             float2 sum[4];
-            steps_of(d, sum, bias, scale, e - t0 - lane * 4, a);
+            steps_of(d, sum, bias, scale, e - s - c * Q - lane * 4, a);
 #pragma unroll
             for (int i = 1; i < 4; ++i) sum[i] = add_pairs(sum[i - 1], sum[i]);
             float2 total = sum[3];
@@ -290,17 +308,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             *reinterpret_cast<float4 *>(g.d + lane * 4) = make_float4(d[0], d[1], d[2], d[3]);
             *reinterpret_cast<float4 *>(g.weight + lane * 4) = make_float4(weight[0], weight[1], weight[2], weight[3]);
             warp_arrive(&sm.gates_full[st], lane);
-            if (c + 1 < chunks) fetch(c + 1);
-            if (FULL && c >= 1) {
-                if (!wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
-                load_c(t0);
-            }
-        }
-        if (c < chunks) {  // gave up: let the copies land before the shared memory goes
-            int quiet = 0;
-            for (int i = max(0, issued - 2); i < issued; ++i) wait_all(&sm.b_full[i & 1], (i / 2) & 1, &quiet);
-            for (int i = max(0, issued - 3); i < issued; ++i) wait_all(&sm.x_full[i % 3], (i / 3) & 1, &quiet);
-            if (FULL) wait_all(&sm.c_full, max(0, c - 1) & 1, &quiet);
         }
     } else if (warp == kOutWarp) {
         if constexpr (FULL) {
