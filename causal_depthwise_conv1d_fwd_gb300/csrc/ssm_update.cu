@@ -9,6 +9,8 @@
 // 128-byte lines, and no shared memory or barrier is needed.  A group of lanes has R rows next to each other; what goes by the row
 // (x, the step, the decay where a head has one, the output) is one lane's work and reaches the others by shuffles, and the sums
 // over the lanes are taken for all rows at once, so that each ends with the lane that its row belongs to.
+#include <algorithm>
+
 #include "ssm_common.cuh"
 
 namespace ccv {
@@ -51,57 +53,24 @@ __device__ __forceinline__ void load_bf16x4(const uint16_t *p, int64_t stride, i
 // LANES x NV x 4: dim_state rounded up.  R: rows of the state a group of lanes has.  PER: A has a value a state.
 // V: dim_state and every stride and pointer allow 16-byte vectors of the state and 8-byte vectors of B and C.
 template <int LANES, int NV, int R, bool PER, bool V>
-__global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6) ssm_recurrent_kernel(const __grid_constant__ ccv_ssm_args a,
-                                                                    const __grid_constant__ SsmRows rw, int slices) {
+__global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : PER ? 5 : R == 1 ? 8 : 6) ssm_recurrent_kernel(const __grid_constant__ ccv_ssm_args a,
+                                                                    const __grid_constant__ SsmRows rw, int slices, int per) {
     constexpr int kGroups = kSsmThreads / LANES;
     wait_prior_grid();
     release_next_grid();
-    const int b = blockIdx.x / static_cast<unsigned>(slices), slice = blockIdx.x - b * slices;
+    const int part = blockIdx.x / static_cast<unsigned>(slices), slice = blockIdx.x - part * slices;
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const bool first = threadIdx.x == 0 && slice == 0;  // counts a row's error once
 
-    int64_t t0 = 0, row = b;
-    int n = rw.seqlen;
-    if (rw.query_start_loc != nullptr) {
-        const int s = rw.query_start_loc[b], e = rw.query_start_loc[b + 1];
-        if (s < 0 || e < s || e > rw.total_tokens) {
-            if (first) count_error(rw.err_count);
-            return;
-        }
-        t0 = s;
-        n = e - s;
-        row = 0;
-    }
-    if (n == 0) return;
-    const int line = rw.state_indices != nullptr ? rw.state_indices[b] : b;
-    if (line == a.pad_slot_id) return;
-    const bool fresh = a.state == nullptr || (rw.query_start_loc != nullptr &&
-                                              (rw.has_initial_state == nullptr || rw.has_initial_state[b] == 0));
-    bool good = a.state == nullptr || (line >= 0 && line < a.num_lines);
-    int64_t from = line;
-    if (rw.num_accepted != nullptr) {
-        const int kept = rw.num_accepted[b];
-        if (kept >= 1 && kept <= rw.oidx_steps) {
-            from = rw.out_indices[b * rw.oi_stride_b + (kept - 1) * rw.oi_stride_step];
-            good = from >= 0 && from < a.num_lines;
-        } else {
-            good = false;
-        }
-    }
-    if (!good) {
-        if (first) count_error(rw.err_count);
-        return;
-    }
-
     const int rows = a.num_heads * a.head_dim, rep = a.num_heads / a.num_groups;
     const int first_row = (slice * kGroups + group) * R;
-    float s[R][NV][4], decay[PER ? R : 1][PER ? NV : 1][PER ? 4 : 1];
+    float decay[PER ? R : 1][PER ? NV : 1][PER ? 4 : 1];
     int64_t off[R];  // of the row in a state line
     int grp[R];
     const int own_row = first_row + lane % R;  // the lane's
     const bool own = lane < R && own_row < rows;
     int own_h = 0, own_ch = 0;
-    {
+    const auto find_rows = [&] {
         // one division for the first row; the others follow it
         int h = min(first_row, rows - 1), ch = 0, g = 0;
         if (a.head_dim != 1) {
@@ -113,17 +82,12 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6
         int in_group = h - g * rep;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool use = first_row + r < rows;
             off[r] = h * a.s_stride_head + ch * a.s_stride_dim;
             grp[r] = g;
             if (lane % R == r) {
                 own_h = h;
                 own_ch = ch;
             }
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                load4<V>(fresh ? a.A : a.state + from * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
-                         use && !fresh ? a.dim_state : 0, s[r][j]);
             if constexpr (PER) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
@@ -148,86 +112,131 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : R == 1 ? 8 : 6
                 }
             }
         }
-    }
-    const int h = own_h, ch = own_ch;
-    const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f, skip = a.D != nullptr ? a.D[h] : 0.0f;
-    const float rate = PER ? 0.0f : a.A[h] * kLog2e;
-
-    const auto at = [&](const ccv_heads_view &v, int64_t head, int64_t dim) {
-        return static_cast<const uint16_t *>(v.data) + row * v.stride_row + t0 * v.stride_tok + head * v.stride_head + dim * v.stride_dim;
     };
-    const uint16_t *xp = at(a.x, h, ch), *zp = at(a.z, h, ch), *bp = at(a.B, 0, 0), *cp = at(a.C, 0, 0);
-    uint16_t *op = const_cast<uint16_t *>(at(a.out, h, ch));
-    int64_t step = row * a.dt_stride_row + t0 * a.dt_stride_tok + h * a.dt_stride_head;
-
-    for (int t = 0; t < n; ++t) {
-        const float x = bf16_bits(*xp), d = ssm_step(ssm_raw_step(a, step), bias, a);
-        const float z = a.z.data != nullptr ? bf16_bits(*zp) : 0.0f;
-        const float dx = d * x, same = PER ? d : ex2_approx(d * rate);
-        float y[R], bv[NV][4], cv[NV][4];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float e_or_d = __shfl_sync(kFullMask, same, r, LANES), w = __shfl_sync(kFullMask, dx, r, LANES);
-            if (r == 0 || grp[r] != grp[r - 1]) {
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    load_bf16x4<V>(bp + grp[r] * a.B.stride_head, a.B.stride_dim, (j * LANES + lane) * 4, a.dim_state, bv[j]);
-                    load_bf16x4<V>(cp + grp[r] * a.C.stride_head, a.C.stride_dim, (j * LANES + lane) * 4, a.dim_state, cv[j]);
-                }
-            }
-            y[r] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = PER ? ex2_approx(e_or_d * decay[PER ? r : 0][PER ? j : 0][PER ? i : 0]) : e_or_d;
-                    s[r][j][i] = fmaf(e, s[r][j][i], w * bv[j][i]);
-                    y[r] = fmaf(s[r][j][i], cv[j][i], y[r]);
-                }
-        }
-        // halving: after the steps that the rows' count allows each lane has one row's sum over some lanes, then over all
-#pragma unroll
-        for (int m = R / 2; m > 0; m >>= 1)
-#pragma unroll
-            for (int r = 0; r < m; ++r) {
-                const bool upper = (lane & m) != 0;
-                const float keep = upper ? y[r + m] : y[r], give = upper ? y[r] : y[r + m];
-                y[r] = keep + __shfl_xor_sync(kFullMask, give, m);
-            }
-#pragma unroll
-        for (int m = R; m < LANES; m <<= 1) y[0] += __shfl_xor_sync(kFullMask, y[0], m);
-        if (own) {
-            float o = fmaf(skip, x, y[0]);
-            if (a.z.data != nullptr) o *= silu(z);
-            *op = round_bf16(o);
-        }
-        if (rw.out_indices != nullptr) {
-            const int64_t to = rw.out_indices[b * rw.oi_stride_b + t * rw.oi_stride_step];
-            if (to >= a.num_lines) {
+    if (PER) find_rows();
+    const int end = PER ? min((part + 1) * per, rw.batch) : part + 1;
+    for (int b = PER ? part * per : part; b < end; ++b) {
+        int64_t t0 = 0, row = b;
+        int n = rw.seqlen;
+        if (rw.query_start_loc != nullptr) {
+            const int s = rw.query_start_loc[b], e = rw.query_start_loc[b + 1];
+            if (s < 0 || e < s || e > rw.total_tokens) {
                 if (first) count_error(rw.err_count);
-            } else if (to >= 0) {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int j = 0; j < NV; ++j)
-                        store4<V>(a.state + to * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
-                                  first_row + r < rows ? a.dim_state : 0, s[r][j]);
+                continue;
+            }
+            t0 = s;
+            n = e - s;
+            row = 0;
+        }
+        if (n == 0) continue;
+        const int line = rw.state_indices != nullptr ? rw.state_indices[b] : b;
+        if (line == a.pad_slot_id) continue;
+        const bool fresh = a.state == nullptr || (rw.query_start_loc != nullptr &&
+                                                  (rw.has_initial_state == nullptr || rw.has_initial_state[b] == 0));
+        bool good = a.state == nullptr || (line >= 0 && line < a.num_lines);
+        int64_t from = line;
+        if (rw.num_accepted != nullptr) {
+            const int kept = rw.num_accepted[b];
+            if (kept >= 1 && kept <= rw.oidx_steps) {
+                from = rw.out_indices[b * rw.oi_stride_b + (kept - 1) * rw.oi_stride_step];
+                good = from >= 0 && from < a.num_lines;
+            } else {
+                good = false;
             }
         }
-        xp += a.x.stride_tok;
-        zp += a.z.stride_tok;
-        bp += a.B.stride_tok;
-        cp += a.C.stride_tok;
-        op += a.out.stride_tok;
-        step += a.dt_stride_tok;
-    }
-    if (rw.out_indices == nullptr && a.state != nullptr) {
+        if (!good) {
+            if (first) count_error(rw.err_count);
+            continue;
+        }
+
+        if (!PER) find_rows();
+        float s[R][NV][4];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                store4<V>(a.state + line * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
-                          first_row + r < rows ? a.dim_state : 0, s[r][j]);
+                load4<V>(fresh ? a.A : a.state + from * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
+                         first_row + r < rows && !fresh ? a.dim_state : 0, s[r][j]);
+        const int h = own_h, ch = own_ch;
+        const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f, skip = a.D != nullptr ? a.D[h] : 0.0f;
+        const float rate = PER ? 0.0f : a.A[h] * kLog2e;
+
+        const auto at = [&](const ccv_heads_view &v, int64_t head, int64_t dim) {
+            return static_cast<const uint16_t *>(v.data) + row * v.stride_row + t0 * v.stride_tok + head * v.stride_head + dim * v.stride_dim;
+        };
+        const uint16_t *xp = at(a.x, h, ch), *zp = at(a.z, h, ch), *bp = at(a.B, 0, 0), *cp = at(a.C, 0, 0);
+        uint16_t *op = const_cast<uint16_t *>(at(a.out, h, ch));
+        int64_t step = row * a.dt_stride_row + t0 * a.dt_stride_tok + h * a.dt_stride_head;
+
+        for (int t = 0; t < n; ++t) {
+            const float x = bf16_bits(*xp), d = ssm_step(ssm_raw_step(a, step), bias, a);
+            const float z = a.z.data != nullptr ? bf16_bits(*zp) : 0.0f;
+            const float dx = d * x, same = PER ? d : ex2_approx(d * rate);
+            float y[R], bv[NV][4], cv[NV][4];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float e_or_d = __shfl_sync(kFullMask, same, r, LANES), w = __shfl_sync(kFullMask, dx, r, LANES);
+                if (r == 0 || grp[r] != grp[r - 1]) {
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        load_bf16x4<V>(bp + grp[r] * a.B.stride_head, a.B.stride_dim, (j * LANES + lane) * 4, a.dim_state, bv[j]);
+                        load_bf16x4<V>(cp + grp[r] * a.C.stride_head, a.C.stride_dim, (j * LANES + lane) * 4, a.dim_state, cv[j]);
+                    }
+                }
+                y[r] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float e = PER ? ex2_approx(e_or_d * decay[PER ? r : 0][PER ? j : 0][PER ? i : 0]) : e_or_d;
+                        s[r][j][i] = fmaf(e, s[r][j][i], w * bv[j][i]);
+                        y[r] = fmaf(s[r][j][i], cv[j][i], y[r]);
+                    }
+            }
+            // halving: after the steps that the rows' count allows each lane has one row's sum over some lanes, then over all
+#pragma unroll
+            for (int m = R / 2; m > 0; m >>= 1)
+#pragma unroll
+                for (int r = 0; r < m; ++r) {
+                    const bool upper = (lane & m) != 0;
+                    const float keep = upper ? y[r + m] : y[r], give = upper ? y[r] : y[r + m];
+                    y[r] = keep + __shfl_xor_sync(kFullMask, give, m);
+                }
+#pragma unroll
+            for (int m = R; m < LANES; m <<= 1) y[0] += __shfl_xor_sync(kFullMask, y[0], m);
+            if (own) {
+                float o = fmaf(skip, x, y[0]);
+                if (a.z.data != nullptr) o *= silu(z);
+                *op = round_bf16(o);
+            }
+            if (rw.out_indices != nullptr) {
+                const int64_t to = rw.out_indices[b * rw.oi_stride_b + t * rw.oi_stride_step];
+                if (to >= a.num_lines) {
+                    if (first) count_error(rw.err_count);
+                } else if (to >= 0) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int j = 0; j < NV; ++j)
+                            store4<V>(a.state + to * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
+                                      first_row + r < rows ? a.dim_state : 0, s[r][j]);
+                }
+            }
+            xp += a.x.stride_tok;
+            zp += a.z.stride_tok;
+            bp += a.B.stride_tok;
+            cp += a.C.stride_tok;
+            op += a.out.stride_tok;
+            step += a.dt_stride_tok;
+        }
+        if (rw.out_indices == nullptr && a.state != nullptr) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    store4<V>(a.state + line * a.s_stride_line + off[r], a.s_stride_state, (j * LANES + lane) * 4,
+                              first_row + r < rows ? a.dim_state : 0, s[r][j]);
+        }
     }
 }
 
@@ -235,10 +244,19 @@ template <int LANES, int NV, int R, bool PER, bool V>
 int launch(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
     constexpr int kRows = kSsmThreads / LANES * R;
     const int slices = (a.num_heads * a.head_dim + kRows - 1) / kRows;
-    const int64_t blocks = static_cast<int64_t>(slices) * rows.batch;
+    // With a decay a state the block's rates are as large as its rows of the state, and it keeps them for up to 6 of the batch's
+    // rows, as long as two waves of blocks are left (5 an SM of 152).  A row a block takes for 64, 128, 256 and 512 rows of 8192
+    // channels 22, 41, 85 and 162 us, and this 20, 36, 70 and 132; for 16 rows 7.2, and two rows a block 8.0.
+    int per = 1;
+    if (PER) {
+        per = static_cast<int>(std::min<int64_t>(6, std::max<int64_t>(1, static_cast<int64_t>(slices) * rows.batch / (2 * 5 * 152))));
+        const int parts = (rows.batch + per - 1) / per;
+        per = (rows.batch + parts - 1) / parts;
+    }
+    const int64_t blocks = static_cast<int64_t>(slices) * ((rows.batch + per - 1) / per);
     if (blocks > 0x7fffffff) return CCV_ERR_SIZE;
     return launch_pdl(ssm_recurrent_kernel<LANES, NV, R, PER, V>, dim3(static_cast<unsigned>(blocks)), dim3(kSsmThreads), 0, stream,
-                      a, rows, slices);
+                      a, rows, slices, per);
 }
 
 template <bool PER, bool V>
