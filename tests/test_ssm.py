@@ -453,3 +453,19 @@ def test_one_chunk_of_many_sequences(ccv):
     for heads, dim, states, per in ((2, 64, 64, False), (40, 1, 16, True)):
         t = make(sum(lengths), heads, dim, 1, states, 37, per_state=per)
         check_fwd(ccv, t, lengths, init=[i % 3 == 0 for i in range(300)], channels=per)
+
+
+@pytest.mark.parametrize("rows,channels,states", [(1100, 300, 16), (3100, 129, 7), (1601, 50, 100)])
+def test_update_rows_that_share_rates(ccv, rows, channels, states):
+    """A batch so large that a block takes several of its rows, among them skipped and refused ones."""
+    t = update_case(rows, 1, channels, 1, 1, states, 38, per_state=True, gated=True)
+    lines = torch.randperm(rows, generator=torch.Generator().manual_seed(39)).to(torch.int32)
+    lines[::7], lines[5], lines[rows - 1] = -1, rows, -2
+    check_update(ccv, t, lines=lines, flat=True, channels=True, err_wanted=True)
+
+
+def test_fwd_sequences_that_share_rates(ccv, path):
+    path("recurrent")
+    lengths = [i % 4 for i in range(1300)]
+    t = make(sum(lengths), 300, 1, 1, 16, 40, per_state=True)
+    check_fwd(ccv, t, lengths, init=[i % 3 == 0 for i in range(1300)], channels=True)
