@@ -737,9 +737,9 @@ int launch_all(const SsmFwd &p, const Maps &maps, int vec_out, cudaStream_t stre
 bool ssm_chunked_dims(int dim_state, int a_per_state) { return !a_per_state && dim_state <= 128; }
 
 // Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device).  In
-// chunk times of a block (7 us): the first pass takes 0.6 of one a chunk, a block 0.8 to start and end, the two launches more 3.
-// Each pass runs in waves of one block an SM.  11027 tokens of 32 heads take 136 us so and 600 whole; 2 x 4000 of 64 heads 191
-// in two segments, 199 whole, and 222 in segments of 4 chunks.
+// chunk times of a block (3 us): the first pass takes 0.6 of one a chunk, a block 0.8 to start and end, the two launches more 3.
+// Each pass runs in waves of one block an SM.  11027 tokens of 32 heads take 118 us so and 251 whole, 30000 of 64 493 and 675;
+// 2 x 4000 of 64 heads 138 in two segments and 105 whole.
 int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int num_groups, int head_dim) {
     const char *forced = std::getenv("CCV_SSM_SEGMENT");  // chunks of a segment (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;

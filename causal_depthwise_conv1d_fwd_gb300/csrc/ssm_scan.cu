@@ -9,8 +9,11 @@
 // for its own states: an exponential, two multiplications and two multiply-adds a state, in pairs.  The sums over the lanes are
 // taken for LANES tokens at once, halving what each lane holds at every step, so that a lane ends with one token's output.
 //
-// What bounds it is the exponential: 16 lanes of one a cycle and SM, 465 us for 4 x 4096 tokens of 8192 channels with 16 states,
-// where the copies take 160.
+// 4 x 4096 tokens of 8192 channels with 16 states take 834 us, 1.2 TB/s of what has to be moved.  Nothing in it is at its limit
+// alone: shared memory is busy for 73 % of the time (each lane reads a token's B, C and steps), instructions are issued in 64 % of
+// the cycles, and the exponentials need 235 us of it (32 a cycle and SM).  More lanes a row, more rows a lane, and exponentials by
+// polynomials on the multiply-add pipes were all slower.  The same for 1009 + 37 + 300 tokens of 2048 channels, in segments of
+// 128: 58 us.
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
@@ -485,20 +488,23 @@ int64_t ssm_scan_workspace(int total_tokens, int batch, int num_heads, int head_
 }
 
 // Units of 128 tokens of a segment, or 0 to leave sequences whole.  Offsets are on the device, so the longest sequence is taken to
-// be halfway between the average and all tokens.  In cycles: a token takes 140 in a block with an SM to itself, and 57 of the SM's
-// throughput; cutting does three quarters of the work once more, a segment of the join takes 700 and the two launches 20000.
+// be halfway between the average and all tokens.  In ns: a token takes 45 and 28 more for each of the blocks that an SM has;
+// cutting does 0.6 of the work once more, a segment of the join takes 700 and the two launches 8000.  5000 tokens of 4096 channels
+// take 222 us so (segments of 256) and 381 whole, 2000 of 2048 channels 62 and 153; 4 x 4096 of 8192 channels 834 whole and 1150
+// in segments of 1024.
 int ssm_scan_segments(int total_tokens, int batch, int num_heads, int num_groups, int head_dim, int dim_state) {
     const char *forced = std::getenv("CCV_SSM_SEGMENT");  // (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;
     constexpr double kSms = 152;  // a GB300's: the workspace's size may not depend on the device that is current
     const double rows = dim_state <= 16 ? 32 : dim_state <= 64 ? 16 : 8;
     const double blocks = num_groups * std::ceil(static_cast<double>(num_heads / num_groups) * head_dim / rows);
-    const double longest = 0.5 * (static_cast<double>(total_tokens) / batch + total_tokens);
-    const double work = total_tokens * blocks / kSms * 57;
-    double best = std::max(work, longest * 140);
+    const double average = static_cast<double>(total_tokens) / batch, longest = 0.5 * (average + total_tokens);
+    const auto token = [&](double n) { return 45 + 28 * std::ceil(n / kSms); };  // of n blocks
+    double best = std::max(average * token(blocks * batch), longest * token(blocks));
     int choice = 0;
-    for (int units = 1; units <= 64 && units * kUnit < longest; units *= 2) {
-        const double cost = std::max(1.75 * work, 1.75 * 140 * units * kUnit) + longest / (units * kUnit) * 700 + 20000;
+    for (int units = 1; units <= 64 && units * kUnit < longest; ++units) {
+        const double tokens = units * kUnit, segments = std::ceil(average / tokens) * batch;
+        const double cost = 1.6 * tokens * token(blocks * segments) + 700 * longest / tokens + 8000;
         if (cost < best) {
             best = cost;
             choice = units;
