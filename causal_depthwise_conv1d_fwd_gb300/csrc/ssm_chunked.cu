@@ -10,7 +10,7 @@
 //   the state in registers (thread n has 16 channels of row n), its parts to shared memory for C S, and its multiply-add;
 //   the weighted tokens' parts for the state's sum; M from C B^T (tensor memory to tensor memory), 32 of its columns; and the
 //   outputs, 16 channels.
-// Four more warps copy tiles, sum the steps, issue what leads to the outputs, and issue the sum for the state.
+// Three more warps copy tiles, sum the steps, and issue the products.
 // Heads wider than 64 are cut into panels of 64.  With a role a warpgroup the hot instructions were twice as many and missed the
 // instruction cache, a third of all stalls; with two heads a block, two warpgroups each, the registers for twice the state left
 // too few to overlap M's arithmetic.
@@ -38,9 +38,9 @@ namespace {
 
 constexpr int Q = 128;              // tokens of a chunk
 constexpr int kTile = Q * 128;      // bytes of 128 rows of 64 bf16 values
-constexpr int kThreads = 640;
 constexpr int kCompute = 16;  // warps that compute; the others:
-constexpr int kCopyWarp = kCompute, kOutWarp = kCompute + 1, kSumWarp = kCompute + 2, kStepWarp = kCompute + 3;
+constexpr int kCopyWarp = kCompute, kStepWarp = kCompute + 1, kIssueWarp = kCompute + 2;
+constexpr int kThreads = (kCompute + 3) * 32;
 // Columns of tensor memory: C B^T; M in two halves of 64 tokens, each in two parts; M x; C S; the sum for the state.
 constexpr uint32_t kColCB = 0, kColM = 128, kColMX = 256, kColCS = 320, kColSum = 448;  // C S twice
 constexpr int kStateFloats = 128 * 64;  // of a head's panel in the workspace
@@ -61,10 +61,10 @@ struct Smem {
     uint8_t s[2][kTile];        // part: the state
     Gates gates[2];             // stage
     float since[4][Q];          // 32 rows of M: G of the tokens up to them, counted from the rows' first
-    // What the compute warps produce for a chunk's products they produce again only after they waited for these products' end;
-    // so only what is made ahead has a barrier for its way back.
-    uint64_t x_full[3], x_free[3], b_full[2], b_free[2], c_full, c_free, gates_full[2], gates_free[2];
-    uint64_t cb_full, cb_free, m_full[2], mx_full, cs_full, s_full, w_full[2], sum_full, x_ok, drain[2];
+    // Whoever waits for a chunk's last products has all of what it made for the chunk free again, and one warp issues all products
+    // in order: what is not made ahead needs no barrier for its way back.
+    uint64_t in_full[3], x_free[3], b_free[2], c_full, c_free, gates_free[2];  // in: x, B and the steps
+    uint64_t parts_full, m_full, cb_full, sum_full, mx_full, drain;            // parts: of the weighted tokens and the state
     int first_bad[64];          // channel: the first of the block's tokens whose x is not finite
     int any_bad;
     int seq, start, end, abort;
@@ -198,28 +198,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     if (tid == 0) {
         sm.abort = sm.any_bad = 0;
         const auto init = [](uint64_t &b, int n) { mbar_init(&b, n); };
-        for (int i = 0; i < 2; ++i) {
-            init(sm.b_full[i], 1);
-            init(sm.b_free[i], FULL ? 2 : 1);  // the products' issuers
-            init(sm.gates_full[i], 1);
-            init(sm.gates_free[i], kCompute);
-            init(sm.m_full[i], kCompute / 2);
-            init(sm.w_full[i], kCompute);
-            init(sm.drain[i], 1);
-        }
         for (int i = 0; i < 3; ++i) {
-            init(sm.x_full[i], 1);
+            init(sm.in_full[i], 2);  // the copies and the steps
             init(sm.x_free[i], kCompute);
         }
-        init(sm.c_full, 1);
-        init(sm.c_free, 1);
-        init(sm.cb_full, 1);
-        init(sm.cb_free, kCompute);
-        init(sm.mx_full, 1);
-        init(sm.cs_full, 1);
-        init(sm.s_full, kCompute);
-        init(sm.sum_full, 1);
-        init(sm.x_ok, kCompute);
+        for (int i = 0; i < 2; ++i) {
+            init(sm.b_free[i], 1);
+            init(sm.gates_free[i], kCompute);
+        }
+        init(sm.parts_full, kCompute);
+        init(sm.m_full, kCompute);
+        for (uint64_t *bar : {&sm.c_full, &sm.c_free, &sm.cb_full, &sm.sum_full, &sm.mx_full, &sm.drain}) init(*bar, 1);
         mbar_init_fence();
     }
     if (tid < 64) sm.first_bad[tid] = INT_MAX;
@@ -244,10 +233,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             if (c >= 2 && !wait_all(&sm.b_free[st], (c / 2 - 1) & 1, abort)) break;
             if (c >= 3 && !wait_all(&sm.x_free[c % 3], (c / 3 - 1) & 1, abort)) break;
             if (lane == 0) {
-                mbar_expect_tx(&sm.x_full[c % 3], kTile);
-                tensor_load(sm.x[c % 3], &maps.x, panel * 64, h, t0, &sm.x_full[c % 3]);
-                mbar_expect_tx(&sm.b_full[st], 2 * kTile);
-                for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.b_full[st]);
+                mbar_expect_tx(&sm.in_full[c % 3], 3 * kTile);
+                tensor_load(sm.x[c % 3], &maps.x, panel * 64, h, t0, &sm.in_full[c % 3]);
+                for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.in_full[c % 3]);
             }
             __syncwarp();
             issued = c + 1;
@@ -258,8 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         }
         if (c < chunks) {  // gave up: let the copies land before the shared memory goes
             int quiet = 0;
-            for (int i = max(0, issued - 2); i < issued; ++i) wait_all(&sm.b_full[i & 1], (i / 2) & 1, &quiet);
-            for (int i = max(0, issued - 3); i < issued; ++i) wait_all(&sm.x_full[i % 3], (i / 3) & 1, &quiet);
+            for (int i = max(0, issued - 3); i < issued; ++i) wait_all(&sm.in_full[i % 3], (i / 3) & 1, &quiet);
             if (FULL) wait_all(&sm.c_full, max(0, c - 1) & 1, &quiet);
         }
     } else if (warp == kStepWarp) {
@@ -307,20 +294,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             *reinterpret_cast<float4 *>(g.lo + lane * 4) = make_float4(sum[0].y, sum[1].y, sum[2].y, sum[3].y);
             *reinterpret_cast<float4 *>(g.d + lane * 4) = make_float4(d[0], d[1], d[2], d[3]);
             *reinterpret_cast<float4 *>(g.weight + lane * 4) = make_float4(weight[0], weight[1], weight[2], weight[3]);
-            warp_arrive(&sm.gates_full[st], lane);
+            warp_arrive(&sm.in_full[c % 3], lane);
         }
-    } else if (warp == kOutWarp) {
-        if constexpr (FULL) {
-            const uint32_t el = elect_lane();
-            const uint32_t cc = desc_low(smem_u32(sm.c[0])), s0 = desc_low(smem_u32(sm.s[0]));
-            bool ok = true;
-            for (int c = 0; ok && c < chunks; ++c) {
-                const int st = c & 1, quarters = quarters_of(e - s - c * Q);
-                const uint32_t b = desc_low(smem_u32(sm.b[st][0])), x = desc_low(smem_u32(sm.x[c % 3]));
-                // C B^T
-                ok = wait_all(&sm.b_full[st], (c / 2) & 1, abort) && wait_all(&sm.c_full, c & 1, abort) &&
-                     (c == 0 || wait_all(&sm.cb_free, (c - 1) & 1, abort));
-                if (!ok) break;
+    } else if (warp == kIssueWarp) {
+        const uint32_t el = elect_lane(), w = desc_low(smem_u32(sm.w[0])), cc = desc_low(smem_u32(sm.c[0])), s0 = desc_low(smem_u32(sm.s[0]));
+        bool ok = true;
+        for (int c = 0; ok && c < chunks; ++c) {
+            const int rows = e - s - c * Q, quarters = quarters_of(rows);
+            const uint32_t b = desc_low(smem_u32(sm.b[c & 1][0])), x = desc_low(smem_u32(sm.x[c % 3]));
+            if (!(ok = wait_all(&sm.in_full[c % 3], (c / 3) & 1, abort))) break;
+            if constexpr (FULL) {  // C B^T
+                if (!(ok = wait_all(&sm.c_full, c & 1, abort))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 4 * NP; ++ks) {
@@ -328,24 +312,35 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     mma_ss(tmem + kColCB, cc + at, b + at, mma_desc(128, 128, false), ks > 0, el);
                 }
                 mma_commit(&sm.cb_full, el);
-                mma_commit(&sm.b_free[st], el);
-                // C S: all warps have left the outputs before the last behind them
-                if (!(ok = wait_all(&sm.s_full, c & 1, abort))) break;
-                tc_fence_after();
+            }
+            if (!(ok = wait_all(&sm.parts_full, c & 1, abort))) break;
+            tc_fence_after();
+            if constexpr (FULL) {  // C S: all warps have left the outputs before the last behind them
 #pragma unroll
                 for (int part = 1; part >= 0; --part)
 #pragma unroll
                     for (int ks = 0; ks < 4 * NP; ++ks)
-                        mma_ss(tmem + kColCS + (c & 1) * 64, cc + ((ks / 4) * kTile + (ks % 4) * 32) / 16, s0 + (part * kTile + ks * 2048) / 16,
-                               mma_desc(128, 64, true), part < 1 || ks > 0, el);
-                mma_commit(&sm.cs_full, el);
+                        mma_ss(tmem + kColCS + (c & 1) * 64, cc + ((ks / 4) * kTile + (ks % 4) * 32) / 16,
+                               s0 + (part * kTile + ks * 2048) / 16, mma_desc(128, 64, true), part < 1 || ks > 0, el);
                 mma_commit(&sm.c_free, el);
-                // M x: they have left the last
-                if (!(ok = wait_all(&sm.x_ok, c & 1, abort))) break;
+            }
+            // the chunk's sum for the state; B is MN-major here, its panels are kTile apart
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!(ok = wait_all(&sm.m_full[half], c & 1, abort))) break;
-                    tc_fence_after();
+            for (int half = 0; half < 2; ++half)
+                if (half * 64 < rows)
+#pragma unroll
+                    for (int part = 1; part >= 0; --part)
+#pragma unroll
+                        for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                            mma_ss(tmem + kColSum, (b | ((kTile / 16) << 16)) + ks * 2048 / 16, w + (part * kTile + ks * 2048) / 16,
+                                   mma_desc(128, 64, true) | (1u << 15), half > 0 || part < 1 || ks > 0, el);
+            mma_commit(&sm.sum_full, el);
+            mma_commit(&sm.b_free[c & 1], el);
+            if constexpr (FULL) {  // M x
+                if (!(ok = wait_all(&sm.m_full, c & 1, abort))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int part = 1; part >= 0; --part)
 #pragma unroll
@@ -353,44 +348,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                             if (half * 4 + ks < 2 * quarters)
                                 mma_ts(tmem + kColMX, tmem + kColM + half * 64 + part * 32 + ks * 8, x + (half * 4 + ks) * 2048 / 16,
                                        mma_desc(128, 64, true), half + (1 - part) + ks > 0, el);
-                }
-                if (!ok) break;
                 mma_commit(&sm.mx_full, el);
             }
-            if (!ok) {  // gave up: let the products end before their memories go
-                if (el) count_error(p.err_count);
-                int quiet = 0;
-                mma_commit(&sm.drain[0], el);
-                wait_all(&sm.drain[0], 0, &quiet);
-            }
         }
-    } else if (warp == kSumWarp) {
-        const uint32_t el = elect_lane(), w = desc_low(smem_u32(sm.w[0]));
-        bool ok = true;
-        for (int c = 0; ok && c < chunks; ++c) {
-            const int st = c & 1, rows = e - s - c * Q;
-            const uint32_t b = desc_low(smem_u32(sm.b[st][0])) | ((kTile / 16) << 16);  // MN-major: its panels are kTile apart
-            if (!(ok = wait_all(&sm.b_full[st], (c / 2) & 1, abort))) break;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (half * 64 >= rows || !(ok = wait_all(&sm.w_full[half], c & 1, abort))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int part = 1; part >= 0; --part)
-#pragma unroll
-                    for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                        mma_ss(tmem + kColSum, b + ks * 2048 / 16, w + (part * kTile + ks * 2048) / 16, mma_desc(128, 64, true) | (1u << 15),
-                               half > 0 || part < 1 || ks > 0, el);
-            }
-            if (!ok) break;
-            mma_commit(&sm.sum_full, el);
-            mma_commit(&sm.b_free[st], el);
-        }
-        if (!ok) {
+        if (!ok) {  // gave up: let the products end before their memories go
             if (el) count_error(p.err_count);
             int quiet = 0;
-            mma_commit(&sm.drain[1], el);
-            wait_all(&sm.drain[1], 0, &quiet);
+            mma_commit(&sm.drain, el);
+            wait_all(&sm.drain, 0, &quiet);
         }
     } else if (warp < kCompute) {
         // Thread i of a warpgroup has token i and row i of the state; the warpgroup has 16 channels, and 32 of M's columns.
@@ -438,7 +403,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             bool bad = false;
             if (c >= 0) {
                 if constexpr (FULL) {
-                    warp_arrive(&sm.x_ok, lane);
                     // M's columns of 32 tokens, from C B^T: times d_j and e^{G_i - G_j}, G counted from the first token of the warp's
                     // rows (where the decays are weak that is as exact as it needs, and where they are strong the difference is large).
                     const float ghi = g.hi[i], glo = g.lo[i];
@@ -484,14 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                         tmem_wait_store();
                     }
                     tc_fence_before();
-                    warp_arrive(&sm.m_full[qd >> 1], lane);
-                    warp_arrive(&sm.cb_free, lane);
+                    warp_arrive(&sm.m_full, lane);
                 }
                 const float gamma = ex2_approx(g.hi[Q - 1] + g.lo[Q - 1]);
                 warp_arrive(&sm.gates_free[stage], lane);
 
                 // S <- e^{G_Q} S + the chunk's sum
-                if (!(ok = wait_all(&sm.sum_full, c & 1, abort))) break;
+                if (!(ok = wait_all(&sm.sum_full, c & 1, abort))) break;  // and C S is done with the state's parts
                 tc_fence_after();
                 const f32x2 g2 = same2(gamma);
                 {
@@ -517,12 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             }
             if (next < chunks) {
                 const int ns = next & 1, left = e - s - next * Q;
-                if (!(ok = wait_all(&sm.gates_full[ns], (next / 2) & 1, abort) && wait_all(&sm.b_full[ns], (next / 2) & 1, abort) &&
-                           wait_all(&sm.x_full[next % 3], (next / 3) & 1, abort)))
-                    break;
+                if (!(ok = wait_all(&sm.in_full[next % 3], (next / 3) & 1, abort))) break;
                 uint8_t *nx = sm.x[next % 3];
                 if constexpr (FULL) {  // the state's parts for C S
-                    if (c >= 0 && !(ok = wait_all(&sm.cs_full, c & 1, abort))) break;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         uint32_t hi[4], mid[4];
@@ -532,8 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                         *reinterpret_cast<uint4 *>(sm.s[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4 *>(sm.s[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
                     }
-                    fence_async_shared();
-                    warp_arrive(&sm.s_full, lane);
                 }
                 // The weighted tokens' parts, and what is wrong with the tile: rows of another sequence, values that are not finite.
 #pragma unroll
@@ -573,9 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     for (int j = 0; j < 4; ++j) split_bf16x2(mul2(f[j], wt), hi[j], mid[j]);
                     *reinterpret_cast<uint4 *>(sm.w[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(sm.w[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    fence_async_shared();
-                    warp_arrive(&sm.w_full[half], lane);
                 }
+                fence_async_shared();
+                warp_arrive(&sm.parts_full, lane);
                 if (!FULL) warp_arrive(&sm.x_free[next % 3], lane);
             }
             if (c < 0) continue;
