@@ -7,7 +7,7 @@
 // penalties' arithmetic, which has no branches.  A row's history is read by all of its blocks, from L2 after the first.
 //
 // In place and without a mask only the tokens that were seen matter.  Where they are few enough for a hash table in shared memory
-// a block takes a whole row: it counts the history there, lists the slots in use, and goes through the list at each position.
+// a block takes a whole row: it counts the history there and goes through the table's slots at each position.
 #include <algorithm>
 
 #include "ccv_common.cuh"
@@ -263,7 +263,6 @@ __global__ void __launch_bounds__(kLogitsThreads, IN ? 1 : 4) logits_kernel(cons
     if (__syncthreads_or(odd) && tid == 0) count_error(err_count);
 }
 
-constexpr int kRowThreads = 1024;
 constexpr int kMaxSlots = 16384;
 constexpr uint32_t kNone = 0xffffffffu;
 
@@ -274,21 +273,18 @@ int hash_slots(const ccv_logits_args &a) {
     while (3 * static_cast<int64_t>(slots) < 4 * tokens && slots <= kMaxSlots) slots *= 2;
     return slots <= kMaxSlots ? slots : 0;
 }
-size_t hash_bytes(int slots) { return static_cast<size_t>(slots) * 10; }  // key, entry, and a place in the list for each
+size_t hash_bytes(int slots) { return static_cast<size_t>(slots) * 8; }  // key and entry
 
 // A block a row, in place and without a mask.  slots: a power of two, at most three quarters of them used.
-template <bool F32>
-__global__ void __launch_bounds__(kRowThreads) logits_row_kernel(const __grid_constant__ ccv_logits_args a, int slots, int *err_count) {
+template <bool F32, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_row_kernel(const __grid_constant__ ccv_logits_args a, int slots, int *err_count) {
     extern __shared__ __align__(16) uint32_t hash[];
     uint32_t *key = hash, *entry = hash + slots;
-    uint16_t *list = reinterpret_cast<uint16_t *>(entry + slots);
-    __shared__ int used;
     const int tid = threadIdx.x, b = blockIdx.x, shift = 32 - (31 - __clz(slots));
-    for (int i = tid; i < slots / 4; i += kRowThreads) {
+    for (int i = tid; i < slots / 4; i += THREADS) {
         reinterpret_cast<uint4 *>(key)[i] = make_uint4(kNone, kNone, kNone, kNone);
         reinterpret_cast<uint4 *>(entry)[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    if (tid == 0) used = 0;
     wait_prior_grid();
     release_next_grid();
     const int line = a.history_indices != nullptr ? a.history_indices[b] : b;
@@ -305,7 +301,6 @@ __global__ void __launch_bounds__(kRowThreads) logits_row_kernel(const __grid_co
         uint32_t at = (static_cast<uint32_t>(token) * 2654435769u) >> shift;  // multiplicative hashing (Knuth)
         for (;; at = (at + 1) & (slots - 1)) {  // some slots stay empty, so it ends
             const uint32_t old = atomicCAS(&key[at], kNone, static_cast<uint32_t>(token));
-            if (old == kNone) list[atomicAdd(&used, 1)] = static_cast<uint16_t>(at);
             if (old == kNone || old == static_cast<uint32_t>(token)) break;
         }
         if (flag == 0u) atomicAdd(&entry[at], 1u);
@@ -317,12 +312,12 @@ __global__ void __launch_bounds__(kRowThreads) logits_row_kernel(const __grid_co
         told = min(max(told, 0), a.history_size);
         prompt = min(max(prompt, 0), a.history_size);
         const int32_t *ids = a.history + line * a.h_stride_line;
-        for (int i0 = tid; i0 < told; i0 += kRowThreads * kAhead) {
+        for (int i0 = tid; i0 < told; i0 += THREADS * kAhead) {
             int token[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) token[j] = i0 + j * kRowThreads < told ? __ldg(ids + i0 + j * kRowThreads) : -1;
+            for (int j = 0; j < kAhead; ++j) token[j] = i0 + j * THREADS < told ? __ldg(ids + i0 + j * THREADS) : -1;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) note(token[j], i0 + j * kRowThreads < prompt ? kPrompt : 0u);
+            for (int j = 0; j < kAhead; ++j) note(token[j], i0 + j * THREADS < prompt ? kPrompt : 0u);
         }
     }
     const float repetition = a.repetition != nullptr ? a.repetition[b] : 1.0f;
@@ -333,40 +328,46 @@ __global__ void __launch_bounds__(kRowThreads) logits_row_kernel(const __grid_co
                       a.bias_ids + b * a.b_stride_b,
                       a.bias + b * a.b_stride_b,
                       a.bias_size};
-    for (int i = tid; i < p.size; i += kRowThreads) note(p.ids[i], kBiased);
+    for (int i = tid; i < p.size; i += THREADS) note(p.ids[i], kBiased);
     for (int pos = 0; pos < a.num_positions; ++pos) {
         if (pos > 0 && a.draft_tokens != nullptr) {
             __syncthreads();  // the last position's threads are done with the table
             if (tid == 0) note(a.draft_tokens[b * a.d_stride_b + (pos - 1) * a.d_stride_pos], 0u);
         }
         __syncthreads();
-        const int count = used;
         const int64_t from = b * a.l_stride_b + pos * a.l_stride_pos;
-        for (int i0 = tid; i0 < count; i0 += kRowThreads * 4) {
-            uint32_t at[4], token[4];
-            float f[4];
+        // eight slots a thread at once: their logits' loads are in flight together
+        for (int i0 = tid; i0 < slots; i0 += THREADS * 8) {
+            uint32_t token[8];
+            float f[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = i0 + j * kRowThreads;
-                at[j] = i < count ? list[i] : 0u;
-                token[j] = i < count ? key[at[j]] : kNone;
-                f[j] = i < count ? load_logit<F32>(a.logits, from + token[j]) : 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                const int i = i0 + j * THREADS;
+                token[j] = i < slots ? key[i] : kNone;
+                f[j] = token[j] != kNone ? load_logit<F32>(a.logits, from + token[j]) : 0.0f;
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (token[j] != kNone) store_logit<F32>(a.out, from + token[j], adjust(f[j], entry[at[j]], static_cast<int>(token[j]), p));
+            for (int j = 0; j < 8; ++j)
+                if (token[j] != kNone) store_logit<F32>(a.out, from + token[j], adjust(f[j], entry[i0 + j * THREADS], static_cast<int>(token[j]), p));
         }
     }
     if (__syncthreads_or(odd) && tid == 0) count_error(err_count);
 }
 
-template <bool F32>
-int launch_rows(const ccv_logits_args &a, int slots, int *err_count, cudaStream_t stream) {
+template <bool F32, int THREADS>
+int launch_row_blocks(const ccv_logits_args &a, int slots, int *err_count, cudaStream_t stream) {
     int dev = 0;
     current_device_sms(&dev);
     cudaError_t err;
-    if (resident_blocks<logits_row_kernel<F32>>(kRowThreads, hash_bytes(kMaxSlots), dev, &err) == 0) return static_cast<int>(err);
-    return launch_pdl(logits_row_kernel<F32>, dim3(static_cast<unsigned>(a.batch)), dim3(kRowThreads), hash_bytes(slots), stream, a, slots, err_count);
+    if (resident_blocks<logits_row_kernel<F32, THREADS>>(THREADS, hash_bytes(kMaxSlots), dev, &err) == 0) return static_cast<int>(err);
+    return launch_pdl(logits_row_kernel<F32, THREADS>, dim3(static_cast<unsigned>(a.batch)), dim3(THREADS), hash_bytes(slots), stream, a, slots, err_count);
+}
+
+// Two blocks of 512 threads fit an SM, and up to 4096 slots are little work: 256 rows of 131072 logits with 300, 900 and 2000
+// tokens take 4.7, 7.0 and 11 us so, with 1024 threads 7.9, 9.9 and 14; with 4000 (8192 slots) 25 and 21.
+template <bool F32>
+int launch_rows(const ccv_logits_args &a, int slots, int *err_count, cudaStream_t stream) {
+    return slots <= 4096 ? launch_row_blocks<F32, 512>(a, slots, err_count, stream) : launch_row_blocks<F32, 1024>(a, slots, err_count, stream);
 }
 
 int check(const ccv_logits_args *a) {
