@@ -469,14 +469,17 @@ int launch_scan(const SsmFwd &p, const ScanVec &vec, cudaStream_t stream) {
     return launch_pdl(ssm_scan_kernel<LANES, NS, R, ROWS, TOKENS, PER, true>, grid, block, 0, stream, p, vec);
 }
 
+// Lanes a row, states a lane, rows and tokens a tile by what is fastest for 2 x 2048 tokens of 4096 channels: 32 states 235 us (16
+// rows 250, 4 x 8 lanes 329), 64 states 337 (16 rows 369, 16 x 4 lanes 508), 128 states 664 (16 x 8 lanes 717 to 1170, 32 tokens
+// 850), 256 states 1330 (8 rows 2256).
 template <bool PER>
 int launch_states(const SsmFwd &p, const ScanVec &vec, cudaStream_t stream) {
     const int n = p.a.dim_state;
     if (n <= 16) return launch_scan<4, 4, 1, 32, 32, PER>(p, vec, stream);
-    if (n <= 32) return launch_scan<8, 4, 1, 16, 32, PER>(p, vec, stream);
-    if (n <= 64) return launch_scan<8, 8, 1, 16, 32, PER>(p, vec, stream);
-    if (n <= 128) return launch_scan<16, 8, 1, 8, 32, PER>(p, vec, stream);
-    return launch_scan<16, 16, 1, 8, 16, PER>(p, vec, stream);
+    if (n <= 32) return launch_scan<8, 4, 1, 32, 32, PER>(p, vec, stream);
+    if (n <= 64) return launch_scan<8, 8, 1, 32, 32, PER>(p, vec, stream);
+    if (n <= 128) return launch_scan<8, 16, 1, 16, 16, PER>(p, vec, stream);
+    return launch_scan<16, 16, 1, 16, 16, PER>(p, vec, stream);
 }
 
 }  // namespace
@@ -488,23 +491,32 @@ int64_t ssm_scan_workspace(int total_tokens, int batch, int num_heads, int head_
 }
 
 // Units of 128 tokens of a segment, or 0 to leave sequences whole.  Offsets are on the device, so the longest sequence is taken to
-// be halfway between the average and all tokens.  In ns: a token takes 45 and 28 more for each of the blocks that an SM has;
-// cutting does 0.6 of the work once more, a segment of the join takes 700 and the two launches 8000.  5000 tokens of 4096 channels
-// take 222 us so (segments of 256) and 381 whole, 2000 of 2048 channels 62 and 153; 4 x 4096 of 8192 channels 834 whole and 1150
-// in segments of 1024.
+// be halfway between the average and all tokens.  In ns, as measured: a token takes `lone` in a block with an SM to itself, and
+// `first` and `each` more for each of the blocks that an SM has; cutting does part of the work once more and costs a block the time
+// of some tokens (`start`), a segment of the join takes 700 and the two launches 8000.
+// 16 states: 5000 tokens of 4096 channels take 222 us so (segments of 256) and 381 whole, 2000 of 2048 channels 62 and 153; 4 x 4096
+// of 8192 channels 834 whole and 1150 in segments of 1024.  More states: 2000 tokens of 512 channels with 256 states 163 and 329;
+// 2 x 2048 of 4096 channels with 32 states 235 whole and 525 in segments of 128.
 int ssm_scan_segments(int total_tokens, int batch, int num_heads, int num_groups, int head_dim, int dim_state) {
     const char *forced = std::getenv("CCV_SSM_SEGMENT");  // (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;
     constexpr double kSms = 152;  // a GB300's: the workspace's size may not depend on the device that is current
-    const double rows = dim_state <= 16 ? 32 : dim_state <= 64 ? 16 : 8;
-    const double blocks = num_groups * std::ceil(static_cast<double>(num_heads / num_groups) * head_dim / rows);
+    struct Cost {
+        double rows, lone, first, each, again, start;
+    };
+    const Cost t = dim_state <= 16    ? Cost{32, 73, 45, 28, 0.6, 0}
+                   : dim_state <= 32  ? Cost{32, 57, 0, 68, 0.4, 100}
+                   : dim_state <= 64  ? Cost{32, 82, 0, 82, 0.4, 100}
+                   : dim_state <= 128 ? Cost{16, 124, 0, 96, 0.4, 100}
+                                      : Cost{16, 165, 0, 193, 0.4, 100};
+    const double blocks = num_groups * std::ceil(static_cast<double>(num_heads / num_groups) * head_dim / t.rows);
     const double average = static_cast<double>(total_tokens) / batch, longest = 0.5 * (average + total_tokens);
-    const auto token = [&](double n) { return 45 + 28 * std::ceil(n / kSms); };  // of n blocks
+    const auto token = [&](double n) { return n <= kSms ? t.lone : t.first + t.each * std::ceil(n / kSms); };  // of n blocks
     double best = std::max(average * token(blocks * batch), longest * token(blocks));
     int choice = 0;
     for (int units = 1; units <= 64 && units * kUnit < longest; ++units) {
         const double tokens = units * kUnit, segments = std::ceil(average / tokens) * batch;
-        const double cost = 1.6 * tokens * token(blocks * segments) + 700 * longest / tokens + 8000;
+        const double cost = (1 + t.again) * (tokens + t.start) * token(blocks * segments) + 700 * longest / tokens + 8000;
         if (cost < best) {
             best = cost;
             choice = units;

@@ -259,13 +259,17 @@ int launch(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
                       a, rows, slices, per);
 }
 
+// Lanes, groups of 4 values a lane, and rows of a group of lanes.  256 rows of 8192 channels with 16 states: 68 us, with 2 rows 93;
+// with 15 states (single elements) 179, with 2 rows 276; but one decay a head, 128 rows of 64 heads of 64 with 15 states, 37 with
+// 2 rows, 47 with 4.  128 rows of 64 heads of 64 channels with 64 states: 54 us (4 rows 58, 16 lanes 62), with 63 states 179 (one
+// row 203), with 128 states 88 (2 rows 122, 16 lanes with 2 rows 105), with 256 states 170 (8 lanes 195, 2 rows 233, 32 lanes 276).
 template <bool PER, bool V>
 int launch_states(const ccv_ssm_args &a, const SsmRows &rows, cudaStream_t stream) {
-    if (a.dim_state <= 16) return launch<4, 1, V ? 4 : 2, PER, V>(a, rows, stream);
-    if (a.dim_state <= 32) return launch<8, 1, V ? 4 : 2, PER, V>(a, rows, stream);
-    if (a.dim_state <= 64) return launch<8, 2, V ? 2 : 1, PER, V>(a, rows, stream);
+    if (a.dim_state <= 16) return launch<4, 1, V || PER ? 4 : 2, PER, V>(a, rows, stream);
+    if (a.dim_state <= 32) return launch<8, 1, V || PER ? 4 : 2, PER, V>(a, rows, stream);
+    if (a.dim_state <= 64) return launch<8, 2, 2, PER, V>(a, rows, stream);
     if (a.dim_state <= 128) return launch<8, 4, 1, PER, V>(a, rows, stream);
-    return launch<8, 8, 1, PER, V>(a, rows, stream);
+    return launch<16, 4, 1, PER, V>(a, rows, stream);
 }
 
 bool vector_ok(const ccv_ssm_args &a) {

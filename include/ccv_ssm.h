@@ -62,6 +62,20 @@ typedef struct ccv_ssm_args {
  * decrease: a sequence whose own offsets do, or leave [0, total_tokens], is
  * skipped and counted in err_count, and the other sequences' results are then
  * undefined.  Tokens past the last sequence are not written.
+ * Values that are not finite stay where the formulas carry them: to later
+ * tokens of the same sequence and head, for x to the same channel alone, for B
+ * and C to their group's heads; C and z to their own token.
+ * Three forms, chosen from the integer sizes: token by token with the state in
+ * registers (up to 8 tokens a sequence on average); 128 tokens a step on the
+ * tensor cores (one decay a head, dim_state <= 128, head_dim >= 8), where
+ * operands of products keep 16 bits and sums 24; a scan of tiles of tokens
+ * (the others).  The last two cut sequences into segments where that pays.
+ * CCV_SSM_PATH=recurrent, =chunked or =scan and CCV_SSM_SEGMENT (128s of
+ * tokens, 0: whole sequences) in the environment force a choice where it can
+ * run; they are read at each call and by ssm_fwd_workspace.
+ * A wait inside the chunked kernel that does not end within two seconds ends
+ * the call instead: outputs and states it did not reach are NaN, and err_count
+ * is raised.
  * workspace     ssm_fwd_workspace(...) bytes, 128-byte aligned, not shared
  *               with another call in flight.
  */
