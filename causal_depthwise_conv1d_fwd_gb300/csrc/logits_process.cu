@@ -5,9 +5,13 @@
 // them in a bitmap, then goes through the positions, adding the draft that each one follows, eight logits at a time.  Where no
 // lane of a warp has more than two bits they are stored once more, one by one; else all of the warp's logits go through the
 // penalties' arithmetic, which has no branches.  A row's history is read by all of its blocks, from L2 after the first.
+// 64 rows of 5 positions of 131072 bf16 logits with histories of 4000 tokens and a mask take 55 us (3.1 TB/s of what has to be
+// moved): 9 for the histories, 12 for the adjustments, the rest the latency of 1024 blocks at 4 an SM.  A share of 8192 tokens is
+// a table of 32 KB; with 4096 every history is read twice as often, and it took no less.
 //
 // In place and without a mask only the tokens that were seen matter.  Where they are few enough for a hash table in shared memory
 // a block takes a whole row: it counts the history there and goes through the table's slots at each position.
+// 256 rows of 131072 fp32 logits with 4000 tokens take 21 us (by shares 124): two waves of a block's latency.
 #include <algorithm>
 
 #include "ccv_common.cuh"

@@ -10,7 +10,7 @@
 // taken for LANES tokens at once, halving what each lane holds at every step, so that a lane ends with one token's output.
 //
 // 4 x 4096 tokens of 8192 channels with 16 states take 834 us, 1.2 TB/s of what has to be moved.  Nothing in it is at its limit
-// alone: shared memory is busy for 73 % of the time (each lane reads a token's B, C and steps), instructions are issued in 64 % of
+// alone: shared memory is busy for 72 % of the time (each lane reads a token's B, C and steps), instructions are issued in 64 % of
 // the cycles, and the exponentials need 235 us of it (32 a cycle and SM).  More lanes a row, more rows a lane, and exponentials by
 // polynomials on the multiply-add pipes were all slower.  The same for 1009 + 37 + 300 tokens of 2048 channels, in segments of
 // 128: 58 us.

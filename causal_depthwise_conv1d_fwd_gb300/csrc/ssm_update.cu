@@ -9,6 +9,10 @@
 // 128-byte lines, and no shared memory or barrier is needed.  A group of lanes has R rows next to each other; what goes by the row
 // (x, the step, the decay where a head has one, the output) is one lane's work and reaches the others by shuffles, and the sums
 // over the lanes are taken for all rows at once, so that each ends with the lane that its row belongs to.
+//
+// 256 rows of 128 heads of 64 channels with 128 states take 344 us (6.3 TB/s), 64 rows of 4 tokens with every state kept 204, one
+// row 4.  256 rows of 8192 channels with 16 states and a decay for each take 68 (4.2 TB/s): there instructions (61 % of the slots)
+// and latency count as well.
 #include <algorithm>
 
 #include "ssm_common.cuh"
