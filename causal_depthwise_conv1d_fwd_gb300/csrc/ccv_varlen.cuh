@@ -36,7 +36,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
                                  const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The driver's encoder, looked up once (the library links no driver symbols).
+// CUDA's encoder, looked up once (the library links none of libcuda's symbols).
 inline EncodeTiled tensor_map_encoder() {
     static const EncodeTiled fn = [] {
         void *f = nullptr;
