@@ -403,7 +403,11 @@ int check(const ccv_logits_args *a) {
         bad(a->frequency, 1, 0, 1, 0, b) || bad(a->presence, 1, 0, 1, 0, b) || bad(a->bias_ids, b, a->b_stride_b, 1, 0, a->bias_size) ||
         bad(a->bias, b, a->b_stride_b, 1, 0, a->bias_size) || bad(a->mask, b, a->m_stride_b, n, a->m_stride_pos, (v + 31) / 32))
         return CCV_ERR_ALIAS;
-    return CCV_OK;
+    // The output's rows lie apart: positions inside batch rows, or the other way round.
+    const int64_t ob = b > 1 ? a->o_stride_b : 0, op = n > 1 ? a->o_stride_pos : 0;
+    const bool inside = (n == 1 || op >= v) && (b == 1 || ob >= (n - 1) * op + v);
+    const bool around = (b == 1 || ob >= v) && (n == 1 || op >= (b - 1) * ob + v);
+    return inside || around ? CCV_OK : CCV_ERR_STRIDE;
 }
 
 }  // namespace

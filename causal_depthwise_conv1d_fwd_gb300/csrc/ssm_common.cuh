@@ -2,6 +2,7 @@
 // launch.
 #pragma once
 
+#include <algorithm>
 #include <cmath>
 
 #include "ccv_common.cuh"
@@ -54,6 +55,21 @@ inline Extent ssm_extent(const ccv_heads_view &v, int64_t rows, int64_t toks, in
     return Extent{base, base + static_cast<uintptr_t>(last) * size + size - 1};
 }
 
+// Whether each element of a written view has a place of its own: each axis steps over all of those with smaller strides.
+inline bool ssm_apart(const ccv_heads_view &v, int64_t rows, int64_t toks, int64_t heads, int64_t dim) {
+    struct Axis {
+        int64_t stride, count;
+    } axes[4] = {{v.stride_row, rows}, {v.stride_tok, toks}, {v.stride_head, heads}, {v.stride_dim, dim}};
+    std::sort(axes, axes + 4, [](const Axis &a, const Axis &b) { return a.stride < b.stride; });
+    int64_t span = 1;
+    for (const Axis &a : axes) {
+        if (a.count <= 1) continue;
+        if (a.stride < span) return false;
+        span += (a.count - 1) * a.stride;
+    }
+    return true;
+}
+
 // Sizes, strides, pointers and overlaps of a call over `rows` x `toks` tokens.
 inline int ssm_check(const ccv_ssm_args *a, int64_t rows, int64_t toks) {
     if (a == nullptr) return CCV_ERR_NULL_POINTER;
@@ -88,6 +104,14 @@ inline int ssm_check(const ccv_ssm_args *a, int64_t rows, int64_t toks) {
         if (overlaps(ssm_extent(sv, a->num_lines, h, p, n, 4), eo)) return CCV_ERR_ALIAS;
     }
     return CCV_OK;
+}
+
+// That of a call's written tensors, once ssm_check has passed it.
+inline int ssm_check_written(const ccv_ssm_args &a, int64_t rows, int64_t toks) {
+    const ccv_heads_view state{a.state, a.s_stride_line, a.s_stride_head, a.s_stride_dim, a.s_stride_state};
+    const bool apart = ssm_apart(a.out, rows, toks, a.num_heads, a.head_dim) &&
+                       (a.state == nullptr || ssm_apart(state, a.num_lines, a.num_heads, a.head_dim, a.dim_state));
+    return apart ? CCV_OK : CCV_ERR_STRIDE;
 }
 
 // Which tokens and state lines the recurrent kernel's rows use: `seqlen` tokens of a batch row, or a varlen sequence

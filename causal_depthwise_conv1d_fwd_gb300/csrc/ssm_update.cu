@@ -301,13 +301,14 @@ extern "C" int ssm_update(const ccv_ssm_args *args, const int32_t *state_indices
                           int batch, int seqlen, int *err_count, ccv_stream_t stream) {
     using namespace ccv;
     if (batch < 0 || seqlen < 0) return CCV_ERR_SIZE;
-    const int status = ssm_check(args, batch, seqlen);
+    int status = ssm_check(args, batch, seqlen);
     if (status != CCV_OK) return status;
     if (oi_stride_b < 0 || oi_stride_step < 0) return CCV_ERR_STRIDE;
     if (num_accepted_tokens != nullptr && output_state_indices == nullptr) return CCV_ERR_ARGUMENT;
     if (output_state_indices != nullptr && oidx_steps < seqlen) return CCV_ERR_CAPACITY;
     if (batch == 0 || seqlen == 0 || args->num_heads == 0 || args->head_dim == 0 || args->dim_state == 0) return CCV_OK;
     if (args->state == nullptr) return CCV_ERR_NULL_POINTER;
+    if ((status = ssm_check_written(*args, batch, seqlen)) != CCV_OK) return status;
     const SsmRows rows{nullptr,     state_indices,  nullptr,    num_accepted_tokens, output_state_indices,
                        oi_stride_b, oi_stride_step, oidx_steps, batch,               seqlen,
                        0,           err_count};

@@ -27,7 +27,7 @@ extern "C" {
  *               (logits_fp32, out_fp32) fp32.  out may be logits itself (same
  *               pointer, type and strides), where a logit that nothing changes
  *               is neither read nor written; otherwise it must not overlap an
- *               input.
+ *               input.  out's rows must lie apart (CCV_ERR_STRIDE).
  * history       int32 (num_lines, history_size >= 0), stride 1 along a line: the
  *               tokens of a request, its prompt first; NULL: none (then
  *               history_lengths and prompt_lengths are not read).  Row b has

@@ -26,7 +26,9 @@ extern "C" {
  * Layers whose channels each have their own step are heads of head_dim 1.
  *
  * x, z, out     (.., num_heads, head_dim) bf16; z.data NULL: no gate.  out must
- *               not overlap an input.
+ *               not overlap an input.  The elements of out, and those of state,
+ *               lie apart, each axis past those of smaller strides
+ *               (CCV_ERR_STRIDE).
  * B, C          (.., num_groups, dim_state) bf16.
  * dt            (.., num_heads) bf16, or fp32 when dt_fp32 is set.
  * A             fp32, contiguous: [num_heads], or (a_per_state)

@@ -91,6 +91,19 @@ def test_ssm_refusals(lib, call):
     assert call(lib, states=0) == OK
 
 
+@pytest.mark.parametrize("call", [fwd, upd])
+def test_ssm_elements_that_share_places_are_refused(lib, call):
+    """An expanded output or pool, and ones whose axes reach into one another."""
+    assert call(lib, out=(O, 512, 512, 0, 1)) == STRIDE
+    assert call(lib, out=(O, 511, 511, 64, 1)) == STRIDE
+    assert call(lib, out=(O, 512, 512, 64, 0)) == STRIDE
+    assert call(lib, out=(O, 512, 512, 63, 1)) == STRIDE
+    assert call(lib, sl=0) == STRIDE
+    assert call(lib, sl=65535) == STRIDE
+    assert call(lib, sd=64) == STRIDE
+    assert call(lib, ss=0) == STRIDE
+
+
 def test_ssm_fwd_refusals(lib):
     assert fwd(lib, total=-1) == SIZE
     assert fwd(lib, total=(1 << 30) + 1) == SIZE
@@ -158,6 +171,17 @@ def test_logits_refusals(lib):
     assert process(lib, n=0) == OK
     assert process(lib, vocab=0) == OK
     assert lib.logits_process(None, None, None) == NULLP
+
+
+def test_logits_rows_that_share_places_are_refused(lib):
+    """An expanded output, or one whose rows reach into the next."""
+    assert process(lib, ob=0) == STRIDE
+    assert process(lib, op=0) == STRIDE
+    assert process(lib, op=999) == STRIDE
+    assert process(lib, ob=2999) == STRIDE
+    assert process(lib, ob=1000, op=1999) == STRIDE
+    assert process(lib, x=O, xb=0, ob=0) == STRIDE  # in place
+    assert process(lib, ob=0, batch=1, vocab=0) == OK
 
 
 def test_binding_refusals():
