@@ -469,3 +469,21 @@ def test_fwd_sequences_that_share_rates(ccv, path):
     lengths = [i % 4 for i in range(1300)]
     t = make(sum(lengths), 300, 1, 1, 16, 40, per_state=True)
     check_fwd(ccv, t, lengths, init=[i % 3 == 0 for i in range(1300)], channels=True)
+
+
+@pytest.mark.parametrize("states", [32, 50, 100, 128, 130, 200])
+@pytest.mark.parametrize("segment", [0, 1])
+def test_fwd_channels_of_more_states(ccv, path, states, segment):
+    """The token scan's tiles for every width of the state, whole and in segments, with decays a state and one decay a channel."""
+    path("scan", segment)
+    lengths = [300, 0, 17, 129]
+    for channels, per in ((50, True), (35, False)):
+        t = make(sum(lengths), channels, 1, 1, states, 41, per_state=per, gated=per)
+        check_fwd(ccv, t, lengths, init=[True, True, False, True], channels=True)
+
+
+@pytest.mark.parametrize("states", [20, 60, 129, 252])
+@pytest.mark.parametrize("per_state", [False, True])
+def test_update_of_more_states(ccv, states, per_state):
+    check_update(ccv, update_case(3, 2, 5, 7, 1, states, 42, per_state=per_state, gated=True))
+    check_update(ccv, update_case(2, 1, 4, 64, 2, states, 43, per_state=per_state), flat=True)
