@@ -57,16 +57,16 @@ struct Gates {  // of a chunk's tokens: G log2(e) as a pair of floats, the steps
 };
 
 struct Smem {
-    uint8_t x[3][kTile];        // stage; the outputs are written over it
+    uint8_t x[2][kTile];        // stage; the outputs are written over it
     uint8_t b[2][2][kTile];     // stage, panel of 64 states
     uint8_t c[2][kTile];        // panel
-    uint8_t w[2][kTile];        // part: weighted tokens
+    uint8_t w[3][kTile];        // part: weighted tokens
     uint8_t s[2][kTile];        // part: the state
     Gates gates[2];             // stage
     float since[4][Q];          // 32 rows of M: G of the tokens up to them, counted from the rows' first
     // Whoever waits for a chunk's last products has all of what it made for the chunk free again, and one warp issues all products
     // in order: what is not made ahead needs no barrier for its way back.
-    uint64_t in_full[3], x_free[3], b_free[2], c_full, c_free, gates_free[2];  // in: x, B and the steps
+    uint64_t in_full[2], x_free[2], b_free[2], c_full, c_free, gates_free[2];  // in: x, B and the steps
     uint64_t parts_full, m_full, cb_full, sum_full, mx_full, drain;            // parts: of the weighted tokens and the state
     int first_bad[64];          // channel: the first of the block's tokens whose x is not finite
     int any_bad;
@@ -201,11 +201,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     if (tid == 0) {
         sm.abort = sm.any_bad = 0;
         const auto init = [](uint64_t &b, int n) { mbar_init(&b, n); };
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
             init(sm.in_full[i], 2);  // the copies and the steps
             init(sm.x_free[i], kCompute);
-        }
-        for (int i = 0; i < 2; ++i) {
             init(sm.b_free[i], 1);
             init(sm.gates_free[i], kCompute);
         }
@@ -234,14 +232,16 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         for (; c < chunks; ++c) {
             const int st = c & 1, t0 = s + c * Q;
             if (c >= 2 && !wait_all(&sm.b_free[st], (c / 2 - 1) & 1, abort)) break;
-            if (c >= 3 && !wait_all(&sm.x_free[c % 3], (c / 3 - 1) & 1, abort)) break;
             if (lane == 0) {
-                mbar_expect_tx(&sm.in_full[c % 3], 3 * kTile);
-                tensor_load(sm.x[c % 3], &maps.x, panel * 64, h, t0, &sm.in_full[c % 3]);
-                for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.in_full[c % 3]);
+                mbar_expect_tx(&sm.in_full[st], 3 * kTile);
+                for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.in_full[st]);
             }
             __syncwarp();
+            const bool free = c < 2 || wait_all(&sm.x_free[st], (c / 2 - 1) & 1, abort);
+            if (lane == 0) tensor_load(sm.x[st], &maps.x, panel * 64, h, t0, &sm.in_full[st]);  // even if given up: the others wait for the sum
+            __syncwarp();
             issued = c + 1;
+            if (!free) break;
             if (FULL) {
                 if (c >= 1 && !wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
                 load_c(t0);
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         }
         if (c < chunks) {  // gave up: let the copies land before the shared memory goes
             int quiet = 0;
-            for (int i = max(0, issued - 3); i < issued; ++i) wait_all(&sm.in_full[i % 3], (i / 3) & 1, &quiet);
+            for (int i = max(0, issued - 2); i < issued; ++i) wait_all(&sm.in_full[i & 1], (i / 2) & 1, &quiet);
             if (FULL) wait_all(&sm.c_full, max(0, c - 1) & 1, &quiet);
         }
     } else if (warp == kStepWarp) {
@@ -297,15 +297,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             *reinterpret_cast<float4 *>(g.lo + lane * 4) = make_float4(sum[0].y, sum[1].y, sum[2].y, sum[3].y);
             *reinterpret_cast<float4 *>(g.d + lane * 4) = make_float4(d[0], d[1], d[2], d[3]);
             *reinterpret_cast<float4 *>(g.weight + lane * 4) = make_float4(weight[0], weight[1], weight[2], weight[3]);
-            warp_arrive(&sm.in_full[c % 3], lane);
+            warp_arrive(&sm.in_full[c & 1], lane);
         }
     } else if (warp == kIssueWarp) {
         const uint32_t el = elect_lane(), w = desc_low(smem_u32(sm.w[0])), cc = desc_low(smem_u32(sm.c[0])), s0 = desc_low(smem_u32(sm.s[0]));
         bool ok = true;
         for (int c = 0; ok && c < chunks; ++c) {
             const int rows = e - s - c * Q, quarters = quarters_of(rows);
-            const uint32_t b = desc_low(smem_u32(sm.b[c & 1][0])), x = desc_low(smem_u32(sm.x[c % 3]));
-            if (!(ok = wait_all(&sm.in_full[c % 3], (c / 3) & 1, abort))) break;
+            const uint32_t b = desc_low(smem_u32(sm.b[c & 1][0])), x = desc_low(smem_u32(sm.x[c & 1]));
+            if (!(ok = wait_all(&sm.in_full[c & 1], (c / 2) & 1, abort))) break;
             if constexpr (FULL) {  // C B^T
                 if (!(ok = wait_all(&sm.c_full, c & 1, abort))) break;
                 tc_fence_after();
@@ -332,11 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             for (int half = 0; half < 2; ++half)
                 if (half * 64 < rows)
 #pragma unroll
-                    for (int part = 1; part >= 0; --part)
+                    for (int part = 2; part >= 0; --part)
 #pragma unroll
                         for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
                             mma_ss(tmem + kColSum, (b | ((kTile / 16) << 16)) + ks * 2048 / 16, w + (part * kTile + ks * 2048) / 16,
-                                   mma_desc(128, 64, true) | (1u << 15), half > 0 || part < 1 || ks > 0, el);
+                                   mma_desc(128, 64, true) | (1u << 15), half > 0 || part < 2 || ks > 0, el);
             mma_commit(&sm.sum_full, el);
             mma_commit(&sm.b_free[c & 1], el);
             if constexpr (FULL) {  // M x
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         for (c = -1; c < chunks; ++c) {
             const int stage = c & 1, rows = e - s - c * Q, quarters = quarters_of(rows), next = c + 1;
             const Gates &g = sm.gates[stage];
-            uint8_t *xt = sm.x[(c + 3) % 3];
+            uint8_t *xt = sm.x[c & 1];
             float row_decay = 0.0f;
             bool bad = false;
             if (c >= 0) {
@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             }
             if (next < chunks) {
                 const int ns = next & 1, left = e - s - next * Q;
-                if (!(ok = wait_all(&sm.in_full[next % 3], (next / 3) & 1, abort))) break;
-                uint8_t *nx = sm.x[next % 3];
+                if (!(ok = wait_all(&sm.in_full[next & 1], (next / 2) & 1, abort))) break;
+                uint8_t *nx = sm.x[next & 1];
                 if constexpr (FULL) {  // the state's parts for C S
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -530,15 +530,16 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                         for (int j = 0; j < 4; ++j) f[j] = pack2(bf16_lo(word[j]), bf16_hi(word[j]));
                         *reinterpret_cast<uint4 *>(nx + at) = make_uint4(word[0], word[1], word[2], word[3]);
                     }
-                    uint32_t hi[4], mid[4];
+                    uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) split_bf16x2(mul2(f[j], wt), hi[j], mid[j]);
+                    for (int j = 0; j < 4; ++j) split_bf16x3(mul2(f[j], wt), hi[j], mid[j], lo[j]);
                     *reinterpret_cast<uint4 *>(sm.w[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(sm.w[1] + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    *reinterpret_cast<uint4 *>(sm.w[2] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_async_shared();
                 warp_arrive(&sm.parts_full, lane);
-                if (!FULL) warp_arrive(&sm.x_free[next % 3], lane);
+                if (!FULL) warp_arrive(&sm.x_free[next & 1], lane);
             }
             if (c < 0) continue;
 
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     }
                 }
                 fence_async_shared();
-                warp_arrive(&sm.x_free[c % 3], lane);
+                warp_arrive(&sm.x_free[c & 1], lane);
             }
         }
         if (FULL && !ok)  // gave up
