@@ -57,8 +57,8 @@ struct Gates {  // of a chunk's tokens: G log2(e) as a pair of floats, the steps
 };
 
 struct Smem {
-    uint8_t x[2][kTile];        // stage; the outputs are written over it
-    uint8_t b[2][2][kTile];     // stage, panel of 64 states
+    uint8_t x[3][kTile];        // stage; the outputs are written over it
+    uint8_t b[2][kTile];        // panel of 64 states
     uint8_t c[2][kTile];        // panel
     uint8_t w[3][kTile];        // part: weighted tokens
     uint8_t s[2][kTile];        // part: the state
@@ -66,7 +66,7 @@ struct Smem {
     float since[4][Q];          // 32 rows of M: G of the tokens up to them, counted from the rows' first
     // Whoever waits for a chunk's last products has all of what it made for the chunk free again, and one warp issues all products
     // in order: what is not made ahead needs no barrier for its way back.
-    uint64_t in_full[2], x_free[2], b_free[2], c_full, c_free, gates_free[2];  // in: x, B and the steps
+    uint64_t in_full[3], x_free[3], b_full, b_free, c_full, c_free, gates_free[2];  // in: x and the steps
     uint64_t parts_full, m_full, cb_full, sum_full, mx_full, drain;            // parts: of the weighted tokens and the state
     int first_bad[64];          // channel: the first of the block's tokens whose x is not finite
     int any_bad;
@@ -201,15 +201,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     if (tid == 0) {
         sm.abort = sm.any_bad = 0;
         const auto init = [](uint64_t &b, int n) { mbar_init(&b, n); };
-        for (int i = 0; i < 2; ++i) {
-            init(sm.in_full[i], 2);  // the copies and the steps
+        for (int i = 0; i < 3; ++i) {
+            init(sm.in_full[i], 2);  // the copy and the steps
             init(sm.x_free[i], kCompute);
-            init(sm.b_free[i], 1);
-            init(sm.gates_free[i], kCompute);
         }
+        for (int i = 0; i < 2; ++i) init(sm.gates_free[i], kCompute);
         init(sm.parts_full, kCompute);
         init(sm.m_full, kCompute);
-        for (uint64_t *bar : {&sm.c_full, &sm.c_free, &sm.cb_full, &sm.sum_full, &sm.mx_full, &sm.drain}) init(*bar, 1);
+        for (uint64_t *bar : {&sm.b_full, &sm.b_free, &sm.c_full, &sm.c_free, &sm.cb_full, &sm.sum_full, &sm.mx_full, &sm.drain}) init(*bar, 1);
         mbar_init_fence();
     }
     if (tid < 64) sm.first_bad[tid] = INT_MAX;
@@ -221,36 +220,39 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     volatile int *abort = &sm.abort;
 
     if (warp == kCopyWarp) {
-        int issued = 0, c = 0;
-        const auto load_c = [&](int t0) {
-            if (lane == 0) {
-                mbar_expect_tx(&sm.c_full, NP * kTile);
-                for (int i = 0; i < NP; ++i) tensor_load(sm.c[i], &maps.c, i * 64, group, t0, &sm.c_full);
-            }
-            __syncwarp();
-        };
+        int issued = 0, issued_b = 0, issued_c = 0, c = 0;
         for (; c < chunks; ++c) {
-            const int st = c & 1, t0 = s + c * Q;
-            if (c >= 2 && !wait_all(&sm.b_free[st], (c / 2 - 1) & 1, abort)) break;
+            const int t0 = s + c * Q;
+            if (c >= 3 && !wait_all(&sm.x_free[c % 3], (c / 3 - 1) & 1, abort)) break;
             if (lane == 0) {
-                mbar_expect_tx(&sm.in_full[st], 3 * kTile);
-                for (int i = 0; i < 2; ++i) tensor_load(sm.b[st][i], &maps.b, i * 64, group, t0, &sm.in_full[st]);
+                mbar_expect_tx(&sm.in_full[c % 3], kTile);
+                tensor_load(sm.x[c % 3], &maps.x, panel * 64, h, t0, &sm.in_full[c % 3]);
             }
-            __syncwarp();
-            const bool free = c < 2 || wait_all(&sm.x_free[st], (c / 2 - 1) & 1, abort);
-            if (lane == 0) tensor_load(sm.x[st], &maps.x, panel * 64, h, t0, &sm.in_full[st]);  // even if given up: the others wait for the sum
             __syncwarp();
             issued = c + 1;
-            if (!free) break;
-            if (FULL) {
+            // C is free before B, and both early enough: C B^T of the next chunk is wanted a chunk's time later.
+            if constexpr (FULL) {
                 if (c >= 1 && !wait_all(&sm.c_free, (c - 1) & 1, abort)) break;
-                load_c(t0);
+                if (lane == 0) {
+                    mbar_expect_tx(&sm.c_full, NP * kTile);
+                    for (int i = 0; i < NP; ++i) tensor_load(sm.c[i], &maps.c, i * 64, group, t0, &sm.c_full);
+                }
+                __syncwarp();
+                issued_c = c + 1;
             }
+            if (c >= 1 && !wait_all(&sm.b_free, (c - 1) & 1, abort)) break;
+            if (lane == 0) {
+                mbar_expect_tx(&sm.b_full, 2 * kTile);
+                for (int i = 0; i < 2; ++i) tensor_load(sm.b[i], &maps.b, i * 64, group, t0, &sm.b_full);
+            }
+            __syncwarp();
+            issued_b = c + 1;
         }
         if (c < chunks) {  // gave up: let the copies land before the shared memory goes
             int quiet = 0;
-            for (int i = max(0, issued - 2); i < issued; ++i) wait_all(&sm.in_full[i & 1], (i / 2) & 1, &quiet);
-            if (FULL) wait_all(&sm.c_full, max(0, c - 1) & 1, &quiet);
+            for (int i = max(0, issued - 3); i < issued; ++i) wait_all(&sm.in_full[i % 3], (i / 3) & 1, &quiet);
+            if (issued_b > 0) wait_all(&sm.b_full, (issued_b - 1) & 1, &quiet);
+            if (issued_c > 0) wait_all(&sm.c_full, (issued_c - 1) & 1, &quiet);
         }
     } else if (warp == kStepWarp) {
         // A chunk's steps and their sums, four tokens a lane.  What it loads it converts a chunk later.
@@ -297,15 +299,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             *reinterpret_cast<float4 *>(g.lo + lane * 4) = make_float4(sum[0].y, sum[1].y, sum[2].y, sum[3].y);
             *reinterpret_cast<float4 *>(g.d + lane * 4) = make_float4(d[0], d[1], d[2], d[3]);
             *reinterpret_cast<float4 *>(g.weight + lane * 4) = make_float4(weight[0], weight[1], weight[2], weight[3]);
-            warp_arrive(&sm.in_full[c & 1], lane);
+            warp_arrive(&sm.in_full[c % 3], lane);
         }
     } else if (warp == kIssueWarp) {
         const uint32_t el = elect_lane(), w = desc_low(smem_u32(sm.w[0])), cc = desc_low(smem_u32(sm.c[0])), s0 = desc_low(smem_u32(sm.s[0]));
         bool ok = true;
         for (int c = 0; ok && c < chunks; ++c) {
             const int rows = e - s - c * Q, quarters = quarters_of(rows);
-            const uint32_t b = desc_low(smem_u32(sm.b[c & 1][0])), x = desc_low(smem_u32(sm.x[c & 1]));
-            if (!(ok = wait_all(&sm.in_full[c & 1], (c / 2) & 1, abort))) break;
+            const uint32_t b = desc_low(smem_u32(sm.b[0])), x = desc_low(smem_u32(sm.x[c % 3]));
+            if (!(ok = wait_all(&sm.b_full, c & 1, abort))) break;
             if constexpr (FULL) {  // C B^T
                 if (!(ok = wait_all(&sm.c_full, c & 1, abort))) break;
                 tc_fence_after();
@@ -338,9 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                             mma_ss(tmem + kColSum, (b | ((kTile / 16) << 16)) + ks * 2048 / 16, w + (part * kTile + ks * 2048) / 16,
                                    mma_desc(128, 64, true) | (1u << 15), half > 0 || part < 2 || ks > 0, el);
             mma_commit(&sm.sum_full, el);
-            mma_commit(&sm.b_free[c & 1], el);
+            mma_commit(&sm.b_free, el);
             if constexpr (FULL) {  // M x
-                if (!(ok = wait_all(&sm.m_full, c & 1, abort))) break;
+                if (!(ok = wait_all(&sm.m_full, c & 1, abort) && wait_all(&sm.in_full[c % 3], (c / 3) & 1, abort))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         for (c = -1; c < chunks; ++c) {
             const int stage = c & 1, rows = e - s - c * Q, quarters = quarters_of(rows), next = c + 1;
             const Gates &g = sm.gates[stage];
-            uint8_t *xt = sm.x[c & 1];
+            uint8_t *xt = sm.x[(c + 3) % 3];
             float row_decay = 0.0f;
             bool bad = false;
             if (c >= 0) {
@@ -484,8 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             }
             if (next < chunks) {
                 const int ns = next & 1, left = e - s - next * Q;
-                if (!(ok = wait_all(&sm.in_full[next & 1], (next / 2) & 1, abort))) break;
-                uint8_t *nx = sm.x[next & 1];
+                if (!(ok = wait_all(&sm.in_full[next % 3], (next / 3) & 1, abort))) break;
+                if (left < Q && !(ok = wait_all(&sm.b_full, next & 1, abort))) break;  // its other rows become zeros here
+                uint8_t *nx = sm.x[next % 3];
                 if constexpr (FULL) {  // the state's parts for C S
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -507,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     if (row >= left) {
                         x = make_uint4(0u, 0u, 0u, 0u);
                         *reinterpret_cast<uint4 *>(nx + at) = x;
-                        *reinterpret_cast<uint4 *>(sm.b[ns][0] + at) = x;
-                        *reinterpret_cast<uint4 *>(sm.b[ns][1] + at) = x;
+                        *reinterpret_cast<uint4 *>(sm.b[0] + at) = x;
+                        *reinterpret_cast<uint4 *>(sm.b[1] + at) = x;
                     }
                     uint32_t word[4] = {x.x, x.y, x.z, x.w};
                     f32x2 f[4], odd = 0ull;
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 }
                 fence_async_shared();
                 warp_arrive(&sm.parts_full, lane);
-                if (!FULL) warp_arrive(&sm.x_free[next & 1], lane);
+                if (!FULL) warp_arrive(&sm.x_free[next % 3], lane);
             }
             if (c < 0) continue;
 
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     }
                 }
                 fence_async_shared();
-                warp_arrive(&sm.x_free[c & 1], lane);
+                warp_arrive(&sm.x_free[c % 3], lane);
             }
         }
         if (FULL && !ok)  // gave up
