@@ -66,7 +66,7 @@ struct Smem {
     float since[4][Q];          // 32 rows of M: G of the tokens up to them, counted from the rows' first
     // Whoever waits for a chunk's last products has all of what it made for the chunk free again, and one warp issues all products
     // in order: what is not made ahead needs no barrier for its way back.
-    uint64_t in_full[3], x_free[3], b_full, b_free, c_full, c_free, gates_free[2];  // in: x and the steps
+    uint64_t in_full[3], x_free[3], b_full[2], b_free[2], c_full, c_free, gates_free[2];  // in: x and the steps
     uint64_t parts_full, m_full, cb_full, sum_full, mx_full, drain;            // parts: of the weighted tokens and the state
     int first_bad[64];          // channel: the first of the block's tokens whose x is not finite
     int any_bad;
@@ -205,10 +205,14 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             init(sm.in_full[i], 2);  // the copy and the steps
             init(sm.x_free[i], kCompute);
         }
-        for (int i = 0; i < 2; ++i) init(sm.gates_free[i], kCompute);
+        for (int i = 0; i < 2; ++i) {
+            init(sm.gates_free[i], kCompute);
+            init(sm.b_full[i], 1);
+            init(sm.b_free[i], 1);
+        }
         init(sm.parts_full, kCompute);
         init(sm.m_full, kCompute);
-        for (uint64_t *bar : {&sm.b_full, &sm.b_free, &sm.c_full, &sm.c_free, &sm.cb_full, &sm.sum_full, &sm.mx_full, &sm.drain}) init(*bar, 1);
+        for (uint64_t *bar : {&sm.c_full, &sm.c_free, &sm.cb_full, &sm.sum_full, &sm.mx_full, &sm.drain}) init(*bar, 1);
         mbar_init_fence();
     }
     if (tid < 64) sm.first_bad[tid] = INT_MAX;
@@ -218,6 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFullMask, sm.tmem, 0);
     volatile int *abort = &sm.abort;
+    // Stages of B: the states alone have no use for C's place, and are done with a chunk sooner.
+    constexpr int kStages = FULL ? 1 : 2;
+    const auto tile_b = [&](int c, int i) { return c % kStages == 0 ? sm.b[i] : sm.c[i]; };
 
     if (warp == kCopyWarp) {
         int issued = 0, issued_b = 0, issued_c = 0, c = 0;
@@ -240,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 __syncwarp();
                 issued_c = c + 1;
             }
-            if (c >= 1 && !wait_all(&sm.b_free, (c - 1) & 1, abort)) break;
+            if (c >= kStages && !wait_all(&sm.b_free[c % kStages], (c / kStages - 1) & 1, abort)) break;
             if (lane == 0) {
-                mbar_expect_tx(&sm.b_full, 2 * kTile);
-                for (int i = 0; i < 2; ++i) tensor_load(sm.b[i], &maps.b, i * 64, group, t0, &sm.b_full);
+                mbar_expect_tx(&sm.b_full[c % kStages], 2 * kTile);
+                for (int i = 0; i < 2; ++i) tensor_load(tile_b(c, i), &maps.b, i * 64, group, t0, &sm.b_full[c % kStages]);
             }
             __syncwarp();
             issued_b = c + 1;
@@ -251,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         if (c < chunks) {  // gave up: let the copies land before the shared memory goes
             int quiet = 0;
             for (int i = max(0, issued - 3); i < issued; ++i) wait_all(&sm.in_full[i % 3], (i / 3) & 1, &quiet);
-            if (issued_b > 0) wait_all(&sm.b_full, (issued_b - 1) & 1, &quiet);
+            for (int i = max(0, issued_b - kStages); i < issued_b; ++i) wait_all(&sm.b_full[i % kStages], (i / kStages) & 1, &quiet);
             if (issued_c > 0) wait_all(&sm.c_full, (issued_c - 1) & 1, &quiet);
         }
     } else if (warp == kStepWarp) {
@@ -306,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         bool ok = true;
         for (int c = 0; ok && c < chunks; ++c) {
             const int rows = e - s - c * Q, quarters = quarters_of(rows);
-            const uint32_t b = desc_low(smem_u32(sm.b[0])), x = desc_low(smem_u32(sm.x[c % 3]));
-            if (!(ok = wait_all(&sm.b_full, c & 1, abort))) break;
+            const uint32_t b = desc_low(smem_u32(tile_b(c, 0))), x = desc_low(smem_u32(sm.x[c % 3]));
+            if (!(ok = wait_all(&sm.b_full[c % kStages], (c / kStages) & 1, abort))) break;
             if constexpr (FULL) {  // C B^T
                 if (!(ok = wait_all(&sm.c_full, c & 1, abort))) break;
                 tc_fence_after();
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                             mma_ss(tmem + kColSum, (b | ((kTile / 16) << 16)) + ks * 2048 / 16, w + (part * kTile + ks * 2048) / 16,
                                    mma_desc(128, 64, true) | (1u << 15), half > 0 || part < 2 || ks > 0, el);
             mma_commit(&sm.sum_full, el);
-            mma_commit(&sm.b_free, el);
+            mma_commit(&sm.b_free[c % kStages], el);
             if constexpr (FULL) {  // M x
                 if (!(ok = wait_all(&sm.m_full, c & 1, abort) && wait_all(&sm.in_full[c % 3], (c / 3) & 1, abort))) break;
                 tc_fence_after();
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
             if (next < chunks) {
                 const int ns = next & 1, left = e - s - next * Q;
                 if (!(ok = wait_all(&sm.in_full[next % 3], (next / 3) & 1, abort))) break;
-                if (left < Q && !(ok = wait_all(&sm.b_full, next & 1, abort))) break;  // its other rows become zeros here
+                if (left < Q && !(ok = wait_all(&sm.b_full[next % kStages], (next / kStages) & 1, abort))) break;  // its other rows become zeros here
                 uint8_t *nx = sm.x[next % 3];
                 if constexpr (FULL) {  // the state's parts for C S
 #pragma unroll
@@ -510,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     if (row >= left) {
                         x = make_uint4(0u, 0u, 0u, 0u);
                         *reinterpret_cast<uint4 *>(nx + at) = x;
-                        *reinterpret_cast<uint4 *>(sm.b[0] + at) = x;
-                        *reinterpret_cast<uint4 *>(sm.b[1] + at) = x;
+                        *reinterpret_cast<uint4 *>(tile_b(next, 0) + at) = x;
+                        *reinterpret_cast<uint4 *>(tile_b(next, 1) + at) = x;
                     }
                     uint32_t word[4] = {x.x, x.y, x.z, x.w};
                     f32x2 f[4], odd = 0ull;
