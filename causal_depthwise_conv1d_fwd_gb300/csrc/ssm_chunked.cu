@@ -13,17 +13,18 @@
 // Three more warps copy tiles, sum the steps, and issue the products.  Heads wider than 64 are cut into panels of 64.
 //
 // What bounds it: 700 instructions a warp and chunk, on four warps a scheduler (46 % of the issue slots while a block runs); no warp
-// waits for a product any more.  4 x 4096 tokens of 128 heads with 128 states take 346 us, 0.28 of the tensor cores' cycles, where
-// the bytes take 96; 11027 tokens of 32 heads in segments 109 (15); 232 tokens in 4 prompts 10.  On the way here: a role a warpgroup
-// took 1097 us (the hot instructions were twice as many and missed the instruction cache), two heads a block 424 (registers), one
-// with the copies and the steps in one warp 396, with a barrier for every hand-over 383.
+// waits for a product any more.  4 x 4096 tokens of 128 heads with 128 states take 358 us, 0.30 of the tensor cores' cycles, where
+// the bytes take 96; 11027 tokens of 32 heads in segments 121 (15); 232 tokens in 4 prompts 11.  On the way here, still with two
+// parts of the weighted tokens: a role a warpgroup took 1097 us (the hot instructions were twice as many and missed the instruction
+// cache), two heads a block 424 (registers), one with the copies and the steps in one warp 396, with a barrier for every hand-over
+// 383, without either 346.  Three parts with two stages of x and of B took 398, since x came late.
 //
-// Precision.  Every operand that is not bf16 from the start (M, the state in C S, the weighted tokens) enters the tensor cores as
-// two bf16 parts, which hold 16 bits of it: 2^-17 of each term of a sum whose other factors, x, B and C, are exact.  Sums and the
-// state are fp32: the tensor cores' accumulators within a chunk, a multiply-add from chunk to chunk.  The state is 3e-6 of itself
-// off that way, 500 times less than by one part; a third part for the weighted tokens would leave 1e-7 and costs half as many
-// products and instructions again.  Smaller parts are added first, since the tensor cores' sums truncate.  G is summed in pairs
-// of floats, and so are its differences.
+// Precision.  What is not bf16 from the start enters the tensor cores in bf16 parts; the other factors, x, B and C, are exact.  The
+// weighted tokens, which make the state, have three parts, all 24 bits: with two the state was 3e-6 of itself off, with three it is
+// as near as the recurrent forms'.  M and the state in C S reach the outputs alone, which are rounded to 8 bits, and have two parts
+// (2^-17 of each term).  Sums and the state are fp32: the tensor cores' accumulators within a chunk, a multiply-add from chunk to
+// chunk.  Smaller parts are added first, since the tensor cores' sums truncate.  G is summed in pairs of floats, and so are its
+// differences.
 //
 // What is not finite.  A sum over a chunk takes zeros for the tokens after its own, and 0 * NaN is NaN.  So an x that is not
 // finite is left out of the products, and its channel is NaN from that token on, the final state too; a step that is not finite
@@ -711,8 +712,8 @@ bool ssm_chunked_dims(int dim_state, int a_per_state) { return !a_per_state && d
 
 // Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device).  In
 // chunk times of a block (3 us): the first pass takes 0.6 of one a chunk, a block 0.8 to start and end, the two launches more 3.
-// Each pass runs in waves of one block an SM.  11027 tokens of 32 heads take 118 us so and 251 whole, 30000 of 64 493 and 675;
-// 2 x 4000 of 64 heads 138 in two segments and 105 whole.
+// Each pass runs in waves of one block an SM.  11027 tokens of 32 heads take 121 us so and 232 whole, 30000 of 64 507 and 616;
+// 2 x 4000 of 64 heads 137 in two segments and 92 whole.
 int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int num_groups, int head_dim) {
     const char *forced = std::getenv("CCV_SSM_SEGMENT");  // chunks of a segment (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;

@@ -56,11 +56,11 @@ bool mapped(const ccv_heads_view &v, int heads) {
 enum Form { kRecurrent, kChunked, kScan };
 
 // Up to 8 tokens a sequence the recurrent form, whose blocks read and write a state as they are and start at once: 16 (128)
-// sequences of 8 tokens of 32 heads of 64 channels with 128 states take 21 (123) us, chunked 27 (162), and of 16 tokens 35 (215)
-// and 27 (164); 128 of 8 tokens of 4096 channels with 16 states 51, by the scan 126 (a single one 10 and 8).  Above that the
-// tensor cores where one decay a head and the states allow it: 8 x 500 tokens of 32 heads with 16 states take 31 us and by the
-// scan 118, with 64 31 and 214; heads of 8 channels (256 of them, whose tiles are an eighth full) 181 and 442 (but 32 x 60 tokens
-// 307 and 232), and of 4 (512) 450 and 662, but 32 x 60 tokens of those 649 and 332.
+// sequences of 8 tokens of 32 heads of 64 channels with 128 states take 21 (123) us, chunked 27 (166), and of 16 tokens 35 (215)
+// and 27 (168); 128 of 8 tokens of 4096 channels with 16 states 51, by the scan 126 (a single one 10 and 8).  Above that the
+// tensor cores where one decay a head and the states allow it: 8 x 500 tokens of 32 heads with 16 states take 34 us and by the
+// scan 118, with 64 35 and 214; heads of 8 channels (256 of them, whose tiles are an eighth full) 197 and 442 (but 32 x 60 tokens
+// 314 and 232), and of 4 (512) 450 and 662, but 32 x 60 tokens of those 649 and 332.
 // CCV_SSM_PATH=recurrent, =chunked or =scan, read at each call, forces a form where it can run (for testing and tuning).
 Form choose(int total_tokens, int batch, int head_dim, int dim_state, int a_per_state) {
     const char *path = std::getenv("CCV_SSM_PATH");

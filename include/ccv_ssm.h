@@ -70,8 +70,8 @@ typedef struct ccv_ssm_args {
  * Three forms, chosen from the integer sizes: token by token with the state in
  * registers (up to 8 tokens a sequence on average); 128 tokens a step on the
  * tensor cores (one decay a head, dim_state <= 128, head_dim >= 8), where
- * operands of products keep 16 bits and sums 24; a scan of tiles of tokens
- * (the others).  The last two cut sequences into segments where that pays.
+ * what makes the state keeps 24 bits and what makes outputs alone 16; a scan of
+ * tiles of tokens (the others).  The last two cut sequences into segments where that pays.
  * CCV_SSM_PATH=recurrent, =chunked or =scan and CCV_SSM_SEGMENT (128s of
  * tokens, 0: whole sequences) in the environment force a choice where it can
  * run; they are read at each call and by ssm_fwd_workspace.
