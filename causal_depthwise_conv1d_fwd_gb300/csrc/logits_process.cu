@@ -281,10 +281,10 @@ size_t hash_bytes(int slots) { return static_cast<size_t>(slots) * 8; }  // key 
 
 // A block a row, in place and without a mask.  slots: a power of two, at most three quarters of them used.
 template <bool F32, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_row_kernel(const __grid_constant__ ccv_logits_args a, int slots, int *err_count) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_row_kernel(const __grid_constant__ ccv_logits_args a, int slots, int parts, int *err_count) {
     extern __shared__ __align__(16) uint32_t hash[];
     uint32_t *key = hash, *entry = hash + slots;
-    const int tid = threadIdx.x, b = blockIdx.x, shift = 32 - (31 - __clz(slots));
+    const int tid = threadIdx.x, b = blockIdx.x / parts, part = blockIdx.x % parts, shift = 32 - (31 - __clz(slots));
     for (int i = tid; i < slots / 4; i += THREADS) {
         reinterpret_cast<uint4 *>(key)[i] = make_uint4(kNone, kNone, kNone, kNone);
         reinterpret_cast<uint4 *>(entry)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_row_kernel(con
     const int line = a.history_indices != nullptr ? a.history_indices[b] : b;
     if (a.history_indices != nullptr && line == a.pad_slot_id) return;
     if (a.history != nullptr && (line < 0 || line >= a.num_lines)) {
-        if (tid == 0) count_error(err_count);
+        if (tid == 0 && part == 0) count_error(err_count);
         return;
     }
     __syncthreads();
@@ -333,8 +333,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_row_kernel(con
                       a.bias + b * a.b_stride_b,
                       a.bias_size};
     for (int i = tid; i < p.size; i += THREADS) note(p.ids[i], kBiased);
-    for (int pos = 0; pos < a.num_positions; ++pos) {
-        if (pos > 0 && a.draft_tokens != nullptr) {
+    // The part's positions, and the drafts before them; the last part has seen them all.
+    const int first_pos = parts > 1 ? part : 0, end_pos = parts > 1 ? part + 1 : a.num_positions;
+    if (a.draft_tokens != nullptr)
+        for (int i = tid; i < first_pos; i += THREADS) note(a.draft_tokens[b * a.d_stride_b + i * a.d_stride_pos], 0u);
+    for (int pos = first_pos; pos < end_pos; ++pos) {
+        if (pos > first_pos && a.draft_tokens != nullptr) {
             __syncthreads();  // the last position's threads are done with the table
             if (tid == 0) note(a.draft_tokens[b * a.d_stride_b + (pos - 1) * a.d_stride_pos], 0u);
         }
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_row_kernel(con
                 if (token[j] != kNone) store_logit<F32>(a.out, from + token[j], adjust(f[j], entry[i0 + j * THREADS], static_cast<int>(token[j]), p));
         }
     }
-    if (__syncthreads_or(odd) && tid == 0) count_error(err_count);
+    if (__syncthreads_or(odd) && tid == 0 && part == parts - 1) count_error(err_count);
 }
 
 template <bool F32, int THREADS>
@@ -364,7 +368,14 @@ int launch_row_blocks(const ccv_logits_args &a, int slots, int *err_count, cudaS
     current_device_sms(&dev);
     cudaError_t err;
     if (resident_blocks<logits_row_kernel<F32, THREADS>>(THREADS, hash_bytes(kMaxSlots), dev, &err) == 0) return static_cast<int>(err);
-    return launch_pdl(logits_row_kernel<F32, THREADS>, dim3(static_cast<unsigned>(a.batch)), dim3(THREADS), hash_bytes(slots), stream, a, slots, err_count);
+    // A block a position where that takes less time by waves of blocks: a table takes about as long as a position, and a block a row
+    // makes one table for n positions.  5 positions with 4000 tokens: 8 rows 10 us, in a block a row 23; 30 rows 11 and 24; 64 rows
+    // in a block a row 30; with 900 tokens 64 rows 9 and 12.
+    const int64_t room = 152 * (1024 / THREADS), n = a.num_positions;
+    const auto waves = [&](int64_t blocks) { return (blocks + room - 1) / room; };
+    const int parts = 2 * waves(a.batch * n) < waves(a.batch) * (1 + n) && a.batch * n < (1 << 30) ? static_cast<int>(n) : 1;
+    return launch_pdl(logits_row_kernel<F32, THREADS>, dim3(static_cast<unsigned>(a.batch) * parts), dim3(THREADS), hash_bytes(slots), stream, a,
+                      slots, parts, err_count);
 }
 
 // Two blocks of 512 threads fit an SM, and up to 4096 slots are little work: 256 rows of 131072 logits with 300, 900 and 2000

@@ -264,3 +264,9 @@ def test_offsets_past_32_bits(ccv):
     out = torch.empty(2 ** 31 + 2 ** 20, dtype=BF16, device="cuda").as_strided((2, 1, 5000), (2 ** 31 + 64, 5000, 1))
     assert torch.equal(call(ccv, d, logits=far, out=out), want)
     assert torch.equal(call(ccv, d, logits=far, out=far), want)
+
+
+@pytest.mark.parametrize("b,n,size", [(1, 9, 5000), (2, 5, 900), (70, 3, 3000), (330, 3, 900), (200, 2, 5000)])
+def test_positions_of_a_row_in_one_block_and_in_several(ccv, b, n, size):
+    """Without a mask, so that in place a row's table serves all of its positions, or each position has one."""
+    check(ccv, make(b, n, 2001, size, 7 * b + n, bias=3, mask=False))
