@@ -27,9 +27,9 @@
 // differences.
 //
 // What is not finite.  A sum over a chunk takes zeros for the tokens after its own, and 0 * NaN is NaN.  So an x that is not
-// finite is left out of the products, and its channel is NaN from that token on, the final state too; a step that is not finite
-// makes M's rows from its own on, and the state, NaN by itself; so do B and C, whose products are masked and not multiplied by
-// zero.  Rows of the last tile that belong to the next sequence are zeroed.
+// finite is left out of the products, and its channel is NaN from that token on, the final state too; a step that is not
+// finite, or whose rate is NaN, makes M's rows from its own on, and the state, NaN by itself; so do B and C, whose products are
+// masked and not multiplied by zero.  Rows of the last tile that belong to the next sequence are zeroed.
 #include <climits>
 #include <cstdlib>
 #include <cstring>
@@ -122,6 +122,7 @@ __device__ __forceinline__ void steps_of(float (&d)[4], float2 (&g)[4], float bi
         d[i] = i >= real ? 0.0f : d[i] < a.dt_min ? a.dt_min : d[i] > a.dt_max ? a.dt_max : d[i];
         constexpr float kHi = 1.4426950216293335f, kLo = 1.9259629911266175e-8f;  // log2(e)
         float u = d[i] * scale, rest = fmaf(d[i], scale, -u);
+        const bool wrong = !(fabsf(d[i]) < INFINITY) || (i < real && u != u);  // the rate may be NaN, too
         // e^-200 is 0 in fp32 and e^1000 infinite
         if (!(u >= -200.0f && u <= 1000.0f)) {
             u = u < -200.0f ? -200.0f : u > 1000.0f ? 1000.0f : 0.0f;
@@ -129,7 +130,7 @@ __device__ __forceinline__ void steps_of(float (&d)[4], float2 (&g)[4], float bi
         }
         g[i].x = u * kHi;
         g[i].y = fmaf(u, kHi, -g[i].x) + fmaf(u, kLo, rest * kHi);
-        if (!(fabsf(d[i]) < INFINITY)) d[i] = NAN;
+        if (wrong) d[i] = NAN;
     }
 }
 
