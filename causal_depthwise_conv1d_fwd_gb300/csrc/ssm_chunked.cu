@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         // A chunk's steps and their sums, four tokens a lane.  What it loads it converts a chunk later.
         uint32_t raw[4];
         const int shift = a.dt_fp32 ? 0 : 16;
-        const float scale = a.A[h], bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
+        const float scale = bounded_rate(a.A[h]), bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
         const auto fetch = [&](int chunk) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "ccv_common.cuh"
@@ -41,6 +42,13 @@ __device__ __forceinline__ float ssm_step(float raw, float bias, const ccv_ssm_a
 }
 __device__ __forceinline__ float ssm_raw_step(const ccv_ssm_args &a, int64_t off) {
     return a.dt_fp32 ? static_cast<const float *>(a.dt)[off] : bf16_bits(static_cast<const uint16_t *>(a.dt)[off]);
+}
+
+// A rate, or a multiple of one, with fp32's lowest number for minus infinity: a step of 0, as tokens past a tile's end have, then
+// leaves the state (0 times infinity is NaN), and larger ones leave nothing of it.  NaN stays.
+__device__ __forceinline__ float bounded_rate(float a) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-FLT_MAX));
+    return a;
 }
 
 // ------------------------------------------------------------ host side ----

@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan
         for (int j = 0; j < NS; j += 2) {
             const int n = (j / 4) * 4 * LANES + lane * 4 + (j & 3);
             st[q][j / 2] = pack2(some && n < a.dim_state ? from[n * step] : 0.0f, some && n + 1 < a.dim_state ? from[(n + 1) * step] : 0.0f);
-            if (PER) decay[q][j / 2] = pack2(n < a.dim_state ? rates[n] * kLog2e : 0.0f, n + 1 < a.dim_state ? rates[n + 1] * kLog2e : 0.0f);
+            if (PER) decay[q][j / 2] = pack2(n < a.dim_state ? bounded_rate(rates[n] * kLog2e) : 0.0f, n + 1 < a.dim_state ? bounded_rate(rates[n + 1] * kLog2e) : 0.0f);
         }
-        if (!PER) decay[q][0] = pack2(rates[0] * kLog2e, rates[0] * kLog2e);
+        if (!PER) decay[q][0] = pack2(bounded_rate(rates[0] * kLog2e), bounded_rate(rates[0] * kLog2e));
     }
     // The row whose outputs the lane ends with, of every LANES / R-th token.
     const int out_row = row + lane % R, out_tok = lane / R;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(256) ssm_scan_join_kernel(const __grid_constan
     if (line == a.pad_slot_id || (a.state != nullptr && (line < 0 || line >= a.num_lines))) return;
     const int row = static_cast<int>(at / a.dim_state), n = static_cast<int>(at % a.dim_state), h = row / a.head_dim, ch = row % a.head_dim;
     const int segments = (e - s + unit - 1) / unit;
-    const float rate = a.A[a.a_per_state ? static_cast<int64_t>(h) * a.dim_state + n : h];
+    const float rate = bounded_rate(a.A[a.a_per_state ? static_cast<int64_t>(h) * a.dim_state + n : h]);
     float f = 0.0f;
     if (a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0)
         f = a.state[line * a.s_stride_line + h * a.s_stride_head + ch * a.s_stride_dim + n * a.s_stride_state];

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : PER ? 5 : R ==
                         load4<false>(rates, 1, d, a.dim_state, decay[r][j]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) decay[r][j][i] *= kLog2e;
+                    for (int i = 0; i < 4; ++i) decay[r][j][i] = bounded_rate(decay[r][j][i] * kLog2e);
                 }
             }
             if (first_row + r + 1 < rows && ++ch == a.head_dim) {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kSsmThreads, !V || NV > 4 ? 1 : PER ? 5 : R ==
                          first_row + r < rows && !fresh ? a.dim_state : 0, s[r][j]);
         const int h = own_h, ch = own_ch;
         const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f, skip = a.D != nullptr ? a.D[h] : 0.0f;
-        const float rate = PER ? 0.0f : a.A[h] * kLog2e;
+        const float rate = PER ? 0.0f : bounded_rate(a.A[h] * kLog2e);
 
         const auto at = [&](const ccv_heads_view &v, int64_t head, int64_t dim) {
             return static_cast<const uint16_t *>(v.data) + row * v.stride_row + t0 * v.stride_tok + head * v.stride_head + dim * v.stride_dim;

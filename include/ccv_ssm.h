@@ -33,7 +33,9 @@ extern "C" {
  * dt            (.., num_heads) bf16, or fp32 when dt_fp32 is set.
  * A             fp32, contiguous: [num_heads], or (a_per_state)
  *               [num_heads, dim_state].  Decays are meant to be at most 1
- *               (A <= 0 and d >= 0); larger ones hold until fp32 overflows.
+ *               (A <= 0 and d >= 0); larger ones hold until fp32 overflows.  Minus
+ *               infinity counts as fp32's lowest number: a step of 0 leaves the
+ *               state, and one above 1e-36 nothing of it.
  * D, dt_bias    fp32 [num_heads] or NULL (0).
  * dt_min, dt_max  bounds of d (-inf and inf: none; 0 and inf are usual).
  * state         pool (num_lines, num_heads, head_dim, dim_state) fp32.
