@@ -122,7 +122,6 @@ __device__ __forceinline__ void steps_of(float (&d)[4], float2 (&g)[4], float bi
         d[i] = i >= real ? 0.0f : d[i] < a.dt_min ? a.dt_min : d[i] > a.dt_max ? a.dt_max : d[i];
         constexpr float kHi = 1.4426950216293335f, kLo = 1.9259629911266175e-8f;  // log2(e)
         float u = d[i] * scale, rest = fmaf(d[i], scale, -u);
-        const bool wrong = !(fabsf(d[i]) < INFINITY) || (i < real && u != u);  // the rate may be NaN, too
         // e^-200 is 0 in fp32 and e^1000 infinite
         if (!(u >= -200.0f && u <= 1000.0f)) {
             u = u < -200.0f ? -200.0f : u > 1000.0f ? 1000.0f : 0.0f;
@@ -130,7 +129,7 @@ __device__ __forceinline__ void steps_of(float (&d)[4], float2 (&g)[4], float bi
         }
         g[i].x = u * kHi;
         g[i].y = fmaf(u, kHi, -g[i].x) + fmaf(u, kLo, rest * kHi);
-        if (wrong) d[i] = NAN;
+        if (!(fabsf(d[i]) < INFINITY)) d[i] = NAN;
     }
 }
 
@@ -267,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
         // A chunk's steps and their sums, four tokens a lane.  What it loads it converts a chunk later.
         uint32_t raw[4];
         const int shift = a.dt_fp32 ? 0 : 16;
-        const float scale = bounded_rate(a.A[h]), bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
+        const float scale = bounded_rate(a.A[h]);
+        const float bias = scale != scale ? NAN : a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;  // a rate that is NaN shows in the steps
         const auto fetch = [&](int chunk) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
