@@ -122,6 +122,14 @@ inline int ssm_check_written(const ccv_ssm_args &a, int64_t rows, int64_t toks) 
     return apart ? CCV_OK : CCV_ERR_STRIDE;
 }
 
+// The arguments with limits that do not cross: min(max(d, lo), hi) is hi throughout where lo is above hi, and the kernels compare
+// with lo first.
+inline ccv_ssm_args ssm_ordered(const ccv_ssm_args &args) {
+    ccv_ssm_args a = args;
+    if (a.dt_min > a.dt_max) a.dt_min = a.dt_max;
+    return a;
+}
+
 // Which tokens and state lines the recurrent kernel's rows use: `seqlen` tokens of a batch row, or a varlen sequence
 // when query_start_loc is set.
 struct SsmRows {

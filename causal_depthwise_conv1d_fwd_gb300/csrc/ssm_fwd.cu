@@ -103,7 +103,7 @@ extern "C" int ssm_fwd(const ccv_ssm_args *args, const int32_t *query_start_loc,
     if (batch == 0 || total_tokens == 0 || args->num_heads == 0 || args->head_dim == 0 || args->dim_state == 0) return CCV_OK;
     if (query_start_loc == nullptr) return CCV_ERR_NULL_POINTER;
     if ((status = ssm_check_written(*args, 1, total_tokens)) != CCV_OK) return status;
-    const ccv_ssm_args &a = *args;
+    const ccv_ssm_args a = ssm_ordered(*args);
     const bool copies = !mapped(a.x, a.num_heads) || !mapped(a.B, a.num_groups) || !mapped(a.C, a.num_groups);
     const int64_t need = ssm_fwd_workspace(total_tokens, batch, a.num_heads, a.num_groups, a.head_dim, a.dim_state, a.a_per_state, copies);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 127u) != 0))

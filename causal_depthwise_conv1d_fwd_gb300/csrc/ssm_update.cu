@@ -312,5 +312,5 @@ extern "C" int ssm_update(const ccv_ssm_args *args, const int32_t *state_indices
     const SsmRows rows{nullptr,     state_indices,  nullptr,    num_accepted_tokens, output_state_indices,
                        oi_stride_b, oi_stride_step, oidx_steps, batch,               seqlen,
                        0,           err_count};
-    return ssm_launch_recurrent(*args, rows, stream);
+    return ssm_launch_recurrent(ssm_ordered(*args), rows, stream);
 }
