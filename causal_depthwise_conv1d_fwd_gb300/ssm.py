@@ -16,6 +16,7 @@ from .layer import (_BF16, _F32, _I32, _U8, _Tensor, _call, _device, _empty_like
 # struct ccv_ssm_args of include/ccv_ssm.h, packed into bytes as in :mod:`.layer`.
 _SSM = struct.Struct("<" + "Qqqqq" * 5 + "Qqqq" + "QQQ" + "Qqqqq" + "ff" + "i" * 9 + "4x")
 _NO_LIMIT = (0.0, float("inf"))
+_MAX = torch.finfo(torch.float32).max
 
 
 def _pack_ssm(x, dt, A, B, C, state, D, z, dt_bias, dt_softplus, dt_limit, pad_slot_id, out, lead):
@@ -70,6 +71,10 @@ def _pack_ssm(x, dt, A, B, C, state, D, z, dt_bias, dt_softplus, dt_limit, pad_s
         if out.shape != xs:
             raise ValueError("out must have x's shape")
     lo, hi = dt_limit
+    if hi > _MAX:  # no limit, which fp32 has a value for
+        hi = _NO_LIMIT[1]
+    if lo < -_MAX:
+        lo = -_NO_LIMIT[1]
     # row, token, head and dim strides: ssm_fwd's tokens are flat (no row), and a row of ssm_update
     # has one token, or as many as there are
     v, o, b, c, d = x.stride(), out.stride(), B.stride(), C.stride(), dt.stride()

@@ -40,3 +40,11 @@ def test_limits_that_cross(ccv, path, form, per_state, update):  # noqa: F811
                                                 pool(1, h, p, n, 60)[0].double(), t["D"])
         ref.assert_out(want[0], out, bound)
         ref.assert_state(want[1][0], state, mag)
+
+
+@pytest.mark.parametrize("limit", [(0.0, 1e300), (-1e300, INF), (-1e300, 1e300)])
+def test_limits_past_fp32_are_none(ccv, limit):  # noqa: F811
+    t = make(70, 3, 64, 1, 128, 62)
+    for update in (False, True):
+        want, got = run(ccv, t, (0.0, INF), update), run(ccv, t, limit, update)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
