@@ -481,7 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                 }
                 tc_fence_before();
                 whole *= gamma;
-                bad = sm.any_bad != 0;  // what this chunk has is noted before sum_full
+                // What this chunk has is noted before sum_full.  Another warp may be noting the next chunk's meanwhile, so the lanes
+                // vote: those of a row store it together below.
+                bad = __any_sync(kFullMask, sm.any_bad != 0);
                 if (bad) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
