@@ -717,7 +717,7 @@ bool ssm_chunked_dims(int dim_state, int a_per_state) { return !a_per_state && d
 // chunk times of a block (3 us): the first pass takes 0.6 of one a chunk, a block 0.8 to start and end, the two launches more 3.
 // Each pass runs in waves of one block an SM.  11027 tokens of 32 heads take 121 us so and 232 whole, 30000 of 64 507 and 616;
 // 2 x 4000 of 64 heads 137 in two segments and 92 whole.
-int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int num_groups, int head_dim) {
+int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int head_dim) {
     const char *forced = std::getenv("CCV_SSM_SEGMENT");  // chunks of a segment (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;
     constexpr int kSms = 152;  // a GB300's: the workspace's size may not depend on the device that is current

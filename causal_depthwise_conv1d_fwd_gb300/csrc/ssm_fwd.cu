@@ -87,7 +87,7 @@ extern "C" int64_t ssm_fwd_workspace(int total_tokens, int batch, int num_heads,
         return ssm_scan_workspace(total_tokens, batch, num_heads, head_dim, dim_state,
                                   ssm_scan_segments(total_tokens, batch, num_heads, num_groups, head_dim, dim_state));
     int64_t bytes = ssm_chunked_workspace(total_tokens, batch, num_heads, head_dim,
-                                          ssm_chunked_segments(total_tokens, batch, num_heads, num_groups, head_dim));
+                                          ssm_chunked_segments(total_tokens, batch, num_heads, head_dim));
     if (copies) bytes += copy_bytes(total_tokens, num_heads, head_dim) + 2 * copy_bytes(total_tokens, num_groups, dim_state);
     return bytes;
 }
@@ -115,7 +115,7 @@ extern "C" int ssm_fwd(const ccv_ssm_args *args, const int32_t *query_start_loc,
     }
     SsmFwd p{a, query_start_loc, cache_indices, has_initial_state, batch, total_tokens, err_count,
              form == kScan ? ssm_scan_segments(total_tokens, batch, a.num_heads, a.num_groups, a.head_dim, a.dim_state)
-                           : ssm_chunked_segments(total_tokens, batch, a.num_heads, a.num_groups, a.head_dim),
+                           : ssm_chunked_segments(total_tokens, batch, a.num_heads, a.head_dim),
              nullptr, nullptr};
     if (form == kScan) return ssm_launch_scan(p, workspace, stream);
     if (copies) {

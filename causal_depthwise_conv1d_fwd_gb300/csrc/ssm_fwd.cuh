@@ -19,7 +19,7 @@ struct SsmFwd {
 // The chunked form: one decay a head, dim_state up to 128, x, B and C as tensor maps take them.
 bool ssm_chunked_dims(int dim_state, int a_per_state);
 int64_t ssm_chunked_workspace(int total_tokens, int batch, int num_heads, int head_dim, int seg_chunks);
-int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int num_groups, int head_dim);
+int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int head_dim);
 int ssm_launch_chunked(const SsmFwd &p, void *workspace, cudaStream_t stream);
 
 // The scan: any sizes and strides.

@@ -1,8 +1,8 @@
 // Selective state space scan over varlen sequences (prefill), token by token, for layers whose channels each have their own
 // step and a decay for every state, and for whatever else the chunked form does not take.
 //
-// A row (head h, channel p) has dim_state states in the registers of LANES lanes; a block has 128 / LANES rows of one group of
-// one sequence (or segment) and goes through its tokens in tiles of 32 (16).  The tile's inputs come to registers while the one
+// A row (head h, channel p) has dim_state states in the registers of LANES lanes; a block has 32 (16) rows of one group of one
+// sequence (or segment), in 128 or 256 threads, and goes through its tokens in tiles of 32 (16).  The tile's inputs come to registers while the one
 // before is worked on; from there the steps (one a row and token, where the lanes would each repeat it) go to shared memory as
 // pairs d, d x, and B and C as floats.  For a token a lane then needs
 //     e = 2^{d A log2 e},   s <- e s + (d x) B,   y += s C
@@ -26,9 +26,9 @@ namespace {
 
 constexpr int kUnit = 128;    // tokens of a segment's unit
 
-template <int LANES, int NS, int R, int ROWS, int TOKENS>
+template <int LANES, int NS, int ROWS, int TOKENS>
 struct ScanSmem {
-    static constexpr int rows = ROWS, states = LANES * NS, T = TOKENS, threads = LANES * ROWS / R;
+    static constexpr int rows = ROWS, states = LANES * NS, T = TOKENS, threads = LANES * ROWS;
     float2 step[T][rows];        // d, d x; two rows' pairs (16 bytes) are at place_of(row / 2)
     // A thread writes eight rows of a token, so the eight threads of a token write 64 bytes apart: the places' low bits spread
     // them over the banks, and leave the rows of a warp's loads side by side.
@@ -62,17 +62,17 @@ __device__ __forceinline__ uint4 load8(const ccv_heads_view &v, int64_t tok, int
 
 // FULL: outputs and the sequences' final states; otherwise segments' own states and the sums of their steps, for the join.
 // LANES x NS: dim_state rounded up.  PER: A has a value a state.
-template <int LANES, int NS, int R, int ROWS, int TOKENS, bool PER, bool FULL>
-__global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan_kernel(const __grid_constant__ SsmFwd p, const __grid_constant__ ScanVec vec) {
-    using S = ScanSmem<LANES, NS, R, ROWS, TOKENS>;
+template <int LANES, int NS, int ROWS, int TOKENS, bool PER, bool FULL>
+__global__ void __launch_bounds__(LANES * ROWS, LANES == 4 ? 7 : 1) ssm_scan_kernel(const __grid_constant__ SsmFwd p, const __grid_constant__ ScanVec vec) {
+    using S = ScanSmem<LANES, NS, ROWS, TOKENS>;
     constexpr int T = S::T, kRows = S::rows, kThreads = S::threads, kPieces = kRows / 8;
     constexpr int kLoads = (T * kPieces + kThreads - 1) / kThreads;              // groups of 8 rows that a thread brings
-    constexpr int kAllQuads = T * S::states / 4, kQuads = (kAllQuads + kThreads - 1) / kThreads;  // and of 4 states
-    static_assert(kPieces >= 1 && kThreads % kPieces == 0 && T % LANES == 0 && LANES % R == 0 && ROWS % R == 0, "");
+    constexpr int kQuads = T * S::states / 4 / kThreads;                         // and of 4 states
+    static_assert(kPieces >= 1 && kThreads % kPieces == 0 && T % LANES == 0 && T * S::states / 4 % kThreads == 0, "");
     __shared__ S sm;
     const ccv_ssm_args &a = p.a;
     const int tid = threadIdx.x, lane = tid % 32 / (32 / LANES);
-    const int row = (tid / 32 * (32 / LANES) + tid % (32 / LANES)) * R;  // the first of the lane's rows
+    const int row = tid / 32 * (32 / LANES) + tid % (32 / LANES);
     const int rep = a.num_heads / a.num_groups, group_rows = rep * a.head_dim;
     const int per_group = (group_rows + kRows - 1) / kRows, blocks = a.num_groups * per_group;
     const int unit = blockIdx.x / blocks, rest = blockIdx.x % blocks;
@@ -124,41 +124,37 @@ __global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan
         if (!last) e = s + unit_tokens;
     }
 
-    // The lane's R rows of the state: states j * 4 LANES + 4 lane + i.
+    // The lane's states of its row: j * 4 LANES + 4 lane + i.
     const int all_rows = a.num_heads * a.head_dim;
-    const auto pool_at = [&](int r) {
+    const int r = r0 + row, row_head = head0 + (r < group_rows ? r / a.head_dim : 0);
+    const auto pool_at = [&] {
         const int h = r / a.head_dim;
         return a.state + line * a.s_stride_line + (head0 + h) * a.s_stride_head + (r - h * a.head_dim) * a.s_stride_dim;
     };
-    const auto slot_at = [&](int r) { return p.seg_state + (static_cast<int64_t>(unit) * all_rows + head0 * a.head_dim + r) * S::states; };
-    f32x2 st[R][NS / 2], decay[R][PER ? NS / 2 : 1];
+    const auto slot_at = [&] { return p.seg_state + (static_cast<int64_t>(unit) * all_rows + head0 * a.head_dim + r) * S::states; };
+    f32x2 st[NS / 2], decay[PER ? NS / 2 : 1];
     const bool kept = FULL && segments > 1, init = FULL && a.state != nullptr && p.has_initial_state != nullptr && p.has_initial_state[seq] != 0;
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-        const int r = r0 + row + q;
-        const bool real = r < group_rows, some = real && (kept || init);
-        const float *from = !some ? a.A : kept ? slot_at(r) : pool_at(r);
+    {
+        const bool some = r < group_rows && (kept || init);
+        const float *from = !some ? a.A : kept ? slot_at() : pool_at();
         const int64_t step = kept ? 1 : a.s_stride_state;
-        const float *rates = a.A + static_cast<int64_t>(head0 + (real ? r / a.head_dim : 0)) * (PER ? a.dim_state : 1);
+        const float *rates = a.A + static_cast<int64_t>(row_head) * (PER ? a.dim_state : 1);
 #pragma unroll
         for (int j = 0; j < NS; j += 2) {
             const int n = (j / 4) * 4 * LANES + lane * 4 + (j & 3);
-            st[q][j / 2] = pack2(some && n < a.dim_state ? from[n * step] : 0.0f, some && n + 1 < a.dim_state ? from[(n + 1) * step] : 0.0f);
-            if (PER) decay[q][j / 2] = pack2(n < a.dim_state ? bounded_rate(rates[n] * kLog2e) : 0.0f, n + 1 < a.dim_state ? bounded_rate(rates[n + 1] * kLog2e) : 0.0f);
+            st[j / 2] = pack2(some && n < a.dim_state ? from[n * step] : 0.0f, some && n + 1 < a.dim_state ? from[(n + 1) * step] : 0.0f);
+            if (PER) decay[j / 2] = pack2(n < a.dim_state ? bounded_rate(rates[n] * kLog2e) : 0.0f, n + 1 < a.dim_state ? bounded_rate(rates[n + 1] * kLog2e) : 0.0f);
         }
-        if (!PER) decay[q][0] = pack2(bounded_rate(rates[0] * kLog2e), bounded_rate(rates[0] * kLog2e));
+        if (!PER) decay[0] = pack2(bounded_rate(rates[0] * kLog2e), bounded_rate(rates[0] * kLog2e));
     }
-    // The row whose outputs the lane ends with, of every LANES / R-th token.
-    const int out_row = row + lane % R, out_tok = lane / R;
-    const float skip = FULL && a.D != nullptr && r0 + out_row < group_rows ? a.D[head0 + (r0 + out_row) / a.head_dim] : 0.0f;
+    const float skip = FULL && a.D != nullptr && r < group_rows ? a.D[row_head] : 0.0f;
 
     // The next tile's inputs: token tid / kPieces (+ ..), 8 rows.
     const int piece = tid % kPieces, tok = tid / kPieces, at = r0 + piece * 8;
     const auto loads = [&](int l) { return tok + l * (kThreads / kPieces) < T; };
     constexpr int kStep = kThreads / kPieces;  // tokens between a thread's loads
     uint4 xr[kLoads], zr[kLoads], dr[kLoads][2];
-    constexpr bool kAhead = kQuads <= 4;
-    uint2 br[kAhead ? kQuads : 1], cr[kAhead ? kQuads : 1];
+    uint2 br[kQuads], cr[kQuads];
     auto load_quad = [&](const ccv_heads_view &v, int64_t t, int n) {
         const uint16_t *src = static_cast<const uint16_t *>(v.data) + t * v.stride_tok + group * v.stride_head + n * v.stride_dim;
         if (vec.bc && n + 4 <= a.dim_state) return __ldg(reinterpret_cast<const uint2 *>(src));
@@ -202,15 +198,12 @@ __global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan
                 }
             }
         }
-        if constexpr (kAhead) {
 #pragma unroll
-            for (int i = 0; i < kQuads; ++i) {
-                const int quad = tid + i * kThreads, n = quad % (S::states / 4) * 4;
-                const int64_t t = t0 + quad / (S::states / 4);
-                const bool in = t < e && (kAllQuads % kThreads == 0 || quad < kAllQuads);
-                br[i] = in ? load_quad(a.B, t, n) : make_uint2(0u, 0u);
-                if (FULL) cr[i] = in ? load_quad(a.C, t, n) : make_uint2(0u, 0u);
-            }
+        for (int i = 0; i < kQuads; ++i) {
+            const int quad = tid + i * kThreads, n = quad % (S::states / 4) * 4;
+            const int64_t t = t0 + quad / (S::states / 4);
+            br[i] = t < e ? load_quad(a.B, t, n) : make_uint2(0u, 0u);
+            if (FULL) cr[i] = t < e ? load_quad(a.C, t, n) : make_uint2(0u, 0u);
         }
     };
     f32x2 bias[4];
@@ -221,13 +214,8 @@ __global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan
     }
     const bool limits = a.dt_max < INFINITY || !(a.dt_min <= (a.dt_softplus ? 0.0f : -INFINITY));
     auto widen = [](uint2 w) { return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)); };
-    float sum_d[R];  // of the rows' steps
-    int row_at[R];
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-        sum_d[q] = 0.0f;
-        row_at[q] = 2 * S::place_of((row + q) / 2) + ((row + q) & 1);
-    }
+    float sum_d = 0.0f;  // of the row's steps
+    const int row_at = 2 * S::place_of(row / 2) + (row & 1);
 
     fetch(s);
     for (int t0 = s; t0 < e; t0 += T) {
@@ -265,87 +253,52 @@ __global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
             const int quad = tid + i * kThreads, at_n = quad % (S::states / 4) * 4, t = quad / (S::states / 4);
-            if (kAllQuads % kThreads != 0 && quad >= kAllQuads) continue;
-            uint2 bw = make_uint2(0u, 0u), cw = bw;
-            if constexpr (kAhead) {
-                bw = br[i];
-                if (FULL) cw = cr[i];
-            } else if (t < n) {
-                bw = load_quad(a.B, t0 + t, at_n);
-                if (FULL) cw = load_quad(a.C, t0 + t, at_n);
-            }
-            *reinterpret_cast<float4 *>(&sm.b[t][at_n]) = widen(bw);
-            if (FULL) *reinterpret_cast<float4 *>(&sm.c[t][at_n]) = widen(cw);
+            *reinterpret_cast<float4 *>(&sm.b[t][at_n]) = widen(br[i]);
+            if (FULL) *reinterpret_cast<float4 *>(&sm.c[t][at_n]) = widen(cr[i]);
         }
         __syncthreads();
         if (t0 + T < e) fetch(t0 + T);
 
         // Sums first and outputs after them: a store to shared memory would keep the next tokens' loads behind it.
-        constexpr int kTogether = LANES / R;  // tokens whose sums are taken together
-        float sums[T / kTogether];
+        float sums[T / LANES];
 #pragma unroll
-        for (int g = 0; g < T; g += kTogether) {
+        for (int g = 0; g < T; g += LANES) {  // tokens whose sums are taken together
             float y[LANES];
 #pragma unroll
-            for (int l = 0; l < kTogether; ++l) {
-                f32x2 d2[R], dx2[R], acc[R], same[R];
-                if constexpr (R % 2 == 0) {
-#pragma unroll
-                    for (int q = 0; q < R; q += 2) {
-                        const float4 step = *reinterpret_cast<const float4 *>(&sm.step[g + l][row_at[q]]);
-                        d2[q] = pack2(step.x, step.x);
-                        dx2[q] = pack2(step.y, step.y);
-                        d2[q + 1] = pack2(step.z, step.z);
-                        dx2[q + 1] = pack2(step.w, step.w);
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < R; ++q) {
-                        const float2 step = sm.step[g + l][row_at[q]];
-                        d2[q] = pack2(step.x, step.x);
-                        dx2[q] = pack2(step.y, step.y);
-                    }
+            for (int l = 0; l < LANES; ++l) {
+                const float2 step = sm.step[g + l][row_at];
+                const f32x2 d2 = pack2(step.x, step.x), dx2 = pack2(step.y, step.y);
+                f32x2 acc = 0ull, same = 0ull;
+                if constexpr (!PER) {
+                    float u0, u1;
+                    unpack2(mul2(d2, decay[0]), u0, u1);
+                    const float a1 = ex2_approx(u0);
+                    same = pack2(a1, a1);
                 }
-#pragma unroll
-                for (int q = 0; q < R; ++q) {
-                    acc[q] = same[q] = 0ull;
-                    if constexpr (!PER) {
-                        float u0, u1;
-                        unpack2(mul2(d2[q], decay[q][0]), u0, u1);
-                        const float a1 = ex2_approx(u0);
-                        same[q] = pack2(a1, a1);
-                    }
-                    if (!FULL) sum_d[q] += __uint_as_float(static_cast<uint32_t>(d2[q]));
-                }
+                if (!FULL) sum_d += step.x;
 #pragma unroll
                 for (int j = 0; j < NS; j += 4) {
                     const ulonglong2 b2 = *reinterpret_cast<const ulonglong2 *>(&sm.b[g + l][j * LANES + lane * 4]);
                     ulonglong2 c2 = make_ulonglong2(0ull, 0ull);
                     if (FULL) c2 = *reinterpret_cast<const ulonglong2 *>(&sm.c[g + l][j * LANES + lane * 4]);
-#pragma unroll
-                    for (int q = 0; q < R; ++q) {
-                        f32x2 e0 = same[q], e1 = same[q];
-                        if constexpr (PER) {
-                            float u0, u1, u2, u3;
-                            unpack2(mul2(d2[q], decay[q][j / 2]), u0, u1);
-                            unpack2(mul2(d2[q], decay[q][j / 2 + 1]), u2, u3);
-                            e0 = pack2(ex2_approx(u0), ex2_approx(u1));
-                            e1 = pack2(ex2_approx(u2), ex2_approx(u3));
-                        }
-                        st[q][j / 2] = fma2(e0, st[q][j / 2], mul2(dx2[q], b2.x));
-                        st[q][j / 2 + 1] = fma2(e1, st[q][j / 2 + 1], mul2(dx2[q], b2.y));
-                        if constexpr (FULL) {
-                            acc[q] = j == 0 ? mul2(st[q][0], c2.x) : fma2(st[q][j / 2], c2.x, acc[q]);
-                            acc[q] = fma2(st[q][j / 2 + 1], c2.y, acc[q]);
-                        }
+                    f32x2 e0 = same, e1 = same;
+                    if constexpr (PER) {
+                        float u0, u1, u2, u3;
+                        unpack2(mul2(d2, decay[j / 2]), u0, u1);
+                        unpack2(mul2(d2, decay[j / 2 + 1]), u2, u3);
+                        e0 = pack2(ex2_approx(u0), ex2_approx(u1));
+                        e1 = pack2(ex2_approx(u2), ex2_approx(u3));
+                    }
+                    st[j / 2] = fma2(e0, st[j / 2], mul2(dx2, b2.x));
+                    st[j / 2 + 1] = fma2(e1, st[j / 2 + 1], mul2(dx2, b2.y));
+                    if constexpr (FULL) {
+                        acc = j == 0 ? mul2(st[0], c2.x) : fma2(st[j / 2], c2.x, acc);
+                        acc = fma2(st[j / 2 + 1], c2.y, acc);
                     }
                 }
-#pragma unroll
-                for (int q = 0; q < R; ++q) {
-                    float lo, hi;
-                    unpack2(acc[q], lo, hi);
-                    y[l * R + q] = lo + hi;
-                }
+                float lo, hi;
+                unpack2(acc, lo, hi);
+                y[l] = lo + hi;
             }
             if constexpr (FULL) {
                 // y[i] summed over the lanes for lane i: at each step a lane keeps the half of the sums that has its bit
@@ -357,16 +310,16 @@ __global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan
                         const float keep = upper ? y[l + m] : y[l], give = upper ? y[l] : y[l + m];
                         y[l] = keep + __shfl_xor_sync(kFullMask, give, m * (32 / LANES));
                     }
-                sums[g / kTogether] = y[0];
+                sums[g / LANES] = y[0];
             }
         }
         if constexpr (FULL) {
 #pragma unroll
-            for (int g = 0; g < T; g += kTogether) {
-                const int t = g + out_tok;
-                float o = fmaf(skip, bf16_bits(sm.x[t][out_row]), sums[g / kTogether]);
-                if (a.z.data != nullptr) o *= silu(bf16_bits(sm.z[t][out_row]));
-                sm.x[t][out_row] = round_bf16(o);
+            for (int g = 0; g < T; g += LANES) {
+                const int t = g + lane;
+                float o = fmaf(skip, bf16_bits(sm.x[t][row]), sums[g / LANES]);
+                if (a.z.data != nullptr) o *= silu(bf16_bits(sm.z[t][row]));
+                sm.x[t][row] = round_bf16(o);
             }
         }
         __syncthreads();
@@ -393,24 +346,20 @@ __global__ void __launch_bounds__(LANES * ROWS / R, LANES == 4 ? 7 : 1) ssm_scan
         }
     }
 
+    if (r >= group_rows) return;
+    if (!FULL || (last && a.state != nullptr)) {
+        float *to = FULL ? pool_at() : slot_at();
+        const int64_t step = FULL ? a.s_stride_state : 1;
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-        const int r = r0 + row + q;
-        if (r >= group_rows) continue;
-        if (!FULL || (last && a.state != nullptr)) {
-            float *to = FULL ? pool_at(r) : slot_at(r);
-            const int64_t step = FULL ? a.s_stride_state : 1;
-#pragma unroll
-            for (int j = 0; j < NS; j += 2) {
-                const int n = (j / 4) * 4 * LANES + lane * 4 + (j & 3);
-                float f0, f1;
-                unpack2(st[q][j / 2], f0, f1);
-                if (n < a.dim_state) to[n * step] = f0;
-                if (n + 1 < a.dim_state) to[(n + 1) * step] = f1;
-            }
+        for (int j = 0; j < NS; j += 2) {
+            const int n = (j / 4) * 4 * LANES + lane * 4 + (j & 3);
+            float f0, f1;
+            unpack2(st[j / 2], f0, f1);
+            if (n < a.dim_state) to[n * step] = f0;
+            if (n + 1 < a.dim_state) to[(n + 1) * step] = f1;
         }
-        if (!FULL && lane == 0) p.seg_decay[static_cast<int64_t>(unit) * all_rows + head0 * a.head_dim + r] = sum_d[q];
     }
+    if (!FULL && lane == 0) p.seg_decay[static_cast<int64_t>(unit) * all_rows + head0 * a.head_dim + r] = sum_d;
 }
 
 // The segments' first states, one after the other, from their own: F <- e^{A sum of d} F + own, a thread a row and state; the
@@ -451,22 +400,22 @@ int64_t segment_slots(int total_tokens, int batch, int seg_units) {
 // States that a row has room for.
 int padded_states(int dim_state) { return dim_state <= 16 ? 16 : dim_state <= 32 ? 32 : dim_state <= 64 ? 64 : dim_state <= 128 ? 128 : 256; }
 
-template <int LANES, int NS, int R, int ROWS, int TOKENS, bool PER>
+template <int LANES, int NS, int ROWS, int TOKENS, bool PER>
 int launch_scan(const SsmFwd &p, const ScanVec &vec, cudaStream_t stream) {
     const int rows = ROWS, group_rows = p.a.num_heads / p.a.num_groups * p.a.head_dim;
     const int64_t blocks = static_cast<int64_t>(p.a.num_groups) * ((group_rows + rows - 1) / rows);
     const int64_t units = p.seg_chunks > 0 ? segment_slots(p.total_tokens, p.batch, p.seg_chunks) : p.batch;
     if (blocks * units > 0x7fffffff) return CCV_ERR_SIZE;
-    const dim3 grid(static_cast<unsigned>(blocks * units)), block(LANES * ROWS / R);
+    const dim3 grid(static_cast<unsigned>(blocks * units)), block(LANES * ROWS);
     if (p.seg_chunks > 0) {
-        int status = launch_pdl(ssm_scan_kernel<LANES, NS, R, ROWS, TOKENS, PER, false>, grid, block, 0, stream, p, vec);
+        int status = launch_pdl(ssm_scan_kernel<LANES, NS, ROWS, TOKENS, PER, false>, grid, block, 0, stream, p, vec);
         if (status != CCV_OK) return status;
         const int64_t joins = p.batch * ((static_cast<int64_t>(p.a.num_heads) * p.a.head_dim * p.a.dim_state + 255) / 256);
         if (joins > 0x7fffffff) return CCV_ERR_SIZE;
         status = launch_pdl(ssm_scan_join_kernel, dim3(static_cast<unsigned>(joins)), dim3(256), 0, stream, p, LANES * NS);
         if (status != CCV_OK) return status;
     }
-    return launch_pdl(ssm_scan_kernel<LANES, NS, R, ROWS, TOKENS, PER, true>, grid, block, 0, stream, p, vec);
+    return launch_pdl(ssm_scan_kernel<LANES, NS, ROWS, TOKENS, PER, true>, grid, block, 0, stream, p, vec);
 }
 
 // Lanes a row, states a lane, rows and tokens a tile by what is fastest for 2 x 2048 tokens of 4096 channels: 32 states 235 us (16
@@ -475,11 +424,11 @@ int launch_scan(const SsmFwd &p, const ScanVec &vec, cudaStream_t stream) {
 template <bool PER>
 int launch_states(const SsmFwd &p, const ScanVec &vec, cudaStream_t stream) {
     const int n = p.a.dim_state;
-    if (n <= 16) return launch_scan<4, 4, 1, 32, 32, PER>(p, vec, stream);
-    if (n <= 32) return launch_scan<8, 4, 1, 32, 32, PER>(p, vec, stream);
-    if (n <= 64) return launch_scan<8, 8, 1, 32, 32, PER>(p, vec, stream);
-    if (n <= 128) return launch_scan<8, 16, 1, 16, 16, PER>(p, vec, stream);
-    return launch_scan<16, 16, 1, 16, 16, PER>(p, vec, stream);
+    if (n <= 16) return launch_scan<4, 4, 32, 32, PER>(p, vec, stream);
+    if (n <= 32) return launch_scan<8, 4, 32, 32, PER>(p, vec, stream);
+    if (n <= 64) return launch_scan<8, 8, 32, 32, PER>(p, vec, stream);
+    if (n <= 128) return launch_scan<8, 16, 16, 16, PER>(p, vec, stream);
+    return launch_scan<16, 16, 16, 16, PER>(p, vec, stream);
 }
 
 }  // namespace
