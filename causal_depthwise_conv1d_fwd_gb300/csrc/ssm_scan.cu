@@ -385,11 +385,16 @@ __global__ void __launch_bounds__(256) ssm_scan_join_kernel(const __grid_constan
     const int64_t slot = first_slot(s, seq, unit);
     float *to = p.seg_state + (slot * rows + row) * states + n;
     const float *sum = p.seg_decay + slot * rows + row;
+    const int64_t next = static_cast<int64_t>(rows) * states;
+    float own = *to, d = *sum;  // there are two segments at least; the last one's own are not wanted
     for (int i = 0; i < segments; ++i) {
-        const float own = i + 1 < segments ? *to : 0.0f, d = i + 1 < segments ? *sum : 0.0f;
+        const bool more = i + 2 < segments;
+        const float own1 = more ? to[next] : 0.0f, d1 = more ? sum[rows] : 0.0f;  // ahead of the store, behind which they would wait
         *to = f;
         f = fmaf(expf(d * rate), f, own);
-        to += static_cast<int64_t>(rows) * states;
+        own = own1;
+        d = d1;
+        to += next;
         sum += rows;
     }
 }
