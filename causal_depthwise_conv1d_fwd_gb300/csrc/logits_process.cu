@@ -7,11 +7,15 @@
 // penalties' arithmetic, which has no branches.  A row's history is read by all of its blocks, from L2 after the first.
 // 64 rows of 5 positions of 131072 bf16 logits with histories of 4000 tokens and a mask take 55 us (3.1 TB/s of what has to be
 // moved): 9 for the histories, 12 for the adjustments, the rest the latency of 1024 blocks at 4 an SM.  A share of 8192 tokens is
-// a table of 32 KB; with 4096 every history is read twice as often, and it took no less.
+// a table of 32 KB; with 4096 every history is read twice as often, and it took no less.  256 rows of one position, histories of
+// 3000: bf16 44 us (floor 20), fp32 78 (40); with a mask 53 and 91, in place 54 and 98.  Every block reads its row's history: 64 x 5
+// positions with 32768 tokens take 74 us, with 100000 128.  A bias list is searched for each of its tokens: 64 rows of fp32 with 30
+// entries take 21 us, with 300 68, with 3000 1500.
 //
 // In place and without a mask only the tokens that were seen matter.  Where they are few enough for a hash table in shared memory
 // a block takes a whole row: it counts the history there and goes through the table's slots at each position.
-// 256 rows of 131072 fp32 logits with 4000 tokens take 21 us (by shares 124): two waves of a block's latency.
+// 256 rows of 131072 fp32 logits with up to 4000 tokens take 21 us (by shares 61): two waves of a block's latency.  It is the
+// pool's width that the table has to hold, since lengths are not known to the host: from 12289 tokens a line on it is shares.
 #include <algorithm>
 
 #include "ccv_common.cuh"

@@ -13,15 +13,15 @@
 // Three more warps copy tiles, sum the steps, and issue the products.  Heads wider than 64 are cut into panels of 64.
 //
 // What bounds it: 700 instructions a warp and chunk, on four warps a scheduler (46 % of the issue slots while a block runs); no warp
-// waits for a product any more.  4 x 4096 tokens of 128 heads with 128 states take 358 us, 0.30 of the tensor cores' cycles, where
-// the bytes take 96; 11027 tokens of 32 heads in segments 121 (15); 232 tokens in 4 prompts 11.  On the way here, still with two
+// waits for a product any more.  4 x 4096 tokens of 128 heads with 128 states take 360 us, 0.30 of the tensor cores' cycles, where
+// the bytes take 96; 11027 tokens of 32 heads in segments 122 (15); 232 tokens in 4 prompts 11.  On the way here, still with two
 // parts of the weighted tokens: a role a warpgroup took 1097 us (the hot instructions were twice as many and missed the instruction
 // cache), two heads a block 424 (registers), one with the copies and the steps in one warp 396, with a barrier for every hand-over
 // 383, without either 346.  Three parts with two stages of x and of B took 398, since x came late.
 //
 // Precision.  What is not bf16 from the start enters the tensor cores in bf16 parts; the other factors, x, B and C, are exact.  The
-// weighted tokens, which make the state, have three parts, all 24 bits: with two the state was 3e-6 of itself off, with three it is
-// as near as the recurrent forms'.  M and the state in C S reach the outputs alone, which are rounded to 8 bits, and have two parts
+// weighted tokens, which make the state, have three parts, all 24 bits: with two the state is 2.6e-6 of itself off, with three
+// 2e-7, as much as the steps are off (the forms that multiply it by a decay a token are 1e-6 off after 1000).  M and the state in C S reach the outputs alone, which are rounded to 8 bits, and have two parts
 // (2^-17 of each term).  Sums and the state are fp32: the tensor cores' accumulators within a chunk, a multiply-add from chunk to
 // chunk.  Smaller parts are added first, since the tensor cores' sums truncate.  G is summed in pairs of floats, and so are its
 // differences.
@@ -433,6 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const __grid_con
                     if (!(ok = wait_all(&sm.cb_full, c & 1, abort))) break;
                     tc_fence_after();
                     if (mine) {
+                        // Unrolled, like the issuing warp's loops.  With rolled loops around tensor memory's instructions, whose
+                        // operands then went by the loop's counter, an early form stopped with a misaligned address.  All of its
+                        // accesses to vectors were checked and none was misaligned; the cause is not known.  What is known to
+                        // differ: its warps' numbers came straight from threadIdx, so to the compiler those operands could differ
+                        // from lane to lane, which these instructions do not allow.
                         const float *since = sm.since[w] + qd * 32, *steps = g.d + qd * 32;
 #pragma unroll
                         for (int j0 = 0; j0 < 32; j0 += 16) {
@@ -715,8 +720,9 @@ bool ssm_chunked_dims(int dim_state, int a_per_state) { return !a_per_state && d
 
 // Chunks of a segment, or 0 to leave sequences whole, for sequences of equal lengths (their offsets are on the device).  In
 // chunk times of a block (3 us): the first pass takes 0.6 of one a chunk, a block 0.8 to start and end, the two launches more 3.
-// Each pass runs in waves of one block an SM.  11027 tokens of 32 heads take 121 us so and 232 whole, 30000 of 64 507 and 616;
-// 2 x 4000 of 64 heads 137 in two segments and 92 whole.
+// Each pass runs in waves of one block an SM.  11027 tokens of 32 heads take 122 us so and 232 whole, 30000 of 64 507 and 616;
+// 2 x 4000 of 64 heads 137 in two segments and 92 whole.  Lengths that differ are not seen: 11000 tokens and 23 prompts of 40, 32
+// heads, stay whole and take 233, in segments of 29 chunks 147.
 int ssm_chunked_segments(int total_tokens, int batch, int num_heads, int head_dim) {
     const char *forced = std::getenv("CCV_SSM_SEGMENT");  // chunks of a segment (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;

@@ -60,7 +60,8 @@ enum Form { kRecurrent, kChunked, kScan };
 // and 27 (168); 128 of 8 tokens of 4096 channels with 16 states 51, by the scan 126 (a single one 10 and 8).  Above that the
 // tensor cores where one decay a head and the states allow it: 8 x 500 tokens of 32 heads with 16 states take 34 us and by the
 // scan 118, with 64 35 and 214; heads of 8 channels (256 of them, whose tiles are an eighth full) 197 and 442 (but 32 x 60 tokens
-// 314 and 232), and of 4 (512) 450 and 662, but 32 x 60 tokens of those 649 and 332.
+// 314 and 232), and of 4 (512) 450 and 662, but 32 x 60 tokens of those 649 and 332.  The average is all that the sizes tell: 255
+// sequences of one token and one of 1700, 32 heads, go token by token and take 1263 us, by the chunked form 358.
 // CCV_SSM_PATH=recurrent, =chunked or =scan, read at each call, forces a form where it can run (for testing and tuning).
 Form choose(int total_tokens, int batch, int head_dim, int dim_state, int a_per_state) {
     const char *path = std::getenv("CCV_SSM_PATH");

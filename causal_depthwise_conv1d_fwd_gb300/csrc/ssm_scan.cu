@@ -1,19 +1,20 @@
 // Selective state space scan over varlen sequences (prefill), token by token, for layers whose channels each have their own
 // step and a decay for every state, and for whatever else the chunked form does not take.
 //
-// A row (head h, channel p) has dim_state states in the registers of LANES lanes; a block has 32 (16) rows of one group of one
-// sequence (or segment), in 128 or 256 threads, and goes through its tokens in tiles of 32 (16).  The tile's inputs come to registers while the one
-// before is worked on; from there the steps (one a row and token, where the lanes would each repeat it) go to shared memory as
-// pairs d, d x, and B and C as floats.  For a token a lane then needs
+// A row (head h, channel p) has dim_state states in the registers of LANES lanes; a block has 32 rows (16 above 64 states) of one
+// group of one sequence (or segment), LANES threads each, and goes through its tokens in tiles of as many.  The tile's inputs come
+// to registers while the one before is worked on; from there the steps (one a row and token, where the lanes would each repeat it)
+// go to shared memory as pairs d, d x, and B and C as floats.  For a token a lane then needs
 //     e = 2^{d A log2 e},   s <- e s + (d x) B,   y += s C
 // for its own states: an exponential, two multiplications and two multiply-adds a state, in pairs.  The sums over the lanes are
 // taken for LANES tokens at once, halving what each lane holds at every step, so that a lane ends with one token's output.
 //
-// 4 x 4096 tokens of 8192 channels with 16 states take 834 us, 1.2 TB/s of what has to be moved.  Nothing in it is at its limit
+// 4 x 4096 tokens of 8192 channels with 16 states take 836 us, 1.2 TB/s of what has to be moved.  Nothing in it is at its limit
 // alone: shared memory is busy for 72 % of the time (each lane reads a token's B, C and steps), instructions are issued in 64 % of
 // the cycles, and the exponentials need 235 us of it (32 a cycle and SM).  More lanes a row, more rows a lane, and exponentials by
-// polynomials on the multiply-add pipes were all slower.  The same for 1009 + 37 + 300 tokens of 2048 channels, in segments of
-// 128: 58 us.
+// polynomials on the multiply-add pipes were all slower.  At 16 states a thread has 72 registers for seven blocks an SM, and 28
+// bytes (for the segments' own states 76) go to local memory.  The same for 1009 + 37 + 300 tokens of 2048 channels, in segments of
+// 128: 56 us.
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
@@ -423,7 +424,7 @@ int launch_scan(const SsmFwd &p, const ScanVec &vec, cudaStream_t stream) {
     return launch_pdl(ssm_scan_kernel<LANES, NS, ROWS, TOKENS, PER, true>, grid, block, 0, stream, p, vec);
 }
 
-// Lanes a row, states a lane, rows and tokens a tile by what is fastest for 2 x 2048 tokens of 4096 channels: 32 states 235 us (16
+// Lanes a row, states a lane, rows and tokens a tile by what is fastest for 2 x 2048 ungated tokens of 4096 channels: 32 states 235 us (16
 // rows 250, 4 x 8 lanes 329), 64 states 337 (16 rows 369, 16 x 4 lanes 508), 128 states 664 (16 x 8 lanes 717 to 1170, 32 tokens
 // 850), 256 states 1330 (8 rows 2256).
 template <bool PER>
@@ -448,9 +449,9 @@ int64_t ssm_scan_workspace(int total_tokens, int batch, int num_heads, int head_
 // be halfway between the average and all tokens.  In ns, as measured: a token takes `lone` in a block with an SM to itself, and
 // `first` and `each` more for each of the blocks that an SM has; cutting does part of the work once more and costs a block the time
 // of some tokens (`start`), a segment of the join takes 700 and the two launches 8000.
-// 16 states: 5000 tokens of 4096 channels take 222 us so (segments of 256) and 381 whole, 2000 of 2048 channels 62 and 153; 4 x 4096
-// of 8192 channels 834 whole and 1150 in segments of 1024.  More states: 2000 tokens of 512 channels with 256 states 163 and 329;
-// 2 x 2048 of 4096 channels with 32 states 235 whole and 525 in segments of 128.
+// 16 states: 5000 tokens of 4096 channels take 216 us so (segments of 256) and 381 whole, 2000 of 2048 channels 60 and 154; 4 x 4096
+// of 8192 channels 836 whole and 1150 in segments of 1024.  More states, without a gate: 2000 tokens of 512 channels with 256
+// states 161 and 330; 2 x 2048 of 4096 channels with 32 states 235 whole and 525 in segments of 128.
 int ssm_scan_segments(int total_tokens, int batch, int num_heads, int num_groups, int head_dim, int dim_state) {
     const char *forced = std::getenv("CCV_SSM_SEGMENT");  // (for testing and tuning)
     if (forced != nullptr) return std::atoi(forced) > 0 && std::atoi(forced) < (1 << 20) ? std::atoi(forced) : 0;

@@ -25,8 +25,9 @@ extern "C" {
  *
  * logits, out   (batch, num_positions, vocab <= 2^30), vocab stride 1, bf16 or
  *               (logits_fp32, out_fp32) fp32.  out may be logits itself (same
- *               pointer, type and strides), where a logit that nothing changes
- *               is neither read nor written; otherwise it must not overlap an
+ *               pointer, type and strides); without a mask a logit that nothing
+ *               changes is then neither read nor written, with one it may be
+ *               written once more as it is.  Otherwise out must not overlap an
  *               input.  out's rows must lie apart (CCV_ERR_STRIDE).
  * history       int32 (num_lines, history_size >= 0), stride 1 along a line: the
  *               tokens of a request, its prompt first; NULL: none (then
@@ -44,7 +45,9 @@ extern "C" {
  * repetition, frequency, presence  fp32 [batch] or NULL (1, 0, 0); repetition
  *               above 0.
  * bias_ids, bias  int32 and fp32 (batch, bias_size), stride 1 along a row, one
- *               row stride; or NULL.
+ *               row stride; or NULL.  Meant for up to some hundred entries:
+ *               the time grows with their square.  Many tokens are better
+ *               excluded by the mask.
  * mask          int32 (batch, num_positions, (vocab + 31) / 32), stride 1 along
  *               the last: bit v % 32 of word v / 32 is 1 where v may follow; NULL:
  *               everything may.
