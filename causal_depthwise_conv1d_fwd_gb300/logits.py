@@ -96,10 +96,11 @@ def _marshal(logits, history, history_lengths, prompt_lengths, history_indices, 
         if history.dim() != 2 or (history.shape[1] > 1 and history.stride(1) != 1):
             raise ValueError("history must be (num_lines, size) with stride 1 along a line")
         lines, size = history.shape
-        hp, hs = history.data_ptr(), history.stride(0)
+        # an empty pool has no address, but is not none: any other one, which nothing reads
+        hp, hs = history.data_ptr() or logits.data_ptr(), history.stride(0)
         if history_lengths is None:
             raise ValueError("history needs history_lengths")
-        hl = _vector(dev, history_lengths, "history_lengths", _I32, lines)
+        hl = _vector(dev, history_lengths, "history_lengths", _I32, lines) or hp
         pl = _vector(dev, prompt_lengths, "prompt_lengths", _I32, lines)
         if history_indices is None and lines < b:
             raise ValueError(f"history has {lines} lines, needs {b}")
