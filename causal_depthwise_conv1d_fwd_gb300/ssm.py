@@ -61,7 +61,8 @@ def _pack_ssm(x, dt, A, B, C, state, D, z, dt_bias, dt_softplus, dt_limit, pad_s
         if len(st) < 3 or st[1:] != ((h, n) if channels else (h, p, n)):
             raise ValueError("state must be (num_lines, heads, head_dim, dim_state), without "
                              "head_dim where x has none")
-        lines, ss, sp = st[0], state.stride(), state.data_ptr()
+        # an empty pool has no address, but is not none: any other one, which nothing reads
+        lines, ss, sp = st[0], state.stride(), state.data_ptr() or x.data_ptr()
         if channels:
             ss = (ss[0], ss[1], 0, ss[2])
     if out is None:

@@ -32,3 +32,19 @@ def test_histories(ccv, place, masked):  # noqa: F811
         if skipped < 3:
             want = torch.full_like(logits[0], -torch.inf) if masked else logits[0]
             assert torch.equal(out[0], want)
+
+
+def test_states(ccv):  # noqa: F811
+    for heads, dim, states, per in ((2, 64, 128, False), (40, 1, 16, True)):
+        for length in (40, 2):
+            t = cuda(make(length, heads, dim, 1, states, 90, per_state=per))
+            state = torch.zeros(0, heads, dim, states, device="cuda")
+            args = tuple(t[k] for k in ("x", "dt", "A", "B", "C"))
+            for lines, counted in ((i32(0), True), (i32(-1), False)):
+                err, out = i32(0), torch.full_like(t["x"], 7.0)
+                ccv.ssm_fwd(*args, state, i32(0, length), lines, out=out, err_count=err)
+                assert bool((out == 7).all()) and (int(err) > 0) == counted
+                err = i32(0)
+                ccv.ssm_update(*(a[None] if a.shape[0] == length and k != 2 else a for k, a in enumerate(args)), state, lines,
+                               out=out[None], err_count=err)
+                assert bool((out == 7).all()) and (int(err) > 0) == counted
